@@ -398,3 +398,9 @@ def sgemm_status_string(status: int) -> str:
 
 def sgemm_version() -> str:
     return load().sgemm_version().decode()
+
+
+from . import decode as _decode  # noqa: E402  (it uses the names above)
+from .decode import *  # noqa: E402,F401,F403
+
+__all__ += _decode.__all__

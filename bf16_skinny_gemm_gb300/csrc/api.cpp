@@ -485,6 +485,16 @@ sgemm_status_t run(const sgemm_pair_t *items, int batch, int M, int N, int K,
 
 namespace sk {
 
+sgemm_status_t device_ready(int *sms, int **err) {
+    int dev = 0;
+    DeviceState *st = nullptr;
+    const sgemm_status_t s = probe_device(&dev, &st);
+    if (s != SGEMM_OK) return s;
+    *sms = st->sms;
+    *err = st->err;
+    return SGEMM_OK;
+}
+
 int split_kps(int K, int split) {
     const int chunks = K / 8;
     const int per = (chunks + split - 1) / split;

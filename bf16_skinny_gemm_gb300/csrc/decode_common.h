@@ -1,0 +1,65 @@
+// Host helpers shared by the operators of sgemm_decode.h.
+#pragma once
+
+#include <cuda_runtime.h>
+
+#include <cstdint>
+#include <cstring>
+
+#include "internal.h"
+#include "sgemm_decode.h"
+
+namespace sk {
+
+constexpr unsigned kDecodeFlags = SGEMM_FLAG_PDL | SGEMM_FLAG_WEIGHTS_READONLY;
+constexpr int kErrBadIndex = 2;  // device error word: an index out of range was met and skipped
+
+inline bool aligned(const void *p, unsigned bytes) {
+    return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) == 0;
+}
+
+// Whether two arrays of `rows` rows (`wa` and `wb` bytes wide, strides `sa` and
+// `sb` bytes) share a byte.  Arrays of one stride are compared column by
+// column, so that two column ranges of one buffer count as apart; arrays of
+// different strides count as overlapping when their extents do.
+inline bool rows_overlap(const void *a, long long wa, long long sa, const void *b, long long wb,
+                         long long sb, long long rows) {
+    if (!a || !b || rows < 1) return false;
+    const uintptr_t pa = reinterpret_cast<uintptr_t>(a), pb = reinterpret_cast<uintptr_t>(b);
+    const uintptr_t ea = pa + static_cast<uintptr_t>((rows - 1) * sa + wa);
+    const uintptr_t eb = pb + static_cast<uintptr_t>((rows - 1) * sb + wb);
+    if (pa >= eb || pb >= ea) return false;
+    if (sa != sb || sa < 1) return true;
+    const uintptr_t s = static_cast<uintptr_t>(sa);
+    if (pa <= pb) {
+        const uintptr_t d = (pb - pa) % s;
+        return d < static_cast<uintptr_t>(wa) || d + static_cast<uintptr_t>(wb) > s;
+    }
+    const uintptr_t d = (pa - pb) % s;
+    return d < static_cast<uintptr_t>(wb) || d + static_cast<uintptr_t>(wa) > s;
+}
+
+inline bool valid_flags(unsigned flags) { return (flags & ~kDecodeFlags) == 0; }
+
+// Launch `fn` with one parameter structure, as a programmatic dependent of the
+// previous kernel on the stream when `pdl`.
+inline cudaError_t launch(const void *fn, dim3 grid, dim3 block, size_t smem, cudaStream_t stream,
+                          bool pdl, void *params) {
+    cudaLaunchConfig_t cfg;
+    std::memset(&cfg, 0, sizeof(cfg));
+    cfg.gridDim = grid;
+    cfg.blockDim = block;
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    if (pdl) {
+        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[0].val.programmaticStreamSerializationAllowed = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+    }
+    void *args[] = {params};
+    return cudaLaunchKernelExC(&cfg, fn, args);
+}
+
+}  // namespace sk

@@ -104,6 +104,10 @@ long long ctas_wanted(const sgemm_plan_t &plan, int N);
 // Let a kernel use all the dynamic shared memory its static part leaves.
 cudaError_t allow_max_dynamic_smem(const void *fn);
 
+// Checks that the current device is supported; its SM count and error word
+// (defined in api.cpp, cached per device).
+sgemm_status_t device_ready(int *sms, int **err);
+
 // The device error word of the current device (a static device variable of
 // the library; bit 0: a kernel gave up a bounded wait).  Defined in
 // tc05_launch.cu, which owns the variable.

@@ -1,0 +1,253 @@
+"""Binding of the operators between a decode step's projections (``include/sgemm_decode.h``):
+
+- :func:`sgemm_bf16_add_rmsnorm`, :func:`sgemm_bf16_add_rmsnorm_e4m3`: residual add and RMS norm,
+- :func:`sgemm_bf16_latent_append`: append to a paged latent cache, rotating on the way,
+- :func:`sgemm_bf16_latent_attention`: attention over that cache (absorbed form).
+
+As in the rest of the package, the functions check and marshal their arguments; every step of
+the computation runs in the library's CUDA kernels.  Each takes preallocated outputs (allocating
+nothing then), launch flags and a stream, and can be captured into a CUDA graph.
+"""
+from __future__ import annotations
+
+import ctypes
+import struct
+
+import torch
+
+from . import SgemmError, load
+
+__all__ = [
+    "sgemm_bf16_add_rmsnorm", "sgemm_bf16_add_rmsnorm_e4m3", "sgemm_bf16_latent_append",
+    "sgemm_bf16_latent_attention", "sgemm_latent_attention_workspace",
+    "SGEMM_NORM_BF16", "SGEMM_NORM_E4M3_ROW", "SGEMM_NORM_E4M3_GROUP128", "LATENT_WORKSPACE_MAX",
+]
+
+SGEMM_NORM_BF16 = 0
+SGEMM_NORM_E4M3_ROW = 1
+SGEMM_NORM_E4M3_GROUP128 = 2
+LATENT_WORKSPACE_MAX = 64 << 20
+
+# the argument structures of the header, field by field (natural alignment, no padding)
+_NORM = struct.Struct("<6Q6qiifI")        # sgemm_add_rmsnorm_t
+_APPEND = struct.Struct("<8Q11q5ifIi")    # sgemm_latent_append_t
+_ATTN = struct.Struct("<8Q11q7ifIi")      # sgemm_latent_attention_t
+
+_BF16 = torch.bfloat16
+_fns: dict = {}
+
+
+def _fn(name: str):
+    f = _fns.get(name)
+    if f is None:
+        f = getattr(load(), name)
+        f.argtypes = [ctypes.c_char_p, ctypes.c_void_p]
+        f.restype = ctypes.c_int
+        _fns[name] = f
+    return f
+
+
+def _call(name: str, args: bytes, t: torch.Tensor, stream) -> None:
+    if stream is None:
+        stream = torch._C._cuda_getCurrentRawStream(t.get_device())
+    elif isinstance(stream, torch.cuda.Stream):
+        stream = stream.cuda_stream
+    status = _fn(name)(args, stream)
+    if status:
+        raise SgemmError(status, name)
+
+
+def _need(t, name: str, dtype, dim: int) -> torch.Tensor:
+    """A CUDA tensor of this type and rank, its last dimension of unit stride."""
+    if not isinstance(t, torch.Tensor) or t.dtype != dtype or t.dim() != dim:
+        raise TypeError(f"{name} must be a {dim}-D {dtype} tensor")
+    if not t.is_cuda:
+        raise TypeError(f"{name} must be on a CUDA device")
+    if t.stride(-1) != 1 and t.shape[-1] > 1:
+        raise ValueError(f"{name} must have unit stride along its last dimension")
+    return t
+
+
+def _shaped(t, name: str, dtype, shape) -> torch.Tensor:
+    _need(t, name, dtype, len(shape))
+    if t.shape != shape:
+        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+    return t
+
+
+def _ptr(t) -> int:
+    return 0 if t is None else t.data_ptr()
+
+
+# ----------------------------------------------------------------------------- residual RMS norm
+def _norm(name, x, weight, residual, eps, form, y, y_dtype, scales, residual_out, flags, stream):
+    T, D = _need(x, "x", _BF16, 2).shape
+    _shaped(weight, "weight", _BF16, (D,))
+    if residual is not None:
+        _shaped(residual, "residual", _BF16, (T, D))
+        if residual_out is None:
+            residual_out = torch.empty((T, D), dtype=_BF16, device=x.device)
+    if residual_out is not None:
+        _shaped(residual_out, "residual_out", _BF16, (T, D))
+    if y is None:
+        y = torch.empty((T, D), dtype=y_dtype, device=x.device)
+    _shaped(y, "y" if form == SGEMM_NORM_BF16 else "q", y_dtype, (T, D))
+    lds = 0
+    if form != SGEMM_NORM_BF16:
+        groups = -(-D // 128) if form == SGEMM_NORM_E4M3_GROUP128 else 1
+        if scales is None:
+            scales = torch.empty((T, groups), dtype=torch.float32, device=x.device)
+        _shaped(scales, "scales", torch.float32, (T, groups))
+        lds = scales.stride(0) if T > 1 else groups
+    if T == 0:
+        return y, scales, residual_out
+    one = T == 1  # the row stride of a single row is of no account
+    _call("sgemm_bf16_add_rmsnorm", _NORM.pack(
+        x.data_ptr(), _ptr(residual), weight.data_ptr(), _ptr(residual_out), y.data_ptr(), _ptr(scales),
+        D if one else x.stride(0), D if one or residual is None else residual.stride(0),
+        D if one or residual_out is None else residual_out.stride(0), D if one else y.stride(0), lds,
+        T, D, form, eps, flags), x, stream)
+    return y, scales, residual_out
+
+
+def sgemm_bf16_add_rmsnorm(x: torch.Tensor, weight: torch.Tensor, residual: torch.Tensor | None = None,
+                           eps: float = 1e-6, y: torch.Tensor | None = None,
+                           residual_out: torch.Tensor | None = None, flags: int = 0, stream=None):
+    """``h = x + residual``, ``y = bf16(h * rsqrt(mean(h**2) + eps) * weight)``; returns
+    ``(y, residual_out)`` with ``residual_out = bf16(h)`` (None where neither a residual nor a
+    buffer for it is given).  x, residual: BF16 [T, D], rows of any stride; weight: BF16 [D].
+    ``residual_out`` may be ``residual`` or ``x``, and ``y`` may be ``x``: in place."""
+    y, _, residual_out = _norm("sgemm_bf16_add_rmsnorm", x, weight, residual, eps, SGEMM_NORM_BF16, y, _BF16,
+                               None, residual_out, flags, stream)
+    return y, residual_out
+
+
+def sgemm_bf16_add_rmsnorm_e4m3(x: torch.Tensor, weight: torch.Tensor, residual: torch.Tensor | None = None,
+                                eps: float = 1e-6, group: int = 128, q: torch.Tensor | None = None,
+                                scales: torch.Tensor | None = None,
+                                residual_out: torch.Tensor | None = None, flags: int = 0, stream=None):
+    """:func:`sgemm_bf16_add_rmsnorm` with y in 8 bits: returns ``(q, scales, residual_out)``,
+    ``q = e4m3(y / scale)`` (torch.float8_e4m3fn [T, D]) and FP32 scales ``max|y| / 448``
+    (1 where that is 0) per 128 columns (``group=128``: [T, ceil(D / 128)]) or per row
+    (``group=0``: [T, 1])."""
+    if group not in (0, 128):
+        raise ValueError(f"group must be 128 (columns a scale) or 0 (one scale a row), got {group}")
+    form = SGEMM_NORM_E4M3_GROUP128 if group else SGEMM_NORM_E4M3_ROW
+    return _norm("sgemm_bf16_add_rmsnorm", x, weight, residual, eps, form, q, torch.float8_e4m3fn, scales,
+                 residual_out, flags, stream)
+
+
+# ---------------------------------------------------------------------------------- cache append
+def sgemm_bf16_latent_append(kv: torch.Tensor, cache: torch.Tensor, slots: torch.Tensor,
+                             positions: torch.Tensor, cos_sin: torch.Tensor,
+                             weight: torch.Tensor | None = None, eps: float = 1e-6,
+                             q: torch.Tensor | None = None, q_out: torch.Tensor | None = None,
+                             interleaved: bool = True, flags: int = 0, stream=None):
+    """Write each token's row into the paged latent cache; returns ``(cache, q_out)``.
+
+    kv: BF16 [T, R + E], the latent vector and the E elements to rotate; cache: BF16
+    [pages, page_size, R + E] (pages and rows of any stride); slots, positions: int64 [T], the
+    row ``page * page_size + i`` each token goes to (negative: none) and its position; cos_sin:
+    FP32 [positions, E], cosines then sines.  With ``weight`` (BF16 [R]) the latent vector is
+    RMS-normalised on the way.  q, q_out: BF16 [T, H, E] views, the part of each head's query
+    that is rotated and where it goes (may be the same).  ``interleaved``: the rotated pairs are
+    (2i, 2i + 1), else (i, E / 2 + i)."""
+    T, W = _need(kv, "kv", _BF16, 2).shape
+    pages, page_size, width = _need(cache, "cache", _BF16, 3).shape
+    limit, E = _need(cos_sin, "cos_sin", torch.float32, 2).shape
+    R = W - E
+    if width != W:
+        raise ValueError(f"cache rows must be as wide as kv's ({W}), got {width}")
+    if R < 1:
+        raise ValueError(f"kv rows ({W}) must be wider than cos_sin's ({E})")
+    _shaped(slots, "slots", torch.int64, (T,))
+    _shaped(positions, "positions", torch.int64, (T,))
+    if weight is not None:
+        _shaped(weight, "weight", _BF16, (R,))
+    H, strides = 0, (0, 0, 0, 0)
+    if q is not None:
+        H = _need(q, "q", _BF16, 3).shape[1]
+        if q.shape[0] != T or q.shape[2] != E:
+            raise ValueError(f"q must be [{T}, heads, {E}], got {list(q.shape)}")
+        if q_out is None:
+            q_out = torch.empty((T, H, E), dtype=_BF16, device=kv.device)
+        _shaped(q_out, "q_out", _BF16, (T, H, E))
+        strides = (q.stride(0), q.stride(1), q_out.stride(0), q_out.stride(1))
+    elif q_out is not None:
+        raise ValueError("q_out without q")
+    if T == 0:
+        return cache, q_out
+    _call("sgemm_bf16_latent_append", _APPEND.pack(
+        kv.data_ptr(), _ptr(weight), cos_sin.data_ptr(), positions.data_ptr(), slots.data_ptr(), cache.data_ptr(),
+        _ptr(q) if H else 0, _ptr(q_out) if H else 0,
+        W if T == 1 else kv.stride(0), E if limit == 1 else cos_sin.stride(0), W if page_size == 1 else cache.stride(1),
+        cache.stride(0) if pages > 1 else page_size * max(W, cache.stride(1)), *strides,
+        T, limit, pages, page_size, R, E, H, 1 if interleaved else 0, eps, flags, 0), kv, stream)
+    return cache, q_out
+
+
+# ------------------------------------------------------------------------------ latent attention
+def sgemm_latent_attention_workspace(batch: int, heads: int, rank: int, rope: int, page_size: int,
+                                     table_width: int, max_q: int = 1) -> int:
+    """Bytes of scratch :func:`sgemm_bf16_latent_attention` needs for such a call
+    (at most ``LATENT_WORKSPACE_MAX``)."""
+    n = ctypes.c_longlong(0)
+    f = _fn("sgemm_latent_attention_workspace")
+    args = _ATTN.pack(*([0] * 16), 1, 0, batch * max_q, page_size, table_width, batch, heads, rank, rope, max_q,
+                      1.0, 0, 0)
+    status = f(args, ctypes.addressof(n))
+    if status:
+        raise SgemmError(status, "sgemm_latent_attention_workspace")
+    return n.value
+
+
+def sgemm_bf16_latent_attention(q: torch.Tensor, cache: torch.Tensor, block_table: torch.Tensor,
+                                seq_lens: torch.Tensor, rank: int, scale: float,
+                                cu_q: torch.Tensor | None = None, max_q: int = 1,
+                                out: torch.Tensor | None = None, lse: torch.Tensor | None = None,
+                                workspace: torch.Tensor | None = None, flags: int = 0, stream=None):
+    """Attention over a paged latent cache, absorbed form; returns ``(out, lse)``.
+
+    q: BF16 [total_q, H, rank + E]; cache: BF16 [pages, page_size, rank + E], whose first ``rank``
+    elements are also the values; block_table: int32 [B, width]; seq_lens: int32 [B], cached rows
+    of each sequence, its new tokens' among them.  ``cu_q``: int32 [B + 1], where each sequence's
+    query tokens begin, at most ``max_q`` each (None: ``max_q`` each).  Token i of a sequence's n
+    sees its first ``seq_lens - n + i + 1`` rows; one that sees none gets zeros (and -inf).
+    out: BF16 [total_q, H, rank]; lse: FP32 [total_q, H] or None (not written).  ``workspace``:
+    scratch on the device (:func:`sgemm_latent_attention_workspace` bytes; allocated for the call
+    where None)."""
+    total, H, W = _need(q, "q", _BF16, 3).shape
+    pages, page_size, width = _need(cache, "cache", _BF16, 3).shape
+    B, table_width = _need(block_table, "block_table", torch.int32, 2).shape
+    _shaped(seq_lens, "seq_lens", torch.int32, (B,))
+    if width != W:
+        raise ValueError(f"cache rows must be as wide as q's ({W}), got {width}")
+    if cu_q is not None:
+        _shaped(cu_q, "cu_q", torch.int32, (B + 1,))
+    elif total != B * max_q:
+        raise ValueError(f"q must hold {B} x {max_q} tokens without cu_q, got {total}")
+    if out is None:
+        out = torch.empty((total, H, rank), dtype=_BF16, device=q.device)
+    _shaped(out, "out", _BF16, (total, H, rank))
+    if lse is not None:
+        _shaped(lse, "lse", torch.float32, (total, H))
+    if total == 0 or B == 0:
+        return out, lse
+    if workspace is None:
+        need = sgemm_latent_attention_workspace(B, H, rank, W - rank, page_size, table_width, max_q)
+        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+        if stream is not None and need:
+            workspace.record_stream(stream if isinstance(stream, torch.cuda.Stream)
+                                    else torch.cuda.ExternalStream(int(stream)))
+    elif not workspace.is_cuda or not workspace.is_contiguous():
+        raise TypeError("workspace must be a contiguous CUDA tensor")
+    _call("sgemm_bf16_latent_attention", _ATTN.pack(
+        q.data_ptr(), cache.data_ptr(), block_table.data_ptr(), seq_lens.data_ptr(), _ptr(cu_q), out.data_ptr(),
+        _ptr(lse), workspace.data_ptr(),
+        q.stride(0), q.stride(1), cache.stride(1) if page_size > 1 else W,
+        cache.stride(0) if pages > 1 else page_size * max(W, cache.stride(1)),
+        block_table.stride(0) if B > 1 else table_width, out.stride(0), out.stride(1),
+        lse.stride(0) if lse is not None else 0,
+        pages, workspace.numel() * workspace.element_size(), total,
+        page_size, table_width, B, H, rank, W - rank, max_q, scale, flags, 0), q, stream)
+    return out, lse
