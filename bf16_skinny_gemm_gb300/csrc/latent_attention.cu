@@ -24,9 +24,10 @@
 //    latent elements, a slot; the E elements in a ring of their own).  Slots
 //    rather than tiles: a slot is free again as soon as its part of O^T is
 //    done, and what is left of shared memory beside Q holds 1.75 to 2.5 tiles.
-//  * One thread of warp 1 issues the products.  It takes whichever is ready:
-//    O^T of tile t as soon as its weights are there, else the next slot of
-//    S^T of tile t + 1; waiting for the latter first would hold tile t's slots.
+//  * Warp 1 issues the first product, warp 6 the second.  Two warps, because
+//    neither may wait for the other's operands: O^T of tile t is issued as soon
+//    as its weights are there, which frees the tile's slots, and S^T of tile
+//    t + 1 as its slots arrive.
 //  * Warps 2..5 do the softmax: S^T is read in the 16 x 256-bit form, so that
 //    all lanes hold scores though M = 64 fills half of the lanes.  The running
 //    maximum of a row is over keys, which lie across lanes and warps; it is
@@ -34,7 +35,7 @@
 //    more than 2^8 (in units of the result), else the old one stands: one
 //    barrier with a vote a tile.  The weights are then at most 2^8, and neither
 //    their rounding to BF16 nor the FP32 sums care about that factor.
-//  * Warps 6 and 7 copy the queries of the next piece of work (any strides).
+//  * Warp 7 copies the queries of the next piece of work (any strides).
 //
 // Work split.  The tiles of all sequences form one line, cut into equal shares,
 // one for each group of CTAs (a group has a CTA for each NT rows of a sequence
@@ -64,12 +65,15 @@ constexpr int kChunk = kTile * 64 * 2;   // 64 keys x 64 elements
 constexpr int kSlot = 2 * kChunk;        // 128 latent elements (M of the second product)
 constexpr int kMaxSlots = 12;
 constexpr int kMaxRopeSlots = 3;
-constexpr int kThreads = 256;            // producer, MMA, 4 softmax and 2 query-loading warps
-constexpr int kStaticSmem = 4096;        // bound on the static shared memory below
+constexpr int kThreads = 256;            // producer, first product, 4 softmax, second product, queries
+constexpr int kPrefetch = 2;             // tiles that are fetched into the L2 cache ahead of the copies
+constexpr int kMaxCopies = 8;            // copies of a chunk of a tile: pages of at least 8 rows
+constexpr int kBarBytes = 384;           // the mbarriers
 
 struct LatentParams {
     CUtensorMap tv;  // the latent part: {64, page rows, R / 64, pages}
     CUtensorMap tr;  // the rotated part: {E, page rows, pages}
+    CUtensorMap qv, qr;  // the same parts of the queries, where (token, head) rows are evenly spaced
     const uint16_t *q;
     const int *table;
     const int *lens;
@@ -85,7 +89,12 @@ struct LatentParams {
     int slots, rope_slots;  // rings
     float scale_log2;       // scale * log2(e)
     int flags;
-    int nseg, by_seq, cw, pw;  // the joining kernel's grid
+    int q_even;   // the queries' rows are evenly spaced: copied with TMA
+    int out16;    // out's rows start on 16 bytes
+    long long page_bytes;  // from page to page, where a page's rows lie back to back; else 0
+    const uint8_t *cache;
+    int by_seq;   // descriptors of split sequences: one a sequence, else one a group
+    int cw, pw;   // the joining kernel's block: warps for elements, warps for pieces
 };
 
 // ------------------------------------------------------------------ the work's line of tiles
@@ -124,30 +133,63 @@ __device__ __forceinline__ int tiles_of(const Seq &s) {
     return s.n > 0 ? max(1, (s.len + kTile - 1) / kTile) : 0;
 }
 
-// Exclusive prefix sum over the block's threads, and the total.  `part`: 32 ints.
-__device__ __forceinline__ int block_prefix(int v, int *part, int *total) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
-    int x = v;
-#pragma unroll
-    for (int off = 1; off < 32; off <<= 1) {
-        const int y = __shfl_up_sync(0xffffffffu, x, off);
-        if (lane >= off) x += y;
-    }
-    if (lane == 31) part[warp] = x;
-    __syncthreads();
-    int before = 0, all = 0;
-    for (int w = 0; w < warps; ++w) {
-        const int y = part[w];
-        if (w < warp) before += y;
-        all += y;
-    }
-    __syncthreads();
-    *total = all;
-    return before + x - v;
-}
-
 __device__ __forceinline__ int share_begin(int units, int g, int groups) {
     return static_cast<int>(static_cast<long long>(units) * g / groups);
+}
+
+// A group's share of the line.
+struct Share {
+    int units, groups;  // tiles on the line, shares it is cut into
+    int u0, u1;         // this share's tiles
+    int b, k;           // sequence and tile of the first
+};
+
+// Found by each warp by itself (no block barrier before the first copies): a pass over the
+// sequences for the line's length, one for the place of the share's beginning.
+__device__ __forceinline__ Share share_of(const LatentParams &p, int g, bool report) {
+    const int lane = threadIdx.x & 31;
+    Share s;
+    s.units = 0;
+    int mine = 0;
+    for (int c = 0; c < p.B; c += 32) {
+        int t = 0;
+        if (c + lane < p.B) {
+            const Seq q = seq_of(p, c + lane);
+            if (q.bad && report) atomicOr(p.err, kErrBadIndex);
+            t = tiles_of(q);
+        }
+        if (c == 0) mine = t;
+        s.units += static_cast<int>(__reduce_add_sync(0xffffffffu, static_cast<unsigned>(t)));
+    }
+    s.groups = min(p.groups, max(s.units, 1));
+    s.u0 = s.u1 = s.b = s.k = 0;
+    if (g >= s.groups) return s;
+    s.u0 = share_begin(s.units, g, s.groups);
+    s.u1 = share_begin(s.units, g + 1, s.groups);
+    if (s.u0 >= s.u1) return s;
+    for (int c = 0, at = 0;; c += 32) {
+        const int t = c == 0 ? mine : c + lane < p.B ? tiles_of(seq_of(p, c + lane)) : 0;
+        int x = t;
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, x, off);
+            if (lane >= off) x += y;
+        }
+        const unsigned past = __ballot_sync(0xffffffffu, s.u0 < at + x);
+        if (past) {
+            const int w = __ffs(past) - 1;
+            s.b = c + w;
+            s.k = s.u0 - at - __shfl_sync(0xffffffffu, x - t, w);
+            return s;
+        }
+        at += __shfl_sync(0xffffffffu, x, 31);
+    }
+}
+
+// Scratch: descriptors, then two slots a CTA, each O (NT x R), m and l of a piece.  Slot 1 holds
+// a sequence's first piece, slot 0 a later one.
+__device__ __forceinline__ float *slot_of(const LatentParams &p, int cta, int which, int nt) {
+    return p.ws + 4 * ((p.groups + 3) / 4 * 4) + (static_cast<long long>(cta) * 2 + which) * nt * (p.R + 2);
 }
 
 // One piece of a share: rows row0 .. row0 + nrows of sequence b, its tiles k0 .. k1 - 1 (none
@@ -156,6 +198,7 @@ struct Piece {
     Seq s;
     int b, row0, nrows, k0, k1;
     bool first, last;  // holds the sequence's first / last tile
+    int left;          // tiles of the share from the piece's first on
 };
 
 struct Walk {
@@ -166,6 +209,7 @@ struct Walk {
             const int kt = tiles_of(o.s);
             const int take = min(kt - k, left);
             o.b = b;
+            o.left = left;
             o.k0 = k;
             o.first = k == 0;
             o.last = k + take == kt;
@@ -185,6 +229,62 @@ struct Walk {
     }
 };
 
+// The pages of a piece's tiles, read 32 table entries at a time (one load a warp for 8 to 32
+// tiles), a batch ahead.  A tile is copied in `copies` pieces of `rows` rows of a page each.
+struct Pages {
+    const int *table;
+    int rows, per, page_size, limit;  // rows a copy, copies a whole tile; rows the sequence has
+    int first;                        // the first tile of the batch in `now`
+    int now, next;
+    int k, copies, row;               // the current tile, its copies, the first one's row in its page
+    int bad;                          // the page that reads as zeros
+    bool whole;                       // a tile lies in one page
+
+    __device__ __forceinline__ int look(int tile) const {
+        const int lane = threadIdx.x & 31;
+        const int key = (tile + lane / per) * kTile + (lane % per) * rows;
+        return key < limit ? table[key / page_size] : -1;
+    }
+    __device__ __forceinline__ Pages(const LatentParams &p, const Piece &o) {
+        table = p.table + static_cast<long long>(o.b) * p.ldt;
+        page_size = p.page_size;
+        rows = min(kTile, page_size);
+        per = kTile / rows;
+        whole = per == 1;
+        limit = min(o.s.len, o.k1 * kTile);
+        bad = p.pages;
+        first = o.k0;
+        now = look(first);
+        next = look(first + 32 / per);
+    }
+    __device__ __forceinline__ void step(const LatentParams &p, int tile) {
+        k = tile;
+        if (k == first + 32 / per) {
+            first = k;
+            now = next;
+            next = look(k + 32 / per);
+        }
+        const int keys = min(kTile, limit - k * kTile);
+        copies = (keys + rows - 1) / rows;
+        row = whole ? (k * kTile) % page_size : 0;
+        // an entry out of range among those that are used is reported; it reads as zeros
+        const int lane = threadIdx.x & 31;
+        const int mine = __shfl_sync(0xffffffffu, now, ((k - first) * per + lane) & 31);
+        if (lane < copies && (mine < 0 || mine >= bad)) atomicOr(p.err, kErrBadIndex);
+    }
+    // the page of copy f of the current tile
+    __device__ __forceinline__ int page(int f) const {
+        const int v = __shfl_sync(0xffffffffu, now, (k - first) * per + f);
+        return v < 0 || v >= bad ? bad : v;
+    }
+    // the table's entry for copy f of a tile at most a batch ahead (a lane's f of no copy: any)
+    __device__ __forceinline__ int ahead(int tile, int f) const {
+        const int at = (tile - first) * per + (f < per ? f : 0);
+        const int x = __shfl_sync(0xffffffffu, now, at & 31), y = __shfl_sync(0xffffffffu, next, at & 31);
+        return at < 32 ? x : y;
+    }
+};
+
 // ------------------------------------------------------------------------------- primitives
 using tc05::bar_arrive;
 using tc05::bar_try;
@@ -193,18 +293,6 @@ using tc05::prefetch_tmap;
 using tc05::tc_fence_after;
 using tc05::tc_fence_before;
 using tc05::tmem_ld16;
-
-__device__ __forceinline__ bool bar_test(uint32_t b, unsigned parity) {
-    uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok)
-        : "r"(b), "r"(parity)
-        : "memory");
-    return ok != 0;
-}
 
 // Wait for a phase, at most kWaitLimitNs, and not past another role's giving up.
 __device__ __forceinline__ bool wait_or_stop(uint32_t b, unsigned parity, int *stop) {
@@ -220,6 +308,17 @@ __device__ __forceinline__ bool wait_or_stop(uint32_t b, unsigned parity, int *s
     return true;
 }
 
+// The same for a whole warp, which goes on together.
+__device__ __forceinline__ bool all_wait(uint32_t b, unsigned parity, int *stop) {
+    if (__all_sync(0xffffffffu, bar_try(b, parity))) return true;
+    return __all_sync(0xffffffffu, wait_or_stop(b, parity, stop));
+}
+
+// A value that all lanes of the warp have alike, by an instruction whose result the compiler
+// knows to be: the issuing warps' loops and descriptors then stay in uniform registers, where
+// tcgen05.mma and the copies want them.
+__device__ __forceinline__ int alike(int v) { return static_cast<int>(__reduce_or_sync(0xffffffffu, static_cast<unsigned>(v))); }
+
 // Barrier of the 128 softmax threads, alone or with the OR of a predicate.
 __device__ __forceinline__ void soft_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
 __device__ __forceinline__ bool soft_any(bool v) {
@@ -232,6 +331,17 @@ __device__ __forceinline__ bool soft_any(bool v) {
         : "=r"(r)
         : "r"(v ? 1u : 0u)
         : "memory");
+    return r != 0;
+}
+
+// One lane of a converged warp, the same each time.
+__device__ __forceinline__ bool elect() {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "elect.sync _|p, 0xffffffff;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(r)::"memory");
     return r != 0;
 }
 
@@ -283,6 +393,19 @@ __device__ __forceinline__ void tma_4d(uint32_t dst, const CUtensorMap *map, int
         : "memory");
 }
 
+// Bytes (16-byte aligned, a multiple of 16) into the L2 cache.
+__device__ __forceinline__ void l2_ahead(const void *src, unsigned bytes) {
+    asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(src), "r"(bytes) : "memory");
+}
+
+// Four 8 x 8 BF16 fragments, each stored turned: lane l gives the address of row l % 8 (its
+// column in the fragment) of fragment l / 8.
+__device__ __forceinline__ void stmatrix_turned(uint32_t addr, const uint32_t (&q)[4]) {
+    asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(q[0]),
+                 "r"(q[1]), "r"(q[2]), "r"(q[3])
+                 : "memory");
+}
+
 // S^T of 64 keys x NT rows: lane l of the warp gets keys l / 4 and l / 4 + 8 of the warp's 16,
 // and of each 8 rows the pair 2 (l % 4): s[4i], s[4i+1] of the first key, s[4i+2], s[4i+3] of
 // the second.
@@ -320,6 +443,26 @@ __device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t (&r)[16]
         : "memory");
 }
 
+// Wait (bounded) for a copy in flight.
+__device__ __forceinline__ void landed(uint32_t bar, unsigned parity) {
+    const unsigned long long t0 = global_ns();
+    while (!bar_try(bar, parity))
+        if (static_cast<long long>(global_ns() - t0) > kWaitLimitNs) break;
+}
+
+// Wait (bounded) until every product this warp issued is complete.
+__device__ __forceinline__ void finish(uint32_t bar, int *stop) {
+    if (elect()) mma_commit(bar);
+    __syncwarp();
+    const unsigned long long t0 = global_ns();
+    while (!bar_try(bar, 0))
+        if (static_cast<long long>(global_ns() - t0) > kWaitLimitNs) {
+            atomicExch(stop, 1);
+            break;
+        }
+    __syncwarp();
+}
+
 // BF16 pairs with infinities and NaN set to 0.
 __device__ __forceinline__ uint32_t finite_or_zero(uint32_t w) {
     if ((w & 0x7f80u) == 0x7f80u) w &= 0xffff0000u;
@@ -337,23 +480,20 @@ __global__ void __launch_bounds__(kThreads, 1) latent_attention_kernel(const __g
                                  (static_cast<uint32_t>(kTile >> 4) << 24);
     constexpr uint32_t kIdescO = (1u << 4) | (1u << 7) | (1u << 10) | (1u << 15) | (1u << 16) |
                                  (static_cast<uint32_t>(NT >> 3) << 17) | (static_cast<uint32_t>(128 >> 4) << 24);
-    extern __shared__ uint8_t smem_raw[];
-    __shared__ __align__(8) uint64_t bars[2 * kMaxSlots + 2 * kMaxRopeSlots + 11];
-    __shared__ __align__(16) float ex[2][4][NT];   // a warp's maxima (or sums) of each row
-    __shared__ __align__(16) float fs[NT], ms[NT];  // a row's factor for O^T; its maximum
-    __shared__ long long off[NT];    // a row's place in out
-    __shared__ int part[32], plan[3];
-    __shared__ uint32_t tmem_slot;
-    __shared__ int stop;
-
-    uint8_t *base = smem_raw + ((1024u - (saddr(smem_raw) & 1023u)) & 1023u);
+    extern __shared__ __align__(1024) uint8_t base[];  // the only shared memory: it starts on 1 KiB
     const int pairs = p.R / 128;            // slots a tile
     const int qchunk = NT * 128;            // bytes of a chunk of Q
+    const int S = p.slots, RS = p.rope_slots;
     const uint32_t s_q = saddr(base);
     const uint32_t s_p = s_q + (2 * pairs + 1) * qchunk;
     const uint32_t s_r = s_p + 2 * kChunk;
-    const uint32_t s_v = s_r + p.rope_slots * kChunk;
-    const int S = p.slots, RS = p.rope_slots;
+    const uint32_t s_v = s_r + RS * kChunk;
+    uint8_t *misc = base + (s_v - s_q) + S * kSlot;
+    uint64_t *bars = reinterpret_cast<uint64_t *>(misc);
+    float(*ex)[4][NT] = reinterpret_cast<float(*)[4][NT]>(misc + kBarBytes);  // [2] a warp's maxima (or sums) of each row
+    float *fs = reinterpret_cast<float *>(misc + kBarBytes + 32 * NT), *ms = fs + NT;  // a row's factor for O^T, its maximum
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(ms + NT);
+    int &stop = *reinterpret_cast<int *>(tmem_slot + 1);
 
     const uint32_t vfull = saddr(bars), vempty = vfull + 8 * kMaxSlots;
     const uint32_t rfull = vempty + 8 * kMaxSlots, rempty = rfull + 8 * kMaxRopeSlots;
@@ -367,8 +507,11 @@ __global__ void __launch_bounds__(kThreads, 1) latent_attention_kernel(const __g
         if (lane == 0) {
             prefetch_tmap(&p.tv);
             prefetch_tmap(&p.tr);
+            if (p.q_even) {
+                prefetch_tmap(&p.qv);
+                prefetch_tmap(&p.qr);
+            }
             stop = 0;
-            plan[2] = 0;
             for (int i = 0; i < kMaxSlots; ++i) {
                 bar_init(vfull + 8 * i, 1);
                 bar_init(vempty + 8 * i, 1);
@@ -377,217 +520,168 @@ __global__ void __launch_bounds__(kThreads, 1) latent_attention_kernel(const __g
                 bar_init(rfull + 8 * i, 1);
                 bar_init(rempty + 8 * i, 1);
             }
-            bar_init(qfull, 2);
+            bar_init(qfull, 1);
             bar_init(qempty, 1);
             for (int i = 0; i < 2; ++i) {
                 bar_init(sfull + 8 * i, 1);
                 bar_init(sempty + 8 * i, 4);
                 bar_init(pfull + 8 * i, 4);
                 bar_init(pvd + 8 * i, 1);
+                bar_init(fin + 8 * i, 1);
             }
-            bar_init(fin, 1);
             asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         }
         __syncwarp();
     }
     if (p.flags & kFlagPdl) pdl_wait();
-    // Tensor memory is taken after the wait: a CTA of the previous kernel may still want its
-    // own, and this one holds its columns until that kernel is done.
-    if (warp == 1) {
-        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(saddr(&tmem_slot)),
-                     "r"(kTmem)
-                     : "memory");
-        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
-    }
-    __syncthreads();
-    // this CTA's share of the line
-    {
-        const int per = (p.B + kThreads - 1) / kThreads;
-        const int b0 = min(p.B, static_cast<int>(threadIdx.x) * per), b1 = min(p.B, b0 + per);
-        int sum = 0, units;
-        for (int b = b0; b < b1; ++b) {
-            const Seq s = seq_of(p, b);
-            if (s.bad && blockIdx.x == 0) atomicOr(p.err, kErrBadIndex);
-            sum += tiles_of(s);
+    uint32_t tmem = 0;
+    if (warp == 0) {
+        // the producer goes on: it needs the mbarriers only, which are its own work
+        asm volatile("bar.arrive 2, 256;" ::: "memory");
+    } else {
+        // Tensor memory is taken after the wait: a CTA of the previous kernel may still want its
+        // own, and this one holds its columns until that kernel is done.
+        if (warp == 1) {
+            asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(saddr(tmem_slot)),
+                         "r"(kTmem)
+                         : "memory");
+            asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
         }
-        int at = block_prefix(sum, part, &units);
-        const int ge = min(p.groups, max(units, 1));
-        if (g < ge) {
-            const int u0 = share_begin(units, g, ge), u1 = share_begin(units, g + 1, ge);
-            if (u0 < u1 && u0 >= at && u0 < at + sum) {
-                for (int b = b0; b < b1; ++b) {
-                    const int kt = tiles_of(seq_of(p, b));
-                    if (u0 < at + kt) {
-                        plan[0] = b;
-                        plan[1] = u0 - at;
-                        plan[2] = u1 - u0;
-                        break;
-                    }
-                    at += kt;
-                }
-            }
-        }
+        tc_fence_before();
+        asm volatile("bar.sync 2, 256;" ::: "memory");
+        tc_fence_after();
+        tmem = *tmem_slot;
+        pdl_launch_dependents();
     }
-    tc_fence_before();
-    __syncthreads();
-    tc_fence_after();
-    pdl_launch_dependents();
-    const uint32_t tmem = tmem_slot;
+    const Share sh = share_of(p, g, blockIdx.x == 0 && warp == 2);
     const uint32_t t_o = tmem + 2 * kSCols;
-    Walk walk{plan[0], plan[1], plan[2]};
+    Walk walk{sh.b, sh.k, sh.u1 - sh.u0};
     const bool stall = (p.flags & kFlagTestStall) != 0;
     Piece o;
     int issued = 0, rissued = 0;  // slots of each ring that the producer filled
+    int pieces = 0;               // pieces whose queries were copied
 
     if (warp == 0) {
-        // ------------------------------------------------------------------- producer
-        const int rows = min(kTile, p.page_size);       // rows of one copy
-        const bool whole = rows == kTile;
-        int n = 0;
+        // ------------------------------------------- producer of the latent elements' ring
+        int at = 0, slot = 0;  // slots filled; the next one
+        unsigned ph = 0;       // parity of the ring's round
         bool ok = true;
         while (ok && walk.next(p, r, o)) {
-            const int *table = p.table + static_cast<long long>(o.b) * p.ldt;
-            auto page_of = [&](int k) {
-                // lane f: the page of the f-th copy of tile k (or the page past the last one,
-                // which reads as zeros)
-                const int key = k * kTile + (whole ? 0 : lane * rows);
-                const bool in = whole ? key < o.s.len : lane < kTile / rows && key < o.s.len;
-                if (!in || k >= o.k1) return p.pages;
-                const int page = table[key / p.page_size];
-                if (page < 0 || page >= p.pages) {
-                    if (lane == 0 || !whole) atomicOr(p.err, kErrBadIndex);
-                    return p.pages;
-                }
-                return page;
-            };
-            int next = o.k0 < o.k1 ? page_of(o.k0) : 0;
-            for (int k = o.k0; ok && k < o.k1; ++k, ++n) {
-                const int page = next;
-                if (k + 1 < o.k1) next = page_of(k + 1);
-                const int keys = min(kTile, o.s.len - k * kTile);
-                const int nf = (keys + rows - 1) / rows;  // copies of each chunk
-                const int row = whole ? (k * kTile) % p.page_size : 0;
+            Pages pages(p, o);
+            for (int k = o.k0; ok && k < o.k1; ++k) {
+                pages.step(p, k);
+                const int copies = alike(pages.copies), step = pages.rows * 128;
+                const int row = alike(pages.row);
+                int page[kMaxCopies];
+#pragma unroll
+                for (int f = 0; f < kMaxCopies; ++f)
+                    if (f < copies) page[f] = alike(pages.page(f));
                 for (int j = 0; j < pairs; ++j) {
-                    const int at = n * pairs + j, slot = at % S;
-                    if (lane == 0) {
-                        ok = at < S || wait_or_stop(vempty + 8 * slot, ((at / S) - 1) & 1, &stop);
-                        if (ok) bar_expect_tx(vfull + 8 * slot, static_cast<unsigned>(2 * nf * rows * 128));
+                    if (!(ok = at < S || all_wait(vempty + 8 * slot, ph ^ 1, &stop))) break;
+                    if (!stall) issued = at + 1;
+                    const uint32_t dst = s_v + slot * kSlot, bar = vfull + 8 * slot;
+                    if (elect()) {
+                        bar_expect_tx(bar, static_cast<unsigned>(2 * copies * step));
+                        if (!stall) {
+                            if (pages.whole) {
+                                tma_4d(dst, &p.tv, 0, row, 2 * j, page[0], bar);
+                            } else {
+#pragma unroll
+                                for (int f = 0; f < kMaxCopies; ++f)
+                                    if (f < copies) {
+                                        tma_4d(dst + f * step, &p.tv, 0, 0, 2 * j, page[f], bar);
+                                        tma_4d(dst + f * step + kChunk, &p.tv, 0, 0, 2 * j + 1, page[f], bar);
+                                    }
+                            }
+                        }
                     }
-                    ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
-                    if (!ok) break;
-                    issued = stall ? 0 : at + 1;
-                    if (stall) continue;
-                    const uint32_t dst = s_v + slot * kSlot;
-                    if (whole) {
-                        if (lane == 0) tma_4d(dst, &p.tv, 0, row, 2 * j, page, vfull + 8 * slot);
-                    } else {
-                        const int f = lane % nf, c = lane / nf;
-                        const int pg = __shfl_sync(0xffffffffu, page, f);
-                        if (c < 2) tma_4d(dst + c * kChunk + f * rows * 128, &p.tv, 0, 0, 2 * j + c, pg, vfull + 8 * slot);
+                    __syncwarp();
+                    ++at;
+                    if (++slot == S) {
+                        slot = 0;
+                        ph ^= 1;
                     }
                 }
-                if (!ok) break;
-                const int slot = n % RS;
-                if (lane == 0) {
-                    ok = n < RS || wait_or_stop(rempty + 8 * slot, ((n / RS) - 1) & 1, &stop);
-                    if (ok) bar_expect_tx(rfull + 8 * slot, static_cast<unsigned>(nf * rows * 128));
-                }
-                ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
-                if (!ok) break;
-                rissued = stall ? 0 : n + 1;
-                if (!stall && lane < (whole ? 1 : nf))
-                    tma_3d(s_r + slot * kChunk + lane * rows * 128, &p.tr, 0, row, page, rfull + 8 * slot);
             }
         }
     } else if (warp == 1) {
-        // --------------------------------------------------------------- the products
-        if (lane == 0) {
-            int ns = 0, no = 0;  // tiles whose S^T, whose O^T is issued
-            int step = 0, tile = 0, piece = -1;
-            unsigned opens = 0;  // bit (tile & 3): the first tile of its piece, O^T starts anew
-            bool have = false, more = true, idle = false;
-            unsigned long long t0 = 0;
-            while (more || have || no < ns) {
-                bool did = false;
-                if (no < ns && bar_test(pfull + 8 * (no & 1), (no >> 1) & 1)) {
+        // --------------------------------------------------- the first product, S^T = K Q^T
+        // The whole warp follows the loop, one elected lane issues: a branch on the lane's
+        // number in its place made every tcgen05.mma take 100 to 250 cycles to issue.
+        int n = 0, slot = 0, rslot = 0, piece = 0;
+        unsigned ph = 0, rph = 0;  // parities of the rings' rounds
+        bool ok = true;
+        const uint32_t base_d = alike(static_cast<int>(tmem));
+        while (ok && alike(walk.next(p, r, o) ? 1 : 0)) {
+            const int tiles = alike(o.k1 - o.k0);
+            if (tiles == 0) continue;
+            ok = all_wait(qfull, piece & 1, &stop);
+            for (int k = 0; ok && k < tiles; ++k, ++n) {
+                ok = n < 2 || all_wait(sempty + 8 * (n & 1), ((n >> 1) - 1) & 1, &stop);
+                const uint32_t d = base_d + (n & 1) * kSCols;
+                for (int j = 0; ok && j < pairs; ++j) {
+                    if (!(ok = all_wait(vfull + 8 * slot, ph, &stop))) break;
                     tc_fence_after();
-                    const uint32_t pb = s_p + (no & 1) * kChunk;
-                    const bool open = (opens >> (no & 3)) & 1;
-                    for (int j = 0; j < pairs; ++j) {
-                        const int slot = (no * pairs + j) % S;
-                        const uint32_t a = s_v + slot * kSlot;
+                    if (elect()) {
+                        const uint64_t a = tc05::sw128_desc(s_v + slot * kSlot), b = tc05::sw128_desc(s_q + j * (2 * NT * 128));
 #pragma unroll
-                        for (int kk = 0; kk < kTile / 16; ++kk)
-                            mma(t_o + j * NT, mn_desc(a + kk * 2048), mn_desc(pb + kk * 2048), kIdescO, !(open && kk == 0));
-                        mma_commit(vempty + 8 * slot);
-                    }
-                    mma_commit(pvd + 8 * (no & 1));
-                    ++no;
-                    did = true;
-                }
-                if (more && !have) {
-                    more = walk.next(p, r, o);
-                    if (more && o.k0 < o.k1) {
-                        have = true;
-                        tile = o.k0;
-                        ++piece;
-                    }
-                    did = true;
-                }
-                if (have) {
-                    bool ready = true;
-                    if (step == 0)
-                        ready = (ns < 2 || bar_test(sempty + 8 * (ns & 1), ((ns >> 1) - 1) & 1)) &&
-                                (tile != o.k0 || bar_test(qfull, piece & 1));
-                    const int at = ns * pairs + step;
-                    if (ready)
-                        ready = step < pairs ? bar_test(vfull + 8 * (at % S), (at / S) & 1)
-                                             : bar_test(rfull + 8 * (ns % RS), (ns / RS) & 1);
-                    if (ready) {
-                        tc_fence_after();
-                        const uint32_t d = tmem + (ns & 1) * kSCols;
-                        const uint32_t a = step < pairs ? s_v + (at % S) * kSlot : s_r + (ns % RS) * kChunk;
-                        const uint32_t b = s_q + 2 * step * qchunk;
-                        const int chunks = step < pairs ? 2 : 1;
-                        for (int c = 0; c < chunks; ++c)
+                        for (int c = 0; c < 2; ++c)
 #pragma unroll
                             for (int kk = 0; kk < 4; ++kk)
-                                mma(d, tc05::sw128_desc(a + c * kChunk + 32 * kk), tc05::sw128_desc(b + c * qchunk + 32 * kk),
-                                    kIdescS, (step | c | kk) != 0);
-                        if (++step > pairs) {
-                            mma_commit(rempty + 8 * (ns % RS));
-                            mma_commit(sfull + 8 * (ns & 1));
-                            if (tile + 1 == o.k1) mma_commit(qempty);
-                            opens = (opens & ~(1u << (ns & 3))) | (tile == o.k0 ? 1u << (ns & 3) : 0u);
-                            ++ns;
-                            step = 0;
-                            if (++tile == o.k1) have = false;
-                        }
-                        did = true;
+                                mma(d, a + ((c * kChunk + 32 * kk) >> 4), b + ((c * NT * 128 + 32 * kk) >> 4), kIdescS,
+                                    (c | kk) != 0 || j != 0);
+                    }
+                    __syncwarp();
+                    if (++slot == S) {
+                        slot = 0;
+                        ph ^= 1;
                     }
                 }
-                if (did) {
-                    idle = false;
-                } else if (!idle) {
-                    idle = true;
-                    t0 = global_ns();
-                } else if (*reinterpret_cast<volatile int *>(&stop)) {
-                    break;
-                } else if (static_cast<long long>(global_ns() - t0) > kWaitLimitNs) {
-                    atomicExch(&stop, 1);
-                    break;
+                if (!ok || !(ok = all_wait(rfull + 8 * rslot, rph, &stop))) break;
+                tc_fence_after();
+                if (elect()) {
+                    const uint64_t a = tc05::sw128_desc(s_r + rslot * kChunk), b = tc05::sw128_desc(s_q + pairs * (2 * NT * 128));
+#pragma unroll
+                    for (int kk = 0; kk < 4; ++kk) mma(d, a + ((32 * kk) >> 4), b + ((32 * kk) >> 4), kIdescS, true);
+                    mma_commit(sfull + 8 * (n & 1));
+                    mma_commit(rempty + 8 * rslot);
+                    if (k + 1 == tiles) mma_commit(qempty);
+                }
+                __syncwarp();
+                if (++rslot == RS) {
+                    rslot = 0;
+                    rph ^= 1;
                 }
             }
-            // every product issued is complete before the tensor memory is given back
-            mma_commit(fin);
-            const unsigned long long w0 = global_ns();
-            while (!bar_try(fin, 0))
-                if (static_cast<long long>(global_ns() - w0) > kWaitLimitNs) {
-                    atomicExch(&stop, 1);
-                    break;
-                }
+            ++piece;
         }
+        finish(fin, &stop);
+    } else if (warp == 6) {
+        // ----------------------------------------------- the second product, O^T += V^T P^T
+        int n = 0, slot = 0;
+        bool ok = true;
+        const uint32_t base_d = alike(static_cast<int>(t_o));
+        while (ok && alike(walk.next(p, r, o) ? 1 : 0)) {
+            const int tiles = alike(o.k1 - o.k0);
+            for (int k = 0; k < tiles; ++k, ++n) {
+                if (!(ok = all_wait(pfull + 8 * (n & 1), (n >> 1) & 1, &stop))) break;
+                tc_fence_after();
+                for (int j = 0; j < pairs; ++j) {
+                    if (elect()) {
+                        const uint64_t a = mn_desc(s_v + slot * kSlot), b = mn_desc(s_p + (n & 1) * kChunk);
+#pragma unroll
+                        for (int kk = 0; kk < kTile / 16; ++kk)
+                            mma(base_d + j * NT, a + kk * (2048 >> 4), b + kk * (2048 >> 4), kIdescO, kk != 0 || k != 0);
+                        mma_commit(vempty + 8 * slot);
+                        if (j == pairs - 1) mma_commit(pvd + 8 * (n & 1));
+                    }
+                    __syncwarp();
+                    if (++slot == S) slot = 0;
+                }
+            }
+        }
+        finish(fin + 8, &stop);
     } else if (warp < 6) {
         // ------------------------------------------------------------------- softmax
         const int sw = warp & 3;  // tensor-memory lanes 32 sw .. and keys 16 sw .. of a tile
@@ -597,7 +691,16 @@ __global__ void __launch_bounds__(kThreads, 1) latent_attention_kernel(const __g
         const float inf = __int_as_float(0x7f800000), nan = __int_as_float(0x7fc00000);
         int n = 0;
         bool ok = true, dead = false;
+        // descriptors for the joining kernel: {q0, tokens, first, last group} of a split sequence
+        int4 *desc = reinterpret_cast<int4 *>(p.ws);
+        const bool tell = r == 0 && tid == 0 && p.groups > 1;
+        if (tell && !p.by_seq) desc[g] = make_int4(0, 0, 0, -1);
         while (walk.next(p, r, o)) {
+            if (tell && o.first) {
+                const int u_last = sh.u0 + (sh.u1 - sh.u0 - o.left) + tiles_of(o.s) - 1;
+                const int g1 = static_cast<int>((static_cast<long long>(u_last + 1) * sh.groups - 1) / sh.units);
+                if (p.by_seq || !o.last) desc[p.by_seq ? o.b : g] = make_int4(o.s.q0, o.s.n, g, o.last ? -1 : g1);
+            }
             float m[NC], l[NC];
             int lim[NC];  // keys a row sees
 #pragma unroll
@@ -752,94 +855,189 @@ __global__ void __launch_bounds__(kThreads, 1) latent_attention_kernel(const __g
                     if (sw == 0) *reinterpret_cast<float2 *>(&ms[8 * i + c0]) = make_float2(m[2 * i], m[2 * i + 1]);
                 }
             dead = soft_any(!ok || dead);
-            const bool direct = o.first && o.last;
-            float *ws = p.ws + (static_cast<long long>(blockIdx.x) * 2 + (o.first ? 1 : 0)) * NT * (p.R + 2);
-            if (tid < NT) {
-                const float sum = (ex[n & 1][0][tid] + ex[n & 1][1][tid]) + (ex[n & 1][2][tid] + ex[n & 1][3][tid]);
-                const int row = o.row0 + tid, tok = o.s.q0 + row / p.H, head = row % p.H;
-                if (direct) {
-                    fs[tid] = dead ? nan : sum == 0.0f ? 0.0f : 1.0f / sum;
+            const bool empty = o.k0 >= o.k1;
+            auto total = [&](int col) {
+                return (ex[n & 1][0][col] + ex[n & 1][1][col]) + (ex[n & 1][2][col] + ex[n & 1][3][col]);
+            };
+            if (o.first && o.last) {
+                // The whole sequence: O / l, BF16, turned in shared memory (where the weights
+                // were) so that rows of out are written 16 bytes a thread.  The tensor memory is
+                // read in the 16 x 256-bit form again, whose fragments stmatrix stores turned.
+                long long *off = reinterpret_cast<long long *>(&ex[(n & 1) ^ 1][0][0]);
+                if (tid < NT) {
+                    const int row = o.row0 + tid, tok = o.s.q0 + row / p.H, head = row % p.H;
                     off[tid] = tok * p.out_token + head * p.out_head;
+                    const float sum = total(tid);
                     if (p.lse && tid < o.nrows)
                         p.lse[tok * p.lse_token + head] =
                             dead ? nan : sum == 0.0f ? -inf : (ms[tid] + log2f(sum)) * 0.69314718056f;
-                } else {
+                }
+                float inv[NC];
+#pragma unroll
+                for (int c = 0; c < NC; ++c) {
+                    const float sum = total(8 * (c >> 1) + c0 + (c & 1));
+                    inv[c] = dead ? nan : sum == 0.0f ? 0.0f : 1.0f / sum;
+                }
+                for (int j = 0; j < pairs; ++j) {
+                    constexpr int kStage = NT * 256;  // a row's 128 elements, 16-byte units swizzled
+                    const uint32_t stage = s_p + (NT == 64 ? 0 : (j & 1) * kStage);
+                    if (NT == 64 && j > 0) soft_sync();
+#pragma unroll
+                    for (int half = 0; half < 2; ++half) {
+                        uint32_t v[4 * (NT / 8)];
+                        if (empty || dead) {
+#pragma unroll
+                            for (int i = 0; i < 4 * (NT / 8); ++i) v[i] = 0u;
+                        } else {
+                            tmem_ld_s(t_o + quarter + (static_cast<uint32_t>(16 * half) << 16) + j * NT, v);
+                            asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+                        }
+#pragma unroll
+                        for (int i = 0; i < NT / 8; i += 2) {
+                            uint32_t q[4];
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                const int c = 2 * (i + (e >> 1)), at = 4 * (i + (e >> 1)) + 2 * (e & 1);
+                                q[e] = bf16x2(__uint_as_float(v[at]) * inv[c], __uint_as_float(v[at + 1]) * inv[c + 1]);
+                            }
+                            const int col = 8 * (i + (lane >> 4)) + (lane & 7), unit = 4 * sw + 2 * half + ((lane >> 3) & 1);
+                            stmatrix_turned(stage + col * 256 + ((unit ^ (col & 7)) << 4), q);
+                        }
+                    }
+                    soft_sync();
+                    for (int i = tid; i < o.nrows * 16; i += 128) {
+                        const int row = i >> 4, u = i & 15;
+                        const uint4 v = *reinterpret_cast<const uint4 *>(base + (stage - s_q) + row * 256 + ((u ^ (row & 7)) << 4));
+                        uint16_t *dst = p.out + off[row] + 128 * j + 8 * u;
+                        if (p.out16) {
+                            *reinterpret_cast<uint4 *>(dst) = v;
+                        } else {
+                            uint32_t *d4 = reinterpret_cast<uint32_t *>(dst);
+                            d4[0] = v.x;
+                            d4[1] = v.y;
+                            d4[2] = v.z;
+                            d4[3] = v.w;
+                        }
+                    }
+                }
+            } else {
+                // A piece: O, m and l as they are, FP32.  O in groups of four rows, [group][element][4]:
+                // a thread holds one element of all rows and stores 16 bytes a group.
+                float *ws = slot_of(p, static_cast<int>(blockIdx.x), o.first ? 1 : 0, NT);
+                if (tid < NT) {
+                    const float sum = total(tid);
                     // a NaN score leaves the maximum alone: the piece's is then NaN itself, so
                     // that joining keeps it whatever the maximum
                     ws[NT * p.R + tid] = dead || sum != sum ? nan : ms[tid];
                     ws[NT * p.R + NT + tid] = dead ? nan : sum;
                 }
-            }
-            soft_sync();
-            const bool empty = o.k0 >= o.k1;
-            if (direct || !(empty || dead)) {
-                for (int c = 0; c < pairs * NT; c += 16) {
-                    uint32_t v[16];
-                    if (empty || dead) {
-#pragma unroll
-                        for (int i = 0; i < 16; ++i) v[i] = __float_as_uint(dead ? nan : 0.0f);
-                    } else {
+                if (!empty && !dead) {
+                    float4 *o4 = reinterpret_cast<float4 *>(ws) + 32 * sw + lane;
+                    const int groups = (o.nrows + 3) / 4;
+                    for (int c = 0; c < pairs * NT; c += 16) {
+                        uint32_t v[16];
                         tmem_ld16(t_o + quarter + c, v);
-                    }
-                    const int d = (c / NT) * 128 + 32 * sw + lane, col = c % NT;
-                    if (direct) {
-                        // two lanes exchange, so that each stores a pair of elements of one row
 #pragma unroll
-                        for (int i = 0; i < 16; i += 2) {
-                            const float a = __uint_as_float(v[i]) * fs[col + i], b = __uint_as_float(v[i + 1]) * fs[col + i + 1];
-                            const bool odd = lane & 1;
-                            const float got = __shfl_xor_sync(0xffffffffu, odd ? a : b, 1);
-                            const int row = col + i + (odd ? 1 : 0);
-                            if (row < o.nrows)
-                                *reinterpret_cast<uint32_t *>(p.out + off[row] + (d & ~1)) = odd ? bf16x2(got, b) : bf16x2(a, got);
-                        }
-                    } else {
-#pragma unroll
-                        for (int i = 0; i < 16; ++i)
-                            if (col + i < o.nrows) ws[static_cast<long long>(col + i) * p.R + d] = __uint_as_float(v[i]);
+                        for (int i = 0; i < 16; i += 4)
+                            if ((c % NT + i) / 4 < groups)
+                                o4[(c + i) / 4 * 128] = make_float4(__uint_as_float(v[i]), __uint_as_float(v[i + 1]),
+                                                                    __uint_as_float(v[i + 2]), __uint_as_float(v[i + 3]));
                     }
                 }
-                tc_fence_before();
             }
-            soft_sync();  // fs, off and ex are used again
+            tc_fence_before();
+            soft_sync();  // the shared buffers are used again
         }
     } else {
-        // ------------------------------------------------------------------ queries
-        const int tid = threadIdx.x - 192;
+        // ----- the queries, the rotated elements' ring, and the tiles ahead into the L2 cache
         const int units = (2 * pairs + 1) * 8, width = p.R + p.E;
-        int piece = 0;
-        while (walk.next(p, r, o)) {
+        int n = 0, rslot = 0;
+        unsigned rph = 0;
+        bool ok = true;
+        while (ok && walk.next(p, r, o)) {
             if (o.k0 >= o.k1) continue;
-            if (!__all_sync(0xffffffffu, piece == 0 || wait_or_stop(qempty, (piece - 1) & 1, &stop))) break;
-            for (int i = tid; i < NT * units; i += 64) {
-                const int row = i / units, u = i % units;
-                // rows past the piece and elements past the width are 0
-                const bool in = row < o.nrows && 8 * u < width;
-                const int rr = in ? o.row0 + row : o.row0;
-                const uint16_t *src = p.q + (o.s.q0 + rr / p.H) * p.q_token + (rr % p.H) * p.q_head + (in ? 8 * u : 0);
-                copy16(s_q + (u >> 3) * qchunk + row * 128 + (((u & 7) ^ (row & 7)) << 4), src, in ? 16 : 0);
+            if (!(ok = pieces == 0 || all_wait(qempty, (pieces - 1) & 1, &stop))) break;
+            ++pieces;
+            if (p.q_even) {
+                // rows past the sequence's are the next one's (or zeros past the last): their
+                // products are columns of S^T that nothing reads
+                if (elect()) {
+                    const int row = o.s.q0 * p.H + o.row0;
+                    bar_expect_tx(qfull, static_cast<unsigned>((2 * pairs + 1) * qchunk));
+                    tma_3d(s_q, &p.qv, 0, row, 0, qfull);
+                    tc05::tma_load_2d(s_q + 2 * pairs * qchunk, &p.qr, 0, row, qfull);
+                }
+                __syncwarp();
+            } else {
+                int tok = o.s.q0 + o.row0 / p.H, head = o.row0 % p.H;
+                for (int row = 0; row < NT; ++row) {
+                    // rows past the piece and elements past the width are 0
+                    const bool in = row < o.nrows;
+                    const uint16_t *src = in ? p.q + tok * p.q_token + head * p.q_head : p.q;
+#pragma unroll 3
+                    for (int u = lane; u < units; u += 32)
+                        copy16(s_q + (u >> 3) * qchunk + row * 128 + (((u & 7) ^ (row & 7)) << 4),
+                               in && 8 * u < width ? src + 8 * u : p.q, in && 8 * u < width ? 16 : 0);
+                    if (++head == p.H) {
+                        head = 0;
+                        ++tok;
+                    }
+                }
+                asm volatile("cp.async.wait_all;" ::: "memory");
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                __syncwarp();
+                if (lane == 0) bar_arrive(qfull);
             }
-            asm volatile("cp.async.wait_all;" ::: "memory");
-            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-            __syncwarp();
-            if (lane == 0) bar_arrive(qfull);
-            ++piece;
+            Pages pages(p, o);
+            for (int k = o.k0; ok && k < o.k1; ++k, ++n) {
+                pages.step(p, k);
+                const int copies = alike(pages.copies), step = pages.rows * 128;
+                const int row = alike(pages.row);
+                int page[kMaxCopies];
+#pragma unroll
+                for (int f = 0; f < kMaxCopies; ++f)
+                    if (f < copies) page[f] = alike(pages.page(f));
+                if (!(ok = n < RS || all_wait(rempty + 8 * rslot, rph ^ 1, &stop))) break;
+                if (!stall) rissued = n + 1;
+                const uint32_t dst = s_r + rslot * kChunk, bar = rfull + 8 * rslot;
+                if (elect()) {
+                    bar_expect_tx(bar, static_cast<unsigned>(copies * step));
+                    if (!stall) {
+#pragma unroll
+                        for (int f = 0; f < kMaxCopies; ++f)
+                            if (f < copies) tma_3d(dst + f * step, &p.tr, 0, row, page[f], bar);
+                    }
+                }
+                __syncwarp();
+                if (++rslot == RS) {
+                    rslot = 0;
+                    rph ^= 1;
+                }
+                // the pages' rows lie back to back: one request a copy, for all of their bytes
+                if (p.page_bytes && k + kPrefetch < o.k1) {
+                    const int ahead = pages.ahead(k + kPrefetch, lane);
+                    const int arow = pages.whole ? ((k + kPrefetch) * kTile) % p.page_size : 0;
+                    if (lane < (pages.whole ? 1 : kTile / pages.rows) && ahead >= 0 && ahead < p.pages &&
+                        (k + kPrefetch) * kTile + lane * pages.rows < o.s.len)
+                        l2_ahead(p.cache + ahead * p.page_bytes + static_cast<long long>(arow) * 2 * width,
+                                 static_cast<unsigned>(pages.rows * 2 * width));
+                }
+            }
         }
     }
     __syncwarp();
-    // a producer that was stopped: its copies have landed before the shared memory goes
-    if (warp == 0 && lane == 0 && *reinterpret_cast<volatile int *>(&stop)) {
-        const unsigned long long w0 = global_ns();
-        for (int i = max(0, issued - S); i < issued; ++i)
-            while (!bar_try(vfull + 8 * (i % S), (i / S) & 1))
-                if (static_cast<long long>(global_ns() - w0) > kWaitLimitNs) break;
-        for (int i = max(0, rissued - RS); i < rissued; ++i)
-            while (!bar_try(rfull + 8 * (i % RS), (i / RS) & 1))
-                if (static_cast<long long>(global_ns() - w0) > kWaitLimitNs) break;
+    // after a stop: the copies issued have landed before the shared memory goes
+    if (lane == 0 && *reinterpret_cast<volatile int *>(&stop)) {
+        if (warp == 0)
+            for (int i = max(0, issued - S); i < issued; ++i) landed(vfull + 8 * (i % S), (i / S) & 1);
+        if (warp == 7) {
+            for (int i = max(0, rissued - RS); i < rissued; ++i) landed(rfull + 8 * (i % RS), (i / RS) & 1);
+            if (pieces > 0) landed(qfull, (pieces - 1) & 1);
+        }
     }
     tc_fence_before();
     __syncthreads();
-    if (threadIdx.x == 0 && stop) atomicOr(p.err, 1);
+    if (threadIdx.x == 32 && stop) atomicOr(p.err, 1);
     if (warp == 1) {
         tc_fence_after();
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmem) : "memory");
@@ -847,93 +1045,93 @@ __global__ void __launch_bounds__(kThreads, 1) latent_attention_kernel(const __g
 }
 
 // ------------------------------------------------------------------ joining partial results
-// One block takes one row of one sequence that several shares hold a piece of: cw warps wide
-// (128 elements each), pw warps taking every pw-th piece, added in that order.
+// A warp takes 32 elements of four rows of a split sequence and every pw-th piece; a block's pw
+// warps of the same elements are added in that order.
 __global__ void __launch_bounds__(512) latent_join_kernel(const __grid_constant__ LatentParams p) {
-    __shared__ int part[32], found[3];
-    __shared__ __align__(16) float acc[16][128];
-    __shared__ float lsum[16];
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    if (threadIdx.x == 0) found[0] = -1;
-    __syncthreads();
+    __shared__ __align__(16) float4 acc[16][32], lacc[16], tacc[16];
     pdl_launch_dependents();
-    const int per = (p.B + static_cast<int>(blockDim.x) - 1) / static_cast<int>(blockDim.x);
-    const int b0 = min(p.B, static_cast<int>(threadIdx.x) * per), b1 = min(p.B, b0 + per);
-    int sum = 0, units;
-    for (int b = b0; b < b1; ++b) sum += tiles_of(seq_of(p, b));
-    int at = block_prefix(sum, part, &units);
-    const int ge = min(p.groups, max(units, 1));
-    const int seg = blockIdx.x;
-    // by sequence: the seg-th sequence; else the one that share seg + 1 begins inside of, if it
-    // is the first share to do so
-    const int u = p.by_seq ? 0 : (seg + 1 < ge ? share_begin(units, seg + 1, ge) : units);
-    for (int b = b0; b < b1; ++b) {
-        const int kt = tiles_of(seq_of(p, b));
-        if (p.by_seq ? b == seg : (u > at && u < at + kt && share_begin(units, seg, ge) <= at)) {
-            found[0] = b;
-            found[1] = at;
-            found[2] = kt;
-        }
-        at += kt;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    // a sequence without tokens has no pieces, and no descriptor
+    if (p.by_seq && seq_of(p, blockIdx.x).n == 0) {
+        pdl_wait();
+        return;
     }
-    __syncthreads();
     pdl_wait();
-    if (found[0] < 0 || found[2] == 0) return;
-    const int begin = found[1], end = found[1] + found[2];
-    // first and last share that hold a tile of it
-    int g0 = static_cast<int>(static_cast<long long>(begin) * ge / units);
-    while (g0 + 1 < ge && share_begin(units, g0 + 1, ge) <= begin) ++g0;
-    while (share_begin(units, g0, ge) > begin) --g0;
-    int g1 = static_cast<int>(static_cast<long long>(end - 1) * ge / units);
-    while (g1 + 1 < ge && share_begin(units, g1 + 1, ge) <= end - 1) ++g1;
-    while (share_begin(units, g1, ge) > end - 1) --g1;
-    if (g0 == g1) return;
-    const Seq s = seq_of(p, found[0]);
-    const int rr = blockIdx.y, r = rr / p.nt, i = rr % p.nt;
-    if (rr >= s.n * p.H) return;
-
-    const long long size = static_cast<long long>(p.nt) * (p.R + 2);
-    auto slot = [&](int g) { return p.ws + ((static_cast<long long>(g) * p.rt + r) * 2 + (g == g0 ? 1 : 0)) * size; };
+    const int4 d = reinterpret_cast<const int4 *>(p.ws)[blockIdx.x];
+    const int g0 = d.z, g1 = d.w;
+    if (g1 < 0) return;
+    const int row0 = 4 * static_cast<int>(blockIdx.y), r = row0 / p.nt, i = row0 % p.nt, rows = d.y * p.H;
+    if (row0 >= rows) return;
+    auto slot = [&](int g) { return slot_of(p, g * p.rt + r, g == g0 ? 1 : 0, p.nt); };
     const float inf = __int_as_float(0x7f800000);
-    float top = -inf;
-    for (int g = g0 + lane; g <= g1; g += 32) top = fmaxf(top, slot(g)[p.nt * p.R + i]);
+    const int wp = warp / p.cw, slab = static_cast<int>(blockIdx.z) * p.cw + warp % p.cw;  // 32 elements
+    const int at = ((slab >> 2) * (p.nt / 4) + i / 4) * 128 + (slab & 3) * 32 + lane;
+    // running maxima, sums and elements of the four rows, a batch of pieces loaded at once
+    float top[4], l[4], a[4];
 #pragma unroll
-    for (int d = 16; d >= 1; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-    if (top == -inf) top = 0.0f;
-    const int wp = warp / p.cw, col = (blockIdx.z * p.cw + warp % p.cw) * 128 + 4 * lane;
-    float4 a = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    float l = 0.0f;
-#pragma unroll 4
-    for (int g = g0 + wp; g <= g1; g += p.pw) {
-        const float *w = slot(g);
-        const float f = ex2(w[p.nt * p.R + i] - top);  // 0 for a piece without a key
-        const float4 v = *reinterpret_cast<const float4 *>(w + static_cast<long long>(i) * p.R + col);
-        if (f != 0.0f) {
-            l = fmaf(f, w[p.nt * p.R + p.nt + i], l);
-            a.x = fmaf(f, v.x, a.x);
-            a.y = fmaf(f, v.y, a.y);
-            a.z = fmaf(f, v.z, a.z);
-            a.w = fmaf(f, v.w, a.w);
+    for (int e = 0; e < 4; ++e) {
+        top[e] = -inf;
+        l[e] = a[e] = 0.0f;
+    }
+    auto add = [&](float m, float lv, float v, int e) {
+        // a piece that has no key for the row (m = -inf) holds nothing: its O was not written
+        const float t = fmaxf(top[e], m);
+        const float f = top[e] == t ? 1.0f : ex2(top[e] - t), h = m == t ? 1.0f : ex2(m - t);
+        if (m != -inf) {
+            l[e] = fmaf(l[e], f, lv * h);
+            a[e] = fmaf(a[e], f, v * h);
+            top[e] = t;
+        }
+    };
+    constexpr int kBatch = 5;
+    for (int g = g0 + wp; g <= g1; g += kBatch * p.pw) {
+        float4 m[kBatch], lv[kBatch], v[kBatch];
+#pragma unroll
+        for (int q = 0; q < kBatch; ++q) {
+            const float *w = slot(min(g + q * p.pw, g1));
+            m[q] = *reinterpret_cast<const float4 *>(w + p.nt * p.R + i);
+            lv[q] = *reinterpret_cast<const float4 *>(w + p.nt * p.R + p.nt + i);
+            v[q] = reinterpret_cast<const float4 *>(w)[at];
+        }
+#pragma unroll
+        for (int q = 0; q < kBatch; ++q)
+            if (g + q * p.pw <= g1) {
+                add(m[q].x, lv[q].x, v[q].x, 0);
+                add(m[q].y, lv[q].y, v[q].y, 1);
+                add(m[q].z, lv[q].z, v[q].z, 2);
+                add(m[q].w, lv[q].w, v[q].w, 3);
+            }
+    }
+    if (p.pw > 1) {
+        acc[warp][lane] = make_float4(a[0], a[1], a[2], a[3]);
+        if (lane == 0) {
+            auto kept = [&](int e) { return l[e] != l[e] ? l[e] : top[e]; };  // NaN whatever the maximum
+            tacc[warp] = make_float4(kept(0), kept(1), kept(2), kept(3));
+            lacc[warp] = make_float4(l[0], l[1], l[2], l[3]);
+        }
+        __syncthreads();
+        if (wp > 0) return;
+        for (int w = 1; w < p.pw; ++w) {
+            const float4 m = tacc[w * p.cw + warp], x = lacc[w * p.cw + warp], v = acc[w * p.cw + warp][lane];
+            add(m.x, x.x, v.x, 0);
+            add(m.y, x.y, v.y, 1);
+            add(m.z, x.z, v.z, 2);
+            add(m.w, x.w, v.w, 3);
         }
     }
-    *reinterpret_cast<float4 *>(&acc[warp][4 * lane]) = a;
-    if (lane == 0) lsum[warp] = l;
-    __syncthreads();
-    if (wp > 0) return;
-    for (int w = 1; w < p.pw; ++w) {
-        const float4 v = *reinterpret_cast<const float4 *>(&acc[w * p.cw + warp][4 * lane]);
-        a.x += v.x;
-        a.y += v.y;
-        a.z += v.z;
-        a.w += v.w;
-        l += lsum[w * p.cw + warp];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        const int row = row0 + e;
+        const float v = l[e] == 0.0f ? 0.0f : a[e] / l[e];
+        const float other = __shfl_xor_sync(0xffffffffu, v, 1);
+        if (row < rows) {
+            const long long tok = d.x + row / p.H, head = row % p.H;
+            if (!(lane & 1))
+                *reinterpret_cast<uint32_t *>(p.out + tok * p.out_token + head * p.out_head + 32 * slab + lane) = bf16x2(v, other);
+            if (p.lse && slab == 0 && lane == 0)
+                p.lse[tok * p.lse_token + head] = l[e] == 0.0f ? -inf : (top[e] + log2f(l[e])) * 0.69314718056f;
+        }
     }
-    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-    const long long tok = s.q0 + rr / p.H, head = rr % p.H;
-    uint32_t *out = reinterpret_cast<uint32_t *>(p.out + tok * p.out_token + head * p.out_head + col);
-    out[0] = bf16x2(a.x * inv, a.y * inv);
-    out[1] = bf16x2(a.z * inv, a.w * inv);
-    if (p.lse && col == 0) p.lse[tok * p.lse_token + head] = l == 0.0f ? -inf : (top + log2f(l)) * 0.69314718056f;
 }
 
 const void *kernel_of(int nt) {
@@ -955,7 +1153,7 @@ Split split_of(const sgemm_latent_attention_t &a, int sms) {
     s.rt = static_cast<int>((rows + s.nt - 1) / s.nt);
     const long long tiles = std::max(1LL, (static_cast<long long>(a.table_width) * a.page_size + kTile - 1) / kTile);
     s.groups = static_cast<int>(std::max(1LL, std::min<long long>(sms / s.rt, tiles * a.B)));
-    s.ws_bytes = s.groups > 1 ? static_cast<long long>(s.groups) * s.rt * 2 * s.nt * (a.R + 2) * 4 : 0;
+    s.ws_bytes = s.groups > 1 ? (s.groups + 3) / 4 * 64 + static_cast<long long>(s.groups) * s.rt * 2 * s.nt * (a.R + 2) * 4 : 0;
     return s;
 }
 
@@ -991,6 +1189,22 @@ PFN_cuTensorMapEncodeTiled_v12000 encoder() {
 bool encode_maps(LatentParams &p, const sgemm_latent_attention_t &a) {
     auto enc = encoder();
     if (!enc) return false;
+    if (p.q_even) {
+        const cuuint64_t n = static_cast<cuuint64_t>(a.total_q) * static_cast<cuuint64_t>(a.H);
+        const cuuint64_t step = static_cast<cuuint64_t>(a.H > 1 ? a.q_head : a.q_token) * 2;
+        const cuuint32_t ones[3] = {1, 1, 1}, nt = static_cast<cuuint32_t>(p.nt), chunks = static_cast<cuuint32_t>(a.R / 64);
+        const cuuint64_t dims[3] = {64, n, chunks}, strides[2] = {step, 128};
+        const cuuint32_t box[3] = {64, nt, chunks};
+        const cuuint64_t rdims[2] = {static_cast<cuuint64_t>(a.E), n}, rstrides[1] = {step};
+        const cuuint32_t rbox[2] = {64, nt};
+        if (enc(&p.qv, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<uint16_t *>(a.q), dims, strides, box, ones,
+                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS ||
+            enc(&p.qr, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<uint16_t *>(a.q) + a.R, rdims, rstrides, rbox, ones,
+                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+            return false;
+    }
     const cuuint32_t rows = static_cast<cuuint32_t>(std::min(kTile, a.page_size));
     const cuuint64_t ps = static_cast<cuuint64_t>(a.page_size), pages = static_cast<cuuint64_t>(a.pages);
     const cuuint64_t rs = static_cast<cuuint64_t>(a.row_stride) * 2, pg = static_cast<cuuint64_t>(a.page_stride) * 2;
@@ -1064,6 +1278,11 @@ extern "C" sgemm_status_t sgemm_bf16_latent_attention(const sgemm_latent_attenti
     if (st != SGEMM_OK) return st;
     const Split sp = split_of(*a, sms);
     if (sp.ws_bytes > 0 && (!a->workspace || a->workspace_bytes < sp.ws_bytes)) return SGEMM_ERR_NO_WORKSPACE;
+    p.nt = sp.nt;
+    // one stride from each (token, head) row to the next, wide enough that rows are apart (a
+    // tensor map's strides are)
+    const long long step = a->H > 1 ? a->q_head : a->q_token;
+    p.q_even = (a->H == 1 || a->total_q == 1 || a->q_token == a->H * a->q_head) && step >= W && step < (1LL << 38) ? 1 : 0;
     if (!encode_maps(p, *a)) return SGEMM_ERR_CUDA;
     p.q = a->q;
     p.table = a->block_table;
@@ -1087,17 +1306,22 @@ extern "C" sgemm_status_t sgemm_bf16_latent_attention(const sgemm_latent_attenti
     p.R = a->R;
     p.E = a->E;
     p.max_q = a->max_q;
-    p.nt = sp.nt;
     p.rt = sp.rt;
     p.groups = sp.groups;
     p.scale_log2 = static_cast<float>(static_cast<double>(a->scale) * 1.4426950408889634);
     p.flags = static_cast<int>(a->flags);
 
-    const int fixed = (a->R / 64 + 1) * sp.nt * 128 + 2 * kChunk + 1024;
-    p.rope_slots = sp.nt == 64 ? 2 : 3;
-    const int room = static_cast<int>(kMaxSmemOptin) - kStaticSmem - fixed - p.rope_slots * kChunk;
-    p.slots = std::min(kMaxSlots, room / kSlot);
-    const int smem = fixed + p.rope_slots * kChunk + p.slots * kSlot;
+    p.cache = reinterpret_cast<const uint8_t *>(a->cache);
+    p.page_bytes = a->row_stride == W ? a->page_stride * 2 : 0;
+    p.out16 = aligned(a->out, 16) && a->out_token % 8 == 0 && a->out_head % 8 == 0 ? 1 : 0;
+    p.by_seq = a->B < sp.groups ? 1 : 0;
+    // Shared memory: Q, two buffers of weights, the rotated elements' ring, then as many slots of
+    // latent elements as there is room for.  With 64 rows one slot of rotated elements: it is
+    // needed last of a tile and free again first, and makes room for two whole tiles of slots.
+    p.rope_slots = sp.nt == 64 ? 1 : 3;
+    const int fixed = (a->R / 64 + 1) * sp.nt * 128 + 2 * kChunk + p.rope_slots * kChunk + kBarBytes + 40 * sp.nt + 16;
+    p.slots = std::min(kMaxSlots, (static_cast<int>(kMaxSmemOptin) - fixed) / kSlot);
+    const int smem = fixed + p.slots * kSlot;
     const void *fn = kernel_of(sp.nt);
     {
         // once per kernel and device: allow the shared memory
@@ -1116,17 +1340,14 @@ extern "C" sgemm_status_t sgemm_bf16_latent_attention(const sgemm_latent_attenti
                (a->flags & SGEMM_FLAG_PDL) != 0, &p) != cudaSuccess)
         return SGEMM_ERR_CUDA;
     if (sp.groups == 1) return SGEMM_OK;
-    // sequences that may be split: each at most once by sequence, or by the shares' beginnings
-    p.by_seq = a->B < sp.groups ? 1 : 0;
-    p.nseg = p.by_seq ? a->B : sp.groups - 1;
-    const int parts = p.by_seq ? (sp.groups + a->B - 1) / a->B + 1 : 2;
-    const int blocks = a->R / 128;
-    p.cw = parts > 16 ? 1 : blocks;
-    p.pw = parts > 16 ? 16 : parts > 4 ? 4 : parts > 2 ? 2 : 1;
-    const dim3 grid(static_cast<unsigned>(p.nseg),
-                    static_cast<unsigned>(std::min<long long>(static_cast<long long>(sp.rt) * sp.nt,
-                                                              static_cast<long long>(a->max_q) * a->H)),
-                    static_cast<unsigned>(blocks / p.cw));
+    // a block of the joining kernel for 4 rows: up to 16 warps, over elements (32 each) and over
+    // the pieces that a sequence may have
+    const int parts = p.by_seq ? (sp.groups + a->B - 1) / a->B + 1 : 2, slabs = a->R / 32;
+    p.pw = parts > 40 ? 16 : parts > 20 ? 8 : parts > 10 ? 4 : parts > 5 ? 2 : 1;
+    p.cw = std::min(slabs, std::max(1, 4 / p.pw));
+    const long long rows = static_cast<long long>(a->max_q) * a->H;
+    const dim3 grid(static_cast<unsigned>(p.by_seq ? a->B : sp.groups), static_cast<unsigned>((rows + 3) / 4),
+                    static_cast<unsigned>(slabs / p.cw));
     if (launch(reinterpret_cast<const void *>(&latent_join_kernel), grid, dim3(static_cast<unsigned>(32 * p.cw * p.pw)), 0,
                cs, true, &p) != cudaSuccess)
         return SGEMM_ERR_CUDA;
