@@ -67,8 +67,27 @@ constexpr int kMaxSlots = 12;
 constexpr int kMaxRopeSlots = 3;
 constexpr int kThreads = 256;            // producer, first product, 4 softmax, second product, queries
 constexpr int kPrefetch = 2;             // tiles that are fetched into the L2 cache ahead of the copies
+constexpr float kLazy = 8.0f;            // log2 of the largest weight before a maximum moves
+constexpr float kNoMax = -3.4028234e38f;  // no score is smaller: the maximum of none
 constexpr int kMaxCopies = 8;            // copies of a chunk of a tile: pages of at least 8 rows
 constexpr int kBarBytes = 384;           // the mbarriers
+
+// Division by a number of the call, exact for 0 <= n < 2^30: n m / 2^s with m = ceil(2^s / d),
+// s = 30 + ceil(log2 d).  (A division by a number the compiler does not know takes 100 cycles and
+// more, and the warps here wait for a chain of them before the first copy.)
+struct Divisor {
+    unsigned m;
+    int s, d;
+    static Divisor of(int d) {
+        int l = 0;
+        while ((1LL << l) < d) ++l;
+        return {static_cast<unsigned>(((1ULL << (30 + l)) + d - 1) / d), 30 + l, d};
+    }
+    __device__ __forceinline__ int div(int n) const {
+        return static_cast<int>((static_cast<unsigned long long>(static_cast<unsigned>(n)) * m) >> s);
+    }
+    __device__ __forceinline__ int mod(int n) const { return n - div(n) * d; }
+};
 
 struct LatentParams {
     CUtensorMap tv;  // the latent part: {64, page rows, R / 64, pages}
@@ -87,6 +106,9 @@ struct LatentParams {
     int B, H, R, E, max_q;
     int nt, rt, groups;     // rows a CTA, CTAs a group, groups
     int slots, rope_slots;  // rings
+    Divisor heads, ctas;    // by H, by rt
+    Divisor page_tiles;     // by the tiles of a page (pages of whole tiles)
+    int row_shift;          // log2 of the rows of one copy: of a tile, or of a page where that is smaller
     float scale_log2;       // scale * log2(e)
     int flags;
     int q_even;   // the queries' rows are evenly spaced: copied with TMA
@@ -94,7 +116,7 @@ struct LatentParams {
     long long page_bytes;  // from page to page, where a page's rows lie back to back; else 0
     const uint8_t *cache;
     int by_seq;   // descriptors of split sequences: one a sequence, else one a group
-    int cw, pw;   // the joining kernel's block: warps for elements, warps for pieces
+    int pw;       // warps of the joining kernel that share a sequence's pieces
 };
 
 // ------------------------------------------------------------------ the work's line of tiles
@@ -133,9 +155,14 @@ __device__ __forceinline__ int tiles_of(const Seq &s) {
     return s.n > 0 ? max(1, (s.len + kTile - 1) / kTile) : 0;
 }
 
-__device__ __forceinline__ int share_begin(int units, int g, int groups) {
-    return static_cast<int>(static_cast<long long>(units) * g / groups);
+// a b / c for counts of tiles and groups (the quotient fits 32 bits): in 32 bits where that
+// holds the product.
+__device__ __forceinline__ int mul_div(int a, int b, int c) {
+    if (a < (1 << 20) && b < (1 << 11)) return static_cast<int>(static_cast<unsigned>(a * b) / static_cast<unsigned>(c));
+    return static_cast<int>(static_cast<long long>(a) * b / c);
 }
+
+__device__ __forceinline__ int share_begin(int units, int g, int groups) { return mul_div(units, g, groups); }
 
 // A group's share of the line.
 struct Share {
@@ -221,7 +248,7 @@ struct Walk {
             if (take == 0 || o.row0 >= rows) continue;
             o.nrows = min(p.nt, rows - o.row0);
             // keys that the piece's last row sees
-            const int seen = o.s.len - o.s.n_all + (o.row0 + o.nrows - 1) / p.H + 1;
+            const int seen = o.s.len - o.s.n_all + p.heads.div(o.row0 + o.nrows - 1) + 1;
             o.k1 = max(o.k0, min(o.k0 + take, (max(seen, 0) + kTile - 1) / kTile));
             return true;
         }
@@ -233,53 +260,60 @@ struct Walk {
 // tiles), a batch ahead.  A tile is copied in `copies` pieces of `rows` rows of a page each.
 struct Pages {
     const int *table;
-    int rows, per, page_size, limit;  // rows a copy, copies a whole tile; rows the sequence has
-    int first;                        // the first tile of the batch in `now`
+    int rows, shift, per;  // rows a copy, log2 of the copies of a whole tile, their number
+    int limit;             // rows the sequence has, as far as the piece goes
+    int first;             // the first tile of the batch in `now`
     int now, next;
-    int k, copies, row;               // the current tile, its copies, the first one's row in its page
-    int bad;                          // the page that reads as zeros
-    bool whole;                       // a tile lies in one page
+    int k, copies, row;    // the current tile, its copies, the first one's row in its page
+    int pages;             // (the page past the last one reads as zeros)
+    bool whole;            // a tile lies in one page
 
-    __device__ __forceinline__ int look(int tile) const {
+    // the table's entry for copy f of a tile, -1 past the piece's end
+    __device__ __forceinline__ int look(const LatentParams &p, int tile, int f) const {
+        if (tile * kTile + f * rows >= limit) return -1;
+        return table[whole ? p.page_tiles.div(tile) : (tile << shift) + f];
+    }
+    __device__ __forceinline__ int look(const LatentParams &p, int tile) const {
         const int lane = threadIdx.x & 31;
-        const int key = (tile + lane / per) * kTile + (lane % per) * rows;
-        return key < limit ? table[key / page_size] : -1;
+        return look(p, tile + (lane >> shift), lane & (per - 1));
     }
     __device__ __forceinline__ Pages(const LatentParams &p, const Piece &o) {
         table = p.table + static_cast<long long>(o.b) * p.ldt;
-        page_size = p.page_size;
-        rows = min(kTile, page_size);
-        per = kTile / rows;
-        whole = per == 1;
+        rows = 1 << p.row_shift;
+        shift = 6 - p.row_shift;
+        per = 1 << shift;
+        whole = p.page_size >= kTile;
         limit = min(o.s.len, o.k1 * kTile);
-        bad = p.pages;
+        pages = p.pages;
         first = o.k0;
-        now = look(first);
-        next = look(first + 32 / per);
+        now = look(p, first);
+        next = look(p, first + (32 >> shift));
+        row = whole ? p.page_tiles.mod(first) * kTile - kTile : 0;
     }
+    // on to a tile: the first one, then one by one
     __device__ __forceinline__ void step(const LatentParams &p, int tile) {
         k = tile;
-        if (k == first + 32 / per) {
+        if (k == first + (32 >> shift)) {
             first = k;
             now = next;
-            next = look(k + 32 / per);
+            next = look(p, k + (32 >> shift));
         }
-        const int keys = min(kTile, limit - k * kTile);
-        copies = (keys + rows - 1) / rows;
-        row = whole ? (k * kTile) % page_size : 0;
-        // an entry out of range among those that are used is reported; it reads as zeros
-        const int lane = threadIdx.x & 31;
-        const int mine = __shfl_sync(0xffffffffu, now, ((k - first) * per + lane) & 31);
-        if (lane < copies && (mine < 0 || mine >= bad)) atomicOr(p.err, kErrBadIndex);
+        copies = (min(kTile, limit - k * kTile) + rows - 1) >> p.row_shift;
+        if (whole) {
+            row += kTile;
+            if (row == p.page_size) row = 0;
+        }
     }
-    // the page of copy f of the current tile
-    __device__ __forceinline__ int page(int f) const {
-        const int v = __shfl_sync(0xffffffffu, now, (k - first) * per + f);
-        return v < 0 || v >= bad ? bad : v;
+    // the page of copy f of the current tile; an entry out of range is reported
+    __device__ __forceinline__ int page(const LatentParams &p, int f) const {
+        const int v = __shfl_sync(0xffffffffu, now, ((k - first) << shift) + f);
+        if (v >= 0 && v < pages) return v;
+        if ((threadIdx.x & 31) == 0) atomicOr(p.err, kErrBadIndex);
+        return pages;
     }
-    // the table's entry for copy f of a tile at most a batch ahead (a lane's f of no copy: any)
+    // the table's entry for copy f of a tile at most a batch ahead
     __device__ __forceinline__ int ahead(int tile, int f) const {
-        const int at = (tile - first) * per + (f < per ? f : 0);
+        const int at = ((tile - first) << shift) + (f & (per - 1));
         const int x = __shfl_sync(0xffffffffu, now, at & 31), y = __shfl_sync(0xffffffffu, next, at & 31);
         return at < 32 ? x : y;
     }
@@ -501,7 +535,7 @@ __global__ void __launch_bounds__(kThreads, 1) latent_attention_kernel(const __g
     const uint32_t sfull = qempty + 8, sempty = sfull + 16, pfull = sempty + 16, pvd = pfull + 16, fin = pvd + 16;
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int g = static_cast<int>(blockIdx.x) / p.rt, r = static_cast<int>(blockIdx.x) % p.rt;
+    const int g = p.ctas.div(static_cast<int>(blockIdx.x)), r = static_cast<int>(blockIdx.x) - g * p.rt;
 
     if (warp == 0) {
         if (lane == 0) {
@@ -512,26 +546,14 @@ __global__ void __launch_bounds__(kThreads, 1) latent_attention_kernel(const __g
                 prefetch_tmap(&p.qr);
             }
             stop = 0;
-            for (int i = 0; i < kMaxSlots; ++i) {
-                bar_init(vfull + 8 * i, 1);
-                bar_init(vempty + 8 * i, 1);
-            }
-            for (int i = 0; i < kMaxRopeSlots; ++i) {
-                bar_init(rfull + 8 * i, 1);
-                bar_init(rempty + 8 * i, 1);
-            }
-            bar_init(qfull, 1);
-            bar_init(qempty, 1);
-            for (int i = 0; i < 2; ++i) {
-                bar_init(sfull + 8 * i, 1);
-                bar_init(sempty + 8 * i, 4);
-                bar_init(pfull + 8 * i, 4);
-                bar_init(pvd + 8 * i, 1);
-                bar_init(fin + 8 * i, 1);
-            }
-            asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         }
+        // in the order of their addresses: the softmax warps arrive one by one on sempty, pfull
+        for (int i = lane; i < (static_cast<int>(fin - vfull) >> 3) + 2; i += 32) {
+            const uint32_t bar = vfull + 8 * i;
+            bar_init(bar, bar >= sempty && bar < pvd ? 4 : 1);
+        }
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         __syncwarp();
     }
     if (p.flags & kFlagPdl) pdl_wait();
@@ -576,7 +598,7 @@ __global__ void __launch_bounds__(kThreads, 1) latent_attention_kernel(const __g
                 int page[kMaxCopies];
 #pragma unroll
                 for (int f = 0; f < kMaxCopies; ++f)
-                    if (f < copies) page[f] = alike(pages.page(f));
+                    if (f < copies) page[f] = alike(pages.page(p, f));
                 for (int j = 0; j < pairs; ++j) {
                     if (!(ok = at < S || all_wait(vempty + 8 * slot, ph ^ 1, &stop))) break;
                     if (!stall) issued = at + 1;
@@ -698,7 +720,9 @@ __global__ void __launch_bounds__(kThreads, 1) latent_attention_kernel(const __g
         while (walk.next(p, r, o)) {
             if (tell && o.first) {
                 const int u_last = sh.u0 + (sh.u1 - sh.u0 - o.left) + tiles_of(o.s) - 1;
-                const int g1 = static_cast<int>((static_cast<long long>(u_last + 1) * sh.groups - 1) / sh.units);
+                // the last share that begins at or before u_last: ceil((u_last + 1) groups / units) - 1
+                int g1 = mul_div(u_last + 1, sh.groups, sh.units);
+                if (share_begin(sh.units, g1, sh.groups) > u_last) --g1;
                 if (p.by_seq || !o.last) desc[p.by_seq ? o.b : g] = make_int4(o.s.q0, o.s.n, g, o.last ? -1 : g1);
             }
             float m[NC], l[NC];
@@ -706,16 +730,15 @@ __global__ void __launch_bounds__(kThreads, 1) latent_attention_kernel(const __g
 #pragma unroll
             for (int c = 0; c < NC; ++c) {
                 const int col = 8 * (c >> 1) + c0 + (c & 1);
-                m[c] = -inf;
+                m[c] = kNoMax;
                 l[c] = 0.0f;
-                lim[c] = col < o.nrows ? o.s.len - o.s.n_all + (o.row0 + col) / p.H + 1 : 0;
+                lim[c] = col < o.nrows ? o.s.len - o.s.n_all + p.heads.div(o.row0 + col) + 1 : 0;
             }
-            const int lim_min = max(0, o.s.len - o.s.n_all + o.row0 / p.H + 1);
+            const int lim_min = max(0, o.s.len - o.s.n_all + p.heads.div(o.row0) + 1);
             for (int k = o.k0; k < o.k1 && !dead; ++k, ++n) {
                 ok = wait_or_stop(sfull + 8 * (n & 1), (n >> 1) & 1, &stop) && ok;
                 ok = __all_sync(0xffffffffu, ok);
-                uint32_t sr[4 * (NT / 8)];
-                float s[4 * (NT / 8)];
+                uint32_t sr[4 * (NT / 8)] = {};
                 if (ok) {
                     tc_fence_after();
                     tmem_ld_s(tmem + quarter + (n & 1) * kSCols, sr);
@@ -724,29 +747,40 @@ __global__ void __launch_bounds__(kThreads, 1) latent_attention_kernel(const __g
                 }
                 __syncwarp();
                 if (lane == 0) bar_arrive(sempty + 8 * (n & 1));
+                // exponents: scores in base 2 less the maximum in use; over a lazy threshold some
+                // maximum has to move
                 const int key = k * kTile + 16 * sw + (lane >> 2);
                 const bool edge = (k + 1) * kTile > lim_min || o.nrows < NT;
-                bool over = !ok;
+                float x[4 * (NT / 8)];
+                auto hide = [&]() {
+#pragma unroll
+                    for (int i = 0; i < NT / 8; ++i)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            if (key + 8 * (e >> 1) >= lim[2 * i + (e & 1)]) x[4 * i + e] = -inf;
+                };
 #pragma unroll
                 for (int i = 0; i < NT / 8; ++i)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const int c = 2 * i + (e & 1);
-                        float v = ok ? __uint_as_float(sr[4 * i + e]) * p.scale_log2 : 0.0f;
-                        if (edge && key + 8 * (e >> 1) >= lim[c]) v = -inf;
-                        s[4 * i + e] = v;
-                        over |= v > m[c] + 8.0f;
-                    }
-                if (soft_any(over)) {
+                    for (int e = 0; e < 4; ++e)
+                        x[4 * i + e] = fmaf(__uint_as_float(sr[4 * i + e]), p.scale_log2, -m[2 * i + (e & 1)]);
+                if (edge) hide();
+                float most = -inf;
+#pragma unroll
+                for (int i = 0; i < 4 * (NT / 8); ++i) most = fmaxf(most, x[i]);
+                if (soft_any(most > kLazy || !ok)) {
                     if (soft_any(!ok)) {
                         dead = true;
                         break;
                     }
                     float f[NC];
 #pragma unroll
+                    for (int i = 0; i < 4 * (NT / 8); ++i) x[i] = __uint_as_float(sr[i]) * p.scale_log2;
+                    if (edge) hide();
+#pragma unroll
                     for (int c = 0; c < NC; ++c) {
                         const int i = c >> 1, e = c & 1;
-                        float v = fmaxf(s[4 * i + e], s[4 * i + 2 + e]);
+                        float v = fmaxf(x[4 * i + e], x[4 * i + 2 + e]);
 #pragma unroll
                         for (int d = 4; d <= 16; d <<= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, d));
                         f[c] = v;
@@ -761,17 +795,19 @@ __global__ void __launch_bounds__(kThreads, 1) latent_attention_kernel(const __g
                         float2 v = make_float2(m[2 * i], m[2 * i + 1]);
 #pragma unroll
                         for (int w = 0; w < 4; ++w) {
-                            const float2 x = *reinterpret_cast<const float2 *>(&ex[n & 1][w][8 * i + c0]);
-                            v.x = fmaxf(v.x, x.x);
-                            v.y = fmaxf(v.y, x.y);
+                            const float2 y = *reinterpret_cast<const float2 *>(&ex[n & 1][w][8 * i + c0]);
+                            v.x = fmaxf(v.x, y.x);
+                            v.y = fmaxf(v.y, y.y);
                         }
                         const float nm[2] = {v.x, v.y};
 #pragma unroll
                         for (int e = 0; e < 2; ++e) {
                             const int c = 2 * i + e;
-                            f[c] = nm[e] == m[c] ? 1.0f : ex2(m[c] - nm[e]);  // 0 from -inf
+                            f[c] = ex2(m[c] - nm[e]);
                             l[c] *= f[c];
                             m[c] = nm[e];
+                            x[4 * i + e] -= nm[e];
+                            x[4 * i + 2 + e] -= nm[e];
                         }
                     }
                     if (k > o.k0) {
@@ -827,7 +863,7 @@ __global__ void __launch_bounds__(kThreads, 1) latent_attention_kernel(const __g
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
                             const int c = 2 * i + (e & 1);
-                            w[e] = ex2(s[4 * i + e] - (m[c] == -inf ? 0.0f : m[c]));
+                            w[e] = ex2(x[4 * i + e]);
                             l[c] += w[e];
                         }
                         const int at = ((i ^ (lane >> 2)) << 4) + 2 * c0;  // key_in % 8 = lane / 4
@@ -865,7 +901,7 @@ __global__ void __launch_bounds__(kThreads, 1) latent_attention_kernel(const __g
                 // read in the 16 x 256-bit form again, whose fragments stmatrix stores turned.
                 long long *off = reinterpret_cast<long long *>(&ex[(n & 1) ^ 1][0][0]);
                 if (tid < NT) {
-                    const int row = o.row0 + tid, tok = o.s.q0 + row / p.H, head = row % p.H;
+                    const int row = o.row0 + tid, tok = o.s.q0 + p.heads.div(row), head = p.heads.mod(row);
                     off[tid] = tok * p.out_token + head * p.out_head;
                     const float sum = total(tid);
                     if (p.lse && tid < o.nrows)
@@ -928,7 +964,7 @@ __global__ void __launch_bounds__(kThreads, 1) latent_attention_kernel(const __g
                     const float sum = total(tid);
                     // a NaN score leaves the maximum alone: the piece's is then NaN itself, so
                     // that joining keeps it whatever the maximum
-                    ws[NT * p.R + tid] = dead || sum != sum ? nan : ms[tid];
+                    ws[NT * p.R + tid] = dead || sum != sum ? nan : sum == 0.0f ? -inf : ms[tid];
                     ws[NT * p.R + NT + tid] = dead ? nan : sum;
                 }
                 if (!empty && !dead) {
@@ -969,7 +1005,7 @@ __global__ void __launch_bounds__(kThreads, 1) latent_attention_kernel(const __g
                 }
                 __syncwarp();
             } else {
-                int tok = o.s.q0 + o.row0 / p.H, head = o.row0 % p.H;
+                int tok = o.s.q0 + p.heads.div(o.row0), head = p.heads.mod(o.row0);
                 for (int row = 0; row < NT; ++row) {
                     // rows past the piece and elements past the width are 0
                     const bool in = row < o.nrows;
@@ -991,12 +1027,28 @@ __global__ void __launch_bounds__(kThreads, 1) latent_attention_kernel(const __g
             Pages pages(p, o);
             for (int k = o.k0; ok && k < o.k1; ++k, ++n) {
                 pages.step(p, k);
+                // near the piece's end: the next one's queries, table entries and first tiles
+                if (p.page_bytes && k == max(o.k0, o.k1 - 4)) {
+                    Walk then = walk;
+                    Piece q;
+                    if (then.next(p, r, q) && q.k0 < q.k1) {
+                        const Pages to(p, q);
+                        const int tile = q.k0 + (lane >> to.shift);
+                        if (tile < q.k0 + kPrefetch && to.now >= 0 && to.now < p.pages)
+                            l2_ahead(p.cache + to.now * p.page_bytes +
+                                         static_cast<long long>(to.whole ? p.page_tiles.mod(tile) * kTile : 0) * 2 * width,
+                                     static_cast<unsigned>(to.rows * 2 * width));
+                        if (lane == 31 && p.q_even && p.q_head == width)
+                            l2_ahead(p.q + (static_cast<long long>(q.s.q0) * p.H + q.row0) * width,
+                                     static_cast<unsigned>(q.nrows * 2 * width));
+                    }
+                }
                 const int copies = alike(pages.copies), step = pages.rows * 128;
                 const int row = alike(pages.row);
                 int page[kMaxCopies];
 #pragma unroll
                 for (int f = 0; f < kMaxCopies; ++f)
-                    if (f < copies) page[f] = alike(pages.page(f));
+                    if (f < copies) page[f] = alike(pages.page(p, f));
                 if (!(ok = n < RS || all_wait(rempty + 8 * rslot, rph ^ 1, &stop))) break;
                 if (!stall) rissued = n + 1;
                 const uint32_t dst = s_r + rslot * kChunk, bar = rfull + 8 * rslot;
@@ -1016,8 +1068,8 @@ __global__ void __launch_bounds__(kThreads, 1) latent_attention_kernel(const __g
                 // the pages' rows lie back to back: one request a copy, for all of their bytes
                 if (p.page_bytes && k + kPrefetch < o.k1) {
                     const int ahead = pages.ahead(k + kPrefetch, lane);
-                    const int arow = pages.whole ? ((k + kPrefetch) * kTile) % p.page_size : 0;
-                    if (lane < (pages.whole ? 1 : kTile / pages.rows) && ahead >= 0 && ahead < p.pages &&
+                    const int arow = pages.whole ? p.page_tiles.mod(k + kPrefetch) * kTile : 0;
+                    if (lane < pages.per && ahead >= 0 && ahead < p.pages &&
                         (k + kPrefetch) * kTile + lane * pages.rows < o.s.len)
                         l2_ahead(p.cache + ahead * p.page_bytes + static_cast<long long>(arow) * 2 * width,
                                  static_cast<unsigned>(pages.rows * 2 * width));
@@ -1045,92 +1097,143 @@ __global__ void __launch_bounds__(kThreads, 1) latent_attention_kernel(const __g
 }
 
 // ------------------------------------------------------------------ joining partial results
-// A warp takes 32 elements of four rows of a split sequence and every pw-th piece; a block's pw
-// warps of the same elements are added in that order.
-__global__ void __launch_bounds__(512) latent_join_kernel(const __grid_constant__ LatentParams p) {
-    __shared__ __align__(16) float4 acc[16][32], lacc[16], tacc[16];
+// A warp takes ES slabs of 32 elements of four rows of a split sequence, PB pieces at a time; the
+// pw warps of a block with the same elements take every pw-th PB pieces and are added in their
+// order.  Lane 4 q + e works out the weight of piece q for row e.  Few pieces (a batch of
+// sequences): 4 at a time and 128 elements, so that a weight serves 16 products.  Many (a long
+// sequence over all groups): 8 at a time, up to 32 warps, so that all are read at once.
+template <int PB, int ES>
+__global__ void __launch_bounds__(PB == 8 ? 1024 : 128) latent_join_kernel(const __grid_constant__ LatentParams p) {
+    constexpr int kWarps = PB == 8 ? 32 : 1;  // warps that share elements
+    __shared__ __align__(16) float4 acc[kWarps][32];
+    __shared__ float tacc[kWarps][4], lacc[kWarps][4];
     pdl_launch_dependents();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    // a sequence without tokens has no pieces, and no descriptor
-    if (p.by_seq && seq_of(p, blockIdx.x).n == 0) {
-        pdl_wait();
-        return;
-    }
-    pdl_wait();
-    const int4 d = reinterpret_cast<const int4 *>(p.ws)[blockIdx.x];
-    const int g0 = d.z, g1 = d.w;
-    if (g1 < 0) return;
-    const int row0 = 4 * static_cast<int>(blockIdx.y), r = row0 / p.nt, i = row0 % p.nt, rows = d.y * p.H;
-    if (row0 >= rows) return;
-    auto slot = [&](int g) { return slot_of(p, g * p.rt + r, g == g0 ? 1 : 0, p.nt); };
-    const float inf = __int_as_float(0x7f800000);
-    const int wp = warp / p.cw, slab = static_cast<int>(blockIdx.z) * p.cw + warp % p.cw;  // 32 elements
+    const int row0 = 4 * static_cast<int>(blockIdx.y), i = row0 & (p.nt - 1), r = row0 / p.nt;
+    // many: the block's warps share one slab; few: each has its own ES slabs
+    const int wp = PB == 8 ? warp : 0;
+    const int slab = PB == 8 ? static_cast<int>(blockIdx.z) : warp * ES;
     const int at = ((slab >> 2) * (p.nt / 4) + i / 4) * 128 + (slab & 3) * 32 + lane;
-    // running maxima, sums and elements of the four rows, a batch of pieces loaded at once
-    float top[4], l[4], a[4];
+    const float inf = __int_as_float(0x7f800000);
+    // a sequence without tokens has no pieces, and no descriptor
+    const bool none = p.by_seq && seq_of(p, blockIdx.x).n == 0;
+    pdl_wait();
+    if (none) return;
+    const int4 d = reinterpret_cast<const int4 *>(p.ws)[blockIdx.x];
+    const int g0 = d.z, g1 = d.w, rows = d.y * p.H;
+    if (g1 < 0 || row0 >= rows) return;
+    auto slot = [&](int g) { return slot_of(p, g * p.rt + r, g == g0 ? 1 : 0, p.nt); };
+
+    const int e = lane & 3, mine_at = (lane >> 2) & (PB - 1);
+    float top = -inf, l = 0.0f;  // of row e, the same in all its lanes
+    float4 a[ES];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-        top[e] = -inf;
-        l[e] = a[e] = 0.0f;
-    }
-    auto add = [&](float m, float lv, float v, int e) {
-        // a piece that has no key for the row (m = -inf) holds nothing: its O was not written
-        const float t = fmaxf(top[e], m);
-        const float f = top[e] == t ? 1.0f : ex2(top[e] - t), h = m == t ? 1.0f : ex2(m - t);
-        if (m != -inf) {
-            l[e] = fmaf(l[e], f, lv * h);
-            a[e] = fmaf(a[e], f, v * h);
-            top[e] = t;
-        }
-    };
-    constexpr int kBatch = 5;
-    for (int g = g0 + wp; g <= g1; g += kBatch * p.pw) {
-        float4 m[kBatch], lv[kBatch], v[kBatch];
+    for (int c = 0; c < ES; ++c) a[c] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    for (int g = g0 + PB * wp; g <= g1; g += PB * p.pw) {
+        const int mine = g + mine_at;
+        const float *ml = slot(min(mine, g1)) + p.nt * p.R + i + e;
+        float m = ml[0], lm = ml[p.nt];
+        float4 v[PB][ES];
 #pragma unroll
-        for (int q = 0; q < kBatch; ++q) {
-            const float *w = slot(min(g + q * p.pw, g1));
-            m[q] = *reinterpret_cast<const float4 *>(w + p.nt * p.R + i);
-            lv[q] = *reinterpret_cast<const float4 *>(w + p.nt * p.R + p.nt + i);
-            v[q] = reinterpret_cast<const float4 *>(w)[at];
-        }
+        for (int q = 0; q < PB; ++q)
+            if (g + q <= g1) {
+                const float4 *o4 = reinterpret_cast<const float4 *>(slot(g + q)) + at;
 #pragma unroll
-        for (int q = 0; q < kBatch; ++q)
-            if (g + q * p.pw <= g1) {
-                add(m[q].x, lv[q].x, v[q].x, 0);
-                add(m[q].y, lv[q].y, v[q].y, 1);
-                add(m[q].z, lv[q].z, v[q].z, 2);
-                add(m[q].w, lv[q].w, v[q].w, 3);
+                for (int c = 0; c < ES; ++c) v[q][c] = o4[32 * c];
             }
-    }
-    if (p.pw > 1) {
-        acc[warp][lane] = make_float4(a[0], a[1], a[2], a[3]);
-        if (lane == 0) {
-            auto kept = [&](int e) { return l[e] != l[e] ? l[e] : top[e]; };  // NaN whatever the maximum
-            tacc[warp] = make_float4(kept(0), kept(1), kept(2), kept(3));
-            lacc[warp] = make_float4(l[0], l[1], l[2], l[3]);
-        }
-        __syncthreads();
-        if (wp > 0) return;
-        for (int w = 1; w < p.pw; ++w) {
-            const float4 m = tacc[w * p.cw + warp], x = lacc[w * p.cw + warp], v = acc[w * p.cw + warp][lane];
-            add(m.x, x.x, v.x, 0);
-            add(m.y, x.y, v.y, 1);
-            add(m.z, x.z, v.z, 2);
-            add(m.w, x.w, v.w, 3);
-        }
-    }
+        if (mine > g1) m = -inf;
+        float t = m;
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-        const int row = row0 + e;
-        const float v = l[e] == 0.0f ? 0.0f : a[e] / l[e];
-        const float other = __shfl_xor_sync(0xffffffffu, v, 1);
-        if (row < rows) {
-            const long long tok = d.x + row / p.H, head = row % p.H;
-            if (!(lane & 1))
-                *reinterpret_cast<uint32_t *>(p.out + tok * p.out_token + head * p.out_head + 32 * slab + lane) = bf16x2(v, other);
-            if (p.lse && slab == 0 && lane == 0)
-                p.lse[tok * p.lse_token + head] = l[e] == 0.0f ? -inf : (top[e] + log2f(l[e])) * 0.69314718056f;
+        for (int o = 4; o < 4 * PB; o <<= 1) t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, o));
+        t = fmaxf(t, top);
+        const float base = t == -inf ? 0.0f : t;
+        const float f = ex2(top - base);
+        // a piece that has no key for the row (m = -inf) holds nothing: its O was not written
+        const float w = m == -inf ? 0.0f : ex2(m - base);
+        float lw = m == -inf ? 0.0f : w * lm;
+#pragma unroll
+        for (int o = 4; o < 4 * PB; o <<= 1) lw += __shfl_xor_sync(0xffffffffu, lw, o);
+        l = l * f + lw;
+        top = t;
+        const float f0 = __shfl_sync(0xffffffffu, f, 0), f1 = __shfl_sync(0xffffffffu, f, 1);
+        const float f2 = __shfl_sync(0xffffffffu, f, 2), f3 = __shfl_sync(0xffffffffu, f, 3);
+#pragma unroll
+        for (int c = 0; c < ES; ++c) a[c] = make_float4(a[c].x * f0, a[c].y * f1, a[c].z * f2, a[c].w * f3);
+#pragma unroll
+        for (int q = 0; q < PB; ++q) {
+            const float w0 = __shfl_sync(0xffffffffu, w, 4 * q), w1 = __shfl_sync(0xffffffffu, w, 4 * q + 1);
+            const float w2 = __shfl_sync(0xffffffffu, w, 4 * q + 2), w3 = __shfl_sync(0xffffffffu, w, 4 * q + 3);
+#pragma unroll
+            for (int c = 0; c < ES; ++c) {
+                a[c].x = w0 == 0.0f ? a[c].x : fmaf(w0, v[q][c].x, a[c].x);
+                a[c].y = w1 == 0.0f ? a[c].y : fmaf(w1, v[q][c].y, a[c].y);
+                a[c].z = w2 == 0.0f ? a[c].z : fmaf(w2, v[q][c].z, a[c].z);
+                a[c].w = w3 == 0.0f ? a[c].w : fmaf(w3, v[q][c].w, a[c].w);
+            }
         }
+    }
+    if constexpr (PB == 8) {
+        if (p.pw > 1) {
+            acc[warp][lane] = a[0];
+            if (lane < 4) {
+                tacc[warp][e] = top;
+                lacc[warp][e] = l;
+            }
+            __syncthreads();
+            if (wp > 0) return;
+            // the same once more, over the warps: lane 4 q + e has row e of warps q, q + 8, ...
+            float m[4], f[4], t = -inf;
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                const int w = mine_at + 8 * c;
+                m[c] = w < p.pw ? tacc[w][e] : -inf;
+                t = fmaxf(t, m[c]);
+            }
+#pragma unroll
+            for (int o = 4; o <= 16; o <<= 1) t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, o));
+            const float base = t == -inf ? 0.0f : t;
+            l = 0.0f;
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                const int w = mine_at + 8 * c;
+                f[c] = ex2(m[c] - base);
+                // the sum of a warp whose scores were NaN is NaN though its maximum may be -inf
+                const float x = w < p.pw ? lacc[w][e] : 0.0f;
+                l += f[c] == 0.0f && x == x ? 0.0f : f[c] * x;
+            }
+#pragma unroll
+            for (int o = 4; o <= 16; o <<= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+            top = t;
+            float4 s4 = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+                for (int q = 0; q < 8 && 8 * c + q < p.pw; ++q) {
+                    const float4 v = acc[8 * c + q][lane];
+                    s4.x = fmaf(__shfl_sync(0xffffffffu, f[c], 4 * q), v.x, s4.x);
+                    s4.y = fmaf(__shfl_sync(0xffffffffu, f[c], 4 * q + 1), v.y, s4.y);
+                    s4.z = fmaf(__shfl_sync(0xffffffffu, f[c], 4 * q + 2), v.z, s4.z);
+                    s4.w = fmaf(__shfl_sync(0xffffffffu, f[c], 4 * q + 3), v.w, s4.w);
+                }
+            a[0] = s4;
+        }
+    }
+    const float inv_e = l == 0.0f ? 0.0f : 1.0f / l;
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+        const int row = row0 + c;
+        const float inv = __shfl_sync(0xffffffffu, inv_e, c);
+        const long long tok = d.x + p.heads.div(row), head = p.heads.mod(row);
+        uint16_t *out = p.out + tok * p.out_token + head * p.out_head + 32 * slab + lane;
+#pragma unroll
+        for (int z = 0; z < ES; ++z) {
+            const float v = (c == 0 ? a[z].x : c == 1 ? a[z].y : c == 2 ? a[z].z : a[z].w) * inv;
+            const float other = __shfl_xor_sync(0xffffffffu, v, 1);
+            if (row < rows && !(lane & 1)) *reinterpret_cast<uint32_t *>(out + 32 * z) = bf16x2(v, other);
+        }
+    }
+    if (p.lse && slab == 0 && lane < 4 && row0 + lane < rows) {
+        const long long tok = d.x + p.heads.div(row0 + lane), head = p.heads.mod(row0 + lane);
+        p.lse[tok * p.lse_token + head] = l == 0.0f ? -inf : (top + log2f(l)) * 0.69314718056f;
     }
 }
 
@@ -1312,6 +1415,10 @@ extern "C" sgemm_status_t sgemm_bf16_latent_attention(const sgemm_latent_attenti
     p.flags = static_cast<int>(a->flags);
 
     p.cache = reinterpret_cast<const uint8_t *>(a->cache);
+    p.heads = Divisor::of(a->H);
+    p.ctas = Divisor::of(sp.rt);
+    p.page_tiles = Divisor::of(std::max(1, a->page_size / kTile));
+    p.row_shift = a->page_size >= kTile ? 6 : a->page_size == 32 ? 5 : a->page_size == 16 ? 4 : 3;
     p.page_bytes = a->row_stride == W ? a->page_stride * 2 : 0;
     p.out16 = aligned(a->out, 16) && a->out_token % 8 == 0 && a->out_head % 8 == 0 ? 1 : 0;
     p.by_seq = a->B < sp.groups ? 1 : 0;
@@ -1340,16 +1447,17 @@ extern "C" sgemm_status_t sgemm_bf16_latent_attention(const sgemm_latent_attenti
                (a->flags & SGEMM_FLAG_PDL) != 0, &p) != cudaSuccess)
         return SGEMM_ERR_CUDA;
     if (sp.groups == 1) return SGEMM_OK;
-    // a block of the joining kernel for 4 rows: up to 16 warps, over elements (32 each) and over
-    // the pieces that a sequence may have
-    const int parts = p.by_seq ? (sp.groups + a->B - 1) / a->B + 1 : 2, slabs = a->R / 32;
-    p.pw = parts > 40 ? 16 : parts > 20 ? 8 : parts > 10 ? 4 : parts > 5 ? 2 : 1;
-    p.cw = std::min(slabs, std::max(1, 4 / p.pw));
+    // pieces that a sequence may have: by the line's equal shares, if all sequences were as long
+    // as the table allows; few are joined by one warp, many by up to 32
+    const int parts = p.by_seq ? (sp.groups + a->B - 1) / a->B + 1 : 2;
+    const bool few = parts <= 8;
+    p.pw = few ? 1 : std::min(32, (parts + 7) / 8);
     const long long rows = static_cast<long long>(a->max_q) * a->H;
     const dim3 grid(static_cast<unsigned>(p.by_seq ? a->B : sp.groups), static_cast<unsigned>((rows + 3) / 4),
-                    static_cast<unsigned>(slabs / p.cw));
-    if (launch(reinterpret_cast<const void *>(&latent_join_kernel), grid, dim3(static_cast<unsigned>(32 * p.cw * p.pw)), 0,
-               cs, true, &p) != cudaSuccess)
+                    static_cast<unsigned>(few ? 1 : a->R / 32));
+    const void *join = few ? reinterpret_cast<const void *>(&latent_join_kernel<4, 4>)
+                           : reinterpret_cast<const void *>(&latent_join_kernel<8, 1>);
+    if (launch(join, grid, dim3(static_cast<unsigned>(32 * (few ? a->R / 128 : p.pw))), 0, cs, true, &p) != cudaSuccess)
         return SGEMM_ERR_CUDA;
     return SGEMM_OK;
 }
