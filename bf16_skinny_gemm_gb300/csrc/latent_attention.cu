@@ -20,11 +20,11 @@
 //        O^T[R, NT]       += K[:, :R]^T P^T        both MN-major, M = 128 a time
 //    One copy of the tile in shared memory (64 rows x 128 bytes per chunk of 64
 //    elements, 128-byte swizzle) serves as A of both products.
-//  * Warp 0 streams the tiles with TMA into a ring of slots (two chunks, 128
-//    latent elements, a slot; the E elements in a ring of their own).  Slots
+//  * Warp 0 and the last one stream the tiles with TMA into a ring of slots (two
+//    chunks, 128 latent elements, a slot; the E elements in a ring of their own).  Slots
 //    rather than tiles: a slot is free again as soon as its part of O^T is
 //    done, and what is left of shared memory beside Q holds 1.75 to 2.5 tiles.
-//  * Warp 1 issues the first product, warp 6 the second.  Two warps, because
+//  * Warp 1 issues the first product (and copies the queries), the last but one the second.  Two warps, because
 //    neither may wait for the other's operands: O^T of tile t is issued as soon
 //    as its weights are there, which frees the tile's slots, and S^T of tile
 //    t + 1 as its slots arrive.
@@ -35,7 +35,6 @@
 //    more than 2^8 (in units of the result), else the old one stands: one
 //    barrier with a vote a tile.  The weights are then at most 2^8, and neither
 //    their rounding to BF16 nor the FP32 sums care about that factor.
-//  * Warp 7 copies the queries of the next piece of work (any strides).
 //
 // Work split.  The tiles of all sequences form one line, cut into equal shares,
 // one for each group of CTAs (a group has a CTA for each NT rows of a sequence
@@ -65,8 +64,13 @@ constexpr int kChunk = kTile * 64 * 2;   // 64 keys x 64 elements
 constexpr int kSlot = 2 * kChunk;        // 128 latent elements (M of the second product)
 constexpr int kMaxSlots = 12;
 constexpr int kMaxRopeSlots = 3;
-constexpr int kThreads = 256;            // producer, first product, 4 softmax, second product, queries
-constexpr int kPrefetch = 2;             // tiles that are fetched into the L2 cache ahead of the copies
+// Warps: copies, first product, 4 soft_parts of softmax, second product, copies.
+__host__ __device__ constexpr int soft_parts(int nt) { return nt == 64 ? 2 : 1; }
+// Buffers of weights, 8 KiB each.  With 64 rows one: it is read long before it is written again,
+// and what it frees holds a second slot of rotated elements beside two whole tiles of latent ones.
+__host__ __device__ constexpr int weight_buffers(int nt) { return nt == 64 ? 1 : 2; }
+__host__ __device__ constexpr int threads_of(int nt) { return 128 + 128 * soft_parts(nt); }
+constexpr int kPieceCost = 1;            // see tiles_of
 constexpr float kLazy = 8.0f;            // log2 of the largest weight before a maximum moves
 constexpr float kNoMax = -3.4028234e38f;  // no score is smaller: the maximum of none
 constexpr int kMaxCopies = 8;            // copies of a chunk of a tile: pages of at least 8 rows
@@ -113,8 +117,6 @@ struct LatentParams {
     int flags;
     int q_even;   // the queries' rows are evenly spaced: copied with TMA
     int out16;    // out's rows start on 16 bytes
-    long long page_bytes;  // from page to page, where a page's rows lie back to back; else 0
-    const uint8_t *cache;
     int by_seq;   // descriptors of split sequences: one a sequence, else one a group
     int pw;       // warps of the joining kernel that share a sequence's pieces
 };
@@ -149,10 +151,11 @@ __device__ __forceinline__ Seq seq_of(const LatentParams &p, int b) {
     return s;
 }
 
-// Tiles of a sequence on the line: at least one where it has tokens (their results are
-// written though they see nothing).
+// Length of a sequence on the line: its tiles, and before them what turning to it costs a CTA
+// (its queries, the last piece's result), in tiles.  At least one where it has tokens (their
+// results are written though they see nothing).
 __device__ __forceinline__ int tiles_of(const Seq &s) {
-    return s.n > 0 ? max(1, (s.len + kTile - 1) / kTile) : 0;
+    return s.n > 0 ? max(1, (s.len + kTile - 1) / kTile + kPieceCost) : 0;
 }
 
 // a b / c for counts of tiles and groups (the quotient fits 32 bits): in 32 bits where that
@@ -237,7 +240,8 @@ struct Walk {
             const int take = min(kt - k, left);
             o.b = b;
             o.left = left;
-            o.k0 = k;
+            o.k0 = max(0, k - kPieceCost);
+            const int end = max(0, k + take - kPieceCost);
             o.first = k == 0;
             o.last = k + take == kt;
             o.row0 = r * p.nt;
@@ -249,7 +253,7 @@ struct Walk {
             o.nrows = min(p.nt, rows - o.row0);
             // keys that the piece's last row sees
             const int seen = o.s.len - o.s.n_all + p.heads.div(o.row0 + o.nrows - 1) + 1;
-            o.k1 = max(o.k0, min(o.k0 + take, (max(seen, 0) + kTile - 1) / kTile));
+            o.k1 = max(o.k0, min(end, (max(seen, 0) + kTile - 1) / kTile));
             return true;
         }
         return false;
@@ -311,12 +315,6 @@ struct Pages {
         if ((threadIdx.x & 31) == 0) atomicOr(p.err, kErrBadIndex);
         return pages;
     }
-    // the table's entry for copy f of a tile at most a batch ahead
-    __device__ __forceinline__ int ahead(int tile, int f) const {
-        const int at = ((tile - first) << shift) + (f & (per - 1));
-        const int x = __shfl_sync(0xffffffffu, now, at & 31), y = __shfl_sync(0xffffffffu, next, at & 31);
-        return at < 32 ? x : y;
-    }
 };
 
 // ------------------------------------------------------------------------------- primitives
@@ -353,17 +351,21 @@ __device__ __forceinline__ bool all_wait(uint32_t b, unsigned parity, int *stop)
 // tcgen05.mma and the copies want them.
 __device__ __forceinline__ int alike(int v) { return static_cast<int>(__reduce_or_sync(0xffffffffu, static_cast<unsigned>(v))); }
 
-// Barrier of the 128 softmax threads, alone or with the OR of a predicate.
-__device__ __forceinline__ void soft_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
+// Barrier of the N softmax threads, alone or with the OR of a predicate.
+template <int N>
+__device__ __forceinline__ void soft_sync() {
+    asm volatile("bar.sync 1, %0;" ::"n"(N) : "memory");
+}
+template <int N>
 __device__ __forceinline__ bool soft_any(bool v) {
     uint32_t r;
     asm volatile(
         "{\n\t.reg .pred p, q;\n\t"
         "setp.ne.b32 p, %1, 0;\n\t"
-        "bar.red.or.pred q, 1, 128, p;\n\t"
+        "bar.red.or.pred q, 1, %2, p;\n\t"
         "selp.u32 %0, 1, 0, q;\n\t}"
         : "=r"(r)
-        : "r"(v ? 1u : 0u)
+        : "r"(v ? 1u : 0u), "n"(N)
         : "memory");
     return r != 0;
 }
@@ -419,17 +421,22 @@ __device__ __forceinline__ void tma_3d(uint32_t dst, const CUtensorMap *map, int
         : "memory");
 }
 __device__ __forceinline__ void tma_4d(uint32_t dst, const CUtensorMap *map, int c0, int c1, int c2, int c3,
-                                       uint32_t bar) {
+                                       uint32_t bar, uint64_t policy) {
     asm volatile(
-        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
-        "[%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(bar)
+        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint "
+        "[%0], [%1, {%2, %3, %4, %5}], [%6], %7;" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(bar), "l"(policy)
         : "memory");
 }
 
-// Bytes (16-byte aligned, a multiple of 16) into the L2 cache.
-__device__ __forceinline__ void l2_ahead(const void *src, unsigned bytes) {
-    asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(src), "r"(bytes) : "memory");
+// How the L2 cache keeps what is copied: evicted first where this CTA is its only reader.
+__device__ __forceinline__ uint64_t policy_of(bool once) {
+    uint64_t r;
+    if (once)
+        asm("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(r));
+    else
+        asm("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(r));
+    return r;
 }
 
 // Four 8 x 8 BF16 fragments, each stored turned: lane l gives the address of row l % 8 (its
@@ -506,10 +513,14 @@ __device__ __forceinline__ uint32_t finite_or_zero(uint32_t w) {
 
 // ----------------------------------------------------------------------------- the kernel
 template <int NT>
-__global__ void __launch_bounds__(kThreads, 1) latent_attention_kernel(const __grid_constant__ LatentParams p) {
+__global__ void __launch_bounds__(threads_of(NT), 1) latent_attention_kernel(const __grid_constant__ LatentParams p) {
     constexpr int kSCols = NT;                    // tensor-memory columns of one S^T
     constexpr int kTmem = NT == 64 ? 512 : NT == 32 ? 256 : 128;
-    constexpr int NC = NT / 4;                    // rows a softmax thread holds scores of
+    constexpr int NP = weight_buffers(NT);
+    constexpr int W = soft_parts(NT), CT = NT / W;  // softmax warps per quarter, their rows
+    constexpr int kSoft = 128 * W;                // softmax threads
+    constexpr int kLast = 3 + 4 * W;              // the last warp
+    constexpr int NC = CT / 4;                    // rows a softmax thread holds scores of
     constexpr uint32_t kIdescS = (1u << 4) | (1u << 7) | (1u << 10) | (static_cast<uint32_t>(NT >> 3) << 17) |
                                  (static_cast<uint32_t>(kTile >> 4) << 24);
     constexpr uint32_t kIdescO = (1u << 4) | (1u << 7) | (1u << 10) | (1u << 15) | (1u << 16) |
@@ -520,7 +531,7 @@ __global__ void __launch_bounds__(kThreads, 1) latent_attention_kernel(const __g
     const int S = p.slots, RS = p.rope_slots;
     const uint32_t s_q = saddr(base);
     const uint32_t s_p = s_q + (2 * pairs + 1) * qchunk;
-    const uint32_t s_r = s_p + 2 * kChunk;
+    const uint32_t s_r = s_p + NP * kChunk;
     const uint32_t s_v = s_r + RS * kChunk;
     uint8_t *misc = base + (s_v - s_q) + S * kSlot;
     uint64_t *bars = reinterpret_cast<uint64_t *>(misc);
@@ -550,7 +561,7 @@ __global__ void __launch_bounds__(kThreads, 1) latent_attention_kernel(const __g
         // in the order of their addresses: the softmax warps arrive one by one on sempty, pfull
         for (int i = lane; i < (static_cast<int>(fin - vfull) >> 3) + 2; i += 32) {
             const uint32_t bar = vfull + 8 * i;
-            bar_init(bar, bar >= sempty && bar < pvd ? 4 : 1);
+            bar_init(bar, bar >= sempty && bar < pvd ? 4 * W : 1);
         }
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -560,7 +571,7 @@ __global__ void __launch_bounds__(kThreads, 1) latent_attention_kernel(const __g
     uint32_t tmem = 0;
     if (warp == 0) {
         // the producer goes on: it needs the mbarriers only, which are its own work
-        asm volatile("bar.arrive 2, 256;" ::: "memory");
+        asm volatile("bar.arrive 2, %0;" ::"n"(threads_of(NT)) : "memory");
     } else {
         // Tensor memory is taken after the wait: a CTA of the previous kernel may still want its
         // own, and this one holds its columns until that kernel is done.
@@ -571,7 +582,7 @@ __global__ void __launch_bounds__(kThreads, 1) latent_attention_kernel(const __g
             asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
         }
         tc_fence_before();
-        asm volatile("bar.sync 2, 256;" ::: "memory");
+        asm volatile("bar.sync 2, %0;" ::"n"(threads_of(NT)) : "memory");
         tc_fence_after();
         tmem = *tmem_slot;
         pdl_launch_dependents();
@@ -584,14 +595,18 @@ __global__ void __launch_bounds__(kThreads, 1) latent_attention_kernel(const __g
     int issued = 0, rissued = 0;  // slots of each ring that the producer filled
     int pieces = 0;               // pieces whose queries were copied
 
-    if (warp == 0) {
-        // ------------------------------------------- producer of the latent elements' ring
-        int at = 0, slot = 0;  // slots filled; the next one
-        unsigned ph = 0;       // parity of the ring's round
+    if (warp == 0 || warp == kLast) {
+        // ------------------------------------------------------------------ the copies
+        // Two warps, every other slot of latent elements each, the second the rotated elements
+        // too: one warp's wait, expect and copy take 630 cycles a slot, two warps 370.
+        const uint64_t policy = policy_of(p.rt == 1);
+        int at = 0, slot = 0, n = 0, rslot = 0;  // slots and tiles done; the rings' next slots
+        unsigned ph = 0, rph = 0;                // parities of the rings' rounds
         bool ok = true;
         while (ok && walk.next(p, r, o)) {
+            if (o.k0 >= o.k1) continue;
             Pages pages(p, o);
-            for (int k = o.k0; ok && k < o.k1; ++k) {
+            for (int k = o.k0; ok && k < o.k1; ++k, ++n) {
                 pages.step(p, k);
                 const int copies = alike(pages.copies), step = pages.rows * 128;
                 const int row = alike(pages.row);
@@ -600,30 +615,49 @@ __global__ void __launch_bounds__(kThreads, 1) latent_attention_kernel(const __g
                 for (int f = 0; f < kMaxCopies; ++f)
                     if (f < copies) page[f] = alike(pages.page(p, f));
                 for (int j = 0; j < pairs; ++j) {
-                    if (!(ok = at < S || all_wait(vempty + 8 * slot, ph ^ 1, &stop))) break;
-                    if (!stall) issued = at + 1;
-                    const uint32_t dst = s_v + slot * kSlot, bar = vfull + 8 * slot;
-                    if (elect()) {
-                        bar_expect_tx(bar, static_cast<unsigned>(2 * copies * step));
-                        if (!stall) {
-                            if (pages.whole) {
-                                tma_4d(dst, &p.tv, 0, row, 2 * j, page[0], bar);
-                            } else {
+                    if ((at & 1) == (warp == 0 ? 0 : 1)) {
+                        if (!(ok = at < S || all_wait(vempty + 8 * slot, ph ^ 1, &stop))) break;
+                        if (!stall) issued = at + 1;
+                        const uint32_t dst = s_v + slot * kSlot, bar = vfull + 8 * slot;
+                        if (elect()) {
+                            bar_expect_tx(bar, static_cast<unsigned>(2 * copies * step));
+                            if (!stall) {
+                                if (pages.whole) {
+                                    tma_4d(dst, &p.tv, 0, row, 2 * j, page[0], bar, policy);
+                                } else {
 #pragma unroll
-                                for (int f = 0; f < kMaxCopies; ++f)
-                                    if (f < copies) {
-                                        tma_4d(dst + f * step, &p.tv, 0, 0, 2 * j, page[f], bar);
-                                        tma_4d(dst + f * step + kChunk, &p.tv, 0, 0, 2 * j + 1, page[f], bar);
-                                    }
+                                    for (int f = 0; f < kMaxCopies; ++f)
+                                        if (f < copies) {
+                                            tma_4d(dst + f * step, &p.tv, 0, 0, 2 * j, page[f], bar, policy);
+                                            tma_4d(dst + f * step + kChunk, &p.tv, 0, 0, 2 * j + 1, page[f], bar, policy);
+                                        }
+                                }
                             }
                         }
+                        __syncwarp();
                     }
-                    __syncwarp();
                     ++at;
                     if (++slot == S) {
                         slot = 0;
                         ph ^= 1;
                     }
+                }
+                if (warp == 0 || !ok) continue;
+                if (!(ok = n < RS || all_wait(rempty + 8 * rslot, rph ^ 1, &stop))) break;
+                if (!stall) rissued = n + 1;
+                const uint32_t dst = s_r + rslot * kChunk, bar = rfull + 8 * rslot;
+                if (elect()) {
+                    bar_expect_tx(bar, static_cast<unsigned>(copies * step));
+                    if (!stall) {
+#pragma unroll
+                        for (int f = 0; f < kMaxCopies; ++f)
+                            if (f < copies) tma_3d(dst + f * step, &p.tr, 0, row, page[f], bar);
+                    }
+                }
+                __syncwarp();
+                if (++rslot == RS) {
+                    rslot = 0;
+                    rph ^= 1;
                 }
             }
         }
@@ -631,14 +665,48 @@ __global__ void __launch_bounds__(kThreads, 1) latent_attention_kernel(const __g
         // --------------------------------------------------- the first product, S^T = K Q^T
         // The whole warp follows the loop, one elected lane issues: a branch on the lane's
         // number in its place made every tcgen05.mma take 100 to 250 cycles to issue.
-        int n = 0, slot = 0, rslot = 0, piece = 0;
+        const int units = (2 * pairs + 1) * 8, width = p.R + p.E;
+        int n = 0, slot = 0, rslot = 0;
         unsigned ph = 0, rph = 0;  // parities of the rings' rounds
         bool ok = true;
         const uint32_t base_d = alike(static_cast<int>(tmem));
         while (ok && alike(walk.next(p, r, o) ? 1 : 0)) {
             const int tiles = alike(o.k1 - o.k0);
             if (tiles == 0) continue;
-            ok = all_wait(qfull, piece & 1, &stop);
+            // the queries, when the last piece's products have read the ones before
+            if (!(ok = pieces == 0 || all_wait(qempty, (pieces - 1) & 1, &stop))) break;
+            ++pieces;
+            if (p.q_even) {
+                // rows past the sequence's are the next one's (or zeros past the last): their
+                // products are columns of S^T that nothing reads
+                if (elect()) {
+                    const int row = o.s.q0 * p.H + o.row0;
+                    bar_expect_tx(qfull, static_cast<unsigned>((2 * pairs + 1) * qchunk));
+                    tma_3d(s_q, &p.qv, 0, row, 0, qfull);
+                    tc05::tma_load_2d(s_q + 2 * pairs * qchunk, &p.qr, 0, row, qfull);
+                }
+                __syncwarp();
+            } else {
+                int tok = o.s.q0 + p.heads.div(o.row0), head = p.heads.mod(o.row0);
+                for (int row = 0; row < NT; ++row) {
+                    // rows past the piece and elements past the width are 0
+                    const bool in = row < o.nrows;
+                    const uint16_t *src = in ? p.q + tok * p.q_token + head * p.q_head : p.q;
+#pragma unroll 3
+                    for (int u = lane; u < units; u += 32)
+                        copy16(s_q + (u >> 3) * qchunk + row * 128 + (((u & 7) ^ (row & 7)) << 4),
+                               in && 8 * u < width ? src + 8 * u : p.q, in && 8 * u < width ? 16 : 0);
+                    if (++head == p.H) {
+                        head = 0;
+                        ++tok;
+                    }
+                }
+                asm volatile("cp.async.wait_all;" ::: "memory");
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                __syncwarp();
+                if (lane == 0) bar_arrive(qfull);
+            }
+            ok = all_wait(qfull, (pieces - 1) & 1, &stop);
             for (int k = 0; ok && k < tiles; ++k, ++n) {
                 ok = n < 2 || all_wait(sempty + 8 * (n & 1), ((n >> 1) - 1) & 1, &stop);
                 const uint32_t d = base_d + (n & 1) * kSCols;
@@ -676,10 +744,9 @@ __global__ void __launch_bounds__(kThreads, 1) latent_attention_kernel(const __g
                     rph ^= 1;
                 }
             }
-            ++piece;
         }
         finish(fin, &stop);
-    } else if (warp == 6) {
+    } else if (warp == 2 + 4 * W) {
         // ----------------------------------------------- the second product, O^T += V^T P^T
         int n = 0, slot = 0;
         bool ok = true;
@@ -691,7 +758,7 @@ __global__ void __launch_bounds__(kThreads, 1) latent_attention_kernel(const __g
                 tc_fence_after();
                 for (int j = 0; j < pairs; ++j) {
                     if (elect()) {
-                        const uint64_t a = mn_desc(s_v + slot * kSlot), b = mn_desc(s_p + (n & 1) * kChunk);
+                        const uint64_t a = mn_desc(s_v + slot * kSlot), b = mn_desc(s_p + n % NP * kChunk);
 #pragma unroll
                         for (int kk = 0; kk < kTile / 16; ++kk)
                             mma(base_d + j * NT, a + kk * (2048 >> 4), b + kk * (2048 >> 4), kIdescO, kk != 0 || k != 0);
@@ -704,14 +771,14 @@ __global__ void __launch_bounds__(kThreads, 1) latent_attention_kernel(const __g
             }
         }
         finish(fin + 8, &stop);
-    } else if (warp < 6) {
+    } else if (warp < 2 + 4 * W) {
         // ------------------------------------------------------------------- softmax
         const int sw = warp & 3;  // tensor-memory lanes 32 sw .. and keys 16 sw .. of a tile
-        const int tid = threadIdx.x - 64;
+        const int tid = threadIdx.x - 64, part = (warp - 2) >> 2, col0 = part * CT;  // this warp's rows (columns of S^T)
         const int c0 = 2 * (lane & 3);
         const uint32_t quarter = static_cast<uint32_t>(32 * sw) << 16;
         const float inf = __int_as_float(0x7f800000), nan = __int_as_float(0x7fc00000);
-        int n = 0;
+        int n = 0, vslot = 0;  // tiles done; the next one's first slot
         bool ok = true, dead = false;
         // descriptors for the joining kernel: {q0, tokens, first, last group} of a split sequence
         int4 *desc = reinterpret_cast<int4 *>(p.ws);
@@ -729,7 +796,7 @@ __global__ void __launch_bounds__(kThreads, 1) latent_attention_kernel(const __g
             int lim[NC];  // keys a row sees
 #pragma unroll
             for (int c = 0; c < NC; ++c) {
-                const int col = 8 * (c >> 1) + c0 + (c & 1);
+                const int col = col0 + 8 * (c >> 1) + c0 + (c & 1);
                 m[c] = kNoMax;
                 l[c] = 0.0f;
                 lim[c] = col < o.nrows ? o.s.len - o.s.n_all + p.heads.div(o.row0 + col) + 1 : 0;
@@ -738,10 +805,10 @@ __global__ void __launch_bounds__(kThreads, 1) latent_attention_kernel(const __g
             for (int k = o.k0; k < o.k1 && !dead; ++k, ++n) {
                 ok = wait_or_stop(sfull + 8 * (n & 1), (n >> 1) & 1, &stop) && ok;
                 ok = __all_sync(0xffffffffu, ok);
-                uint32_t sr[4 * (NT / 8)] = {};
+                uint32_t sr[4 * (CT / 8)] = {};
                 if (ok) {
                     tc_fence_after();
-                    tmem_ld_s(tmem + quarter + (n & 1) * kSCols, sr);
+                    tmem_ld_s(tmem + quarter + (n & 1) * kSCols + col0, sr);
                     asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
                     tc_fence_before();
                 }
@@ -751,31 +818,31 @@ __global__ void __launch_bounds__(kThreads, 1) latent_attention_kernel(const __g
                 // maximum has to move
                 const int key = k * kTile + 16 * sw + (lane >> 2);
                 const bool edge = (k + 1) * kTile > lim_min || o.nrows < NT;
-                float x[4 * (NT / 8)];
+                float x[4 * (CT / 8)];
                 auto hide = [&]() {
 #pragma unroll
-                    for (int i = 0; i < NT / 8; ++i)
+                    for (int i = 0; i < CT / 8; ++i)
 #pragma unroll
                         for (int e = 0; e < 4; ++e)
                             if (key + 8 * (e >> 1) >= lim[2 * i + (e & 1)]) x[4 * i + e] = -inf;
                 };
 #pragma unroll
-                for (int i = 0; i < NT / 8; ++i)
+                for (int i = 0; i < CT / 8; ++i)
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
                         x[4 * i + e] = fmaf(__uint_as_float(sr[4 * i + e]), p.scale_log2, -m[2 * i + (e & 1)]);
                 if (edge) hide();
                 float most = -inf;
 #pragma unroll
-                for (int i = 0; i < 4 * (NT / 8); ++i) most = fmaxf(most, x[i]);
-                if (soft_any(most > kLazy || !ok)) {
-                    if (soft_any(!ok)) {
+                for (int i = 0; i < 4 * (CT / 8); ++i) most = fmaxf(most, x[i]);
+                if (soft_any<kSoft>(most > kLazy || !ok)) {
+                    if (soft_any<kSoft>(!ok)) {
                         dead = true;
                         break;
                     }
                     float f[NC];
 #pragma unroll
-                    for (int i = 0; i < 4 * (NT / 8); ++i) x[i] = __uint_as_float(sr[i]) * p.scale_log2;
+                    for (int i = 0; i < 4 * (CT / 8); ++i) x[i] = __uint_as_float(sr[i]) * p.scale_log2;
                     if (edge) hide();
 #pragma unroll
                     for (int c = 0; c < NC; ++c) {
@@ -787,15 +854,15 @@ __global__ void __launch_bounds__(kThreads, 1) latent_attention_kernel(const __g
                     }
                     if (lane < 4)
 #pragma unroll
-                        for (int i = 0; i < NT / 8; ++i)
-                            *reinterpret_cast<float2 *>(&ex[n & 1][sw][8 * i + c0]) = make_float2(f[2 * i], f[2 * i + 1]);
-                    soft_sync();
+                        for (int i = 0; i < CT / 8; ++i)
+                            *reinterpret_cast<float2 *>(&ex[n & 1][sw][col0 + 8 * i + c0]) = make_float2(f[2 * i], f[2 * i + 1]);
+                    soft_sync<kSoft>();
 #pragma unroll
-                    for (int i = 0; i < NT / 8; ++i) {
+                    for (int i = 0; i < CT / 8; ++i) {
                         float2 v = make_float2(m[2 * i], m[2 * i + 1]);
 #pragma unroll
                         for (int w = 0; w < 4; ++w) {
-                            const float2 y = *reinterpret_cast<const float2 *>(&ex[n & 1][w][8 * i + c0]);
+                            const float2 y = *reinterpret_cast<const float2 *>(&ex[n & 1][w][col0 + 8 * i + c0]);
                             v.x = fmaxf(v.x, y.x);
                             v.y = fmaxf(v.y, y.y);
                         }
@@ -814,19 +881,20 @@ __global__ void __launch_bounds__(kThreads, 1) latent_attention_kernel(const __g
                         // O^T of the tiles before: complete, then scaled in place
                         if (sw == 0 && lane < 4)
 #pragma unroll
-                            for (int i = 0; i < NT / 8; ++i)
-                                *reinterpret_cast<float2 *>(&fs[8 * i + c0]) = make_float2(f[2 * i], f[2 * i + 1]);
+                            for (int i = 0; i < CT / 8; ++i)
+                                *reinterpret_cast<float2 *>(&fs[col0 + 8 * i + c0]) = make_float2(f[2 * i], f[2 * i + 1]);
                         ok = wait_or_stop(pvd + 8 * ((n - 1) & 1), ((n - 1) >> 1) & 1, &stop) && ok;
-                        soft_sync();
+                        soft_sync<kSoft>();
                         tc_fence_after();
-                        for (int c = 0; c < pairs * NT; c += 16) {
-                            uint32_t v[16];
-                            tmem_ld16(t_o + quarter + c, v);
+                        for (int j = 0; j < pairs; ++j)
 #pragma unroll
-                            for (int i = 0; i < 16; ++i)
-                                v[i] = __float_as_uint(__uint_as_float(v[i]) * fs[(c + i) % NT]);
-                            tmem_st16(t_o + quarter + c, v);
-                        }
+                            for (int c = col0; c < col0 + CT; c += 16) {
+                                uint32_t v[16];
+                                tmem_ld16(t_o + quarter + j * NT + c, v);
+#pragma unroll
+                                for (int i = 0; i < 16; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * fs[c + i]);
+                                tmem_st16(t_o + quarter + j * NT + c, v);
+                            }
                         asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
                         tc_fence_before();
                     }
@@ -836,29 +904,31 @@ __global__ void __launch_bounds__(kThreads, 1) latent_attention_kernel(const __g
                     // hold must not turn that into NaN: rows past the sequence's end (never
                     // copied, or left over in the page) become 0, infinities and NaN of others 0.
                     const int r0 = max(0, lim_min - k * kTile), end = o.s.len - k * kTile;
-                    const int units = 2 * pairs * 8;
-                    for (int i = tid; i < (kTile - r0) * units; i += 128) {
-                        const int row = r0 + i / units, u = i % units, c = u >> 3;
-                        uint8_t *at = base + (s_v - s_q) + ((n * pairs + (c >> 1)) % S) * kSlot + (c & 1) * kChunk +
-                                      row * 128 + (u & 7) * 16;
-                        uint4 v = make_uint4(0u, 0u, 0u, 0u);
-                        if (row < end) {
-                            v = *reinterpret_cast<const uint4 *>(at);
-                            v.x = finite_or_zero(v.x);
-                            v.y = finite_or_zero(v.y);
-                            v.z = finite_or_zero(v.z);
-                            v.w = finite_or_zero(v.w);
+                    for (int row = r0 + (warp - 2); row < kTile; row += 4 * W)
+#pragma unroll 2
+                        for (int u = lane; u < 16 * pairs; u += 32) {
+                            int slot = vslot + (u >> 4);
+                            slot = slot >= S ? slot - S : slot;
+                            uint4 *at = reinterpret_cast<uint4 *>(base + (s_v - s_q) + slot * kSlot + ((u >> 3) & 1) * kChunk +
+                                                                  row * 128 + (u & 7) * 16);
+                            uint4 v = make_uint4(0u, 0u, 0u, 0u);
+                            if (row < end) {
+                                v = *at;
+                                v.x = finite_or_zero(v.x);
+                                v.y = finite_or_zero(v.y);
+                                v.z = finite_or_zero(v.z);
+                                v.w = finite_or_zero(v.w);
+                            }
+                            *at = v;
                         }
-                        *reinterpret_cast<uint4 *>(at) = v;
-                    }
                 }
-                // the weights, BF16 (their sum keeps FP32), into the buffer that tile n - 2 used
-                if (n >= 2) ok = wait_or_stop(pvd + 8 * (n & 1), ((n >> 1) - 1) & 1, &stop) && ok;
+                // the weights, BF16 (their sum keeps FP32), into the buffer that tile n - NP used
+                if (n >= NP) ok = wait_or_stop(pvd + 8 * ((n - NP) & 1), ((n - NP) >> 1) & 1, &stop) && ok;
                 {
                     const int key_in = 16 * sw + (lane >> 2);
-                    uint8_t *row = base + (s_p - s_q) + (n & 1) * kChunk + key_in * 128;
+                    uint8_t *row = base + (s_p - s_q) + n % NP * kChunk + key_in * 128;
 #pragma unroll
-                    for (int i = 0; i < NT / 8; ++i) {
+                    for (int i = 0; i < CT / 8; ++i) {
                         float w[4];
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
@@ -866,7 +936,7 @@ __global__ void __launch_bounds__(kThreads, 1) latent_attention_kernel(const __g
                             w[e] = ex2(x[4 * i + e]);
                             l[c] += w[e];
                         }
-                        const int at = ((i ^ (lane >> 2)) << 4) + 2 * c0;  // key_in % 8 = lane / 4
+                        const int at = (((i + col0 / 8) ^ (lane >> 2)) << 4) + 2 * c0;  // key_in % 8 = lane / 4
                         *reinterpret_cast<uint32_t *>(row + at) = bf16x2(w[0], w[1]);
                         *reinterpret_cast<uint32_t *>(row + 8 * 128 + at) = bf16x2(w[2], w[3]);
                     }
@@ -874,6 +944,8 @@ __global__ void __launch_bounds__(kThreads, 1) latent_attention_kernel(const __g
                 asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                 __syncwarp();
                 if (lane == 0) bar_arrive(pfull + 8 * (n & 1));
+                vslot += pairs;
+                if (vslot >= S) vslot -= S;
             }
             // ---------------------------------------------------------- the piece's result
             if (!dead && o.k0 < o.k1) {
@@ -886,11 +958,11 @@ __global__ void __launch_bounds__(kThreads, 1) latent_attention_kernel(const __g
                 for (int d = 4; d <= 16; d <<= 1) l[c] += __shfl_xor_sync(0xffffffffu, l[c], d);
             if (lane < 4)
 #pragma unroll
-                for (int i = 0; i < NT / 8; ++i) {
-                    *reinterpret_cast<float2 *>(&ex[n & 1][sw][8 * i + c0]) = make_float2(l[2 * i], l[2 * i + 1]);
-                    if (sw == 0) *reinterpret_cast<float2 *>(&ms[8 * i + c0]) = make_float2(m[2 * i], m[2 * i + 1]);
+                for (int i = 0; i < CT / 8; ++i) {
+                    *reinterpret_cast<float2 *>(&ex[n & 1][sw][col0 + 8 * i + c0]) = make_float2(l[2 * i], l[2 * i + 1]);
+                    if (sw == 0) *reinterpret_cast<float2 *>(&ms[col0 + 8 * i + c0]) = make_float2(m[2 * i], m[2 * i + 1]);
                 }
-            dead = soft_any(!ok || dead);
+            dead = soft_any<kSoft>(!ok || dead);
             const bool empty = o.k0 >= o.k1;
             auto total = [&](int col) {
                 return (ex[n & 1][0][col] + ex[n & 1][1][col]) + (ex[n & 1][2][col] + ex[n & 1][3][col]);
@@ -911,40 +983,44 @@ __global__ void __launch_bounds__(kThreads, 1) latent_attention_kernel(const __g
                 float inv[NC];
 #pragma unroll
                 for (int c = 0; c < NC; ++c) {
-                    const float sum = total(8 * (c >> 1) + c0 + (c & 1));
+                    const float sum = total(col0 + 8 * (c >> 1) + c0 + (c & 1));
                     inv[c] = dead ? nan : sum == 0.0f ? 0.0f : 1.0f / sum;
                 }
-                for (int j = 0; j < pairs; ++j) {
-                    constexpr int kStage = NT * 256;  // a row's 128 elements, 16-byte units swizzled
-                    const uint32_t stage = s_p + (NT == 64 ? 0 : (j & 1) * kStage);
-                    if (NT == 64 && j > 0) soft_sync();
+                // 32 rows at a time (of 128 elements, 16-byte units swizzled), alternating where
+                // there are two buffers
+                for (int turn = 0; turn < pairs * (NT > 32 ? 2 : 1); ++turn) {
+                    const int j = NT > 32 ? turn >> 1 : turn, rows0 = NT > 32 ? 32 * (turn & 1) : 0;
+                    const uint32_t stage = s_p + (NP == 2 ? (turn & 1) * kChunk : 0);
+                    if (NP == 1 && turn > 0) soft_sync<kSoft>();
+                    if (NT <= 32 || rows0 == col0)
 #pragma unroll
-                    for (int half = 0; half < 2; ++half) {
-                        uint32_t v[4 * (NT / 8)];
-                        if (empty || dead) {
+                        for (int half = 0; half < 2; ++half) {
+                            uint32_t v[4 * (CT / 8)];
+                            if (empty || dead) {
 #pragma unroll
-                            for (int i = 0; i < 4 * (NT / 8); ++i) v[i] = 0u;
-                        } else {
-                            tmem_ld_s(t_o + quarter + (static_cast<uint32_t>(16 * half) << 16) + j * NT, v);
-                            asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
-                        }
-#pragma unroll
-                        for (int i = 0; i < NT / 8; i += 2) {
-                            uint32_t q[4];
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) {
-                                const int c = 2 * (i + (e >> 1)), at = 4 * (i + (e >> 1)) + 2 * (e & 1);
-                                q[e] = bf16x2(__uint_as_float(v[at]) * inv[c], __uint_as_float(v[at + 1]) * inv[c + 1]);
+                                for (int i = 0; i < 4 * (CT / 8); ++i) v[i] = 0u;
+                            } else {
+                                tmem_ld_s(t_o + quarter + (static_cast<uint32_t>(16 * half) << 16) + j * NT + col0, v);
+                                asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
                             }
-                            const int col = 8 * (i + (lane >> 4)) + (lane & 7), unit = 4 * sw + 2 * half + ((lane >> 3) & 1);
-                            stmatrix_turned(stage + col * 256 + ((unit ^ (col & 7)) << 4), q);
+#pragma unroll
+                            for (int i = 0; i < CT / 8; i += 2) {
+                                uint32_t q[4];
+#pragma unroll
+                                for (int e = 0; e < 4; ++e) {
+                                    const int c = 2 * (i + (e >> 1)), at = 4 * (i + (e >> 1)) + 2 * (e & 1);
+                                    q[e] = bf16x2(__uint_as_float(v[at]) * inv[c], __uint_as_float(v[at + 1]) * inv[c + 1]);
+                                }
+                                const int col = col0 - rows0 + 8 * (i + (lane >> 4)) + (lane & 7);
+                                const int unit = 4 * sw + 2 * half + ((lane >> 3) & 1);
+                                stmatrix_turned(stage + col * 256 + ((unit ^ (col & 7)) << 4), q);
+                            }
                         }
-                    }
-                    soft_sync();
-                    for (int i = tid; i < o.nrows * 16; i += 128) {
+                    soft_sync<kSoft>();
+                    for (int i = tid; i < min(32, o.nrows - rows0) * 16; i += kSoft) {
                         const int row = i >> 4, u = i & 15;
                         const uint4 v = *reinterpret_cast<const uint4 *>(base + (stage - s_q) + row * 256 + ((u ^ (row & 7)) << 4));
-                        uint16_t *dst = p.out + off[row] + 128 * j + 8 * u;
+                        uint16_t *dst = p.out + off[rows0 + row] + 128 * j + 8 * u;
                         if (p.out16) {
                             *reinterpret_cast<uint4 *>(dst) = v;
                         } else {
@@ -970,122 +1046,32 @@ __global__ void __launch_bounds__(kThreads, 1) latent_attention_kernel(const __g
                 if (!empty && !dead) {
                     float4 *o4 = reinterpret_cast<float4 *>(ws) + 32 * sw + lane;
                     const int groups = (o.nrows + 3) / 4;
-                    for (int c = 0; c < pairs * NT; c += 16) {
+                    for (int j = 0; j < pairs; ++j)
+#pragma unroll
+                    for (int c = col0; c < col0 + CT; c += 16) {
                         uint32_t v[16];
-                        tmem_ld16(t_o + quarter + c, v);
+                        tmem_ld16(t_o + quarter + j * NT + c, v);
 #pragma unroll
                         for (int i = 0; i < 16; i += 4)
-                            if ((c % NT + i) / 4 < groups)
-                                o4[(c + i) / 4 * 128] = make_float4(__uint_as_float(v[i]), __uint_as_float(v[i + 1]),
+                            if ((c + i) / 4 < groups)
+                                o4[(j * NT + c + i) / 4 * 128] = make_float4(__uint_as_float(v[i]), __uint_as_float(v[i + 1]),
                                                                     __uint_as_float(v[i + 2]), __uint_as_float(v[i + 3]));
                     }
                 }
             }
             tc_fence_before();
-            soft_sync();  // the shared buffers are used again
-        }
-    } else {
-        // ----- the queries, the rotated elements' ring, and the tiles ahead into the L2 cache
-        const int units = (2 * pairs + 1) * 8, width = p.R + p.E;
-        int n = 0, rslot = 0;
-        unsigned rph = 0;
-        bool ok = true;
-        while (ok && walk.next(p, r, o)) {
-            if (o.k0 >= o.k1) continue;
-            if (!(ok = pieces == 0 || all_wait(qempty, (pieces - 1) & 1, &stop))) break;
-            ++pieces;
-            if (p.q_even) {
-                // rows past the sequence's are the next one's (or zeros past the last): their
-                // products are columns of S^T that nothing reads
-                if (elect()) {
-                    const int row = o.s.q0 * p.H + o.row0;
-                    bar_expect_tx(qfull, static_cast<unsigned>((2 * pairs + 1) * qchunk));
-                    tma_3d(s_q, &p.qv, 0, row, 0, qfull);
-                    tc05::tma_load_2d(s_q + 2 * pairs * qchunk, &p.qr, 0, row, qfull);
-                }
-                __syncwarp();
-            } else {
-                int tok = o.s.q0 + p.heads.div(o.row0), head = p.heads.mod(o.row0);
-                for (int row = 0; row < NT; ++row) {
-                    // rows past the piece and elements past the width are 0
-                    const bool in = row < o.nrows;
-                    const uint16_t *src = in ? p.q + tok * p.q_token + head * p.q_head : p.q;
-#pragma unroll 3
-                    for (int u = lane; u < units; u += 32)
-                        copy16(s_q + (u >> 3) * qchunk + row * 128 + (((u & 7) ^ (row & 7)) << 4),
-                               in && 8 * u < width ? src + 8 * u : p.q, in && 8 * u < width ? 16 : 0);
-                    if (++head == p.H) {
-                        head = 0;
-                        ++tok;
-                    }
-                }
-                asm volatile("cp.async.wait_all;" ::: "memory");
-                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-                __syncwarp();
-                if (lane == 0) bar_arrive(qfull);
-            }
-            Pages pages(p, o);
-            for (int k = o.k0; ok && k < o.k1; ++k, ++n) {
-                pages.step(p, k);
-                // near the piece's end: the next one's queries, table entries and first tiles
-                if (p.page_bytes && k == max(o.k0, o.k1 - 4)) {
-                    Walk then = walk;
-                    Piece q;
-                    if (then.next(p, r, q) && q.k0 < q.k1) {
-                        const Pages to(p, q);
-                        const int tile = q.k0 + (lane >> to.shift);
-                        if (tile < q.k0 + kPrefetch && to.now >= 0 && to.now < p.pages)
-                            l2_ahead(p.cache + to.now * p.page_bytes +
-                                         static_cast<long long>(to.whole ? p.page_tiles.mod(tile) * kTile : 0) * 2 * width,
-                                     static_cast<unsigned>(to.rows * 2 * width));
-                        if (lane == 31 && p.q_even && p.q_head == width)
-                            l2_ahead(p.q + (static_cast<long long>(q.s.q0) * p.H + q.row0) * width,
-                                     static_cast<unsigned>(q.nrows * 2 * width));
-                    }
-                }
-                const int copies = alike(pages.copies), step = pages.rows * 128;
-                const int row = alike(pages.row);
-                int page[kMaxCopies];
-#pragma unroll
-                for (int f = 0; f < kMaxCopies; ++f)
-                    if (f < copies) page[f] = alike(pages.page(p, f));
-                if (!(ok = n < RS || all_wait(rempty + 8 * rslot, rph ^ 1, &stop))) break;
-                if (!stall) rissued = n + 1;
-                const uint32_t dst = s_r + rslot * kChunk, bar = rfull + 8 * rslot;
-                if (elect()) {
-                    bar_expect_tx(bar, static_cast<unsigned>(copies * step));
-                    if (!stall) {
-#pragma unroll
-                        for (int f = 0; f < kMaxCopies; ++f)
-                            if (f < copies) tma_3d(dst + f * step, &p.tr, 0, row, page[f], bar);
-                    }
-                }
-                __syncwarp();
-                if (++rslot == RS) {
-                    rslot = 0;
-                    rph ^= 1;
-                }
-                // the pages' rows lie back to back: one request a copy, for all of their bytes
-                if (p.page_bytes && k + kPrefetch < o.k1) {
-                    const int ahead = pages.ahead(k + kPrefetch, lane);
-                    const int arow = pages.whole ? p.page_tiles.mod(k + kPrefetch) * kTile : 0;
-                    if (lane < pages.per && ahead >= 0 && ahead < p.pages &&
-                        (k + kPrefetch) * kTile + lane * pages.rows < o.s.len)
-                        l2_ahead(p.cache + ahead * p.page_bytes + static_cast<long long>(arow) * 2 * width,
-                                 static_cast<unsigned>(pages.rows * 2 * width));
-                }
-            }
+            soft_sync<kSoft>();  // the shared buffers are used again
         }
     }
     __syncwarp();
     // after a stop: the copies issued have landed before the shared memory goes
     if (lane == 0 && *reinterpret_cast<volatile int *>(&stop)) {
-        if (warp == 0)
-            for (int i = max(0, issued - S); i < issued; ++i) landed(vfull + 8 * (i % S), (i / S) & 1);
-        if (warp == 7) {
+        if (warp == 0 || warp == kLast) {
+            for (int i = max(0, issued - S); i < issued; ++i)
+                if ((i & 1) == (warp == 0 ? 0 : 1)) landed(vfull + 8 * (i % S), (i / S) & 1);
             for (int i = max(0, rissued - RS); i < rissued; ++i) landed(rfull + 8 * (i % RS), (i / RS) & 1);
-            if (pieces > 0) landed(qfull, (pieces - 1) & 1);
         }
+        if (warp == 1 && pieces > 0) landed(qfull, (pieces - 1) & 1);
     }
     tc_fence_before();
     __syncthreads();
@@ -1271,7 +1257,7 @@ sgemm_status_t check_sizes(const sgemm_latent_attention_t &a) {
     const long long big = 1LL << 30;
     if (a.pages >= big || a.total_q >= big || static_cast<long long>(a.max_q) * a.H >= big ||
         static_cast<long long>(a.max_q) * a.B >= big || static_cast<long long>(a.table_width) * a.page_size >= big ||
-        (static_cast<long long>(a.table_width) * a.page_size / kTile + 2) * a.B >= big)
+        (static_cast<long long>(a.table_width) * a.page_size / kTile + 2 + kPieceCost) * a.B >= big)
         return SGEMM_ERR_UNSUPPORTED_SHAPE;
     return SGEMM_OK;
 }
@@ -1414,19 +1400,17 @@ extern "C" sgemm_status_t sgemm_bf16_latent_attention(const sgemm_latent_attenti
     p.scale_log2 = static_cast<float>(static_cast<double>(a->scale) * 1.4426950408889634);
     p.flags = static_cast<int>(a->flags);
 
-    p.cache = reinterpret_cast<const uint8_t *>(a->cache);
     p.heads = Divisor::of(a->H);
     p.ctas = Divisor::of(sp.rt);
     p.page_tiles = Divisor::of(std::max(1, a->page_size / kTile));
     p.row_shift = a->page_size >= kTile ? 6 : a->page_size == 32 ? 5 : a->page_size == 16 ? 4 : 3;
-    p.page_bytes = a->row_stride == W ? a->page_stride * 2 : 0;
     p.out16 = aligned(a->out, 16) && a->out_token % 8 == 0 && a->out_head % 8 == 0 ? 1 : 0;
     p.by_seq = a->B < sp.groups ? 1 : 0;
-    // Shared memory: Q, two buffers of weights, the rotated elements' ring, then as many slots of
-    // latent elements as there is room for.  With 64 rows one slot of rotated elements: it is
-    // needed last of a tile and free again first, and makes room for two whole tiles of slots.
-    p.rope_slots = sp.nt == 64 ? 1 : 3;
-    const int fixed = (a->R / 64 + 1) * sp.nt * 128 + 2 * kChunk + p.rope_slots * kChunk + kBarBytes + 40 * sp.nt + 16;
+    // Shared memory: Q, the weights, the rotated elements' ring, then as many slots of latent
+    // elements as there is room for
+    p.rope_slots = sp.nt == 64 ? 2 : 3;
+    const int fixed = (a->R / 64 + 1) * sp.nt * 128 + weight_buffers(sp.nt) * kChunk + p.rope_slots * kChunk + kBarBytes +
+                      40 * sp.nt + 16;
     p.slots = std::min(kMaxSlots, (static_cast<int>(kMaxSmemOptin) - fixed) / kSlot);
     const int smem = fixed + p.slots * kSlot;
     const void *fn = kernel_of(sp.nt);
@@ -1443,7 +1427,7 @@ extern "C" sgemm_status_t sgemm_bf16_latent_attention(const sgemm_latent_attenti
         }
     }
     const cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
-    if (launch(fn, dim3(static_cast<unsigned>(sp.groups * sp.rt)), dim3(kThreads), static_cast<size_t>(smem), cs,
+    if (launch(fn, dim3(static_cast<unsigned>(sp.groups * sp.rt)), dim3(static_cast<unsigned>(threads_of(sp.nt))), static_cast<size_t>(smem), cs,
                (a->flags & SGEMM_FLAG_PDL) != 0, &p) != cudaSuccess)
         return SGEMM_ERR_CUDA;
     if (sp.groups == 1) return SGEMM_OK;
