@@ -5,9 +5,7 @@
 // per head.
 //
 // Every byte is read and written once and there are a few operations an
-// element: bound by memory for many tokens, by latency for few.  One block
-// takes one token: warp 0 the latent vector (R / 8 16-byte pieces, kept in
-// registers over the reduction), the other warps the H + 1 rotated rows.
+// element: bound by memory for many tokens, by latency for few.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -23,6 +21,7 @@ namespace append {
 struct AppendParams {
     sgemm_latent_append_t a;
     int *err;
+    int group;  // threads a token (a power of two, a whole number of warps)
 };
 
 constexpr int kMaxPieces = 4;  // 16-byte pieces of the latent vector a lane keeps: R <= 1024
@@ -58,108 +57,121 @@ __device__ __forceinline__ uint16_t *row_of(const AppendParams &p, long long slo
 }
 
 // 16-byte accesses: every row of every array starts on 16 bytes, R is a multiple of 8 and
-// at most 1024, and E / 2 a multiple of 8 (4 if interleaved).
+// at most 1024, and a rotated row's pieces (E / 8 of 16 bytes if interleaved, else E / 16 pairs of
+// them) divide a warp, so that a thread meets the same elements, and angles, in every row.
+// `p.group` threads take a token: the first warp its latent vector, all of them its H + 1 rotated
+// rows, kBatch pieces at a time.  What a thread loads is requested before it waits for the
+// token's position and then its angles, a chain of two loads.
+template <bool INTER>
 __global__ void __launch_bounds__(512) latent_append_vec_kernel(const __grid_constant__ AppendParams p) {
+    constexpr int kBatch = 4, kV = INTER ? 1 : 2;  // 16-byte accesses a piece
     const sgemm_latent_append_t &a = p.a;
     if (a.flags & SGEMM_FLAG_PDL) {
         pdl_launch_dependents();
         pdl_wait();
     }
-    const long long t = blockIdx.x;
-    const int lane = threadIdx.x & 31;
+    const int lane = threadIdx.x & 31, in = threadIdx.x & (p.group - 1);
+    const long long t = static_cast<long long>(blockIdx.x) * (blockDim.x / p.group) + threadIdx.x / p.group;
+    if (t >= a.T) return;  // whole warps; no block barrier below
+    const long long pos = a.positions[t], slot = a.slots[t];
     const uint16_t *kv = a.kv + t * a.ldkv;
-    if (threadIdx.x < 32) {
-        uint4 in[kMaxPieces];
-        const int pieces = a.R / 8;
+    const int per = a.E / (8 * kV), half = a.E / 2, u = in & (per - 1);
+    const int items = (a.H + 1) * per, rows = p.group / per;  // pieces; rows a turn
+    const uint16_t *q = a.q + t * a.q_token + 8 * u;
+    uint16_t *qo = a.q_out + t * a.qo_token + 8 * u;
+
+    // row 0 is the key's, row 1 + h head h's
+    uint4 v[kBatch][kV];
+    auto load = [&](int i) {
+        int row = i / per;
 #pragma unroll
-        for (int i = 0; i < kMaxPieces; ++i)
-            if (lane + 32 * i < pieces) in[i] = *reinterpret_cast<const uint4 *>(kv + 8 * (lane + 32 * i));
-        const long long slot = a.slots[t];
-        if (lane == 0 && slot >= a.pages * a.page_size) atomicOr(p.err, kErrBadIndex);
-        uint16_t *row = row_of(p, slot);
-        if (!row) return;
+        for (int b = 0; b < kBatch; ++b, row += rows)
+            if (i + b * p.group < items) {
+                const uint16_t *src = row == 0 ? kv + a.R + 8 * u : q + (row - 1) * a.q_head;
+#pragma unroll
+                for (int w = 0; w < kV; ++w) v[b][w] = *reinterpret_cast<const uint4 *>(src + w * half);
+            }
+    };
+    load(in);
+    uint4 latent[kMaxPieces], g[kMaxPieces];
+    const int pieces = in < 32 ? a.R / 8 : 0;
+#pragma unroll
+    for (int i = 0; i < kMaxPieces; ++i)
+        if (lane + 32 * i < pieces) {
+            latent[i] = *reinterpret_cast<const uint4 *>(kv + 8 * (lane + 32 * i));
+            if (a.weight) g[i] = *reinterpret_cast<const uint4 *>(a.weight + 8 * (lane + 32 * i));
+        }
+    const bool bad = pos < 0 || pos >= a.max_position;
+    const float *cs = a.cos_sin + (bad ? 0 : pos) * a.ldcs;
+    constexpr int kPairs = INTER ? 4 : 8;  // of a piece
+    float c[kPairs], s[kPairs];
+#pragma unroll
+    for (int i = 0; i < kPairs; i += 4) {
+        const float4 x = *reinterpret_cast<const float4 *>(cs + kPairs * u + i);
+        const float4 y = *reinterpret_cast<const float4 *>(cs + half + kPairs * u + i);
+        c[i] = x.x, c[i + 1] = x.y, c[i + 2] = x.z, c[i + 3] = x.w;
+        s[i] = y.x, s[i + 1] = y.y, s[i + 2] = y.z, s[i + 3] = y.w;
+    }
+    if (bad) {
+#pragma unroll
+        for (int i = 0; i < kPairs; ++i) c[i] = s[i] = __int_as_float(0x7fc00000);
+    }
+    uint16_t *row0 = row_of(p, slot);
+    if (in == 0 && (slot >= a.pages * a.page_size || (bad && slot >= 0))) atomicOr(p.err, kErrBadIndex);
+    if (in < 32 && row0) {
         if (a.weight) {
-            uint4 w[kMaxPieces];
-#pragma unroll
-            for (int i = 0; i < kMaxPieces; ++i)
-                if (lane + 32 * i < pieces) w[i] = *reinterpret_cast<const uint4 *>(a.weight + 8 * (lane + 32 * i));
             float ss = 0.0f;
 #pragma unroll
             for (int i = 0; i < kMaxPieces; ++i)
                 if (lane + 32 * i < pieces) {
-                    float v[8];
-                    unpack(in[i], v);
+                    float x[8];
+                    unpack(latent[i], x);
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) ss = fmaf(v[j], v[j], ss);
+                    for (int j = 0; j < 8; ++j) ss = fmaf(x[j], x[j], ss);
                 }
             const float rs = rsqrtf(warp_sum(ss) / static_cast<float>(a.R) + a.eps);
 #pragma unroll
             for (int i = 0; i < kMaxPieces; ++i)
                 if (lane + 32 * i < pieces) {
-                    float v[8], g[8];
-                    unpack(in[i], v);
-                    unpack(w[i], g);
+                    float x[8], y[8];
+                    unpack(latent[i], x);
+                    unpack(g[i], y);
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) v[j] = v[j] * rs * g[j];
-                    in[i] = pack(v);
+                    for (int j = 0; j < 8; ++j) x[j] = x[j] * rs * y[j];
+                    latent[i] = pack(x);
                 }
         }
 #pragma unroll
         for (int i = 0; i < kMaxPieces; ++i)
-            if (lane + 32 * i < pieces) *reinterpret_cast<uint4 *>(row + 8 * (lane + 32 * i)) = in[i];
-        return;
+            if (lane + 32 * i < pieces) *reinterpret_cast<uint4 *>(row0 + 8 * (lane + 32 * i)) = latent[i];
     }
-    // row 0 is the key's, row 1 + h head h's
-    const int half = a.E / 2;
-    const int per = a.interleaved ? a.E / 8 : a.E / 16;  // threads a row
-    const long long pos = a.positions[t];
-    const bool bad = pos < 0 || pos >= a.max_position;
-    const float *cs = a.cos_sin + (bad ? 0 : pos) * a.ldcs;
-    const float nan = __int_as_float(0x7fc00000);
-    for (int i = static_cast<int>(threadIdx.x) - 32; i < (a.H + 1) * per; i += static_cast<int>(blockDim.x) - 32) {
-        const int h = i / per - 1, u = i % per;
-        const uint16_t *src = h < 0 ? kv + a.R : a.q + t * a.q_token + h * a.q_head;
-        uint16_t *dst;
-        if (h < 0) {
-            const long long slot = a.slots[t];
-            if (u == 0 && bad && slot >= 0) atomicOr(p.err, kErrBadIndex);
-            dst = row_of(p, slot);
-            if (!dst) continue;
-            dst += a.R;
-        } else {
-            dst = a.q_out + t * a.qo_token + h * a.qo_head;
-        }
-        if (a.interleaved) {
-            float v[8];
-            unpack(*reinterpret_cast<const uint4 *>(src + 8 * u), v);
-            const float4 c = *reinterpret_cast<const float4 *>(cs + 4 * u);
-            const float4 s = *reinterpret_cast<const float4 *>(cs + half + 4 * u);
-            const float cc[4] = {c.x, c.y, c.z, c.w}, sn[4] = {s.x, s.y, s.z, s.w};
+    for (int i = in; i < items; i += kBatch * p.group) {
+        if (i != in) load(i);
+        int row = i / per;
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const float x = v[2 * j], y = v[2 * j + 1];
-                v[2 * j] = bad ? nan : x * cc[j] - y * sn[j];
-                v[2 * j + 1] = bad ? nan : y * cc[j] + x * sn[j];
-            }
-            *reinterpret_cast<uint4 *>(dst + 8 * u) = pack(v);
-        } else {
+        for (int b = 0; b < kBatch; ++b, row += rows) {
+            if (i + b * p.group >= items || (row == 0 && !row0)) continue;
+            uint16_t *dst = row == 0 ? row0 + a.R + 8 * u : qo + (row - 1) * a.qo_head;
             float x[8], y[8];
-            unpack(*reinterpret_cast<const uint4 *>(src + 8 * u), x);
-            unpack(*reinterpret_cast<const uint4 *>(src + half + 8 * u), y);
-#pragma unroll
-            for (int g = 0; g < 2; ++g) {
-                const float4 c = *reinterpret_cast<const float4 *>(cs + 8 * u + 4 * g);
-                const float4 s = *reinterpret_cast<const float4 *>(cs + half + 8 * u + 4 * g);
-                const float cc[4] = {c.x, c.y, c.z, c.w}, sn[4] = {s.x, s.y, s.z, s.w};
+            unpack(v[b][0], x);
+            if constexpr (INTER) {
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    const float xv = x[4 * g + j], yv = y[4 * g + j];
-                    x[4 * g + j] = bad ? nan : xv * cc[j] - yv * sn[j];
-                    y[4 * g + j] = bad ? nan : yv * cc[j] + xv * sn[j];
+                    y[2 * j] = x[2 * j] * c[j] - x[2 * j + 1] * s[j];
+                    y[2 * j + 1] = x[2 * j + 1] * c[j] + x[2 * j] * s[j];
                 }
+                *reinterpret_cast<uint4 *>(dst) = pack(y);
+            } else {
+                unpack(v[b][kV - 1], y);
+                float x2[8], y2[8];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    x2[j] = x[j] * c[j] - y[j] * s[j];
+                    y2[j] = y[j] * c[j] + x[j] * s[j];
+                }
+                *reinterpret_cast<uint4 *>(dst) = pack(x2);
+                *reinterpret_cast<uint4 *>(dst + half) = pack(y2);
             }
-            *reinterpret_cast<uint4 *>(dst + 8 * u) = pack(x);
-            *reinterpret_cast<uint4 *>(dst + half + 8 * u) = pack(y);
         }
     }
 }
@@ -224,6 +236,7 @@ extern "C" sgemm_status_t sgemm_bf16_latent_append(const sgemm_latent_append_t *
         std::isinf(a->eps) || (a->interleaved != 0 && a->interleaved != 1))
         return SGEMM_ERR_INVALID_ARG;
     if (T == 0) return SGEMM_OK;
+    if (a->max_position < 1) return SGEMM_ERR_INVALID_ARG;
     if (!a->kv || !a->cos_sin || !a->positions || !a->slots || !a->cache || (a->H > 0 && (!a->q || !a->q_out)))
         return SGEMM_ERR_INVALID_ARG;
     if (a->ldkv < W || a->ldcs < a->E || a->row_stride < W ||
@@ -275,18 +288,34 @@ extern "C" sgemm_status_t sgemm_bf16_latent_append(const sgemm_latent_append_t *
 
     const bool one = T == 1;
     auto rows16 = [&](const void *q, long long ld) { return aligned(q, 16) && (one || ld % 8 == 0); };
-    const bool vec = a->R % 8 == 0 && a->R <= 256 * append::kMaxPieces && (a->E / 2) % (a->interleaved ? 4 : 8) == 0 &&
-                     rows16(a->kv, a->ldkv) && aligned(a->weight, 16) && aligned(a->cache, 16) &&
+    const int per = a->interleaved ? a->E / 8 : a->E / 16;  // 16-byte pieces (pairs of them) of a rotated row
+    const bool vec = a->R % 8 == 0 && a->R <= 256 * append::kMaxPieces && a->E % (a->interleaved ? 8 : 16) == 0 &&
+                     32 % per == 0 && rows16(a->kv, a->ldkv) && aligned(a->weight, 16) && aligned(a->cache, 16) &&
                      a->row_stride % 8 == 0 && a->page_stride % 8 == 0 && aligned(a->cos_sin, 16) && a->ldcs % 4 == 0 &&
                      (a->H == 0 || (rows16(a->q, a->q_token) && rows16(a->q_out, a->qo_token) && a->q_head % 8 == 0 &&
                                     a->qo_head % 8 == 0));
-    const long long work = vec ? static_cast<long long>(a->H + 1) * (a->interleaved ? a->E / 8 : a->E / 16)
-                               : static_cast<long long>(a->H + 1) * (a->E / 2);
-    const int threads = 32 + static_cast<int>(std::min<long long>(480, (work + 31) / 32 * 32));
-    const void *fn = vec ? reinterpret_cast<const void *>(&append::latent_append_vec_kernel)
-                         : reinterpret_cast<const void *>(&append::latent_append_any_kernel);
-    if (launch(fn, dim3(static_cast<unsigned>(T)), dim3(static_cast<unsigned>(threads)), 0,
-               reinterpret_cast<cudaStream_t>(stream), (a->flags & SGEMM_FLAG_PDL) != 0, &p) != cudaSuccess)
-        return SGEMM_ERR_CUDA;
+    const bool pdl = (a->flags & SGEMM_FLAG_PDL) != 0;
+    const cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
+    cudaError_t e;
+    if (vec) {
+        // Few tokens: a thread a piece (up to 512 a token), for the shortest chain.  Many: 64
+        // threads a token, so that each has several loads in flight.
+        const long long items = static_cast<long long>(a->H + 1) * per;
+        int group = 64;
+        if (T <= 4LL * sms)
+            while (group < 512 && group < items) group *= 2;
+        p.group = group;
+        const int tokens = T <= 4LL * sms ? 1 : 256 / group;
+        e = launch(a->interleaved ? reinterpret_cast<const void *>(&append::latent_append_vec_kernel<true>)
+                                  : reinterpret_cast<const void *>(&append::latent_append_vec_kernel<false>),
+                   dim3(static_cast<unsigned>((T + tokens - 1) / tokens)), dim3(static_cast<unsigned>(group * tokens)), 0, cs,
+                   pdl, &p);
+    } else {
+        const long long work = static_cast<long long>(a->H + 1) * (a->E / 2);
+        const int threads = 32 + static_cast<int>(std::min<long long>(480, (work + 31) / 32 * 32));
+        e = launch(reinterpret_cast<const void *>(&append::latent_append_any_kernel), dim3(static_cast<unsigned>(T)),
+                   dim3(static_cast<unsigned>(threads)), 0, cs, pdl, &p);
+    }
+    if (e != cudaSuccess) return SGEMM_ERR_CUDA;
     return SGEMM_OK;
 }

@@ -52,61 +52,81 @@ def _call(name: str, args: bytes, t: torch.Tensor, stream) -> None:
         stream = torch._C._cuda_getCurrentRawStream(t.get_device())
     elif isinstance(stream, torch.cuda.Stream):
         stream = stream.cuda_stream
-    status = _fn(name)(args, stream)
+    status = (_fns.get(name) or _fn(name))(args, stream)
     if status:
         raise SgemmError(status, name)
 
 
-def _need(t, name: str, dtype, dim: int) -> torch.Tensor:
-    """A CUDA tensor of this type and rank, its last dimension of unit stride."""
-    if not isinstance(t, torch.Tensor) or t.dtype != dtype or t.dim() != dim:
-        raise TypeError(f"{name} must be a {dim}-D {dtype} tensor")
+def _refuse(t, name: str, dtype, shape):
+    """What is wrong with a tensor; its strides if nothing is (a last dimension of one element has
+    a stride of no account)."""
+    if not isinstance(t, torch.Tensor) or t.dtype != dtype or t.dim() != len(shape):
+        raise TypeError(f"{name} must be a {len(shape)}-D {dtype} tensor")
     if not t.is_cuda:
         raise TypeError(f"{name} must be on a CUDA device")
-    if t.stride(-1) != 1 and t.shape[-1] > 1:
+    for n, want in zip(t.shape, shape):
+        if want is not None and n != want:
+            raise ValueError(f"{name} must be {['any' if w is None else w for w in shape]}, got {list(t.shape)}")
+    if t.shape[-1] > 1 and t.stride(-1) != 1:
         raise ValueError(f"{name} must have unit stride along its last dimension")
-    return t
+    return t.stride()
 
 
-def _shaped(t, name: str, dtype, shape) -> torch.Tensor:
-    _need(t, name, dtype, len(shape))
-    if t.shape != shape:
-        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
-    return t
+def _strides(t, name: str, dtype, shape):
+    """The strides of a CUDA tensor of this type and shape whose last dimension has unit stride
+    (one pass over its attributes: a step's calls are short)."""
+    try:
+        if t.dtype is dtype and t.is_cuda and t.shape == shape:
+            s = t.stride()
+            if s[-1] == 1:
+                return s
+    except AttributeError:
+        pass
+    return _refuse(t, name, dtype, shape)
 
 
-def _ptr(t) -> int:
-    return 0 if t is None else t.data_ptr()
+def _shape(t, name: str, dtype, dim: int):
+    """The shape of a tensor that has any of this rank."""
+    try:
+        if t.dtype is dtype and len(t.shape) == dim:
+            return t.shape
+    except AttributeError:
+        pass
+    _refuse(t, name, dtype, (None,) * dim)
 
 
 # ----------------------------------------------------------------------------- residual RMS norm
-def _norm(name, x, weight, residual, eps, form, y, y_dtype, scales, residual_out, flags, stream):
-    T, D = _need(x, "x", _BF16, 2).shape
-    _shaped(weight, "weight", _BF16, (D,))
+def _norm(x, weight, residual, eps, form, y, y_dtype, scales, residual_out, flags, stream):
+    shape = _shape(x, "x", _BF16, 2)
+    T, D = shape
+    ldx = _strides(x, "x", _BF16, shape)[0]
+    _strides(weight, "weight", _BF16, (D,))
+    ldr = ldro = D
+    pr = pro = ps = lds = 0
     if residual is not None:
-        _shaped(residual, "residual", _BF16, (T, D))
+        ldr = _strides(residual, "residual", _BF16, shape)[0]
+        pr = residual.data_ptr()
         if residual_out is None:
-            residual_out = torch.empty((T, D), dtype=_BF16, device=x.device)
+            residual_out = torch.empty(shape, dtype=_BF16, device=x.device)
     if residual_out is not None:
-        _shaped(residual_out, "residual_out", _BF16, (T, D))
+        ldro = _strides(residual_out, "residual_out", _BF16, shape)[0]
+        pro = residual_out.data_ptr()
     if y is None:
-        y = torch.empty((T, D), dtype=y_dtype, device=x.device)
-    _shaped(y, "y" if form == SGEMM_NORM_BF16 else "q", y_dtype, (T, D))
-    lds = 0
+        y = torch.empty(shape, dtype=y_dtype, device=x.device)
+    ldy = _strides(y, "y" if form == SGEMM_NORM_BF16 else "q", y_dtype, shape)[0]
     if form != SGEMM_NORM_BF16:
         groups = -(-D // 128) if form == SGEMM_NORM_E4M3_GROUP128 else 1
         if scales is None:
             scales = torch.empty((T, groups), dtype=torch.float32, device=x.device)
-        _shaped(scales, "scales", torch.float32, (T, groups))
-        lds = scales.stride(0) if T > 1 else groups
-    if T == 0:
-        return y, scales, residual_out
-    one = T == 1  # the row stride of a single row is of no account
+        lds = _strides(scales, "scales", torch.float32, (T, groups))[0]
+        ps = scales.data_ptr()
+    if T <= 1:
+        if T == 0:
+            return y, scales, residual_out
+        ldx = ldr = ldro = ldy = lds = D  # the row stride of a single row is of no account
     _call("sgemm_bf16_add_rmsnorm", _NORM.pack(
-        x.data_ptr(), _ptr(residual), weight.data_ptr(), _ptr(residual_out), y.data_ptr(), _ptr(scales),
-        D if one else x.stride(0), D if one or residual is None else residual.stride(0),
-        D if one or residual_out is None else residual_out.stride(0), D if one else y.stride(0), lds,
-        T, D, form, eps, flags), x, stream)
+        x.data_ptr(), pr, weight.data_ptr(), pro, y.data_ptr(), ps, ldx, ldr, ldro, ldy, lds, T, D, form, eps, flags),
+        x, stream)
     return y, scales, residual_out
 
 
@@ -117,8 +137,7 @@ def sgemm_bf16_add_rmsnorm(x: torch.Tensor, weight: torch.Tensor, residual: torc
     ``(y, residual_out)`` with ``residual_out = bf16(h)`` (None where neither a residual nor a
     buffer for it is given).  x, residual: BF16 [T, D], rows of any stride; weight: BF16 [D].
     ``residual_out`` may be ``residual`` or ``x``, and ``y`` may be ``x``: in place."""
-    y, _, residual_out = _norm("sgemm_bf16_add_rmsnorm", x, weight, residual, eps, SGEMM_NORM_BF16, y, _BF16,
-                               None, residual_out, flags, stream)
+    y, _, residual_out = _norm(x, weight, residual, eps, SGEMM_NORM_BF16, y, _BF16, None, residual_out, flags, stream)
     return y, residual_out
 
 
@@ -133,7 +152,7 @@ def sgemm_bf16_add_rmsnorm_e4m3(x: torch.Tensor, weight: torch.Tensor, residual:
     if group not in (0, 128):
         raise ValueError(f"group must be 128 (columns a scale) or 0 (one scale a row), got {group}")
     form = SGEMM_NORM_E4M3_GROUP128 if group else SGEMM_NORM_E4M3_ROW
-    return _norm("sgemm_bf16_add_rmsnorm", x, weight, residual, eps, form, q, torch.float8_e4m3fn, scales,
+    return _norm(x, weight, residual, eps, form, q, torch.float8_e4m3fn, scales,
                  residual_out, flags, stream)
 
 
@@ -152,36 +171,47 @@ def sgemm_bf16_latent_append(kv: torch.Tensor, cache: torch.Tensor, slots: torch
     RMS-normalised on the way.  q, q_out: BF16 [T, H, E] views, the part of each head's query
     that is rotated and where it goes (may be the same).  ``interleaved``: the rotated pairs are
     (2i, 2i + 1), else (i, E / 2 + i)."""
-    T, W = _need(kv, "kv", _BF16, 2).shape
-    pages, page_size, width = _need(cache, "cache", _BF16, 3).shape
-    limit, E = _need(cos_sin, "cos_sin", torch.float32, 2).shape
+    T, W = shape = _shape(kv, "kv", _BF16, 2)
+    pages, page_size, width = _shape(cache, "cache", _BF16, 3)
+    limit, E = _shape(cos_sin, "cos_sin", torch.float32, 2)
     R = W - E
     if width != W:
         raise ValueError(f"cache rows must be as wide as kv's ({W}), got {width}")
     if R < 1:
         raise ValueError(f"kv rows ({W}) must be wider than cos_sin's ({E})")
-    _shaped(slots, "slots", torch.int64, (T,))
-    _shaped(positions, "positions", torch.int64, (T,))
+    ldkv = _strides(kv, "kv", _BF16, shape)[0]
+    page_stride, row_stride, _ = _strides(cache, "cache", _BF16, (pages, page_size, W))
+    ldcs = _strides(cos_sin, "cos_sin", torch.float32, (limit, E))[0]
+    _strides(slots, "slots", torch.int64, (T,))
+    _strides(positions, "positions", torch.int64, (T,))
+    H = pq = pqo = pw = q_token = q_head = qo_token = qo_head = 0
     if weight is not None:
-        _shaped(weight, "weight", _BF16, (R,))
-    H, strides = 0, (0, 0, 0, 0)
+        _strides(weight, "weight", _BF16, (R,))
+        pw = weight.data_ptr()
     if q is not None:
-        H = _need(q, "q", _BF16, 3).shape[1]
-        if q.shape[0] != T or q.shape[2] != E:
-            raise ValueError(f"q must be [{T}, heads, {E}], got {list(q.shape)}")
+        H = _shape(q, "q", _BF16, 3)[1]
+        q_token, q_head, _ = _strides(q, "q", _BF16, (T, H, E))
         if q_out is None:
             q_out = torch.empty((T, H, E), dtype=_BF16, device=kv.device)
-        _shaped(q_out, "q_out", _BF16, (T, H, E))
-        strides = (q.stride(0), q.stride(1), q_out.stride(0), q_out.stride(1))
+        qo_token, qo_head, _ = _strides(q_out, "q_out", _BF16, (T, H, E))
+        if H:
+            pq, pqo = q.data_ptr(), q_out.data_ptr()
     elif q_out is not None:
         raise ValueError("q_out without q")
     if T == 0:
         return cache, q_out
+    # strides along dimensions of one element are of no account
+    if T == 1:
+        ldkv = W
+    if limit == 1:
+        ldcs = E
+    if page_size == 1:
+        row_stride = W
+    if pages == 1:
+        page_stride = page_size * row_stride
     _call("sgemm_bf16_latent_append", _APPEND.pack(
-        kv.data_ptr(), _ptr(weight), cos_sin.data_ptr(), positions.data_ptr(), slots.data_ptr(), cache.data_ptr(),
-        _ptr(q) if H else 0, _ptr(q_out) if H else 0,
-        W if T == 1 else kv.stride(0), E if limit == 1 else cos_sin.stride(0), W if page_size == 1 else cache.stride(1),
-        cache.stride(0) if pages > 1 else page_size * max(W, cache.stride(1)), *strides,
+        kv.data_ptr(), pw, cos_sin.data_ptr(), positions.data_ptr(), slots.data_ptr(), cache.data_ptr(), pq, pqo,
+        ldkv, ldcs, row_stride, page_stride, q_token, q_head, qo_token, qo_head,
         T, limit, pages, page_size, R, E, H, 1 if interleaved else 0, eps, flags, 0), kv, stream)
     return cache, q_out
 
@@ -216,21 +246,27 @@ def sgemm_bf16_latent_attention(q: torch.Tensor, cache: torch.Tensor, block_tabl
     out: BF16 [total_q, H, rank]; lse: FP32 [total_q, H] or None (not written).  ``workspace``:
     scratch on the device (:func:`sgemm_latent_attention_workspace` bytes; allocated for the call
     where None)."""
-    total, H, W = _need(q, "q", _BF16, 3).shape
-    pages, page_size, width = _need(cache, "cache", _BF16, 3).shape
-    B, table_width = _need(block_table, "block_table", torch.int32, 2).shape
-    _shaped(seq_lens, "seq_lens", torch.int32, (B,))
+    total, H, W = shape = _shape(q, "q", _BF16, 3)
+    pages, page_size, width = _shape(cache, "cache", _BF16, 3)
+    B, table_width = _shape(block_table, "block_table", torch.int32, 2)
     if width != W:
         raise ValueError(f"cache rows must be as wide as q's ({W}), got {width}")
+    q_token, q_head, _ = _strides(q, "q", _BF16, shape)
+    page_stride, row_stride, _ = _strides(cache, "cache", _BF16, (pages, page_size, W))
+    ldt = _strides(block_table, "block_table", torch.int32, (B, table_width))[0]
+    _strides(seq_lens, "seq_lens", torch.int32, (B,))
+    pcu = plse = lse_token = 0
     if cu_q is not None:
-        _shaped(cu_q, "cu_q", torch.int32, (B + 1,))
+        _strides(cu_q, "cu_q", torch.int32, (B + 1,))
+        pcu = cu_q.data_ptr()
     elif total != B * max_q:
         raise ValueError(f"q must hold {B} x {max_q} tokens without cu_q, got {total}")
     if out is None:
         out = torch.empty((total, H, rank), dtype=_BF16, device=q.device)
-    _shaped(out, "out", _BF16, (total, H, rank))
+    out_token, out_head, _ = _strides(out, "out", _BF16, (total, H, rank))
     if lse is not None:
-        _shaped(lse, "lse", torch.float32, (total, H))
+        lse_token = _strides(lse, "lse", torch.float32, (total, H))[0]
+        plse = lse.data_ptr()
     if total == 0 or B == 0:
         return out, lse
     if workspace is None:
@@ -241,13 +277,15 @@ def sgemm_bf16_latent_attention(q: torch.Tensor, cache: torch.Tensor, block_tabl
                                     else torch.cuda.ExternalStream(int(stream)))
     elif not workspace.is_cuda or not workspace.is_contiguous():
         raise TypeError("workspace must be a contiguous CUDA tensor")
+    # strides along dimensions of one element are of no account
+    if page_size == 1:
+        row_stride = W
+    if pages == 1:
+        page_stride = page_size * row_stride
+    if B == 1:
+        ldt = table_width
     _call("sgemm_bf16_latent_attention", _ATTN.pack(
-        q.data_ptr(), cache.data_ptr(), block_table.data_ptr(), seq_lens.data_ptr(), _ptr(cu_q), out.data_ptr(),
-        _ptr(lse), workspace.data_ptr(),
-        q.stride(0), q.stride(1), cache.stride(1) if page_size > 1 else W,
-        cache.stride(0) if pages > 1 else page_size * max(W, cache.stride(1)),
-        block_table.stride(0) if B > 1 else table_width, out.stride(0), out.stride(1),
-        lse.stride(0) if lse is not None else 0,
-        pages, workspace.numel() * workspace.element_size(), total,
-        page_size, table_width, B, H, rank, W - rank, max_q, scale, flags, 0), q, stream)
+        q.data_ptr(), cache.data_ptr(), block_table.data_ptr(), seq_lens.data_ptr(), pcu, out.data_ptr(),
+        plse, workspace.data_ptr(), q_token, q_head, row_stride, page_stride, ldt, out_token, out_head, lse_token,
+        pages, workspace.nbytes, total, page_size, table_width, B, H, rank, W - rank, max_q, scale, flags, 0), q, stream)
     return out, lse

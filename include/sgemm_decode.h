@@ -85,7 +85,8 @@ sgemm_status_t sgemm_bf16_add_rmsnorm(const sgemm_add_rmsnorm_t *args, sgemm_str
  * - Two tokens of one call must not name the same slot.
  * - H = 0 (q and q_out NULL) leaves the queries out.  q_out may be q itself
  *   (same pointer and strides); otherwise outputs overlap no input.
- * - T >= 0, 1 <= R <= 8192, E even, 2 <= E <= 512, 0 <= H, page_size >= 1.
+ * - T >= 0, 1 <= R <= 8192, E even, 2 <= E <= 512, 0 <= H <= 65536,
+ *   page_size >= 1, max_position >= 1.
  *   BF16 arrays 2-byte, cos_sin 4-byte, positions and slots 8-byte aligned. */
 typedef struct {
     const sgemm_bf16_t *kv;    /* [T, R + E], row stride ldkv */
