@@ -21,10 +21,9 @@ namespace append {
 struct AppendParams {
     sgemm_latent_append_t a;
     int *err;
-    int group;  // threads a token (a power of two, a whole number of warps)
+    long long slots;    // rows of the cache
+    int tokens, warps;  // tokens a block; warps for a token's queries
 };
-
-constexpr int kMaxPieces = 4;  // 16-byte pieces of the latent vector a lane keeps: R <= 1024
 
 __device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
@@ -51,129 +50,155 @@ __device__ __forceinline__ uint4 pack(const float (&v)[8]) {
 
 // The token's row of the cache, or null where none is to be written.
 __device__ __forceinline__ uint16_t *row_of(const AppendParams &p, long long slot) {
-    const long long ps = p.a.page_size;
-    if (slot < 0 || slot >= p.a.pages * ps) return nullptr;
-    return p.a.cache + (slot / ps) * p.a.page_stride + (slot % ps) * p.a.row_stride;
+    if (slot < 0 || slot >= p.slots) return nullptr;
+    // 32-bit division where it serves: the 64-bit one takes a few hundred instructions
+    long long page, row;
+    if (p.slots <= 0x7fffffffLL) {
+        const unsigned s = static_cast<unsigned>(slot), ps = static_cast<unsigned>(p.a.page_size);
+        page = s / ps;
+        row = s % ps;
+    } else {
+        page = slot / p.a.page_size;
+        row = slot % p.a.page_size;
+    }
+    return p.a.cache + page * p.a.page_stride + row * p.a.row_stride;
 }
 
-// 16-byte accesses: every row of every array starts on 16 bytes, R is a multiple of 8 and
-// at most 1024, and a rotated row's pieces (E / 8 of 16 bytes if interleaved, else E / 16 pairs of
-// them) divide a warp, so that a thread meets the same elements, and angles, in every row.
-// `p.group` threads take a token: the first warp its latent vector, all of them its H + 1 rotated
-// rows, kBatch pieces at a time.  What a thread loads is requested before it waits for the
-// token's position and then its angles, a chain of two loads.
+constexpr int kBatch = 4;  // pieces of queries a thread loads at once
+
+// Cosines and sines of the pairs of piece u (PAIRS of them) at a position; NaN where it is out
+// of range.
+template <int PAIRS>
+struct Angles {
+    float c[PAIRS], s[PAIRS];
+    __device__ __forceinline__ void load(const sgemm_latent_append_t &a, long long pos, int u) {
+        const bool bad = pos < 0 || pos >= a.max_position;
+        const float *cs = a.cos_sin + (bad ? 0 : pos) * a.ldcs + PAIRS * u;
+#pragma unroll
+        for (int i = 0; i < PAIRS; i += 4) {
+            const float4 x = *reinterpret_cast<const float4 *>(cs + i);
+            const float4 y = *reinterpret_cast<const float4 *>(cs + a.E / 2 + i);
+            c[i] = x.x, c[i + 1] = x.y, c[i + 2] = x.z, c[i + 3] = x.w;
+            s[i] = y.x, s[i + 1] = y.y, s[i + 2] = y.z, s[i + 3] = y.w;
+        }
+        if (bad) {
+#pragma unroll
+            for (int i = 0; i < PAIRS; ++i) c[i] = s[i] = __int_as_float(0x7fc00000);
+        }
+    }
+};
+
+// One piece of a rotated row: 16 bytes with 4 pairs (INTER), or 16 bytes of each half of the row
+// with 8 pairs.
 template <bool INTER>
-__global__ void __launch_bounds__(512) latent_append_vec_kernel(const __grid_constant__ AppendParams p) {
-    constexpr int kBatch = 4, kV = INTER ? 1 : 2;  // 16-byte accesses a piece
+struct Piece {
+    uint4 v[INTER ? 1 : 2];
+    __device__ __forceinline__ void load(const uint16_t *row, int u, int half) {
+        v[0] = *reinterpret_cast<const uint4 *>(row + 8 * u);
+        if constexpr (!INTER) v[1] = *reinterpret_cast<const uint4 *>(row + half + 8 * u);
+    }
+    __device__ __forceinline__ void store(uint16_t *row, int u, int half, const Angles<INTER ? 4 : 8> &t) const {
+        float x[8];
+        unpack(v[0], x);
+        if constexpr (INTER) {
+            float y[8];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                y[2 * j] = x[2 * j] * t.c[j] - x[2 * j + 1] * t.s[j];
+                y[2 * j + 1] = x[2 * j + 1] * t.c[j] + x[2 * j] * t.s[j];
+            }
+            *reinterpret_cast<uint4 *>(row + 8 * u) = pack(y);
+        } else {
+            float y[8], z[8];
+            unpack(v[1], y);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                z[j] = x[j] * t.c[j] - y[j] * t.s[j];
+                y[j] = y[j] * t.c[j] + x[j] * t.s[j];
+            }
+            *reinterpret_cast<uint4 *>(row + 8 * u) = pack(z);
+            *reinterpret_cast<uint4 *>(row + half + 8 * u) = pack(y);
+        }
+    }
+};
+
+// 16-byte accesses: every row of every array starts on 16 bytes, R is a multiple of 8 and at most
+// 256 PIECES, and the pieces of a rotated row divide a warp, so that a thread meets the same
+// elements, and angles, in every row.  A token is taken by one warp for its row of the cache and
+// `p.warps` for its queries, which load kBatch pieces a thread before they wait for the token's
+// position and then its angles, a chain of two loads.
+template <bool INTER, int PIECES>
+__global__ void __launch_bounds__(544) latent_append_vec_kernel(const __grid_constant__ AppendParams p) {
     const sgemm_latent_append_t &a = p.a;
     if (a.flags & SGEMM_FLAG_PDL) {
         pdl_launch_dependents();
         pdl_wait();
     }
-    const int lane = threadIdx.x & 31, in = threadIdx.x & (p.group - 1);
-    const long long t = static_cast<long long>(blockIdx.x) * (blockDim.x / p.group) + threadIdx.x / p.group;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = p.warps + 1;
+    const int which = warp / warps, w = warp % warps - 1;
+    const long long t = static_cast<long long>(blockIdx.x) * p.tokens + which;
     if (t >= a.T) return;  // whole warps; no block barrier below
+    const int half = a.E / 2, per = a.E / (INTER ? 8 : 16), u = lane & (per - 1);
+    Angles<INTER ? 4 : 8> turn;
+    if (w >= 0) {
+        const int first = w * (32 / per) + lane / per, step = p.warps * (32 / per);  // heads
+        const uint16_t *q = a.q + t * a.q_token;
+        uint16_t *qo = a.q_out + t * a.qo_token;
+        const long long pos = a.positions[t];
+        for (int h0 = first; h0 < a.H; h0 += kBatch * step) {
+            Piece<INTER> v[kBatch];
+#pragma unroll
+            for (int b = 0; b < kBatch; ++b)
+                if (h0 + b * step < a.H) v[b].load(q + (h0 + b * step) * a.q_head, u, half);
+            if (h0 == first) turn.load(a, pos, u);
+#pragma unroll
+            for (int b = 0; b < kBatch; ++b)
+                if (h0 + b * step < a.H) v[b].store(qo + (h0 + b * step) * a.qo_head, u, half, turn);
+        }
+        return;
+    }
     const long long pos = a.positions[t], slot = a.slots[t];
     const uint16_t *kv = a.kv + t * a.ldkv;
-    const int per = a.E / (8 * kV), half = a.E / 2, u = in & (per - 1);
-    const int items = (a.H + 1) * per, rows = p.group / per;  // pieces; rows a turn
-    const uint16_t *q = a.q + t * a.q_token + 8 * u;
-    uint16_t *qo = a.q_out + t * a.qo_token + 8 * u;
-
-    // row 0 is the key's, row 1 + h head h's
-    uint4 v[kBatch][kV];
-    auto load = [&](int i) {
-        int row = i / per;
+    uint4 latent[PIECES], g[PIECES];
+    const int pieces = a.R / 8;
 #pragma unroll
-        for (int b = 0; b < kBatch; ++b, row += rows)
-            if (i + b * p.group < items) {
-                const uint16_t *src = row == 0 ? kv + a.R + 8 * u : q + (row - 1) * a.q_head;
-#pragma unroll
-                for (int w = 0; w < kV; ++w) v[b][w] = *reinterpret_cast<const uint4 *>(src + w * half);
-            }
-    };
-    load(in);
-    uint4 latent[kMaxPieces], g[kMaxPieces];
-    const int pieces = in < 32 ? a.R / 8 : 0;
-#pragma unroll
-    for (int i = 0; i < kMaxPieces; ++i)
+    for (int i = 0; i < PIECES; ++i)
         if (lane + 32 * i < pieces) {
             latent[i] = *reinterpret_cast<const uint4 *>(kv + 8 * (lane + 32 * i));
             if (a.weight) g[i] = *reinterpret_cast<const uint4 *>(a.weight + 8 * (lane + 32 * i));
         }
-    const bool bad = pos < 0 || pos >= a.max_position;
-    const float *cs = a.cos_sin + (bad ? 0 : pos) * a.ldcs;
-    constexpr int kPairs = INTER ? 4 : 8;  // of a piece
-    float c[kPairs], s[kPairs];
+    Piece<INTER> key;
+    if (lane < per) key.load(kv + a.R, u, half);
+    turn.load(a, pos, u);
+    uint16_t *row = row_of(p, slot);
+    if (lane == 0 && (slot >= p.slots || (slot >= 0 && (pos < 0 || pos >= a.max_position)))) atomicOr(p.err, kErrBadIndex);
+    if (!row) return;
+    if (lane < per) key.store(row + a.R, u, half, turn);
+    if (a.weight) {
+        float ss = 0.0f;
 #pragma unroll
-    for (int i = 0; i < kPairs; i += 4) {
-        const float4 x = *reinterpret_cast<const float4 *>(cs + kPairs * u + i);
-        const float4 y = *reinterpret_cast<const float4 *>(cs + half + kPairs * u + i);
-        c[i] = x.x, c[i + 1] = x.y, c[i + 2] = x.z, c[i + 3] = x.w;
-        s[i] = y.x, s[i + 1] = y.y, s[i + 2] = y.z, s[i + 3] = y.w;
-    }
-    if (bad) {
+        for (int i = 0; i < PIECES; ++i)
+            if (lane + 32 * i < pieces) {
+                float x[8];
+                unpack(latent[i], x);
 #pragma unroll
-        for (int i = 0; i < kPairs; ++i) c[i] = s[i] = __int_as_float(0x7fc00000);
-    }
-    uint16_t *row0 = row_of(p, slot);
-    if (in == 0 && (slot >= a.pages * a.page_size || (bad && slot >= 0))) atomicOr(p.err, kErrBadIndex);
-    if (in < 32 && row0) {
-        if (a.weight) {
-            float ss = 0.0f;
-#pragma unroll
-            for (int i = 0; i < kMaxPieces; ++i)
-                if (lane + 32 * i < pieces) {
-                    float x[8];
-                    unpack(latent[i], x);
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) ss = fmaf(x[j], x[j], ss);
-                }
-            const float rs = rsqrtf(warp_sum(ss) / static_cast<float>(a.R) + a.eps);
-#pragma unroll
-            for (int i = 0; i < kMaxPieces; ++i)
-                if (lane + 32 * i < pieces) {
-                    float x[8], y[8];
-                    unpack(latent[i], x);
-                    unpack(g[i], y);
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) x[j] = x[j] * rs * y[j];
-                    latent[i] = pack(x);
-                }
-        }
-#pragma unroll
-        for (int i = 0; i < kMaxPieces; ++i)
-            if (lane + 32 * i < pieces) *reinterpret_cast<uint4 *>(row0 + 8 * (lane + 32 * i)) = latent[i];
-    }
-    for (int i = in; i < items; i += kBatch * p.group) {
-        if (i != in) load(i);
-        int row = i / per;
-#pragma unroll
-        for (int b = 0; b < kBatch; ++b, row += rows) {
-            if (i + b * p.group >= items || (row == 0 && !row0)) continue;
-            uint16_t *dst = row == 0 ? row0 + a.R + 8 * u : qo + (row - 1) * a.qo_head;
-            float x[8], y[8];
-            unpack(v[b][0], x);
-            if constexpr (INTER) {
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    y[2 * j] = x[2 * j] * c[j] - x[2 * j + 1] * s[j];
-                    y[2 * j + 1] = x[2 * j + 1] * c[j] + x[2 * j] * s[j];
-                }
-                *reinterpret_cast<uint4 *>(dst) = pack(y);
-            } else {
-                unpack(v[b][kV - 1], y);
-                float x2[8], y2[8];
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    x2[j] = x[j] * c[j] - y[j] * s[j];
-                    y2[j] = y[j] * c[j] + x[j] * s[j];
-                }
-                *reinterpret_cast<uint4 *>(dst) = pack(x2);
-                *reinterpret_cast<uint4 *>(dst + half) = pack(y2);
+                for (int j = 0; j < 8; ++j) ss = fmaf(x[j], x[j], ss);
             }
-        }
+        const float rs = rsqrtf(warp_sum(ss) / static_cast<float>(a.R) + a.eps);
+#pragma unroll
+        for (int i = 0; i < PIECES; ++i)
+            if (lane + 32 * i < pieces) {
+                float x[8], y[8];
+                unpack(latent[i], x);
+                unpack(g[i], y);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) x[j] = x[j] * rs * y[j];
+                latent[i] = pack(x);
+            }
     }
+#pragma unroll
+    for (int i = 0; i < PIECES; ++i)
+        if (lane + 32 * i < pieces) *reinterpret_cast<uint4 *>(row + 8 * (lane + 32 * i)) = latent[i];
 }
 
 // Any strides and alignment: element by element, the latent vector read once for its sum
@@ -190,7 +215,7 @@ __global__ void __launch_bounds__(512) latent_append_any_kernel(const __grid_con
     const long long slot = a.slots[t];
     uint16_t *row = row_of(p, slot);
     if (threadIdx.x < 32) {
-        if (lane == 0 && slot >= a.pages * a.page_size) atomicOr(p.err, kErrBadIndex);
+        if (lane == 0 && slot >= p.slots) atomicOr(p.err, kErrBadIndex);
         if (!row) return;
         float rs = 0.0f;
         if (a.weight) {
@@ -283,13 +308,14 @@ extern "C" sgemm_status_t sgemm_bf16_latent_append(const sgemm_latent_append_t *
     append::AppendParams p;
     std::memset(&p, 0, sizeof(p));
     p.a = *a;
+    p.slots = a->pages * a->page_size;
     const sgemm_status_t st = device_ready(&sms, &p.err);
     if (st != SGEMM_OK) return st;
 
     const bool one = T == 1;
     auto rows16 = [&](const void *q, long long ld) { return aligned(q, 16) && (one || ld % 8 == 0); };
     const int per = a->interleaved ? a->E / 8 : a->E / 16;  // 16-byte pieces (pairs of them) of a rotated row
-    const bool vec = a->R % 8 == 0 && a->R <= 256 * append::kMaxPieces && a->E % (a->interleaved ? 8 : 16) == 0 &&
+    const bool vec = a->R % 8 == 0 && a->R <= 1024 && a->E % (a->interleaved ? 8 : 16) == 0 &&
                      32 % per == 0 && rows16(a->kv, a->ldkv) && aligned(a->weight, 16) && aligned(a->cache, 16) &&
                      a->row_stride % 8 == 0 && a->page_stride % 8 == 0 && aligned(a->cos_sin, 16) && a->ldcs % 4 == 0 &&
                      (a->H == 0 || (rows16(a->q, a->q_token) && rows16(a->q_out, a->qo_token) && a->q_head % 8 == 0 &&
@@ -298,18 +324,21 @@ extern "C" sgemm_status_t sgemm_bf16_latent_append(const sgemm_latent_append_t *
     const cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
     cudaError_t e;
     if (vec) {
-        // Few tokens: a thread a piece (up to 512 a token), for the shortest chain.  Many: 64
-        // threads a token, so that each has several loads in flight.
-        const long long items = static_cast<long long>(a->H + 1) * per;
-        int group = 64;
-        if (T <= 4LL * sms)
-            while (group < 512 && group < items) group *= 2;
-        p.group = group;
-        const int tokens = T <= 4LL * sms ? 1 : 256 / group;
-        e = launch(a->interleaved ? reinterpret_cast<const void *>(&append::latent_append_vec_kernel<true>)
-                                  : reinterpret_cast<const void *>(&append::latent_append_vec_kernel<false>),
-                   dim3(static_cast<unsigned>((T + tokens - 1) / tokens)), dim3(static_cast<unsigned>(group * tokens)), 0, cs,
-                   pdl, &p);
+        // Few tokens: a thread a piece (up to 16 warps a token), for the shortest chain.  Many:
+        // one warp for a token's queries, several loads in flight in each.
+        const int full = (a->H * per + 31) / 32;
+        const bool many = T > 4LL * sms;
+        p.warps = many ? std::min((full + append::kBatch - 1) / append::kBatch, 4) : std::min(full, 16);
+        p.tokens = many ? 2 : 1;
+        const bool narrow = a->R <= 512;
+        const void *fn =
+            a->interleaved
+                ? (narrow ? reinterpret_cast<const void *>(&append::latent_append_vec_kernel<true, 2>)
+                          : reinterpret_cast<const void *>(&append::latent_append_vec_kernel<true, 4>))
+                : (narrow ? reinterpret_cast<const void *>(&append::latent_append_vec_kernel<false, 2>)
+                          : reinterpret_cast<const void *>(&append::latent_append_vec_kernel<false, 4>));
+        e = launch(fn, dim3(static_cast<unsigned>((T + p.tokens - 1) / p.tokens)),
+                   dim3(static_cast<unsigned>(32 * p.tokens * (p.warps + 1))), 0, cs, pdl, &p);
     } else {
         const long long work = static_cast<long long>(a->H + 1) * (a->E / 2);
         const int threads = 32 + static_cast<int>(std::min<long long>(480, (work + 31) / 32 * 32));
