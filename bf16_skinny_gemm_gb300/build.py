@@ -4,6 +4,9 @@ Each translation unit is compiled in parallel (``nvcc -c``), then linked into
 one shared library with the CUDA runtime linked statically, so the library
 needs nothing but the NVIDIA driver at run time.  Output goes to
 ``bf16_skinny_gemm_gb300/_build/``.
+
+Beside it, the host compiler builds ``_marshal.so`` (``native/marshal.cpp``), the short way from
+torch tensors to the decode operators' calls, against the installed torch.
 """
 from __future__ import annotations
 
@@ -12,6 +15,7 @@ import glob
 import os
 import shutil
 import subprocess
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -20,6 +24,8 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD_DIR = os.path.join(PKG, "_build")
 LIB_NAME = "libsgemm_skinny.so"
 LIB_PATH = os.path.join(BUILD_DIR, LIB_NAME)
+MARSHAL_SRC = os.path.join(PKG, "native", "marshal.cpp")
+MARSHAL_PATH = os.path.join(BUILD_DIR, "_marshal.so")
 
 ARCH_FLAGS = ["-gencode", "arch=compute_103a,code=sm_103a"]
 COMMON_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC,-O2",
@@ -42,16 +48,43 @@ def _deps() -> list[str]:
             + glob.glob(os.path.join(CSRC, "*.inc")) + glob.glob(os.path.join(INCLUDE, "*.h")))
 
 
-def is_stale() -> bool:
-    if not os.path.exists(LIB_PATH):
+def _stale(target: str, deps) -> bool:
+    if not os.path.exists(target):
         return True
-    t = os.path.getmtime(LIB_PATH)
-    return any(os.path.getmtime(d) > t for d in _deps())
+    t = os.path.getmtime(target)
+    return any(os.path.getmtime(d) > t for d in deps)
+
+
+def is_stale() -> bool:
+    return _stale(LIB_PATH, _deps())
+
+
+def build_marshal(force: bool = False) -> str:
+    """Compile ``_marshal.so`` if its sources changed; returns its path."""
+    deps = [MARSHAL_SRC, *glob.glob(os.path.join(INCLUDE, "*.h"))]
+    if not force and not _stale(MARSHAL_PATH, deps):
+        return MARSHAL_PATH
+    import torch
+
+    os.makedirs(BUILD_DIR, exist_ok=True)
+    home = os.path.dirname(torch.__file__)
+    cuda = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(nvcc()))), "include")
+    inc = [INCLUDE, os.path.join(home, "include"), os.path.join(home, "include", "torch", "csrc", "api", "include"),
+           sysconfig.get_paths()["include"], cuda]
+    tmp = MARSHAL_PATH + f".tmp{os.getpid()}"
+    cmd = ["g++", "-std=c++17", "-O2", "-fPIC", "-shared", *[f for d in inc for f in ("-isystem", d)], MARSHAL_SRC,
+           "-o", tmp, "-L", os.path.join(home, "lib"), "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10_cuda", "-lc10"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed for {MARSHAL_SRC}:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, MARSHAL_PATH)
+    return MARSHAL_PATH
 
 
 def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) -> str:
     """Compile and link the library if any source changed; returns its path."""
     if not force and not is_stale():
+        build_marshal()
         return LIB_PATH
     os.makedirs(BUILD_DIR, exist_ok=True)
     cc = nvcc()
@@ -68,7 +101,9 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) 
     srcs = sources()
     workers = max(1, min(len(srcs), os.cpu_count() or 4))
     with cf.ThreadPoolExecutor(workers) as ex:
+        marshal = ex.submit(build_marshal, force)
         results = list(ex.map(compile_one, srcs))
+        marshal.result()
     if verbose or ptxas_info:
         for _, log in results:
             if log.strip():

@@ -11,11 +11,15 @@ nothing then), launch flags and a stream, and can be captured into a CUDA graph.
 from __future__ import annotations
 
 import ctypes
+import importlib.machinery
+import importlib.util
+import os
 import struct
 
 import torch
 
 from . import SgemmError, load
+from .build import MARSHAL_PATH
 
 __all__ = [
     "sgemm_bf16_add_rmsnorm", "sgemm_bf16_add_rmsnorm_e4m3", "sgemm_bf16_latent_append",
@@ -37,6 +41,38 @@ _BF16 = torch.bfloat16
 _fns: dict = {}
 
 
+class _Unbound:
+    """Stands in for ``_marshal`` until the first call has loaded the library."""
+
+    def _first(self, name, args):
+        global _short
+        path = MARSHAL_PATH
+        if not os.path.exists(path):
+            raise ImportError(f"{path} is missing: build it first (python -c 'import __graft_entry__ as g; g.build()')")
+        loader = importlib.machinery.ExtensionFileLoader("_marshal", path)
+        module = importlib.util.module_from_spec(importlib.util.spec_from_loader("_marshal", loader))
+        loader.exec_module(module)
+        lib = load()
+        module.bind(*(ctypes.cast(getattr(lib, f), ctypes.c_void_p).value for f in (
+            "sgemm_bf16_add_rmsnorm", "sgemm_bf16_latent_append", "sgemm_bf16_latent_attention")))
+        _short = module
+        return getattr(module, name)(*args)
+
+    def add_rmsnorm(self, *args):
+        return self._first("add_rmsnorm", args)
+
+    def latent_append(self, *args):
+        return self._first("latent_append", args)
+
+    def latent_attention(self, *args):
+        return self._first("latent_attention", args)
+
+
+# The short way of a well-formed call with all its buffers given (native/marshal.cpp): it returns
+# the call's status, or -1 for what the checks below have to look at.
+_short = _Unbound()
+
+
 def _fn(name: str):
     f = _fns.get(name)
     if f is None:
@@ -45,6 +81,11 @@ def _fn(name: str):
         f.restype = ctypes.c_int
         _fns[name] = f
     return f
+
+
+def _raw(stream):
+    """A torch stream's handle; a handle, or None for the current stream, as it is."""
+    return stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else stream
 
 
 def _call(name: str, args: bytes, t: torch.Tensor, stream) -> None:
@@ -137,6 +178,11 @@ def sgemm_bf16_add_rmsnorm(x: torch.Tensor, weight: torch.Tensor, residual: torc
     ``(y, residual_out)`` with ``residual_out = bf16(h)`` (None where neither a residual nor a
     buffer for it is given).  x, residual: BF16 [T, D], rows of any stride; weight: BF16 [D].
     ``residual_out`` may be ``residual`` or ``x``, and ``y`` may be ``x``: in place."""
+    status = _short.add_rmsnorm(x, weight, residual, eps, SGEMM_NORM_BF16, y, None, residual_out, flags, _raw(stream))
+    if status == 0:
+        return y, residual_out
+    if status > 0:
+        raise SgemmError(status, "sgemm_bf16_add_rmsnorm")
     y, _, residual_out = _norm(x, weight, residual, eps, SGEMM_NORM_BF16, y, _BF16, None, residual_out, flags, stream)
     return y, residual_out
 
@@ -152,6 +198,11 @@ def sgemm_bf16_add_rmsnorm_e4m3(x: torch.Tensor, weight: torch.Tensor, residual:
     if group not in (0, 128):
         raise ValueError(f"group must be 128 (columns a scale) or 0 (one scale a row), got {group}")
     form = SGEMM_NORM_E4M3_GROUP128 if group else SGEMM_NORM_E4M3_ROW
+    status = _short.add_rmsnorm(x, weight, residual, eps, form, q, scales, residual_out, flags, _raw(stream))
+    if status == 0:
+        return q, scales, residual_out
+    if status > 0:
+        raise SgemmError(status, "sgemm_bf16_add_rmsnorm")
     return _norm(x, weight, residual, eps, form, q, torch.float8_e4m3fn, scales,
                  residual_out, flags, stream)
 
@@ -171,6 +222,12 @@ def sgemm_bf16_latent_append(kv: torch.Tensor, cache: torch.Tensor, slots: torch
     RMS-normalised on the way.  q, q_out: BF16 [T, H, E] views, the part of each head's query
     that is rotated and where it goes (may be the same).  ``interleaved``: the rotated pairs are
     (2i, 2i + 1), else (i, E / 2 + i)."""
+    status = _short.latent_append(kv, cache, slots, positions, cos_sin, weight, eps, q, q_out, interleaved, flags,
+                                  _raw(stream))
+    if status == 0:
+        return cache, q_out
+    if status > 0:
+        raise SgemmError(status, "sgemm_bf16_latent_append")
     T, W = shape = _shape(kv, "kv", _BF16, 2)
     pages, page_size, width = _shape(cache, "cache", _BF16, 3)
     limit, E = _shape(cos_sin, "cos_sin", torch.float32, 2)
@@ -246,6 +303,12 @@ def sgemm_bf16_latent_attention(q: torch.Tensor, cache: torch.Tensor, block_tabl
     out: BF16 [total_q, H, rank]; lse: FP32 [total_q, H] or None (not written).  ``workspace``:
     scratch on the device (:func:`sgemm_latent_attention_workspace` bytes; allocated for the call
     where None)."""
+    status = _short.latent_attention(q, cache, block_table, seq_lens, rank, scale, cu_q, max_q, out, lse, workspace, flags,
+                                     _raw(stream))
+    if status == 0:
+        return out, lse
+    if status > 0:
+        raise SgemmError(status, "sgemm_bf16_latent_attention")
     total, H, W = shape = _shape(q, "q", _BF16, 3)
     pages, page_size, width = _shape(cache, "cache", _BF16, 3)
     B, table_width = _shape(block_table, "block_table", torch.int32, 2)
