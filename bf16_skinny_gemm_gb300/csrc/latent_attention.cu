@@ -110,7 +110,7 @@ struct LatentParams {
     int B, H, R, E, max_q;
     int nt, rt, groups;     // rows a CTA, CTAs a group, groups
     int slots, rope_slots;  // rings
-    Divisor heads, ctas;    // by H, by rt
+    Divisor heads, ctas, shares;  // by H, by rt, by groups
     Divisor page_tiles;     // by the tiles of a page (pages of whole tiles)
     int row_shift;          // log2 of the rows of one copy: of a tile, or of a page where that is smaller
     float scale_log2;       // scale * log2(e)
@@ -158,20 +158,20 @@ __device__ __forceinline__ int tiles_of(const Seq &s) {
     return s.n > 0 ? max(1, (s.len + kTile - 1) / kTile + kPieceCost) : 0;
 }
 
-// a b / c for counts of tiles and groups (the quotient fits 32 bits): in 32 bits where that
-// holds the product.
-__device__ __forceinline__ int mul_div(int a, int b, int c) {
-    if (a < (1 << 20) && b < (1 << 11)) return static_cast<int>(static_cast<unsigned>(a * b) / static_cast<unsigned>(c));
-    return static_cast<int>(static_cast<long long>(a) * b / c);
+// Where the g-th of `groups` equal shares of a line of `units` tiles begins: floor(units g / groups).
+// A line shorter than p.groups is cut into shares of one tile (groups = units).
+__device__ __forceinline__ int share_begin(const LatentParams &p, int units, int g, int groups) {
+    if (units <= groups) return g;
+    if (units < (1 << 19)) return p.shares.div(units * g);  // groups = p.groups < 2^11
+    return static_cast<int>(static_cast<long long>(units) * g / groups);
 }
-
-__device__ __forceinline__ int share_begin(int units, int g, int groups) { return mul_div(units, g, groups); }
 
 // A group's share of the line.
 struct Share {
     int units, groups;  // tiles on the line, shares it is cut into
     int u0, u1;         // this share's tiles
     int b, k;           // sequence and tile of the first
+    Seq s;              // that sequence
 };
 
 // Found by each warp by itself (no block barrier before the first copies): a pass over the
@@ -180,25 +180,28 @@ __device__ __forceinline__ Share share_of(const LatentParams &p, int g, bool rep
     const int lane = threadIdx.x & 31;
     Share s;
     s.units = 0;
-    int mine = 0;
-    for (int c = 0; c < p.B; c += 32) {
-        int t = 0;
+    Seq mine;  // the lane's sequence of the last 32 read
+    mine.n = 0;
+    int c = 0;
+    for (;;) {
         if (c + lane < p.B) {
-            const Seq q = seq_of(p, c + lane);
-            if (q.bad && report) atomicOr(p.err, kErrBadIndex);
-            t = tiles_of(q);
+            mine = seq_of(p, c + lane);
+            if (mine.bad && report) atomicOr(p.err, kErrBadIndex);
+        } else {
+            mine.n = 0;
         }
-        if (c == 0) mine = t;
-        s.units += static_cast<int>(__reduce_add_sync(0xffffffffu, static_cast<unsigned>(t)));
+        s.units += static_cast<int>(__reduce_add_sync(0xffffffffu, static_cast<unsigned>(tiles_of(mine))));
+        if (c + 32 >= p.B) break;
+        c += 32;
     }
     s.groups = min(p.groups, max(s.units, 1));
     s.u0 = s.u1 = s.b = s.k = 0;
-    if (g >= s.groups) return s;
-    s.u0 = share_begin(s.units, g, s.groups);
-    s.u1 = share_begin(s.units, g + 1, s.groups);
-    if (s.u0 >= s.u1) return s;
-    for (int c = 0, at = 0;; c += 32) {
-        const int t = c == 0 ? mine : c + lane < p.B ? tiles_of(seq_of(p, c + lane)) : 0;
+    if (g >= min(s.groups, s.units)) return s;
+    s.u0 = share_begin(p, s.units, g, s.groups);
+    s.u1 = share_begin(p, s.units, g + 1, s.groups);
+    if (c > 0) mine = seq_of(p, lane);
+    for (int at = 0, b0 = 0;;) {
+        const int t = b0 + lane < p.B ? tiles_of(mine) : 0;
         int x = t;
 #pragma unroll
         for (int off = 1; off < 32; off <<= 1) {
@@ -208,11 +211,17 @@ __device__ __forceinline__ Share share_of(const LatentParams &p, int g, bool rep
         const unsigned past = __ballot_sync(0xffffffffu, s.u0 < at + x);
         if (past) {
             const int w = __ffs(past) - 1;
-            s.b = c + w;
+            s.b = b0 + w;
             s.k = s.u0 - at - __shfl_sync(0xffffffffu, x - t, w);
+            s.s.q0 = __shfl_sync(0xffffffffu, mine.q0, w);
+            s.s.n = __shfl_sync(0xffffffffu, mine.n, w);
+            s.s.n_all = __shfl_sync(0xffffffffu, mine.n_all, w);
+            s.s.len = __shfl_sync(0xffffffffu, mine.len, w);
             return s;
         }
         at += __shfl_sync(0xffffffffu, x, 31);
+        b0 += 32;
+        if (b0 + lane < p.B) mine = seq_of(p, b0 + lane);
     }
 }
 
@@ -233,9 +242,15 @@ struct Piece {
 
 struct Walk {
     int b, k, left;
+    Seq s;       // sequence b, where it is known
+    bool known;
+    __device__ __forceinline__ explicit Walk(const Share &sh)
+        : b(sh.b), k(sh.k), left(sh.u1 - sh.u0), s(sh.s), known(true) {}
     __device__ __forceinline__ bool next(const LatentParams &p, int r, Piece &o) {
         while (left > 0) {
-            o.s = seq_of(p, b);
+            o.s = s;
+            if (!known) o.s = seq_of(p, b);
+            known = false;
             const int kt = tiles_of(o.s);
             const int take = min(kt - k, left);
             o.b = b;
@@ -260,14 +275,14 @@ struct Walk {
     }
 };
 
-// The pages of a piece's tiles, read 32 table entries at a time (one load a warp for 8 to 32
-// tiles), a batch ahead.  A tile is copied in `copies` pieces of `rows` rows of a page each.
+// The pages of a piece's tiles, read 32 table entries at a time (one load a warp for 4 to 32
+// tiles).  A tile is copied in `copies` pieces of `rows` rows of a page each.
 struct Pages {
     const int *table;
     int rows, shift, per;  // rows a copy, log2 of the copies of a whole tile, their number
     int limit;             // rows the sequence has, as far as the piece goes
     int first;             // the first tile of the batch in `now`
-    int now, next;
+    int now;
     int k, copies, row;    // the current tile, its copies, the first one's row in its page
     int pages;             // (the page past the last one reads as zeros)
     bool whole;            // a tile lies in one page
@@ -291,7 +306,6 @@ struct Pages {
         pages = p.pages;
         first = o.k0;
         now = look(p, first);
-        next = look(p, first + (32 >> shift));
         row = whole ? p.page_tiles.mod(first) * kTile - kTile : 0;
     }
     // on to a tile: the first one, then one by one
@@ -299,8 +313,7 @@ struct Pages {
         k = tile;
         if (k == first + (32 >> shift)) {
             first = k;
-            now = next;
-            next = look(p, k + (32 >> shift));
+            now = look(p, k);
         }
         copies = (min(kTile, limit - k * kTile) + rows - 1) >> p.row_shift;
         if (whole) {
@@ -589,7 +602,7 @@ __global__ void __launch_bounds__(threads_of(NT), 1) latent_attention_kernel(con
     }
     const Share sh = share_of(p, g, blockIdx.x == 0 && warp == 2);
     const uint32_t t_o = tmem + 2 * kSCols;
-    Walk walk{sh.b, sh.k, sh.u1 - sh.u0};
+    Walk walk(sh);
     const bool stall = (p.flags & kFlagTestStall) != 0;
     Piece o;
     int issued = 0, rissued = 0;  // slots of each ring that the producer filled
@@ -611,9 +624,11 @@ __global__ void __launch_bounds__(threads_of(NT), 1) latent_attention_kernel(con
                 const int copies = alike(pages.copies), step = pages.rows * 128;
                 const int row = alike(pages.row);
                 int page[kMaxCopies];
+                page[0] = alike(pages.page(p, 0));
+                if (copies > 1)
 #pragma unroll
-                for (int f = 0; f < kMaxCopies; ++f)
-                    if (f < copies) page[f] = alike(pages.page(p, f));
+                    for (int f = 1; f < kMaxCopies; ++f)
+                        if (f < copies) page[f] = alike(pages.page(p, f));
                 for (int j = 0; j < pairs; ++j) {
                     if ((at & 1) == (warp == 0 ? 0 : 1)) {
                         if (!(ok = at < S || all_wait(vempty + 8 * slot, ph ^ 1, &stop))) break;
@@ -649,9 +664,11 @@ __global__ void __launch_bounds__(threads_of(NT), 1) latent_attention_kernel(con
                 if (elect()) {
                     bar_expect_tx(bar, static_cast<unsigned>(copies * step));
                     if (!stall) {
+                        tma_3d(dst, &p.tr, 0, row, page[0], bar);
+                        if (copies > 1)
 #pragma unroll
-                        for (int f = 0; f < kMaxCopies; ++f)
-                            if (f < copies) tma_3d(dst + f * step, &p.tr, 0, row, page[f], bar);
+                            for (int f = 1; f < kMaxCopies; ++f)
+                                if (f < copies) tma_3d(dst + f * step, &p.tr, 0, row, page[f], bar);
                     }
                 }
                 __syncwarp();
@@ -788,8 +805,7 @@ __global__ void __launch_bounds__(threads_of(NT), 1) latent_attention_kernel(con
             if (tell && o.first) {
                 const int u_last = sh.u0 + (sh.u1 - sh.u0 - o.left) + tiles_of(o.s) - 1;
                 // the last share that begins at or before u_last: ceil((u_last + 1) groups / units) - 1
-                int g1 = mul_div(u_last + 1, sh.groups, sh.units);
-                if (share_begin(sh.units, g1, sh.groups) > u_last) --g1;
+                const int g1 = static_cast<int>((static_cast<long long>(u_last + 1) * sh.groups - 1) / sh.units);
                 if (p.by_seq || !o.last) desc[p.by_seq ? o.b : g] = make_int4(o.s.q0, o.s.n, g, o.last ? -1 : g1);
             }
             float m[NC], l[NC];
@@ -1402,6 +1418,7 @@ extern "C" sgemm_status_t sgemm_bf16_latent_attention(const sgemm_latent_attenti
 
     p.heads = Divisor::of(a->H);
     p.ctas = Divisor::of(sp.rt);
+    p.shares = Divisor::of(sp.groups);
     p.page_tiles = Divisor::of(std::max(1, a->page_size / kTile));
     p.row_shift = a->page_size >= kTile ? 6 : a->page_size == 32 ? 5 : a->page_size == 16 ? 4 : 3;
     p.out16 = aligned(a->out, 16) && a->out_token % 8 == 0 && a->out_head % 8 == 0 ? 1 : 0;
