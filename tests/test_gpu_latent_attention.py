@@ -159,6 +159,29 @@ def test_strided_views():
     assert torch.all(big[..., :6] == 5) and torch.all(big[..., 518:] == 5) and torch.all(ld[:, 12:] == 5)
 
 
+@pytest.mark.parametrize("H", [7, 20, 100])
+def test_queries_whose_rows_are_not_evenly_spaced(H):
+    """Some heads of each token: no one stride leads from row to row."""
+    qs, lens = [1, 4, 2], [300, 77, 64]
+    q, cache, table, ln, cu = make(lens, qs, H + 3, page=32, seed=21)
+    out, lse = run(q[:, 2 : 2 + H], cache, table, ln, cu, 512, 0.06, 4)
+    qd = q.to(DEV)
+    got, _ = sk.sgemm_bf16_latent_attention(qd[:, 2 : 2 + H], cache.to(DEV), table.to(DEV), ln.to(DEV), 512, 0.06,
+                                            cu_q=cu.to(DEV), max_q=4)
+    torch.cuda.synchronize()
+    want, wlse, ob, lb = D.latent_attention(q[:, 2 : 2 + H], cache, table, ln, 512, 0.06, cu)
+    D.check(got, want, ob, "out")
+    D.check(lse, wlse, lb, "lse")
+    assert torch.equal(got.view(torch.int16), out.view(torch.int16))
+
+
+def test_one_long_sequence_among_short_ones():
+    """Most shares are pieces of one sequence, whose pieces the few-pieces kernel joins."""
+    lens = [1 + 13 * b % 90 for b in range(40)]
+    lens[17] = 30000
+    compare(lens, [1] * 40, 16, R=128, seed=22)
+
+
 def test_no_lse_no_cu_q_own_workspace_and_stream():
     q, cache, table, ln, cu = make([700, 300], [2, 2], 32, seed=15)
     want, _, ob, _ = D.latent_attention(q, cache, table, ln, 512, 0.05, cu)
