@@ -130,10 +130,8 @@ struct Piece {
 template <bool INTER, int PIECES>
 __global__ void __launch_bounds__(544) latent_append_vec_kernel(const __grid_constant__ AppendParams p) {
     const sgemm_latent_append_t &a = p.a;
-    if (a.flags & SGEMM_FLAG_PDL) {
-        pdl_launch_dependents();
-        pdl_wait();
-    }
+    if (a.flags & SGEMM_FLAG_PDL) pdl_launch_dependents();
+    pdl_wait();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = p.warps + 1;
     const int which = warp / warps, w = warp % warps - 1;
     const long long t = static_cast<long long>(blockIdx.x) * p.tokens + which;
@@ -205,10 +203,8 @@ __global__ void __launch_bounds__(544) latent_append_vec_kernel(const __grid_con
 // and once for its output.
 __global__ void __launch_bounds__(512) latent_append_any_kernel(const __grid_constant__ AppendParams p) {
     const sgemm_latent_append_t &a = p.a;
-    if (a.flags & SGEMM_FLAG_PDL) {
-        pdl_launch_dependents();
-        pdl_wait();
-    }
+    if (a.flags & SGEMM_FLAG_PDL) pdl_launch_dependents();
+    pdl_wait();
     const long long t = blockIdx.x;
     const int lane = threadIdx.x & 31;
     const uint16_t *kv = a.kv + t * a.ldkv;
@@ -320,7 +316,6 @@ extern "C" sgemm_status_t sgemm_bf16_latent_append(const sgemm_latent_append_t *
                      a->row_stride % 8 == 0 && a->page_stride % 8 == 0 && aligned(a->cos_sin, 16) && a->ldcs % 4 == 0 &&
                      (a->H == 0 || (rows16(a->q, a->q_token) && rows16(a->q_out, a->qo_token) && a->q_head % 8 == 0 &&
                                     a->qo_head % 8 == 0));
-    const bool pdl = (a->flags & SGEMM_FLAG_PDL) != 0;
     const cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
     cudaError_t e;
     if (vec) {
@@ -338,12 +333,12 @@ extern "C" sgemm_status_t sgemm_bf16_latent_append(const sgemm_latent_append_t *
                 : (narrow ? reinterpret_cast<const void *>(&append::latent_append_vec_kernel<false, 2>)
                           : reinterpret_cast<const void *>(&append::latent_append_vec_kernel<false, 4>));
         e = launch(fn, dim3(static_cast<unsigned>((T + p.tokens - 1) / p.tokens)),
-                   dim3(static_cast<unsigned>(32 * p.tokens * (p.warps + 1))), 0, cs, pdl, &p);
+                   dim3(static_cast<unsigned>(32 * p.tokens * (p.warps + 1))), 0, cs, &p);
     } else {
         const long long work = static_cast<long long>(a->H + 1) * (a->E / 2);
         const int threads = 32 + static_cast<int>(std::min<long long>(480, (work + 31) / 32 * 32));
         e = launch(reinterpret_cast<const void *>(&append::latent_append_any_kernel), dim3(static_cast<unsigned>(T)),
-                   dim3(static_cast<unsigned>(threads)), 0, cs, pdl, &p);
+                   dim3(static_cast<unsigned>(threads)), 0, cs, &p);
     }
     if (e != cudaSuccess) return SGEMM_ERR_CUDA;
     return SGEMM_OK;

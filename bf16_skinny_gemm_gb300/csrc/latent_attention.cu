@@ -580,7 +580,7 @@ __global__ void __launch_bounds__(threads_of(NT), 1) latent_attention_kernel(con
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         __syncwarp();
     }
-    if (p.flags & kFlagPdl) pdl_wait();
+    pdl_wait();
     uint32_t tmem = 0;
     if (warp == 0) {
         // the producer goes on: it needs the mbarriers only, which are its own work
@@ -1108,7 +1108,7 @@ __global__ void __launch_bounds__(PB == 8 ? 1024 : 128) latent_join_kernel(const
     constexpr int kWarps = PB == 8 ? 32 : 1;  // warps that share elements
     __shared__ __align__(16) float4 acc[kWarps][32];
     __shared__ float tacc[kWarps][4], lacc[kWarps][4];
-    pdl_launch_dependents();
+    if (p.flags & kFlagPdl) pdl_launch_dependents();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int row0 = 4 * static_cast<int>(blockIdx.y), i = row0 & (p.nt - 1), r = row0 / p.nt;
     // many: the block's warps share one slab; few: each has its own ES slabs
@@ -1443,8 +1443,7 @@ extern "C" sgemm_status_t sgemm_bf16_latent_attention(const sgemm_latent_attenti
         }
     }
     const cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
-    if (launch(fn, dim3(static_cast<unsigned>(sp.groups * sp.rt)), dim3(static_cast<unsigned>(threads_of(sp.nt))), static_cast<size_t>(smem), cs,
-               (a->flags & SGEMM_FLAG_PDL) != 0, &p) != cudaSuccess)
+    if (launch(fn, dim3(static_cast<unsigned>(sp.groups * sp.rt)), dim3(static_cast<unsigned>(threads_of(sp.nt))), static_cast<size_t>(smem), cs, &p) != cudaSuccess)
         return SGEMM_ERR_CUDA;
     if (sp.groups == 1) return SGEMM_OK;
     // pieces that a sequence may have: by the line's equal shares, if all sequences were as long
@@ -1457,10 +1456,9 @@ extern "C" sgemm_status_t sgemm_bf16_latent_attention(const sgemm_latent_attenti
                     static_cast<unsigned>(few ? 1 : a->R / 32));
     const void *join = few ? reinterpret_cast<const void *>(&latent_join_kernel<4, 4>)
                            : reinterpret_cast<const void *>(&latent_join_kernel<8, 1>);
-    // As a programmatic dependent, though the first kernel never lets it come early: its launch is
-    // then prepared while that one runs (1.5 to 2 us), but blocks that came early were in the way
-    // of CTAs still running (verification of 8 sequences: 28.8 us, against 26.7).
-    if (launch(join, grid, dim3(static_cast<unsigned>(32 * (few ? a->R / 128 : p.pw))), 0, cs, true, &p) != cudaSuccess)
+    // The first kernel never lets this one come early: blocks that came were in the way of CTAs
+    // still running (verification of 8 sequences: 28.8 us, against 26.7).
+    if (launch(join, grid, dim3(static_cast<unsigned>(32 * (few ? a->R / 128 : p.pw))), 0, cs, &p) != cudaSuccess)
         return SGEMM_ERR_CUDA;
     return SGEMM_OK;
 }

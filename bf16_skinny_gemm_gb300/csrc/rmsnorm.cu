@@ -172,12 +172,11 @@ __global__ void __launch_bounds__(most_threads(NV)) add_rmsnorm_kernel(const __g
     using DL = Deal<VEC>;
     constexpr int E = DL::kUnit;
     __shared__ float part[2][32];
-    const bool pdl = (p.flags & kFlagPdl) != 0;
-    if (pdl) pdl_launch_dependents();
+    if (p.flags & kFlagPdl) pdl_launch_dependents();
     const int tpr = p.tpr, wr = tpr >> 5;
     const int t = threadIdx.x % tpr;
     const long long row = static_cast<long long>(blockIdx.x) * (blockDim.x / tpr) + threadIdx.x / tpr;
-    if (pdl) pdl_wait();
+    pdl_wait();
     if (row >= p.T) return;  // whole warps, and no block barrier is used where a block has several rows
 
     float h[NV][E];
@@ -265,11 +264,8 @@ __global__ void __launch_bounds__(most_threads(NV)) add_rmsnorm_kernel(const __g
 template <int FORM>
 __global__ void __launch_bounds__(1024) add_rmsnorm_long_kernel(const __grid_constant__ NormParams p) {
     __shared__ float part[2][32];
-    const bool pdl = (p.flags & kFlagPdl) != 0;
-    if (pdl) {
-        pdl_launch_dependents();
-        pdl_wait();
-    }
+    if (p.flags & kFlagPdl) pdl_launch_dependents();
+    pdl_wait();
     const long long row = blockIdx.x;
     const int wr = blockDim.x >> 5;
     const uint16_t *x = p.x + row * p.ldx;
@@ -437,7 +433,7 @@ extern "C" sgemm_status_t sgemm_bf16_add_rmsnorm(const sgemm_add_rmsnorm_t *a, s
         block = dim3(static_cast<unsigned>(p.tpr * rows));
         grid = dim3(static_cast<unsigned>((T + rows - 1) / rows));
     }
-    if (launch(fn, grid, block, 0, reinterpret_cast<cudaStream_t>(stream), (a->flags & SGEMM_FLAG_PDL) != 0, &p) !=
+    if (launch(fn, grid, block, 0, reinterpret_cast<cudaStream_t>(stream), &p) !=
         cudaSuccess)
         return SGEMM_ERR_CUDA;
     return SGEMM_OK;

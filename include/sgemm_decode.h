@@ -13,8 +13,14 @@
  * graph.  Results are deterministic: the same inputs give the same bits.
  * Strides are in elements.  The argument structures are HOST memory, read
  * during the call only; clear them (memset) before filling them in.
- * `flags`: 0 or SGEMM_FLAG_PDL (with SGEMM_FLAG_WEIGHTS_READONLY, which covers
- * `weight` here), as for the GEMM calls; other bits are refused.
+ * The kernels are always launched as programmatic dependents of the previous
+ * kernel on the stream, and wait for it before they read or write any memory,
+ * so the order is that of plain launches.  (One thing is asked of a previous
+ * kernel that is a programmatic dependent itself: that it waits for its own,
+ * griddepcontrol.wait, as all of this library's do.)
+ * `flags`: 0, or SGEMM_FLAG_PDL: the kernel also lets the next one, if it is a
+ * programmatic dependent, launch early.  SGEMM_FLAG_WEIGHTS_READONLY is taken
+ * beside it and changes nothing; other bits are refused.
  */
 #ifndef SGEMM_DECODE_H
 #define SGEMM_DECODE_H
