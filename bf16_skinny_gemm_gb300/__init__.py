@@ -386,7 +386,8 @@ def sgemm_init() -> None:
 
 def sgemm_device_errors() -> int:
     """Read and clear the device error word of the current device (synchronous).
-    Bit 0: a kernel gave up a bounded wait for its data and wrote NaN outputs."""
+    Bit 0: a kernel gave up a bounded wait for its data and wrote NaN outputs.  Bit 1: an operator
+    of a decode step met an index in device memory that was out of range, and skipped or cut it."""
     v = ctypes.c_int(0)
     _check(load().sgemm_device_errors(ctypes.byref(v)), "sgemm_device_errors")
     return v.value

@@ -6,6 +6,11 @@
 //
 // Every byte is read and written once and there are a few operations an
 // element: bound by memory for many tokens, by latency for few.
+//
+// Measured on one GB300, calls one after the other: 16384 tokens with 32 heads'
+// queries 33.1 us (176 MB, 5.3 TB/s, 0.78 of the measured copy rate: the queries'
+// parts are 128 bytes every 1152, and a warp waits for a position, then its
+// angles, then stores); 1 to 777 tokens 2.7 us, a launch and that chain.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -64,7 +69,7 @@ __device__ __forceinline__ uint16_t *row_of(const AppendParams &p, long long slo
     return p.a.cache + page * p.a.page_stride + row * p.a.row_stride;
 }
 
-constexpr int kBatch = 4;  // pieces of queries a thread loads at once
+constexpr int kBatch = 4;  // pieces of queries a thread loads at once (16384 tokens: 4 35 us, 2 49, 6 42)
 
 // Cosines and sines of the pairs of piece u (PAIRS of them) at a position; NaN where it is out
 // of range.
@@ -319,10 +324,13 @@ extern "C" sgemm_status_t sgemm_bf16_latent_append(const sgemm_latent_append_t *
     const cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
     cudaError_t e;
     if (vec) {
-        // Few tokens: a thread a piece (up to 16 warps a token), for the shortest chain.  Many:
-        // one warp for a token's queries, several loads in flight in each.
+        // Few tokens: a thread a piece (up to 16 warps a token), for the shortest chain.  More than
+        // one for each SM: one warp for a token's queries where they fit, several loads in flight
+        // in each, two tokens a block.  The one against the other, 128 heads: 8 tokens 2.68 us,
+        // 2.8; 300 tokens 3.1, 2.85; 32 heads: 1200 tokens 5.1, 3.0; 16384 tokens with one token a
+        // block in place of two 34.9 for 35.3, with four 36.9.
         const int full = (a->H * per + 31) / 32;
-        const bool many = T > 4LL * sms;
+        const bool many = T > sms;
         p.warps = many ? std::min((full + append::kBatch - 1) / append::kBatch, 4) : std::min(full, 16);
         p.tokens = many ? 2 : 1;
         const bool narrow = a->R <= 512;

@@ -23,12 +23,13 @@
 //  * Warp 0 and the last one stream the tiles with TMA into a ring of slots (two
 //    chunks, 128 latent elements, a slot; the E elements in a ring of their own).  Slots
 //    rather than tiles: a slot is free again as soon as its part of O^T is
-//    done, and what is left of shared memory beside Q holds 1.75 to 2.5 tiles.
-//  * Warp 1 issues the first product (and copies the queries), the last but one the second.  Two warps, because
-//    neither may wait for the other's operands: O^T of tile t is issued as soon
-//    as its weights are there, which frees the tile's slots, and S^T of tile
-//    t + 1 as its slots arrive.
-//  * Warps 2..5 do the softmax: S^T is read in the 16 x 256-bit form, so that
+//    done, and what is left of shared memory beside Q holds 2 to 2.5 tiles.
+//  * Warp 1 issues the first product (and copies the queries), the last but one
+//    the second.  Two warps, because neither may wait for the other's operands:
+//    O^T of tile t is issued as soon as its weights are there, which frees the
+//    tile's slots, and S^T of tile t + 1 as its slots arrive.  (One warp for
+//    both, one for the copies: 64 sequences of up to 8192 115 us, against 77.5.)
+//  * Warps 2..5 (2..9 with 64 rows) do the softmax: S^T is read in the 16 x 256-bit form, so that
 //    all lanes hold scores though M = 64 fills half of the lanes.  The running
 //    maximum of a row is over keys, which lie across lanes and warps; it is
 //    exchanged only in tiles where some score exceeds the maximum in use by
@@ -43,6 +44,18 @@
 // CTA finds its share itself.  A sequence that a share ends in leaves partial
 // results (FP32 O, m and l), which a second kernel joins in the order of the
 // shares: the result does not depend on timing.
+//
+// Measured on one GB300, calls one after the other, 512 + 64 elements:
+//   32 heads, 64 sequences of up to 8192 (378 MB)    74.0 us  5.1 TB/s
+//   32 heads, one sequence of 131072 (151 MB)        36.7 us  4.1 TB/s
+//   128 heads, 32 sequences of 8192 (73 GFLOP)      105   us  0.69 PFLOP/s
+//   20 heads, 8 x 8 tokens, up to 4099 rows          24.9 us
+//   32 heads, one sequence of 1000                   11.6 us
+// A tile more a CTA costs 1.76 us with 32 heads, 0.94 of the measured copy rate
+// for all SMs; with 128 heads 1.59 us (1.55 from the L2 cache), of which the
+// MMAs are 1.0: there the ring's turn (copy, S^T, softmax, O^T, with two tiles in
+// flight) bounds it.  Beside the tiles a call costs 10 to 20 us: the start until
+// the first copies land, the pieces' results, the joining kernel.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cudaTypedefs.h>
@@ -63,14 +76,14 @@ constexpr int kTile = 64;                // keys per tile (M of the first produc
 constexpr int kChunk = kTile * 64 * 2;   // 64 keys x 64 elements
 constexpr int kSlot = 2 * kChunk;        // 128 latent elements (M of the second product)
 constexpr int kMaxSlots = 12;
-constexpr int kMaxRopeSlots = 3;
+constexpr int kRopeSlots = 2;  // (3: the same times)
 // Warps: copies, first product, 4 soft_parts of softmax, second product, copies.
 __host__ __device__ constexpr int soft_parts(int nt) { return nt == 64 ? 2 : 1; }
 // Buffers of weights, 8 KiB each.  With 64 rows one: it is read long before it is written again,
 // and what it frees holds a second slot of rotated elements beside two whole tiles of latent ones.
 __host__ __device__ constexpr int weight_buffers(int nt) { return nt == 64 ? 1 : 2; }
 __host__ __device__ constexpr int threads_of(int nt) { return 128 + 128 * soft_parts(nt); }
-constexpr int kPieceCost = 1;            // see tiles_of
+constexpr int kPieceCost = 1;            // see tiles_of (1: verification of 8 sequences 32.3 us; 0: 33.9)
 constexpr float kLazy = 8.0f;            // log2 of the largest weight before a maximum moves
 constexpr float kNoMax = -3.4028234e38f;  // no score is smaller: the maximum of none
 constexpr int kMaxCopies = 8;            // copies of a chunk of a tile: pages of at least 8 rows
@@ -109,7 +122,7 @@ struct LatentParams {
     int pages, page_size, width;
     int B, H, R, E, max_q;
     int nt, rt, groups;     // rows a CTA, CTAs a group, groups
-    int slots, rope_slots;  // rings
+    int slots;    // of latent elements in the ring
     Divisor heads, ctas, shares;  // by H, by rt, by groups
     Divisor page_tiles;     // by the tiles of a page (pages of whole tiles)
     int row_shift;          // log2 of the rows of one copy: of a tile, or of a page where that is smaller
@@ -442,7 +455,8 @@ __device__ __forceinline__ void tma_4d(uint32_t dst, const CUtensorMap *map, int
         : "memory");
 }
 
-// How the L2 cache keeps what is copied: evicted first where this CTA is its only reader.
+// How the L2 cache keeps what is copied: evicted first where this CTA is its only reader (one
+// sequence of 131072: 36.7 us, 38.3 without; where two CTAs read a tile, 128 heads, 110 became 132).
 __device__ __forceinline__ uint64_t policy_of(bool once) {
     uint64_t r;
     if (once)
@@ -541,7 +555,8 @@ __global__ void __launch_bounds__(threads_of(NT), 1) latent_attention_kernel(con
     extern __shared__ __align__(1024) uint8_t base[];  // the only shared memory: it starts on 1 KiB
     const int pairs = p.R / 128;            // slots a tile
     const int qchunk = NT * 128;            // bytes of a chunk of Q
-    const int S = p.slots, RS = p.rope_slots;
+    const int S = p.slots;
+    constexpr int RS = kRopeSlots;
     const uint32_t s_q = saddr(base);
     const uint32_t s_p = s_q + (2 * pairs + 1) * qchunk;
     const uint32_t s_r = s_p + NP * kChunk;
@@ -554,8 +569,8 @@ __global__ void __launch_bounds__(threads_of(NT), 1) latent_attention_kernel(con
     int &stop = *reinterpret_cast<int *>(tmem_slot + 1);
 
     const uint32_t vfull = saddr(bars), vempty = vfull + 8 * kMaxSlots;
-    const uint32_t rfull = vempty + 8 * kMaxSlots, rempty = rfull + 8 * kMaxRopeSlots;
-    const uint32_t qfull = rempty + 8 * kMaxRopeSlots, qempty = qfull + 8;
+    const uint32_t rfull = vempty + 8 * kMaxSlots, rempty = rfull + 8 * kRopeSlots;
+    const uint32_t qfull = rempty + 8 * kRopeSlots, qempty = qfull + 8;
     const uint32_t sfull = qempty + 8, sempty = sfull + 16, pfull = sempty + 16, pvd = pfull + 16, fin = pvd + 16;
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -1100,9 +1115,10 @@ __global__ void __launch_bounds__(threads_of(NT), 1) latent_attention_kernel(con
 // ------------------------------------------------------------------ joining partial results
 // A warp takes ES slabs of 32 elements of four rows of a split sequence, PB pieces at a time; the
 // pw warps of a block with the same elements take every pw-th PB pieces and are added in their
-// order.  Lane 4 q + e works out the weight of piece q for row e.  Few pieces (a batch of
-// sequences): 4 at a time and 128 elements, so that a weight serves 16 products.  Many (a long
-// sequence over all groups): 8 at a time, up to 32 warps, so that all are read at once.
+// order.  Lane 4 q + e works out the weight of piece q for row e.  Where there are many rows (a
+// batch of sequences): 4 at a time and 128 elements, so that a weight serves 16 products.  Where
+// there are few (one long sequence over all groups): 8 at a time, up to 32 warps, so that all are
+// read at once.
 template <int PB, int ES>
 __global__ void __launch_bounds__(PB == 8 ? 1024 : 128) latent_join_kernel(const __grid_constant__ LatentParams p) {
     constexpr int kWarps = PB == 8 ? 32 : 1;  // warps that share elements
@@ -1253,6 +1269,9 @@ struct Split {
 Split split_of(const sgemm_latent_attention_t &a, int sms) {
     Split s;
     const long long rows = static_cast<long long>(a.max_q) * a.H;
+    // The fewest that hold a sequence's rows, for the room they leave to the ring and the softmax's
+    // registers (16 sequences of 8192, 16 heads: 16 rows 33.7 us, 32 34.5, 64 36.9; 32 heads: 32 rows
+    // 38.6, 64 40.6); more than 64 would leave room for one tile.
     s.nt = rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
     s.rt = static_cast<int>((rows + s.nt - 1) / s.nt);
     const long long tiles = std::max(1LL, (static_cast<long long>(a.table_width) * a.page_size + kTile - 1) / kTile);
@@ -1424,8 +1443,7 @@ extern "C" sgemm_status_t sgemm_bf16_latent_attention(const sgemm_latent_attenti
     p.by_seq = a->B < sp.groups ? 1 : 0;
     // Shared memory: Q, the weights, the rotated elements' ring, then as many slots of latent
     // elements as there is room for
-    p.rope_slots = sp.nt == 64 ? 2 : 3;
-    const int fixed = (a->R / 64 + 1) * sp.nt * 128 + weight_buffers(sp.nt) * kChunk + p.rope_slots * kChunk + kBarBytes +
+    const int fixed = (a->R / 64 + 1) * sp.nt * 128 + weight_buffers(sp.nt) * kChunk + kRopeSlots * kChunk + kBarBytes +
                       40 * sp.nt + 16;
     p.slots = std::min(kMaxSlots, (static_cast<int>(kMaxSmemOptin) - fixed) / kSlot);
     const int smem = fixed + p.slots * kSlot;
@@ -1446,13 +1464,16 @@ extern "C" sgemm_status_t sgemm_bf16_latent_attention(const sgemm_latent_attenti
     if (launch(fn, dim3(static_cast<unsigned>(sp.groups * sp.rt)), dim3(static_cast<unsigned>(threads_of(sp.nt))), static_cast<size_t>(smem), cs, &p) != cudaSuccess)
         return SGEMM_ERR_CUDA;
     if (sp.groups == 1) return SGEMM_OK;
-    // pieces that a sequence may have: by the line's equal shares, if all sequences were as long
-    // as the table allows; few are joined by one warp, many by up to 32
-    const int parts = p.by_seq ? (sp.groups + a->B - 1) / a->B + 1 : 2;
-    const bool few = parts <= 8;
-    p.pw = few ? 1 : std::min(32, (parts + 7) / 8);
+    // Joining: one warp for 128 elements of four rows of a sequence, where these warps are enough to
+    // keep the loads coming (2.5 for each SM); else warps that share a sequence's pieces (as many as
+    // it would have if all were as long as the table allows), for 32 elements.  The one against the
+    // other, 8192 rows with 32 heads: 9 sequences (288 warps) 26.4 us, 25.3; 12 (384) 30.9, 31.0;
+    // 16 (512) 36.6, 38.6; 64 (2048) 74.2, 79.6; one of 131072 (32) 57.5, 36.7.
     const long long rows = static_cast<long long>(a->max_q) * a->H;
-    const dim3 grid(static_cast<unsigned>(p.by_seq ? a->B : sp.groups), static_cast<unsigned>((rows + 3) / 4),
+    const int n = p.by_seq ? a->B : sp.groups, parts = p.by_seq ? (sp.groups + a->B - 1) / a->B + 1 : 2;
+    const bool few = (rows + 3) / 4 * (a->R / 128) * n * 2 >= 5LL * sms;
+    p.pw = few ? 1 : std::min(32, (parts + 7) / 8);
+    const dim3 grid(static_cast<unsigned>(n), static_cast<unsigned>((rows + 3) / 4),
                     static_cast<unsigned>(few ? 1 : a->R / 32));
     const void *join = few ? reinterpret_cast<const void *>(&latent_join_kernel<4, 4>)
                            : reinterpret_cast<const void *>(&latent_join_kernel<8, 1>);

@@ -328,8 +328,11 @@ sgemm_status_t sgemm_splitk_noalloc_plan(int N, int K, int M, int split_k,
                                          const sgemm_plan_t *selected, sgemm_plan_t *out);
 
 /* Reads and clears the device error word of the current device: bit 0 is set
- * when a kernel gave up a bounded wait for its data (SGEMM_VARIANT_TC05; the
- * outputs of that launch were written as NaN).
+ * when a kernel gave up a bounded wait for its data (SGEMM_VARIANT_TC05,
+ * SGEMM_VARIANT_LDG_CLUSTER, sgemm_bf16_latent_attention; the outputs that
+ * were waited for were written as NaN), bit 1 when an operator of
+ * sgemm_decode.h met an index in device memory that was out of range (it was
+ * skipped or cut as that header says).
  * *flags = 0 when nothing went wrong.  The word is a static device variable
  * of the library (no allocation).  Synchronous (waits for the device); do not
  * call during stream capture. */
