@@ -176,10 +176,16 @@ def test_queries_whose_rows_are_not_evenly_spaced(H):
 
 
 def test_one_long_sequence_among_short_ones():
-    """Most shares are pieces of one sequence, whose pieces the few-pieces kernel joins."""
+    """Most shares are pieces of one sequence, more than its joining warps take in one turn."""
     lens = [1 + 13 * b % 90 for b in range(40)]
     lens[17] = 30000
     compare(lens, [1] * 40, 16, R=128, seed=22)
+
+
+@pytest.mark.parametrize("lens,H", [([1500, 0, 2900, 1, 700], 128), ([3000, 80], 512), ([40] * 20 + [9000], 64)])
+def test_many_pieces_of_many_rows(lens, H):
+    """Rows enough for one joining warp a sequence, and more pieces than it takes in one turn."""
+    compare(lens, [1] * len(lens), H, seed=23)
 
 
 def test_no_lse_no_cu_q_own_workspace_and_stream():
