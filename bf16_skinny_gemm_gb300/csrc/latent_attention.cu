@@ -21,16 +21,17 @@
 //    One copy of the tile in shared memory (64 rows x 128 bytes per chunk of 64
 //    elements, 128-byte swizzle) serves as A of both products.
 //  * Warp 0 and the last one stream the tiles with TMA into a ring of slots (two
-//    chunks, 128 latent elements, a slot; the E elements in a ring of their own).  Slots
-//    rather than tiles: a slot is free again as soon as its part of O^T is
+//    chunks, 128 latent elements, a slot; the E elements in a ring of their
+//    own).  Slots rather than tiles: a slot is free again as soon as its part of O^T is
 //    done, and what is left of shared memory beside Q holds 2 to 2.5 tiles.
 //  * Warp 1 issues the first product (and copies the queries), the last but one
 //    the second.  Two warps, because neither may wait for the other's operands:
 //    O^T of tile t is issued as soon as its weights are there, which frees the
-//    tile's slots, and S^T of tile t + 1 as its slots arrive.  (One warp for
-//    both, one for the copies: 64 sequences of up to 8192 115 us, against 77.5.)
-//  * Warps 2..5 (2..9 with 64 rows) do the softmax: S^T is read in the 16 x 256-bit form, so that
-//    all lanes hold scores though M = 64 fills half of the lanes.  The running
+//    tile's slots, and S^T of tile t + 1 as its slots arrive.  (In an early
+//    form, 64 sequences of up to 8192: 115 us, 127 with one warp for both.)
+//  * Warps 2..5 (2..9 with 64 rows) do the softmax: S^T is read in the 16 x
+//    256-bit form, so that all lanes hold scores though M = 64 fills half of the
+//    lanes.  The running
 //    maximum of a row is over keys, which lie across lanes and warps; it is
 //    exchanged only in tiles where some score exceeds the maximum in use by
 //    more than 2^8 (in units of the result), else the old one stands: one
@@ -48,9 +49,9 @@
 // Measured on one GB300, calls one after the other, 512 + 64 elements:
 //   32 heads, 64 sequences of up to 8192 (378 MB)    74.0 us  5.1 TB/s
 //   32 heads, one sequence of 131072 (151 MB)        36.7 us  4.1 TB/s
-//   128 heads, 32 sequences of 8192 (73 GFLOP)      105   us  0.69 PFLOP/s
-//   20 heads, 8 x 8 tokens, up to 4099 rows          24.9 us
-//   32 heads, one sequence of 1000                   11.6 us
+//   128 heads, 32 sequences of 8192 (73 GFLOP)      106   us  0.69 PFLOP/s
+//   20 heads, 8 x 8 tokens, up to 4099 rows          24.7 us
+//   32 heads, one sequence of 1000                   10.8 us
 // A tile more a CTA costs 1.76 us with 32 heads, 0.94 of the measured copy rate
 // for all SMs; with 128 heads 1.59 us (1.55 from the L2 cache), of which the
 // MMAs are 1.0: there the ring's turn (copy, S^T, softmax, O^T, with two tiles in
@@ -83,7 +84,7 @@ __host__ __device__ constexpr int soft_parts(int nt) { return nt == 64 ? 2 : 1; 
 // and what it frees holds a second slot of rotated elements beside two whole tiles of latent ones.
 __host__ __device__ constexpr int weight_buffers(int nt) { return nt == 64 ? 1 : 2; }
 __host__ __device__ constexpr int threads_of(int nt) { return 128 + 128 * soft_parts(nt); }
-constexpr int kPieceCost = 1;            // see tiles_of (1: verification of 8 sequences 32.3 us; 0: 33.9)
+constexpr int kPieceCost = 1;            // see tiles_of (1: verification of 8 sequences 25.0 us; 0: 26.6; 2: 25.2)
 constexpr float kLazy = 8.0f;            // log2 of the largest weight before a maximum moves
 constexpr float kNoMax = -3.4028234e38f;  // no score is smaller: the maximum of none
 constexpr int kMaxCopies = 8;            // copies of a chunk of a tile: pages of at least 8 rows
@@ -122,6 +123,7 @@ struct LatentParams {
     int pages, page_size, width;
     int B, H, R, E, max_q;
     int nt, rt, groups;     // rows a CTA, CTAs a group, groups
+    int cost;               // kPieceCost, or 0 for a short line
     int slots;    // of latent elements in the ring
     Divisor heads, ctas, shares;  // by H, by rt, by groups
     Divisor page_tiles;     // by the tiles of a page (pages of whole tiles)
@@ -167,8 +169,8 @@ __device__ __forceinline__ Seq seq_of(const LatentParams &p, int b) {
 // Length of a sequence on the line: its tiles, and before them what turning to it costs a CTA
 // (its queries, the last piece's result), in tiles.  At least one where it has tokens (their
 // results are written though they see nothing).
-__device__ __forceinline__ int tiles_of(const Seq &s) {
-    return s.n > 0 ? max(1, (s.len + kTile - 1) / kTile + kPieceCost) : 0;
+__device__ __forceinline__ int tiles_of(const LatentParams &p, const Seq &s) {
+    return s.n > 0 ? max(1, (s.len + kTile - 1) / kTile + p.cost) : 0;
 }
 
 // Where the g-th of `groups` equal shares of a line of `units` tiles begins: floor(units g / groups).
@@ -203,7 +205,7 @@ __device__ __forceinline__ Share share_of(const LatentParams &p, int g, bool rep
         } else {
             mine.n = 0;
         }
-        s.units += static_cast<int>(__reduce_add_sync(0xffffffffu, static_cast<unsigned>(tiles_of(mine))));
+        s.units += static_cast<int>(__reduce_add_sync(0xffffffffu, static_cast<unsigned>(tiles_of(p, mine))));
         if (c + 32 >= p.B) break;
         c += 32;
     }
@@ -214,7 +216,7 @@ __device__ __forceinline__ Share share_of(const LatentParams &p, int g, bool rep
     s.u1 = share_begin(p, s.units, g + 1, s.groups);
     if (c > 0) mine = seq_of(p, lane);
     for (int at = 0, b0 = 0;;) {
-        const int t = b0 + lane < p.B ? tiles_of(mine) : 0;
+        const int t = b0 + lane < p.B ? tiles_of(p, mine) : 0;
         int x = t;
 #pragma unroll
         for (int off = 1; off < 32; off <<= 1) {
@@ -264,12 +266,12 @@ struct Walk {
             o.s = s;
             if (!known) o.s = seq_of(p, b);
             known = false;
-            const int kt = tiles_of(o.s);
+            const int kt = tiles_of(p, o.s);
             const int take = min(kt - k, left);
             o.b = b;
             o.left = left;
-            o.k0 = max(0, k - kPieceCost);
-            const int end = max(0, k + take - kPieceCost);
+            o.k0 = max(0, k - p.cost);
+            const int end = max(0, k + take - p.cost);
             o.first = k == 0;
             o.last = k + take == kt;
             o.row0 = r * p.nt;
@@ -817,7 +819,7 @@ __global__ void __launch_bounds__(threads_of(NT), 1) latent_attention_kernel(con
         if (tell && !p.by_seq) desc[g] = make_int4(0, 0, 0, -1);
         while (walk.next(p, r, o)) {
             if (tell && o.first) {
-                const int u_last = sh.u0 + (sh.u1 - sh.u0 - o.left) + tiles_of(o.s) - 1;
+                const int u_last = sh.u0 + (sh.u1 - sh.u0 - o.left) + tiles_of(p, o.s) - 1;
                 // the last share that begins at or before u_last: ceil((u_last + 1) groups / units) - 1
                 const int g1 = static_cast<int>((static_cast<long long>(u_last + 1) * sh.groups - 1) / sh.units);
                 if (p.by_seq || !o.last) desc[p.by_seq ? o.b : g] = make_int4(o.s.q0, o.s.n, g, o.last ? -1 : g1);
@@ -1260,9 +1262,9 @@ const void *kernel_of(int nt) {
                       : reinterpret_cast<const void *>(&latent_attention_kernel<16>);
 }
 
-// The sizes of a call: rows a CTA, CTAs a group, groups.
+// The sizes of a call: rows a CTA, CTAs a group, groups, a sequence's cost in tiles.
 struct Split {
-    int nt, rt, groups;
+    int nt, rt, groups, cost;
     long long ws_bytes;
 };
 
@@ -1275,6 +1277,10 @@ Split split_of(const sgemm_latent_attention_t &a, int sms) {
     s.nt = rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
     s.rt = static_cast<int>((rows + s.nt - 1) / s.nt);
     const long long tiles = std::max(1LL, (static_cast<long long>(a.table_width) * a.page_size + kTile - 1) / kTile);
+    // A line that is short whatever the lengths has a share for each tile.  Nothing else is counted
+    // then: with a sequence's cost some share has two tiles (one sequence of 1000 rows: 11.9 us,
+    // without it 10.8), or, with a share more for it, one has none (11.0).
+    s.cost = tiles * a.B <= sms / s.rt ? 0 : kPieceCost;
     s.groups = static_cast<int>(std::max(1LL, std::min<long long>(sms / s.rt, tiles * a.B)));
     s.ws_bytes = s.groups > 1 ? (s.groups + 3) / 4 * 64 + static_cast<long long>(s.groups) * s.rt * 2 * s.nt * (a.R + 2) * 4 : 0;
     return s;
@@ -1431,6 +1437,7 @@ extern "C" sgemm_status_t sgemm_bf16_latent_attention(const sgemm_latent_attenti
     p.max_q = a->max_q;
     p.rt = sp.rt;
     p.groups = sp.groups;
+    p.cost = sp.cost;
     p.scale_log2 = static_cast<float>(static_cast<double>(a->scale) * 1.4426950408889634);
     p.flags = static_cast<int>(a->flags);
 
