@@ -49,7 +49,7 @@
 // Measured on one GB300, calls one after the other, 512 + 64 elements:
 //   32 heads, 64 sequences of up to 8192 (378 MB)    74.0 us  5.1 TB/s
 //   32 heads, one sequence of 131072 (151 MB)        36.7 us  4.1 TB/s
-//   128 heads, 32 sequences of 8192 (73 GFLOP)      106   us  0.69 PFLOP/s
+//   128 heads, 32 sequences of 8192 (73 GFLOP)      105.6 us  0.69 PFLOP/s
 //   20 heads, 8 x 8 tokens, up to 4099 rows          24.7 us
 //   32 heads, one sequence of 1000                   10.8 us
 // A tile more a CTA costs 1.76 us with 32 heads, 0.94 of the measured copy rate
@@ -602,21 +602,21 @@ __global__ void __launch_bounds__(threads_of(NT), 1) latent_attention_kernel(con
     if (warp == 0) {
         // the producer goes on: it needs the mbarriers only, which are its own work
         asm volatile("bar.arrive 2, %0;" ::"n"(threads_of(NT)) : "memory");
-    } else {
+    } else if (warp == 1) {
         // Tensor memory is taken after the wait: a CTA of the previous kernel may still want its
         // own, and this one holds its columns until that kernel is done.
-        if (warp == 1) {
-            asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(saddr(tmem_slot)),
-                         "r"(kTmem)
-                         : "memory");
-            asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
-        }
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(saddr(tmem_slot)),
+                     "r"(kTmem)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    const Share sh = share_of(p, g, blockIdx.x == 0 && warp == 2);  // while the tensor memory is taken
+    if (warp != 0) {
         tc_fence_before();
         asm volatile("bar.sync 2, %0;" ::"n"(threads_of(NT)) : "memory");
         tc_fence_after();
         tmem = *tmem_slot;
     }
-    const Share sh = share_of(p, g, blockIdx.x == 0 && warp == 2);
     const uint32_t t_o = tmem + 2 * kSCols;
     Walk walk(sh);
     const bool stall = (p.flags & kFlagTestStall) != 0;
