@@ -163,6 +163,27 @@ def _stream(stream) -> ctypes.c_void_p:
     return ctypes.c_void_p(int(stream))
 
 
+def _empty(shape, dtype, device, stream=None, returned: bool = True) -> torch.Tensor:
+    """A buffer that a call on ``stream`` makes for itself.
+
+    It comes from the allocator's blocks of that stream: one of the current stream's is handed out
+    as soon as it is free for work behind it there, while kernels still to come on that stream may
+    read or write what it was before.  One that is ``returned`` goes back no earlier than what the
+    current stream has been given by then: that is where the caller uses it."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(stream), device=device)
+    here = torch.cuda.current_stream(device)
+    if here.cuda_stream == stream.cuda_stream:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    if returned and t.numel():
+        t.record_stream(here)
+    return t
+
+
 def _check(status: int, what: str):
     if status != SGEMM_OK:
         raise SgemmError(status, what)
@@ -177,7 +198,7 @@ def _bf16_2d(t: torch.Tensor, name: str):
         raise ValueError(f"{name} must have unit stride along its last dimension")
 
 
-def _problem(x, W, y):
+def _problem(x, W, y, stream=None):
     _bf16_2d(x, "x")
     _bf16_2d(W, "W")
     M, K = x.shape
@@ -185,7 +206,7 @@ def _problem(x, W, y):
     if W.shape[1] != K or (W.stride(0) != K and N > 1):
         raise ValueError(f"W must be a contiguous [N, {K}] tensor, got {tuple(W.shape)}")
     if y is None:
-        y = torch.empty((M, N), dtype=torch.bfloat16, device=x.device)
+        y = _empty((M, N), torch.bfloat16, x.device, stream)
     _bf16_2d(y, "y")
     if tuple(y.shape) != (M, N):
         raise ValueError(f"y must be [{M}, {N}], got {tuple(y.shape)}")
@@ -195,7 +216,7 @@ def _problem(x, W, y):
 def sgemm_bf16_skinny(x: torch.Tensor, W: torch.Tensor, y: torch.Tensor | None = None,
                       stream=None) -> torch.Tensor:
     """``y = x @ W.T`` for contiguous x [M,K], W [N,K]; returns y [M,N]."""
-    M, N, K, y = _problem(x, W, y)
+    M, N, K, y = _problem(x, W, y, stream)
     if x.stride(0) != K and M > 1 or y.stride(0) != N and M > 1:
         raise ValueError("sgemm_bf16_skinny wants contiguous x and y; use sgemm_bf16_skinny_ex")
     _check(load().sgemm_bf16_skinny(x.data_ptr(), W.data_ptr(), y.data_ptr(), M, N, K,
@@ -207,7 +228,7 @@ def sgemm_bf16_skinny_ex(x: torch.Tensor, W: torch.Tensor, y: torch.Tensor | Non
                          plan: Plan | None = None, flags: int = 0, stream=None) -> torch.Tensor:
     """Like :func:`sgemm_bf16_skinny` with strided x / y rows, an optional plan
     and launch flags (``SGEMM_FLAG_*``)."""
-    M, N, K, y = _problem(x, W, y)
+    M, N, K, y = _problem(x, W, y, stream)
     ldx = x.stride(0) if M > 1 else K
     ldy = y.stride(0) if M > 1 else N
     _check(load().sgemm_bf16_skinny_ex(x.data_ptr(), ldx, W.data_ptr(), y.data_ptr(), ldy,
@@ -222,7 +243,7 @@ def sgemm_bf16_skinny_rescale_ex(x: torch.Tensor, W: torch.Tensor, y: torch.Tens
     """One decode-chain GEMM with the elementwise step fused into its epilogue:
     ``y = x @ W.T`` and ``x_next[m, k] = bf16(float(y[m, k % N]) * scale)`` for every
     column k of x_next ([M, n_next] BF16, its own buffer).  Returns y."""
-    M, N, K, y = _problem(x, W, y)
+    M, N, K, y = _problem(x, W, y, stream)
     _bf16_2d(x_next, "x_next")
     if x_next.shape[0] != M:
         raise ValueError(f"x_next must have {M} rows, got {x_next.shape[0]}")
@@ -248,7 +269,7 @@ def sgemm_bf16_skinny_f32out_ex(x: torch.Tensor, W: torch.Tensor, y: torch.Tenso
     if W.shape[1] != K or (W.stride(0) != K and N > 1):
         raise ValueError(f"W must be a contiguous [N, {K}] tensor, got {tuple(W.shape)}")
     if y is None:
-        y = torch.empty((M, N), dtype=torch.float32, device=x.device)
+        y = _empty((M, N), torch.float32, x.device, stream)
     if y.dtype != torch.float32 or y.dim() != 2 or tuple(y.shape) != (M, N) or y.stride(1) != 1:
         raise ValueError(f"y must be a float32 [{M}, {N}] tensor with unit column stride")
     ldx = x.stride(0) if M > 1 else K
@@ -260,7 +281,7 @@ def sgemm_bf16_skinny_f32out_ex(x: torch.Tensor, W: torch.Tensor, y: torch.Tenso
     return y
 
 
-def _pairs(items):
+def _pairs(items, stream=None):
     if not 1 <= len(items) <= MAX_BATCH:
         raise ValueError(f"batch must be 1..{MAX_BATCH}")
     arr = (Pair * len(items))()
@@ -269,7 +290,7 @@ def _pairs(items):
     for i, it in enumerate(items):
         x, W = it[0], it[1]
         y = it[2] if len(it) > 2 else None
-        M, N, K, y = _problem(x, W, y)
+        M, N, K, y = _problem(x, W, y, stream)
         if shape is None:
             shape = (M, N, K)
         elif shape != (M, N, K):
@@ -285,7 +306,7 @@ def _pairs(items):
 
 def sgemm_bf16_skinny_batched(items, stream=None) -> list:
     """One launch for ``[(x_i, W_i[, y_i]), ...]`` of one shape; returns the y_i."""
-    arr, (M, N, K), outs = _pairs(items)
+    arr, (M, N, K), outs = _pairs(items, stream)
     _check(load().sgemm_bf16_skinny_batched(arr, len(items), M, N, K, _stream(stream)),
            "sgemm_bf16_skinny_batched")
     return outs
@@ -294,7 +315,7 @@ def sgemm_bf16_skinny_batched(items, stream=None) -> list:
 def sgemm_bf16_skinny_batched_ex(items, plan: Plan | None = None, flags: int = 0,
                                  stream=None) -> list:
     """:func:`sgemm_bf16_skinny_batched` with an explicit plan and launch flags."""
-    arr, (M, N, K), outs = _pairs(items)
+    arr, (M, N, K), outs = _pairs(items, stream)
     _check(load().sgemm_bf16_skinny_batched_ex(arr, len(items), M, N, K,
                                                ctypes.byref(plan) if plan is not None else None,
                                                int(flags), _stream(stream)),
@@ -333,7 +354,7 @@ def sgemm_bf16_skinny_splitk_noalloc(x: torch.Tensor, W: torch.Tensor,
     wrapper creates it with torch).  Results equal ``sgemm_bf16_skinny_ex`` with
     the plan :func:`sgemm_splitk_noalloc_plan` returns.
     """
-    M, N, K, y = _problem(x, W, y)
+    M, N, K, y = _problem(x, W, y, stream)
     need = int(split_k) * M * N * 4
     if need > NOALLOC_SCRATCH_BYTES:
         raise SgemmError(SGEMM_ERR_UNSUPPORTED_SHAPE,

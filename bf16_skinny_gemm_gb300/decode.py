@@ -18,7 +18,7 @@ import struct
 
 import torch
 
-from . import SgemmError, load
+from . import SgemmError, _empty, load
 from .build import MARSHAL_PATH
 
 __all__ = [
@@ -148,17 +148,17 @@ def _norm(x, weight, residual, eps, form, y, y_dtype, scales, residual_out, flag
         ldr = _strides(residual, "residual", _BF16, shape)[0]
         pr = residual.data_ptr()
         if residual_out is None:
-            residual_out = torch.empty(shape, dtype=_BF16, device=x.device)
+            residual_out = _empty(shape, _BF16, x.device, stream)
     if residual_out is not None:
         ldro = _strides(residual_out, "residual_out", _BF16, shape)[0]
         pro = residual_out.data_ptr()
     if y is None:
-        y = torch.empty(shape, dtype=y_dtype, device=x.device)
+        y = _empty(shape, y_dtype, x.device, stream)
     ldy = _strides(y, "y" if form == SGEMM_NORM_BF16 else "q", y_dtype, shape)[0]
     if form != SGEMM_NORM_BF16:
         groups = -(-D // 128) if form == SGEMM_NORM_E4M3_GROUP128 else 1
         if scales is None:
-            scales = torch.empty((T, groups), dtype=torch.float32, device=x.device)
+            scales = _empty((T, groups), torch.float32, x.device, stream)
         lds = _strides(scales, "scales", torch.float32, (T, groups))[0]
         ps = scales.data_ptr()
     if T <= 1:
@@ -249,7 +249,7 @@ def sgemm_bf16_latent_append(kv: torch.Tensor, cache: torch.Tensor, slots: torch
         H = _shape(q, "q", _BF16, 3)[1]
         q_token, q_head, _ = _strides(q, "q", _BF16, (T, H, E))
         if q_out is None:
-            q_out = torch.empty((T, H, E), dtype=_BF16, device=kv.device)
+            q_out = _empty((T, H, E), _BF16, kv.device, stream)
         qo_token, qo_head, _ = _strides(q_out, "q_out", _BF16, (T, H, E))
         if H:
             pq, pqo = q.data_ptr(), q_out.data_ptr()
@@ -325,7 +325,7 @@ def sgemm_bf16_latent_attention(q: torch.Tensor, cache: torch.Tensor, block_tabl
     elif total != B * max_q:
         raise ValueError(f"q must hold {B} x {max_q} tokens without cu_q, got {total}")
     if out is None:
-        out = torch.empty((total, H, rank), dtype=_BF16, device=q.device)
+        out = _empty((total, H, rank), _BF16, q.device, stream)
     out_token, out_head, _ = _strides(out, "out", _BF16, (total, H, rank))
     if lse is not None:
         lse_token = _strides(lse, "lse", torch.float32, (total, H))[0]
@@ -334,10 +334,7 @@ def sgemm_bf16_latent_attention(q: torch.Tensor, cache: torch.Tensor, block_tabl
         return out, lse
     if workspace is None:
         need = sgemm_latent_attention_workspace(B, H, rank, W - rank, page_size, table_width, max_q)
-        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
-        if stream is not None and need:
-            workspace.record_stream(stream if isinstance(stream, torch.cuda.Stream)
-                                    else torch.cuda.ExternalStream(int(stream)))
+        workspace = _empty((need,), torch.uint8, q.device, stream, returned=False)
     elif not workspace.is_cuda or not workspace.is_contiguous():
         raise TypeError("workspace must be a contiguous CUDA tensor")
     # strides along dimensions of one element are of no account
