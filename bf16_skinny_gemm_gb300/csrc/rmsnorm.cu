@@ -40,6 +40,7 @@ struct NormParams {
 
 constexpr float kE4m3Max = 448.0f;
 constexpr int kGroup = 128;
+constexpr long long kMaxD = 1LL << 30;  // columns are counted in 32 bits, in steps of up to 4096
 // y / s is worked out as y (1 / s): a rounding of 2^-24 beside e4m3's of 2^-4, for a tenth of the
 // instructions; below this scale by division
 constexpr float kTinyScale = 1e-30f;
@@ -356,6 +357,7 @@ extern "C" sgemm_status_t sgemm_bf16_add_rmsnorm(const sgemm_add_rmsnorm_t *a, s
     const bool bf16 = a->form == SGEMM_NORM_BF16;
     const long long T = a->T, D = a->D;
     if (T < 0 || T > 0x7fffffffLL || D < 1 || !(a->eps >= 0.0f) || std::isinf(a->eps)) return SGEMM_ERR_INVALID_ARG;
+    if (D > norm::kMaxD) return SGEMM_ERR_UNSUPPORTED_SHAPE;
     if (T == 0) return SGEMM_OK;
     if (!a->x || !a->weight || !a->y || (!bf16 && !a->scales)) return SGEMM_ERR_INVALID_ARG;
     const long long groups = a->form == SGEMM_NORM_E4M3_GROUP128 ? (D + norm::kGroup - 1) / norm::kGroup : 1;

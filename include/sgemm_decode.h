@@ -51,7 +51,7 @@ enum {
  *   aligned, groups = 1 or ceil(D / 128).
  * - residual_out may be x or residual itself (same pointer and stride), and so
  *   may a BF16 y; otherwise outputs overlap no input and not each other.
- * - T >= 0 (0 rows enqueue nothing), 1 <= D, eps >= 0 and finite. */
+ * - T >= 0 (0 rows enqueue nothing), 1 <= D <= 2^30, eps >= 0 and finite. */
 typedef struct {
     const sgemm_bf16_t *x;
     const sgemm_bf16_t *residual;
