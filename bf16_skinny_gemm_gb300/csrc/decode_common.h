@@ -39,6 +39,39 @@ inline bool rows_overlap(const void *a, long long wa, long long sa, const void *
     return d < static_cast<uintptr_t>(wb) || d + static_cast<uintptr_t>(wa) > s;
 }
 
+// Whether a block of `n` bytes touches one of `rows` rows of `w` bytes, `s` bytes apart.
+inline bool block_touches(const void *b, long long n, const void *a, long long w, long long s, long long rows) {
+    if (!a || !b || n < 1 || w < 1 || rows < 1) return false;
+    const uintptr_t pa = reinterpret_cast<uintptr_t>(a), pb = reinterpret_cast<uintptr_t>(b);
+    if (pb + static_cast<uintptr_t>(n) <= pa || pa + static_cast<uintptr_t>((rows - 1) * s + w) <= pb) return false;
+    if (pb <= pa || s < w) return true;
+    const uintptr_t d = (pb - pa) % static_cast<uintptr_t>(s);
+    return d < static_cast<uintptr_t>(w) || d + static_cast<uintptr_t>(n) > static_cast<uintptr_t>(s);
+}
+
+// An array of T x H rows of `w` bytes, `tok` and `head` bytes apart.
+struct Heads {
+    const void *p;
+    long long w, tok, head;
+    long long extent(long long T, long long H) const { return (T - 1) * tok + (H - 1) * head + w; }
+};
+
+// Whether two such arrays (of the same T and H) share a byte: they are apart where their extents
+// are, or, with one stride of both, where the ranges that a token, a head or a row takes of that
+// stride are.
+inline bool heads_overlap(const Heads &a, const Heads &b, long long T, long long H) {
+    if (!rows_overlap(a.p, a.extent(T, H), 0, b.p, b.extent(T, H), 0, 1)) return false;
+    if (T > 1 && !rows_overlap(a.p, a.extent(1, H), a.tok, b.p, b.extent(1, H), b.tok, T)) return false;
+    if (H > 1 && !rows_overlap(a.p, a.extent(T, 1), a.head, b.p, b.extent(T, 1), b.head, H)) return false;
+    if (T > 1 && H > 1 && a.tok == b.tok && a.head == b.head && a.tok > 0 && a.head > 0) {
+        const bool inner = a.head <= a.tok;  // heads inside a token
+        const long long step = inner ? a.head : a.tok, far = inner ? a.tok : a.head;
+        if (far % step == 0)
+            return rows_overlap(a.p, a.w, step, b.p, b.w, step, ((inner ? T : H) - 1) * (far / step) + (inner ? H : T));
+    }
+    return true;
+}
+
 inline bool valid_flags(unsigned flags) { return (flags & ~kDecodeFlags) == 0; }
 
 // Launch `fn` with one parameter structure, as a programmatic dependent of the

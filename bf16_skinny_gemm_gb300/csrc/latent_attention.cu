@@ -1355,6 +1355,19 @@ bool encode_maps(LatentParams &p, const sgemm_latent_attention_t &a) {
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// Whether `n` bytes at `b` (the scratch) or the array `h` (an output of T x H rows) lie in what the
+// call reads beside the queries.
+bool in_inputs(const sgemm_latent_attention_t &a, const Heads *h, const void *b, long long n) {
+    if (h) {
+        b = h->p;
+        n = h->extent(a.total_q, a.H);
+    }
+    const long long page = 2 * ((a.page_size - 1) * a.row_stride + a.R + a.E);
+    return block_touches(b, n, a.cache, page, 2 * a.page_stride, a.pages) ||
+           block_touches(b, n, a.block_table, 4LL * a.table_width, 4 * a.ldt, a.B) ||
+           block_touches(b, n, a.seq_lens, 4LL * a.B, 0, 1) || block_touches(b, n, a.cu_q, 4LL * a.B + 4, 0, 1);
+}
+
 }  // namespace latent
 }  // namespace sk
 
@@ -1397,6 +1410,13 @@ extern "C" sgemm_status_t sgemm_bf16_latent_attention(const sgemm_latent_attenti
         a->page_stride % 8 || !aligned(a->out, 4) || a->out_token % 2 || a->out_head % 2 || !aligned(a->lse, 4) ||
         !aligned(a->block_table, 4) || !aligned(a->seq_lens, 4) || !aligned(a->cu_q, 4) || !aligned(a->workspace, 16))
         return SGEMM_ERR_MISALIGNED;
+    // out and lse lie apart from what is read and from each other
+    const Heads q{a->q, 2 * W, 2 * a->q_token, 2 * a->q_head}, out{a->out, 2LL * a->R, 2 * a->out_token, 2 * a->out_head};
+    const Heads lse{a->lse, 4, 4 * a->lse_token, 4};
+    if (heads_overlap(out, q, a->total_q, a->H) || heads_overlap(lse, q, a->total_q, a->H) ||
+        heads_overlap(out, lse, a->total_q, a->H) || in_inputs(*a, &out, nullptr, 0) ||
+        (a->lse && in_inputs(*a, &lse, nullptr, 0)))
+        return SGEMM_ERR_INVALID_ARG;
     // strides that a tensor map can hold
     if (a->row_stride >= (1LL << 38) || a->page_stride >= (1LL << 38)) return SGEMM_ERR_UNSUPPORTED_SHAPE;
 
@@ -1407,6 +1427,12 @@ extern "C" sgemm_status_t sgemm_bf16_latent_attention(const sgemm_latent_attenti
     if (st != SGEMM_OK) return st;
     const Split sp = split_of(*a, sms);
     if (sp.ws_bytes > 0 && (!a->workspace || a->workspace_bytes < sp.ws_bytes)) return SGEMM_ERR_NO_WORKSPACE;
+    // and so does the scratch that the call uses
+    auto in_scratch = [&](const Heads &h) {
+        return rows_overlap(a->workspace, sp.ws_bytes, 0, h.p, h.extent(a->total_q, a->H), 0, 1);
+    };
+    if (sp.ws_bytes > 0 && (in_scratch(q) || in_scratch(out) || in_scratch(lse) || in_inputs(*a, nullptr, a->workspace, sp.ws_bytes)))
+        return SGEMM_ERR_INVALID_ARG;
     p.nt = sp.nt;
     // one stride from each (token, head) row to the next, wide enough that rows are apart (a
     // tensor map's strides are)

@@ -139,6 +139,8 @@ sgemm_status_t sgemm_bf16_latent_append(const sgemm_latent_append_t *args, sgemm
  *   set bit 1 of the device error word.
  * - q and cache are 16-byte aligned and all their strides multiples of 8; out
  *   is 4-byte aligned with even strides (else SGEMM_ERR_MISALIGNED).
+ * - out, lse and the scratch overlap no input and not each other.  (Column
+ *   ranges of one buffer, with its strides, are apart.)
  * - workspace: device scratch of at least sgemm_latent_attention_workspace
  *   bytes (16-byte aligned; may be NULL where that is 0).  Its contents need
  *   no preparation and do not survive the call.  Calls that may overlap on the
