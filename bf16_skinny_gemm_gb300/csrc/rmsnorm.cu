@@ -51,7 +51,13 @@ __device__ __forceinline__ float max_nan(float a, float b) {
     return r;
 }
 
-__device__ __forceinline__ float scale_of(float top) { return top == 0.0f ? 1.0f : top / kE4m3Max; }
+// A scale too small to be a normal number is rounded up: never to 0, where the largest y would
+// become infinite and a y of 0 NaN, nor so far down that the largest y / s passes e4m3's maximum.
+__device__ __forceinline__ float scale_of(float top) {
+    if (top == 0.0f) return 1.0f;
+    const float s = top / kE4m3Max;
+    return s < 1.17549435e-38f ? __fdiv_ru(top, kE4m3Max) : s;
+}
 
 __device__ __forceinline__ uint16_t pack_e4m3(float a, float b) {
     return __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);

@@ -44,7 +44,8 @@ enum {
  *     residual_out[t][c] = RNE_bf16(h[c])                   (where it is not NULL)
  * SGEMM_NORM_BF16 rounds y once to BF16.  The 8-bit forms write, for each row
  * or group of 128 columns (the last group of a row may be shorter), the scale
- *     s = max |y| / 448   (1 where that maximum is 0; NaN where a y is NaN)
+ *     s = max |y| / 448   (1 where that maximum is 0; rounded up where it is
+ *                          subnormal, so never 0; NaN where a y is NaN)
  * to scales[t][group], and e4m3(y / s), round-to-nearest-even, to y.
  * - x, residual, residual_out: [T, D] with their row strides >= D; weight [D];
  *   y: [T, D] BF16 (2-byte aligned) or bytes; scales: [T, groups], 4-byte
