@@ -41,8 +41,9 @@ struct NormParams {
 constexpr float kE4m3Max = 448.0f;
 constexpr int kGroup = 128;
 constexpr long long kMaxD = 1LL << 30;  // columns are counted in 32 bits, in steps of up to 4096
-// y / s is worked out as y (1 / s): a rounding of 2^-24 beside e4m3's of 2^-4, for a tenth of the
-// instructions; below this scale by division
+// y / s is worked out as y (1 / s), two roundings of 2^-24 beside e4m3's of 2^-4, which differ from
+// one only where y / s is within 2^-23 of a tie; dividing each element is most of the kernel's
+// arithmetic (16384 x 4096, a scale a row: 72.6 us, 90.9 by division).  Below this scale by division.
 constexpr float kTinyScale = 1e-30f;
 
 __device__ __forceinline__ float max_nan(float a, float b) {

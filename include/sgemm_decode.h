@@ -46,7 +46,9 @@ enum {
  * or group of 128 columns (the last group of a row may be shorter), the scale
  *     s = max |y| / 448   (1 where that maximum is 0; rounded up where it is
  *                          subnormal, so never 0; NaN where a y is NaN)
- * to scales[t][group], and e4m3(y / s), round-to-nearest-even, to y.
+ * to scales[t][group], and e4m3(y / s), round-to-nearest-even, to y.  The
+ * quotient may be off by about 2^-23 of itself (it is y times 1 / s, both FP32), so
+ * that one this near to the middle of two e4m3 values may round to either.
  * - x, residual, residual_out: [T, D] with their row strides >= D; weight [D];
  *   y: [T, D] BF16 (2-byte aligned) or bytes; scales: [T, groups], 4-byte
  *   aligned, groups = 1 or ceil(D / 128).

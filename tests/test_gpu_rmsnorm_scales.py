@@ -53,3 +53,23 @@ def test_rows_of_subnormal_values(width, shift, group):
     torch.cuda.synchronize()
     assert torch.all(scales.cpu().double() == UNIT)
     assert torch.equal(q.cpu().double(), 64 * x)
+
+
+@pytest.mark.parametrize("width,shift", [(512, 0), (512, 1), (4096, 0), (20480, 0)])
+@pytest.mark.parametrize("group", [0, 128])
+def test_each_quotient_is_rounded_to_the_nearest(width, shift, group):
+    """x is +-1 and eps 0, so that y is +-the weight.  A quotient within 2^-22 of the middle of two
+    values (two roundings of FP32 come within 2^-23) may round to either, every other one does not."""
+    g = torch.Generator().manual_seed(width + group)
+    w = torch.randn(width, generator=g).to(torch.bfloat16)
+    x = torch.where(torch.rand((40, width), generator=g) < 0.5, -1.0, 1.0)
+    q, scales, _ = sk.sgemm_bf16_add_rmsnorm_e4m3(view(x.to(torch.bfloat16), shift), w.to(DEV), eps=0.0, group=group)
+    torch.cuda.synchronize()
+    y = x * w.float()
+    top = torch.stack([p.abs().amax(1) for p in y.split(group or width, 1)], 1)
+    assert torch.equal(scales.cpu(), top / 448)  # FP32 division, as the kernel's
+    s = scales.cpu().double()
+    v = y.double() / (s.repeat_interleave(group, 1)[:, :width] if group else s)
+    low, high = [(v * (1 + d)).clamp(-448, 448).float().to(torch.float8_e4m3fn).float() for d in (-2.0 ** -22, 2.0 ** -22)]
+    got = q.cpu().float()
+    assert torch.all((got == low) | (got == high))
