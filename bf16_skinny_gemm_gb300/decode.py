@@ -98,6 +98,14 @@ def _call(name: str, args: bytes, t: torch.Tensor, stream) -> None:
         raise SgemmError(status, name)
 
 
+def _on_current_device(**tensors) -> None:
+    """The library launches on the current device, so that every tensor has to be there."""
+    here = torch.cuda.current_device()
+    for name, t in tensors.items():
+        if t is not None and t.get_device() != here:
+            raise ValueError(f"{name} is on cuda:{t.get_device()}, the current device is cuda:{here}")
+
+
 def _refuse(t, name: str, dtype, shape):
     """What is wrong with a tensor; its strides if nothing is (a last dimension of one element has
     a stride of no account)."""
@@ -154,13 +162,15 @@ def _norm(x, weight, residual, eps, form, y, y_dtype, scales, residual_out, flag
         pro = residual_out.data_ptr()
     if y is None:
         y = _empty(shape, y_dtype, x.device, stream)
-    ldy = _strides(y, "y" if form == SGEMM_NORM_BF16 else "q", y_dtype, shape)[0]
+    named = "y" if form == SGEMM_NORM_BF16 else "q"
+    ldy = _strides(y, named, y_dtype, shape)[0]
     if form != SGEMM_NORM_BF16:
         groups = -(-D // 128) if form == SGEMM_NORM_E4M3_GROUP128 else 1
         if scales is None:
             scales = _empty((T, groups), torch.float32, x.device, stream)
         lds = _strides(scales, "scales", torch.float32, (T, groups))[0]
         ps = scales.data_ptr()
+    _on_current_device(x=x, weight=weight, residual=residual, **{named: y}, scales=scales, residual_out=residual_out)
     if T <= 1:
         if T == 0:
             return y, scales, residual_out
@@ -255,6 +265,7 @@ def sgemm_bf16_latent_append(kv: torch.Tensor, cache: torch.Tensor, slots: torch
             pq, pqo = q.data_ptr(), q_out.data_ptr()
     elif q_out is not None:
         raise ValueError("q_out without q")
+    _on_current_device(kv=kv, cache=cache, slots=slots, positions=positions, cos_sin=cos_sin, weight=weight, q=q, q_out=q_out)
     if T == 0:
         return cache, q_out
     # strides along dimensions of one element are of no account
@@ -330,6 +341,7 @@ def sgemm_bf16_latent_attention(q: torch.Tensor, cache: torch.Tensor, block_tabl
     if lse is not None:
         lse_token = _strides(lse, "lse", torch.float32, (total, H))[0]
         plse = lse.data_ptr()
+    _on_current_device(q=q, cache=cache, block_table=block_table, seq_lens=seq_lens, cu_q=cu_q, out=out, lse=lse)
     if total == 0 or B == 0:
         return out, lse
     if workspace is None:
@@ -337,6 +349,8 @@ def sgemm_bf16_latent_attention(q: torch.Tensor, cache: torch.Tensor, block_tabl
         workspace = _empty((need,), torch.uint8, q.device, stream, returned=False)
     elif not workspace.is_cuda or not workspace.is_contiguous():
         raise TypeError("workspace must be a contiguous CUDA tensor")
+    else:
+        _on_current_device(workspace=workspace)
     # strides along dimensions of one element are of no account
     if page_size == 1:
         row_stride = W

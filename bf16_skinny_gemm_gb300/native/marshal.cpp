@@ -7,6 +7,7 @@
 // say what is wrong; nothing is computed here.
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
+#include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
 
@@ -22,15 +23,27 @@ sgemm_status_t (*g_norm)(const sgemm_add_rmsnorm_t *, sgemm_stream_t) = nullptr;
 sgemm_status_t (*g_append)(const sgemm_latent_append_t *, sgemm_stream_t) = nullptr;
 sgemm_status_t (*g_attention)(const sgemm_latent_attention_t *, sgemm_stream_t) = nullptr;
 
-// A dense CUDA tensor of this type and rank whose last dimension has unit stride.
+// The device that is current in this call, which all of its tensors have to be on: the library
+// launches there.
+struct Device {
+    int at = -1;
+    bool has(const at::Tensor &t) {
+        if (at < 0) at = c10::cuda::current_device();
+        return t.device().index() == at;
+    }
+};
+
+// A dense tensor on that device, of this type and rank, whose last dimension has unit stride.
 struct View {
+    Device &here;
     void *p = nullptr;
     const int64_t *n = nullptr, *s = nullptr;  // sizes, strides
 
+    explicit View(Device &d) : here(d) {}
     bool of(PyObject *o, at::ScalarType type, int rank) {
         if (!THPVariable_Check(o)) return false;
         const at::Tensor &t = THPVariable_Unpack(o);
-        if (t.layout() != at::kStrided || t.scalar_type() != type || !t.is_cuda() || t.dim() != rank) return false;
+        if (t.layout() != at::kStrided || t.scalar_type() != type || !t.is_cuda() || t.dim() != rank || !here.has(t)) return false;
         n = t.sizes().data();
         s = t.strides().data();
         p = t.data_ptr();
@@ -80,7 +93,8 @@ PyObject *add_rmsnorm(PyObject *, PyObject *const *a, Py_ssize_t n) {
     if (n != 10 || !g_norm) return left();
     sgemm_add_rmsnorm_t g;
     std::memset(&g, 0, sizeof(g));
-    View x, v;
+    Device here;
+    View x(here), v(here);
     long long form = 0, flags = 0;
     sgemm_stream_t stream;
     if (!x.of(a[0], kBf16, 2) || x.n[0] < 1 || x.n[1] > kMaxInt || !int_of(a[4], 0, 2, &form) ||
@@ -124,7 +138,8 @@ PyObject *latent_append(PyObject *, PyObject *const *a, Py_ssize_t n) {
     if (n != 12 || !g_append) return left();
     sgemm_latent_append_t g;
     std::memset(&g, 0, sizeof(g));
-    View kv, cache, cs, v;
+    Device here;
+    View kv(here), cache(here), cs(here), v(here);
     long long flags = 0;
     sgemm_stream_t stream;
     if (!kv.of(a[0], kBf16, 2) || !cache.of(a[1], kBf16, 3) || !cs.of(a[4], kF32, 2) || !float_of(a[6], &g.eps) ||
@@ -154,7 +169,7 @@ PyObject *latent_append(PyObject *, PyObject *const *a, Py_ssize_t n) {
         g.weight = v.as<sgemm_bf16_t>();
     }
     if (a[7] != Py_None) {
-        View o;
+        View o(here);
         if (!v.of(a[7], kBf16, 3) || v.n[0] != T || v.n[1] < 1 || v.n[1] > kMaxInt || v.n[2] != E ||
             !o.of(a[8], kBf16, T, v.n[1], E))
             return left();
@@ -179,7 +194,8 @@ PyObject *latent_attention(PyObject *, PyObject *const *a, Py_ssize_t n) {
     if (n != 13 || !g_attention) return left();
     sgemm_latent_attention_t g;
     std::memset(&g, 0, sizeof(g));
-    View q, cache, table, v;
+    Device here;
+    View q(here), cache(here), table(here), v(here);
     long long rank = 0, max_q = 0, flags = 0;
     sgemm_stream_t stream;
     if (!q.of(a[0], kBf16, 3) || !cache.of(a[1], kBf16, 3) || !table.of(a[2], kI32, 2) || !int_of(a[4], 1, kMaxInt, &rank) ||
@@ -226,7 +242,7 @@ PyObject *latent_attention(PyObject *, PyObject *const *a, Py_ssize_t n) {
     }
     if (!THPVariable_Check(a[10])) return left();
     const at::Tensor &w = THPVariable_Unpack(a[10]);
-    if (!w.is_cuda() || !w.is_contiguous()) return left();
+    if (!w.is_cuda() || !w.is_contiguous() || !here.has(w)) return left();
     g.workspace = w.data_ptr();
     g.workspace_bytes = static_cast<long long>(w.nbytes());
     g.flags = static_cast<unsigned>(flags);

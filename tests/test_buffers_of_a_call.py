@@ -80,6 +80,7 @@ def log(monkeypatch):
     monkeypatch.setattr(torch, "empty", empty)
     monkeypatch.setattr(torch.cuda, "stream", stream)
     monkeypatch.setattr(torch.cuda, "ExternalStream", Stream)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
     monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: Stream(now[-1]))
     monkeypatch.setattr(decode, "_call", call)
     monkeypatch.setattr(decode, "sgemm_latent_attention_workspace", lambda *a: 4096)
