@@ -83,6 +83,17 @@ bool float_of(PyObject *o, float *out) {
     return true;
 }
 
+// The call itself, without the interpreter's lock, as through ctypes: a launch waits where the
+// stream's queue is full, and what it waits for may need another thread of this program.
+template <class Args>
+PyObject *launched(sgemm_status_t (*call)(const Args *, sgemm_stream_t), const Args &args, sgemm_stream_t stream) {
+    sgemm_status_t status;
+    Py_BEGIN_ALLOW_THREADS;
+    status = call(&args, stream);
+    Py_END_ALLOW_THREADS;
+    return PyLong_FromLong(status);
+}
+
 PyObject *left() { return PyLong_FromLong(-1); }
 
 constexpr long long kMaxInt = 0x7fffffffLL;
@@ -130,7 +141,7 @@ PyObject *add_rmsnorm(PyObject *, PyObject *const *a, Py_ssize_t n) {
     g.D = static_cast<int>(D);
     g.form = static_cast<int>(form);
     g.flags = static_cast<unsigned>(flags);
-    return PyLong_FromLong(g_norm(&g, stream));
+    return launched(g_norm, g, stream);
 }
 
 // (kv, cache, slots, positions, cos_sin, weight, eps, q, q_out, interleaved, flags, stream)
@@ -186,7 +197,7 @@ PyObject *latent_append(PyObject *, PyObject *const *a, Py_ssize_t n) {
     g.interleaved = PyObject_IsTrue(a[9]);
     if (g.interleaved < 0) return nullptr;
     g.flags = static_cast<unsigned>(flags);
-    return PyLong_FromLong(g_append(&g, stream));
+    return launched(g_append, g, stream);
 }
 
 // (q, cache, block_table, seq_lens, rank, scale, cu_q, max_q, out, lse, workspace, flags, stream)
@@ -246,7 +257,7 @@ PyObject *latent_attention(PyObject *, PyObject *const *a, Py_ssize_t n) {
     g.workspace = w.data_ptr();
     g.workspace_bytes = static_cast<long long>(w.nbytes());
     g.flags = static_cast<unsigned>(flags);
-    return PyLong_FromLong(g_attention(&g, stream));
+    return launched(g_attention, g, stream);
 }
 
 // The addresses of the library's functions.
