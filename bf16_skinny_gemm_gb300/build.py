@@ -5,13 +5,14 @@ one shared library with the CUDA runtime linked statically, so the library
 needs nothing but the NVIDIA driver at run time.  Output goes to
 ``bf16_skinny_gemm_gb300/_build/``.
 
-Beside it, the host compiler builds ``_marshal.so`` (``native/marshal.cpp``), the short way from
-torch tensors to the decode operators' calls, against the installed torch.
+Beside it, the host compiler builds ``_marshal.*.so`` (``native/marshal.cpp``), the short way from
+torch tensors to the decode operators' calls, against the installed torch; its name says which.
 """
 from __future__ import annotations
 
 import concurrent.futures as cf
 import glob
+import hashlib
 import os
 import shutil
 import subprocess
@@ -25,7 +26,6 @@ BUILD_DIR = os.path.join(PKG, "_build")
 LIB_NAME = "libsgemm_skinny.so"
 LIB_PATH = os.path.join(BUILD_DIR, LIB_NAME)
 MARSHAL_SRC = os.path.join(PKG, "native", "marshal.cpp")
-MARSHAL_PATH = os.path.join(BUILD_DIR, "_marshal.so")
 
 ARCH_FLAGS = ["-gencode", "arch=compute_103a,code=sm_103a"]
 COMMON_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC,-O2",
@@ -59,11 +59,22 @@ def is_stale() -> bool:
     return _stale(LIB_PATH, _deps())
 
 
+def marshal_path() -> str:
+    """Where the module for this Python and torch is.  It reads tensors by torch's own layout of
+    them, so one built against another torch is another file."""
+    import torch
+
+    build = f"{torch.version.git_version} {torch._C._GLIBCXX_USE_CXX11_ABI}"
+    return os.path.join(BUILD_DIR, f"_marshal.{sysconfig.get_config_var('SOABI')}.torch-{torch.__version__}-"
+                                   f"{hashlib.sha1(build.encode()).hexdigest()[:8]}.so")
+
+
 def build_marshal(force: bool = False) -> str:
-    """Compile ``_marshal.so`` if its sources changed; returns its path."""
+    """Compile ``native/marshal.cpp`` if it, Python or torch changed; returns the module's path."""
+    path = marshal_path()
     deps = [MARSHAL_SRC, *glob.glob(os.path.join(INCLUDE, "*.h"))]
-    if not force and not _stale(MARSHAL_PATH, deps):
-        return MARSHAL_PATH
+    if not force and not _stale(path, deps):
+        return path
     import torch
 
     os.makedirs(BUILD_DIR, exist_ok=True)
@@ -71,14 +82,14 @@ def build_marshal(force: bool = False) -> str:
     cuda = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(nvcc()))), "include")
     inc = [INCLUDE, os.path.join(home, "include"), os.path.join(home, "include", "torch", "csrc", "api", "include"),
            sysconfig.get_paths()["include"], cuda]
-    tmp = MARSHAL_PATH + f".tmp{os.getpid()}"
+    tmp = path + f".tmp{os.getpid()}"
     cmd = ["g++", "-std=c++17", "-O2", "-fPIC", "-shared", *[f for d in inc for f in ("-isystem", d)], MARSHAL_SRC,
            "-o", tmp, "-L", os.path.join(home, "lib"), "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10_cuda", "-lc10"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"g++ failed for {MARSHAL_SRC}:\n{r.stdout}\n{r.stderr}")
-    os.replace(tmp, MARSHAL_PATH)
-    return MARSHAL_PATH
+    os.replace(tmp, path)
+    return path
 
 
 def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) -> str:

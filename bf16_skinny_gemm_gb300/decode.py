@@ -13,13 +13,13 @@ from __future__ import annotations
 import ctypes
 import importlib.machinery
 import importlib.util
-import os
 import struct
+import warnings
 
 import torch
 
 from . import SgemmError, _empty, load
-from .build import MARSHAL_PATH
+from .build import marshal_path
 
 __all__ = [
     "sgemm_bf16_add_rmsnorm", "sgemm_bf16_add_rmsnorm_e4m3", "sgemm_bf16_latent_append",
@@ -41,20 +41,32 @@ _BF16 = torch.bfloat16
 _fns: dict = {}
 
 
+class _None:
+    """In place of ``_marshal`` where there is none for this Python and torch: the checks below look
+    at every call, which takes longer and is the same call."""
+
+    def add_rmsnorm(self, *args):
+        return -1
+
+    latent_append = latent_attention = add_rmsnorm
+
+
 class _Unbound:
     """Stands in for ``_marshal`` until the first call has loaded the library."""
 
     def _first(self, name, args):
         global _short
-        path = MARSHAL_PATH
-        if not os.path.exists(path):
-            raise ImportError(f"{path} is missing: build it first (python -c 'import __graft_entry__ as g; g.build()')")
-        loader = importlib.machinery.ExtensionFileLoader("_marshal", path)
-        module = importlib.util.module_from_spec(importlib.util.spec_from_loader("_marshal", loader))
-        loader.exec_module(module)
         lib = load()
-        module.bind(*(ctypes.cast(getattr(lib, f), ctypes.c_void_p).value for f in (
-            "sgemm_bf16_add_rmsnorm", "sgemm_bf16_latent_append", "sgemm_bf16_latent_attention")))
+        try:
+            loader = importlib.machinery.ExtensionFileLoader("_marshal", marshal_path())
+            module = importlib.util.module_from_spec(importlib.util.spec_from_loader("_marshal", loader))
+            loader.exec_module(module)
+            module.bind(*(ctypes.cast(getattr(lib, f), ctypes.c_void_p).value for f in (
+                "sgemm_bf16_add_rmsnorm", "sgemm_bf16_latent_append", "sgemm_bf16_latent_attention")))
+        except ImportError as e:
+            warnings.warn(f"calls take longer than they need: {e}; build the module for this torch with "
+                          "python -c 'import __graft_entry__ as g; g.build()'", RuntimeWarning, stacklevel=4)
+            module = _None()
         _short = module
         return getattr(module, name)(*args)
 
