@@ -303,7 +303,8 @@ def sgemm_latent_attention_workspace(batch: int, heads: int, rank: int, rope: in
     (at most ``LATENT_WORKSPACE_MAX``)."""
     n = ctypes.c_longlong(0)
     f = _fn("sgemm_latent_attention_workspace")
-    args = _ATTN.pack(*([0] * 16), 1, 0, batch * max_q, page_size, table_width, batch, heads, rank, rope, max_q,
+    # one token: how many there are does not matter, and sequences of max_q each may be too many
+    args = _ATTN.pack(*([0] * 16), 1, 0, min(batch * max_q, 1), page_size, table_width, batch, heads, rank, rope, max_q,
                       1.0, 0, 0)
     status = f(args, ctypes.addressof(n))
     if status:

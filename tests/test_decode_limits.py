@@ -32,3 +32,16 @@ def test_norm_refuses_rows_whose_columns_pass_its_counters(D, form):
     assert norm(D, 1, form) == sk.SGEMM_ERR_UNSUPPORTED_SHAPE
     assert norm(D, 0, form) == sk.SGEMM_ERR_UNSUPPORTED_SHAPE
     assert norm(1 << 30, 0, form) == sk.SGEMM_OK
+
+
+def test_workspace_of_a_batch_in_which_one_sequence_has_many_tokens():
+    """512 sequences of 128 heads, of up to 32768 tokens each: 2^31 rows if all had as many, which is
+    more than a call takes, but the call may have far fewer."""
+    try:
+        assert 0 <= sk.sgemm_latent_attention_workspace(512, 128, 512, 64, 64, 1000, 32768) <= sk.LATENT_WORKSPACE_MAX
+    except sk.SgemmError as e:
+        assert e.status in (sk.SGEMM_ERR_UNSUPPORTED_DEVICE, sk.SGEMM_ERR_CUDA)
+    for batch, max_q in ((-1, 4), (4, 0), (4, -1)):
+        with pytest.raises(sk.SgemmError) as e:
+            sk.sgemm_latent_attention_workspace(batch, 128, 512, 64, 64, 1000, max_q)
+        assert e.value.status == sk.SGEMM_ERR_INVALID_ARG
