@@ -13,3 +13,14 @@ if ROOT not in sys.path:
 
 def pytest_configure(config):
     config.addinivalue_line("markers", "gpu: needs a CUDA GPU (sm_103) and the built library")
+
+
+def pytest_runtest_setup(item):
+    """Tests for a CPU-only machine may end a call that passes every check at the missing device.
+    Where there is one, such a call would launch a kernel on pointers that are made up."""
+    import pytest
+    import torch
+
+    made_up = ("test_norm_accepts", "test_append_accepts", "test_attention_accepts")
+    if item.path.name == "test_decode_abi.py" and item.name in made_up and torch.cuda.is_available():
+        pytest.skip("for a machine without a GPU: the pointers are made up")
