@@ -10,7 +10,9 @@
 // Measured on one GB300, calls one after the other: 16384 tokens with 32 heads'
 // queries 33.1 us (176 MB, 5.3 TB/s, 0.78 of the measured copy rate: the queries'
 // parts are 128 bytes every 1152, and a warp waits for a position, then its
-// angles, then stores); 1 to 777 tokens 2.7 us, a launch and that chain.
+// angles, then stores), with half-split pairs 37.1 us (a thread holds twice the
+// elements and angles there, and an access covers 64 of a row's 128 bytes);
+// 1 to 777 tokens 2.8 to 3.0 us, a launch and that chain.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 

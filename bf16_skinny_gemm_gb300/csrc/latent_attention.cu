@@ -45,6 +45,11 @@
 // CTA finds its share itself.  A sequence that a share ends in leaves partial
 // results (FP32 O, m and l), which a second kernel joins in the order of the
 // shares: the result does not depend on timing.
+// The CTAs of a group are those of the sequence with the most new tokens, and the
+// groups what the SMs then hold: sequences with fewer tokens leave CTAs of their
+// groups idle, and where a group needs more than half of the SMs there is one, which
+// walks every sequence whole.  128 heads, 64 sequences of 8192: 194 us; with 8 new
+// tokens in one of them 1.4 ms, with 39 12.6 ms.
 //
 // Measured on one GB300, calls one after the other, 512 + 64 elements:
 //   32 heads, 64 sequences of up to 8192 (378 MB)    74.0 us  5.1 TB/s
@@ -954,7 +959,9 @@ __global__ void __launch_bounds__(threads_of(NT), 1) latent_attention_kernel(con
                             *at = v;
                         }
                 }
-                // the weights, BF16 (their sum keeps FP32), into the buffer that tile n - NP used
+                // The weights, into the buffer that tile n - NP used.  BF16, as the values are: both
+                // operands of an MMA have one type.  Their rounding adds up to 1.2e-3 of the result
+                // (root mean square) to the 1.7e-3 of the result's own; their sum keeps FP32.
                 if (n >= NP) ok = wait_or_stop(pvd + 8 * ((n - NP) & 1), ((n - NP) >> 1) & 1, &stop) && ok;
                 {
                     const int key_in = 16 * sw + (lane >> 2);

@@ -272,8 +272,10 @@ __global__ void __launch_bounds__(most_threads(NV)) add_rmsnorm_kernel(const __g
     }
 }
 
-// Rows too long for a block's registers: the row is read again for each pass
-// (sum, maximum, output) by one block, element by element.
+// Rows too long for a block's registers (more than 16384 columns): the row is read
+// again for each pass (sum, maximum, output) by one block, element by element, 2
+// bytes an access.  4000 rows of 16392 columns 228 us (16384, by the other kernel:
+// 94.7, 0.82 of the measured copy rate), one such row 8.3 us (3.3).
 template <int FORM>
 __global__ void __launch_bounds__(1024) add_rmsnorm_long_kernel(const __grid_constant__ NormParams p) {
     __shared__ float part[2][32];

@@ -26,10 +26,12 @@ sgemm_status_t (*g_attention)(const sgemm_latent_attention_t *, sgemm_stream_t) 
 // The device that is current in this call, which all of its tensors have to be on: the library
 // launches there.
 struct Device {
-    int at = -1;
+    c10::DeviceIndex at = -1;
     bool has(const at::Tensor &t) {
+        const c10::Device d = t.device();
+        if (!d.is_cuda()) return false;
         if (at < 0) at = c10::cuda::current_device();
-        return t.device().index() == at;
+        return d.index() == at;
     }
 };
 
@@ -43,7 +45,7 @@ struct View {
     bool of(PyObject *o, at::ScalarType type, int rank) {
         if (!THPVariable_Check(o)) return false;
         const at::Tensor &t = THPVariable_Unpack(o);
-        if (t.layout() != at::kStrided || t.scalar_type() != type || !t.is_cuda() || t.dim() != rank || !here.has(t)) return false;
+        if (t.layout() != at::kStrided || t.scalar_type() != type || t.dim() != rank || !here.has(t)) return false;
         n = t.sizes().data();
         s = t.strides().data();
         p = t.data_ptr();
@@ -60,9 +62,9 @@ struct View {
     }
 };
 
-bool stream_of(PyObject *o, sgemm_stream_t *out) {
+bool stream_of(PyObject *o, const Device &here, sgemm_stream_t *out) {
     if (o == Py_None) {
-        *out = c10::cuda::getCurrentCUDAStream().stream();
+        *out = c10::cuda::getCurrentCUDAStream(here.at).stream();
         return true;
     }
     if (!PyLong_Check(o)) return false;
@@ -109,7 +111,7 @@ PyObject *add_rmsnorm(PyObject *, PyObject *const *a, Py_ssize_t n) {
     long long form = 0, flags = 0;
     sgemm_stream_t stream;
     if (!x.of(a[0], kBf16, 2) || x.n[0] < 1 || x.n[1] > kMaxInt || !int_of(a[4], 0, 2, &form) ||
-        !int_of(a[8], 0, kMaxInt, &flags) || !float_of(a[3], &g.eps) || !stream_of(a[9], &stream))
+        !int_of(a[8], 0, kMaxInt, &flags) || !float_of(a[3], &g.eps) || !stream_of(a[9], here, &stream))
         return left();
     const int64_t T = x.n[0], D = x.n[1];
     auto ld = [&](const View &w, int64_t width) { return T > 1 ? w.s[0] : width; };
@@ -154,7 +156,7 @@ PyObject *latent_append(PyObject *, PyObject *const *a, Py_ssize_t n) {
     long long flags = 0;
     sgemm_stream_t stream;
     if (!kv.of(a[0], kBf16, 2) || !cache.of(a[1], kBf16, 3) || !cs.of(a[4], kF32, 2) || !float_of(a[6], &g.eps) ||
-        !int_of(a[10], 0, kMaxInt, &flags) || !stream_of(a[11], &stream))
+        !int_of(a[10], 0, kMaxInt, &flags) || !stream_of(a[11], here, &stream))
         return left();
     const int64_t T = kv.n[0], W = kv.n[1], E = cs.n[1], R = W - E;
     if (T < 1 || R < 1 || W > kMaxInt || cache.n[2] != W || cache.n[1] > kMaxInt) return left();
@@ -211,7 +213,7 @@ PyObject *latent_attention(PyObject *, PyObject *const *a, Py_ssize_t n) {
     sgemm_stream_t stream;
     if (!q.of(a[0], kBf16, 3) || !cache.of(a[1], kBf16, 3) || !table.of(a[2], kI32, 2) || !int_of(a[4], 1, kMaxInt, &rank) ||
         !float_of(a[5], &g.scale) || !int_of(a[7], 1, kMaxInt, &max_q) || !int_of(a[11], 0, kMaxInt, &flags) ||
-        !stream_of(a[12], &stream))
+        !stream_of(a[12], here, &stream))
         return left();
     const int64_t total = q.n[0], H = q.n[1], W = q.n[2], B = table.n[0];
     if (total < 1 || B < 1 || H > kMaxInt || B > kMaxInt || table.n[1] > kMaxInt || cache.n[1] > kMaxInt || cache.n[2] != W ||
@@ -253,7 +255,7 @@ PyObject *latent_attention(PyObject *, PyObject *const *a, Py_ssize_t n) {
     }
     if (!THPVariable_Check(a[10])) return left();
     const at::Tensor &w = THPVariable_Unpack(a[10]);
-    if (!w.is_cuda() || !w.is_contiguous() || !here.has(w)) return left();
+    if (!here.has(w) || !w.is_contiguous()) return left();
     g.workspace = w.data_ptr();
     g.workspace_bytes = static_cast<long long>(w.nbytes());
     g.flags = static_cast<unsigned>(flags);

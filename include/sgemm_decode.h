@@ -132,7 +132,15 @@ sgemm_status_t sgemm_bf16_latent_append(const sgemm_latent_append_t *args, sgemm
  * The products' weights exp(s_j - m) are rounded to BF16; sums are FP32.
  * - A token that sees no row (len = 0, or len < n) gets out = 0 and lse = -inf.
  *   What lies in rows past a sequence's end, or past what a token sees, never
- *   reaches its result, NaN and infinities included.
+ *   reaches its result, NaN and infinities included.  (A row that it sees with
+ *   an infinity and a score of -inf, so with weight 0, adds NaN where the
+ *   infinity is, or nothing where an earlier token of the call does not see
+ *   the row.)
+ * - The work is split over the SMs by the lengths, and by ceil(max_q * H / 64)
+ *   CTAs for the rows of the sequence with the most new tokens.  Sequences with
+ *   fewer leave some of those CTAs idle, and from 77 on (39 tokens of 128
+ *   heads) the sequences' contexts are not split at all.  Put sequences with
+ *   many new tokens and sequences with few into calls of their own.
  * - R: 128, 256, 384 or 512; E: a multiple of 8, 8 .. 64; 1 <= H <= 1024;
  *   1 <= max_q, the largest n of the call (a larger n in cu_q is computed up
  *   to max_q tokens only and sets bit 1 of the device error word).
