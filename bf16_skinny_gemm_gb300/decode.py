@@ -6,7 +6,10 @@
 
 As in the rest of the package, the functions check and marshal their arguments; every step of
 the computation runs in the library's CUDA kernels.  Each takes preallocated outputs (allocating
-nothing then), launch flags and a stream, and can be captured into a CUDA graph.
+nothing then), launch flags and a stream, and can be captured into a CUDA graph.  All tensors are on
+the current device.  Outputs and scratch that a call is not given come from the allocator's blocks
+of the stream it runs on; the caller orders what it does with the outputs behind that stream, as
+with any work there.
 """
 from __future__ import annotations
 
