@@ -172,11 +172,13 @@ def _empty(shape, dtype, device, stream=None, returned: bool = True) -> torch.Te
     current stream has been given by then: that is where the caller uses it."""
     if stream is None:
         return torch.empty(shape, dtype=dtype, device=device)
-    if not isinstance(stream, torch.cuda.Stream):
-        stream = torch.cuda.ExternalStream(int(stream), device=device)
     here = torch.cuda.current_stream(device)
-    if here.cuda_stream == stream.cuda_stream:
+    handle = stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
+    if handle == here.cuda_stream:
         return torch.empty(shape, dtype=dtype, device=device)
+    if not isinstance(stream, torch.cuda.Stream):
+        # (torch would make a stream of its own for handle 0)
+        stream = torch.cuda.ExternalStream(handle, device=device) if handle else torch.cuda.default_stream(device)
     with torch.cuda.stream(stream):
         t = torch.empty(shape, dtype=dtype, device=device)
     if returned and t.numel():

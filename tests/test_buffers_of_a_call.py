@@ -59,6 +59,11 @@ class Stream:
         self.cuda_stream = handle
 
 
+class External(Stream):
+    def __init__(self, handle, device=None):
+        super().__init__(handle or 0xB00)  # what torch does with 0: a stream from its pool
+
+
 @pytest.fixture
 def log(monkeypatch):
     """(shape, stream that it comes from) of each buffer made, and the streams recorded for it."""
@@ -79,7 +84,8 @@ def log(monkeypatch):
 
     monkeypatch.setattr(torch, "empty", empty)
     monkeypatch.setattr(torch.cuda, "stream", stream)
-    monkeypatch.setattr(torch.cuda, "ExternalStream", Stream)
+    monkeypatch.setattr(torch.cuda, "ExternalStream", External)
+    monkeypatch.setattr(torch.cuda, "default_stream", lambda device=None: Stream(0))
     monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
     monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: Stream(now[-1]))
     monkeypatch.setattr(decode, "_call", call)
@@ -110,10 +116,11 @@ def attention(stream):
 
 
 @pytest.mark.parametrize("operator", [norm, norm_e4m3, append, attention])
-def test_buffers_come_from_the_calls_stream(log, operator):
-    made = operator(THERE)
-    assert ("call", THERE) in log
-    assert {(shape, s) for shape, s, *_ in log if shape not in ("call", "used on")} == {(shape, THERE) for shape in made}
+@pytest.mark.parametrize("there", [THERE, 0])  # 0: the default stream
+def test_buffers_come_from_the_calls_stream(log, operator, there):
+    made = operator(there)
+    assert ("call", there) in log
+    assert {(shape, s) for shape, s, *_ in log if shape not in ("call", "used on")} == {(shape, there) for shape in made}
     # what is returned is used on the current stream, what is not returned is not
     assert {r[1:] for r in log if r[0] == "used on"} == {(shape, HERE) for shape in made if shape != (4096,)}
 
@@ -188,6 +195,21 @@ def test_a_block_the_current_stream_still_uses_is_left_alone():
     torch.cuda.synchronize()
     assert bool((kept == 2).all())
     D.check(y, want, D.norm_y_bound(want, 4096), "y")
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("handle", [True, False])
+def test_a_call_on_the_default_stream_while_another_is_current(handle):
+    """By its handle, which is 0, and by torch's object."""
+    x, w = torch.randn((64, 4096), device="cuda").to(BF16), torch.ones(4096, device="cuda").to(BF16)
+    want, _ = sk.sgemm_bf16_add_rmsnorm(x, w)
+    torch.cuda.synchronize()
+    default = torch.cuda.default_stream()
+    assert default.cuda_stream == 0
+    with torch.cuda.stream(torch.cuda.Stream()):
+        y, _ = sk.sgemm_bf16_add_rmsnorm(x, w, stream=0 if handle else default)
+    torch.cuda.synchronize()
+    assert torch.equal(y, want)
 
 
 @pytest.mark.gpu
