@@ -427,4 +427,7 @@ def sgemm_version() -> str:
 from . import decode as _decode  # noqa: E402  (it uses the names above)
 from .decode import *  # noqa: E402,F401,F403
 
-__all__ += _decode.__all__
+from . import layers as _layers  # noqa: E402
+from .layers import *  # noqa: E402,F401,F403
+
+__all__ += _decode.__all__ + _layers.__all__

@@ -80,18 +80,23 @@ inline bool valid_flags(unsigned flags) { return (flags & ~kDecodeFlags) == 0; }
 // what overlaps is the launch itself, which costs as much as a small call does
 // (norm of 1 x 4096: 2.5 us a call, 4.1 without; attention of one token over
 // 131072 rows: 36.7, 39.0; both as calls one after the other).
-inline cudaError_t launch(const void *fn, dim3 grid, dim3 block, size_t smem, cudaStream_t stream, void *params) {
+// `cluster`: CTAs of a thread-block cluster.
+inline cudaError_t launch(const void *fn, dim3 grid, dim3 block, size_t smem, cudaStream_t stream, void *params,
+                          int cluster = 1) {
     cudaLaunchConfig_t cfg;
     std::memset(&cfg, 0, sizeof(cfg));
     cfg.gridDim = grid;
     cfg.blockDim = block;
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = static_cast<unsigned>(cluster);
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
     void *args[] = {params};
     return cudaLaunchKernelExC(&cfg, fn, args);
 }

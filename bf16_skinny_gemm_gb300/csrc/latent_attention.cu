@@ -51,6 +51,10 @@
 // walks every sequence whole.  128 heads, 64 sequences of 8192: 194 us; with 8 new
 // tokens in one of them 1.4 ms, with 39 12.6 ms.
 //
+// Drafted tokens (sgemm_bf16_latent_tree_attention): the new tokens' rows are the last of a
+// sequence, so that only its last tiles hold rows that a mask decides on.  The same kernel, with
+// masks in place of the causal limit there (a template argument: the other's code stays as it is).
+//
 // Measured on one GB300, calls one after the other, 512 + 64 elements:
 //   32 heads, 64 sequences of up to 8192 (378 MB)    74.0 us  5.1 TB/s
 //   32 heads, one sequence of 131072 (151 MB)        36.7 us  4.1 TB/s
@@ -73,7 +77,8 @@
 #include <cstring>
 
 #include "decode_common.h"
-#include "skinny_tc05.cuh"
+#include "sgemm_layers.h"
+#include "tc05_roles.cuh"
 
 namespace sk {
 namespace latent {
@@ -138,6 +143,9 @@ struct LatentParams {
     int q_even;   // the queries' rows are evenly spaced: copied with TMA
     int out16;    // out's rows start on 16 bytes
     int by_seq;   // descriptors of split sequences: one a sequence, else one a group
+    int words;    // of a drafted token's mask
+    const unsigned long long *tree;  // the masks, or null
+    long long ld_tree;
     int pw;       // warps of the joining kernel that share a sequence's pieces
 };
 
@@ -266,6 +274,7 @@ struct Walk {
     bool known;
     __device__ __forceinline__ explicit Walk(const Share &sh)
         : b(sh.b), k(sh.k), left(sh.u1 - sh.u0), s(sh.s), known(true) {}
+    template <bool TREE>
     __device__ __forceinline__ bool next(const LatentParams &p, int r, Piece &o) {
         while (left > 0) {
             o.s = s;
@@ -286,8 +295,8 @@ struct Walk {
             left -= take;
             if (take == 0 || o.row0 >= rows) continue;
             o.nrows = min(p.nt, rows - o.row0);
-            // keys that the piece's last row sees
-            const int seen = o.s.len - o.s.n_all + p.heads.div(o.row0 + o.nrows - 1) + 1;
+            // keys that the piece's last row sees (any drafted token's row may be one of them)
+            const int seen = TREE ? o.s.len : o.s.len - o.s.n_all + p.heads.div(o.row0 + o.nrows - 1) + 1;
             o.k1 = max(o.k0, min(end, (max(seen, 0) + kTile - 1) / kTile));
             return true;
         }
@@ -351,38 +360,7 @@ struct Pages {
 };
 
 // ------------------------------------------------------------------------------- primitives
-using tc05::bar_arrive;
-using tc05::bar_try;
-using tc05::mma_commit;
-using tc05::prefetch_tmap;
-using tc05::tc_fence_after;
-using tc05::tc_fence_before;
-using tc05::tmem_ld16;
-
-// Wait for a phase, at most kWaitLimitNs, and not past another role's giving up.
-__device__ __forceinline__ bool wait_or_stop(uint32_t b, unsigned parity, int *stop) {
-    if (bar_try(b, parity)) return true;
-    const unsigned long long t0 = global_ns();
-    while (!bar_try(b, parity)) {
-        if (*reinterpret_cast<volatile int *>(stop)) return false;
-        if (static_cast<long long>(global_ns() - t0) > kWaitLimitNs) {
-            atomicExch(stop, 1);
-            return false;
-        }
-    }
-    return true;
-}
-
-// The same for a whole warp, which goes on together.
-__device__ __forceinline__ bool all_wait(uint32_t b, unsigned parity, int *stop) {
-    if (__all_sync(0xffffffffu, bar_try(b, parity))) return true;
-    return __all_sync(0xffffffffu, wait_or_stop(b, parity, stop));
-}
-
-// A value that all lanes of the warp have alike, by an instruction whose result the compiler
-// knows to be: the issuing warps' loops and descriptors then stay in uniform registers, where
-// tcgen05.mma and the copies want them.
-__device__ __forceinline__ int alike(int v) { return static_cast<int>(__reduce_or_sync(0xffffffffu, static_cast<unsigned>(v))); }
+using namespace roles;
 
 // Barrier of the N softmax threads, alone or with the OR of a predicate.
 template <int N>
@@ -403,82 +381,10 @@ __device__ __forceinline__ bool soft_any(bool v) {
     return r != 0;
 }
 
-// One lane of a converged warp, the same each time.
-__device__ __forceinline__ bool elect() {
-    uint32_t r;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "elect.sync _|p, 0xffffffff;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(r)::"memory");
-    return r != 0;
-}
-
-__device__ __forceinline__ float ex2(float x) {
-    float r;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-    return r;
-}
-
-__device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
-    uint32_t r;
-    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-    return r;
-}
-
-__device__ __forceinline__ void mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add) {
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-        "l"(a), "l"(b), "r"(idesc), "r"(add ? 1u : 0u)
-        : "memory");
-}
-
 // Descriptor of an MN-major operand in 128-byte swizzle atoms (64 elements x 8 k): atoms of
 // the next 64 elements 8 KiB on (leading byte offset), of the next 8 k 1 KiB on (stride).
 __device__ __forceinline__ uint64_t mn_desc(uint32_t addr) {
     return tc05::kDescHi | (static_cast<uint64_t>(kChunk >> 4) << 16) | static_cast<uint64_t>((addr & 0x3FFFFu) >> 4);
-}
-
-// 16 bytes global -> shared, asynchronously; zeros where `bytes` is 0.
-__device__ __forceinline__ void copy16(uint32_t dst, const void *src, int bytes) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
-}
-
-__device__ __forceinline__ void tma_3d(uint32_t dst, const CUtensorMap *map, int c0, int c1, int c2, uint32_t bar) {
-    asm volatile(
-        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
-        "[%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(bar)
-        : "memory");
-}
-__device__ __forceinline__ void tma_4d(uint32_t dst, const CUtensorMap *map, int c0, int c1, int c2, int c3,
-                                       uint32_t bar, uint64_t policy) {
-    asm volatile(
-        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint "
-        "[%0], [%1, {%2, %3, %4, %5}], [%6], %7;" ::"r"(dst),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(bar), "l"(policy)
-        : "memory");
-}
-
-// How the L2 cache keeps what is copied: evicted first where this CTA is its only reader (one
-// sequence of 131072: 36.7 us, 38.3 without; where two CTAs read a tile, 128 heads, 110 became 132).
-__device__ __forceinline__ uint64_t policy_of(bool once) {
-    uint64_t r;
-    if (once)
-        asm("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(r));
-    else
-        asm("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(r));
-    return r;
-}
-
-// Four 8 x 8 BF16 fragments, each stored turned: lane l gives the address of row l % 8 (its
-// column in the fragment) of fragment l / 8.
-__device__ __forceinline__ void stmatrix_turned(uint32_t addr, const uint32_t (&q)[4]) {
-    asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(q[0]),
-                 "r"(q[1]), "r"(q[2]), "r"(q[3])
-                 : "memory");
 }
 
 // S^T of 64 keys x NT rows: lane l of the warp gets keys l / 4 and l / 4 + 8 of the warp's 16,
@@ -509,44 +415,8 @@ __device__ __forceinline__ void tmem_ld_s(uint32_t addr, uint32_t (&r)[32]) {
         : "r"(addr));
 }
 
-__device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t (&r)[16]) {
-    asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
-        "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(addr),
-        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
-        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
-        : "memory");
-}
-
-// Wait (bounded) for a copy in flight.
-__device__ __forceinline__ void landed(uint32_t bar, unsigned parity) {
-    const unsigned long long t0 = global_ns();
-    while (!bar_try(bar, parity))
-        if (static_cast<long long>(global_ns() - t0) > kWaitLimitNs) break;
-}
-
-// Wait (bounded) until every product this warp issued is complete.
-__device__ __forceinline__ void finish(uint32_t bar, int *stop) {
-    if (elect()) mma_commit(bar);
-    __syncwarp();
-    const unsigned long long t0 = global_ns();
-    while (!bar_try(bar, 0))
-        if (static_cast<long long>(global_ns() - t0) > kWaitLimitNs) {
-            atomicExch(stop, 1);
-            break;
-        }
-    __syncwarp();
-}
-
-// BF16 pairs with infinities and NaN set to 0.
-__device__ __forceinline__ uint32_t finite_or_zero(uint32_t w) {
-    if ((w & 0x7f80u) == 0x7f80u) w &= 0xffff0000u;
-    if ((w & 0x7f800000u) == 0x7f800000u) w &= 0x0000ffffu;
-    return w;
-}
-
 // ----------------------------------------------------------------------------- the kernel
-template <int NT>
+template <int NT, bool TREE>
 __global__ void __launch_bounds__(threads_of(NT), 1) latent_attention_kernel(const __grid_constant__ LatentParams p) {
     constexpr int kSCols = NT;                    // tensor-memory columns of one S^T
     constexpr int kTmem = NT == 64 ? 512 : NT == 32 ? 256 : 128;
@@ -637,7 +507,7 @@ __global__ void __launch_bounds__(threads_of(NT), 1) latent_attention_kernel(con
         int at = 0, slot = 0, n = 0, rslot = 0;  // slots and tiles done; the rings' next slots
         unsigned ph = 0, rph = 0;                // parities of the rings' rounds
         bool ok = true;
-        while (ok && walk.next(p, r, o)) {
+        while (ok && walk.template next<TREE>(p, r, o)) {
             if (o.k0 >= o.k1) continue;
             Pages pages(p, o);
             for (int k = o.k0; ok && k < o.k1; ++k, ++n) {
@@ -708,7 +578,7 @@ __global__ void __launch_bounds__(threads_of(NT), 1) latent_attention_kernel(con
         unsigned ph = 0, rph = 0;  // parities of the rings' rounds
         bool ok = true;
         const uint32_t base_d = alike(static_cast<int>(tmem));
-        while (ok && alike(walk.next(p, r, o) ? 1 : 0)) {
+        while (ok && alike(walk.template next<TREE>(p, r, o) ? 1 : 0)) {
             const int tiles = alike(o.k1 - o.k0);
             if (tiles == 0) continue;
             // the queries, when the last piece's products have read the ones before
@@ -789,7 +659,7 @@ __global__ void __launch_bounds__(threads_of(NT), 1) latent_attention_kernel(con
         int n = 0, slot = 0;
         bool ok = true;
         const uint32_t base_d = alike(static_cast<int>(t_o));
-        while (ok && alike(walk.next(p, r, o) ? 1 : 0)) {
+        while (ok && alike(walk.template next<TREE>(p, r, o) ? 1 : 0)) {
             const int tiles = alike(o.k1 - o.k0);
             for (int k = 0; k < tiles; ++k, ++n) {
                 if (!(ok = all_wait(pfull + 8 * (n & 1), (n >> 1) & 1, &stop))) break;
@@ -822,7 +692,7 @@ __global__ void __launch_bounds__(threads_of(NT), 1) latent_attention_kernel(con
         int4 *desc = reinterpret_cast<int4 *>(p.ws);
         const bool tell = r == 0 && tid == 0 && p.groups > 1;
         if (tell && !p.by_seq) desc[g] = make_int4(0, 0, 0, -1);
-        while (walk.next(p, r, o)) {
+        while (walk.template next<TREE>(p, r, o)) {
             if (tell && o.first) {
                 const int u_last = sh.u0 + (sh.u1 - sh.u0 - o.left) + tiles_of(p, o.s) - 1;
                 // the last share that begins at or before u_last: ceil((u_last + 1) groups / units) - 1
@@ -830,15 +700,15 @@ __global__ void __launch_bounds__(threads_of(NT), 1) latent_attention_kernel(con
                 if (p.by_seq || !o.last) desc[p.by_seq ? o.b : g] = make_int4(o.s.q0, o.s.n, g, o.last ? -1 : g1);
             }
             float m[NC], l[NC];
-            int lim[NC];  // keys a row sees
+            int lim[NC];  // keys a row sees (all it sees, or those before the drafted tokens')
 #pragma unroll
             for (int c = 0; c < NC; ++c) {
                 const int col = col0 + 8 * (c >> 1) + c0 + (c & 1);
                 m[c] = kNoMax;
                 l[c] = 0.0f;
-                lim[c] = col < o.nrows ? o.s.len - o.s.n_all + p.heads.div(o.row0 + col) + 1 : 0;
+                lim[c] = col < o.nrows ? o.s.len - o.s.n_all + (TREE ? 0 : p.heads.div(o.row0 + col) + 1) : 0;
             }
-            const int lim_min = max(0, o.s.len - o.s.n_all + p.heads.div(o.row0) + 1);
+            const int lim_min = max(0, o.s.len - o.s.n_all + (TREE ? 0 : p.heads.div(o.row0) + 1));
             for (int k = o.k0; k < o.k1 && !dead; ++k, ++n) {
                 ok = wait_or_stop(sfull + 8 * (n & 1), (n >> 1) & 1, &stop) && ok;
                 ok = __all_sync(0xffffffffu, ok);
@@ -860,8 +730,19 @@ __global__ void __launch_bounds__(threads_of(NT), 1) latent_attention_kernel(con
 #pragma unroll
                     for (int i = 0; i < CT / 8; ++i)
 #pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            if (key + 8 * (e >> 1) >= lim[2 * i + (e & 1)]) x[4 * i + e] = -inf;
+                        for (int e = 0; e < 4; ++e) {
+                            const int at = key + 8 * (e >> 1), c = 2 * i + (e & 1);
+                            bool hidden = at >= lim[c];
+                            if (TREE && hidden) {
+                                // a drafted token's row: its bit in the mask of the query's token
+                                const int col = col0 + 8 * i + c0 + (e & 1), draft = at - (o.s.len - o.s.n_all);
+                                if (col < o.nrows && at < o.s.len && draft < 64 * p.words) {
+                                    const int tok = o.s.q0 + p.heads.div(o.row0 + col);
+                                    hidden = !((p.tree[tok * p.ld_tree + (draft >> 6)] >> (draft & 63)) & 1);
+                                }
+                            }
+                            if (hidden) x[4 * i + e] = -inf;
+                        }
                 };
 #pragma unroll
                 for (int i = 0; i < CT / 8; ++i)
@@ -1263,11 +1144,19 @@ __global__ void __launch_bounds__(PB == 8 ? 1024 : 128) latent_join_kernel(const
     }
 }
 
+template <bool TREE>
 const void *kernel_of(int nt) {
-    return nt == 64   ? reinterpret_cast<const void *>(&latent_attention_kernel<64>)
-           : nt == 32 ? reinterpret_cast<const void *>(&latent_attention_kernel<32>)
-                      : reinterpret_cast<const void *>(&latent_attention_kernel<16>);
+    return nt == 64   ? reinterpret_cast<const void *>(&latent_attention_kernel<64, TREE>)
+           : nt == 32 ? reinterpret_cast<const void *>(&latent_attention_kernel<32, TREE>)
+                      : reinterpret_cast<const void *>(&latent_attention_kernel<16, TREE>);
 }
+
+// The drafted tokens' masks of a call.
+struct Tree {
+    const long long *masks;
+    long long ld;
+    int words;
+};
 
 // The sizes of a call: rows a CTA, CTAs a group, groups, a sequence's cost in tiles.
 struct Split {
@@ -1375,32 +1264,16 @@ bool in_inputs(const sgemm_latent_attention_t &a, const Heads *h, const void *b,
            block_touches(b, n, a.seq_lens, 4LL * a.B, 0, 1) || block_touches(b, n, a.cu_q, 4LL * a.B + 4, 0, 1);
 }
 
-}  // namespace latent
-}  // namespace sk
-
-extern "C" sgemm_status_t sgemm_latent_attention_workspace(const sgemm_latent_attention_t *a, long long *bytes) {
-    using namespace sk;
-    if (!a || !bytes) return SGEMM_ERR_INVALID_ARG;
-    *bytes = 0;
-    sgemm_status_t st = latent::check_sizes(*a);
-    if (st != SGEMM_OK) return st;
-    if (a->B == 0 || a->total_q == 0) return SGEMM_OK;
-    int sms = 0, *err = nullptr;
-    st = device_ready(&sms, &err);
-    if (st != SGEMM_OK) return st;
-    *bytes = latent::split_of(*a, sms).ws_bytes;
-    return SGEMM_OK;
-}
-
-extern "C" sgemm_status_t sgemm_bf16_latent_attention(const sgemm_latent_attention_t *a, sgemm_stream_t stream) {
-    using namespace sk;
-    using namespace sk::latent;
+sgemm_status_t attend(const sgemm_latent_attention_t *a, const Tree *tree, sgemm_stream_t stream) {
     if (!a) return SGEMM_ERR_INVALID_ARG;
     sgemm_status_t st = check_sizes(*a);
     if (st != SGEMM_OK) return st;
+    if (tree && (tree->words < 1 || a->max_q > 64LL * tree->words || tree->ld < tree->words || tree->ld >= (1LL << 28)))
+        return SGEMM_ERR_INVALID_ARG;
     if (a->B == 0 || a->total_q == 0) return SGEMM_OK;
     const long long W = a->R + a->E;
-    if (!a->q || !a->cache || !a->block_table || !a->seq_lens || !a->out) return SGEMM_ERR_INVALID_ARG;
+    if (!a->q || !a->cache || !a->block_table || !a->seq_lens || !a->out || (tree && !tree->masks))
+        return SGEMM_ERR_INVALID_ARG;
     if (!a->cu_q && a->total_q != static_cast<long long>(a->B) * a->max_q) return SGEMM_ERR_INVALID_ARG;
     if (a->ldt < a->table_width || a->row_stride < W || a->page_stride < (a->page_size - 1) * a->row_stride + W ||
         a->q_token < 0 || a->q_head < 0 || a->workspace_bytes < 0 || std::isnan(a->scale) || std::isinf(a->scale))
@@ -1415,7 +1288,8 @@ extern "C" sgemm_status_t sgemm_bf16_latent_attention(const sgemm_latent_attenti
     }
     if (!aligned(a->q, 16) || a->q_token % 8 || a->q_head % 8 || !aligned(a->cache, 16) || a->row_stride % 8 ||
         a->page_stride % 8 || !aligned(a->out, 4) || a->out_token % 2 || a->out_head % 2 || !aligned(a->lse, 4) ||
-        !aligned(a->block_table, 4) || !aligned(a->seq_lens, 4) || !aligned(a->cu_q, 4) || !aligned(a->workspace, 16))
+        !aligned(a->block_table, 4) || !aligned(a->seq_lens, 4) || !aligned(a->cu_q, 4) || !aligned(a->workspace, 16) ||
+        (tree && !aligned(tree->masks, 8)))
         return SGEMM_ERR_MISALIGNED;
     // out and lse lie apart from what is read and from each other
     const Heads q{a->q, 2 * W, 2 * a->q_token, 2 * a->q_head}, out{a->out, 2LL * a->R, 2 * a->out_token, 2 * a->out_head};
@@ -1423,6 +1297,12 @@ extern "C" sgemm_status_t sgemm_bf16_latent_attention(const sgemm_latent_attenti
     if (heads_overlap(out, q, a->total_q, a->H) || heads_overlap(lse, q, a->total_q, a->H) ||
         heads_overlap(out, lse, a->total_q, a->H) || in_inputs(*a, &out, nullptr, 0) ||
         (a->lse && in_inputs(*a, &lse, nullptr, 0)))
+        return SGEMM_ERR_INVALID_ARG;
+    // and so are the masks (a block of out or lse touches one of their rows)
+    auto on_masks = [&](const void *b, long long n) {
+        return tree && block_touches(b, n, tree->masks, 8LL * tree->words, 8 * tree->ld, a->total_q);
+    };
+    if (on_masks(out.p, out.extent(a->total_q, a->H)) || (a->lse && on_masks(lse.p, lse.extent(a->total_q, a->H))))
         return SGEMM_ERR_INVALID_ARG;
     // strides that a tensor map can hold
     if (a->row_stride >= (1LL << 38) || a->page_stride >= (1LL << 38)) return SGEMM_ERR_UNSUPPORTED_SHAPE;
@@ -1438,7 +1318,8 @@ extern "C" sgemm_status_t sgemm_bf16_latent_attention(const sgemm_latent_attenti
     auto in_scratch = [&](const Heads &h) {
         return rows_overlap(a->workspace, sp.ws_bytes, 0, h.p, h.extent(a->total_q, a->H), 0, 1);
     };
-    if (sp.ws_bytes > 0 && (in_scratch(q) || in_scratch(out) || in_scratch(lse) || in_inputs(*a, nullptr, a->workspace, sp.ws_bytes)))
+    if (sp.ws_bytes > 0 && (in_scratch(q) || in_scratch(out) || in_scratch(lse) || in_inputs(*a, nullptr, a->workspace, sp.ws_bytes) ||
+                            on_masks(a->workspace, sp.ws_bytes)))
         return SGEMM_ERR_INVALID_ARG;
     p.nt = sp.nt;
     // one stride from each (token, head) row to the next, wide enough that rows are apart (a
@@ -1474,6 +1355,11 @@ extern "C" sgemm_status_t sgemm_bf16_latent_attention(const sgemm_latent_attenti
     p.scale_log2 = static_cast<float>(static_cast<double>(a->scale) * 1.4426950408889634);
     p.flags = static_cast<int>(a->flags);
 
+    if (tree) {
+        p.tree = reinterpret_cast<const unsigned long long *>(tree->masks);
+        p.ld_tree = tree->ld;
+        p.words = tree->words;
+    }
     p.heads = Divisor::of(a->H);
     p.ctas = Divisor::of(sp.rt);
     p.shares = Divisor::of(sp.groups);
@@ -1487,13 +1373,13 @@ extern "C" sgemm_status_t sgemm_bf16_latent_attention(const sgemm_latent_attenti
                       40 * sp.nt + 16;
     p.slots = std::min(kMaxSlots, (static_cast<int>(kMaxSmemOptin) - fixed) / kSlot);
     const int smem = fixed + p.slots * kSlot;
-    const void *fn = kernel_of(sp.nt);
+    const void *fn = tree ? kernel_of<true>(sp.nt) : kernel_of<false>(sp.nt);
     {
         // once per kernel and device: allow the shared memory
-        static std::atomic<unsigned long long> done[3];
+        static std::atomic<unsigned long long> done[6];
         int dev = 0;
         if (cudaGetDevice(&dev) != cudaSuccess) return SGEMM_ERR_CUDA;
-        std::atomic<unsigned long long> &d = done[sp.nt == 64 ? 2 : sp.nt == 32 ? 1 : 0];
+        std::atomic<unsigned long long> &d = done[(sp.nt == 64 ? 2 : sp.nt == 32 ? 1 : 0) + (tree ? 3 : 0)];
         const unsigned long long bit = dev < 64 ? 1ULL << dev : 0ULL;
         if (!(d.load(std::memory_order_acquire) & bit)) {
             if (allow_max_dynamic_smem(fn) != cudaSuccess) return SGEMM_ERR_CUDA;
@@ -1522,4 +1408,31 @@ extern "C" sgemm_status_t sgemm_bf16_latent_attention(const sgemm_latent_attenti
     if (launch(join, grid, dim3(static_cast<unsigned>(32 * (few ? a->R / 128 : p.pw))), 0, cs, &p) != cudaSuccess)
         return SGEMM_ERR_CUDA;
     return SGEMM_OK;
+}
+
+}  // namespace latent
+}  // namespace sk
+
+extern "C" sgemm_status_t sgemm_latent_attention_workspace(const sgemm_latent_attention_t *a, long long *bytes) {
+    using namespace sk;
+    if (!a || !bytes) return SGEMM_ERR_INVALID_ARG;
+    *bytes = 0;
+    sgemm_status_t st = latent::check_sizes(*a);
+    if (st != SGEMM_OK) return st;
+    if (a->B == 0 || a->total_q == 0) return SGEMM_OK;
+    int sms = 0, *err = nullptr;
+    st = device_ready(&sms, &err);
+    if (st != SGEMM_OK) return st;
+    *bytes = latent::split_of(*a, sms).ws_bytes;
+    return SGEMM_OK;
+}
+
+extern "C" sgemm_status_t sgemm_bf16_latent_attention(const sgemm_latent_attention_t *a, sgemm_stream_t stream) {
+    return sk::latent::attend(a, nullptr, stream);
+}
+
+extern "C" sgemm_status_t sgemm_bf16_latent_tree_attention(const sgemm_latent_attention_t *a, const long long *tree,
+                                                           long long ld_tree, int words, sgemm_stream_t stream) {
+    const sk::latent::Tree t{tree, ld_tree, words};
+    return sk::latent::attend(a, &t, stream);
 }

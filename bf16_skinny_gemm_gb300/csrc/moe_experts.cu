@@ -1,0 +1,503 @@
+// The experts' products for a few tokens (declared in include/sgemm_layers.h):
+//
+//     h[t,e] = silu(x_t Wg_e^T) * (x_t Wu_e^T),   y_t = sum_e w[t,e] h[t,e] Wd_e^T
+//
+// What bounds it.  Every chosen expert's 3 F D weights are read once, for the few tokens that
+// chose it: 2 operations a byte and token.  Up to 128 tokens the bytes bound it.
+//
+// So the tensor cores have time to spare, and the kernels spend it on not sorting anything: the
+// products are made for ALL tokens of the call (N = 16, 32, 64 or 128 columns of tcgen05.mma, the
+// weights' rows on the M side), and the first kernel's epilogue keeps what a token chose.
+//
+//  * Up: tiles of 8..64 gate rows and the same up rows of one expert against x (T x D).  The epilogue
+//    brings gate and up of an element together in shared memory and writes
+//    w[t,e] silu(gate) up, BF16, as row t of expert e's block of scratch; zeros for tokens that did
+//    not choose e.  (The rounding of that product to BF16, the operand type of the second one,
+//    is the only one between x and y: 2^-9 of it at most, at random over F elements.)
+//  * Down: with those zeros, y = sum_e H_e Wd_e^T is ONE product over k = (expert, element of F),
+//    accumulated in tensor memory over all experts, in the order of their indices.  The two CTAs
+//    of a cluster take half of that k each for 8..128 rows of y, and swap FP32 partial sums
+//    through distributed shared memory (st.async), half of the tokens each, added in rank order.
+//    No atomics, no sorting: the result does not depend on timing.
+//
+// Both kernels stream with TMA into a ring of 64-element chunks: one warp copies the weights, one
+// the other operand (x or H, from the L2 cache), one issues the MMAs, four do the epilogue.  A ring
+// takes less than half of the shared memory, so that the second kernel's CTAs are there, their
+// barriers and tables ready, when the first one's end.  The rows a tile has are chosen on the host
+// so that the tiles divide evenly over the SMs.
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <atomic>
+#include <cmath>
+#include <cstring>
+
+#include "decode_common.h"
+#include "sgemm_layers.h"
+#include "tc05_roles.cuh"
+#include "tensor_map.h"
+
+namespace sk {
+namespace moe {
+
+using namespace roles;
+
+constexpr int kMostExperts = 1024;
+constexpr int kMostTokens = 128;
+constexpr int kMostEntries = 32;  // a token
+constexpr int kThreadsExperts = 32 * 7;  // weights, MMA, 4 of epilogue, the other operand
+constexpr int kRing = 16;         // slots at most
+constexpr int kSplit = 2;         // CTAs of a cluster that share the second product's k
+constexpr int kRingBytes = 90 * 1024;
+
+struct ExpertParams {
+    CUtensorMap tw;  // the weights: {D, 2F, E}, or {F, D, E}
+    CUtensorMap tb;  // the other operand: x {D, T, 1}, or H {F, T, experts}
+    const int *ids;
+    const float *weights;
+    uint16_t *h;     // H, [expert of the list][T][F]
+    uint16_t *y;
+    int *err;
+    long long ldi, ldwt, ldy;
+    int T, D, F, E, k;
+    int rows;        // of weights (of gate and of up, or of down) a tile
+    int tiles;       // of an expert (up)
+    int box;         // rows of a box of the other operand
+    int slots, flags;
+};
+
+__host__ __device__ constexpr int slot_bytes(bool up, int rows, int n) { return ((up ? 2 : 1) * rows + n) * 128; }
+// behind the ring: an MMA reads 128 rows of weights though a tile may have fewer
+__host__ __device__ constexpr int tail_bytes(bool up, int rows, int n) {
+    return 128 > (up ? 2 : 1) * rows + n ? (128 - (up ? 2 : 1) * rows - n) * 128 : 0;
+}
+
+template <int N, bool UP>
+__global__ void __launch_bounds__(kThreadsExperts, 1) moe_experts_kernel(const __grid_constant__ ExpertParams p) {
+    constexpr int kAcc = UP ? 2 : 1;
+    constexpr int kTmem = kAcc * N < 32 ? 32 : kAcc * N;
+    constexpr uint32_t kIdescN = (1u << 4) | (1u << 7) | (1u << 10) | (static_cast<uint32_t>(N >> 3) << 17) |
+                                 (static_cast<uint32_t>(128 >> 4) << 24);
+    extern __shared__ uint8_t raw[];
+    __shared__ __align__(8) uint64_t bars[2 * kRing + 2 * 2 + 2];
+    __shared__ uint32_t tmem_slot;
+    __shared__ int stop;
+    __shared__ unsigned chosen[kMostExperts / 32];
+    __shared__ int list[kMostExperts], count;
+    __shared__ float wt[kMostTokens];
+    __shared__ int on[kMostTokens];
+    __shared__ float ex[UP ? 128 : 1][17];
+    uint8_t *base = raw + ((1024u - (saddr(raw) & 1023u)) & 1023u);  // swizzled operands start on 1 KiB
+    // partial sums, [rank][token][128]
+    float *red = reinterpret_cast<float *>(base + p.slots * slot_bytes(UP, p.rows, N) + tail_bytes(UP, p.rows, N));
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int S = p.slots, per_slot = slot_bytes(UP, p.rows, N), w_bytes = (UP ? 2 : 1) * p.rows * 128;
+    const uint32_t ring = saddr(base);
+    const uint32_t full = saddr(bars), empty = full + 8 * kRing, afull = empty + 8 * kRing, aempty = afull + 16,
+                   fin = aempty + 16, redb = fin + 8;
+    const uint32_t rank = UP ? 0u : cluster_rank();
+
+    // the second kernel may always come (it waits for this one), the caller's next one where asked
+    if (UP || (p.flags & kFlagPdl)) pdl_launch_dependents();
+    if (warp == 0) {
+        if (lane == 0) {
+            prefetch_tmap(&p.tw);
+            prefetch_tmap(&p.tb);
+            stop = 0;
+        }
+        for (int i = lane; i < 2 * S; i += 32) bar_init(i < S ? full + 8 * i : empty + 8 * (i - S), i < S ? 2 : 1);
+        if (lane < 6) bar_init(afull + 8 * lane, lane == 2 || lane == 3 ? 4 : 1);
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    }
+    for (int i = threadIdx.x; i < kMostExperts / 32; i += kThreadsExperts) chosen[i] = 0u;
+    __syncthreads();
+    if (!UP) cluster_arrive_relaxed();  // this CTA has started (paired with the wait before the partial sums)
+    pdl_wait();
+    // the experts that some token chose, in the order of their indices
+    for (int i = threadIdx.x; i < p.T * p.k; i += kThreadsExperts) {
+        const int t = i / p.k, id = p.ids[t * p.ldi + (i - t * p.k)];
+        if (id >= p.E) {
+            if (blockIdx.x == 0) atomicOr(p.err, kErrBadIndex);
+        } else if (id >= 0) {
+            atomicOr(&chosen[id >> 5], 1u << (id & 31));
+        }
+    }
+    if (warp == 1) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(saddr(&tmem_slot)), "r"(kTmem)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    __syncthreads();
+    if (warp == 2) {
+        unsigned bits = chosen[lane];
+        int before = __popc(bits);
+        const int mine = before;
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, before, off);
+            if (lane >= off) before += y;
+        }
+        if (lane == 31) count = before;
+        before -= mine;
+        while (bits) {
+            list[before++] = 32 * lane + __ffs(bits) - 1;
+            bits &= bits - 1;
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = tmem_slot;
+    const bool stall = (p.flags & kFlagTestStall) != 0;
+
+    // this CTA's tiles, and its chunks of k: of each tile (up), or of the one tile it has (down)
+    const int kc = ((UP ? p.D : p.F) + 63) / 64;
+    const long long all = static_cast<long long>(count) * (UP ? p.tiles : kc);
+    const int t0 = UP ? static_cast<int>(all * blockIdx.x / gridDim.x) : 0;
+    const int t1 = UP ? static_cast<int>(all * (blockIdx.x + 1) / gridDim.x) : 1;
+    const int c0 = UP ? 0 : static_cast<int>(all * rank / kSplit);
+    const int c1 = UP ? kc : static_cast<int>(all * (rank + 1) / kSplit);
+    const int d0 = UP ? 0 : static_cast<int>(blockIdx.x) / kSplit * p.rows;
+    int issued = 0;  // slots that this warp's copies were issued for
+
+    if (warp == 0 || warp == 6) {
+        // -------------------------------------------------------------------- the copies
+        const uint64_t policy = policy_of(warp == 0);
+        int slot = 0, n = 0;
+        unsigned ph = 1;
+        bool ok = true;
+        for (int t = t0; ok && t < t1; ++t) {
+            const int a = UP ? t / p.tiles : c0 / kc;
+            int slotted = a, c = UP ? 0 : c0 - a * kc;
+            const int f0 = UP ? (t - a * p.tiles) * p.rows : d0;
+            int e = c0 < c1 ? alike(list[slotted]) : 0;
+            for (int i = c0; i < c1; ++i, ++n) {
+                if (!(ok = n < S || all_wait(empty + 8 * slot, ph, &stop))) break;
+                if (!stall) issued = n + 1;
+                const uint32_t dst = ring + slot * per_slot, bar = full + 8 * slot;
+                if (elect()) {
+                    if (warp == 0) {
+                        bar_expect_tx(bar, static_cast<unsigned>(w_bytes));
+                        if (!stall) {
+                            tma_3d_hint(dst, &p.tw, 64 * c, f0, e, bar, policy);
+                            if (UP) tma_3d_hint(dst + p.rows * 128, &p.tw, 64 * c, p.F + f0, e, bar, policy);
+                        }
+                    } else {
+                        bar_expect_tx(bar, static_cast<unsigned>(p.box * 128));
+                        if (!stall) tma_3d(dst + w_bytes, &p.tb, 64 * c, 0, UP ? 0 : slotted, bar);
+                    }
+                }
+                __syncwarp();
+                if (++slot == S) {
+                    slot = 0;
+                    ph ^= 1;
+                }
+                if (++c == kc && !UP) {
+                    c = 0;
+                    if (i + 1 < c1) e = alike(list[++slotted]);
+                }
+            }
+        }
+    } else if (warp == 1) {
+        // ------------------------------------------------------------------ the products
+        int slot = 0, n = 0;
+        unsigned ph = 0;
+        bool ok = true;
+        const uint32_t base_d = alike(static_cast<int>(tmem));
+        for (int t = t0; ok && t < t1; ++t) {
+            const int i = t - t0;
+            ok = i < 2 || all_wait(aempty + 8 * (i & 1), ((i >> 1) - 1) & 1, &stop);
+            tc_fence_after();
+            const uint32_t d = base_d + (UP ? (i & 1) * N : 0);
+            for (int c = c0; ok && c < c1; ++c, ++n) {
+                if (!(ok = all_wait(full + 8 * slot, ph, &stop))) break;
+                tc_fence_after();
+                if (elect()) {
+                    const uint64_t a = tc05::sw128_desc(ring + slot * per_slot), b = tc05::sw128_desc(ring + slot * per_slot + w_bytes);
+#pragma unroll
+                    for (int kk = 0; kk < 4; ++kk) mma(d, a + ((32 * kk) >> 4), b + ((32 * kk) >> 4), kIdescN, c != c0 || kk != 0);
+                    mma_commit(empty + 8 * slot);
+                    if (c + 1 == c1) mma_commit(afull + 8 * (i & 1));
+                }
+                __syncwarp();
+                if (++slot == S) {
+                    slot = 0;
+                    ph ^= 1;
+                }
+            }
+        }
+        finish(fin, &stop);
+    } else {
+        // ------------------------------------------------------------------ the epilogue
+        const int q = warp & 3, row = 32 * q + lane, tid = threadIdx.x - 64;
+        const uint32_t quarter = static_cast<uint32_t>(32 * q) << 16;
+        const float nan = __int_as_float(0x7fc00000);
+        if constexpr (UP) {
+            int last = -1;
+            bool ok = true;
+            for (int t = t0; t < t1; ++t) {
+                const int i = t - t0, a = t / p.tiles, f0 = (t - a * p.tiles) * p.rows;
+                if (a != last) {
+                    // the tokens' weights for this expert
+                    const int e = list[a];
+                    if (last >= 0) asm volatile("bar.sync 1, 128;" ::: "memory");  // the last one's are read
+                    if (tid < p.T) {
+                        float w = 0.0f;
+                        int any = 0;
+                        for (int j = 0; j < p.k; ++j)
+                            if (p.ids[tid * p.ldi + j] == e) {
+                                w += p.weights[tid * p.ldwt + j];
+                                any = 1;
+                            }
+                        wt[tid] = w;
+                        on[tid] = any;
+                    }
+                    last = a;
+                }
+                ok = ok && wait_or_stop(afull + 8 * (i & 1), (i >> 1) & 1, &stop);
+                ok = __all_sync(0xffffffffu, ok);
+                if (ok) tc_fence_after();
+                const int f = tid & 63, half = tid >> 6;  // this thread's element, and half of 16 tokens
+                uint16_t *out = p.h + static_cast<long long>(a) * p.T * p.F + f0 + f;
+                const bool mine = f < p.rows && f0 + f < p.F;
+#pragma unroll 1
+                for (int c = 0; c < N; c += 16) {
+                    if (c >= p.T) break;
+                    uint32_t v[16];
+                    if (ok) {
+                        tc05::tmem_ld16(tmem + quarter + (i & 1) * N + c, v);
+                    } else {
+#pragma unroll
+                        for (int m = 0; m < 16; ++m) v[m] = __float_as_uint(nan);
+                    }
+                    asm volatile("bar.sync 1, 128;" ::: "memory");  // what was there is read
+#pragma unroll
+                    for (int m = 0; m < 16; ++m) ex[row][m] = __uint_as_float(v[m]);
+                    asm volatile("bar.sync 1, 128;" ::: "memory");
+                    if (mine)
+#pragma unroll
+                        for (int m = 8 * half; m < 8 * half + 8; ++m)
+                            if (c + m < p.T) {
+                                const float g = ex[f][m], u = ex[p.rows + f][m];
+                                const float h = g / (1.0f + expf(-g)) * u * wt[c + m];
+                                out[(c + m) * p.F] = on[c + m] ? f32_to_bf16_rn(h) : 0;
+                            }
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) bar_arrive(aempty + 8 * (i & 1));
+            }
+        } else {
+            bool ok = true;
+            if (c0 < c1) {
+                ok = wait_or_stop(afull, 0, &stop);
+                ok = __all_sync(0xffffffffu, ok);
+                if (ok) tc_fence_after();
+            }
+            cluster_wait_acquire();  // the other CTA's shared memory and mbarriers are there
+            const int each = (p.T + kSplit - 1) / kSplit;  // tokens a rank adds up
+            const int first = static_cast<int>(rank) * each, own = max(0, min(p.T, first + each) - first);
+            if (tid == 0) bar_expect_tx(redb, static_cast<unsigned>((kSplit - 1) * own * p.rows * 4));
+            for (int c = 0; c < N; c += 16) {
+                if (c >= p.T) break;
+                uint32_t v[16];
+#pragma unroll
+                for (int m = 0; m < 16; ++m) v[m] = ok ? 0u : __float_as_uint(nan);
+                if (ok && c0 < c1) tc05::tmem_ld16(tmem + quarter + c, v);
+                if (row < p.rows)
+#pragma unroll
+                    for (int m = 0; m < 16; ++m) {
+                        const int t = c + m;
+                        if (t >= p.T) continue;
+                        const uint32_t to = static_cast<uint32_t>(t / each);
+                        float *at = red + (rank * each + (t - to * each)) * 128 + row;
+                        if (to == rank)
+                            *at = __uint_as_float(v[m]);
+                        else
+                            st_async1(cluster_addr(saddr(at), to), __uint_as_float(v[m]), cluster_addr(redb, to));
+                    }
+            }
+            const bool got = bar_wait_cluster(redb, 0);
+            if (!got) atomicExch(&stop, 1);
+            if (row < p.rows && d0 + row < p.D)
+                for (int t = 0; t < own; ++t) {
+                    float s = red[t * 128 + row];
+#pragma unroll
+                    for (int r = 1; r < kSplit; ++r) s += red[(r * each + t) * 128 + row];
+                    p.y[(first + t) * p.ldy + d0 + row] = f32_to_bf16_rn(got ? s : nan);
+                }
+        }
+    }
+    if (!UP && (warp < 2 || warp == 6)) cluster_wait_acquire();
+    __syncwarp();
+    // after a stop: the copies issued have landed before the shared memory goes
+    if (lane == 0 && *reinterpret_cast<volatile int *>(&stop) && (warp == 0 || warp == 6))
+        for (int i = max(0, issued - S); i < issued; ++i) landed(full + 8 * (i % S), (i / S) & 1);
+    tc_fence_before();
+    __syncthreads();
+    if (threadIdx.x == 32 && stop) atomicOr(p.err, 1);
+    if (!UP && stop) {
+        // A CTA that gave up may have got here before the other one's stores into it were issued:
+        // this barrier waits for every thread of the cluster that has not exited, then (bounded)
+        // for those stores.
+        cluster_arrive_release();
+        cluster_wait_acquire();
+        if (warp == 2 && lane == 0) (void)bar_wait_cluster(redb, 0);
+    }
+    if (warp == 1) {
+        tc_fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmem) : "memory");
+    }
+}
+
+int columns_of(int T) { return T <= 16 ? 16 : T <= 32 ? 32 : T <= 64 ? 64 : 128; }
+
+template <bool UP>
+const void *kernel_of(int n) {
+    return n == 16   ? reinterpret_cast<const void *>(&moe_experts_kernel<16, UP>)
+           : n == 32 ? reinterpret_cast<const void *>(&moe_experts_kernel<32, UP>)
+           : n == 64 ? reinterpret_cast<const void *>(&moe_experts_kernel<64, UP>)
+                     : reinterpret_cast<const void *>(&moe_experts_kernel<128, UP>);
+}
+
+// Rows of a tile (a multiple of 8 up to `most`), so that `count` blocks of `of` rows fall evenly on
+// `ctas`: the fewest rows on the CTA that has the most, and the largest tile of equals.
+int rows_of(long long count, long long of, int most, int ctas) {
+    int best = 8;
+    long long least = -1;
+    for (int r = 8; r <= most && r < of + 8; r += 8) {
+        const long long tiles = count * ((of + r - 1) / r), load = (tiles + ctas - 1) / ctas * r;
+        if (least < 0 || load <= least) {
+            least = load;
+            best = r;
+        }
+    }
+    return best;
+}
+
+sgemm_status_t check_sizes(const sgemm_moe_experts_t &a) {
+    if (a.flags & ~(kDecodeFlags | SGEMM_FLAG_TEST_STALL)) return SGEMM_ERR_INVALID_ARG;
+    if (a.T < 0 || a.D < 1 || a.F < 1 || a.E < 1 || a.E > kMostExperts || a.k < 1 || a.k > kMostEntries || a.D > (1 << 20) ||
+        a.F > (1 << 20))
+        return SGEMM_ERR_INVALID_ARG;
+    if (a.T > kMostTokens || a.D % 8 || a.F % 8) return SGEMM_ERR_UNSUPPORTED_SHAPE;
+    return SGEMM_OK;
+}
+
+long long listed(const sgemm_moe_experts_t &a) { return std::min<long long>(a.E, static_cast<long long>(a.T) * a.k); }
+long long scratch(const sgemm_moe_experts_t &a) { return listed(a) * a.T * a.F * 2; }
+
+// Allow a kernel all the shared memory that there is, once per device.
+bool allow(const void *fn, std::atomic<unsigned long long> &done) {
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return false;
+    const unsigned long long bit = dev < 64 ? 1ULL << dev : 0ULL;
+    if (!(done.load(std::memory_order_acquire) & bit)) {
+        if (allow_max_dynamic_smem(fn) != cudaSuccess) return false;
+        done.fetch_or(bit, std::memory_order_release);
+    }
+    return true;
+}
+
+}  // namespace moe
+}  // namespace sk
+
+extern "C" sgemm_status_t sgemm_moe_experts_workspace(const sgemm_moe_experts_t *a, long long *bytes) {
+    using namespace sk::moe;
+    if (!a || !bytes) return SGEMM_ERR_INVALID_ARG;
+    *bytes = 0;
+    const sgemm_status_t st = check_sizes(*a);
+    if (st == SGEMM_OK) *bytes = scratch(*a);
+    return st;
+}
+
+extern "C" sgemm_status_t sgemm_bf16_moe_experts(const sgemm_moe_experts_t *a, sgemm_stream_t stream) {
+    using namespace sk;
+    using namespace sk::moe;
+    if (!a) return SGEMM_ERR_INVALID_ARG;
+    sgemm_status_t st = check_sizes(*a);
+    if (st != SGEMM_OK || a->T == 0) return st;
+    if (!a->x || !a->w_gate_up || !a->w_down || !a->ids || !a->weights || !a->y || a->workspace_bytes < 0) return SGEMM_ERR_INVALID_ARG;
+    const long long far = kMapStride;
+    if (a->ldx < a->D || a->gu_row < a->D || a->dn_row < a->F || a->ldi < a->k || a->ldwt < a->k || a->ldy < a->D ||
+        a->gu_expert < (2LL * a->F - 1) * a->gu_row + a->D || a->dn_expert < (a->D - 1LL) * a->dn_row + a->F)
+        return SGEMM_ERR_INVALID_ARG;
+    if (a->ldx >= far || a->gu_row >= far || a->dn_row >= far || a->ldi >= far || a->ldwt >= far || a->ldy >= far ||
+        a->gu_expert >= far || a->dn_expert >= far)
+        return SGEMM_ERR_UNSUPPORTED_SHAPE;
+    if (!aligned(a->x, 16) || !aligned(a->w_gate_up, 16) || !aligned(a->w_down, 16) || a->ldx % 8 || a->gu_row % 8 ||
+        a->gu_expert % 8 || a->dn_row % 8 || a->dn_expert % 8 || !aligned(a->y, 2) || !aligned(a->ids, 4) ||
+        !aligned(a->weights, 4) || !aligned(a->workspace, 128))
+        return SGEMM_ERR_MISALIGNED;
+    const long long need = scratch(*a);
+    if (!a->workspace || a->workspace_bytes < need) return SGEMM_ERR_NO_WORKSPACE;
+    // what is written lies apart from what is read, and the scratch from the output
+    auto on_inputs = [&](const void *b, long long n) {
+        return block_touches(b, n, a->x, 2LL * a->D, 2 * a->ldx, a->T) ||
+               block_touches(b, n, a->w_gate_up, (a->gu_row * (2LL * a->F - 1) + a->D) * 2, 2 * a->gu_expert, a->E) ||
+               block_touches(b, n, a->w_down, (a->dn_row * (a->D - 1LL) + a->F) * 2, 2 * a->dn_expert, a->E) ||
+               block_touches(b, n, a->ids, 4LL * a->k, 4 * a->ldi, a->T) ||
+               block_touches(b, n, a->weights, 4LL * a->k, 4 * a->ldwt, a->T);
+    };
+    auto in_y = [&](const void *b, long long n) { return block_touches(b, n, a->y, 2LL * a->D, 2 * a->ldy, a->T); };
+    const long long wx = 2LL * a->D;
+    if (rows_overlap(a->y, wx, 2 * a->ldy, a->x, wx, 2 * a->ldx, a->T) ||
+        on_inputs(a->workspace, need) || in_y(a->workspace, need) ||
+        in_y(a->w_gate_up, ((a->E - 1) * a->gu_expert + a->gu_row * (2LL * a->F - 1) + a->D) * 2) ||
+        in_y(a->w_down, ((a->E - 1) * a->dn_expert + a->dn_row * (a->D - 1LL) + a->F) * 2) ||
+        in_y(a->ids, 4 * ((a->T - 1) * a->ldi + a->k)) || in_y(a->weights, 4 * ((a->T - 1) * a->ldwt + a->k)))
+        return SGEMM_ERR_INVALID_ARG;
+    ExpertParams p;
+    std::memset(&p, 0, sizeof(p));
+    int sms = 0;
+    st = device_ready(&sms, &p.err);
+    if (st != SGEMM_OK) return st;
+    p.ids = a->ids;
+    p.weights = a->weights;
+    p.h = static_cast<uint16_t *>(a->workspace);
+    p.y = a->y;
+    p.ldi = a->ldi;
+    p.ldwt = a->ldwt;
+    p.ldy = a->ldy;
+    p.T = a->T;
+    p.D = a->D;
+    p.F = a->F;
+    p.E = a->E;
+    p.k = a->k;
+    p.flags = static_cast<int>(a->flags);
+    const int n = columns_of(a->T);
+    p.box = std::min(n, (a->T + 7) / 8 * 8);
+    const cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
+    static std::atomic<unsigned long long> done[8];
+    const int which = n == 16 ? 0 : n == 32 ? 1 : n == 64 ? 2 : 3;
+    const long long experts = listed(*a);
+    auto ring = [&](bool up) {
+        p.slots = std::max(3, std::min(kRing, kRingBytes / slot_bytes(up, p.rows, n)));
+        return static_cast<size_t>(p.slots) * slot_bytes(up, p.rows, n) + tail_bytes(up, p.rows, n) + 1024;
+    };
+    {
+        const void *fn = kernel_of<true>(n);
+        p.rows = rows_of(experts, a->F, 64, sms);
+        p.tiles = (a->F + p.rows - 1) / p.rows;
+        const size_t smem = ring(true);
+        if (!map_3d(&p.tw, a->w_gate_up, a->D, 2LL * a->F, a->E, a->gu_row, a->gu_expert, p.rows, CU_TENSOR_MAP_L2_PROMOTION_L2_256B) ||
+            !map_3d(&p.tb, a->x, a->D, a->T, 1, a->ldx, a->ldx, p.box, CU_TENSOR_MAP_L2_PROMOTION_L2_128B) || !allow(fn, done[which]))
+            return SGEMM_ERR_CUDA;
+        const long long ctas = std::min<long long>(sms, experts * p.tiles);
+        if (launch(fn, dim3(static_cast<unsigned>(ctas)), dim3(kThreadsExperts), smem, cs, &p) != cudaSuccess) return SGEMM_ERR_CUDA;
+    }
+    const void *fn = kernel_of<false>(n);
+    p.rows = rows_of(kSplit, a->D, 128, sms);
+    const size_t smem = ring(false) + static_cast<size_t>(kSplit) * ((a->T + kSplit - 1) / kSplit) * 512;
+    if (!map_3d(&p.tw, a->w_down, a->F, a->D, a->E, a->dn_row, a->dn_expert, p.rows, CU_TENSOR_MAP_L2_PROMOTION_L2_256B) ||
+        !map_3d(&p.tb, a->workspace, a->F, a->T, experts, a->F, static_cast<long long>(a->T) * a->F, p.box,
+                CU_TENSOR_MAP_L2_PROMOTION_L2_128B) ||
+        !allow(fn, done[4 + which]))
+        return SGEMM_ERR_CUDA;
+    const unsigned tiles = static_cast<unsigned>((a->D + p.rows - 1) / p.rows);
+    if (launch(fn, dim3(kSplit * tiles), dim3(kThreadsExperts), smem, cs, &p, kSplit) != cudaSuccess) return SGEMM_ERR_CUDA;
+    return SGEMM_OK;
+}
