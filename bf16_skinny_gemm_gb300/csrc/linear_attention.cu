@@ -1,0 +1,1054 @@
+// Linear attention with a decay for each head, whole sequences (declared in
+// include/sgemm_layers.h).  In chunks of 64 tokens, with G_i the sum of g over a chunk's tokens up to i:
+//
+//     o_i = scale (exp(G_i) q_i^T S + sum_{j <= i} exp(G_i - G_j) (q_i . k_j) v_j)
+//     S'  = exp(G) S + sum_j exp(G - G_j) k_j v_j^T
+//
+// What bounds it.  A token and head's q, k, v, out are 4 x 128 elements, 1 KiB, for about 10^5
+// operations: 100 a byte, below what the tensor cores do for each byte of memory.  So memory bounds it,
+// if the chain of the chunks' states does not: that chain has to be short, and there have to be
+// enough of them.
+//
+// Work split.  The chunks of all (sequence, head) pairs form one line, cut into equal shares, one
+// for each SM; a share ends anywhere inside a sequence.  Three launches:
+//   1. states: for every share that ends inside a sequence, what its part of that sequence adds to
+//      the state, U = sum_j exp(sum of g from j to the share's end) k_j v_j^T, and the sum of its g.  The
+//      chunks are taken from the last to the first, so that the factor of a key is known at once
+//      and the sum stays in tensor memory untouched.
+//   2. joining: along each cut sequence, S' = exp(G) S + U from share to share, element by element.
+//   3. outputs: every share from the state it begins with.
+// Keys and values of cut sequences are read twice.
+//
+// The output kernel, a CTA an SM, all products transposed so that the value's elements are the 128
+// rows (lanes of tensor memory) and tokens the columns:
+//     A   = Q K^T          64 x 64          both from shared memory
+//     O1  = Sb^T Q^T       128 x 64         Sb, the state rounded to BF16, as operand from tensor memory
+//     O2  = V^T P^T        128 x 64         P = A with its decays, BF16, through shared memory
+//     S^T += V^T K'        128 x Dk         K' = exp(G - G_j) k_j as two BF16 numbers (two products)
+// The state stays in tensor memory, FP32, for the whole sequence; a lane holds a value element's row, so that
+// scaling it and rounding it for the next O1 needs no exchange.  out = scale (exp(G_i) O1 + O2) is put
+// together in FP32.  Why K' in two numbers: its rounding would be the state's only error above
+// FP32's, 2^-9 of every summand, and it goes on to all later tokens; 2^-17 costs one product in six.
+// P and Sb are rounded once: what they make is rounded to BF16 right after.
+// Roles: one warp copies (TMA, a ring of chunks), one issues all products, two sum the decays and scale the
+// keys, and four each carry the state, apply the decays to A, and write the outputs.  Exponents' sums are
+// kept as pairs of FP32 numbers: differences of long sums keep their digits.
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <atomic>
+#include <cmath>
+#include <cstring>
+
+#include "linear_common.h"
+#include "tc05_roles.cuh"
+#include "tensor_map.h"
+
+namespace sk {
+namespace linear {
+
+using namespace roles;
+
+constexpr int kC = 64;                 // tokens a chunk
+constexpr int kPart = kC * 128;        // 64 tokens x 64 elements, bytes
+constexpr int kStages = 4;             // of chunks in a ring, at most
+constexpr int kFew = 4;                // chunks a share has at least
+constexpr int kOutThreads = 16 * 32;   // copies, products, keys (2 warps), state, decays, outputs (4 each)
+constexpr int kSums = 8;               // chunks whose sums of g are kept
+constexpr int kStateThreads = 10 * 32;
+constexpr float kLeast = -1e6f;        // a decay's exponent (base 2) is cut here: 2^-1e6 is 0
+
+struct LinearParams {
+    CUtensorMap tq, tk, tv;  // {D, N, heads}, boxes of 64 tokens x 64 elements
+    const float *g;
+    float *state;
+    const long long *slots;
+    const int *cu, *fresh;
+    uint16_t *out;
+    float *ws;
+    int *err;
+    long long g_token, g_head, s_slot, s_head, o_token, o_head, pool, N;
+    int B, Hv, share;  // sequences, value heads, value heads a key head
+    int Dk, Dv;
+    int groups;        // shares at most
+    int stages;
+    int flags;
+    float scale;
+};
+
+// ------------------------------------------------------------------ the line of chunks
+struct Seq {
+    int t0, len, chunks;  // first token, tokens, chunks (at least one; 0: the offsets are no sequence's)
+    long long slot;       // negative: none
+    bool bad;
+};
+
+__device__ __forceinline__ Seq seq_of(const LinearParams &p, int b) {
+    Seq s;
+    const int a = p.cu[b], e = p.cu[b + 1];
+    s.slot = p.slots[b];
+    s.bad = s.slot >= p.pool;
+    if (s.bad) s.slot = -1;
+    s.t0 = a;
+    s.len = e - a;
+    if (a < 0 || e < a || e > p.N) {
+        s.bad = true;
+        s.t0 = s.len = s.chunks = 0;
+    } else {
+        s.chunks = max(1, (s.len + kC - 1) / kC);
+    }
+    return s;
+}
+
+struct Share {
+    int units, groups, u0, u1;
+};
+
+__device__ __forceinline__ int begin_of(int units, int g, int groups) {
+    return static_cast<int>(static_cast<long long>(units) * g / groups);
+}
+
+// The line's length and share g of it (by a whole warp).
+__device__ __forceinline__ Share share_of(const LinearParams &p, int g, bool report) {
+    const int lane = threadIdx.x & 31;
+    Share s;
+    s.units = 0;
+    for (int c = 0; c < p.B; c += 32) {
+        int mine = 0;
+        if (c + lane < p.B) {
+            const Seq q = seq_of(p, c + lane);
+            mine = q.chunks * p.Hv;
+            if (q.bad && report) atomicOr(p.err, kErrBadIndex);
+        }
+        s.units += static_cast<int>(__reduce_add_sync(0xffffffffu, static_cast<unsigned>(mine)));
+    }
+    s.groups = max(1, min(p.groups, (s.units + kFew - 1) / kFew));
+    s.u0 = s.u1 = 0;
+    if (g < s.groups) {
+        s.u0 = begin_of(s.units, g, s.groups);
+        s.u1 = begin_of(s.units, g + 1, s.groups);
+    }
+    return s;
+}
+
+// A place on the line: chunk k of head h of sequence b.
+struct Place {
+    int b, h, k;
+    Seq s;
+};
+
+__device__ __forceinline__ Place place_of(const LinearParams &p, int u) {
+    const int lane = threadIdx.x & 31;
+    Place o;
+    for (int c = 0, at = 0;; c += 32) {
+        int mine = 0;
+        if (c + lane < p.B) mine = seq_of(p, c + lane).chunks * p.Hv;
+        int x = mine;
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, x, off);
+            if (lane >= off) x += y;
+        }
+        const unsigned past = __ballot_sync(0xffffffffu, u < at + x);
+        if (past || c + 32 >= p.B) {
+            const int w = past ? __ffs(past) - 1 : 0;
+            o.b = c + w;
+            const int left = u - at - __shfl_sync(0xffffffffu, x - mine, w);
+            o.s = seq_of(p, o.b);
+            o.h = left / max(1, o.s.chunks);
+            o.k = left - o.h * o.s.chunks;
+            return o;
+        }
+        at += __shfl_sync(0xffffffffu, x, 31);
+    }
+}
+
+// The chunks of a share one by one.
+struct Chunk {
+    int b, h, t0, valid;  // first token, tokens
+    bool head, tail;      // the first of its piece of a sequence, the sequence's last
+    bool first;           // the sequence's first
+};
+struct Cursor {
+    Place at;
+    int left;
+    bool head;
+    __device__ __forceinline__ Cursor(const Place &o, int n) : at(o), left(n), head(true) {}
+    __device__ __forceinline__ bool next(const LinearParams &p, Chunk &c) {
+        if (left <= 0) return false;
+        --left;
+        c.b = at.b;
+        c.h = at.h;
+        c.t0 = at.s.t0 + at.k * kC;
+        c.valid = max(0, min(kC, at.s.len - at.k * kC));
+        c.first = at.k == 0;
+        c.head = head || c.first;
+        c.tail = at.k + 1 == at.s.chunks;
+        head = false;
+        if (++at.k == at.s.chunks) {
+            at.k = 0;
+            if (++at.h == p.Hv) {
+                at.h = 0;
+                if (left > 0)
+                    do at.s = seq_of(p, ++at.b);
+                    while (at.s.chunks == 0);
+            }
+        }
+        return true;
+    }
+};
+
+// Scratch: the sum of g of each share's cut piece, then its state (what the next share begins
+// with, after the joining), then what a cut sequence begins with.
+__device__ __forceinline__ float *state_of(const LinearParams &p, int g) {
+    return p.ws + (p.groups + 3) / 4 * 4 + static_cast<long long>(g) * p.Dk * p.Dv;
+}
+__device__ __forceinline__ float *begin_state(const LinearParams &p, int g) { return state_of(p, p.groups + g); }
+
+// ------------------------------------------------------------------------- sums of exponents
+struct Pair {
+    float hi, lo;
+};
+__device__ __forceinline__ Pair add(Pair a, Pair b) {
+    const float s = a.hi + b.hi, bb = s - a.hi;
+    const float e = (a.hi - (s - bb)) + (b.hi - bb) + (a.lo + b.lo);
+    Pair r;
+    r.hi = s + e;
+    r.lo = e - (r.hi - s);
+    return r;
+}
+__device__ __forceinline__ float less(Pair a, Pair b) { return (a.hi - b.hi) + (a.lo - b.lo); }
+__device__ __forceinline__ Pair shfl(Pair a, int from) {
+    return Pair{__shfl_sync(0xffffffffu, a.hi, from), __shfl_sync(0xffffffffu, a.lo, from)};
+}
+
+// g of tokens 2 lane and 2 lane + 1 of a chunk (0 behind its tokens), in base 2.
+struct Decays {
+    float a, b;
+};
+__device__ __forceinline__ Decays load_g(const LinearParams &p, const Chunk &c) {
+    const int i = 2 * (threadIdx.x & 31);
+    const float *at = p.g + (c.t0 + static_cast<long long>(i)) * p.g_token + c.h * p.g_head;
+    Decays d;
+    d.a = i < c.valid ? at[0] : 0.0f;
+    d.b = i + 1 < c.valid ? at[p.g_token] : 0.0f;
+    return d;
+}
+// Sums up to the lane's two tokens (inclusive), and the chunk's.
+__device__ __forceinline__ void sums_of(Decays d, Pair &a, Pair &b, Pair &all) {
+    constexpr float kLog2e = 1.4426950408889634f;
+    const int lane = threadIdx.x & 31;
+    d.a *= kLog2e;
+    d.b *= kLog2e;
+    d.a = d.a < kLeast ? kLeast : d.a;  // (NaN stays)
+    d.b = d.b < kLeast ? kLeast : d.b;
+    const Pair pa{d.a, 0.0f}, pb{d.b, 0.0f};
+    Pair x = add(pa, pb);
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+        const Pair y{__shfl_up_sync(0xffffffffu, x.hi, off), __shfl_up_sync(0xffffffffu, x.lo, off)};
+        if (lane >= off) x = add(y, x);
+    }
+    b = x;
+    all = shfl(x, 31);
+    Pair before{__shfl_up_sync(0xffffffffu, x.hi, 1), __shfl_up_sync(0xffffffffu, x.lo, 1)};
+    if (lane == 0) before = Pair{0.0f, 0.0f};
+    a = add(before, pa);
+}
+
+// The product with A in tensor memory.
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool add) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "l"(b), "r"(idesc), "r"(add ? 1u : 0u)
+        : "memory");
+}
+
+// An operand whose rows are not along k: 64 elements x 8 k an atom, the next 64 elements kPart on.
+__device__ __forceinline__ uint64_t mn_desc(uint32_t addr) {
+    return tc05::kDescHi | (static_cast<uint64_t>(kPart >> 4) << 16) | static_cast<uint64_t>((addr & 0x3FFFFu) >> 4);
+}
+__host__ __device__ constexpr uint32_t idesc_of(int m, int n, bool a_mn, bool b_mn) {
+    return (1u << 4) | (1u << 7) | (1u << 10) | (a_mn ? 1u << 15 : 0u) | (b_mn ? 1u << 16 : 0u) |
+           (static_cast<uint32_t>(n >> 3) << 17) | (static_cast<uint32_t>(m >> 4) << 24);
+}
+
+// 64 columns of a 64-row accumulator in the 16 x 256-bit form: lane l has rows l / 4 and l / 4 + 8
+// of the warp's 16, of each 8 columns the pair 2 (l % 4).
+__device__ __forceinline__ void tmem_ld_a(uint32_t addr, uint32_t (&r)[32]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x256b.x8.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+          "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+          "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(addr));
+    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+}
+
+// Rows row0, row0 + step, .. of a chunk's keys, times w, as two BF16 numbers each; rows from
+// `valid` on are 0 (whatever lies there).  A warp takes 32 units of 16 bytes at a time.
+// `wa`, `wb`: the factors of rows 2 lane, 2 lane + 1.
+template <int WARPS, int DK>
+__device__ __forceinline__ void scale_keys(const uint8_t *k, uint8_t *hi, uint8_t *lo, int warp, int valid, float wa, float wb) {
+    constexpr int kUnits = DK / 8, kRows = 32 / kUnits, kEach = kC / WARPS;  // units a row, rows at a time, rows a warp
+    const int lane = threadIdx.x & 31, u = lane % kUnits;
+#pragma unroll
+    for (int i = 0; i < kEach; i += kRows) {
+        const int row = warp * kEach + i + lane / kUnits;
+        const float fa = __shfl_sync(0xffffffffu, wa, row >> 1), fb = __shfl_sync(0xffffffffu, wb, row >> 1);
+        const float w = row & 1 ? fb : fa;
+        const int at = (u >> 3) * kPart + row * 128 + (((u & 7) ^ (row & 7)) << 4);
+        uint4 h = make_uint4(0u, 0u, 0u, 0u), l = h;
+        if (row < valid) {
+            const uint4 x = *reinterpret_cast<const uint4 *>(k + at);
+            const uint32_t in[4] = {x.x, x.y, x.z, x.w};
+            uint32_t oh[4], ol[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const float a = bf16_lo(in[e]) * w, b = bf16_hi(in[e]) * w;
+                oh[e] = bf16x2(a, b);
+                ol[e] = bf16x2(a - bf16_lo(oh[e]), b - bf16_hi(oh[e]));
+            }
+            h = make_uint4(oh[0], oh[1], oh[2], oh[3]);
+            l = make_uint4(ol[0], ol[1], ol[2], ol[3]);
+        }
+        *reinterpret_cast<uint4 *>(hi + at) = h;
+        *reinterpret_cast<uint4 *>(lo + at) = l;
+    }
+}
+
+// Values behind a chunk's tokens become 0 (another sequence's, or nothing that was ever written).
+template <int WARPS>
+__device__ __forceinline__ void clear_values(uint8_t *v, int parts, int warp, int valid) {
+    const int lane = threadIdx.x & 31;
+    for (int row = valid + warp; row < kC; row += WARPS)
+        if (lane < 8 * parts) *reinterpret_cast<uint4 *>(v + (lane >> 3) * kPart + row * 128 + (lane & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
+}
+
+__host__ __device__ constexpr int chunk_bytes(int dk, int dv, bool with_q) { return ((with_q ? 2 : 1) * dk + dv) / 64 * kPart; }
+constexpr int kMisc = 1024 + 3 * kSums * kC * 4;  // barriers and small arrays
+__host__ __device__ constexpr int out_fixed(int dk) { return 2 * 2 * dk / 64 * kPart + 2 * kPart + kMisc; }
+__host__ __device__ constexpr int state_fixed(int dk) { return 2 * 2 * dk / 64 * kPart + kPart + kMisc; }
+
+// ------------------------------------------------------------------------ 1. states of cut pieces
+template <int DK>
+__global__ void __launch_bounds__(kStateThreads, 1) linear_states_kernel(const __grid_constant__ LinearParams p) {
+    constexpr int kKParts = DK / 64, kKeys = kKParts * kPart, kWarps = 8;
+    constexpr int kTmem = DK;
+    extern __shared__ uint8_t raw[];
+    uint8_t *base = raw + ((1024u - (saddr(raw) & 1023u)) & 1023u);
+    const int vparts = p.Dv / 64, stage = chunk_bytes(DK, p.Dv, false), S = p.stages;
+    uint8_t *keys = base + S * stage;  // two buffers of both numbers; a product reads 128 value
+                                       // elements though there may be 64: what follows is keys
+    uint8_t *misc = keys + 4 * kKeys + kPart;
+    uint64_t *bars = reinterpret_cast<uint64_t *>(misc);
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(misc + 256);
+    int &stop = *reinterpret_cast<int *>(misc + 260);
+    const uint32_t full = saddr(bars), empty = full + 8 * kStages, kready = empty + 8 * kStages, kfree = kready + 16, fin = kfree + 16;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = static_cast<int>(blockIdx.x);
+    if (threadIdx.x == 0) {
+        prefetch_tmap(&p.tk);
+        prefetch_tmap(&p.tv);
+        stop = 0;
+        for (int i = 0; i < S; ++i) {
+            bar_init(full + 8 * i, 1);
+            bar_init(empty + 8 * i, 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            bar_init(kready + 8 * i, kWarps);
+            bar_init(kfree + 8 * i, 1);
+        }
+        bar_init(fin, 1);
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    }
+    pdl_launch_dependents();  // the next kernels are this call's
+    pdl_wait();
+    const Share sh = share_of(p, g, false);
+    if (sh.u1 <= sh.u0) return;
+    const Place last = place_of(p, sh.u1 - 1);
+    if (last.k + 1 >= last.s.chunks) return;  // no cut sequence at this share's end
+    const int chunks = min(last.k + 1, sh.u1 - sh.u0);
+    if (warp == 1) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(saddr(tmem_slot)), "r"(kTmem)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    const bool stall = (p.flags & kFlagTestStall) != 0;
+    int issued = 0;
+    if (warp == 0) {
+        int slot = 0;
+        unsigned ph = 1;
+        for (int n = 0; n < chunks; ++n) {
+            if (n >= S && !all_wait(empty + 8 * slot, ph, &stop)) break;
+            if (!stall) issued = n + 1;
+            const uint32_t dst = saddr(base) + slot * stage, bar = full + 8 * slot;
+            if (elect()) {
+                bar_expect_tx(bar, static_cast<unsigned>(stage));
+                if (!stall) {
+                    const int t = last.s.t0 + (last.k - n) * kC;
+                    for (int c = 0; c < kKParts; ++c) tma_3d(dst + c * kPart, &p.tk, 64 * c, t, last.h / p.share, bar);
+                    for (int c = 0; c < vparts; ++c) tma_3d(dst + kKeys + c * kPart, &p.tv, 64 * c, t, last.h, bar);
+                }
+            }
+            __syncwarp();
+            if (++slot == S) {
+                slot = 0;
+                ph ^= 1;
+            }
+        }
+    } else if (warp == 1) {
+        int slot = 0;
+        unsigned ph = 0;
+        constexpr uint32_t kIdesc = idesc_of(128, DK, true, true);
+        const uint32_t d = alike(static_cast<int>(tmem));
+        for (int n = 0; n < chunks; ++n) {
+            if (!all_wait(full + 8 * slot, ph, &stop) || !all_wait(kready + 8 * (n & 1), (n >> 1) & 1, &stop)) break;
+            tc_fence_after();
+            if (elect()) {
+                const uint64_t a = mn_desc(saddr(base) + slot * stage + kKeys), b = mn_desc(saddr(keys) + (n & 1) * 2 * kKeys);
+#pragma unroll
+                for (int part = 0; part < 2; ++part)
+#pragma unroll
+                    for (int kk = 0; kk < kC / 16; ++kk)
+                        mma(d, a + kk * (2048 >> 4), b + ((part * kKeys) >> 4) + kk * (2048 >> 4), kIdesc, n != 0 || part != 0 || kk != 0);
+                mma_commit(empty + 8 * slot);
+                mma_commit(kfree + 8 * (n & 1));
+            }
+            __syncwarp();
+            if (++slot == S) {
+                slot = 0;
+                ph ^= 1;
+            }
+        }
+        finish(fin, &stop);
+    } else {
+        const int w = warp - 2;
+        Pair after{0.0f, 0.0f};  // the sum of g behind the chunk, to the piece's end
+        bool ok = true;
+        int slot = 0;
+        unsigned ph = 0;
+        Chunk c;
+        c.h = last.h;
+        auto chunk = [&](int n) {
+            c.t0 = last.s.t0 + (last.k - n) * kC;
+            c.valid = min(kC, last.s.len - (last.k - n) * kC);  // (a cut piece has whole chunks only)
+        };
+        chunk(0);
+        Decays next = load_g(p, c);
+        for (int n = 0; n < chunks; ++n) {
+            const Decays now = next;
+            const int valid = c.valid;
+            if (n + 1 < chunks) {
+                chunk(n + 1);
+                next = load_g(p, c);
+            }
+            Pair a, b, all;
+            sums_of(now, a, b, all);
+            const Pair to = add(all, after);
+            const float wa = exp2f(less(to, a)), wb = exp2f(less(to, b));
+            after = to;
+            ok = ok && all_wait(full + 8 * slot, ph, &stop) && (n < 2 || all_wait(kfree + 8 * (n & 1), ((n >> 1) - 1) & 1, &stop));
+            if (!ok) break;
+            uint8_t *out = keys + (n & 1) * 2 * kKeys;
+            scale_keys<kWarps, DK>(base + slot * stage, out, out + kKeys, w, valid, wa, wb);
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            __syncwarp();
+            if (lane == 0) bar_arrive(kready + 8 * (n & 1));
+            if (++slot == S) {
+                slot = 0;
+                ph ^= 1;
+            }
+        }
+        // the piece's state, [Dk][Dv], by warps 2..5 and 6..9: half of the columns each
+        ok = ok && all_wait(fin, 0, &stop) && *reinterpret_cast<volatile int *>(&stop) == 0;
+        ok = __all_sync(0xffffffffu, ok);
+        const float nan = __int_as_float(0x7fc00000);
+        const int q = warp & 3, dv = 32 * q + lane, half = w >> 2;
+        tc_fence_after();
+        float *to = state_of(p, g) + dv;
+        for (int col = half * (DK / 2); col < (half + 1) * (DK / 2); col += 16) {
+            uint32_t v[16];
+            if (ok) tc05::tmem_ld16(tmem + (static_cast<uint32_t>(32 * q) << 16) + col, v);
+            if (dv < p.Dv)
+#pragma unroll
+                for (int i = 0; i < 16; ++i) to[(col + i) * p.Dv] = ok ? __uint_as_float(v[i]) : nan;
+        }
+        if (w == 0 && lane == 0) p.ws[g] = ok ? exp2f(after.hi + after.lo) : nan;
+    }
+    __syncwarp();
+    if (lane == 0 && *reinterpret_cast<volatile int *>(&stop) && warp == 0)
+        for (int i = max(0, issued - S); i < issued; ++i) landed(full + 8 * (i % S), (i / S) & 1);
+    tc_fence_before();
+    __syncthreads();
+    if (threadIdx.x == 32 && stop) atomicOr(p.err, 1);
+    if (warp == 1) {
+        tc_fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmem) : "memory");
+    }
+}
+
+// ------------------------------------------------------------------------------------ 2. joining
+// Along a cut sequence, from the share it begins in: S' = exp(G) S + U, in place of U, four elements
+// a thread; and a copy of what it begins with, for the third kernel, whose other CTAs may have
+// written its last state by the time it is read.
+constexpr int kJoinThreads = 256, kJoinBatch = 8;
+__global__ void __launch_bounds__(kJoinThreads) linear_join_kernel(const __grid_constant__ LinearParams p) {
+    pdl_launch_dependents();
+    pdl_wait();
+    const int g = static_cast<int>(blockIdx.x);
+    const Share sh = share_of(p, g, false);
+    if (sh.u1 <= sh.u0) return;
+    const Place last = place_of(p, sh.u1 - 1);
+    if (last.k + 1 >= last.s.chunks || last.k >= sh.u1 - sh.u0) return;  // not cut, or begun in an earlier share
+    const long long at = 4LL * (blockIdx.y * kJoinThreads + threadIdx.x);
+    if (at >= static_cast<long long>(p.Dk) * p.Dv) return;
+    float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    if (last.s.slot >= 0 && !(p.fresh && p.fresh[last.b]))
+        s = *reinterpret_cast<const float4 *>(p.state + last.s.slot * p.s_slot + last.h * p.s_head + at);
+    *reinterpret_cast<float4 *>(begin_state(p, g) + at) = s;
+    // the shares whose end the sequence goes on behind
+    const int rest = last.s.chunks - last.k - 1;  // chunks behind this share
+    int end = g + 1;                              // one past the last such share
+    while (end < sh.groups && begin_of(sh.units, end + 1, sh.groups) - sh.u1 < rest) ++end;
+    for (int i = g; i < end; i += kJoinBatch) {
+        float4 u[kJoinBatch];
+        float e[kJoinBatch];
+#pragma unroll
+        for (int j = 0; j < kJoinBatch; ++j)
+            if (i + j < end) {
+                u[j] = *reinterpret_cast<const float4 *>(state_of(p, i + j) + at);
+                e[j] = p.ws[i + j];
+            }
+#pragma unroll
+        for (int j = 0; j < kJoinBatch; ++j)
+            if (i + j < end) {
+                s.x = fmaf(e[j], s.x, u[j].x);
+                s.y = fmaf(e[j], s.y, u[j].y);
+                s.z = fmaf(e[j], s.z, u[j].z);
+                s.w = fmaf(e[j], s.w, u[j].w);
+                *reinterpret_cast<float4 *>(state_of(p, i + j) + at) = s;
+            }
+    }
+}
+
+// ------------------------------------------------------------------------------------ 3. outputs
+template <int DK>
+__global__ void __launch_bounds__(kOutThreads, 1) linear_outputs_kernel(const __grid_constant__ LinearParams p) {
+    constexpr int kKParts = DK / 64, kKeys = kKParts * kPart;
+    // columns of tensor memory
+    constexpr int kState = 0, kSb = 128, kA = 192, kO = 256;
+    extern __shared__ uint8_t raw[];
+    uint8_t *base = raw + ((1024u - (saddr(raw) & 1023u)) & 1023u);
+    const int vparts = p.Dv / 64, stage = chunk_bytes(DK, p.Dv, true), S = p.stages;
+    uint8_t *keys = base + S * stage;   // two buffers of both numbers
+    uint8_t *ps = keys + 4 * kKeys;     // two buffers of P
+    uint8_t *misc = ps + 2 * kPart;
+    uint64_t *bars = reinterpret_cast<uint64_t *>(misc);
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(misc + 512);
+    int &stop = *reinterpret_cast<int *>(misc + 516);
+    float *all_e = reinterpret_cast<float *>(misc + 528);  // exp(G) of a chunk
+    // of each of its tokens: G_i as a pair, and exp(G_i)
+    float *ghi = reinterpret_cast<float *>(misc + 1024), *glo = ghi + kSums * kC, *eg = glo + kSums * kC;
+    uint32_t at = saddr(bars);
+    auto take = [&](int n) {
+        const uint32_t b = at;
+        at += 8 * n;
+        return b;
+    };
+    const uint32_t full = take(kStages), empty = take(kStages), gready = take(kSums), kready = take(2), sdone = take(2), afull = take(1),
+                   afree = take(1), pready = take(2), odone = take(2), ofree = take(2), sscaled = take(1), sbready = take(1),
+                   o1done = take(1), fin = take(1);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = static_cast<int>(blockIdx.x);
+    if (threadIdx.x == 0) {
+        prefetch_tmap(&p.tq);
+        prefetch_tmap(&p.tk);
+        prefetch_tmap(&p.tv);
+        stop = 0;
+        auto init = [&](uint32_t b, int n, int count) {
+            for (int i = 0; i < n; ++i) bar_init(b + 8 * i, static_cast<unsigned>(count));
+        };
+        init(full, kStages, 1);
+        init(empty, kStages, 1);
+        init(gready, kSums, 1);
+        init(kready, 2, 2);
+        init(sdone, 2, 1);
+        init(afull, 1, 1);
+        init(afree, 1, 4);
+        init(pready, 2, 4);
+        init(odone, 2, 1);
+        init(ofree, 2, 4);
+        init(sscaled, 1, 4);
+        init(sbready, 1, 4);
+        init(o1done, 1, 1);
+        init(fin, 1, 1);
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    }
+    if (p.flags & kFlagPdl) pdl_launch_dependents();
+    pdl_wait();
+    const Share sh = share_of(p, g, g == 0 && warp == 0);
+    if (sh.u1 <= sh.u0) return;
+    if (warp == 1) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(saddr(tmem_slot)), "r"(512)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    Cursor cursor(place_of(p, sh.u0), sh.u1 - sh.u0);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    const bool stall = (p.flags & kFlagTestStall) != 0;
+    const float nan = __int_as_float(0x7fc00000);
+    const int total = sh.u1 - sh.u0;
+    const int q = warp & 3;
+    const uint32_t quarter = static_cast<uint32_t>(32 * q) << 16;
+    int issued = 0;
+    Chunk c;
+
+    if (warp == 0) {
+        // -------------------------------------------------------------------- the copies
+        int slot = 0;
+        unsigned ph = 1;
+        for (int n = 0; cursor.next(p, c); ++n) {
+            if (n >= S && !all_wait(empty + 8 * slot, ph, &stop)) break;
+            const bool any = c.valid > 0;  // (of a sequence without tokens nothing is read)
+            if (!stall && any) issued = n + 1;
+            const uint32_t dst = saddr(base) + slot * stage, bar = full + 8 * slot;
+            if (elect()) {
+                if (any)
+                    bar_expect_tx(bar, static_cast<unsigned>(stage));
+                else
+                    bar_arrive(bar);
+                if (!stall && any) {
+                    const int hk = c.h / p.share;
+                    for (int i = 0; i < kKParts; ++i) tma_3d(dst + i * kPart, &p.tq, 64 * i, c.t0, hk, bar);
+                    for (int i = 0; i < kKParts; ++i) tma_3d(dst + kKeys + i * kPart, &p.tk, 64 * i, c.t0, hk, bar);
+                    for (int i = 0; i < vparts; ++i) tma_3d(dst + 2 * kKeys + i * kPart, &p.tv, 64 * i, c.t0, c.h, bar);
+                }
+            }
+            __syncwarp();
+            if (++slot == S) {
+                slot = 0;
+                ph ^= 1;
+            }
+        }
+    } else if (warp == 1) {
+        // ------------------------------------------------------------------ the products
+        constexpr uint32_t kIdA = idesc_of(64, 64, false, false), kIdO1 = idesc_of(128, 64, false, false),
+                           kIdO2 = idesc_of(128, 64, true, false), kIdS = idesc_of(128, DK, true, true);
+        const uint32_t d = alike(static_cast<int>(tmem));
+        int slot = 0, aslot = 0;  // of the current chunk, of the next A
+        unsigned aph = 0;
+        bool ok = true;
+        auto scores = [&](int n) {
+            ok = all_wait(full + 8 * aslot, aph, &stop) && (n == 0 || all_wait(afree, (n - 1) & 1, &stop));
+            if (!ok) return;
+            tc_fence_after();
+            if (elect()) {
+                const uint32_t st = saddr(base) + aslot * stage;
+#pragma unroll
+                for (int i = 0; i < kKParts; ++i)
+#pragma unroll
+                    for (int kk = 0; kk < 4; ++kk)
+                        mma(d + kA, tc05::sw128_desc(st + i * kPart) + ((32 * kk) >> 4),
+                            tc05::sw128_desc(st + kKeys + i * kPart) + ((32 * kk) >> 4), kIdA, i != 0 || kk != 0);
+                mma_commit(afull);
+            }
+            __syncwarp();
+            if (++aslot == S) {
+                aslot = 0;
+                aph ^= 1;
+            }
+        };
+        scores(0);
+        for (int n = 0; ok && n < total; ++n) {
+            const uint32_t st = saddr(base) + slot * stage, o = d + kO + 128 * (n & 1);
+            // the state's chain first
+            if (!(ok = all_wait(kready + 8 * (n & 1), (n >> 1) & 1, &stop) && all_wait(sscaled, n & 1, &stop))) break;
+            tc_fence_after();
+            if (elect()) {
+                const uint64_t a = mn_desc(st + 2 * kKeys), b = mn_desc(saddr(keys) + (n & 1) * 2 * kKeys);
+#pragma unroll
+                for (int part = 0; part < 2; ++part)
+#pragma unroll
+                    for (int kk = 0; kk < kC / 16; ++kk)
+                        mma(d + kState, a + kk * (2048 >> 4), b + ((part * kKeys) >> 4) + kk * (2048 >> 4), kIdS, true);
+                mma_commit(sdone + 8 * (n & 1));
+            }
+            __syncwarp();
+            if (!(ok = all_wait(sbready, n & 1, &stop) && (n < 2 || all_wait(ofree + 8 * (n & 1), ((n >> 1) - 1) & 1, &stop)))) break;
+            tc_fence_after();
+            if (elect()) {
+#pragma unroll
+                for (int i = 0; i < kKParts; ++i)
+#pragma unroll
+                    for (int kk = 0; kk < 4; ++kk)
+                        mma_ts(o, d + kSb + 32 * i + 8 * kk, tc05::sw128_desc(st + i * kPart) + ((32 * kk) >> 4), kIdO1, i != 0 || kk != 0);
+                mma_commit(o1done);
+            }
+            __syncwarp();
+            if (n + 1 < total) scores(n + 1);
+            if (!ok || !(ok = all_wait(pready + 8 * (n & 1), (n >> 1) & 1, &stop))) break;
+            tc_fence_after();
+            if (elect()) {
+                const uint64_t a = mn_desc(st + 2 * kKeys), b = tc05::sw128_desc(saddr(ps) + (n & 1) * kPart);
+#pragma unroll
+                for (int kk = 0; kk < kC / 16; ++kk) mma(o + 64, a + kk * (2048 >> 4), b + ((32 * kk) >> 4), kIdO2, kk != 0);
+                mma_commit(odone + 8 * (n & 1));
+                mma_commit(empty + 8 * slot);
+            }
+            __syncwarp();
+            if (++slot == S) slot = 0;
+        }
+        finish(fin, &stop);
+    } else if (warp < 4) {
+        // ------------------------------------------------------ keys, and the sums of decays
+        const int w = warp - 2;
+        Cursor ahead = cursor;
+        Chunk nc;
+        Decays next{0.0f, 0.0f};
+        if (ahead.next(p, nc)) next = load_g(p, nc);
+        int slot = 0;
+        unsigned ph = 0;
+        bool ok = true;
+        for (int n = 0; cursor.next(p, c); ++n) {
+            const Decays now = next;
+            if (ahead.next(p, nc)) next = load_g(p, nc);
+            Pair a, b, all;
+            sums_of(now, a, b, all);
+            if (!(ok = n < 2 || all_wait(sdone + 8 * (n & 1), ((n >> 1) - 1) & 1, &stop))) break;
+            if (w == 0) {
+                const int to = (n & (kSums - 1)) * kC + 2 * lane;
+                *reinterpret_cast<float2 *>(&ghi[to]) = make_float2(a.hi, b.hi);
+                *reinterpret_cast<float2 *>(&glo[to]) = make_float2(a.lo, b.lo);
+                *reinterpret_cast<float2 *>(&eg[to]) = make_float2(exp2f(a.hi + a.lo), exp2f(b.hi + b.lo));
+                if (lane == 0) all_e[n & 3] = exp2f(all.hi + all.lo);
+                __syncwarp();
+                if (lane == 0) bar_arrive(gready + 8 * (n & (kSums - 1)));
+            }
+            if (!(ok = all_wait(full + 8 * slot, ph, &stop))) break;
+            uint8_t *out = keys + (n & 1) * 2 * kKeys, *st = base + slot * stage;
+            scale_keys<2, DK>(st + kKeys, out, out + kKeys, w, c.valid, exp2f(less(all, a)), exp2f(less(all, b)));
+            if (c.valid < kC) clear_values<2>(st + 2 * kKeys, vparts, w, c.valid);
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            __syncwarp();
+            if (lane == 0) bar_arrive(kready + 8 * (n & 1));
+            if (++slot == S) {
+                slot = 0;
+                ph ^= 1;
+            }
+        }
+    } else if (warp < 8) {
+        // -------------------------------------------------------------------- the state
+        const int dv = 32 * q + lane;
+        const bool mine = dv < p.Dv;
+        bool ok = true;
+        for (int n = 0; cursor.next(p, c); ++n) {
+            if (ok) ok = all_wait(gready + 8 * (n & (kSums - 1)), (n / kSums) & 1, &stop);
+            if (ok && !c.head) ok = all_wait(sdone + 8 * ((n - 1) & 1), ((n - 1) >> 1) & 1, &stop);
+            const float *from = nullptr;
+            if (c.head) {
+                const long long slot = p.slots[c.b];
+                if (!c.first)
+                    from = state_of(p, g - 1);
+                else if (slot >= 0 && slot < p.pool && !(p.fresh && p.fresh[c.b])) {
+                    // a sequence cut by the share's end begins with the second kernel's copy
+                    from = p.state + slot * p.s_slot + c.h * p.s_head;
+                    if (!c.tail) {
+                        const int a = p.cu[c.b], chunks = (p.cu[c.b + 1] - a + kC - 1) / kC;
+                        if (chunks > total - n) from = begin_state(p, g);
+                    }
+                }
+            }
+            if (ok) {
+                tc_fence_after();
+                const float e = all_e[n & 3];
+                uint32_t sb[DK / 2];
+#pragma unroll
+                for (int col = 0; col < DK; col += 16) {
+                    uint32_t v[16];
+                    if (c.head) {
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) v[i] = from && mine ? __float_as_uint(from[(col + i) * p.Dv + dv]) : 0u;
+                    } else {
+                        tc05::tmem_ld16(tmem + quarter + kState + col, v);
+                    }
+#pragma unroll
+                    for (int i = 0; i < 16; i += 2) sb[(col + i) / 2] = bf16x2(__uint_as_float(v[i]), __uint_as_float(v[i + 1]));
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * e);
+                    tmem_st16(tmem + quarter + kState + col, v);
+                }
+                asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) bar_arrive(sscaled);
+                ok = n == 0 || all_wait(o1done, (n - 1) & 1, &stop);
+                if (ok) {
+                    tc_fence_after();
+#pragma unroll
+                    for (int col = 0; col < DK / 2; col += 16) {
+                        uint32_t v[16];
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) v[i] = sb[col + i];
+                        tmem_st16(tmem + quarter + kSb + col, v);
+                    }
+                    asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+                    tc_fence_before();
+                }
+                __syncwarp();
+                if (lane == 0) bar_arrive(sbready);
+            }
+            if (c.tail) {
+                // the sequence's last state
+                if (ok) ok = all_wait(sdone + 8 * (n & 1), (n >> 1) & 1, &stop);
+                const Seq s = seq_of(p, c.b);
+                const bool fresh = p.fresh && p.fresh[c.b];
+                if (s.slot >= 0 && (s.len > 0 || fresh)) {
+                    float *to = p.state + s.slot * p.s_slot + c.h * p.s_head + dv;
+                    tc_fence_after();
+                    for (int col = 0; col < DK; col += 16) {
+                        uint32_t v[16];
+                        if (ok) tc05::tmem_ld16(tmem + quarter + kState + col, v);
+                        if (mine)
+#pragma unroll
+                            for (int i = 0; i < 16; ++i) to[(col + i) * p.Dv] = ok ? __uint_as_float(v[i]) : nan;
+                    }
+                    tc_fence_before();
+                }
+            }
+        }
+    } else if (warp < 12) {
+        // ------------------------------------------------------------- the decays of a chunk
+        bool ok = true;
+        for (int n = 0; cursor.next(p, c); ++n) {
+            if (!(ok = all_wait(gready + 8 * (n & (kSums - 1)), (n / kSums) & 1, &stop) && all_wait(afull, n & 1, &stop))) break;
+            tc_fence_after();
+            uint32_t r[32];
+            tmem_ld_a(tmem + quarter + kA, r);
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) bar_arrive(afree);
+            const int i0 = 16 * q + (lane >> 2), j0 = 2 * (lane & 3);
+            const float *hi = ghi + (n & (kSums - 1)) * kC, *lo = glo + (n & (kSums - 1)) * kC;
+            const float h0 = hi[i0], l0 = lo[i0], h1 = hi[i0 + 8], l1 = lo[i0 + 8];
+            if (!(ok = n < 2 || all_wait(odone + 8 * (n & 1), ((n >> 1) - 1) & 1, &stop))) break;
+            uint8_t *row = ps + (n & 1) * kPart + i0 * 128;
+#pragma unroll
+            for (int t = 0; t < 8; ++t) {
+                const int j = 8 * t + j0;
+                const float2 hj = *reinterpret_cast<const float2 *>(&hi[j]), lj = *reinterpret_cast<const float2 *>(&lo[j]);
+                float w[4];
+                w[0] = ex2((h0 - hj.x) + (l0 - lj.x)) * __uint_as_float(r[4 * t]);
+                w[1] = ex2((h0 - hj.y) + (l0 - lj.y)) * __uint_as_float(r[4 * t + 1]);
+                w[2] = ex2((h1 - hj.x) + (l1 - lj.x)) * __uint_as_float(r[4 * t + 2]);
+                w[3] = ex2((h1 - hj.y) + (l1 - lj.y)) * __uint_as_float(r[4 * t + 3]);
+                // later tokens, and rows behind the chunk's
+                if (j > i0 || i0 >= c.valid) w[0] = 0.0f;
+                if (j + 1 > i0 || i0 >= c.valid) w[1] = 0.0f;
+                if (j > i0 + 8 || i0 + 8 >= c.valid) w[2] = 0.0f;
+                if (j + 1 > i0 + 8 || i0 + 8 >= c.valid) w[3] = 0.0f;
+                const int to = ((t ^ (lane >> 2)) << 4) + 2 * j0;  // i0 % 8 = lane / 4
+                *reinterpret_cast<uint32_t *>(row + to) = bf16x2(w[0], w[1]);
+                *reinterpret_cast<uint32_t *>(row + 8 * 128 + to) = bf16x2(w[2], w[3]);
+            }
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            __syncwarp();
+            if (lane == 0) bar_arrive(pready + 8 * (n & 1));
+        }
+    } else {
+        // ------------------------------------------------------------------- the outputs
+        const int dv = 32 * q + lane;
+        bool ok = true;
+        for (int n = 0; cursor.next(p, c); ++n) {
+            if (ok) ok = all_wait(odone + 8 * (n & 1), (n >> 1) & 1, &stop);
+            if (ok) tc_fence_after();
+            uint16_t *to = p.out + static_cast<long long>(c.t0) * p.o_token + c.h * p.o_head + dv;
+            const float *e = eg + (n & (kSums - 1)) * kC;
+#pragma unroll 1
+            for (int i = 0; i < kC; i += 16) {
+                if (i >= c.valid) break;
+                uint32_t a[16], b[16];
+                if (ok) {
+                    tc05::tmem_ld16(tmem + quarter + kO + 128 * (n & 1) + i, a);
+                    tc05::tmem_ld16(tmem + quarter + kO + 128 * (n & 1) + 64 + i, b);
+                }
+                if (dv < p.Dv)
+#pragma unroll
+                    for (int j = 0; j < 16; ++j)
+                        if (i + j < c.valid) {
+                            const float x = p.scale * fmaf(e[i + j], __uint_as_float(a[j]), __uint_as_float(b[j]));
+                            to[(i + j) * p.o_token] = f32_to_bf16_rn(ok ? x : nan);
+                        }
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) bar_arrive(ofree + 8 * (n & 1));
+        }
+    }
+    __syncwarp();
+    // after a stop: the copies issued have landed before the shared memory goes
+    if (lane == 0 && *reinterpret_cast<volatile int *>(&stop) && warp == 0)
+        for (int i = max(0, issued - S); i < issued; ++i) landed(full + 8 * (i % S), (i / S) & 1);
+    tc_fence_before();
+    __syncthreads();
+    if (threadIdx.x == 32 && stop) atomicOr(p.err, 1);
+    if (warp == 1) {
+        tc_fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512) : "memory");
+    }
+}
+
+int stages_of(int dk, int dv, bool with_q) {
+    const int room = static_cast<int>(kMaxSmemOptin) - 1024 - (with_q ? out_fixed(dk) : state_fixed(dk));
+    return std::min(kStages, room / chunk_bytes(dk, dv, with_q));
+}
+
+// Shares of a line, at most: one an SM, each of kFew chunks or more.
+int groups_of(const sgemm_linear_attention_t &a, int sms) {
+    const long long units = (a.N / kC + 2 * a.B) * a.Hv;
+    return static_cast<int>(std::max(1LL, std::min<long long>(sms, (units + kFew - 1) / kFew)));
+}
+
+sgemm_status_t check_sizes(const sgemm_linear_attention_t &a) {
+    if (a.flags & ~(kDecodeFlags | SGEMM_FLAG_TEST_STALL)) return SGEMM_ERR_INVALID_ARG;
+    if (a.N < 0 || a.B < 0 || a.Hk < 1 || a.Hv < a.Hk || a.Hv % a.Hk || a.Hv > 1024) return SGEMM_ERR_INVALID_ARG;
+    if ((a.Dk != 64 && a.Dk != 128) || (a.Dv != 64 && a.Dv != 128)) return SGEMM_ERR_UNSUPPORTED_SHAPE;
+    if (a.N >= (1LL << 31) / a.Hv || a.B >= (1LL << 28) / a.Hv) return SGEMM_ERR_UNSUPPORTED_SHAPE;
+    return SGEMM_OK;
+}
+
+long long scratch(const sgemm_linear_attention_t &a, int groups) {
+    return groups > 1 ? (groups + 3) / 4 * 16 + 2LL * groups * a.Dk * a.Dv * 4 : 0;
+}
+
+bool allow(const void *fn, std::atomic<unsigned long long> &done) {
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return false;
+    const unsigned long long bit = dev < 64 ? 1ULL << dev : 0ULL;
+    if (!(done.load(std::memory_order_acquire) & bit)) {
+        if (allow_max_dynamic_smem(fn) != cudaSuccess) return false;
+        done.fetch_or(bit, std::memory_order_release);
+    }
+    return true;
+}
+
+}  // namespace linear
+}  // namespace sk
+
+extern "C" sgemm_status_t sgemm_linear_attention_workspace(const sgemm_linear_attention_t *a, long long *bytes) {
+    using namespace sk;
+    using namespace sk::linear;
+    if (!a || !bytes) return SGEMM_ERR_INVALID_ARG;
+    *bytes = 0;
+    sgemm_status_t st = check_sizes(*a);
+    if (st != SGEMM_OK || a->B == 0) return st;
+    int sms = 0, *err = nullptr;
+    st = device_ready(&sms, &err);
+    if (st != SGEMM_OK) return st;
+    *bytes = scratch(*a, groups_of(*a, sms));
+    return SGEMM_OK;
+}
+
+extern "C" sgemm_status_t sgemm_bf16_linear_attention(const sgemm_linear_attention_t *a, sgemm_stream_t stream) {
+    using namespace sk;
+    using namespace sk::linear;
+    if (!a) return SGEMM_ERR_INVALID_ARG;
+    sgemm_status_t st = check_sizes(*a);
+    if (st != SGEMM_OK) return st;
+    if (!std::isfinite(a->scale)) return SGEMM_ERR_INVALID_ARG;
+    if (a->B == 0) return SGEMM_OK;
+    if (!a->slots || !a->cu || (a->pool > 0 && !a->state) || (a->N > 0 && (!a->q || !a->k || !a->v || !a->g || !a->out)) || a->pool < 0 ||
+        a->pool >= (1LL << 40) || a->workspace_bytes < 0)
+        return SGEMM_ERR_INVALID_ARG;
+    const LinearView io{a->q, a->k, a->v, a->g, a->state, a->out, a->q_token, a->q_head, a->k_token, a->k_head, a->v_token,
+                        a->v_head, a->g_token, a->g_head, a->s_slot, a->s_head, a->o_token, a->o_head, a->N, a->pool, a->Hk,
+                        a->Hv, a->Dk, a->Dv};
+    st = check_linear(io);
+    if (st != SGEMM_OK) return st;
+    // the copies' strides
+    if (a->N > 1 && (a->q_token < 8 || a->k_token < 8 || a->v_token < 8)) return SGEMM_ERR_INVALID_ARG;
+    if ((a->Hk > 1 && (a->q_head < 8 || a->k_head < 8)) || (a->Hv > 1 && a->v_head < 8)) return SGEMM_ERR_INVALID_ARG;
+    if (!aligned(a->slots, 8) || !aligned(a->cu, 4) || !aligned(a->fresh, 4) || !aligned(a->workspace, 16)) return SGEMM_ERR_MISALIGNED;
+    if (linear_touches(io, a->slots, 8 * a->B) || linear_touches(io, a->cu, 4 * a->B + 4) || linear_touches(io, a->fresh, 4 * a->B))
+        return SGEMM_ERR_INVALID_ARG;
+    LinearParams p;
+    std::memset(&p, 0, sizeof(p));
+    int sms = 0;
+    st = device_ready(&sms, &p.err);
+    if (st != SGEMM_OK) return st;
+    p.groups = groups_of(*a, sms);
+    const long long need = scratch(*a, p.groups);
+    if (need > 0 && (!a->workspace || a->workspace_bytes < need)) return SGEMM_ERR_NO_WORKSPACE;
+    if (need > 0) {
+        auto meets = [&](const void *b, long long bytes) { return b && rows_overlap(a->workspace, need, 0, b, bytes, 0, 1); };
+        auto span = [&](long long tok, int heads, long long head, long long w) { return (a->N - 1) * tok + (heads - 1) * head + w; };
+        if (linear_touches(io, a->workspace, need) || meets(a->q, 2 * span(a->q_token, a->Hk, a->q_head, a->Dk)) ||
+            meets(a->k, 2 * span(a->k_token, a->Hk, a->k_head, a->Dk)) || meets(a->v, 2 * span(a->v_token, a->Hv, a->v_head, a->Dv)) ||
+            meets(a->g, 4 * span(a->g_token, a->Hv, a->g_head, 1)) || meets(a->slots, 8 * a->B) || meets(a->cu, 4 * a->B + 4) ||
+            meets(a->fresh, 4 * a->B))
+            return SGEMM_ERR_INVALID_ARG;
+    }
+    // without tokens nothing is copied, and any address will do for the maps
+    const long long rows = std::max(1LL, a->N);
+    const void *none = reinterpret_cast<const void *>(4096);
+    const CUtensorMapL2promotion promote = CU_TENSOR_MAP_L2_PROMOTION_L2_256B;
+    if (!map_3d(&p.tq, a->N ? a->q : none, a->Dk, rows, a->Hk, a->q_token, a->q_head, kC, promote) ||
+        !map_3d(&p.tk, a->N ? a->k : none, a->Dk, rows, a->Hk, a->k_token, a->k_head, kC, promote) ||
+        !map_3d(&p.tv, a->N ? a->v : none, a->Dv, rows, a->Hv, a->v_token, a->v_head, kC, promote))
+        return SGEMM_ERR_CUDA;
+    p.g = a->g;
+    p.state = a->state;
+    p.slots = a->slots;
+    p.cu = a->cu;
+    p.fresh = a->fresh;
+    p.out = a->out;
+    p.ws = static_cast<float *>(a->workspace);
+    p.g_token = a->g_token;
+    p.g_head = a->g_head;
+    p.s_slot = a->s_slot;
+    p.s_head = a->s_head;
+    p.o_token = a->o_token;
+    p.o_head = a->o_head;
+    p.pool = a->pool;
+    p.N = a->N;
+    p.B = static_cast<int>(a->B);
+    p.Hv = a->Hv;
+    p.share = a->Hv / a->Hk;
+    p.Dk = a->Dk;
+    p.Dv = a->Dv;
+    p.scale = a->scale;
+    p.flags = static_cast<int>(a->flags);
+    const cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
+    const bool wide = a->Dk == 128;
+    static std::atomic<unsigned long long> done[4];
+    if (p.groups > 1) {
+        const void *fn = wide ? reinterpret_cast<const void *>(&linear_states_kernel<128>) : reinterpret_cast<const void *>(&linear_states_kernel<64>);
+        if (!allow(fn, done[wide])) return SGEMM_ERR_CUDA;
+        p.stages = stages_of(a->Dk, a->Dv, false);
+        const size_t smem = 1024 + static_cast<size_t>(p.stages) * chunk_bytes(a->Dk, a->Dv, false) + state_fixed(a->Dk);
+        if (launch(fn, dim3(static_cast<unsigned>(p.groups)), dim3(kStateThreads), smem, cs, &p) != cudaSuccess) return SGEMM_ERR_CUDA;
+        const unsigned slices = static_cast<unsigned>((a->Dk * a->Dv / 4 + kJoinThreads - 1) / kJoinThreads);
+        if (launch(reinterpret_cast<const void *>(&linear_join_kernel), dim3(static_cast<unsigned>(p.groups), slices), dim3(kJoinThreads),
+                   0, cs, &p) != cudaSuccess)
+            return SGEMM_ERR_CUDA;
+    }
+    const void *fn = wide ? reinterpret_cast<const void *>(&linear_outputs_kernel<128>) : reinterpret_cast<const void *>(&linear_outputs_kernel<64>);
+    if (!allow(fn, done[2 + wide])) return SGEMM_ERR_CUDA;
+    p.stages = stages_of(a->Dk, a->Dv, true);
+    const size_t smem = 1024 + static_cast<size_t>(p.stages) * chunk_bytes(a->Dk, a->Dv, true) + out_fixed(a->Dk);
+    if (launch(fn, dim3(static_cast<unsigned>(p.groups)), dim3(kOutThreads), smem, cs, &p) != cudaSuccess) return SGEMM_ERR_CUDA;
+    return SGEMM_OK;
+}

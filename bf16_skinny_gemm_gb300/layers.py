@@ -2,7 +2,8 @@
 
 - :func:`sgemm_bf16_moe_route`, :func:`sgemm_bf16_moe_experts`: a mixture of experts for a few tokens,
 - :func:`sgemm_bf16_latent_tree_attention`: latent attention for a tree of drafted tokens,
-- :func:`sgemm_bf16_linear_step`: linear attention with a decay for each head, one token a sequence.
+- :func:`sgemm_bf16_linear_step`, :func:`sgemm_bf16_linear_attention`: linear attention with a decay
+  for each head, one token a sequence and whole prompts.
 
 As in ``decode``: the functions check and marshal, every step of the computation runs in the
 library's CUDA kernels, outputs and scratch may be given (nothing is allocated then), tensors are
@@ -20,8 +21,8 @@ from .decode import _ATTN, _fn, _on_current_device, _shape, _strides, sgemm_late
 
 __all__ = [
     "sgemm_bf16_moe_route", "sgemm_bf16_moe_experts", "sgemm_moe_experts_workspace",
-    "sgemm_bf16_latent_tree_attention", "sgemm_bf16_linear_step",
-    "SGEMM_ROUTE_SOFTMAX", "SGEMM_ROUTE_SIGMOID", "MOE_MAX_TOKENS",
+    "sgemm_bf16_latent_tree_attention", "sgemm_bf16_linear_step", "sgemm_bf16_linear_attention",
+    "sgemm_linear_attention_workspace", "SGEMM_ROUTE_SOFTMAX", "SGEMM_ROUTE_SIGMOID", "MOE_MAX_TOKENS",
 ]
 
 SGEMM_ROUTE_SOFTMAX = 0
@@ -32,6 +33,7 @@ MOE_MAX_TOKENS = 128
 _ROUTE = struct.Struct("<5Q5q5ifIi")     # sgemm_moe_route_t
 _EXPERTS = struct.Struct("<7Q9q5iI")     # sgemm_moe_experts_t
 _STEP = struct.Struct("<7Q14q4ifI")      # sgemm_linear_step_t
+_LINEAR = struct.Struct("<10Q16q4ifI")   # sgemm_linear_attention_t
 
 _BF16 = torch.bfloat16
 _SCORING = {"softmax": SGEMM_ROUTE_SOFTMAX, "sigmoid": SGEMM_ROUTE_SIGMOID}
@@ -255,4 +257,46 @@ def sgemm_bf16_linear_step(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g:
     _call("sgemm_bf16_linear_step", _STEP.pack(
         q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), state.data_ptr(), slots.data_ptr(), out.data_ptr(),
         *s, B, pool, Hk, Hv, Dk, Dv, scale, flags), q, stream)
+    return out
+
+
+def sgemm_linear_attention_workspace(tokens: int, batch: int, heads: int, key_width: int, value_width: int) -> int:
+    """Bytes of scratch :func:`sgemm_bf16_linear_attention` needs for ``tokens`` tokens in ``batch``
+    sequences with ``heads`` value heads."""
+    n = ctypes.c_longlong(0)
+    args = _LINEAR.pack(*([0] * 22), tokens, batch, 0, 0, 1, heads, key_width, value_width, 1.0, 0)
+    status = _fn("sgemm_linear_attention_workspace")(args, ctypes.addressof(n))
+    if status:
+        raise SgemmError(status, "sgemm_linear_attention_workspace")
+    return n.value
+
+
+def sgemm_bf16_linear_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Tensor, state: torch.Tensor,
+                                slots: torch.Tensor, cu: torch.Tensor, scale: float = 1.0,
+                                fresh: torch.Tensor | None = None, out: torch.Tensor | None = None,
+                                workspace: torch.Tensor | None = None, flags: int = 0, stream=None) -> torch.Tensor:
+    """Whole sequences through linear attention with a decay for each head, in chunks; returns out.
+
+    q, k: BF16 [N, Hk, Dk]; v, out: BF16 [N, Hv, Dv]; g: FP32 [N, Hv]; state: FP32 [slots, Hv, Dk, Dv],
+    as for :func:`sgemm_bf16_linear_step`, whose recurrence this is.  Sequence b has the tokens
+    ``cu[b] .. cu[b + 1] - 1`` (cu: int32 [B + 1]), starts from ``state[slots[b]]`` (from zeros where
+    ``fresh[b]``, int32 [B], is not 0) and leaves its last state there (slots: int64 [B]; negative:
+    from zeros, not kept).  ``workspace``: scratch on the device
+    (:func:`sgemm_linear_attention_workspace` bytes; allocated for the call where None)."""
+    (N, pool, Hk, Hv, Dk, Dv), s, out = _linear(q, k, v, g, state, out, stream)
+    B = _shape(slots, "slots", torch.int64, 1)[0]
+    _strides(slots, "slots", torch.int64, (B,))
+    _strides(cu, "cu", torch.int32, (B + 1,))
+    pf = 0
+    if fresh is not None:
+        _strides(fresh, "fresh", torch.int32, (B,))
+        pf = fresh.data_ptr()
+    _on_current_device(q=q, k=k, v=v, g=g, state=state, slots=slots, cu=cu, fresh=fresh, out=out)
+    if B == 0:
+        return out
+    need = 0 if workspace is not None else sgemm_linear_attention_workspace(N, B, Hv, Dk, Dv)
+    workspace, pws, nws = _scratch(workspace, need, q.device, stream)
+    _call("sgemm_bf16_linear_attention", _LINEAR.pack(
+        q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), state.data_ptr(), slots.data_ptr(), cu.data_ptr(), pf,
+        out.data_ptr(), pws, *s, N, B, pool, nws, Hk, Hv, Dk, Dv, scale, flags), q, stream)
     return out

@@ -6,6 +6,7 @@
  *   sgemm_bf16_moe_experts            the chosen experts' products
  *   sgemm_bf16_latent_tree_attention  latent attention for a tree of drafted tokens
  *   sgemm_bf16_linear_step            linear attention with decays, one token a sequence
+ *   sgemm_bf16_linear_attention       the same for prompts, in chunks
  *
  * The conventions are those of sgemm_decode.h: device pointers owned by the
  * caller on the current device, raw BF16 bits, asynchronous work on `stream`,
@@ -155,6 +156,53 @@ typedef struct {
 } sgemm_linear_step_t;
 
 sgemm_status_t sgemm_bf16_linear_step(const sgemm_linear_step_t *args, sgemm_stream_t stream);
+
+/* The same recurrence over whole sequences: sequence b has the tokens (rows of q, k,
+ * v, g, out) cu[b] .. cu[b+1]-1, starts from state[slots[b]] (from zeros where
+ * fresh[b] is not 0, whatever the slot holds) and leaves its last state there.
+ * Computed in chunks of 64 tokens, with G_i = sum of g over the chunk's tokens up to i:
+ *     o_i = scale (exp(G_i) q_i^T S + sum_{j <= i} exp(G_i - G_j) (q_i . k_j) v_j)
+ *     S'  = exp(G) S + sum_j exp(G - G_j) k_j v_j^T
+ * Sums and states are FP32.  Rounded to BF16, as operands of products: the weights
+ * exp(G_i - G_j) (q_i . k_j), and S in the outputs; decayed keys are pairs of BF16 values
+ * whose sum is off by 2^-17, so that the states keep FP32's accuracy nearly.
+ * - slots[b] < 0: starts from zeros, and the last state is not kept.  A slot past
+ *   the pool is treated the same and sets bit 1 of the device error word.
+ * - A sequence without tokens leaves its slot as it is (zeros where fresh).
+ * - cu rises from 0 or more to at most N; where it does not, the sequence is taken
+ *   as one without tokens whose slot stays as it is, and bit 1 of the error word is
+ *   set.  Rows of out before cu[0] and from cu[B] on are left as they are.
+ * - Two sequences of one call must not name the same slot.
+ * - g <= 0 is what this is made for.  exp(g) may exceed 1 as long as no exp(G_i - G_j)
+ *   overflows; g = -inf drops what came before.  An infinity or a NaN in q, k or v
+ *   reaches results of its own chunk of 64 tokens and later ones of its
+ *   sequence and head only.
+ * - Sizes, alignments and strides as for sgemm_bf16_linear_step; N < 2^31 / Hv.
+ * - workspace: device scratch of at least sgemm_linear_attention_workspace bytes
+ *   (16-byte aligned; may be NULL where that is 0), as for the other operators.
+ * - Waits inside the kernels are bounded, as in sgemm_bf16_moe_experts. */
+typedef struct {
+    const sgemm_bf16_t *q;   /* [N, Hk, Dk], strides q_token, q_head */
+    const sgemm_bf16_t *k;   /* [N, Hk, Dk], strides k_token, k_head */
+    const sgemm_bf16_t *v;   /* [N, Hv, Dv], strides v_token, v_head */
+    const float *g;          /* [N, Hv], strides g_token, g_head */
+    float *state;            /* [slots, Hv, Dk, Dv], strides s_slot, s_head */
+    const long long *slots;  /* [B] */
+    const int *cu;           /* [B + 1] */
+    const int *fresh;        /* [B] or NULL: none is */
+    sgemm_bf16_t *out;       /* [N, Hv, Dv], strides o_token, o_head */
+    void *workspace;
+    long long q_token, q_head, k_token, k_head, v_token, v_head, g_token, g_head;
+    long long s_slot, s_head, o_token, o_head;
+    long long N, B, pool, workspace_bytes;
+    int Hk, Hv, Dk, Dv;
+    float scale;
+    unsigned flags;
+} sgemm_linear_attention_t;
+
+sgemm_status_t sgemm_linear_attention_workspace(const sgemm_linear_attention_t *args, long long *bytes);
+
+sgemm_status_t sgemm_bf16_linear_attention(const sgemm_linear_attention_t *args, sgemm_stream_t stream);
 
 #ifdef __cplusplus
 }

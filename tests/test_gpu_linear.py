@@ -155,3 +155,201 @@ def test_step_captured():
     want, last, ob, sb = expect(*three, state, slots, [3] * 3, 1.0, False)
     D.check(out, want[2::3], ob[2::3], "out")
     D.check(d[4], last, sb + 1e-300, "state")
+
+
+# ----------------------------------------------------------------------------------------- prompts
+def prompt(q, k, v, g, state, slots, lens, scale=1.0, fresh=None, errors=0, cu=None, **kw):
+    s = state.to(DEV)
+    if cu is None:
+        cu = [sum(lens[:b]) for b in range(len(lens) + 1)]
+    out = sk.sgemm_bf16_linear_attention(
+        q.to(DEV), k.to(DEV), v.to(DEV), g.to(DEV), s, slots.to(DEV), torch.tensor(cu, dtype=torch.int32, device=DEV), scale,
+        fresh=None if fresh is None else torch.tensor(fresh, dtype=torch.int32, device=DEV), **kw)
+    torch.cuda.synchronize()
+    assert sk.sgemm_device_errors() == errors
+    return out, s
+
+
+def compare(lens, Hk, Hv, Dk=128, Dv=128, seed=0, scale=1.0, fresh=None, slowest=1000.0):
+    p = problem(lens, Hk, Hv, Dk, Dv, seed, slowest)
+    out, s = prompt(*p, lens, scale, fresh)
+    want, last, ob, sb = expect(*p, lens, scale, True, fresh)
+    D.check(out, want, ob, "out")
+    D.check(s, last, sb + 1e-300, "state")
+    return out, s
+
+
+@pytest.mark.parametrize("n", [1, 2, 15, 16, 63, 64, 65, 127, 128, 129, 191, 256, 300, 511, 1000])
+def test_lengths(n):
+    compare([n], 2, 2, seed=n)
+
+
+@pytest.mark.parametrize("Dk,Dv", [(128, 128), (64, 128), (128, 64), (64, 64)])
+@pytest.mark.parametrize("n", [1, 64, 100, 400])
+def test_widths(Dk, Dv, n):
+    compare([n], 3, 6, Dk, Dv, seed=n + Dk, scale=0.3)
+
+
+@pytest.mark.parametrize("Hk,Hv", [(1, 1), (1, 8), (2, 4), (5, 5), (16, 16), (4, 64)])
+def test_heads(Hk, Hv):
+    compare([150, 70], Hk, Hv, 64, 64, seed=Hk * 10 + Hv)
+
+
+@pytest.mark.parametrize("lens", [[1, 1, 1], [64, 64], [5, 700, 1, 128, 63], [0, 10, 0], [0, 0], [300] * 7, [2000, 3, 1]])
+def test_ragged(lens):
+    compare(lens, 2, 2, seed=sum(lens) + len(lens), fresh=[b % 2 for b in range(len(lens))])
+
+
+def test_many_sequences():
+    compare([1 + (37 * b * b) % 150 for b in range(90)], 1, 2, 64, 64, seed=3, fresh=[b % 3 == 0 for b in range(90)])
+
+
+@pytest.mark.parametrize("Hv", [1, 3])
+def test_long(Hv):
+    compare([9000], 1, Hv, 64, 64, seed=Hv, slowest=1e4)
+
+
+def test_decays():
+    """Fast and slow ones, none, all, and what passes single precision's range."""
+    p = problem([400], 1, 6, 128, 128, 4)
+    g = p[3]
+    g[:, 0] = 0.0
+    g[:, 1] = -100.0
+    g[::37, 2] = -INF
+    g[:, 3] = -1e-6
+    g[:, 4] = -3e38
+    g[150:250, 5] = 0.01
+    out, s = prompt(*p, [400])
+    want, last, ob, sb = expect(*p, [400], 1.0, True)
+    D.check(out, want, ob, "out")
+    D.check(s, last, sb + 1e-300, "state")
+
+
+def test_slots():
+    """No slot: from zeros and not kept; fresh: from zeros whatever the slot holds."""
+    lens = [70, 200, 5, 64]
+    p = problem(lens, 2, 4, 128, 128, 5)
+    p[5][1] = -1
+    p[4][p[5][2]] = NAN
+    out, s = prompt(*p, lens, fresh=[0, 0, 1, 0])
+    state = p[4].clone()
+    state[p[5][2]] = 0
+    want, last, ob, sb = expect(*p[:4], state, p[5], lens, 1.0, True)
+    D.check(out, want, ob, "out")
+    D.check(s, last, sb + 1e-300, "state")
+    p[5][3] = 99
+    prompt(*p, lens, errors=2)
+
+
+def test_sequences_without_tokens_keep_their_slots():
+    q, k, v, g, state, slots = problem([50, 60], 2, 2, 64, 128, 6, pool=6)
+    slots = torch.tensor([3, 0, 5, 1])
+    cu = [0, 50, 50, 50, 110]
+    out, s = prompt(q, k, v, g, state, slots, None, cu=cu, fresh=[0, 0, 1, 1])
+    assert torch.equal(s[0].cpu(), state[0]) and torch.all(s[5] == 0)
+    assert torch.equal(s[[2, 4]].cpu(), state[[2, 4]])
+    want, last, ob, sb = expect(q, k, v, g, state, torch.tensor([3, 1]), [50, 60], 1.0, True, [0, 1])
+    D.check(out, want, ob, "out")
+    D.check(s[[1, 3]], last[[1, 3]], sb[[1, 3]], "state")
+
+
+def test_offsets_that_fall_are_skipped():
+    q, k, v, g, state, slots = problem([50, 60], 2, 2, 64, 64, 7, pool=6)
+    for cu in ([0, 50, 40, 110], [0, 50, 111, 110], [-1, 50, 50, 110]):
+        out = torch.full((110, 2, 64), 9.0, dtype=torch.bfloat16, device=DEV)
+        _, s = prompt(q, k, v, g, state, torch.tensor([2, 4, 1]), None, cu=cu, errors=2, out=out)
+        bad = [b for b in range(3) if not 0 <= cu[b] <= cu[b + 1] <= 110]
+        for b in bad:
+            assert torch.equal(s[[2, 4, 1][b]].cpu(), state[[2, 4, 1][b]])
+
+
+def test_rows_outside_the_sequences_are_left_alone():
+    q, k, v, g, state, slots = problem([30, 100, 40], 2, 2, 128, 128, 8)
+    for t in (q, k, v, g):
+        t[:30], t[130:] = NAN, NAN
+    out = torch.full((170, 2, 128), 9.0, dtype=torch.bfloat16, device=DEV)
+    _, s = prompt(q, k, v, g, state, slots[1:2], None, cu=[30, 130], out=out)
+    assert torch.all(out[:30] == 9) and torch.all(out[130:] == 9)
+    r = slice(30, 130)
+    want, last, ob, sb = expect(q[r], k[r], v[r], g[r], state, slots[1:2], [100], 1.0, True)
+    D.check(out[r], want, ob, "out")
+    D.check(s, last, sb + 1e-300, "state")
+
+
+def test_a_neighbour_of_nan_reaches_no_other_sequence():
+    lens = [100, 77, 200]
+    p = problem(lens, 2, 4, 128, 128, 9)
+    clean, cs = prompt(*p, lens)
+    for t in p[:4]:
+        t[100:177] = NAN
+    out, s = prompt(*p, lens)
+    rows = [*range(100), *range(177, 377)]
+    assert torch.equal(out[rows], clean[rows]) and torch.equal(s[p[5][[0, 2]]], cs[p[5][[0, 2]]])
+
+
+def test_strided():
+    lens = [90, 75]
+    p = problem(lens, 3, 6, 128, 64, 10)
+    q, k, v, g, states, out = strided(*p[:5])
+    o = out.transpose(0, 1)[:165, :, :64]
+    cu = torch.tensor([0, 90, 165], dtype=torch.int32, device=DEV)
+    work = torch.full((sk.sgemm_linear_attention_workspace(165, 2, 6, 128, 64),), 255, dtype=torch.uint8, device=DEV)
+    sk.sgemm_bf16_linear_attention(q, k, v, g, states[:, :, :128], p[5].to(DEV), cu, 1.5, out=o, workspace=work)
+    torch.cuda.synchronize()
+    want, last, ob, sb = expect(*p, lens, 1.5, True)
+    D.check(o, want, ob, "out")
+    D.check(states[:, :, :128], last, sb + 1e-300, "state")
+    assert torch.all(states[:, :, 128] == 5) and torch.all(out[:, 165] == 9) and torch.all(out[:, :, 64:] == 9)
+
+
+def test_a_prompt_in_parts_and_then_tokens():
+    """A prompt in two calls, then single tokens, is the recurrence over all of it."""
+    n, cut = 203, 200
+    p = problem([n], 2, 4, 128, 128, 11)
+    q, k, v, g, state, slots = [t.to(DEV) for t in p]
+    outs = []
+    for a, b in ((0, 77), (77, cut)):
+        outs.append(sk.sgemm_bf16_linear_attention(q[a:b], k[a:b], v[a:b], g[a:b], state, slots,
+                                                   torch.tensor([0, b - a], dtype=torch.int32, device=DEV)))
+    for t in range(cut, n):
+        r = slice(t, t + 1)
+        outs.append(sk.sgemm_bf16_linear_step(q[r], k[r], v[r], g[r], state, slots))
+    torch.cuda.synchronize()
+    want, last, ob, sb = expect(*p, [n], 1.0, True)
+    D.check(torch.cat(outs), want, ob, "out")
+    D.check(state, last, sb + 1e-300, "state")
+
+
+def test_captured():
+    lens = [100, 300]
+    p = problem(lens, 2, 2, 128, 128, 12)
+    d = [t.to(DEV) for t in p]
+    cu = torch.tensor([0, 100, 400], dtype=torch.int32, device=DEV)
+    out = torch.empty_like(d[2])
+    work = torch.empty(sk.sgemm_linear_attention_workspace(400, 2, 2, 128, 128), dtype=torch.uint8, device=DEV)
+
+    def call():
+        sk.sgemm_bf16_linear_attention(*d, cu, out=out, workspace=work, flags=sk.SGEMM_FLAG_PDL)
+
+    call()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call()
+    for lens in ([100, 300], [250, 150], [0, 400]):
+        cu.copy_(torch.tensor([0, lens[0], 400]))
+        d[4].copy_(p[4])
+        graph.replay()
+        torch.cuda.synchronize()
+        want, last, ob, sb = expect(*p, lens, 1.0, True)
+        D.check(out, want, ob, "out")
+        D.check(d[4], last, sb + 1e-300, "state")
+    assert sk.sgemm_device_errors() == 0
+
+
+def test_stalled_copies_end_in_nan_and_an_error():
+    lens = [300]
+    p = problem(lens, 2, 2, 128, 128, 13)
+    out, _ = prompt(*p, lens, errors=1, flags=sk.SGEMM_FLAG_TEST_STALL)
+    assert torch.isnan(out).all()
+    compare(lens, 2, 2, seed=13)
