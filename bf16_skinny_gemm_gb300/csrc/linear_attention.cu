@@ -24,14 +24,14 @@
 //     A   = Q K^T          64 x 64          both from shared memory
 //     O1  = Sb^T Q^T       128 x 64         Sb, the state rounded to BF16, as operand from tensor memory
 //     O2  = V^T P^T        128 x 64         P = A with its decays, BF16, through shared memory
-//     S^T += V^T K'        128 x Dk         K' = exp(G - G_j) k_j as two BF16 numbers (two products)
+//     S^T += V^T K'        128 x Dk         K' = exp(G - G_j) k_j as three BF16 numbers (three products)
 // The state stays in tensor memory, FP32, for the whole sequence; a lane holds a value element's row, so that
 // scaling it and rounding it for the next O1 needs no exchange.  out = scale (exp(G_i) O1 + O2) is put
-// together in FP32.  Why K' in two numbers: its rounding would be the state's only error above
-// FP32's, 2^-9 of every summand, and it goes on to all later tokens; 2^-17 costs one product in six.
+// together in FP32.  Why K' in three numbers: its rounding would be the state's only error above
+// FP32's, 2^-9 of every summand (in two numbers 2^-18), and it goes on to all later tokens.
 // P and Sb are rounded once: what they make is rounded to BF16 right after.
-// Roles: one warp copies (TMA, a ring of chunks), one issues all products, two sum the decays and scale the
-// keys, and four each carry the state, apply the decays to A, and write the outputs.  Exponents' sums are
+// Roles: one warp copies (TMA, a ring of chunks), one issues all products, four each sum the decays and scale
+// the keys, carry the state, apply the decays to A, and write the outputs.  Exponents' sums are
 // kept as pairs of FP32 numbers: differences of long sums keep their digits.
 #include <cuda.h>
 #include <cuda_runtime.h>
@@ -54,7 +54,7 @@ constexpr int kC = 64;                 // tokens a chunk
 constexpr int kPart = kC * 128;        // 64 tokens x 64 elements, bytes
 constexpr int kStages = 4;             // of chunks in a ring, at most
 constexpr int kFew = 4;                // chunks a share has at least
-constexpr int kOutThreads = 16 * 32;   // copies, products, keys (2 warps), state, decays, outputs (4 each)
+constexpr int kOutThreads = 18 * 32;   // copies, products, keys (2 + 2 warps), state, decays, outputs (4 each)
 constexpr int kSums = 8;               // chunks whose sums of g are kept
 constexpr int kStateThreads = 10 * 32;
 constexpr float kLeast = -1e6f;        // a decay's exponent (base 2) is cut here: 2^-1e6 is 0
@@ -276,50 +276,72 @@ __host__ __device__ constexpr uint32_t idesc_of(int m, int n, bool a_mn, bool b_
            (static_cast<uint32_t>(n >> 3) << 17) | (static_cast<uint32_t>(m >> 4) << 24);
 }
 
-// 64 columns of a 64-row accumulator in the 16 x 256-bit form: lane l has rows l / 4 and l / 4 + 8
+// 16 columns of a 64-row accumulator in the 16 x 256-bit form: lane l has rows l / 4 and l / 4 + 8
 // of the warp's 16, of each 8 columns the pair 2 (l % 4).
-__device__ __forceinline__ void tmem_ld_a(uint32_t addr, uint32_t (&r)[32]) {
+__device__ __forceinline__ void tmem_ld_a(uint32_t addr, uint32_t (&r)[8]) {
+    asm volatile("tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                 : "r"(addr));
+    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+}
+// 32 columns of the warp's lanes.
+__device__ __forceinline__ void tmem_ld32(uint32_t addr, uint32_t (&r)[32]) {
     asm volatile(
-        "tcgen05.ld.sync.aligned.16x256b.x8.b32 "
-        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
-        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19, "
+        "%20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
         : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
-          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
-          "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
-          "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]),
+          "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]),
+          "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]),
+          "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
         : "r"(addr));
     asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 }
+__device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t (&r)[32]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
+        "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19, %20, "
+        "%21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(addr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
+        "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]),
+        "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]),
+        "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+        : "memory");
+}
 
-// Rows row0, row0 + step, .. of a chunk's keys, times w, as two BF16 numbers each; rows from
-// `valid` on are 0 (whatever lies there).  A warp takes 32 units of 16 bytes at a time.
-// `wa`, `wb`: the factors of rows 2 lane, 2 lane + 1.
+// A chunk's keys times their factors, as three BF16 numbers each (arrays kKeys apart): a warp's rows,
+// 32 units of 16 bytes at a time.  Rows from `valid` on are 0, whatever lies there.  `wa`, `wb`: the factors
+// of rows 2 lane, 2 lane + 1.
 template <int WARPS, int DK>
-__device__ __forceinline__ void scale_keys(const uint8_t *k, uint8_t *hi, uint8_t *lo, int warp, int valid, float wa, float wb) {
+__device__ __forceinline__ void scale_keys(const uint8_t *k, uint8_t *out, int warp, int valid, float wa, float wb) {
     constexpr int kUnits = DK / 8, kRows = 32 / kUnits, kEach = kC / WARPS;  // units a row, rows at a time, rows a warp
+    constexpr int kKeys = DK / 64 * kPart;
     const int lane = threadIdx.x & 31, u = lane % kUnits;
-#pragma unroll
+#pragma unroll 2
     for (int i = 0; i < kEach; i += kRows) {
         const int row = warp * kEach + i + lane / kUnits;
         const float fa = __shfl_sync(0xffffffffu, wa, row >> 1), fb = __shfl_sync(0xffffffffu, wb, row >> 1);
         const float w = row & 1 ? fb : fa;
-        const int at = (u >> 3) * kPart + row * 128 + (((u & 7) ^ (row & 7)) << 4);
-        uint4 h = make_uint4(0u, 0u, 0u, 0u), l = h;
-        if (row < valid) {
-            const uint4 x = *reinterpret_cast<const uint4 *>(k + at);
-            const uint32_t in[4] = {x.x, x.y, x.z, x.w};
-            uint32_t oh[4], ol[4];
+        const int off = (u >> 3) * kPart + row * 128 + (((u & 7) ^ (row & 7)) << 4);
+        const uint4 x = *reinterpret_cast<const uint4 *>(k + off);
+        uint32_t in[4] = {x.x, x.y, x.z, x.w}, o[3][4];
+        if (row >= valid)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const float a = bf16_lo(in[e]) * w, b = bf16_hi(in[e]) * w;
-                oh[e] = bf16x2(a, b);
-                ol[e] = bf16x2(a - bf16_lo(oh[e]), b - bf16_hi(oh[e]));
+            for (int e = 0; e < 4; ++e) in[e] = 0u;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            float a = bf16_lo(in[e]) * w, b = bf16_hi(in[e]) * w;
+#pragma unroll
+            for (int m = 0; m < 3; ++m) {
+                o[m][e] = bf16x2(a, b);
+                a -= bf16_lo(o[m][e]);
+                b -= bf16_hi(o[m][e]);
             }
-            h = make_uint4(oh[0], oh[1], oh[2], oh[3]);
-            l = make_uint4(ol[0], ol[1], ol[2], ol[3]);
         }
-        *reinterpret_cast<uint4 *>(hi + at) = h;
-        *reinterpret_cast<uint4 *>(lo + at) = l;
+#pragma unroll
+        for (int m = 0; m < 3; ++m)
+            *reinterpret_cast<uint4 *>(out + m * kKeys + off) = make_uint4(o[m][0], o[m][1], o[m][2], o[m][3]);
     }
 }
 
@@ -333,8 +355,8 @@ __device__ __forceinline__ void clear_values(uint8_t *v, int parts, int warp, in
 
 __host__ __device__ constexpr int chunk_bytes(int dk, int dv, bool with_q) { return ((with_q ? 2 : 1) * dk + dv) / 64 * kPart; }
 constexpr int kMisc = 1024 + 3 * kSums * kC * 4;  // barriers and small arrays
-__host__ __device__ constexpr int out_fixed(int dk) { return 2 * 2 * dk / 64 * kPart + 2 * kPart + kMisc; }
-__host__ __device__ constexpr int state_fixed(int dk) { return 2 * 2 * dk / 64 * kPart + kPart + kMisc; }
+__host__ __device__ constexpr int out_fixed(int dk) { return 2 * 3 * dk / 64 * kPart + 2 * kPart + kMisc; }
+__host__ __device__ constexpr int state_fixed(int dk) { return 2 * 3 * dk / 64 * kPart + kPart + kMisc; }
 
 // ------------------------------------------------------------------------ 1. states of cut pieces
 template <int DK>
@@ -344,9 +366,9 @@ __global__ void __launch_bounds__(kStateThreads, 1) linear_states_kernel(const _
     extern __shared__ uint8_t raw[];
     uint8_t *base = raw + ((1024u - (saddr(raw) & 1023u)) & 1023u);
     const int vparts = p.Dv / 64, stage = chunk_bytes(DK, p.Dv, false), S = p.stages;
-    uint8_t *keys = base + S * stage;  // two buffers of both numbers; a product reads 128 value
+    uint8_t *keys = base + S * stage;  // two buffers of three numbers; a product reads 128 value
                                        // elements though there may be 64: what follows is keys
-    uint8_t *misc = keys + 4 * kKeys + kPart;
+    uint8_t *misc = keys + 6 * kKeys + kPart;
     uint64_t *bars = reinterpret_cast<uint64_t *>(misc);
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(misc + 256);
     int &stop = *reinterpret_cast<int *>(misc + 260);
@@ -416,9 +438,9 @@ __global__ void __launch_bounds__(kStateThreads, 1) linear_states_kernel(const _
             if (!all_wait(full + 8 * slot, ph, &stop) || !all_wait(kready + 8 * (n & 1), (n >> 1) & 1, &stop)) break;
             tc_fence_after();
             if (elect()) {
-                const uint64_t a = mn_desc(saddr(base) + slot * stage + kKeys), b = mn_desc(saddr(keys) + (n & 1) * 2 * kKeys);
+                const uint64_t a = mn_desc(saddr(base) + slot * stage + kKeys), b = mn_desc(saddr(keys) + (n & 1) * 3 * kKeys);
 #pragma unroll
-                for (int part = 0; part < 2; ++part)
+                for (int part = 0; part < 3; ++part)
 #pragma unroll
                     for (int kk = 0; kk < kC / 16; ++kk)
                         mma(d, a + kk * (2048 >> 4), b + ((part * kKeys) >> 4) + kk * (2048 >> 4), kIdesc, n != 0 || part != 0 || kk != 0);
@@ -460,8 +482,8 @@ __global__ void __launch_bounds__(kStateThreads, 1) linear_states_kernel(const _
             after = to;
             ok = ok && all_wait(full + 8 * slot, ph, &stop) && (n < 2 || all_wait(kfree + 8 * (n & 1), ((n >> 1) - 1) & 1, &stop));
             if (!ok) break;
-            uint8_t *out = keys + (n & 1) * 2 * kKeys;
-            scale_keys<kWarps, DK>(base + slot * stage, out, out + kKeys, w, valid, wa, wb);
+            uint8_t *out = keys + (n & 1) * 3 * kKeys;
+            scale_keys<kWarps, DK>(base + slot * stage, out, w, valid, wa, wb);
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             __syncwarp();
             if (lane == 0) bar_arrive(kready + 8 * (n & 1));
@@ -551,8 +573,8 @@ __global__ void __launch_bounds__(kOutThreads, 1) linear_outputs_kernel(const __
     extern __shared__ uint8_t raw[];
     uint8_t *base = raw + ((1024u - (saddr(raw) & 1023u)) & 1023u);
     const int vparts = p.Dv / 64, stage = chunk_bytes(DK, p.Dv, true), S = p.stages;
-    uint8_t *keys = base + S * stage;   // two buffers of both numbers
-    uint8_t *ps = keys + 4 * kKeys;     // two buffers of P
+    uint8_t *keys = base + S * stage;   // two buffers of three numbers
+    uint8_t *ps = keys + 6 * kKeys;     // two buffers of P
     uint8_t *misc = ps + 2 * kPart;
     uint64_t *bars = reinterpret_cast<uint64_t *>(misc);
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(misc + 512);
@@ -567,8 +589,7 @@ __global__ void __launch_bounds__(kOutThreads, 1) linear_outputs_kernel(const __
         return b;
     };
     const uint32_t full = take(kStages), empty = take(kStages), gready = take(kSums), kready = take(2), sdone = take(2), afull = take(1),
-                   afree = take(1), pready = take(2), odone = take(2), ofree = take(2), sscaled = take(1), sbready = take(1),
-                   o1done = take(1), fin = take(1);
+                   afree = take(1), pready = take(2), odone = take(2), ofree = take(2), sready = take(1), fin = take(1);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = static_cast<int>(blockIdx.x);
     if (threadIdx.x == 0) {
         prefetch_tmap(&p.tq);
@@ -581,16 +602,14 @@ __global__ void __launch_bounds__(kOutThreads, 1) linear_outputs_kernel(const __
         init(full, kStages, 1);
         init(empty, kStages, 1);
         init(gready, kSums, 1);
-        init(kready, 2, 2);
+        init(kready, 2, 4);
         init(sdone, 2, 1);
         init(afull, 1, 1);
         init(afree, 1, 4);
         init(pready, 2, 4);
         init(odone, 2, 1);
         init(ofree, 2, 4);
-        init(sscaled, 1, 4);
-        init(sbready, 1, 4);
-        init(o1done, 1, 1);
+        init(sready, 1, 4);
         init(fin, 1, 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -675,20 +694,7 @@ __global__ void __launch_bounds__(kOutThreads, 1) linear_outputs_kernel(const __
         scores(0);
         for (int n = 0; ok && n < total; ++n) {
             const uint32_t st = saddr(base) + slot * stage, o = d + kO + 128 * (n & 1);
-            // the state's chain first
-            if (!(ok = all_wait(kready + 8 * (n & 1), (n >> 1) & 1, &stop) && all_wait(sscaled, n & 1, &stop))) break;
-            tc_fence_after();
-            if (elect()) {
-                const uint64_t a = mn_desc(st + 2 * kKeys), b = mn_desc(saddr(keys) + (n & 1) * 2 * kKeys);
-#pragma unroll
-                for (int part = 0; part < 2; ++part)
-#pragma unroll
-                    for (int kk = 0; kk < kC / 16; ++kk)
-                        mma(d + kState, a + kk * (2048 >> 4), b + ((part * kKeys) >> 4) + kk * (2048 >> 4), kIdS, true);
-                mma_commit(sdone + 8 * (n & 1));
-            }
-            __syncwarp();
-            if (!(ok = all_wait(sbready, n & 1, &stop) && (n < 2 || all_wait(ofree + 8 * (n & 1), ((n >> 1) - 1) & 1, &stop)))) break;
+            if (!(ok = all_wait(sready, n & 1, &stop) && (n < 2 || all_wait(ofree + 8 * (n & 1), ((n >> 1) - 1) & 1, &stop)))) break;
             tc_fence_after();
             if (elect()) {
 #pragma unroll
@@ -696,7 +702,18 @@ __global__ void __launch_bounds__(kOutThreads, 1) linear_outputs_kernel(const __
 #pragma unroll
                     for (int kk = 0; kk < 4; ++kk)
                         mma_ts(o, d + kSb + 32 * i + 8 * kk, tc05::sw128_desc(st + i * kPart) + ((32 * kk) >> 4), kIdO1, i != 0 || kk != 0);
-                mma_commit(o1done);
+            }
+            __syncwarp();
+            if (!(ok = all_wait(kready + 8 * (n & 1), (n >> 1) & 1, &stop))) break;
+            tc_fence_after();
+            if (elect()) {
+                const uint64_t a = mn_desc(st + 2 * kKeys), b = mn_desc(saddr(keys) + (n & 1) * 3 * kKeys);
+#pragma unroll
+                for (int part = 0; part < 3; ++part)
+#pragma unroll
+                    for (int kk = 0; kk < kC / 16; ++kk)
+                        mma(d + kState, a + kk * (2048 >> 4), b + ((part * kKeys) >> 4) + kk * (2048 >> 4), kIdS, true);
+                mma_commit(sdone + 8 * (n & 1));  // (O1 has then read Sb too)
             }
             __syncwarp();
             if (n + 1 < total) scores(n + 1);
@@ -713,9 +730,9 @@ __global__ void __launch_bounds__(kOutThreads, 1) linear_outputs_kernel(const __
             if (++slot == S) slot = 0;
         }
         finish(fin, &stop);
-    } else if (warp < 4) {
+    } else if (warp < 4 || warp >= 16) {
         // ------------------------------------------------------ keys, and the sums of decays
-        const int w = warp - 2;
+        const int w = warp < 4 ? warp - 2 : warp - 14;
         Cursor ahead = cursor;
         Chunk nc;
         Decays next{0.0f, 0.0f};
@@ -734,14 +751,14 @@ __global__ void __launch_bounds__(kOutThreads, 1) linear_outputs_kernel(const __
                 *reinterpret_cast<float2 *>(&ghi[to]) = make_float2(a.hi, b.hi);
                 *reinterpret_cast<float2 *>(&glo[to]) = make_float2(a.lo, b.lo);
                 *reinterpret_cast<float2 *>(&eg[to]) = make_float2(exp2f(a.hi + a.lo), exp2f(b.hi + b.lo));
-                if (lane == 0) all_e[n & 3] = exp2f(all.hi + all.lo);
+                if (lane == 0) all_e[n & (kSums - 1)] = exp2f(all.hi + all.lo);
                 __syncwarp();
                 if (lane == 0) bar_arrive(gready + 8 * (n & (kSums - 1)));
             }
             if (!(ok = all_wait(full + 8 * slot, ph, &stop))) break;
-            uint8_t *out = keys + (n & 1) * 2 * kKeys, *st = base + slot * stage;
-            scale_keys<2, DK>(st + kKeys, out, out + kKeys, w, c.valid, exp2f(less(all, a)), exp2f(less(all, b)));
-            if (c.valid < kC) clear_values<2>(st + 2 * kKeys, vparts, w, c.valid);
+            uint8_t *out = keys + (n & 1) * 3 * kKeys, *st = base + slot * stage;
+            scale_keys<4, DK>(st + kKeys, out, w, c.valid, exp2f(less(all, a)), exp2f(less(all, b)));
+            if (c.valid < kC) clear_values<4>(st + 2 * kKeys, vparts, w, c.valid);
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             __syncwarp();
             if (lane == 0) bar_arrive(kready + 8 * (n & 1));
@@ -774,42 +791,30 @@ __global__ void __launch_bounds__(kOutThreads, 1) linear_outputs_kernel(const __
             }
             if (ok) {
                 tc_fence_after();
-                const float e = all_e[n & 3];
-                uint32_t sb[DK / 2];
-#pragma unroll
-                for (int col = 0; col < DK; col += 16) {
-                    uint32_t v[16];
+                const float e = all_e[n & (kSums - 1)];
+#pragma unroll 1
+                for (int col = 0; col < DK; col += 32) {
+                    uint32_t v[32], sb[16];
                     if (c.head) {
 #pragma unroll
-                        for (int i = 0; i < 16; ++i) v[i] = from && mine ? __float_as_uint(from[(col + i) * p.Dv + dv]) : 0u;
+                        for (int i = 0; i < 32; ++i) v[i] = from && mine ? __float_as_uint(from[(col + i) * p.Dv + dv]) : 0u;
                     } else {
-                        tc05::tmem_ld16(tmem + quarter + kState + col, v);
+                        tmem_ld32(tmem + quarter + kState + col, v);
                     }
 #pragma unroll
-                    for (int i = 0; i < 16; i += 2) sb[(col + i) / 2] = bf16x2(__uint_as_float(v[i]), __uint_as_float(v[i + 1]));
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * e);
-                    tmem_st16(tmem + quarter + kState + col, v);
+                    for (int i = 0; i < 16; ++i) {
+                        const float a = __uint_as_float(v[2 * i]), b = __uint_as_float(v[2 * i + 1]);
+                        sb[i] = bf16x2(a, b);
+                        v[2 * i] = __float_as_uint(a * e);
+                        v[2 * i + 1] = __float_as_uint(b * e);
+                    }
+                    tmem_st16(tmem + quarter + kSb + col / 2, sb);
+                    tmem_st32(tmem + quarter + kState + col, v);
                 }
                 asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) bar_arrive(sscaled);
-                ok = n == 0 || all_wait(o1done, (n - 1) & 1, &stop);
-                if (ok) {
-                    tc_fence_after();
-#pragma unroll
-                    for (int col = 0; col < DK / 2; col += 16) {
-                        uint32_t v[16];
-#pragma unroll
-                        for (int i = 0; i < 16; ++i) v[i] = sb[col + i];
-                        tmem_st16(tmem + quarter + kSb + col, v);
-                    }
-                    asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
-                    tc_fence_before();
-                }
-                __syncwarp();
-                if (lane == 0) bar_arrive(sbready);
+                if (lane == 0) bar_arrive(sready);
             }
             if (c.tail) {
                 // the sequence's last state
@@ -819,6 +824,7 @@ __global__ void __launch_bounds__(kOutThreads, 1) linear_outputs_kernel(const __
                 if (s.slot >= 0 && (s.len > 0 || fresh)) {
                     float *to = p.state + s.slot * p.s_slot + c.h * p.s_head + dv;
                     tc_fence_after();
+#pragma unroll 1
                     for (int col = 0; col < DK; col += 16) {
                         uint32_t v[16];
                         if (ok) tc05::tmem_ld16(tmem + quarter + kState + col, v);
@@ -835,35 +841,35 @@ __global__ void __launch_bounds__(kOutThreads, 1) linear_outputs_kernel(const __
         bool ok = true;
         for (int n = 0; cursor.next(p, c); ++n) {
             if (!(ok = all_wait(gready + 8 * (n & (kSums - 1)), (n / kSums) & 1, &stop) && all_wait(afull, n & 1, &stop))) break;
+            if (!(ok = n < 2 || all_wait(odone + 8 * (n & 1), ((n >> 1) - 1) & 1, &stop))) break;
             tc_fence_after();
-            uint32_t r[32];
-            tmem_ld_a(tmem + quarter + kA, r);
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) bar_arrive(afree);
             const int i0 = 16 * q + (lane >> 2), j0 = 2 * (lane & 3);
             const float *hi = ghi + (n & (kSums - 1)) * kC, *lo = glo + (n & (kSums - 1)) * kC;
             const float h0 = hi[i0], l0 = lo[i0], h1 = hi[i0 + 8], l1 = lo[i0 + 8];
-            if (!(ok = n < 2 || all_wait(odone + 8 * (n & 1), ((n >> 1) - 1) & 1, &stop))) break;
+            // a row's tokens up to its own; none of a row behind the chunk's
+            const int last0 = i0 < c.valid ? i0 : -1, last1 = i0 + 8 < c.valid ? i0 + 8 : -1;
             uint8_t *row = ps + (n & 1) * kPart + i0 * 128;
+#pragma unroll 1
+            for (int t = 0; t < 4; ++t) {
+                uint32_t r[8];
+                tmem_ld_a(tmem + quarter + kA + 16 * t, r);
 #pragma unroll
-            for (int t = 0; t < 8; ++t) {
-                const int j = 8 * t + j0;
-                const float2 hj = *reinterpret_cast<const float2 *>(&hi[j]), lj = *reinterpret_cast<const float2 *>(&lo[j]);
-                float w[4];
-                w[0] = ex2((h0 - hj.x) + (l0 - lj.x)) * __uint_as_float(r[4 * t]);
-                w[1] = ex2((h0 - hj.y) + (l0 - lj.y)) * __uint_as_float(r[4 * t + 1]);
-                w[2] = ex2((h1 - hj.x) + (l1 - lj.x)) * __uint_as_float(r[4 * t + 2]);
-                w[3] = ex2((h1 - hj.y) + (l1 - lj.y)) * __uint_as_float(r[4 * t + 3]);
-                // later tokens, and rows behind the chunk's
-                if (j > i0 || i0 >= c.valid) w[0] = 0.0f;
-                if (j + 1 > i0 || i0 >= c.valid) w[1] = 0.0f;
-                if (j > i0 + 8 || i0 + 8 >= c.valid) w[2] = 0.0f;
-                if (j + 1 > i0 + 8 || i0 + 8 >= c.valid) w[3] = 0.0f;
-                const int to = ((t ^ (lane >> 2)) << 4) + 2 * j0;  // i0 % 8 = lane / 4
-                *reinterpret_cast<uint32_t *>(row + to) = bf16x2(w[0], w[1]);
-                *reinterpret_cast<uint32_t *>(row + 8 * 128 + to) = bf16x2(w[2], w[3]);
+                for (int m = 0; m < 2; ++m) {
+                    const int j = 16 * t + 8 * m + j0;
+                    const float2 hj = *reinterpret_cast<const float2 *>(&hi[j]), lj = *reinterpret_cast<const float2 *>(&lo[j]);
+                    // (later tokens' exponents may overflow: they are not used)
+                    const float a = j <= last0 ? ex2((h0 - hj.x) + (l0 - lj.x)) * __uint_as_float(r[4 * m]) : 0.0f;
+                    const float b = j + 1 <= last0 ? ex2((h0 - hj.y) + (l0 - lj.y)) * __uint_as_float(r[4 * m + 1]) : 0.0f;
+                    const float e = j <= last1 ? ex2((h1 - hj.x) + (l1 - lj.x)) * __uint_as_float(r[4 * m + 2]) : 0.0f;
+                    const float f = j + 1 <= last1 ? ex2((h1 - hj.y) + (l1 - lj.y)) * __uint_as_float(r[4 * m + 3]) : 0.0f;
+                    const int to = (((2 * t + m) ^ (lane >> 2)) << 4) + 2 * j0;  // i0 % 8 = lane / 4
+                    *reinterpret_cast<uint32_t *>(row + to) = bf16x2(a, b);
+                    *reinterpret_cast<uint32_t *>(row + 8 * 128 + to) = bf16x2(e, f);
+                }
             }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) bar_arrive(afree);
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             __syncwarp();
             if (lane == 0) bar_arrive(pready + 8 * (n & 1));
@@ -877,6 +883,7 @@ __global__ void __launch_bounds__(kOutThreads, 1) linear_outputs_kernel(const __
             if (ok) tc_fence_after();
             uint16_t *to = p.out + static_cast<long long>(c.t0) * p.o_token + c.h * p.o_head + dv;
             const float *e = eg + (n & (kSums - 1)) * kC;
+            const int end = dv < p.Dv ? c.valid : 0;
 #pragma unroll 1
             for (int i = 0; i < kC; i += 16) {
                 if (i >= c.valid) break;
@@ -885,13 +892,12 @@ __global__ void __launch_bounds__(kOutThreads, 1) linear_outputs_kernel(const __
                     tc05::tmem_ld16(tmem + quarter + kO + 128 * (n & 1) + i, a);
                     tc05::tmem_ld16(tmem + quarter + kO + 128 * (n & 1) + 64 + i, b);
                 }
-                if (dv < p.Dv)
 #pragma unroll
-                    for (int j = 0; j < 16; ++j)
-                        if (i + j < c.valid) {
-                            const float x = p.scale * fmaf(e[i + j], __uint_as_float(a[j]), __uint_as_float(b[j]));
-                            to[(i + j) * p.o_token] = f32_to_bf16_rn(ok ? x : nan);
-                        }
+                for (int j = 0; j < 16; ++j, to += p.o_token)
+                    if (i + j < end) {
+                        const float x = p.scale * fmaf(e[i + j], __uint_as_float(a[j]), __uint_as_float(b[j]));
+                        *to = f32_to_bf16_rn(ok ? x : nan);
+                    }
             }
             tc_fence_before();
             __syncwarp();

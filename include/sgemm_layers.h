@@ -164,8 +164,8 @@ sgemm_status_t sgemm_bf16_linear_step(const sgemm_linear_step_t *args, sgemm_str
  *     o_i = scale (exp(G_i) q_i^T S + sum_{j <= i} exp(G_i - G_j) (q_i . k_j) v_j)
  *     S'  = exp(G) S + sum_j exp(G - G_j) k_j v_j^T
  * Sums and states are FP32.  Rounded to BF16, as operands of products: the weights
- * exp(G_i - G_j) (q_i . k_j), and S in the outputs; decayed keys are pairs of BF16 values
- * whose sum is off by 2^-17, so that the states keep FP32's accuracy nearly.
+ * exp(G_i - G_j) (q_i . k_j), and S in the outputs; decayed keys are three BF16 values
+ * each, whose sum is the FP32 product, so that the states keep FP32's accuracy.
  * - slots[b] < 0: starts from zeros, and the last state is not kept.  A slot past
  *   the pool is treated the same and sets bit 1 of the device error word.
  * - A sequence without tokens leaves its slot as it is (zeros where fresh).
