@@ -19,20 +19,26 @@
 //   3. outputs: every share from the state it begins with.
 // Keys and values of cut sequences are read twice.
 //
-// The output kernel, a CTA an SM, all products transposed so that the value's elements are the 128
-// rows (lanes of tensor memory) and tokens the columns:
-//     A   = Q K^T          64 x 64          both from shared memory
-//     O1  = Sb^T Q^T       128 x 64         Sb, the state rounded to BF16, as operand from tensor memory
-//     O2  = V^T P^T        128 x 64         P = A with its decays, BF16, through shared memory
-//     S^T += V^T K'        128 x Dk         K' = exp(G - G_j) k_j as three BF16 numbers (three products)
+// The state kernel: U = K'^T V.  Its warps read the keys turned (ldmatrix), scale them and put them into tensor
+// memory as the first operand, element of the key a lane; the second are the values as they came.
+//
+// The output kernel, a CTA an SM, all products but A turned so that the value's elements are the 128
+// rows (lanes of tensor memory) and tokens or the key's elements the columns:
+//     A    = Q K^T         64 x 64          both from shared memory
+//     S^T += V^T K'        128 x Dk         V^T from tensor memory, K' = exp(G - G_j) k_j, three BF16 numbers each
+//     O1   = Sb^T Q^T      128 x 64         Sb, the state rounded to BF16, from tensor memory
+//     O2   = V^T P^T       128 x 64         P = A with its decays, BF16, through shared memory
 // The state stays in tensor memory, FP32, for the whole sequence; a lane holds a value element's row, so that
 // scaling it and rounding it for the next O1 needs no exchange.  out = scale (exp(G_i) O1 + O2) is put
-// together in FP32.  Why K' in three numbers: its rounding would be the state's only error above
-// FP32's, 2^-9 of every summand (in two numbers 2^-18), and it goes on to all later tokens.
-// P and Sb are rounded once: what they make is rounded to BF16 right after.
-// Roles: one warp copies (TMA, a ring of chunks), one issues all products, four each sum the decays and scale
-// the keys, carry the state, apply the decays to A, and write the outputs.  Exponents' sums are
-// kept as pairs of FP32 numbers: differences of long sums keep their digits.
+// together in FP32.  Why K' in three numbers (cut off after 8 bits each: 24 bits): its rounding would be the
+// state's only error above FP32's, 2^-9 of every summand (in two numbers 2^-18), and it goes on to all later
+// tokens.  P and Sb are rounded once: what they make is rounded to BF16 right after.
+// Roles: a warp copies (TMA, a ring of chunks), a warp issues all products, a warp sums the decays, and
+// four each scale the keys, carry the state, turn the values and apply the decays to A, and write the outputs.
+// Exponents' sums are kept as pairs of FP32 numbers where states are made of them: differences of long sums
+// keep their digits.
+// The roles' loops are short on purpose: unrolled, their code did not fit the instruction cache, and a chunk
+// took 9600 cycles (4500 without any other change).
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -52,12 +58,14 @@ using namespace roles;
 
 constexpr int kC = 64;                 // tokens a chunk
 constexpr int kPart = kC * 128;        // 64 tokens x 64 elements, bytes
-constexpr int kStages = 4;             // of chunks in a ring, at most
+constexpr int kStages = 6;             // of chunks in a ring, at most
 constexpr int kFew = 4;                // chunks a share has at least
-constexpr int kOutThreads = 18 * 32;   // copies, products, keys (2 + 2 warps), state, decays, outputs (4 each)
-constexpr int kSums = 8;               // chunks whose sums of g are kept
+constexpr int kOutThreads = 20 * 32;   // copies, products, sums, (none), state, values, outputs, keys (4 each)
+constexpr int kSums = 4;               // chunks whose sums of g are kept
 constexpr int kStateThreads = 10 * 32;
-constexpr float kLeast = -1e6f;        // a decay's exponent (base 2) is cut here: 2^-1e6 is 0
+// A decay's exponent (base 2) is cut here: 2^-200 is 0.  The sum of a chunk's is then 12800 at most, one
+// FP32 number of it off by 2^-11, and a factor exp2 of a difference by 2^-10.5: below BF16's rounding.
+constexpr float kLeast = -200.0f;
 
 struct LinearParams {
     CUtensorMap tq, tk, tv;  // {D, N, heads}, boxes of 64 tokens x 64 elements
@@ -73,6 +81,7 @@ struct LinearParams {
     int Dk, Dv;
     int groups;        // shares at most
     int stages;
+    int out16;         // out's rows start on 16 bytes
     int flags;
     float scale;
 };
@@ -279,96 +288,140 @@ __host__ __device__ constexpr uint32_t idesc_of(int m, int n, bool a_mn, bool b_
 // 16 columns of a 64-row accumulator in the 16 x 256-bit form: lane l has rows l / 4 and l / 4 + 8
 // of the warp's 16, of each 8 columns the pair 2 (l % 4).
 __device__ __forceinline__ void tmem_ld_a(uint32_t addr, uint32_t (&r)[8]) {
-    asm volatile("tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
-                 : "r"(addr));
+    tmem_ld_s(addr, r);
     asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 }
-// 32 columns of the warp's lanes.
-__device__ __forceinline__ void tmem_ld32(uint32_t addr, uint32_t (&r)[32]) {
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
-        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19, "
-        "%20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
-          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]),
-          "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]),
-          "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]),
-          "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
-        : "r"(addr));
-    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+// 16 lanes x 4 N columns (N = 2, 4 here): register 2 i of lane l goes to row l / 4, column 4 i + l % 4, register 2 i + 1
+// to row l / 4 + 8.  This is how turned 8 x 8 matrices of BF16 pairs come from shared memory.
+__device__ __forceinline__ void tmem_st_turned(uint32_t addr, const uint32_t (&r)[8]) {
+    asm volatile("tcgen05.st.sync.aligned.16x128b.x4.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(addr), "r"(r[0]), "r"(r[1]),
+                 "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+                 : "memory");
 }
-__device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t (&r)[32]) {
+__device__ __forceinline__ void tmem_st_turned(uint32_t addr, const uint32_t (&r)[16]) {
     asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
-        "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19, %20, "
-        "%21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(addr),
-        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
-        "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]),
-        "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]),
-        "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+        "tcgen05.st.sync.aligned.16x128b.x8.b32 [%0], "
+        "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(addr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
         : "memory");
 }
+// Tokens t0 .. t0 + 15 of elements d0 .. d0 + 15 of a chunk in shared memory, turned: register 2 i + j of lane l has
+// tokens t0 + 8 i + 2 (l % 4) and the next one of element d0 + 8 j + l / 4.
+__device__ __forceinline__ void load_turned(uint32_t chunk, int t0, int d0, uint32_t &r0, uint32_t &r1, uint32_t &r2, uint32_t &r3) {
+    const int lane = threadIdx.x & 31, m = lane >> 3;
+    const int row = t0 + 8 * (m >> 1) + (lane & 7), u = (d0 >> 3) + (m & 1);
+    const uint32_t at = chunk + (u >> 3) * kPart + row * 128 + (((u & 7) ^ (row & 7)) << 4);
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r0), "=r"(r1), "=r"(r2), "=r"(r3)
+                 : "r"(at)
+                 : "memory");
+}
 
-// A chunk's keys times their factors, as three BF16 numbers each (arrays kKeys apart): a warp's rows,
-// 32 units of 16 bytes at a time.  Rows from `valid` on are 0, whatever lies there.  `wa`, `wb`: the factors
-// of rows 2 lane, 2 lane + 1.
-template <int WARPS, int DK>
-__device__ __forceinline__ void scale_keys(const uint8_t *k, uint8_t *out, int warp, int valid, float wa, float wb) {
-    constexpr int kUnits = DK / 8, kRows = 32 / kUnits, kEach = kC / WARPS;  // units a row, rows at a time, rows a warp
-    constexpr int kKeys = DK / 64 * kPart;
-    const int lane = threadIdx.x & 31, u = lane % kUnits;
-#pragma unroll 2
-    for (int i = 0; i < kEach; i += kRows) {
-        const int row = warp * kEach + i + lane / kUnits;
-        const float fa = __shfl_sync(0xffffffffu, wa, row >> 1), fb = __shfl_sync(0xffffffffu, wb, row >> 1);
-        const float w = row & 1 ? fb : fa;
-        const int off = (u >> 3) * kPart + row * 128 + (((u & 7) ^ (row & 7)) << 4);
-        const uint4 x = *reinterpret_cast<const uint4 *>(k + off);
-        uint32_t in[4] = {x.x, x.y, x.z, x.w}, o[3][4];
-        if (row >= valid)
+__device__ __forceinline__ unsigned long long mul2(unsigned long long a, unsigned long long b) {
+    unsigned long long r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ void unpack2(unsigned long long v, uint32_t &a, uint32_t &b) {
+    asm("mov.b64 {%0, %1}, %2;" : "=r"(a), "=r"(b) : "l"(v));
+}
+__device__ __forceinline__ unsigned long long pack2(uint32_t a, uint32_t b) {
+    unsigned long long r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(a), "r"(b));
+    return r;
+}
+// Two BF16 numbers, each times its factor, as three pairs of BF16 numbers whose sums the FP32 products
+// are: 8 bits each, cut off.
+__device__ __forceinline__ void split(uint32_t v, unsigned long long f, uint32_t (&o)[3]) {
+    const unsigned long long minus = pack2(0xbf800000u, 0xbf800000u);  // -1, -1
+    unsigned long long x = mul2(pack2(v << 16, v & 0xffff0000u), f);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) in[e] = 0u;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            float a = bf16_lo(in[e]) * w, b = bf16_hi(in[e]) * w;
-#pragma unroll
-            for (int m = 0; m < 3; ++m) {
-                o[m][e] = bf16x2(a, b);
-                a -= bf16_lo(o[m][e]);
-                b -= bf16_hi(o[m][e]);
-            }
-        }
-#pragma unroll
-        for (int m = 0; m < 3; ++m)
-            *reinterpret_cast<uint4 *>(out + m * kKeys + off) = make_uint4(o[m][0], o[m][1], o[m][2], o[m][3]);
+    for (int m = 0; m < 3; ++m) {
+        uint32_t a, b;
+        unpack2(x, a, b);
+        o[m] = __byte_perm(a, b, 0x7632);
+        if (m < 2) x = ffma2(pack2(a & 0xffff0000u, b & 0xffff0000u), minus, x);
     }
 }
 
-// Values behind a chunk's tokens become 0 (another sequence's, or nothing that was ever written).
-template <int WARPS>
-__device__ __forceinline__ void clear_values(uint8_t *v, int parts, int warp, int valid) {
-    const int lane = threadIdx.x & 31;
-    for (int row = valid + warp; row < kC; row += WARPS)
-        if (lane < 8 * parts) *reinterpret_cast<uint4 *>(v + (lane >> 3) * kPart + row * 128 + (lane & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
+// 16 columns of the warp's lanes; they are there after the wait.
+__device__ __forceinline__ void tmem_ld16_soon(uint32_t addr, uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(addr));
+}
+__device__ __forceinline__ void tmem_wait16(uint32_t (&r)[16]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                   "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]),
+                   "+r"(r[15])
+                 :
+                 : "memory");
+}
+__device__ __forceinline__ void tmem_st8(uint32_t addr, const uint32_t (&r)[8]) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(addr), "r"(r[0]), "r"(r[1]),
+                 "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+                 : "memory");
+}
+
+// A chunk's keys times their factors w, as three BF16 numbers each (arrays DK / 64 parts apart), by four warps,
+// 32 units of 16 bytes at a time, four times in flight.  Rows from `valid` on are 0, whatever lies there.
+template <int DK>
+__device__ __forceinline__ void scale_keys(const uint8_t *k, uint8_t *out, const float *w, int warp, int valid) {
+    constexpr int kUnits = DK / 8, kRows = 32 / kUnits, kEach = kC / 4;  // units a row, rows at a time, rows a warp
+    constexpr int kKeys = DK / 64 * kPart, kBatch = 4;
+    const int lane = threadIdx.x & 31, u = lane % kUnits;
+#pragma unroll 1
+    for (int i = 0; i < kEach; i += kBatch * kRows) {
+        uint4 x[kBatch];
+        float f[kBatch];
+        const int row0 = warp * kEach + i + lane / kUnits;
+        auto place = [&](int m) {
+            const int row = row0 + m * kRows;
+            return (u >> 3) * kPart + row * 128 + (((u & 7) ^ (row & 7)) << 4);
+        };
+#pragma unroll
+        for (int m = 0; m < kBatch; ++m) {
+            x[m] = *reinterpret_cast<const uint4 *>(k + place(m));
+            f[m] = w[row0 + m * kRows];
+        }
+#pragma unroll
+        for (int m = 0; m < kBatch; ++m) {
+            const bool in = row0 + m * kRows < valid;
+            const uint32_t v[4] = {x[m].x, x[m].y, x[m].z, x[m].w};
+            const unsigned long long ff = pack_f32x2(f[m], f[m]);
+            uint32_t o[4][3];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) split(in ? v[e] : 0u, ff, o[e]);
+#pragma unroll
+            for (int s = 0; s < 3; ++s) *reinterpret_cast<uint4 *>(out + s * kKeys + place(m)) = make_uint4(o[0][s], o[1][s], o[2][s], o[3][s]);
+        }
+    }
 }
 
 __host__ __device__ constexpr int chunk_bytes(int dk, int dv, bool with_q) { return ((with_q ? 2 : 1) * dk + dv) / 64 * kPart; }
-constexpr int kMisc = 1024 + 3 * kSums * kC * 4;  // barriers and small arrays
-__host__ __device__ constexpr int out_fixed(int dk) { return 2 * 3 * dk / 64 * kPart + 2 * kPart + kMisc; }
-__host__ __device__ constexpr int state_fixed(int dk) { return 2 * 3 * dk / 64 * kPart + kPart + kMisc; }
+// barriers, and arrays of each chunk's tokens or values
+constexpr int kMiscOut = 1024 + 3 * kSums * kC * 4 + 4 * 128 * 4;
+constexpr int kOutStage = 32 * 256;  // 32 tokens' outputs on their way
+__host__ __device__ constexpr int out_fixed(int dk) { return 2 * 3 * dk / 64 * kPart + 2 * kPart + kOutStage + kMiscOut; }
+constexpr int kStateFixed = 512;
+// Columns of tensor memory: the state kernel's (U, two buffers of keys in three numbers), the output kernel's
+// (two buffers of values).
+constexpr int kU = 0, kKeyT = 128;
+constexpr int kState = 0, kSb = 128, kA = 192, kO1 = 256, kO2 = 320, kValueT = 384;
 
 // ------------------------------------------------------------------------ 1. states of cut pieces
 template <int DK>
 __global__ void __launch_bounds__(kStateThreads, 1) linear_states_kernel(const __grid_constant__ LinearParams p) {
     constexpr int kKParts = DK / 64, kKeys = kKParts * kPart, kWarps = 8;
-    constexpr int kTmem = DK;
     extern __shared__ uint8_t raw[];
     uint8_t *base = raw + ((1024u - (saddr(raw) & 1023u)) & 1023u);
     const int vparts = p.Dv / 64, stage = chunk_bytes(DK, p.Dv, false), S = p.stages;
-    uint8_t *keys = base + S * stage;  // two buffers of three numbers; a product reads 128 value
-                                       // elements though there may be 64: what follows is keys
-    uint8_t *misc = keys + 6 * kKeys + kPart;
+    uint8_t *misc = base + S * stage;
     uint64_t *bars = reinterpret_cast<uint64_t *>(misc);
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(misc + 256);
     int &stop = *reinterpret_cast<int *>(misc + 260);
@@ -396,9 +449,9 @@ __global__ void __launch_bounds__(kStateThreads, 1) linear_states_kernel(const _
     if (sh.u1 <= sh.u0) return;
     const Place last = place_of(p, sh.u1 - 1);
     if (last.k + 1 >= last.s.chunks) return;  // no cut sequence at this share's end
-    const int chunks = min(last.k + 1, sh.u1 - sh.u0);
+    const int chunks = min(last.k + 1, sh.u1 - sh.u0);  // all of them whole: the sequence goes on behind
     if (warp == 1) {
-        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(saddr(tmem_slot)), "r"(kTmem)
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(saddr(tmem_slot)), "r"(512)
                      : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
@@ -432,18 +485,18 @@ __global__ void __launch_bounds__(kStateThreads, 1) linear_states_kernel(const _
     } else if (warp == 1) {
         int slot = 0;
         unsigned ph = 0;
-        constexpr uint32_t kIdesc = idesc_of(128, DK, true, true);
-        const uint32_t d = alike(static_cast<int>(tmem));
+        const uint32_t d = alike(static_cast<int>(tmem)), idesc = alike(static_cast<int>(idesc_of(128, p.Dv, false, true)));
         for (int n = 0; n < chunks; ++n) {
             if (!all_wait(full + 8 * slot, ph, &stop) || !all_wait(kready + 8 * (n & 1), (n >> 1) & 1, &stop)) break;
             tc_fence_after();
             if (elect()) {
-                const uint64_t a = mn_desc(saddr(base) + slot * stage + kKeys), b = mn_desc(saddr(keys) + (n & 1) * 3 * kKeys);
+                const uint64_t b = mn_desc(saddr(base) + slot * stage + kKeys);
+                const uint32_t a = d + kKeyT + 96 * (n & 1);
 #pragma unroll
                 for (int part = 0; part < 3; ++part)
 #pragma unroll
                     for (int kk = 0; kk < kC / 16; ++kk)
-                        mma(d, a + kk * (2048 >> 4), b + ((part * kKeys) >> 4) + kk * (2048 >> 4), kIdesc, n != 0 || part != 0 || kk != 0);
+                        mma_ts(d + kU, a + 32 * part + 8 * kk, b + kk * (2048 >> 4), idesc, n != 0 || part != 0 || kk != 0);
                 mma_commit(empty + 8 * slot);
                 mma_commit(kfree + 8 * (n & 1));
             }
@@ -455,36 +508,54 @@ __global__ void __launch_bounds__(kStateThreads, 1) linear_states_kernel(const _
         }
         finish(fin, &stop);
     } else {
-        const int w = warp - 2;
+        // keys: a warp's 32 elements (a quarter of the lanes), half of the tokens
+        const int q = warp & 3, half = (warp - 2) >> 2, d0 = 32 * q;
+        const uint32_t quarter = static_cast<uint32_t>(32 * q) << 16;
         Pair after{0.0f, 0.0f};  // the sum of g behind the chunk, to the piece's end
         bool ok = true;
         int slot = 0;
         unsigned ph = 0;
         Chunk c;
         c.h = last.h;
-        auto chunk = [&](int n) {
-            c.t0 = last.s.t0 + (last.k - n) * kC;
-            c.valid = min(kC, last.s.len - (last.k - n) * kC);  // (a cut piece has whole chunks only)
-        };
-        chunk(0);
+        c.valid = kC;
+        c.t0 = last.s.t0 + last.k * kC;
         Decays next = load_g(p, c);
         for (int n = 0; n < chunks; ++n) {
             const Decays now = next;
-            const int valid = c.valid;
-            if (n + 1 < chunks) {
-                chunk(n + 1);
-                next = load_g(p, c);
-            }
+            c.t0 -= kC;
+            if (n + 1 < chunks) next = load_g(p, c);
             Pair a, b, all;
             sums_of(now, a, b, all);
-            const Pair to = add(all, after);
-            const float wa = exp2f(less(to, a)), wb = exp2f(less(to, b));
-            after = to;
-            ok = ok && all_wait(full + 8 * slot, ph, &stop) && (n < 2 || all_wait(kfree + 8 * (n & 1), ((n >> 1) - 1) & 1, &stop));
+            after = add(all, after);
+            const float wa = exp2f(less(after, a)), wb = exp2f(less(after, b));
+            ok = all_wait(full + 8 * slot, ph, &stop) && (n < 2 || all_wait(kfree + 8 * (n & 1), ((n >> 1) - 1) & 1, &stop));
             if (!ok) break;
-            uint8_t *out = keys + (n & 1) * 3 * kKeys;
-            scale_keys<kWarps, DK>(base + slot * stage, out, w, valid, wa, wb);
-            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            if (n >= 2) tc_fence_after();
+            if (d0 < DK) {
+                unsigned long long ff[4];  // of tokens 32 half + 8 i + 2 (lane % 4) and the next
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    ff[i] = pack_f32x2(__shfl_sync(0xffffffffu, wa, 16 * half + 4 * i + (lane & 3)),
+                                       __shfl_sync(0xffffffffu, wb, 16 * half + 4 * i + (lane & 3)));
+#pragma unroll 1
+                for (int h = 0; h < 2; ++h) {  // 16 elements
+                    uint32_t r[8], o[3][8];
+                    load_turned(saddr(base) + slot * stage, 32 * half, d0 + 16 * h, r[0], r[1], r[2], r[3]);
+                    load_turned(saddr(base) + slot * stage, 32 * half + 16, d0 + 16 * h, r[4], r[5], r[6], r[7]);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        uint32_t s[3];
+                        split(r[i], ff[i >> 1], s);
+#pragma unroll
+                        for (int m = 0; m < 3; ++m) o[m][i] = s[m];
+                    }
+#pragma unroll
+                    for (int m = 0; m < 3; ++m)
+                        tmem_st_turned(tmem + quarter + (static_cast<uint32_t>(16 * h) << 16) + kKeyT + 96 * (n & 1) + 32 * m + 16 * half, o[m]);
+                }
+                asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+            }
+            tc_fence_before();
             __syncwarp();
             if (lane == 0) bar_arrive(kready + 8 * (n & 1));
             if (++slot == S) {
@@ -492,21 +563,24 @@ __global__ void __launch_bounds__(kStateThreads, 1) linear_states_kernel(const _
                 ph ^= 1;
             }
         }
-        // the piece's state, [Dk][Dv], by warps 2..5 and 6..9: half of the columns each
+        // the piece's state, [Dk][Dv]: a row a lane, half of the columns a warp
         ok = ok && all_wait(fin, 0, &stop) && *reinterpret_cast<volatile int *>(&stop) == 0;
         ok = __all_sync(0xffffffffu, ok);
         const float nan = __int_as_float(0x7fc00000);
-        const int q = warp & 3, dv = 32 * q + lane, half = w >> 2;
         tc_fence_after();
-        float *to = state_of(p, g) + dv;
-        for (int col = half * (DK / 2); col < (half + 1) * (DK / 2); col += 16) {
-            uint32_t v[16];
-            if (ok) tc05::tmem_ld16(tmem + (static_cast<uint32_t>(32 * q) << 16) + col, v);
-            if (dv < p.Dv)
+        if (d0 < DK) {
+            float4 *to = reinterpret_cast<float4 *>(state_of(p, g) + (d0 + lane) * p.Dv);
+            for (int col = half * (p.Dv / 2); col < (half + 1) * (p.Dv / 2); col += 16) {
+                uint32_t v[16];
+                if (ok) tc05::tmem_ld16(tmem + quarter + kU + col, v);
 #pragma unroll
-                for (int i = 0; i < 16; ++i) to[(col + i) * p.Dv] = ok ? __uint_as_float(v[i]) : nan;
+                for (int i = 0; i < 16; i += 4)
+                    to[(col + i) / 4] = ok ? make_float4(__uint_as_float(v[i]), __uint_as_float(v[i + 1]), __uint_as_float(v[i + 2]),
+                                                         __uint_as_float(v[i + 3]))
+                                           : make_float4(nan, nan, nan, nan);
+            }
         }
-        if (w == 0 && lane == 0) p.ws[g] = ok ? exp2f(after.hi + after.lo) : nan;
+        if (warp == 2 && lane == 0) p.ws[g] = ok ? exp2f(after.hi + after.lo) : nan;
     }
     __syncwarp();
     if (lane == 0 && *reinterpret_cast<volatile int *>(&stop) && warp == 0)
@@ -516,7 +590,7 @@ __global__ void __launch_bounds__(kStateThreads, 1) linear_states_kernel(const _
     if (threadIdx.x == 32 && stop) atomicOr(p.err, 1);
     if (warp == 1) {
         tc_fence_after();
-        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmem) : "memory");
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512) : "memory");
     }
 }
 
@@ -568,28 +642,30 @@ __global__ void __launch_bounds__(kJoinThreads) linear_join_kernel(const __grid_
 template <int DK>
 __global__ void __launch_bounds__(kOutThreads, 1) linear_outputs_kernel(const __grid_constant__ LinearParams p) {
     constexpr int kKParts = DK / 64, kKeys = kKParts * kPart;
-    // columns of tensor memory
-    constexpr int kState = 0, kSb = 128, kA = 192, kO = 256;
     extern __shared__ uint8_t raw[];
     uint8_t *base = raw + ((1024u - (saddr(raw) & 1023u)) & 1023u);
     const int vparts = p.Dv / 64, stage = chunk_bytes(DK, p.Dv, true), S = p.stages;
     uint8_t *keys = base + S * stage;   // two buffers of three numbers
     uint8_t *ps = keys + 6 * kKeys;     // two buffers of P
-    uint8_t *misc = ps + 2 * kPart;
+    uint8_t *os = ps + 2 * kPart;       // outputs on their way
+    uint8_t *misc = os + kOutStage;
     uint64_t *bars = reinterpret_cast<uint64_t *>(misc);
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(misc + 512);
     int &stop = *reinterpret_cast<int *>(misc + 516);
-    float *all_e = reinterpret_cast<float *>(misc + 528);  // exp(G) of a chunk
-    // of each of its tokens: G_i as a pair, and exp(G_i)
-    float *ghi = reinterpret_cast<float *>(misc + 1024), *glo = ghi + kSums * kC, *eg = glo + kSums * kC;
+    float *all_e = reinterpret_cast<float *>(misc + 528);  // [kSums] exp(G) of a chunk
+    int *vbad = reinterpret_cast<int *>(misc + 576);       // [4][4] whether a warp's values are not all finite
+    // [kSums][64] of each token: G_i, scale exp(G_i), exp(G - G_i)
+    float *gs = reinterpret_cast<float *>(misc + 1024), *eg = gs + kSums * kC, *wk = eg + kSums * kC;
+    int *first_bad = reinterpret_cast<int *>(wk + kSums * kC);  // [4][128] the first token with such a value
     uint32_t at = saddr(bars);
     auto take = [&](int n) {
         const uint32_t b = at;
         at += 8 * n;
         return b;
     };
-    const uint32_t full = take(kStages), empty = take(kStages), gready = take(kSums), kready = take(2), sdone = take(2), afull = take(1),
-                   afree = take(1), pready = take(2), odone = take(2), ofree = take(2), sready = take(1), fin = take(1);
+    const uint32_t full = take(kStages), empty = take(kStages), gready = take(kSums), kready = take(2), vready = take(2),
+                   sdone = take(2), afull = take(1), afree = take(1), pready = take(2), odone = take(2), ofree = take(1),
+                   sready = take(1), o1done = take(1), fin = take(1);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = static_cast<int>(blockIdx.x);
     if (threadIdx.x == 0) {
         prefetch_tmap(&p.tq);
@@ -603,13 +679,15 @@ __global__ void __launch_bounds__(kOutThreads, 1) linear_outputs_kernel(const __
         init(empty, kStages, 1);
         init(gready, kSums, 1);
         init(kready, 2, 4);
+        init(vready, 2, 4);
         init(sdone, 2, 1);
         init(afull, 1, 1);
         init(afree, 1, 4);
         init(pready, 2, 4);
         init(odone, 2, 1);
-        init(ofree, 2, 4);
+        init(ofree, 1, 4);
         init(sready, 1, 4);
+        init(o1done, 1, 1);
         init(fin, 1, 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -636,6 +714,8 @@ __global__ void __launch_bounds__(kOutThreads, 1) linear_outputs_kernel(const __
     int issued = 0;
     Chunk c;
 
+    // Barriers with two phases in flight are pairs, taken in turn: none is passed twice before everyone who
+    // waits on it has seen it once.
     if (warp == 0) {
         // -------------------------------------------------------------------- the copies
         int slot = 0;
@@ -652,8 +732,8 @@ __global__ void __launch_bounds__(kOutThreads, 1) linear_outputs_kernel(const __
                     bar_arrive(bar);
                 if (!stall && any) {
                     const int hk = c.h / p.share;
-                    for (int i = 0; i < kKParts; ++i) tma_3d(dst + i * kPart, &p.tq, 64 * i, c.t0, hk, bar);
                     for (int i = 0; i < kKParts; ++i) tma_3d(dst + kKeys + i * kPart, &p.tk, 64 * i, c.t0, hk, bar);
+                    for (int i = 0; i < kKParts; ++i) tma_3d(dst + i * kPart, &p.tq, 64 * i, c.t0, hk, bar);
                     for (int i = 0; i < vparts; ++i) tma_3d(dst + 2 * kKeys + i * kPart, &p.tv, 64 * i, c.t0, c.h, bar);
                 }
             }
@@ -665,8 +745,8 @@ __global__ void __launch_bounds__(kOutThreads, 1) linear_outputs_kernel(const __
         }
     } else if (warp == 1) {
         // ------------------------------------------------------------------ the products
-        constexpr uint32_t kIdA = idesc_of(64, 64, false, false), kIdO1 = idesc_of(128, 64, false, false),
-                           kIdO2 = idesc_of(128, 64, true, false), kIdS = idesc_of(128, DK, true, true);
+        constexpr uint32_t kIdA = idesc_of(64, 64, false, false), kIdO = idesc_of(128, 64, false, false),
+                           kIdS = idesc_of(128, DK, false, true);
         const uint32_t d = alike(static_cast<int>(tmem));
         int slot = 0, aslot = 0;  // of the current chunk, of the next A
         unsigned aph = 0;
@@ -693,72 +773,76 @@ __global__ void __launch_bounds__(kOutThreads, 1) linear_outputs_kernel(const __
         };
         scores(0);
         for (int n = 0; ok && n < total; ++n) {
-            const uint32_t st = saddr(base) + slot * stage, o = d + kO + 128 * (n & 1);
-            if (!(ok = all_wait(sready, n & 1, &stop) && (n < 2 || all_wait(ofree + 8 * (n & 1), ((n >> 1) - 1) & 1, &stop)))) break;
+            const uint32_t st = saddr(base) + slot * stage, vt = d + kValueT + 32 * (n & 1);
+            // the state first: its chain is the longest
+            if (!(ok = all_wait(vready + 8 * (n & 1), (n >> 1) & 1, &stop) && all_wait(kready + 8 * (n & 1), (n >> 1) & 1, &stop) &&
+                       all_wait(sready, n & 1, &stop)))
+                break;
+            tc_fence_after();
+            if (elect()) {
+                const uint64_t b = mn_desc(saddr(keys) + (n & 1) * 3 * kKeys);
+#pragma unroll
+                for (int part = 0; part < 3; ++part)
+#pragma unroll
+                    for (int kk = 0; kk < kC / 16; ++kk)
+                        mma_ts(d + kState, vt + 8 * kk, b + ((part * kKeys) >> 4) + kk * (2048 >> 4), kIdS, true);
+                mma_commit(sdone + 8 * (n & 1));
+            }
+            __syncwarp();
+            if (!(ok = n == 0 || all_wait(ofree, (n - 1) & 1, &stop))) break;
             tc_fence_after();
             if (elect()) {
 #pragma unroll
                 for (int i = 0; i < kKParts; ++i)
 #pragma unroll
                     for (int kk = 0; kk < 4; ++kk)
-                        mma_ts(o, d + kSb + 32 * i + 8 * kk, tc05::sw128_desc(st + i * kPart) + ((32 * kk) >> 4), kIdO1, i != 0 || kk != 0);
+                        mma_ts(d + kO1, d + kSb + 32 * i + 8 * kk, tc05::sw128_desc(st + i * kPart) + ((32 * kk) >> 4), kIdO, i != 0 || kk != 0);
+                mma_commit(o1done);
+                mma_commit(empty + 8 * slot);  // keys and values were read before kready and vready
             }
             __syncwarp();
-            if (!(ok = all_wait(kready + 8 * (n & 1), (n >> 1) & 1, &stop))) break;
-            tc_fence_after();
-            if (elect()) {
-                const uint64_t a = mn_desc(st + 2 * kKeys), b = mn_desc(saddr(keys) + (n & 1) * 3 * kKeys);
-#pragma unroll
-                for (int part = 0; part < 3; ++part)
-#pragma unroll
-                    for (int kk = 0; kk < kC / 16; ++kk)
-                        mma(d + kState, a + kk * (2048 >> 4), b + ((part * kKeys) >> 4) + kk * (2048 >> 4), kIdS, true);
-                mma_commit(sdone + 8 * (n & 1));  // (O1 has then read Sb too)
-            }
-            __syncwarp();
+            if (++slot == S) slot = 0;
             if (n + 1 < total) scores(n + 1);
             if (!ok || !(ok = all_wait(pready + 8 * (n & 1), (n >> 1) & 1, &stop))) break;
             tc_fence_after();
             if (elect()) {
-                const uint64_t a = mn_desc(st + 2 * kKeys), b = tc05::sw128_desc(saddr(ps) + (n & 1) * kPart);
+                const uint64_t b = tc05::sw128_desc(saddr(ps) + (n & 1) * kPart);
 #pragma unroll
-                for (int kk = 0; kk < kC / 16; ++kk) mma(o + 64, a + kk * (2048 >> 4), b + ((32 * kk) >> 4), kIdO2, kk != 0);
+                for (int kk = 0; kk < kC / 16; ++kk) mma_ts(d + kO2, vt + 8 * kk, b + ((32 * kk) >> 4), kIdO, kk != 0);
                 mma_commit(odone + 8 * (n & 1));
-                mma_commit(empty + 8 * slot);
             }
             __syncwarp();
-            if (++slot == S) slot = 0;
         }
         finish(fin, &stop);
-    } else if (warp < 4 || warp >= 16) {
-        // ------------------------------------------------------ keys, and the sums of decays
-        const int w = warp < 4 ? warp - 2 : warp - 14;
+    } else if (warp == 2) {
+        // ---------------------------------------------------------------- the sums of decays
         Cursor ahead = cursor;
         Chunk nc;
         Decays next{0.0f, 0.0f};
         if (ahead.next(p, nc)) next = load_g(p, nc);
-        int slot = 0;
-        unsigned ph = 0;
-        bool ok = true;
-        for (int n = 0; cursor.next(p, c); ++n) {
+        for (int n = 0; n < total; ++n) {
             const Decays now = next;
             if (ahead.next(p, nc)) next = load_g(p, nc);
             Pair a, b, all;
             sums_of(now, a, b, all);
-            if (!(ok = n < 2 || all_wait(sdone + 8 * (n & 1), ((n >> 1) - 1) & 1, &stop))) break;
-            if (w == 0) {
-                const int to = (n & (kSums - 1)) * kC + 2 * lane;
-                *reinterpret_cast<float2 *>(&ghi[to]) = make_float2(a.hi, b.hi);
-                *reinterpret_cast<float2 *>(&glo[to]) = make_float2(a.lo, b.lo);
-                *reinterpret_cast<float2 *>(&eg[to]) = make_float2(exp2f(a.hi + a.lo), exp2f(b.hi + b.lo));
-                if (lane == 0) all_e[n & (kSums - 1)] = exp2f(all.hi + all.lo);
-                __syncwarp();
-                if (lane == 0) bar_arrive(gready + 8 * (n & (kSums - 1)));
-            }
-            if (!(ok = all_wait(full + 8 * slot, ph, &stop))) break;
-            uint8_t *out = keys + (n & 1) * 3 * kKeys, *st = base + slot * stage;
-            scale_keys<4, DK>(st + kKeys, out, w, c.valid, exp2f(less(all, a)), exp2f(less(all, b)));
-            if (c.valid < kC) clear_values<4>(st + 2 * kKeys, vparts, w, c.valid);
+            if (n >= 2 && !all_wait(sdone + 8 * (n & 1), ((n >> 1) - 1) & 1, &stop)) break;
+            const int buf = n & (kSums - 1), to = buf * kC + 2 * lane;
+            *reinterpret_cast<float2 *>(&gs[to]) = make_float2(a.hi, b.hi);
+            *reinterpret_cast<float2 *>(&eg[to]) = make_float2(p.scale * exp2f(a.hi + a.lo), p.scale * exp2f(b.hi + b.lo));
+            *reinterpret_cast<float2 *>(&wk[to]) = make_float2(exp2f(less(all, a)), exp2f(less(all, b)));
+            if (lane == 0) all_e[buf] = exp2f(all.hi + all.lo);
+            __syncwarp();
+            if (lane == 0) bar_arrive(gready + 8 * buf);
+        }
+    } else if (warp >= 16) {
+        // -------------------------------------------------------------------------- keys
+        int slot = 0;
+        unsigned ph = 0;
+        for (int n = 0; cursor.next(p, c); ++n) {
+            const int buf = n & (kSums - 1);
+            // (the sums come after the state's product that read this buffer of keys)
+            if (!all_wait(full + 8 * slot, ph, &stop) || !all_wait(gready + 8 * buf, (n / kSums) & 1, &stop)) break;
+            scale_keys<DK>(base + slot * stage + kKeys, keys + (n & 1) * 3 * kKeys, wk + buf * kC, warp - 16, c.valid);
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             __syncwarp();
             if (lane == 0) bar_arrive(kready + 8 * (n & 1));
@@ -767,49 +851,72 @@ __global__ void __launch_bounds__(kOutThreads, 1) linear_outputs_kernel(const __
                 ph ^= 1;
             }
         }
-    } else if (warp < 8) {
+    } else if (warp >= 4 && warp < 8) {
         // -------------------------------------------------------------------- the state
         const int dv = 32 * q + lane;
         const bool mine = dv < p.Dv;
         bool ok = true;
+        float poison = 0.0f;  // NaN once the sequence had a value of this row that is not finite
         for (int n = 0; cursor.next(p, c); ++n) {
-            if (ok) ok = all_wait(gready + 8 * (n & (kSums - 1)), (n / kSums) & 1, &stop);
-            if (ok && !c.head) ok = all_wait(sdone + 8 * ((n - 1) & 1), ((n - 1) >> 1) & 1, &stop);
-            const float *from = nullptr;
+            const int buf = n & (kSums - 1);
+            if (ok) ok = all_wait(gready + 8 * buf, (n / kSums) & 1, &stop);
             if (c.head) {
+                poison = 0.0f;
+                const float *from = nullptr;
                 const long long slot = p.slots[c.b];
                 if (!c.first)
                     from = state_of(p, g - 1);
                 else if (slot >= 0 && slot < p.pool && !(p.fresh && p.fresh[c.b])) {
                     // a sequence cut by the share's end begins with the second kernel's copy
                     from = p.state + slot * p.s_slot + c.h * p.s_head;
-                    if (!c.tail) {
-                        const int a = p.cu[c.b], chunks = (p.cu[c.b + 1] - a + kC - 1) / kC;
-                        if (chunks > total - n) from = begin_state(p, g);
-                    }
+                    const int a = p.cu[c.b], chunks = (p.cu[c.b + 1] - a + kC - 1) / kC;
+                    if (chunks > total - n) from = begin_state(p, g);
                 }
+                if (ok)
+#pragma unroll 1
+                    for (int col = 0; col < DK; col += 32) {
+                        uint32_t v[2][16];
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) v[i >> 4][i & 15] = from && mine ? __float_as_uint(from[(col + i) * p.Dv + dv]) : 0u;
+                        tmem_st16(tmem + quarter + kState + col, v[0]);
+                        tmem_st16(tmem + quarter + kState + col + 16, v[1]);
+                    }
+                asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+            } else {
+                if (ok) ok = all_wait(sdone + 8 * ((n - 1) & 1), ((n - 1) >> 1) & 1, &stop);
+                if (ok && vbad[4 * ((n - 1) & 3) + q] && first_bad[128 * ((n - 1) & 3) + dv] < kC) poison = nan;
             }
             if (ok) {
                 tc_fence_after();
-                const float e = all_e[n & (kSums - 1)];
+                const unsigned long long e = pack_f32x2(all_e[buf], all_e[buf]);
+                const bool poisoned = __any_sync(0xffffffffu, poison != 0.0f);
+                // 16 columns while the next 16 come
+                uint32_t v[2][16];
+                tmem_ld16_soon(tmem + quarter + kState, v[0]);
+                tmem_wait16(v[0]);
+                // O1 of the chunk before has read Sb
+                ok = n == 0 || all_wait(o1done, (n - 1) & 1, &stop);
+                if (ok) tc_fence_after();
 #pragma unroll 1
                 for (int col = 0; col < DK; col += 32) {
-                    uint32_t v[32], sb[16];
-                    if (c.head) {
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) v[i] = from && mine ? __float_as_uint(from[(col + i) * p.Dv + dv]) : 0u;
-                    } else {
-                        tmem_ld32(tmem + quarter + kState + col, v);
-                    }
+                    for (int h = 0; h < 2; ++h) {
+                        const int here = col + 16 * h;
+                        if (here + 16 < DK) tmem_ld16_soon(tmem + quarter + kState + here + 16, v[h ^ 1]);
+                        uint32_t sb[8];
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        const float a = __uint_as_float(v[2 * i]), b = __uint_as_float(v[2 * i + 1]);
-                        sb[i] = bf16x2(a, b);
-                        v[2 * i] = __float_as_uint(a * e);
-                        v[2 * i + 1] = __float_as_uint(b * e);
+                        for (int i = 0; i < 8; ++i) {
+                            if (poisoned) {
+                                v[h][2 * i] = __float_as_uint(__uint_as_float(v[h][2 * i]) + poison);
+                                v[h][2 * i + 1] = __float_as_uint(__uint_as_float(v[h][2 * i + 1]) + poison);
+                            }
+                            sb[i] = bf16x2(__uint_as_float(v[h][2 * i]), __uint_as_float(v[h][2 * i + 1]));
+                            unpack2(mul2(pack2(v[h][2 * i], v[h][2 * i + 1]), e), v[h][2 * i], v[h][2 * i + 1]);
+                        }
+                        tmem_st8(tmem + quarter + kSb + here / 2, sb);
+                        tmem_st16(tmem + quarter + kState + here, v[h]);
+                        if (here + 16 < DK) tmem_wait16(v[h ^ 1]);
                     }
-                    tmem_st16(tmem + quarter + kSb + col / 2, sb);
-                    tmem_st32(tmem + quarter + kState + col, v);
                 }
                 asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
                 tc_fence_before();
@@ -819,6 +926,7 @@ __global__ void __launch_bounds__(kOutThreads, 1) linear_outputs_kernel(const __
             if (c.tail) {
                 // the sequence's last state
                 if (ok) ok = all_wait(sdone + 8 * (n & 1), (n >> 1) & 1, &stop);
+                if (ok && vbad[4 * (n & 3) + q] && first_bad[128 * (n & 3) + dv] < kC) poison = nan;
                 const Seq s = seq_of(p, c.b);
                 const bool fresh = p.fresh && p.fresh[c.b];
                 if (s.slot >= 0 && (s.len > 0 || fresh)) {
@@ -830,22 +938,72 @@ __global__ void __launch_bounds__(kOutThreads, 1) linear_outputs_kernel(const __
                         if (ok) tc05::tmem_ld16(tmem + quarter + kState + col, v);
                         if (mine)
 #pragma unroll
-                            for (int i = 0; i < 16; ++i) to[(col + i) * p.Dv] = ok ? __uint_as_float(v[i]) : nan;
+                            for (int i = 0; i < 16; ++i) to[(col + i) * p.Dv] = ok ? __uint_as_float(v[i]) + poison : nan;
                     }
                     tc_fence_before();
                 }
             }
         }
-    } else if (warp < 12) {
-        // ------------------------------------------------------------- the decays of a chunk
-        bool ok = true;
+    } else if (warp >= 8 && warp < 12) {
+        // ------------------------------------ the values turned, and the decays of a chunk
+        int slot = 0;
+        unsigned ph = 0;
         for (int n = 0; cursor.next(p, c); ++n) {
-            if (!(ok = all_wait(gready + 8 * (n & (kSums - 1)), (n / kSums) & 1, &stop) && all_wait(afull, n & 1, &stop))) break;
-            if (!(ok = n < 2 || all_wait(odone + 8 * (n & 1), ((n >> 1) - 1) & 1, &stop))) break;
+            const int buf = n & (kSums - 1), b4 = n & 3;
+            if (!all_wait(full + 8 * slot, ph, &stop) || (n >= 2 && !all_wait(odone + 8 * (n & 1), ((n >> 1) - 1) & 1, &stop))) break;
+            tc_fence_after();
+            if (32 * q < p.Dv) {
+                const uint32_t vs = saddr(base) + slot * stage + 2 * kKeys;
+                bool any = false;
+#pragma unroll 1
+                for (int h = 0; h < 2; ++h) {  // 16 elements x 64 tokens
+                    uint32_t r[16], x = 0u;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) load_turned(vs, 16 * i, 32 * q + 16 * h, r[4 * i], r[4 * i + 1], r[4 * i + 2], r[4 * i + 3]);
+                    // tokens behind the chunk's are 0, whatever lies there
+                    if (c.valid < kC)
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) {
+                            const int tok = 8 * (i >> 1) + 2 * (lane & 3);
+                            r[i] = tok + 1 < c.valid ? r[i] : tok < c.valid ? r[i] & 0xffffu : 0u;
+                        }
+                    // infinities and NaN: 0 x v is not 0
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) asm("fma.rn.bf16x2 %0, %1, %2, %0;" : "+r"(x) : "r"(r[i]), "r"(0u));
+                    if (__any_sync(0xffffffffu, x != 0u)) {
+                        // They become 0 in the products, which sum over later tokens too, and the row's outputs and
+                        // states NaN from the first such token on.
+                        int *fb = first_bad + 128 * b4 + 32 * q;
+                        if (!any) fb[lane] = kC;
+                        any = true;
+                        __syncwarp();
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) {
+                            const int tok = 8 * (i >> 1) + 2 * (lane & 3), row = 16 * h + 8 * (i & 1) + (lane >> 2);
+                            const bool lo = (r[i] & 0x7f80u) == 0x7f80u, hi = (r[i] & 0x7f800000u) == 0x7f800000u;
+                            if (lo || hi) atomicMin(&fb[row], lo ? tok : tok + 1);
+                            r[i] = finite_or_zero(r[i]);
+                        }
+                    }
+                    tmem_st_turned(tmem + quarter + (static_cast<uint32_t>(16 * h) << 16) + kValueT + 32 * (n & 1), r);
+                }
+                if (lane == 0) vbad[4 * b4 + q] = any;
+                asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+            } else if (lane == 0) {
+                vbad[4 * b4 + q] = 0;
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) bar_arrive(vready + 8 * (n & 1));
+            if (++slot == S) {
+                slot = 0;
+                ph ^= 1;
+            }
+            if (!all_wait(gready + 8 * buf, (n / kSums) & 1, &stop) || !all_wait(afull, n & 1, &stop)) break;
             tc_fence_after();
             const int i0 = 16 * q + (lane >> 2), j0 = 2 * (lane & 3);
-            const float *hi = ghi + (n & (kSums - 1)) * kC, *lo = glo + (n & (kSums - 1)) * kC;
-            const float h0 = hi[i0], l0 = lo[i0], h1 = hi[i0 + 8], l1 = lo[i0 + 8];
+            const float *gj = gs + buf * kC;
+            const float g0 = gj[i0], g1 = gj[i0 + 8];
             // a row's tokens up to its own; none of a row behind the chunk's
             const int last0 = i0 < c.valid ? i0 : -1, last1 = i0 + 8 < c.valid ? i0 + 8 : -1;
             uint8_t *row = ps + (n & 1) * kPart + i0 * 128;
@@ -856,52 +1014,101 @@ __global__ void __launch_bounds__(kOutThreads, 1) linear_outputs_kernel(const __
 #pragma unroll
                 for (int m = 0; m < 2; ++m) {
                     const int j = 16 * t + 8 * m + j0;
-                    const float2 hj = *reinterpret_cast<const float2 *>(&hi[j]), lj = *reinterpret_cast<const float2 *>(&lo[j]);
+                    const float2 g = *reinterpret_cast<const float2 *>(&gj[j]);
                     // (later tokens' exponents may overflow: they are not used)
-                    const float a = j <= last0 ? ex2((h0 - hj.x) + (l0 - lj.x)) * __uint_as_float(r[4 * m]) : 0.0f;
-                    const float b = j + 1 <= last0 ? ex2((h0 - hj.y) + (l0 - lj.y)) * __uint_as_float(r[4 * m + 1]) : 0.0f;
-                    const float e = j <= last1 ? ex2((h1 - hj.x) + (l1 - lj.x)) * __uint_as_float(r[4 * m + 2]) : 0.0f;
-                    const float f = j + 1 <= last1 ? ex2((h1 - hj.y) + (l1 - lj.y)) * __uint_as_float(r[4 * m + 3]) : 0.0f;
+                    const float a = j <= last0 ? ex2(g0 - g.x) * __uint_as_float(r[4 * m]) : 0.0f;
+                    const float b = j + 1 <= last0 ? ex2(g0 - g.y) * __uint_as_float(r[4 * m + 1]) : 0.0f;
+                    const float e = j <= last1 ? ex2(g1 - g.x) * __uint_as_float(r[4 * m + 2]) : 0.0f;
+                    const float f = j + 1 <= last1 ? ex2(g1 - g.y) * __uint_as_float(r[4 * m + 3]) : 0.0f;
                     const int to = (((2 * t + m) ^ (lane >> 2)) << 4) + 2 * j0;  // i0 % 8 = lane / 4
                     *reinterpret_cast<uint32_t *>(row + to) = bf16x2(a, b);
                     *reinterpret_cast<uint32_t *>(row + 8 * 128 + to) = bf16x2(e, f);
                 }
             }
             tc_fence_before();
-            __syncwarp();
-            if (lane == 0) bar_arrive(afree);
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             __syncwarp();
-            if (lane == 0) bar_arrive(pready + 8 * (n & 1));
+            if (lane == 0) {
+                bar_arrive(afree);
+                bar_arrive(pready + 8 * (n & 1));
+            }
         }
-    } else {
+    } else if (warp >= 12) {
         // ------------------------------------------------------------------- the outputs
-        const int dv = 32 * q + lane;
+        // 32 tokens at a time, read in the 16 x 256-bit form, whose fragments stmatrix stores turned:
+        // rows of a token's values, 16 bytes a thread from there on.
+        const int tid = threadIdx.x - 12 * 32, c0 = 2 * (lane & 3);
+        const uint32_t to_s = saddr(os);
+        const unsigned long long scale = pack_f32x2(p.scale, p.scale);
         bool ok = true;
         for (int n = 0; cursor.next(p, c); ++n) {
             if (ok) ok = all_wait(odone + 8 * (n & 1), (n >> 1) & 1, &stop);
             if (ok) tc_fence_after();
-            uint16_t *to = p.out + static_cast<long long>(c.t0) * p.o_token + c.h * p.o_head + dv;
             const float *e = eg + (n & (kSums - 1)) * kC;
-            const int end = dv < p.Dv ? c.valid : 0;
+            const bool bad = ok && vbad[4 * (n & 3) + q] != 0;
+            uint16_t *out = p.out + static_cast<long long>(c.t0) * p.o_token + c.h * p.o_head;
 #pragma unroll 1
-            for (int i = 0; i < kC; i += 16) {
-                if (i >= c.valid) break;
-                uint32_t a[16], b[16];
-                if (ok) {
-                    tc05::tmem_ld16(tmem + quarter + kO + 128 * (n & 1) + i, a);
-                    tc05::tmem_ld16(tmem + quarter + kO + 128 * (n & 1) + 64 + i, b);
-                }
+            for (int t = 0; t < kC; t += 32) {
+                const bool any = t < c.valid;  // (the last turn also frees the accumulators)
+                if (any && 32 * q < p.Dv)
+#pragma unroll 1
+                    for (int h = 0; h < 2; ++h) {
+                        uint32_t a[16], b[16];
+                        if (ok) {
+                            const uint32_t from = tmem + quarter + (static_cast<uint32_t>(16 * h) << 16) + t;
+                            tmem_ld_s(from + kO1, a);
+                            tmem_ld_s(from + kO2, b);
+                            asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+                        } else {
 #pragma unroll
-                for (int j = 0; j < 16; ++j, to += p.o_token)
-                    if (i + j < end) {
-                        const float x = p.scale * fmaf(e[i + j], __uint_as_float(a[j]), __uint_as_float(b[j]));
-                        *to = f32_to_bf16_rn(ok ? x : nan);
+                            for (int i = 0; i < 16; ++i) a[i] = b[i] = __float_as_uint(nan);
+                        }
+                        if (bad)
+#pragma unroll
+                            for (int i = 0; i < 16; ++i) {
+                                const int from = first_bad[128 * (n & 3) + 32 * q + 16 * h + 8 * ((i >> 1) & 1) + (lane >> 2)];
+                                if (t + 8 * (i >> 2) + c0 + (i & 1) >= from) b[i] = __float_as_uint(nan);
+                            }
+#pragma unroll
+                        for (int i = 0; i < 4; i += 2) {
+                            uint32_t o[4];
+#pragma unroll
+                            for (int m = 0; m < 4; ++m) {
+                                const int blk = i + (m >> 1), r = 4 * blk + 2 * (m & 1);
+                                const unsigned long long ee = *reinterpret_cast<const unsigned long long *>(&e[t + 8 * blk + c0]);
+                                uint32_t x, y;
+                                unpack2(ffma2(ee, pack2(a[r], a[r + 1]), mul2(scale, pack2(b[r], b[r + 1]))), x, y);
+                                o[m] = bf16x2(__uint_as_float(x), __uint_as_float(y));
+                            }
+                            stmatrix_turned(to_s + (8 * i + 8 * (lane >> 4) + (lane & 7)) * 256 +
+                                                (((4 * q + 2 * h + ((lane >> 3) & 1)) ^ (lane & 7)) << 4), o);
+                        }
                     }
+                if (t + 32 == kC) {
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) bar_arrive(ofree);
+                }
+                if (!any) continue;
+                asm volatile("bar.sync 1, 128;" ::: "memory");
+                const int shift = p.Dv == 128 ? 4 : 3, end = min(32, c.valid - t) << shift;
+#pragma unroll 4
+                for (int i = tid; i < end; i += 128) {
+                    const int tok = i >> shift, u = i & ((1 << shift) - 1);
+                    const uint4 v = *reinterpret_cast<const uint4 *>(os + tok * 256 + ((u ^ (tok & 7)) << 4));
+                    uint16_t *to = out + (t + tok) * p.o_token + 8 * u;
+                    if (p.out16) {
+                        *reinterpret_cast<uint4 *>(to) = v;
+                    } else {
+                        uint32_t *w = reinterpret_cast<uint32_t *>(to);
+                        w[0] = v.x;
+                        w[1] = v.y;
+                        w[2] = v.z;
+                        w[3] = v.w;
+                    }
+                }
+                asm volatile("bar.sync 1, 128;" ::: "memory");
             }
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) bar_arrive(ofree + 8 * (n & 1));
         }
     }
     __syncwarp();
@@ -918,7 +1125,7 @@ __global__ void __launch_bounds__(kOutThreads, 1) linear_outputs_kernel(const __
 }
 
 int stages_of(int dk, int dv, bool with_q) {
-    const int room = static_cast<int>(kMaxSmemOptin) - 1024 - (with_q ? out_fixed(dk) : state_fixed(dk));
+    const int room = static_cast<int>(kMaxSmemOptin) - 1024 - (with_q ? out_fixed(dk) : kStateFixed);
     return std::min(kStages, room / chunk_bytes(dk, dv, with_q));
 }
 
@@ -1036,6 +1243,7 @@ extern "C" sgemm_status_t sgemm_bf16_linear_attention(const sgemm_linear_attenti
     p.Dk = a->Dk;
     p.Dv = a->Dv;
     p.scale = a->scale;
+    p.out16 = aligned(a->out, 16) && a->o_token % 8 == 0 && a->o_head % 8 == 0 ? 1 : 0;
     p.flags = static_cast<int>(a->flags);
     const cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
     const bool wide = a->Dk == 128;
@@ -1044,7 +1252,7 @@ extern "C" sgemm_status_t sgemm_bf16_linear_attention(const sgemm_linear_attenti
         const void *fn = wide ? reinterpret_cast<const void *>(&linear_states_kernel<128>) : reinterpret_cast<const void *>(&linear_states_kernel<64>);
         if (!allow(fn, done[wide])) return SGEMM_ERR_CUDA;
         p.stages = stages_of(a->Dk, a->Dv, false);
-        const size_t smem = 1024 + static_cast<size_t>(p.stages) * chunk_bytes(a->Dk, a->Dv, false) + state_fixed(a->Dk);
+        const size_t smem = 1024 + static_cast<size_t>(p.stages) * chunk_bytes(a->Dk, a->Dv, false) + kStateFixed;
         if (launch(fn, dim3(static_cast<unsigned>(p.groups)), dim3(kStateThreads), smem, cs, &p) != cudaSuccess) return SGEMM_ERR_CUDA;
         const unsigned slices = static_cast<unsigned>((a->Dk * a->Dv / 4 + kJoinThreads - 1) / kJoinThreads);
         if (launch(reinterpret_cast<const void *>(&linear_join_kernel), dim3(static_cast<unsigned>(p.groups), slices), dim3(kJoinThreads),

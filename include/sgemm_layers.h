@@ -174,9 +174,9 @@ sgemm_status_t sgemm_bf16_linear_step(const sgemm_linear_step_t *args, sgemm_str
  *   set.  Rows of out before cu[0] and from cu[B] on are left as they are.
  * - Two sequences of one call must not name the same slot.
  * - g <= 0 is what this is made for.  exp(g) may exceed 1 as long as no exp(G_i - G_j)
- *   overflows; g = -inf drops what came before.  An infinity or a NaN in q, k or v
- *   reaches results of its own chunk of 64 tokens and later ones of its
- *   sequence and head only.
+ *   overflows; g = -inf drops what came before.  An infinity or a NaN in q reaches its
+ *   token only, in k or g its sequence and head from its token on, in v the same for its
+ *   element (as an infinity or NaN).
  * - Sizes, alignments and strides as for sgemm_bf16_linear_step; N < 2^31 / Hv.
  * - workspace: device scratch of at least sgemm_linear_attention_workspace bytes
  *   (16-byte aligned; may be NULL where that is 0), as for the other operators.

@@ -353,3 +353,40 @@ def test_stalled_copies_end_in_nan_and_an_error():
     out, _ = prompt(*p, lens, errors=1, flags=sk.SGEMM_FLAG_TEST_STALL)
     assert torch.isnan(out).all()
     compare(lens, 2, 2, seed=13)
+
+
+def test_what_is_not_finite_reaches_later_tokens_only():
+    """In q its token, in k and g its head from its token on (of the states, k the element's row), in v its
+    element from its token on."""
+    n = 400
+    p = problem([n], 4, 4, 128, 128, 14)
+    clean, _ = prompt(*p, [n])
+    q, k, v, g = p[:4]
+    q[100, 0] = NAN
+    k[150, 1, 7] = INF
+    v[77, 2, 5], v[200, 2, 100], v[201, 2, 100], v[333, 2, 64] = NAN, -INF, NAN, INF
+    g[390, 3] = NAN
+    out, s = prompt(*p, [n])
+    hit = torch.zeros((n, 4, 128), dtype=torch.bool)
+    hit[100, 0] = True
+    hit[150:, 1] = True
+    hit[77:, 2, 5], hit[200:, 2, 100], hit[333:, 2, 64] = True, True, True
+    hit[390:, 3] = True
+    assert torch.equal(out.cpu()[~hit], clean.cpu()[~hit])
+    assert not torch.isfinite(out.cpu()[hit]).any()
+    last = s[p[5][0]].cpu()
+    assert torch.isfinite(last[0]).all() and not torch.isfinite(last[3]).any()
+    assert not torch.isfinite(last[1][7]).any()  # a key element's row of the state
+    assert torch.isfinite(last[1][torch.arange(128) != 7]).all()
+    gone = torch.zeros(128, dtype=torch.bool)
+    gone[[5, 64, 100]] = True
+    assert not torch.isfinite(last[2][:, gone]).any() and torch.isfinite(last[2][:, ~gone]).all()
+
+
+def test_rows_of_out_that_start_on_four_bytes():
+    n = 130
+    p = problem([n], 2, 2, 128, 128, 15)
+    wide = torch.full((n, 2, 134), 9.0, dtype=torch.bfloat16, device=DEV)
+    out, _ = prompt(*p, [n], out=wide[:, :, 2:130])
+    dense, _ = prompt(*p, [n])
+    assert torch.equal(out, dense) and torch.all(wide[:, :, :2] == 9) and torch.all(wide[:, :, 130:] == 9)
