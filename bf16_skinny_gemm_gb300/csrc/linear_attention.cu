@@ -34,7 +34,7 @@
 // state's only error above FP32's, 2^-9 of every summand (in two numbers 2^-18), and it goes on to all later
 // tokens.  P and Sb are rounded once: what they make is rounded to BF16 right after.
 // Roles: a warp copies (TMA, a ring of chunks), a warp issues all products, a warp sums the decays, and
-// four each scale the keys, carry the state, turn the values and apply the decays to A, and write the outputs.
+// four each turn the values and scale the keys, carry the state, apply the decays to A, and write the outputs.
 // Exponents' sums are kept as pairs of FP32 numbers where states are made of them: differences of long sums
 // keep their digits.
 // The roles' loops are short on purpose: unrolled, their code did not fit the instruction cache, and a chunk
@@ -173,6 +173,8 @@ __device__ __forceinline__ Place place_of(const LinearParams &p, int u) {
     }
 }
 
+constexpr int kHead = 256, kTail = 512, kFirst = 1024;  // flags beside a chunk's tokens
+
 // The chunks of a share one by one.
 struct Chunk {
     int b, h, t0, valid;  // first token, tokens
@@ -207,6 +209,29 @@ struct Cursor {
         return true;
     }
 };
+
+// A wait of a whole warp, as all_wait; what it does when the phase is not there yet is one function for all
+// roles (the instruction cache).
+__device__ __noinline__ bool long_wait(uint32_t b, unsigned parity, int *stop) {
+    return __all_sync(0xffffffffu, wait_or_stop(b, parity, stop));
+}
+__device__ __forceinline__ bool phase(uint32_t b, int parity, int *stop) {
+    return __all_sync(0xffffffffu, bar_try(b, static_cast<unsigned>(parity & 1))) || long_wait(b, static_cast<unsigned>(parity & 1), stop);
+}
+
+// Whether a predicate holds for all of the 128 threads that meet at barrier 1.
+__device__ __forceinline__ bool all_of(bool v) {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.b32 p, %1, 0;\n\t"
+        "bar.red.and.pred q, 1, 128, p;\n\t"
+        "selp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(r)
+        : "r"(v ? 1u : 0u)
+        : "memory");
+    return r != 0;
+}
 
 // Scratch: the sum of g of each share's cut piece, then its state (what the next share begins
 // with, after the joining), then what a cut sequence begins with.
@@ -254,7 +279,7 @@ __device__ __forceinline__ void sums_of(Decays d, Pair &a, Pair &b, Pair &all) {
     d.b = d.b < kLeast ? kLeast : d.b;
     const Pair pa{d.a, 0.0f}, pb{d.b, 0.0f};
     Pair x = add(pa, pb);
-#pragma unroll
+#pragma unroll 1
     for (int off = 1; off < 32; off <<= 1) {
         const Pair y{__shfl_up_sync(0xffffffffu, x.hi, off), __shfl_up_sync(0xffffffffu, x.lo, off)};
         if (lane >= off) x = add(y, x);
@@ -345,69 +370,64 @@ __device__ __forceinline__ void split(uint32_t v, unsigned long long f, uint32_t
     }
 }
 
-// 16 columns of the warp's lanes; they are there after the wait.
-__device__ __forceinline__ void tmem_ld16_soon(uint32_t addr, uint32_t (&r)[16]) {
+// 32 columns of the warp's lanes.
+__device__ __forceinline__ void tmem_ld32(uint32_t addr, uint32_t (&r)[32]) {
     asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
-        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19, "
+        "%20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
         : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
-          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]),
+          "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]),
+          "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]),
+          "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
         : "r"(addr));
+    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 }
-__device__ __forceinline__ void tmem_wait16(uint32_t (&r)[16]) {
-    asm volatile("tcgen05.wait::ld.sync.aligned;"
-                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
-                   "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]),
-                   "+r"(r[15])
-                 :
-                 : "memory");
-}
-__device__ __forceinline__ void tmem_st8(uint32_t addr, const uint32_t (&r)[8]) {
-    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(addr), "r"(r[0]), "r"(r[1]),
-                 "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
-                 : "memory");
+__device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t (&r)[32]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
+        "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19, %20, "
+        "%21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(addr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
+        "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]),
+        "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]),
+        "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+        : "memory");
 }
 
 // A chunk's keys times their factors w, as three BF16 numbers each (arrays DK / 64 parts apart), by four warps,
-// 32 units of 16 bytes at a time, four times in flight.  Rows from `valid` on are 0, whatever lies there.
+// 32 units of 16 bytes at a time.  Rows from `valid` on are 0, whatever lies there.
 template <int DK>
 __device__ __forceinline__ void scale_keys(const uint8_t *k, uint8_t *out, const float *w, int warp, int valid) {
     constexpr int kUnits = DK / 8, kRows = 32 / kUnits, kEach = kC / 4;  // units a row, rows at a time, rows a warp
-    constexpr int kKeys = DK / 64 * kPart, kBatch = 4;
+    constexpr int kKeys = DK / 64 * kPart;
     const int lane = threadIdx.x & 31, u = lane % kUnits;
+    const int row0 = warp * kEach + lane / kUnits;
+    auto place = [&](int row) { return (u >> 3) * kPart + row * 128 + (((u & 7) ^ (row & 7)) << 4); };
+    uint4 next = *reinterpret_cast<const uint4 *>(k + place(row0));
 #pragma unroll 1
-    for (int i = 0; i < kEach; i += kBatch * kRows) {
-        uint4 x[kBatch];
-        float f[kBatch];
-        const int row0 = warp * kEach + i + lane / kUnits;
-        auto place = [&](int m) {
-            const int row = row0 + m * kRows;
-            return (u >> 3) * kPart + row * 128 + (((u & 7) ^ (row & 7)) << 4);
-        };
+    for (int row = row0; row < (warp + 1) * kEach; row += kRows) {
+        const uint4 x = next;
+        const float f = w[row];
+        if (row + kRows < (warp + 1) * kEach) next = *reinterpret_cast<const uint4 *>(k + place(row + kRows));
+        const bool in = row < valid;
+        const uint32_t v[4] = {x.x, x.y, x.z, x.w};
+        const unsigned long long ff = pack_f32x2(f, f);
+        uint32_t o[4][3];
 #pragma unroll
-        for (int m = 0; m < kBatch; ++m) {
-            x[m] = *reinterpret_cast<const uint4 *>(k + place(m));
-            f[m] = w[row0 + m * kRows];
-        }
+        for (int e = 0; e < 4; ++e) split(in ? v[e] : 0u, ff, o[e]);
+        uint8_t *to = out + place(row);
 #pragma unroll
-        for (int m = 0; m < kBatch; ++m) {
-            const bool in = row0 + m * kRows < valid;
-            const uint32_t v[4] = {x[m].x, x[m].y, x[m].z, x[m].w};
-            const unsigned long long ff = pack_f32x2(f[m], f[m]);
-            uint32_t o[4][3];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) split(in ? v[e] : 0u, ff, o[e]);
-#pragma unroll
-            for (int s = 0; s < 3; ++s) *reinterpret_cast<uint4 *>(out + s * kKeys + place(m)) = make_uint4(o[0][s], o[1][s], o[2][s], o[3][s]);
-        }
+        for (int s = 0; s < 3; ++s) *reinterpret_cast<uint4 *>(to + s * kKeys) = make_uint4(o[0][s], o[1][s], o[2][s], o[3][s]);
     }
 }
 
 __host__ __device__ constexpr int chunk_bytes(int dk, int dv, bool with_q) { return ((with_q ? 2 : 1) * dk + dv) / 64 * kPart; }
 // barriers, and arrays of each chunk's tokens or values
 constexpr int kMiscOut = 1024 + 3 * kSums * kC * 4 + 4 * 128 * 4;
-constexpr int kOutStage = 32 * 256;  // 32 tokens' outputs on their way
-__host__ __device__ constexpr int out_fixed(int dk) { return 2 * 3 * dk / 64 * kPart + 2 * kPart + kOutStage + kMiscOut; }
+constexpr int kOutStage = kC * 256;  // a chunk's outputs on their way
+__host__ __device__ constexpr int out_fixed(int dk) { return 2 * 3 * dk / 64 * kPart + kPart + kOutStage + kMiscOut; }
 constexpr int kStateFixed = 512;
 // Columns of tensor memory: the state kernel's (U, two buffers of keys in three numbers), the output kernel's
 // (two buffers of values).
@@ -465,7 +485,7 @@ __global__ void __launch_bounds__(kStateThreads, 1) linear_states_kernel(const _
         int slot = 0;
         unsigned ph = 1;
         for (int n = 0; n < chunks; ++n) {
-            if (n >= S && !all_wait(empty + 8 * slot, ph, &stop)) break;
+            if (n >= S && !phase(empty + 8 * slot, ph, &stop)) break;
             if (!stall) issued = n + 1;
             const uint32_t dst = saddr(base) + slot * stage, bar = full + 8 * slot;
             if (elect()) {
@@ -487,7 +507,7 @@ __global__ void __launch_bounds__(kStateThreads, 1) linear_states_kernel(const _
         unsigned ph = 0;
         const uint32_t d = alike(static_cast<int>(tmem)), idesc = alike(static_cast<int>(idesc_of(128, p.Dv, false, true)));
         for (int n = 0; n < chunks; ++n) {
-            if (!all_wait(full + 8 * slot, ph, &stop) || !all_wait(kready + 8 * (n & 1), (n >> 1) & 1, &stop)) break;
+            if (!phase(full + 8 * slot, ph, &stop) || !phase(kready + 8 * (n & 1), (n >> 1) & 1, &stop)) break;
             tc_fence_after();
             if (elect()) {
                 const uint64_t b = mn_desc(saddr(base) + slot * stage + kKeys);
@@ -528,7 +548,7 @@ __global__ void __launch_bounds__(kStateThreads, 1) linear_states_kernel(const _
             sums_of(now, a, b, all);
             after = add(all, after);
             const float wa = exp2f(less(after, a)), wb = exp2f(less(after, b));
-            ok = all_wait(full + 8 * slot, ph, &stop) && (n < 2 || all_wait(kfree + 8 * (n & 1), ((n >> 1) - 1) & 1, &stop));
+            ok = phase(full + 8 * slot, ph, &stop) && (n < 2 || phase(kfree + 8 * (n & 1), ((n >> 1) - 1) & 1, &stop));
             if (!ok) break;
             if (n >= 2) tc_fence_after();
             if (d0 < DK) {
@@ -564,7 +584,7 @@ __global__ void __launch_bounds__(kStateThreads, 1) linear_states_kernel(const _
             }
         }
         // the piece's state, [Dk][Dv]: a row a lane, half of the columns a warp
-        ok = ok && all_wait(fin, 0, &stop) && *reinterpret_cast<volatile int *>(&stop) == 0;
+        ok = ok && phase(fin, 0, &stop) && *reinterpret_cast<volatile int *>(&stop) == 0;
         ok = __all_sync(0xffffffffu, ok);
         const float nan = __int_as_float(0x7fc00000);
         tc_fence_after();
@@ -646,8 +666,8 @@ __global__ void __launch_bounds__(kOutThreads, 1) linear_outputs_kernel(const __
     uint8_t *base = raw + ((1024u - (saddr(raw) & 1023u)) & 1023u);
     const int vparts = p.Dv / 64, stage = chunk_bytes(DK, p.Dv, true), S = p.stages;
     uint8_t *keys = base + S * stage;   // two buffers of three numbers
-    uint8_t *ps = keys + 6 * kKeys;     // two buffers of P
-    uint8_t *os = ps + 2 * kPart;       // outputs on their way
+    uint8_t *ps = keys + 6 * kKeys;     // P
+    uint8_t *os = ps + kPart;           // outputs on their way
     uint8_t *misc = os + kOutStage;
     uint64_t *bars = reinterpret_cast<uint64_t *>(misc);
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(misc + 512);
@@ -657,14 +677,18 @@ __global__ void __launch_bounds__(kOutThreads, 1) linear_outputs_kernel(const __
     // [kSums][64] of each token: G_i, scale exp(G_i), exp(G - G_i)
     float *gs = reinterpret_cast<float *>(misc + 1024), *eg = gs + kSums * kC, *wk = eg + kSums * kC;
     int *first_bad = reinterpret_cast<int *>(wk + kSums * kC);  // [4][128] the first token with such a value
+    // [8] what chunk n is, by the warp of the sums: {b, h, first token, tokens and flags}
+    int4 *told = reinterpret_cast<int4 *>(misc + 640);
     uint32_t at = saddr(bars);
     auto take = [&](int n) {
         const uint32_t b = at;
         at += 8 * n;
         return b;
     };
-    const uint32_t full = take(kStages), empty = take(kStages), gready = take(kSums), kready = take(2), vready = take(2),
-                   sdone = take(2), afull = take(1), afree = take(1), pready = take(2), odone = take(2), ofree = take(1),
+    // values, keys and queries of a slot by themselves: each is free when it was read
+    const uint32_t vfull = take(kStages), kfull = take(kStages), qfull = take(kStages), vempty = take(kStages),
+                   kempty = take(kStages), qempty = take(kStages), gready = take(kSums), kready = take(2), vready = take(2),
+                   sdone = take(2), afull = take(1), afree = take(1), pready = take(1), odone = take(2), ofree = take(1),
                    sready = take(1), o1done = take(1), fin = take(1);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = static_cast<int>(blockIdx.x);
     if (threadIdx.x == 0) {
@@ -675,15 +699,19 @@ __global__ void __launch_bounds__(kOutThreads, 1) linear_outputs_kernel(const __
         auto init = [&](uint32_t b, int n, int count) {
             for (int i = 0; i < n; ++i) bar_init(b + 8 * i, static_cast<unsigned>(count));
         };
-        init(full, kStages, 1);
-        init(empty, kStages, 1);
+        init(vfull, kStages, 1);
+        init(kfull, kStages, 1);
+        init(qfull, kStages, 1);
+        init(vempty, kStages, 4);
+        init(kempty, kStages, 5);
+        init(qempty, kStages, 1);
         init(gready, kSums, 1);
         init(kready, 2, 4);
         init(vready, 2, 4);
         init(sdone, 2, 1);
         init(afull, 1, 1);
         init(afree, 1, 4);
-        init(pready, 2, 4);
+        init(pready, 1, 4);
         init(odone, 2, 1);
         init(ofree, 1, 4);
         init(sready, 1, 4);
@@ -711,8 +739,19 @@ __global__ void __launch_bounds__(kOutThreads, 1) linear_outputs_kernel(const __
     const int total = sh.u1 - sh.u0;
     const int q = warp & 3;
     const uint32_t quarter = static_cast<uint32_t>(32 * q) << 16;
-    int issued = 0;
+    int issued = 0, vissued = 0, qissued = 0;
     Chunk c;
+    // (the sums of chunk n + 8 come after the state's product of n + 6, so after n's outputs)
+    auto hear = [&](int n) {
+        const int4 v = told[n & 7];
+        c.b = v.x;
+        c.h = v.y;
+        c.t0 = v.z;
+        c.valid = v.w & 255;
+        c.head = (v.w & kHead) != 0;
+        c.tail = (v.w & kTail) != 0;
+        c.first = (v.w & kFirst) != 0;
+    };
 
     // Barriers with two phases in flight are pairs, taken in turn: none is passed twice before everyone who
     // waits on it has seen it once.
@@ -721,23 +760,27 @@ __global__ void __launch_bounds__(kOutThreads, 1) linear_outputs_kernel(const __
         int slot = 0;
         unsigned ph = 1;
         for (int n = 0; cursor.next(p, c); ++n) {
-            if (n >= S && !all_wait(empty + 8 * slot, ph, &stop)) break;
             const bool any = c.valid > 0;  // (of a sequence without tokens nothing is read)
-            if (!stall && any) issued = n + 1;
-            const uint32_t dst = saddr(base) + slot * stage, bar = full + 8 * slot;
-            if (elect()) {
-                if (any)
-                    bar_expect_tx(bar, static_cast<unsigned>(stage));
-                else
-                    bar_arrive(bar);
-                if (!stall && any) {
-                    const int hk = c.h / p.share;
-                    for (int i = 0; i < kKParts; ++i) tma_3d(dst + kKeys + i * kPart, &p.tk, 64 * i, c.t0, hk, bar);
-                    for (int i = 0; i < kKParts; ++i) tma_3d(dst + i * kPart, &p.tq, 64 * i, c.t0, hk, bar);
-                    for (int i = 0; i < vparts; ++i) tma_3d(dst + 2 * kKeys + i * kPart, &p.tv, 64 * i, c.t0, c.h, bar);
+            const int hk = c.h / p.share;
+            // part of the slot: `parts` boxes of one operand
+            auto copy = [&](uint32_t full, uint32_t empty, const CUtensorMap &map, int at, int parts, int head, int &count) {
+                if (n >= S && !phase(empty + 8 * slot, ph, &stop)) return false;
+                if (!stall && any) count = n + 1;
+                if (elect()) {
+                    const uint32_t dst = saddr(base) + slot * stage + at, bar = full + 8 * slot;
+                    if (any)
+                        bar_expect_tx(bar, static_cast<unsigned>(parts * kPart));
+                    else
+                        bar_arrive(bar);
+                    if (!stall && any)
+                        for (int i = 0; i < parts; ++i) tma_3d(dst + i * kPart, &map, 64 * i, c.t0, head, bar);
                 }
-            }
-            __syncwarp();
+                __syncwarp();
+                return true;
+            };
+            if (!copy(kfull, kempty, p.tk, kKeys, kKParts, hk, issued) || !copy(vfull, vempty, p.tv, 2 * kKeys, vparts, c.h, vissued) ||
+                !copy(qfull, qempty, p.tq, 0, kKParts, hk, qissued))
+                break;
             if (++slot == S) {
                 slot = 0;
                 ph ^= 1;
@@ -752,7 +795,7 @@ __global__ void __launch_bounds__(kOutThreads, 1) linear_outputs_kernel(const __
         unsigned aph = 0;
         bool ok = true;
         auto scores = [&](int n) {
-            ok = all_wait(full + 8 * aslot, aph, &stop) && (n == 0 || all_wait(afree, (n - 1) & 1, &stop));
+            ok = phase(qfull + 8 * aslot, aph, &stop) && phase(kfull + 8 * aslot, aph, &stop) && (n == 0 || phase(afree, (n - 1) & 1, &stop));
             if (!ok) return;
             tc_fence_after();
             if (elect()) {
@@ -764,6 +807,7 @@ __global__ void __launch_bounds__(kOutThreads, 1) linear_outputs_kernel(const __
                         mma(d + kA, tc05::sw128_desc(st + i * kPart) + ((32 * kk) >> 4),
                             tc05::sw128_desc(st + kKeys + i * kPart) + ((32 * kk) >> 4), kIdA, i != 0 || kk != 0);
                 mma_commit(afull);
+                mma_commit(kempty + 8 * aslot);
             }
             __syncwarp();
             if (++aslot == S) {
@@ -775,8 +819,8 @@ __global__ void __launch_bounds__(kOutThreads, 1) linear_outputs_kernel(const __
         for (int n = 0; ok && n < total; ++n) {
             const uint32_t st = saddr(base) + slot * stage, vt = d + kValueT + 32 * (n & 1);
             // the state first: its chain is the longest
-            if (!(ok = all_wait(vready + 8 * (n & 1), (n >> 1) & 1, &stop) && all_wait(kready + 8 * (n & 1), (n >> 1) & 1, &stop) &&
-                       all_wait(sready, n & 1, &stop)))
+            if (!(ok = phase(vready + 8 * (n & 1), (n >> 1) & 1, &stop) && phase(kready + 8 * (n & 1), (n >> 1) & 1, &stop) &&
+                       phase(sready, n & 1, &stop)))
                 break;
             tc_fence_after();
             if (elect()) {
@@ -789,7 +833,7 @@ __global__ void __launch_bounds__(kOutThreads, 1) linear_outputs_kernel(const __
                 mma_commit(sdone + 8 * (n & 1));
             }
             __syncwarp();
-            if (!(ok = n == 0 || all_wait(ofree, (n - 1) & 1, &stop))) break;
+            if (!(ok = n == 0 || phase(ofree, (n - 1) & 1, &stop))) break;
             tc_fence_after();
             if (elect()) {
 #pragma unroll
@@ -798,20 +842,20 @@ __global__ void __launch_bounds__(kOutThreads, 1) linear_outputs_kernel(const __
                     for (int kk = 0; kk < 4; ++kk)
                         mma_ts(d + kO1, d + kSb + 32 * i + 8 * kk, tc05::sw128_desc(st + i * kPart) + ((32 * kk) >> 4), kIdO, i != 0 || kk != 0);
                 mma_commit(o1done);
-                mma_commit(empty + 8 * slot);  // keys and values were read before kready and vready
+                mma_commit(qempty + 8 * slot);
             }
             __syncwarp();
             if (++slot == S) slot = 0;
-            if (n + 1 < total) scores(n + 1);
-            if (!ok || !(ok = all_wait(pready + 8 * (n & 1), (n >> 1) & 1, &stop))) break;
+            if (!(ok = phase(pready, n, &stop))) break;
             tc_fence_after();
             if (elect()) {
-                const uint64_t b = tc05::sw128_desc(saddr(ps) + (n & 1) * kPart);
+                const uint64_t b = tc05::sw128_desc(saddr(ps));
 #pragma unroll
                 for (int kk = 0; kk < kC / 16; ++kk) mma_ts(d + kO2, vt + 8 * kk, b + ((32 * kk) >> 4), kIdO, kk != 0);
                 mma_commit(odone + 8 * (n & 1));
             }
             __syncwarp();
+            if (n + 1 < total) scores(n + 1);
         }
         finish(fin, &stop);
     } else if (warp == 2) {
@@ -822,136 +866,34 @@ __global__ void __launch_bounds__(kOutThreads, 1) linear_outputs_kernel(const __
         if (ahead.next(p, nc)) next = load_g(p, nc);
         for (int n = 0; n < total; ++n) {
             const Decays now = next;
+            const int4 what = make_int4(nc.b, nc.h, nc.t0, nc.valid | (nc.head ? kHead : 0) | (nc.tail ? kTail : 0) | (nc.first ? kFirst : 0));
             if (ahead.next(p, nc)) next = load_g(p, nc);
             Pair a, b, all;
             sums_of(now, a, b, all);
-            if (n >= 2 && !all_wait(sdone + 8 * (n & 1), ((n >> 1) - 1) & 1, &stop)) break;
+            if (n >= 2 && !phase(sdone + 8 * (n & 1), ((n >> 1) - 1) & 1, &stop)) break;
             const int buf = n & (kSums - 1), to = buf * kC + 2 * lane;
             *reinterpret_cast<float2 *>(&gs[to]) = make_float2(a.hi, b.hi);
             *reinterpret_cast<float2 *>(&eg[to]) = make_float2(p.scale * exp2f(a.hi + a.lo), p.scale * exp2f(b.hi + b.lo));
             *reinterpret_cast<float2 *>(&wk[to]) = make_float2(exp2f(less(all, a)), exp2f(less(all, b)));
-            if (lane == 0) all_e[buf] = exp2f(all.hi + all.lo);
+            if (lane == 0) {
+                all_e[buf] = exp2f(all.hi + all.lo);
+                told[n & 7] = what;
+            }
             __syncwarp();
             if (lane == 0) bar_arrive(gready + 8 * buf);
         }
     } else if (warp >= 16) {
-        // -------------------------------------------------------------------------- keys
+        // ------------------------------------------- the values turned, and the scaled keys
         int slot = 0;
         unsigned ph = 0;
-        for (int n = 0; cursor.next(p, c); ++n) {
-            const int buf = n & (kSums - 1);
-            // (the sums come after the state's product that read this buffer of keys)
-            if (!all_wait(full + 8 * slot, ph, &stop) || !all_wait(gready + 8 * buf, (n / kSums) & 1, &stop)) break;
-            scale_keys<DK>(base + slot * stage + kKeys, keys + (n & 1) * 3 * kKeys, wk + buf * kC, warp - 16, c.valid);
-            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-            __syncwarp();
-            if (lane == 0) bar_arrive(kready + 8 * (n & 1));
-            if (++slot == S) {
-                slot = 0;
-                ph ^= 1;
-            }
-        }
-    } else if (warp >= 4 && warp < 8) {
-        // -------------------------------------------------------------------- the state
-        const int dv = 32 * q + lane;
-        const bool mine = dv < p.Dv;
-        bool ok = true;
-        float poison = 0.0f;  // NaN once the sequence had a value of this row that is not finite
-        for (int n = 0; cursor.next(p, c); ++n) {
-            const int buf = n & (kSums - 1);
-            if (ok) ok = all_wait(gready + 8 * buf, (n / kSums) & 1, &stop);
-            if (c.head) {
-                poison = 0.0f;
-                const float *from = nullptr;
-                const long long slot = p.slots[c.b];
-                if (!c.first)
-                    from = state_of(p, g - 1);
-                else if (slot >= 0 && slot < p.pool && !(p.fresh && p.fresh[c.b])) {
-                    // a sequence cut by the share's end begins with the second kernel's copy
-                    from = p.state + slot * p.s_slot + c.h * p.s_head;
-                    const int a = p.cu[c.b], chunks = (p.cu[c.b + 1] - a + kC - 1) / kC;
-                    if (chunks > total - n) from = begin_state(p, g);
-                }
-                if (ok)
-#pragma unroll 1
-                    for (int col = 0; col < DK; col += 32) {
-                        uint32_t v[2][16];
-#pragma unroll
-                        for (int i = 0; i < 32; ++i) v[i >> 4][i & 15] = from && mine ? __float_as_uint(from[(col + i) * p.Dv + dv]) : 0u;
-                        tmem_st16(tmem + quarter + kState + col, v[0]);
-                        tmem_st16(tmem + quarter + kState + col + 16, v[1]);
-                    }
-                asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
-            } else {
-                if (ok) ok = all_wait(sdone + 8 * ((n - 1) & 1), ((n - 1) >> 1) & 1, &stop);
-                if (ok && vbad[4 * ((n - 1) & 3) + q] && first_bad[128 * ((n - 1) & 3) + dv] < kC) poison = nan;
-            }
-            if (ok) {
-                tc_fence_after();
-                const unsigned long long e = pack_f32x2(all_e[buf], all_e[buf]);
-                const bool poisoned = __any_sync(0xffffffffu, poison != 0.0f);
-                // 16 columns while the next 16 come
-                uint32_t v[2][16];
-                tmem_ld16_soon(tmem + quarter + kState, v[0]);
-                tmem_wait16(v[0]);
-                // O1 of the chunk before has read Sb
-                ok = n == 0 || all_wait(o1done, (n - 1) & 1, &stop);
-                if (ok) tc_fence_after();
-#pragma unroll 1
-                for (int col = 0; col < DK; col += 32) {
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        const int here = col + 16 * h;
-                        if (here + 16 < DK) tmem_ld16_soon(tmem + quarter + kState + here + 16, v[h ^ 1]);
-                        uint32_t sb[8];
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) {
-                            if (poisoned) {
-                                v[h][2 * i] = __float_as_uint(__uint_as_float(v[h][2 * i]) + poison);
-                                v[h][2 * i + 1] = __float_as_uint(__uint_as_float(v[h][2 * i + 1]) + poison);
-                            }
-                            sb[i] = bf16x2(__uint_as_float(v[h][2 * i]), __uint_as_float(v[h][2 * i + 1]));
-                            unpack2(mul2(pack2(v[h][2 * i], v[h][2 * i + 1]), e), v[h][2 * i], v[h][2 * i + 1]);
-                        }
-                        tmem_st8(tmem + quarter + kSb + here / 2, sb);
-                        tmem_st16(tmem + quarter + kState + here, v[h]);
-                        if (here + 16 < DK) tmem_wait16(v[h ^ 1]);
-                    }
-                }
-                asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) bar_arrive(sready);
-            }
-            if (c.tail) {
-                // the sequence's last state
-                if (ok) ok = all_wait(sdone + 8 * (n & 1), (n >> 1) & 1, &stop);
-                if (ok && vbad[4 * (n & 3) + q] && first_bad[128 * (n & 3) + dv] < kC) poison = nan;
-                const Seq s = seq_of(p, c.b);
-                const bool fresh = p.fresh && p.fresh[c.b];
-                if (s.slot >= 0 && (s.len > 0 || fresh)) {
-                    float *to = p.state + s.slot * p.s_slot + c.h * p.s_head + dv;
-                    tc_fence_after();
-#pragma unroll 1
-                    for (int col = 0; col < DK; col += 16) {
-                        uint32_t v[16];
-                        if (ok) tc05::tmem_ld16(tmem + quarter + kState + col, v);
-                        if (mine)
-#pragma unroll
-                            for (int i = 0; i < 16; ++i) to[(col + i) * p.Dv] = ok ? __uint_as_float(v[i]) + poison : nan;
-                    }
-                    tc_fence_before();
-                }
-            }
-        }
-    } else if (warp >= 8 && warp < 12) {
-        // ------------------------------------ the values turned, and the decays of a chunk
-        int slot = 0;
-        unsigned ph = 0;
-        for (int n = 0; cursor.next(p, c); ++n) {
+        for (int n = 0; n < total; ++n) {
             const int buf = n & (kSums - 1), b4 = n & 3;
-            if (!all_wait(full + 8 * slot, ph, &stop) || (n >= 2 && !all_wait(odone + 8 * (n & 1), ((n >> 1) - 1) & 1, &stop))) break;
+            // (the sums come after the state's product that read this buffer of keys)
+            if (!phase(gready + 8 * buf, n / kSums, &stop) || !phase(vfull + 8 * slot, ph, &stop) ||
+                (n >= 2 && !phase(odone + 8 * (n & 1), (n >> 1) - 1, &stop)))
+                break;
             tc_fence_after();
+            hear(n);
             if (32 * q < p.Dv) {
                 const uint32_t vs = saddr(base) + slot * stage + 2 * kKeys;
                 bool any = false;
@@ -994,19 +936,125 @@ __global__ void __launch_bounds__(kOutThreads, 1) linear_outputs_kernel(const __
             }
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) bar_arrive(vready + 8 * (n & 1));
+            if (lane == 0) {
+                bar_arrive(vready + 8 * (n & 1));
+                bar_arrive(vempty + 8 * slot);
+            }
+            if (!phase(kfull + 8 * slot, ph, &stop)) break;
+            scale_keys<DK>(base + slot * stage + kKeys, keys + (n & 1) * 3 * kKeys, wk + buf * kC, warp - 16, c.valid);
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            __syncwarp();
+            if (lane == 0) {
+                bar_arrive(kready + 8 * (n & 1));
+                bar_arrive(kempty + 8 * slot);
+            }
             if (++slot == S) {
                 slot = 0;
                 ph ^= 1;
             }
-            if (!all_wait(gready + 8 * buf, (n / kSums) & 1, &stop) || !all_wait(afull, n & 1, &stop)) break;
+        }
+    } else if (warp >= 4 && warp < 8) {
+        // -------------------------------------------------------------------- the state
+        const int dv = 32 * q + lane;
+        const bool mine = dv < p.Dv;
+        float poison = 0.0f;  // NaN once the sequence had a value of this row that is not finite
+        int n = 0;
+        auto spoilt = [&](int m) {  // by chunk m
+            if (vbad[4 * (m & 3) + q] && first_bad[128 * (m & 3) + dv] < kC) poison = nan;
+        };
+        for (; n < total; ++n) {
+            const int buf = n & (kSums - 1);
+            if (!phase(gready + 8 * buf, n / kSums, &stop)) break;
+            hear(n);
+            if (c.head) {
+                poison = 0.0f;
+                const float *from = nullptr;
+                const long long s = p.slots[c.b];
+                if (!c.first)
+                    from = state_of(p, g - 1);
+                else if (s >= 0 && s < p.pool && !(p.fresh && p.fresh[c.b])) {
+                    // a sequence cut by the share's end begins with the second kernel's copy
+                    from = p.state + s * p.s_slot + c.h * p.s_head;
+                    const int a = p.cu[c.b], chunks = (p.cu[c.b + 1] - a + kC - 1) / kC;
+                    if (chunks > total - n) from = begin_state(p, g);
+                }
+#pragma unroll 1
+                for (int col = 0; col < DK; col += 32) {
+                    uint32_t v[2][16];
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) v[i >> 4][i & 15] = from && mine ? __float_as_uint(from[(col + i) * p.Dv + dv]) : 0u;
+                    tmem_st16(tmem + quarter + kState + col, v[0]);
+                    tmem_st16(tmem + quarter + kState + col + 16, v[1]);
+                }
+                asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+            } else {
+                if (!phase(sdone + 8 * ((n - 1) & 1), (n - 1) >> 1, &stop)) break;
+                spoilt(n - 1);
+            }
+            // O1 of the chunk before has read Sb
+            if (n > 0 && !phase(o1done, n - 1, &stop)) break;
             tc_fence_after();
+            const unsigned long long e = pack_f32x2(all_e[buf], all_e[buf]);
+            const bool poisoned = __any_sync(0xffffffffu, poison != 0.0f);
+#pragma unroll 1
+            for (int col = 0; col < DK; col += 32) {
+                uint32_t v[32], sb[16];
+                tmem_ld32(tmem + quarter + kState + col, v);
+                if (poisoned)
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) + poison);
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    sb[i] = bf16x2(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]));
+                    unpack2(mul2(pack2(v[2 * i], v[2 * i + 1]), e), v[2 * i], v[2 * i + 1]);
+                }
+                tmem_st16(tmem + quarter + kSb + col / 2, sb);
+                tmem_st32(tmem + quarter + kState + col, v);
+            }
+            asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) bar_arrive(sready);
+            if (c.tail) {
+                // the sequence's last state
+                if (!phase(sdone + 8 * (n & 1), n >> 1, &stop)) break;
+                spoilt(n);
+                const Seq s = seq_of(p, c.b);
+                if (s.slot >= 0 && (s.len > 0 || (p.fresh && p.fresh[c.b]))) {
+                    float *to = p.state + s.slot * p.s_slot + c.h * p.s_head + dv;
+                    tc_fence_after();
+#pragma unroll 1
+                    for (int col = 0; col < DK; col += 16) {
+                        uint32_t v[16];
+                        tc05::tmem_ld16(tmem + quarter + kState + col, v);
+                        if (mine)
+#pragma unroll
+                            for (int i = 0; i < 16; ++i) to[(col + i) * p.Dv] = __uint_as_float(v[i]) + poison;
+                    }
+                    tc_fence_before();
+                }
+            }
+        }
+        // after a stop: NaN for the sequences that were not finished
+        if (n < total)
+            for (int i = 0; cursor.next(p, c); ++i) {
+                const Seq s = seq_of(p, c.b);
+                if (i < n || !c.tail || s.slot < 0 || !mine) continue;
+                for (int col = 0; col < DK; ++col) p.state[s.slot * p.s_slot + c.h * p.s_head + col * p.Dv + dv] = nan;
+            }
+    } else if (warp >= 8 && warp < 12) {
+        // ------------------------------------------------------------- the decays of a chunk
+        for (int n = 0; n < total; ++n) {
+            const int buf = n & (kSums - 1);
+            if (!phase(gready + 8 * buf, n / kSums, &stop) || !phase(afull, n, &stop)) break;
+            tc_fence_after();
+            hear(n);
             const int i0 = 16 * q + (lane >> 2), j0 = 2 * (lane & 3);
             const float *gj = gs + buf * kC;
             const float g0 = gj[i0], g1 = gj[i0 + 8];
             // a row's tokens up to its own; none of a row behind the chunk's
             const int last0 = i0 < c.valid ? i0 : -1, last1 = i0 + 8 < c.valid ? i0 + 8 : -1;
-            uint8_t *row = ps + (n & 1) * kPart + i0 * 128;
+            uint8_t *row = ps + i0 * 128;  // (O2 of the chunk before was issued before A)
 #pragma unroll 1
             for (int t = 0; t < 4; ++t) {
                 uint32_t r[8];
@@ -1030,7 +1078,7 @@ __global__ void __launch_bounds__(kOutThreads, 1) linear_outputs_kernel(const __
             __syncwarp();
             if (lane == 0) {
                 bar_arrive(afree);
-                bar_arrive(pready + 8 * (n & 1));
+                bar_arrive(pready);
             }
         }
     } else if (warp >= 12) {
@@ -1040,81 +1088,75 @@ __global__ void __launch_bounds__(kOutThreads, 1) linear_outputs_kernel(const __
         const int tid = threadIdx.x - 12 * 32, c0 = 2 * (lane & 3);
         const uint32_t to_s = saddr(os);
         const unsigned long long scale = pack_f32x2(p.scale, p.scale);
-        bool ok = true;
-        for (int n = 0; cursor.next(p, c); ++n) {
-            if (ok) ok = all_wait(odone + 8 * (n & 1), (n >> 1) & 1, &stop);
-            if (ok) tc_fence_after();
+        int n = 0;
+        for (; n < total; ++n) {
+            // the four warps go on together, or none (they meet at barriers); what was staged is stored
+            if (!all_of(phase(odone + 8 * (n & 1), n >> 1, &stop))) break;
+            tc_fence_after();
+            hear(n);
             const float *e = eg + (n & (kSums - 1)) * kC;
-            const bool bad = ok && vbad[4 * (n & 3) + q] != 0;
+            const bool bad = vbad[4 * (n & 3) + q] != 0;
             uint16_t *out = p.out + static_cast<long long>(c.t0) * p.o_token + c.h * p.o_head;
+            if (32 * q < p.Dv)
 #pragma unroll 1
-            for (int t = 0; t < kC; t += 32) {
-                const bool any = t < c.valid;  // (the last turn also frees the accumulators)
-                if (any && 32 * q < p.Dv)
+                for (int part = 0; part < 8; ++part) {  // 16 rows x 16 tokens
+                    const int h = part & 1, t1 = 16 * (part >> 1);
+                    const uint32_t from = tmem + quarter + (static_cast<uint32_t>(16 * h) << 16) + t1;
+                    uint32_t a[8], b[8], o[4];
+                    tmem_ld_s(from + kO1, a);
+                    tmem_ld_s(from + kO2, b);
+                    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+                    if (bad)
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            const int first = first_bad[128 * (n & 3) + 32 * q + 16 * h + 8 * ((i >> 1) & 1) + (lane >> 2)];
+                            if (t1 + 8 * (i >> 2) + c0 + (i & 1) >= first) b[i] = __float_as_uint(nan);
+                        }
+#pragma unroll
+                    for (int m = 0; m < 4; ++m) {
+                        const unsigned long long ee = *reinterpret_cast<const unsigned long long *>(&e[t1 + 8 * (m >> 1) + c0]);
+                        uint32_t x, y;
+                        unpack2(ffma2(ee, pack2(a[2 * m], a[2 * m + 1]), mul2(scale, pack2(b[2 * m], b[2 * m + 1]))), x, y);
+                        o[m] = bf16x2(__uint_as_float(x), __uint_as_float(y));
+                    }
+                    stmatrix_turned(to_s + (t1 + 8 * (lane >> 4) + (lane & 7)) * 256 +
+                                        (((4 * q + 2 * h + ((lane >> 3) & 1)) ^ (lane & 7)) << 4), o);
+                }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) bar_arrive(ofree);
+            asm volatile("bar.sync 1, 128;" ::: "memory");
+            const int shift = p.Dv == 128 ? 4 : 3, end = c.valid << shift;
 #pragma unroll 1
-                    for (int h = 0; h < 2; ++h) {
-                        uint32_t a[16], b[16];
-                        if (ok) {
-                            const uint32_t from = tmem + quarter + (static_cast<uint32_t>(16 * h) << 16) + t;
-                            tmem_ld_s(from + kO1, a);
-                            tmem_ld_s(from + kO2, b);
-                            asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
-                        } else {
-#pragma unroll
-                            for (int i = 0; i < 16; ++i) a[i] = b[i] = __float_as_uint(nan);
-                        }
-                        if (bad)
-#pragma unroll
-                            for (int i = 0; i < 16; ++i) {
-                                const int from = first_bad[128 * (n & 3) + 32 * q + 16 * h + 8 * ((i >> 1) & 1) + (lane >> 2)];
-                                if (t + 8 * (i >> 2) + c0 + (i & 1) >= from) b[i] = __float_as_uint(nan);
-                            }
-#pragma unroll
-                        for (int i = 0; i < 4; i += 2) {
-                            uint32_t o[4];
-#pragma unroll
-                            for (int m = 0; m < 4; ++m) {
-                                const int blk = i + (m >> 1), r = 4 * blk + 2 * (m & 1);
-                                const unsigned long long ee = *reinterpret_cast<const unsigned long long *>(&e[t + 8 * blk + c0]);
-                                uint32_t x, y;
-                                unpack2(ffma2(ee, pack2(a[r], a[r + 1]), mul2(scale, pack2(b[r], b[r + 1]))), x, y);
-                                o[m] = bf16x2(__uint_as_float(x), __uint_as_float(y));
-                            }
-                            stmatrix_turned(to_s + (8 * i + 8 * (lane >> 4) + (lane & 7)) * 256 +
-                                                (((4 * q + 2 * h + ((lane >> 3) & 1)) ^ (lane & 7)) << 4), o);
-                        }
-                    }
-                if (t + 32 == kC) {
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) bar_arrive(ofree);
+            for (int i = tid; i < end; i += 128) {
+                const int tok = i >> shift, u = i & ((1 << shift) - 1);
+                const uint4 v = *reinterpret_cast<const uint4 *>(os + tok * 256 + ((u ^ (tok & 7)) << 4));
+                uint16_t *to = out + tok * p.o_token + 8 * u;
+                if (p.out16) {
+                    *reinterpret_cast<uint4 *>(to) = v;
+                } else {
+                    uint32_t *w = reinterpret_cast<uint32_t *>(to);
+                    w[0] = v.x;
+                    w[1] = v.y;
+                    w[2] = v.z;
+                    w[3] = v.w;
                 }
-                if (!any) continue;
-                asm volatile("bar.sync 1, 128;" ::: "memory");
-                const int shift = p.Dv == 128 ? 4 : 3, end = min(32, c.valid - t) << shift;
-#pragma unroll 4
-                for (int i = tid; i < end; i += 128) {
-                    const int tok = i >> shift, u = i & ((1 << shift) - 1);
-                    const uint4 v = *reinterpret_cast<const uint4 *>(os + tok * 256 + ((u ^ (tok & 7)) << 4));
-                    uint16_t *to = out + (t + tok) * p.o_token + 8 * u;
-                    if (p.out16) {
-                        *reinterpret_cast<uint4 *>(to) = v;
-                    } else {
-                        uint32_t *w = reinterpret_cast<uint32_t *>(to);
-                        w[0] = v.x;
-                        w[1] = v.y;
-                        w[2] = v.z;
-                        w[3] = v.w;
-                    }
-                }
-                asm volatile("bar.sync 1, 128;" ::: "memory");
             }
         }
+        // after a stop: NaN for the chunks that were not finished
+        if (n < total)
+            for (int i = 0; cursor.next(p, c); ++i)
+                if (i >= n && tid < p.Dv)
+                    for (int m = 0; m < c.valid; ++m)
+                        p.out[(static_cast<long long>(c.t0) + m) * p.o_token + c.h * p.o_head + tid] = 0x7fc0;
     }
     __syncwarp();
     // after a stop: the copies issued have landed before the shared memory goes
-    if (lane == 0 && *reinterpret_cast<volatile int *>(&stop) && warp == 0)
-        for (int i = max(0, issued - S); i < issued; ++i) landed(full + 8 * (i % S), (i / S) & 1);
+    if (lane == 0 && *reinterpret_cast<volatile int *>(&stop) && warp == 0) {
+        for (int i = max(0, issued - S); i < issued; ++i) landed(kfull + 8 * (i % S), (i / S) & 1);
+        for (int i = max(0, vissued - S); i < vissued; ++i) landed(vfull + 8 * (i % S), (i / S) & 1);
+        for (int i = max(0, qissued - S); i < qissued; ++i) landed(qfull + 8 * (i % S), (i / S) & 1);
+    }
     tc_fence_before();
     __syncthreads();
     if (threadIdx.x == 32 && stop) atomicOr(p.err, 1);
