@@ -34,7 +34,7 @@
 // state's only error above FP32's, 2^-9 of every summand (in two numbers 2^-18), and it goes on to all later
 // tokens.  P and Sb are rounded once: what they make is rounded to BF16 right after.
 // Roles: a warp copies (TMA, a ring of chunks), a warp issues all products, a warp sums the decays, and
-// four each turn the values and scale the keys, carry the state, apply the decays to A, and write the outputs.
+// eight turn the values and scale the keys, and four each carry the state, apply the decays to A, and write the outputs.
 // Exponents' sums are kept as pairs of FP32 numbers where states are made of them: differences of long sums
 // keep their digits.
 // The roles' loops are short on purpose: unrolled, their code did not fit the instruction cache, and a chunk
@@ -59,10 +59,10 @@ using namespace roles;
 constexpr int kC = 64;                 // tokens a chunk
 constexpr int kPart = kC * 128;        // 64 tokens x 64 elements, bytes
 constexpr int kStages = 6;             // of chunks in a ring, at most
-constexpr int kFew = 4;                // chunks a share has at least
-constexpr int kOutThreads = 20 * 32;   // copies, products, sums, (none), state, values, outputs, keys (4 each)
+constexpr int kFew = 8;                // chunks a share has at least
+constexpr int kOutThreads = 24 * 32;   // copies, products, sums, (none), state, decays, outputs (4 each), values and keys (8)
 constexpr int kSums = 4;               // chunks whose sums of g are kept
-constexpr int kStateThreads = 10 * 32;
+constexpr int kStateThreads = 12 * 32;  // copies, products, keys (8), sums, (none)
 // A decay's exponent (base 2) is cut here: 2^-200 is 0.  The sum of a chunk's is then 12800 at most, one
 // FP32 number of it off by 2^-11, and a factor exp2 of a difference by 2^-10.5: below BF16's rounding.
 constexpr float kLeast = -200.0f;
@@ -396,11 +396,11 @@ __device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t (&r)[32]
         : "memory");
 }
 
-// A chunk's keys times their factors w, as three BF16 numbers each (arrays DK / 64 parts apart), by four warps,
+// A chunk's keys times their factors w, as three BF16 numbers each (arrays DK / 64 parts apart), by eight warps,
 // 32 units of 16 bytes at a time.  Rows from `valid` on are 0, whatever lies there.
 template <int DK>
 __device__ __forceinline__ void scale_keys(const uint8_t *k, uint8_t *out, const float *w, int warp, int valid) {
-    constexpr int kUnits = DK / 8, kRows = 32 / kUnits, kEach = kC / 4;  // units a row, rows at a time, rows a warp
+    constexpr int kUnits = DK / 8, kRows = 32 / kUnits, kEach = kC / 8;  // units a row, rows at a time, rows a warp
     constexpr int kKeys = DK / 64 * kPart;
     const int lane = threadIdx.x & 31, u = lane % kUnits;
     const int row0 = warp * kEach + lane / kUnits;
@@ -428,7 +428,7 @@ __host__ __device__ constexpr int chunk_bytes(int dk, int dv, bool with_q) { ret
 constexpr int kMiscOut = 1024 + 3 * kSums * kC * 4 + 4 * 128 * 4;
 constexpr int kOutStage = kC * 256;  // a chunk's outputs on their way
 __host__ __device__ constexpr int out_fixed(int dk) { return 2 * 3 * dk / 64 * kPart + kPart + kOutStage + kMiscOut; }
-constexpr int kStateFixed = 512;
+constexpr int kStateFixed = 512 + 4 * kC * 4;
 // Columns of tensor memory: the state kernel's (U, two buffers of keys in three numbers), the output kernel's
 // (two buffers of values).
 constexpr int kU = 0, kKeyT = 128;
@@ -445,7 +445,9 @@ __global__ void __launch_bounds__(kStateThreads, 1) linear_states_kernel(const _
     uint64_t *bars = reinterpret_cast<uint64_t *>(misc);
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(misc + 256);
     int &stop = *reinterpret_cast<int *>(misc + 260);
-    const uint32_t full = saddr(bars), empty = full + 8 * kStages, kready = empty + 8 * kStages, kfree = kready + 16, fin = kfree + 16;
+    float *wk = reinterpret_cast<float *>(misc + 512);  // [4][64] the factors of a chunk's keys
+    const uint32_t full = saddr(bars), empty = full + 8 * kStages, kready = empty + 8 * kStages, kfree = kready + 16, fin = kfree + 16,
+                   gready = fin + 8;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = static_cast<int>(blockIdx.x);
     if (threadIdx.x == 0) {
         prefetch_tmap(&p.tk);
@@ -460,6 +462,7 @@ __global__ void __launch_bounds__(kStateThreads, 1) linear_states_kernel(const _
             bar_init(kfree + 8 * i, 1);
         }
         bar_init(fin, 1);
+        for (int i = 0; i < 4; ++i) bar_init(gready + 8 * i, 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     }
@@ -527,19 +530,15 @@ __global__ void __launch_bounds__(kStateThreads, 1) linear_states_kernel(const _
             }
         }
         finish(fin, &stop);
-    } else {
-        // keys: a warp's 32 elements (a quarter of the lanes), half of the tokens
-        const int q = warp & 3, half = (warp - 2) >> 2, d0 = 32 * q;
-        const uint32_t quarter = static_cast<uint32_t>(32 * q) << 16;
-        Pair after{0.0f, 0.0f};  // the sum of g behind the chunk, to the piece's end
-        bool ok = true;
-        int slot = 0;
-        unsigned ph = 0;
+    } else if (warp == 10) {
+        // the keys' factors: exp of the sum of g behind them, to the piece's end
+        Pair after{0.0f, 0.0f};
         Chunk c;
         c.h = last.h;
         c.valid = kC;
         c.t0 = last.s.t0 + last.k * kC;
         Decays next = load_g(p, c);
+        bool ok = true;
         for (int n = 0; n < chunks; ++n) {
             const Decays now = next;
             c.t0 -= kC;
@@ -547,16 +546,27 @@ __global__ void __launch_bounds__(kStateThreads, 1) linear_states_kernel(const _
             Pair a, b, all;
             sums_of(now, a, b, all);
             after = add(all, after);
-            const float wa = exp2f(less(after, a)), wb = exp2f(less(after, b));
-            ok = phase(full + 8 * slot, ph, &stop) && (n < 2 || phase(kfree + 8 * (n & 1), ((n >> 1) - 1) & 1, &stop));
+            if (!(ok = n < 2 || phase(kfree + 8 * (n & 1), (n >> 1) - 1, &stop))) break;
+            *reinterpret_cast<float2 *>(&wk[(n & 3) * kC + 2 * lane]) = make_float2(exp2f(less(after, a)), exp2f(less(after, b)));
+            __syncwarp();
+            if (lane == 0) bar_arrive(gready + 8 * (n & 3));
+        }
+        if (lane == 0) p.ws[g] = ok ? exp2f(after.hi + after.lo) : __int_as_float(0x7fc00000);
+    } else if (warp < 10) {
+        // keys: a warp's 32 elements (a quarter of the lanes), half of the tokens
+        const int q = warp & 3, half = (warp - 2) >> 2, d0 = 32 * q;
+        const uint32_t quarter = static_cast<uint32_t>(32 * q) << 16;
+        bool ok = true;
+        int slot = 0;
+        unsigned ph = 0;
+        for (int n = 0; n < chunks; ++n) {
+            // (the factors come after the product that read this buffer)
+            ok = phase(gready + 8 * (n & 3), n >> 2, &stop) && phase(full + 8 * slot, ph, &stop);
             if (!ok) break;
-            if (n >= 2) tc_fence_after();
+            tc_fence_after();
             if (d0 < DK) {
-                unsigned long long ff[4];  // of tokens 32 half + 8 i + 2 (lane % 4) and the next
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    ff[i] = pack_f32x2(__shfl_sync(0xffffffffu, wa, 16 * half + 4 * i + (lane & 3)),
-                                       __shfl_sync(0xffffffffu, wb, 16 * half + 4 * i + (lane & 3)));
+                // the factors of tokens 32 half + 8 i + 2 (lane % 4) and the next
+                const unsigned long long *w = reinterpret_cast<const unsigned long long *>(wk + (n & 3) * kC) + 16 * half + (lane & 3);
 #pragma unroll 1
                 for (int h = 0; h < 2; ++h) {  // 16 elements
                     uint32_t r[8], o[3][8];
@@ -565,7 +575,7 @@ __global__ void __launch_bounds__(kStateThreads, 1) linear_states_kernel(const _
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
                         uint32_t s[3];
-                        split(r[i], ff[i >> 1], s);
+                        split(r[i], w[4 * (i >> 1)], s);
 #pragma unroll
                         for (int m = 0; m < 3; ++m) o[m][i] = s[m];
                     }
@@ -600,7 +610,6 @@ __global__ void __launch_bounds__(kStateThreads, 1) linear_states_kernel(const _
                                            : make_float4(nan, nan, nan, nan);
             }
         }
-        if (warp == 2 && lane == 0) p.ws[g] = ok ? exp2f(after.hi + after.lo) : nan;
     }
     __syncwarp();
     if (lane == 0 && *reinterpret_cast<volatile int *>(&stop) && warp == 0)
@@ -673,7 +682,7 @@ __global__ void __launch_bounds__(kOutThreads, 1) linear_outputs_kernel(const __
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(misc + 512);
     int &stop = *reinterpret_cast<int *>(misc + 516);
     float *all_e = reinterpret_cast<float *>(misc + 528);  // [kSums] exp(G) of a chunk
-    int *vbad = reinterpret_cast<int *>(misc + 576);       // [4][4] whether a warp's values are not all finite
+    int *vbad = reinterpret_cast<int *>(misc + 768);       // [4][4][2] whether a warp's values are not all finite
     // [kSums][64] of each token: G_i, scale exp(G_i), exp(G - G_i)
     float *gs = reinterpret_cast<float *>(misc + 1024), *eg = gs + kSums * kC, *wk = eg + kSums * kC;
     int *first_bad = reinterpret_cast<int *>(wk + kSums * kC);  // [4][128] the first token with such a value
@@ -702,12 +711,12 @@ __global__ void __launch_bounds__(kOutThreads, 1) linear_outputs_kernel(const __
         init(vfull, kStages, 1);
         init(kfull, kStages, 1);
         init(qfull, kStages, 1);
-        init(vempty, kStages, 4);
-        init(kempty, kStages, 5);
+        init(vempty, kStages, 8);
+        init(kempty, kStages, 9);
         init(qempty, kStages, 1);
         init(gready, kSums, 1);
-        init(kready, 2, 4);
-        init(vready, 2, 4);
+        init(kready, 2, 8);
+        init(vready, 2, 8);
         init(sdone, 2, 1);
         init(afull, 1, 1);
         init(afree, 1, 4);
@@ -778,7 +787,7 @@ __global__ void __launch_bounds__(kOutThreads, 1) linear_outputs_kernel(const __
                 __syncwarp();
                 return true;
             };
-            if (!copy(kfull, kempty, p.tk, kKeys, kKParts, hk, issued) || !copy(vfull, vempty, p.tv, 2 * kKeys, vparts, c.h, vissued) ||
+            if (!copy(vfull, vempty, p.tv, 2 * kKeys, vparts, c.h, vissued) || !copy(kfull, kempty, p.tk, kKeys, kKParts, hk, issued) ||
                 !copy(qfull, qempty, p.tq, 0, kKParts, hk, qissued))
                 break;
             if (++slot == S) {
@@ -894,14 +903,17 @@ __global__ void __launch_bounds__(kOutThreads, 1) linear_outputs_kernel(const __
                 break;
             tc_fence_after();
             hear(n);
-            if (32 * q < p.Dv) {
-                const uint32_t vs = saddr(base) + slot * stage + 2 * kKeys;
+            {
+                // 16 elements x 64 tokens a warp
+                const int h = (warp - 16) >> 2;
                 bool any = false;
-#pragma unroll 1
-                for (int h = 0; h < 2; ++h) {  // 16 elements x 64 tokens
+                // which of the rows have one that is not finite is told for all 16 of them
+                int *fb = first_bad + 128 * b4 + 32 * q + 16 * h;
+                if (32 * q < p.Dv) {
                     uint32_t r[16], x = 0u;
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) load_turned(vs, 16 * i, 32 * q + 16 * h, r[4 * i], r[4 * i + 1], r[4 * i + 2], r[4 * i + 3]);
+                    for (int i = 0; i < 4; ++i)
+                        load_turned(saddr(base) + slot * stage + 2 * kKeys, 16 * i, 32 * q + 16 * h, r[4 * i], r[4 * i + 1], r[4 * i + 2], r[4 * i + 3]);
                     // tokens behind the chunk's are 0, whatever lies there
                     if (c.valid < kC)
 #pragma unroll
@@ -912,27 +924,24 @@ __global__ void __launch_bounds__(kOutThreads, 1) linear_outputs_kernel(const __
                     // infinities and NaN: 0 x v is not 0
 #pragma unroll
                     for (int i = 0; i < 16; ++i) asm("fma.rn.bf16x2 %0, %1, %2, %0;" : "+r"(x) : "r"(r[i]), "r"(0u));
-                    if (__any_sync(0xffffffffu, x != 0u)) {
+                    any = __any_sync(0xffffffffu, x != 0u);
+                    if (lane < 16) fb[lane] = kC;
+                    if (any) {
                         // They become 0 in the products, which sum over later tokens too, and the row's outputs and
                         // states NaN from the first such token on.
-                        int *fb = first_bad + 128 * b4 + 32 * q;
-                        if (!any) fb[lane] = kC;
-                        any = true;
                         __syncwarp();
 #pragma unroll
                         for (int i = 0; i < 16; ++i) {
-                            const int tok = 8 * (i >> 1) + 2 * (lane & 3), row = 16 * h + 8 * (i & 1) + (lane >> 2);
+                            const int tok = 8 * (i >> 1) + 2 * (lane & 3);
                             const bool lo = (r[i] & 0x7f80u) == 0x7f80u, hi = (r[i] & 0x7f800000u) == 0x7f800000u;
-                            if (lo || hi) atomicMin(&fb[row], lo ? tok : tok + 1);
+                            if (lo || hi) atomicMin(&fb[8 * (i & 1) + (lane >> 2)], lo ? tok : tok + 1);
                             r[i] = finite_or_zero(r[i]);
                         }
                     }
                     tmem_st_turned(tmem + quarter + (static_cast<uint32_t>(16 * h) << 16) + kValueT + 32 * (n & 1), r);
+                    asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
                 }
-                if (lane == 0) vbad[4 * b4 + q] = any;
-                asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
-            } else if (lane == 0) {
-                vbad[4 * b4 + q] = 0;
+                if (lane == 0) vbad[8 * b4 + 2 * q + h] = any;
             }
             tc_fence_before();
             __syncwarp();
@@ -960,7 +969,7 @@ __global__ void __launch_bounds__(kOutThreads, 1) linear_outputs_kernel(const __
         float poison = 0.0f;  // NaN once the sequence had a value of this row that is not finite
         int n = 0;
         auto spoilt = [&](int m) {  // by chunk m
-            if (vbad[4 * (m & 3) + q] && first_bad[128 * (m & 3) + dv] < kC) poison = nan;
+            if ((vbad[8 * (m & 3) + 2 * q] | vbad[8 * (m & 3) + 2 * q + 1]) && first_bad[128 * (m & 3) + dv] < kC) poison = nan;
         };
         for (; n < total; ++n) {
             const int buf = n & (kSums - 1);
@@ -1095,7 +1104,7 @@ __global__ void __launch_bounds__(kOutThreads, 1) linear_outputs_kernel(const __
             tc_fence_after();
             hear(n);
             const float *e = eg + (n & (kSums - 1)) * kC;
-            const bool bad = vbad[4 * (n & 3) + q] != 0;
+            const bool bad = (vbad[8 * (n & 3) + 2 * q] | vbad[8 * (n & 3) + 2 * q + 1]) != 0;
             uint16_t *out = p.out + static_cast<long long>(c.t0) * p.o_token + c.h * p.o_head;
             if (32 * q < p.Dv)
 #pragma unroll 1
