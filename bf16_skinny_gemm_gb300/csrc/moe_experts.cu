@@ -9,22 +9,23 @@
 // products are made for ALL tokens of the call (N = 16, 32, 64 or 128 columns of tcgen05.mma, the
 // weights' rows on the M side), and the first kernel's epilogue keeps what a token chose.
 //
-//  * Up: tiles of 8..64 gate rows and the same up rows of one expert against x (T x D).  The epilogue
-//    brings gate and up of an element together in shared memory and writes
+//  * Up: tiles of 8..128 gate rows and the same up rows of one expert against x (T x D), two accumulators,
+//    so that gate and up of an element are in one lane of tensor memory.  The epilogue writes
 //    w[t,e] silu(gate) up, BF16, as row t of expert e's block of scratch; zeros for tokens that did
 //    not choose e.  (The rounding of that product to BF16, the operand type of the second one,
 //    is the only one between x and y: 2^-9 of it at most, at random over F elements.)
 //  * Down: with those zeros, y = sum_e H_e Wd_e^T is ONE product over k = (expert, element of F),
-//    accumulated in tensor memory over all experts, in the order of their indices.  The two CTAs
-//    of a cluster take half of that k each for 8..128 rows of y, and swap FP32 partial sums
-//    through distributed shared memory (st.async), half of the tokens each, added in rank order.
+//    accumulated in tensor memory over all experts, in the order of their indices.  The 2, 4 or 8 CTAs
+//    of a cluster take a part of that k each for 8..128 rows of y, and swap FP32 partial sums
+//    through distributed shared memory (st.async), a part of the tokens each, added in rank order.
 //    No atomics, no sorting: the result does not depend on timing.
 //
-// Both kernels stream with TMA into a ring of 64-element chunks: one warp copies the weights, one
-// the other operand (x or H, from the L2 cache), one issues the MMAs, four do the epilogue.  A ring
-// takes less than half of the shared memory, so that the second kernel's CTAs are there, their
-// barriers and tables ready, when the first one's end.  The rows a tile has are chosen on the host
-// so that the tiles divide evenly over the SMs.
+// Both kernels stream with TMA into a ring: one warp copies the weights, one the other operand (x or H,
+// from the L2 cache), one issues the MMAs, four do the epilogue.  A slot holds one or more chunks of 64
+// elements of k: a copy, its wait and its products take about 600 cycles to issue whatever their size.  A ring
+// takes most of the shared memory (64 tokens, 128 experts of 4096 x 1024: 512 us; with half of it, so that
+// the second kernel's CTAs are there when the first one's end, 515 to 540).  The rows a tile has, the chunks a
+// slot and the CTAs a cluster are chosen on the host, see shape_of.
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -48,12 +49,14 @@ constexpr int kMostTokens = 128;
 constexpr int kMostEntries = 32;  // a token
 constexpr int kThreadsExperts = 32 * 7;  // weights, MMA, 4 of epilogue, the other operand
 constexpr int kRing = 16;         // slots at most
-constexpr int kSplit = 2;         // CTAs of a cluster that share the second product's k
-constexpr int kRingBytes = 90 * 1024;
+constexpr int kMostSplit = 8;     // CTAs of a cluster that share the second product's k, at most
+constexpr int kRingBytes = 180 * 1024;
 
 struct ExpertParams {
-    CUtensorMap tw;  // the weights: {D, 2F, E}, or {F, D, E}
-    CUtensorMap tb;  // the other operand: x {D, T, 1}, or H {F, T, experts}
+    // Chunks of 64 elements of k have a dimension of their own where k is a multiple of 64, so that a box
+    // holds several; else there is one, {k, rows, 1, ..}
+    CUtensorMap tw;  // the weights: {64, 2F, D / 64, E}, or {64, D, F / 64, E}
+    CUtensorMap tb;  // the other operand: x {64, T, D / 64, 1}, or H {64, T, F / 64, experts}
     const int *ids;
     const float *weights;
     uint16_t *h;     // H, [expert of the list][T][F]
@@ -64,19 +67,23 @@ struct ExpertParams {
     int rows;        // of weights (of gate and of up, or of down) a tile
     int tiles;       // of an expert (up)
     int box;         // rows of a box of the other operand
+    int deep;        // chunks of k a slot
+    int even;        // whether chunks have a dimension of their own
+    int split;       // CTAs of a cluster (down)
     int slots, flags;
 };
 
-__host__ __device__ constexpr int slot_bytes(bool up, int rows, int n) { return ((up ? 2 : 1) * rows + n) * 128; }
+// A slot: `deep` chunks of weights, then as many of the other operand.
+__host__ __device__ constexpr int slot_bytes(bool up, int rows, int n, int deep) { return deep * ((up ? 2 : 1) * rows + n) * 128; }
 // behind the ring: an MMA reads 128 rows of weights though a tile may have fewer
-__host__ __device__ constexpr int tail_bytes(bool up, int rows, int n) {
-    return 128 > (up ? 2 : 1) * rows + n ? (128 - (up ? 2 : 1) * rows - n) * 128 : 0;
+__host__ __device__ constexpr int tail_bytes(int rows, int n, int deep) {
+    return 128 > rows + deep * n ? (128 - rows - deep * n) * 128 : 0;
 }
 
 template <int N, bool UP>
 __global__ void __launch_bounds__(kThreadsExperts, 1) moe_experts_kernel(const __grid_constant__ ExpertParams p) {
-    constexpr int kAcc = UP ? 2 : 1;
-    constexpr int kTmem = kAcc * N < 32 ? 32 : kAcc * N;
+    constexpr int kAcc = UP ? 2 * N : N;                    // columns of a tile's accumulators
+    constexpr int kTmem = UP ? 2 * kAcc : N < 32 ? 32 : N;  // (up: two tiles in turn)
     constexpr uint32_t kIdescN = (1u << 4) | (1u << 7) | (1u << 10) | (static_cast<uint32_t>(N >> 3) << 17) |
                                  (static_cast<uint32_t>(128 >> 4) << 24);
     extern __shared__ uint8_t raw[];
@@ -87,13 +94,13 @@ __global__ void __launch_bounds__(kThreadsExperts, 1) moe_experts_kernel(const _
     __shared__ int list[kMostExperts], count;
     __shared__ float wt[kMostTokens];
     __shared__ int on[kMostTokens];
-    __shared__ float ex[UP ? 128 : 1][17];
     uint8_t *base = raw + ((1024u - (saddr(raw) & 1023u)) & 1023u);  // swizzled operands start on 1 KiB
     // partial sums, [rank][token][128]
-    float *red = reinterpret_cast<float *>(base + p.slots * slot_bytes(UP, p.rows, N) + tail_bytes(UP, p.rows, N));
+    float *red = reinterpret_cast<float *>(base + p.slots * slot_bytes(UP, p.rows, N, p.deep) + tail_bytes(p.rows, N, p.deep));
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int S = p.slots, per_slot = slot_bytes(UP, p.rows, N), w_bytes = (UP ? 2 : 1) * p.rows * 128;
+    const int S = p.slots, per_slot = slot_bytes(UP, p.rows, N, p.deep);
+    const int half_bytes = p.deep * p.rows * 128, w_bytes = (UP ? 2 : 1) * half_bytes;  // gate's, all of the weights'
     const uint32_t ring = saddr(base);
     const uint32_t full = saddr(bars), empty = full + 8 * kRing, afull = empty + 8 * kRing, aempty = afull + 16,
                    fin = aempty + 16, redb = fin + 8;
@@ -153,19 +160,20 @@ __global__ void __launch_bounds__(kThreadsExperts, 1) moe_experts_kernel(const _
     const uint32_t tmem = tmem_slot;
     const bool stall = (p.flags & kFlagTestStall) != 0;
 
-    // this CTA's tiles, and its chunks of k: of each tile (up), or of the one tile it has (down)
-    const int kc = ((UP ? p.D : p.F) + 63) / 64;
+    // this CTA's tiles, and its slots of k: of each tile (up), or of the one tile it has (down)
+    const int kc = (((UP ? p.D : p.F) + 63) / 64 + p.deep - 1) / p.deep;
     const long long all = static_cast<long long>(count) * (UP ? p.tiles : kc);
     const int t0 = UP ? static_cast<int>(all * blockIdx.x / gridDim.x) : 0;
     const int t1 = UP ? static_cast<int>(all * (blockIdx.x + 1) / gridDim.x) : 1;
-    const int c0 = UP ? 0 : static_cast<int>(all * rank / kSplit);
-    const int c1 = UP ? kc : static_cast<int>(all * (rank + 1) / kSplit);
-    const int d0 = UP ? 0 : static_cast<int>(blockIdx.x) / kSplit * p.rows;
+    const int c0 = UP ? 0 : static_cast<int>(all * rank / p.split);
+    const int c1 = UP ? kc : static_cast<int>(all * (rank + 1) / p.split);
+    const int d0 = UP ? 0 : static_cast<int>(blockIdx.x) / p.split * p.rows;
     int issued = 0;  // slots that this warp's copies were issued for
 
     if (warp == 0 || warp == 6) {
         // -------------------------------------------------------------------- the copies
         const uint64_t policy = policy_of(warp == 0);
+        const int step0 = p.even ? 0 : 64, step2 = p.even ? p.deep : 0;  // coordinates a slot
         int slot = 0, n = 0;
         unsigned ph = 1;
         bool ok = true;
@@ -182,12 +190,13 @@ __global__ void __launch_bounds__(kThreadsExperts, 1) moe_experts_kernel(const _
                     if (warp == 0) {
                         bar_expect_tx(bar, static_cast<unsigned>(w_bytes));
                         if (!stall) {
-                            tma_3d_hint(dst, &p.tw, 64 * c, f0, e, bar, policy);
-                            if (UP) tma_3d_hint(dst + p.rows * 128, &p.tw, 64 * c, p.F + f0, e, bar, policy);
+                            tma_4d(dst, &p.tw, step0 * c, f0, step2 * c, e, bar, policy);
+                            if (UP) tma_4d(dst + half_bytes, &p.tw, step0 * c, p.F + f0, step2 * c, e, bar, policy);
                         }
                     } else {
-                        bar_expect_tx(bar, static_cast<unsigned>(p.box * 128));
-                        if (!stall) tma_3d(dst + w_bytes, &p.tb, 64 * c, 0, UP ? 0 : slotted, bar);
+                        // (a box has p.box rows, an operand N: chunks lie as close as the box has them)
+                        bar_expect_tx(bar, static_cast<unsigned>(p.deep * p.box * 128));
+                        if (!stall) tma_4d(dst + w_bytes, &p.tb, step0 * c, 0, step2 * c, UP ? 0 : slotted, bar, policy);
                     }
                 }
                 __syncwarp();
@@ -211,14 +220,20 @@ __global__ void __launch_bounds__(kThreadsExperts, 1) moe_experts_kernel(const _
             const int i = t - t0;
             ok = i < 2 || all_wait(aempty + 8 * (i & 1), ((i >> 1) - 1) & 1, &stop);
             tc_fence_after();
-            const uint32_t d = base_d + (UP ? (i & 1) * N : 0);
+            const uint32_t d = base_d + (UP ? (i & 1) * kAcc : 0);
             for (int c = c0; ok && c < c1; ++c, ++n) {
                 if (!(ok = all_wait(full + 8 * slot, ph, &stop))) break;
                 tc_fence_after();
                 if (elect()) {
-                    const uint64_t a = tc05::sw128_desc(ring + slot * per_slot), b = tc05::sw128_desc(ring + slot * per_slot + w_bytes);
+                    for (int m = 0; m < p.deep; ++m) {
+                        const uint64_t a = tc05::sw128_desc(ring + slot * per_slot + m * p.rows * 128);
+                        const uint64_t b = tc05::sw128_desc(ring + slot * per_slot + w_bytes + m * p.box * 128);
 #pragma unroll
-                    for (int kk = 0; kk < 4; ++kk) mma(d, a + ((32 * kk) >> 4), b + ((32 * kk) >> 4), kIdescN, c != c0 || kk != 0);
+                        for (int kk = 0; kk < 4; ++kk) {
+                            mma(d, a + ((32 * kk) >> 4), b + ((32 * kk) >> 4), kIdescN, c != c0 || m != 0 || kk != 0);
+                            if (UP) mma(d + N, a + ((half_bytes + 32 * kk) >> 4), b + ((32 * kk) >> 4), kIdescN, c != c0 || m != 0 || kk != 0);
+                        }
+                    }
                     mma_commit(empty + 8 * slot);
                     if (c + 1 == c1) mma_commit(afull + 8 * (i & 1));
                 }
@@ -236,7 +251,7 @@ __global__ void __launch_bounds__(kThreadsExperts, 1) moe_experts_kernel(const _
         const uint32_t quarter = static_cast<uint32_t>(32 * q) << 16;
         const float nan = __int_as_float(0x7fc00000);
         if constexpr (UP) {
-            int last = -1;
+            int last = -1, told = -1;
             bool ok = true;
             for (int t = t0; t < t1; ++t) {
                 const int i = t - t0, a = t / p.tiles, f0 = (t - a * p.tiles) * p.rows;
@@ -260,29 +275,29 @@ __global__ void __launch_bounds__(kThreadsExperts, 1) moe_experts_kernel(const _
                 ok = ok && wait_or_stop(afull + 8 * (i & 1), (i >> 1) & 1, &stop);
                 ok = __all_sync(0xffffffffu, ok);
                 if (ok) tc_fence_after();
-                const int f = tid & 63, half = tid >> 6;  // this thread's element, and half of 16 tokens
-                uint16_t *out = p.h + static_cast<long long>(a) * p.T * p.F + f0 + f;
-                const bool mine = f < p.rows && f0 + f < p.F;
+                uint16_t *out = p.h + static_cast<long long>(a) * p.T * p.F + f0 + row;
+                const bool mine = row < p.rows && f0 + row < p.F;
+                if (a != told) {
+                    asm volatile("bar.sync 1, 128;" ::: "memory");  // the weights are there
+                    told = a;
+                }
 #pragma unroll 1
-                for (int c = 0; c < N; c += 16) {
-                    if (c >= p.T) break;
-                    uint32_t v[16];
+                for (int c = 0; c < p.T; c += 8) {
+                    uint32_t g[8], u[8];
                     if (ok) {
-                        tc05::tmem_ld16(tmem + quarter + (i & 1) * N + c, v);
+                        tmem_ld8(tmem + quarter + (i & 1) * kAcc + c, g);
+                        tmem_ld8(tmem + quarter + (i & 1) * kAcc + N + c, u);
+                        asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
                     } else {
 #pragma unroll
-                        for (int m = 0; m < 16; ++m) v[m] = __float_as_uint(nan);
+                        for (int m = 0; m < 8; ++m) g[m] = u[m] = __float_as_uint(nan);
                     }
-                    asm volatile("bar.sync 1, 128;" ::: "memory");  // what was there is read
-#pragma unroll
-                    for (int m = 0; m < 16; ++m) ex[row][m] = __uint_as_float(v[m]);
-                    asm volatile("bar.sync 1, 128;" ::: "memory");
                     if (mine)
 #pragma unroll
-                        for (int m = 8 * half; m < 8 * half + 8; ++m)
+                        for (int m = 0; m < 8; ++m)
                             if (c + m < p.T) {
-                                const float g = ex[f][m], u = ex[p.rows + f][m];
-                                const float h = g / (1.0f + expf(-g)) * u * wt[c + m];
+                                const float x = __uint_as_float(g[m]);
+                                const float h = x / (1.0f + expf(-x)) * __uint_as_float(u[m]) * wt[c + m];
                                 out[(c + m) * p.F] = on[c + m] ? f32_to_bf16_rn(h) : 0;
                             }
                 }
@@ -298,9 +313,9 @@ __global__ void __launch_bounds__(kThreadsExperts, 1) moe_experts_kernel(const _
                 if (ok) tc_fence_after();
             }
             cluster_wait_acquire();  // the other CTA's shared memory and mbarriers are there
-            const int each = (p.T + kSplit - 1) / kSplit;  // tokens a rank adds up
+            const int each = (p.T + p.split - 1) / p.split;  // tokens a rank adds up
             const int first = static_cast<int>(rank) * each, own = max(0, min(p.T, first + each) - first);
-            if (tid == 0) bar_expect_tx(redb, static_cast<unsigned>((kSplit - 1) * own * p.rows * 4));
+            if (tid == 0) bar_expect_tx(redb, static_cast<unsigned>((p.split - 1) * own * p.rows * 4));
             for (int c = 0; c < N; c += 16) {
                 if (c >= p.T) break;
                 uint32_t v[16];
@@ -325,8 +340,7 @@ __global__ void __launch_bounds__(kThreadsExperts, 1) moe_experts_kernel(const _
             if (row < p.rows && d0 + row < p.D)
                 for (int t = 0; t < own; ++t) {
                     float s = red[t * 128 + row];
-#pragma unroll
-                    for (int r = 1; r < kSplit; ++r) s += red[(r * each + t) * 128 + row];
+                    for (int r = 1; r < p.split; ++r) s += red[(r * each + t) * 128 + row];
                     p.y[(first + t) * p.ldy + d0 + row] = f32_to_bf16_rn(got ? s : nan);
                 }
         }
@@ -363,18 +377,68 @@ const void *kernel_of(int n) {
                      : reinterpret_cast<const void *>(&moe_experts_kernel<128, UP>);
 }
 
-// Rows of a tile (a multiple of 8 up to `most`), so that `count` blocks of `of` rows fall evenly on
-// `ctas`: the fewest rows on the CTA that has the most, and the largest tile of equals.
-int rows_of(long long count, long long of, int most, int ctas) {
-    int best = 8;
-    long long least = -1;
-    for (int r = 8; r <= most && r < of + 8; r += 8) {
-        const long long tiles = count * ((of + r - 1) / r), load = (tiles + ctas - 1) / ctas * r;
-        if (least < 0 || load <= least) {
-            least = load;
-            best = r;
+// What a launch is cut into.
+struct Shape {
+    int rows, deep, split;
+};
+
+// How many clusters of 2, 4 and 8 CTAs the device runs at a time, a CTA an SM (a cluster lies in one part
+// of the GPU, so that larger ones leave SMs over: 76, 36 and 15 here); asked once a device.
+bool clusters_of(int (&most)[3]) {
+    static std::atomic<unsigned> known[64];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return false;
+    unsigned v = dev < 64 ? known[dev].load(std::memory_order_acquire) : 0u;
+    if (!v) {
+        const void *fn = reinterpret_cast<const void *>(&moe_experts_kernel<16, false>);
+        if (allow_max_dynamic_smem(fn) != cudaSuccess) return false;
+        for (int i = 0; i < 3; ++i) {
+            cudaLaunchConfig_t cfg;
+            std::memset(&cfg, 0, sizeof(cfg));
+            cudaLaunchAttribute attr;
+            attr.id = cudaLaunchAttributeClusterDimension;
+            attr.val.clusterDim.x = 2u << i;
+            attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+            cfg.gridDim = dim3(1024);
+            cfg.blockDim = dim3(kThreadsExperts);
+            cfg.dynamicSmemBytes = kRingBytes;
+            cfg.attrs = &attr;
+            cfg.numAttrs = 1;
+            int n = 0;
+            if (cudaOccupancyMaxActiveClusters(&n, fn, &cfg) != cudaSuccess || n < 1) return false;
+            v |= static_cast<unsigned>(std::min(n, 1023)) << (10 * i);
         }
+        if (dev < 64) known[dev].store(v, std::memory_order_release);
     }
+    for (int i = 0; i < 3; ++i) most[i] = static_cast<int>(v >> (10 * i) & 1023);
+    return true;
+}
+
+// The shape whose busiest SM has the least to do, counted in bytes that come from memory: a slot's
+// weights, 0.6 of its other operand (from the L2 cache) and 2560 for its waits and its issue (600 cycles at
+// an SM's share of the memory rate, some of them hidden); of equals the smallest cluster with the largest
+// rows.  `blocks` experts; up: `of` rows each, whose products have `chunks` chunks of k, a tile an SM; down: `of` rows
+// in all, whose products have `blocks` times `chunks` chunks, shared by a cluster.
+// Measured (us for both products): 64 tokens, 128 experts of 4096 x 1024: tiles of 128 rows, down with 4 CTAs a
+// cluster 498; up with 56 rows 678; down with 2 CTAs and 56 rows 545.  8 tokens, 64 experts of 2048 x 1408: 92
+// (112 rows, 4 CTAs); up with 64 rows 95, down with 2 CTAs and 64 rows 99 and more.
+Shape shape_of(bool up, double blocks, long long of, long long chunks, int box, bool even, int sms, const int (&clusters)[3]) {
+    Shape best{8, 1, 1};
+    double least = -1.0;
+    for (int i = 0; i < (up ? 1 : 3); ++i)
+        for (int rows = 8; rows <= 128 && rows < of + 8; rows += 8) {
+            const int split = up ? 1 : 2 << i;
+            int deep = 1;
+            while (even && deep < 4 && 2 * deep * ((up ? 2 : 1) * rows + box) * 128 <= kRingBytes / 3 && deep < chunks) deep *= 2;
+            const long long row_tiles = (of + rows - 1) / rows;
+            const double waves = up ? std::ceil(blocks * static_cast<double>(row_tiles) / sms) : static_cast<double>((row_tiles + clusters[i] - 1) / clusters[i]);
+            const double slots = (up ? 1.0 : blocks) * static_cast<double>(chunks) / deep / split;
+            const double cost = waves * slots * (deep * ((up ? 2 : 1) * rows * 128 + 0.6 * box * 128) + 2560.0);
+            if (least < 0 || cost < 0.999 * least || (cost <= least && split == best.split)) {
+                least = cost;
+                best = {rows, deep, split};
+            }
+        }
     return best;
 }
 
@@ -474,30 +538,43 @@ extern "C" sgemm_status_t sgemm_bf16_moe_experts(const sgemm_moe_experts_t *a, s
     static std::atomic<unsigned long long> done[8];
     const int which = n == 16 ? 0 : n == 32 ? 1 : n == 64 ? 2 : 3;
     const long long experts = listed(*a);
-    auto ring = [&](bool up) {
-        p.slots = std::max(3, std::min(kRing, kRingBytes / slot_bytes(up, p.rows, n)));
-        return static_cast<size_t>(p.slots) * slot_bytes(up, p.rows, n) + tail_bytes(up, p.rows, n) + 1024;
+    // experts that have tokens, as many as independent choices leave (what they are is known on the device only)
+    const double likely = std::max(1.0, a->E * (1.0 - std::pow(1.0 - std::min(1.0, static_cast<double>(a->k) / a->E), a->T)));
+    int clusters[3];
+    if (!clusters_of(clusters)) return SGEMM_ERR_CUDA;
+    auto ring = [&](bool up, const Shape &s) {
+        p.rows = s.rows;
+        p.deep = s.deep;
+        p.split = s.split;
+        const int bytes = slot_bytes(up, s.rows, n, s.deep);
+        // beside the ring: what an MMA reads behind it, alignment, partial sums, 8 KiB of static arrays
+        const int sums = up ? 0 : s.split * ((a->T + s.split - 1) / s.split) * 512;
+        const int rest = tail_bytes(s.rows, n, s.deep) + 1024 + sums;
+        const int room = std::min(kRingBytes, static_cast<int>(kMaxSmemOptin) - rest - 8 * 1024);
+        p.slots = std::min(kRing, room / bytes);  // (3 at least: 48 KiB a slot, 64 KiB of sums at most)
+        return static_cast<size_t>(p.slots) * bytes + rest;
     };
     {
         const void *fn = kernel_of<true>(n);
-        p.rows = rows_of(experts, a->F, 64, sms);
+        p.even = a->D % 64 == 0;
+        const size_t smem = ring(true, shape_of(true, likely, a->F, (a->D + 63) / 64, p.box, p.even, sms, clusters));
         p.tiles = (a->F + p.rows - 1) / p.rows;
-        const size_t smem = ring(true);
-        if (!map_3d(&p.tw, a->w_gate_up, a->D, 2LL * a->F, a->E, a->gu_row, a->gu_expert, p.rows, CU_TENSOR_MAP_L2_PROMOTION_L2_256B) ||
-            !map_3d(&p.tb, a->x, a->D, a->T, 1, a->ldx, a->ldx, p.box, CU_TENSOR_MAP_L2_PROMOTION_L2_128B) || !allow(fn, done[which]))
+        if (!map_4d(&p.tw, a->w_gate_up, a->D, 2LL * a->F, a->E, a->gu_row, a->gu_expert, p.rows, p.deep, p.even, CU_TENSOR_MAP_L2_PROMOTION_L2_256B) ||
+            !map_4d(&p.tb, a->x, a->D, a->T, 1, a->ldx, a->ldx, p.box, p.deep, p.even, CU_TENSOR_MAP_L2_PROMOTION_L2_128B) ||
+            !allow(fn, done[which]))
             return SGEMM_ERR_CUDA;
         const long long ctas = std::min<long long>(sms, experts * p.tiles);
         if (launch(fn, dim3(static_cast<unsigned>(ctas)), dim3(kThreadsExperts), smem, cs, &p) != cudaSuccess) return SGEMM_ERR_CUDA;
     }
     const void *fn = kernel_of<false>(n);
-    p.rows = rows_of(kSplit, a->D, 128, sms);
-    const size_t smem = ring(false) + static_cast<size_t>(kSplit) * ((a->T + kSplit - 1) / kSplit) * 512;
-    if (!map_3d(&p.tw, a->w_down, a->F, a->D, a->E, a->dn_row, a->dn_expert, p.rows, CU_TENSOR_MAP_L2_PROMOTION_L2_256B) ||
-        !map_3d(&p.tb, a->workspace, a->F, a->T, experts, a->F, static_cast<long long>(a->T) * a->F, p.box,
+    p.even = a->F % 64 == 0;
+    const size_t smem = ring(false, shape_of(false, likely, a->D, (a->F + 63) / 64, p.box, p.even, sms, clusters));
+    if (!map_4d(&p.tw, a->w_down, a->F, a->D, a->E, a->dn_row, a->dn_expert, p.rows, p.deep, p.even, CU_TENSOR_MAP_L2_PROMOTION_L2_256B) ||
+        !map_4d(&p.tb, a->workspace, a->F, a->T, experts, a->F, static_cast<long long>(a->T) * a->F, p.box, p.deep, p.even,
                 CU_TENSOR_MAP_L2_PROMOTION_L2_128B) ||
         !allow(fn, done[4 + which]))
         return SGEMM_ERR_CUDA;
     const unsigned tiles = static_cast<unsigned>((a->D + p.rows - 1) / p.rows);
-    if (launch(fn, dim3(kSplit * tiles), dim3(kThreadsExperts), smem, cs, &p, kSplit) != cudaSuccess) return SGEMM_ERR_CUDA;
+    if (launch(fn, dim3(p.split * tiles), dim3(kThreadsExperts), smem, cs, &p, p.split) != cudaSuccess) return SGEMM_ERR_CUDA;
     return SGEMM_OK;
 }
