@@ -414,14 +414,15 @@ bool clusters_of(int (&most)[3]) {
     return true;
 }
 
-// The shape whose busiest SM has the least to do, counted in bytes that come from memory: a slot's
+// The shape that takes the least time, counted in bytes that come from memory: a slot's
 // weights, 0.6 of its other operand (from the L2 cache) and 2560 for its waits and its issue (600 cycles at
 // an SM's share of the memory rate, some of them hidden); of equals the smallest cluster with the largest
 // rows.  `blocks` experts; up: `of` rows each, whose products have `chunks` chunks of k, a tile an SM; down: `of` rows
 // in all, whose products have `blocks` times `chunks` chunks, shared by a cluster.
 // Measured (us for both products): 64 tokens, 128 experts of 4096 x 1024: tiles of 128 rows, down with 4 CTAs a
-// cluster 498; up with 56 rows 678; down with 2 CTAs and 56 rows 545.  8 tokens, 64 experts of 2048 x 1408: 92
-// (112 rows, 4 CTAs); up with 64 rows 95, down with 2 CTAs and 64 rows 99 and more.
+// cluster 498; up with 56 rows 517; down with 2 CTAs and 56 rows 533.  8 tokens, 64 experts of 2048 x 1408: 92
+// (112 rows, 4 CTAs); up with 64 rows 95, down with 2 CTAs and 64 rows 99 and more.  1 token, 8 of 128
+// experts: 38.0 (up 64 rows, down 128); with 56 and 120 rows 40.1.
 Shape shape_of(bool up, double blocks, long long of, long long chunks, int box, bool even, int sms, const int (&clusters)[3]) {
     Shape best{8, 1, 1};
     double least = -1.0;
@@ -431,7 +432,9 @@ Shape shape_of(bool up, double blocks, long long of, long long chunks, int box, 
             int deep = 1;
             while (even && deep < 4 && 2 * deep * ((up ? 2 : 1) * rows + box) * 128 <= kRingBytes / 3 && deep < chunks) deep *= 2;
             const long long row_tiles = (of + rows - 1) / rows;
-            const double waves = up ? std::ceil(blocks * static_cast<double>(row_tiles) / sms) : static_cast<double>((row_tiles + clusters[i] - 1) / clusters[i]);
+            // what the memory takes for all of it, and the busiest SM, which gets 1.15 of its share where others are done
+            const double tiles = up ? blocks * static_cast<double>(row_tiles) / sms : static_cast<double>(row_tiles) / clusters[i];
+            const double waves = std::max(up ? tiles : static_cast<double>(row_tiles) * split / sms, std::ceil(tiles) / 1.15);
             const double slots = (up ? 1.0 : blocks) * static_cast<double>(chunks) / deep / split;
             const double cost = waves * slots * (deep * ((up ? 2 : 1) * rows * 128 + 0.6 * box * 128) + 2560.0);
             if (least < 0 || cost < 0.999 * least || (cost <= least && split == best.split)) {

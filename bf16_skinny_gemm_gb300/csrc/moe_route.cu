@@ -52,9 +52,12 @@ __device__ __forceinline__ unsigned rank_of(float v) {
     return b & 0x80000000u ? ~b : b | 0x80000000u;  // -inf: 0x007fffff
 }
 
+// EACH: experts a lane of the selecting warp holds (4 for up to 128 experts, 8, or 32; a token's k rounds over 32 of
+// them took 2 us more)
+template <int EACH>
 __global__ void __launch_bounds__(kThreadsRoute) moe_route_kernel(const __grid_constant__ RouteParams p) {
     __shared__ float part[kWarps][kExperts][kTokens];
-    __shared__ float logits[kMaxExperts];  // of the token this CTA selects for
+    __shared__ float logits[32 * EACH];  // of the token this CTA selects for
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int rank = static_cast<int>(cluster_rank());
     const long long t0 = static_cast<long long>(blockIdx.x / kCtas) * kTokens;
@@ -124,9 +127,8 @@ __global__ void __launch_bounds__(kThreadsRoute) moe_route_kernel(const __grid_c
 
     // one warp selects; lane l has experts l, l + 32, ...
     const long long tok = t0 + rank;
-    constexpr int kEach = kMaxExperts / 32;
     const float inf = __int_as_float(0x7f800000);
-    unsigned key[kEach];
+    unsigned key[EACH];
     float top = -inf, sum = 0.0f;
     if (p.scoring == SGEMM_ROUTE_SOFTMAX) {
         for (int e = lane; e < p.E; e += 32) top = fmaxf(top, logits[e]);
@@ -138,7 +140,7 @@ __global__ void __launch_bounds__(kThreadsRoute) moe_route_kernel(const __grid_c
     }
     auto score = [&](float v) { return p.scoring == SGEMM_ROUTE_SOFTMAX ? expf(v - top) / sum : 1.0f / (1.0f + expf(-v)); };
 #pragma unroll
-    for (int i = 0; i < kEach; ++i) {
+    for (int i = 0; i < EACH; ++i) {
         const int e = lane + 32 * i;
         key[i] = 0u;
         if (e < p.E) key[i] = rank_of(p.bias ? score(logits[e]) + p.bias[e] : logits[e]);
@@ -149,7 +151,7 @@ __global__ void __launch_bounds__(kThreadsRoute) moe_route_kernel(const __grid_c
         unsigned best = 0u;
         int at = 0;
 #pragma unroll
-        for (int i = 0; i < kEach; ++i)
+        for (int i = 0; i < EACH; ++i)
             if (key[i] > best) {  // the lower index of equal ones
                 best = key[i];
                 at = i;
@@ -157,7 +159,7 @@ __global__ void __launch_bounds__(kThreadsRoute) moe_route_kernel(const __grid_c
         const unsigned most = __reduce_max_sync(0xffffffffu, best);
         const int e = static_cast<int>(__reduce_min_sync(0xffffffffu, best == most ? static_cast<unsigned>(lane + 32 * at) : 0xffffffffu));
 #pragma unroll
-        for (int i = 0; i < kEach; ++i)
+        for (int i = 0; i < EACH; ++i)
             if (e == lane + 32 * i) key[i] = 0u;
         const float s = score(logits[e]);
         total += s;
@@ -224,7 +226,10 @@ extern "C" sgemm_status_t sgemm_bf16_moe_route(const sgemm_moe_route_t *a, sgemm
     p.scale = a->scale;
     p.flags = static_cast<int>(a->flags);
     const unsigned clusters = static_cast<unsigned>((a->T + kTokens - 1) / kTokens);
-    if (launch(reinterpret_cast<const void *>(&moe_route_kernel), dim3(clusters * kCtas), dim3(kThreadsRoute), 0,
+    const void *fn = a->E <= 128   ? reinterpret_cast<const void *>(&moe_route_kernel<4>)
+                     : a->E <= 256 ? reinterpret_cast<const void *>(&moe_route_kernel<8>)
+                                   : reinterpret_cast<const void *>(&moe_route_kernel<32>);
+    if (launch(fn, dim3(clusters * kCtas), dim3(kThreadsRoute), 0,
                reinterpret_cast<cudaStream_t>(stream), &p, kCtas) != cudaSuccess)
         return SGEMM_ERR_CUDA;
     return SGEMM_OK;
