@@ -53,7 +53,11 @@
 //
 // Drafted tokens (sgemm_bf16_latent_tree_attention): the new tokens' rows are the last of a
 // sequence, so that only its last tiles hold rows that a mask decides on.  The same kernel, with
-// masks in place of the causal limit there (a template argument: the other's code stays as it is).
+// masks in place of the causal limit there (a template argument: the other's code stays as it is).  Trees
+// have many rows, and not all as many, so that their line has every NT rows of a sequence by themselves, one after the
+// other, and an SM each share of it: no CTA of a group idles where a sequence has fewer rows than the largest.  The CTAs
+// that read a sequence's keys do so at different times, from the L2 cache.  (8 sequences of up to 24 drafts and
+// 4099 rows, 20 heads: 48.7 us with the groups, TREEB so; 2 of 64 drafts and 16384 rows, 64 heads: 412, TREEW.)
 //
 // Measured on one GB300, calls one after the other, 512 + 64 elements:
 //   32 heads, 64 sequences of up to 8192 (378 MB)    74.0 us  5.1 TB/s
@@ -142,8 +146,10 @@ struct LatentParams {
     int flags;
     int q_even;   // the queries' rows are evenly spaced: copied with TMA
     int out16;    // out's rows start on 16 bytes
-    int by_seq;   // descriptors of split sequences: one a sequence, else one a group
+    int by_seq;   // descriptors of split sequences: one a sequence (drafted tokens: and block of rows), else one a group
+    int most;     // blocks of rows of a sequence with max_q drafted tokens
     int words;    // of a drafted token's mask
+    int tell;     // floats of the descriptors, before the pieces
     const unsigned long long *tree;  // the masks, or null
     long long ld_tree;
     int pw;       // warps of the joining kernel that share a sequence's pieces
@@ -186,6 +192,9 @@ __device__ __forceinline__ int tiles_of(const LatentParams &p, const Seq &s) {
     return s.n > 0 ? max(1, (s.len + kTile - 1) / kTile + p.cost) : 0;
 }
 
+// The blocks of NT rows that a sequence has on a line of drafted tokens.
+__device__ __forceinline__ int blocks_of(const LatentParams &p, const Seq &s) { return (s.n * p.H + p.nt - 1) / p.nt; }
+
 // Where the g-th of `groups` equal shares of a line of `units` tiles begins: floor(units g / groups).
 // A line shorter than p.groups is cut into shares of one tile (groups = units).
 __device__ __forceinline__ int share_begin(const LatentParams &p, int units, int g, int groups) {
@@ -199,11 +208,13 @@ struct Share {
     int units, groups;  // tiles on the line, shares it is cut into
     int u0, u1;         // this share's tiles
     int b, k;           // sequence and tile of the first
+    int r;              // its block of rows (drafted tokens)
     Seq s;              // that sequence
 };
 
 // Found by each warp by itself (no block barrier before the first copies): a pass over the
 // sequences for the line's length, one for the place of the share's beginning.
+template <bool TREE>
 __device__ __forceinline__ Share share_of(const LatentParams &p, int g, bool report) {
     const int lane = threadIdx.x & 31;
     Share s;
@@ -218,18 +229,18 @@ __device__ __forceinline__ Share share_of(const LatentParams &p, int g, bool rep
         } else {
             mine.n = 0;
         }
-        s.units += static_cast<int>(__reduce_add_sync(0xffffffffu, static_cast<unsigned>(tiles_of(p, mine))));
+        s.units += static_cast<int>(__reduce_add_sync(0xffffffffu, static_cast<unsigned>(tiles_of(p, mine) * (TREE ? blocks_of(p, mine) : 1))));
         if (c + 32 >= p.B) break;
         c += 32;
     }
     s.groups = min(p.groups, max(s.units, 1));
-    s.u0 = s.u1 = s.b = s.k = 0;
+    s.u0 = s.u1 = s.b = s.k = s.r = 0;
     if (g >= min(s.groups, s.units)) return s;
     s.u0 = share_begin(p, s.units, g, s.groups);
     s.u1 = share_begin(p, s.units, g + 1, s.groups);
     if (c > 0) mine = seq_of(p, lane);
     for (int at = 0, b0 = 0;;) {
-        const int t = b0 + lane < p.B ? tiles_of(p, mine) : 0;
+        const int t = b0 + lane < p.B ? tiles_of(p, mine) * (TREE ? blocks_of(p, mine) : 1) : 0;
         int x = t;
 #pragma unroll
         for (int off = 1; off < 32; off <<= 1) {
@@ -245,6 +256,11 @@ __device__ __forceinline__ Share share_of(const LatentParams &p, int g, bool rep
             s.s.n = __shfl_sync(0xffffffffu, mine.n, w);
             s.s.n_all = __shfl_sync(0xffffffffu, mine.n_all, w);
             s.s.len = __shfl_sync(0xffffffffu, mine.len, w);
+            if (TREE) {
+                const int tiles = tiles_of(p, s.s);
+                s.r = s.k / tiles;
+                s.k -= s.r * tiles;
+            }
             return s;
         }
         at += __shfl_sync(0xffffffffu, x, 31);
@@ -256,7 +272,7 @@ __device__ __forceinline__ Share share_of(const LatentParams &p, int g, bool rep
 // Scratch: descriptors, then two slots a CTA, each O (NT x R), m and l of a piece.  Slot 1 holds
 // a sequence's first piece, slot 0 a later one.
 __device__ __forceinline__ float *slot_of(const LatentParams &p, int cta, int which, int nt) {
-    return p.ws + 4 * ((p.groups + 3) / 4 * 4) + (static_cast<long long>(cta) * 2 + which) * nt * (p.R + 2);
+    return p.ws + p.tell + (static_cast<long long>(cta) * 2 + which) * nt * (p.R + 2);
 }
 
 // One piece of a share: rows row0 .. row0 + nrows of sequence b, its tiles k0 .. k1 - 1 (none
@@ -270,10 +286,11 @@ struct Piece {
 
 struct Walk {
     int b, k, left;
+    int block;   // of rows (drafted tokens)
     Seq s;       // sequence b, where it is known
     bool known;
     __device__ __forceinline__ explicit Walk(const Share &sh)
-        : b(sh.b), k(sh.k), left(sh.u1 - sh.u0), s(sh.s), known(true) {}
+        : b(sh.b), k(sh.k), left(sh.u1 - sh.u0), block(sh.r), s(sh.s), known(true) {}
     template <bool TREE>
     __device__ __forceinline__ bool next(const LatentParams &p, int r, Piece &o) {
         while (left > 0) {
@@ -288,9 +305,15 @@ struct Walk {
             const int end = max(0, k + take - p.cost);
             o.first = k == 0;
             o.last = k + take == kt;
-            o.row0 = r * p.nt;
+            o.row0 = (TREE ? block : r) * p.nt;
             const int rows = o.s.n * p.H;
-            ++b;
+            if (TREE && ++block < blocks_of(p, o.s)) {
+                s = o.s;
+                known = true;
+            } else {
+                block = 0;
+                ++b;
+            }
             k = 0;
             left -= take;
             if (take == 0 || o.row0 >= rows) continue;
@@ -457,7 +480,7 @@ __global__ void __launch_bounds__(threads_of(NT), 1) latent_attention_kernel(con
                      : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
-    const Share sh = share_of(p, g, blockIdx.x == 0 && warp == 2);  // while the tensor memory is taken
+    const Share sh = share_of<TREE>(p, g, blockIdx.x == 0 && warp == 2);  // while the tensor memory is taken
     if (warp != 0) {
         tc_fence_before();
         asm volatile("bar.sync 2, %0;" ::"n"(threads_of(NT)) : "memory");
@@ -475,7 +498,7 @@ __global__ void __launch_bounds__(threads_of(NT), 1) latent_attention_kernel(con
         // ------------------------------------------------------------------ the copies
         // Two warps, every other slot of latent elements each, the second the rotated elements
         // too: one warp's wait, expect and copy take 630 cycles a slot, two warps 370.
-        const uint64_t policy = policy_of(p.rt == 1);
+        const uint64_t policy = policy_of(TREE ? p.max_q * p.H <= NT : p.rt == 1);
         int at = 0, slot = 0, n = 0, rslot = 0;  // slots and tiles done; the rings' next slots
         unsigned ph = 0, rph = 0;                // parities of the rings' rounds
         bool ok = true;
@@ -669,7 +692,16 @@ __global__ void __launch_bounds__(threads_of(NT), 1) latent_attention_kernel(con
                 const int u_last = sh.u0 + (sh.u1 - sh.u0 - o.left) + tiles_of(p, o.s) - 1;
                 // the last share that begins at or before u_last: ceil((u_last + 1) groups / units) - 1
                 const int g1 = static_cast<int>((static_cast<long long>(u_last + 1) * sh.groups - 1) / sh.units);
-                if (p.by_seq || !o.last) desc[p.by_seq ? o.b : g] = make_int4(o.s.q0, o.s.n, g, o.last ? -1 : g1);
+                if (TREE) {
+                    // (by share: the others that begin in it end in it.)  The rows, and which of the sequence's they are
+                    if (p.by_seq || !o.last) {
+                        const int at = p.by_seq ? o.b * p.most + o.row0 / NT : g;
+                        desc[at] = make_int4(o.s.q0, o.nrows, g, o.last ? -1 : g1);
+                        desc[p.groups + at].x = o.row0;
+                    }
+                } else if (p.by_seq || !o.last) {
+                    desc[p.by_seq ? o.b : g] = make_int4(o.s.q0, o.s.n, g, o.last ? -1 : g1);
+                }
             }
             float m[NC], l[NC];
             int lim[NC];  // keys a row sees (all it sees, or those before the drafted tokens')
@@ -981,7 +1013,7 @@ __global__ void __launch_bounds__(threads_of(NT), 1) latent_attention_kernel(con
 // batch of sequences): 4 at a time and 128 elements, so that a weight serves 16 products.  Where
 // there are few (one long sequence over all groups): 8 at a time, up to 32 warps, so that all are
 // read at once.
-template <int PB, int ES>
+template <int PB, int ES, bool TREE>
 __global__ void __launch_bounds__(PB == 8 ? 1024 : 128) latent_join_kernel(const __grid_constant__ LatentParams p) {
     constexpr int kWarps = PB == 8 ? 32 : 1;  // warps that share elements
     __shared__ __align__(16) float4 acc[kWarps][32];
@@ -995,12 +1027,18 @@ __global__ void __launch_bounds__(PB == 8 ? 1024 : 128) latent_join_kernel(const
     const int at = ((slab >> 2) * (p.nt / 4) + i / 4) * 128 + (slab & 3) * 32 + lane;
     const float inf = __int_as_float(0x7f800000);
     // a sequence without tokens has no pieces, and no descriptor
-    const bool none = p.by_seq && seq_of(p, blockIdx.x).n == 0;
+    const int of = TREE ? static_cast<int>(blockIdx.x) / p.most : static_cast<int>(blockIdx.x);
+    bool none = false;
+    if (p.by_seq) {
+        const Seq s = seq_of(p, of);
+        none = TREE ? static_cast<int>(blockIdx.x) - of * p.most >= blocks_of(p, s) : s.n == 0;
+    }
     pdl_wait();
     if (none) return;
     const int4 d = reinterpret_cast<const int4 *>(p.ws)[blockIdx.x];
-    const int g0 = d.z, g1 = d.w, rows = d.y * p.H;
+    const int g0 = d.z, g1 = d.w, rows = TREE ? d.y : d.y * p.H;
     if (g1 < 0 || row0 >= rows) return;
+    const int base_row = TREE ? reinterpret_cast<const int4 *>(p.ws)[p.groups + blockIdx.x].x : 0;
     auto slot = [&](int g) { return slot_of(p, g * p.rt + r, g == g0 ? 1 : 0, p.nt); };
 
     const int e = lane & 3, mine_at = (lane >> 2) & (PB - 1);
@@ -1101,7 +1139,7 @@ __global__ void __launch_bounds__(PB == 8 ? 1024 : 128) latent_join_kernel(const
     for (int c = 0; c < 4; ++c) {
         const int row = row0 + c;
         const float inv = __shfl_sync(0xffffffffu, inv_e, c);
-        const long long tok = d.x + p.heads.div(row), head = p.heads.mod(row);
+        const long long tok = d.x + p.heads.div(base_row + row), head = p.heads.mod(base_row + row);
         uint16_t *out = p.out + tok * p.out_token + head * p.out_head + 32 * slab + lane;
 #pragma unroll
         for (int z = 0; z < ES; ++z) {
@@ -1111,7 +1149,7 @@ __global__ void __launch_bounds__(PB == 8 ? 1024 : 128) latent_join_kernel(const
         }
     }
     if (p.lse && slab == 0 && lane < 4 && row0 + lane < rows) {
-        const long long tok = d.x + p.heads.div(row0 + lane), head = p.heads.mod(row0 + lane);
+        const long long tok = d.x + p.heads.div(base_row + row0 + lane), head = p.heads.mod(base_row + row0 + lane);
         p.lse[tok * p.lse_token + head] = l == 0.0f ? -inf : (top + log2f(l)) * 0.69314718056f;
     }
 }
@@ -1132,19 +1170,27 @@ struct Tree {
 
 // The sizes of a call: rows a CTA, CTAs a group, groups, a sequence's cost in tiles.
 struct Split {
-    int nt, rt, groups, cost;
+    int nt, rt, groups, cost, most;
     long long ws_bytes;
 };
 
-Split split_of(const sgemm_latent_attention_t &a, int sms) {
+Split split_of(const sgemm_latent_attention_t &a, int sms, bool tree) {
     Split s;
     const long long rows = static_cast<long long>(a.max_q) * a.H;
     // The fewest that hold a sequence's rows, for the room they leave to the ring and the softmax's
     // registers (16 sequences of 8192, 16 heads: 16 rows 33.7 us, 32 34.5, 64 36.9; 32 heads: 32 rows
     // 38.6, 64 40.6); more than 64 would leave room for one tile.
     s.nt = rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
-    s.rt = static_cast<int>((rows + s.nt - 1) / s.nt);
+    s.rt = s.most = static_cast<int>((rows + s.nt - 1) / s.nt);
     const long long tiles = std::max(1LL, (static_cast<long long>(a.table_width) * a.page_size + kTile - 1) / kTile);
+    if (tree) {
+        // a share an SM; the blocks of rows are on the line, all of the largest sequence's at most
+        s.cost = tiles * a.B * s.rt <= sms ? 0 : kPieceCost;
+        s.groups = static_cast<int>(std::max(1LL, std::min<long long>(sms, tiles * a.B * s.rt)));
+        s.rt = 1;
+        s.ws_bytes = s.groups > 1 ? 32LL * s.groups + static_cast<long long>(s.groups) * 2 * s.nt * (a.R + 2) * 4 : 0;
+        return s;
+    }
     // A line that is short whatever the lengths has a share for each tile.  Nothing else is counted
     // then: with a sequence's cost some share has two tiles (one sequence of 1000 rows: 11.9 us,
     // without it 10.8), or, with a share more for it, one has none (11.0).
@@ -1242,6 +1288,9 @@ sgemm_status_t attend(const sgemm_latent_attention_t *a, const Tree *tree, sgemm
     if (st != SGEMM_OK) return st;
     if (tree && (tree->words < 1 || a->max_q > 64LL * tree->words || tree->ld < tree->words || tree->ld >= (1LL << 28)))
         return SGEMM_ERR_INVALID_ARG;
+    // tiles of all blocks of rows, which the kernel counts in 32 bits
+    if (tree && (static_cast<long long>(a->table_width) * a->page_size / kTile + 3) * (a->total_q * a->H / 16 + a->B) >= (1LL << 30))
+        return SGEMM_ERR_UNSUPPORTED_SHAPE;
     if (a->B == 0 || a->total_q == 0) return SGEMM_OK;
     const long long W = a->R + a->E;
     if (!a->q || !a->cache || !a->block_table || !a->seq_lens || !a->out || (tree && !tree->masks))
@@ -1284,7 +1333,7 @@ sgemm_status_t attend(const sgemm_latent_attention_t *a, const Tree *tree, sgemm
     int sms = 0;
     st = device_ready(&sms, &p.err);
     if (st != SGEMM_OK) return st;
-    const Split sp = split_of(*a, sms);
+    const Split sp = split_of(*a, sms, tree != nullptr);
     if (sp.ws_bytes > 0 && (!a->workspace || a->workspace_bytes < sp.ws_bytes)) return SGEMM_ERR_NO_WORKSPACE;
     // and so does the scratch that the call uses
     auto in_scratch = [&](const Heads &h) {
@@ -1321,6 +1370,7 @@ sgemm_status_t attend(const sgemm_latent_attention_t *a, const Tree *tree, sgemm
     p.R = a->R;
     p.E = a->E;
     p.max_q = a->max_q;
+    p.tell = tree ? 8 * sp.groups : (sp.groups + 3) / 4 * 16;
     p.rt = sp.rt;
     p.groups = sp.groups;
     p.cost = sp.cost;
@@ -1338,7 +1388,8 @@ sgemm_status_t attend(const sgemm_latent_attention_t *a, const Tree *tree, sgemm
     p.page_tiles = Divisor::of(std::max(1, a->page_size / kTile));
     p.row_shift = a->page_size >= kTile ? 6 : a->page_size == 32 ? 5 : a->page_size == 16 ? 4 : 3;
     p.out16 = aligned(a->out, 16) && a->out_token % 8 == 0 && a->out_head % 8 == 0 ? 1 : 0;
-    p.by_seq = a->B < sp.groups ? 1 : 0;
+    p.most = sp.most;
+    p.by_seq = (tree ? static_cast<long long>(a->B) * sp.most : a->B) < sp.groups ? 1 : 0;
     // Shared memory: Q, the weights, the rotated elements' ring, then as many slots of latent
     // elements as there is room for
     const int fixed = (a->R / 64 + 1) * sp.nt * 128 + weight_buffers(sp.nt) * kChunk + kRopeSlots * kChunk + kBarBytes +
@@ -1367,14 +1418,16 @@ sgemm_status_t attend(const sgemm_latent_attention_t *a, const Tree *tree, sgemm
     // it would have if all were as long as the table allows), for 32 elements.  The one against the
     // other, 8192 rows with 32 heads: 9 sequences (288 warps) 26.4 us, 25.3; 12 (384) 30.9, 31.0;
     // 16 (512) 36.6, 38.6; 64 (2048) 74.2, 79.6; one of 131072 (32) 57.5, 36.7.
-    const long long rows = static_cast<long long>(a->max_q) * a->H;
-    const int n = p.by_seq ? a->B : sp.groups, parts = p.by_seq ? (sp.groups + a->B - 1) / a->B + 1 : 2;
+    const long long rows = tree ? std::min<long long>(sp.nt, static_cast<long long>(a->max_q) * a->H) : static_cast<long long>(a->max_q) * a->H;
+    const int n = p.by_seq ? a->B * (tree ? sp.most : 1) : sp.groups, parts = p.by_seq ? (sp.groups + n - 1) / n + 1 : 2;
     const bool few = (rows + 3) / 4 * (a->R / 128) * n * 2 >= 5LL * sms;
     p.pw = few ? 1 : std::min(32, (parts + 7) / 8);
     const dim3 grid(static_cast<unsigned>(n), static_cast<unsigned>((rows + 3) / 4),
                     static_cast<unsigned>(few ? 1 : a->R / 32));
-    const void *join = few ? reinterpret_cast<const void *>(&latent_join_kernel<4, 4>)
-                           : reinterpret_cast<const void *>(&latent_join_kernel<8, 1>);
+    const void *join = few ? (tree ? reinterpret_cast<const void *>(&latent_join_kernel<4, 4, true>)
+                                   : reinterpret_cast<const void *>(&latent_join_kernel<4, 4, false>))
+                           : (tree ? reinterpret_cast<const void *>(&latent_join_kernel<8, 1, true>)
+                                   : reinterpret_cast<const void *>(&latent_join_kernel<8, 1, false>));
     // The first kernel never lets this one come early: blocks that came were in the way of CTAs
     // still running (verification of 8 sequences: 28.8 us, against 26.7).
     if (launch(join, grid, dim3(static_cast<unsigned>(32 * (few ? a->R / 128 : p.pw))), 0, cs, &p) != cudaSuccess)
@@ -1385,18 +1438,29 @@ sgemm_status_t attend(const sgemm_latent_attention_t *a, const Tree *tree, sgemm
 }  // namespace latent
 }  // namespace sk
 
-extern "C" sgemm_status_t sgemm_latent_attention_workspace(const sgemm_latent_attention_t *a, long long *bytes) {
-    using namespace sk;
+namespace sk {
+namespace latent {
+sgemm_status_t workspace_of(const sgemm_latent_attention_t *a, bool tree, long long *bytes) {
     if (!a || !bytes) return SGEMM_ERR_INVALID_ARG;
     *bytes = 0;
-    sgemm_status_t st = latent::check_sizes(*a);
+    sgemm_status_t st = check_sizes(*a);
     if (st != SGEMM_OK) return st;
     if (a->B == 0 || a->total_q == 0) return SGEMM_OK;
     int sms = 0, *err = nullptr;
     st = device_ready(&sms, &err);
     if (st != SGEMM_OK) return st;
-    *bytes = latent::split_of(*a, sms).ws_bytes;
+    *bytes = split_of(*a, sms, tree).ws_bytes;
     return SGEMM_OK;
+}
+}  // namespace latent
+}  // namespace sk
+
+extern "C" sgemm_status_t sgemm_latent_attention_workspace(const sgemm_latent_attention_t *a, long long *bytes) {
+    return sk::latent::workspace_of(a, false, bytes);
+}
+
+extern "C" sgemm_status_t sgemm_latent_tree_attention_workspace(const sgemm_latent_attention_t *a, long long *bytes) {
+    return sk::latent::workspace_of(a, true, bytes);
 }
 
 extern "C" sgemm_status_t sgemm_bf16_latent_attention(const sgemm_latent_attention_t *a, sgemm_stream_t stream) {

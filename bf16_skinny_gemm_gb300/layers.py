@@ -17,11 +17,11 @@ import struct
 import torch
 
 from . import SgemmError, _empty
-from .decode import _ATTN, _fn, _on_current_device, _shape, _strides, sgemm_latent_attention_workspace
+from .decode import _ATTN, _fn, _on_current_device, _shape, _strides
 
 __all__ = [
     "sgemm_bf16_moe_route", "sgemm_bf16_moe_experts", "sgemm_moe_experts_workspace",
-    "sgemm_bf16_latent_tree_attention", "sgemm_bf16_linear_step", "sgemm_bf16_linear_attention",
+    "sgemm_bf16_latent_tree_attention", "sgemm_latent_tree_attention_workspace", "sgemm_bf16_linear_step", "sgemm_bf16_linear_attention",
     "sgemm_linear_attention_workspace", "SGEMM_ROUTE_SOFTMAX", "SGEMM_ROUTE_SIGMOID", "MOE_MAX_TOKENS",
 ]
 
@@ -152,6 +152,19 @@ def sgemm_bf16_moe_experts(x: torch.Tensor, w_gate_up: torch.Tensor, w_down: tor
 
 
 # -------------------------------------------------------------------- attention for drafted tokens
+def sgemm_latent_tree_attention_workspace(batch: int, heads: int, rank: int, rope: int, page_size: int,
+                                          table_width: int, max_q: int = 1) -> int:
+    """Bytes of scratch :func:`sgemm_bf16_latent_tree_attention` needs for such a call (at most
+    ``LATENT_WORKSPACE_MAX``)."""
+    n = ctypes.c_longlong(0)
+    args = _ATTN.pack(*([0] * 16), 1, 0, min(batch * max_q, 1), page_size, table_width, batch, heads, rank, rope, max_q,
+                      1.0, 0, 0)
+    status = _fn("sgemm_latent_tree_attention_workspace")(args, ctypes.addressof(n))
+    if status:
+        raise SgemmError(status, "sgemm_latent_tree_attention_workspace")
+    return n.value
+
+
 def sgemm_bf16_latent_tree_attention(q: torch.Tensor, cache: torch.Tensor, block_table: torch.Tensor,
                                      seq_lens: torch.Tensor, rank: int, scale: float, tree: torch.Tensor,
                                      cu_q: torch.Tensor | None = None, max_q: int = 1,
@@ -190,7 +203,7 @@ def sgemm_bf16_latent_tree_attention(q: torch.Tensor, cache: torch.Tensor, block
     _on_current_device(q=q, cache=cache, block_table=block_table, seq_lens=seq_lens, tree=tree, cu_q=cu_q, out=out, lse=lse)
     if total == 0 or B == 0:
         return out, lse
-    need = 0 if workspace is not None else sgemm_latent_attention_workspace(B, H, rank, W - rank, page_size, table_width, max_q)
+    need = 0 if workspace is not None else sgemm_latent_tree_attention_workspace(B, H, rank, W - rank, page_size, table_width, max_q)
     workspace, pws, nws = _scratch(workspace, need, q.device, stream)
     # strides along dimensions of one element are of no account
     if page_size == 1:

@@ -114,15 +114,19 @@ sgemm_status_t sgemm_bf16_moe_experts(const sgemm_moe_experts_t *args, sgemm_str
  *     bit j: tree[t * ld_tree + j / 64] >> (j % 64) & 1        (t: the token's row of q)
  * so that a token that is to see itself has its own bit.  Bits of tokens that the
  * sequence does not have, and of rows before the cache's first, change nothing.
- * All else is as sgemm_bf16_latent_attention has it, its limits on batches of
- * unlike numbers of new tokens among it; the scratch is the same.  (A row of a
- * new token with an infinity or a NaN among its values adds nothing to the tokens
+ * All else is as sgemm_bf16_latent_attention has it, but that the work is split evenly
+ * whatever numbers of new tokens the sequences have, and that the scratch is
+ * sgemm_latent_tree_attention_workspace bytes.  (A row of a new token with an infinity or a NaN among its values adds nothing to the tokens
  * that do not see it, and may add nothing where it is infinite or NaN to those that do.)
+ * - (table_width * page_size / 64 + 3) * (total_q * H / 16 + B) < 2^30.
  * - words >= 1: 64-bit words a token, max_q <= 64 * words; words <= ld_tree < 2^28;
  *   tree is 8-byte aligned and overlaps no output. */
 sgemm_status_t sgemm_bf16_latent_tree_attention(const sgemm_latent_attention_t *args,
                                                 const long long *tree, long long ld_tree, int words,
                                                 sgemm_stream_t stream);
+
+/* 0 .. SGEMM_LATENT_WORKSPACE_MAX, as for the attention without drafted tokens. */
+sgemm_status_t sgemm_latent_tree_attention_workspace(const sgemm_latent_attention_t *args, long long *bytes);
 
 /* ------------------------------------------- linear attention, a decay for each head */
 
