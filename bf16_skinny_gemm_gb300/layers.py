@@ -12,12 +12,16 @@ on the current device, and the calls can be captured into a CUDA graph.
 from __future__ import annotations
 
 import ctypes
+import importlib.machinery
+import importlib.util
 import struct
+import warnings
 
 import torch
 
-from . import SgemmError, _empty
-from .decode import _ATTN, _fn, _on_current_device, _shape, _strides
+from . import SgemmError, _empty, load
+from .build import marshal_path
+from .decode import _ATTN, _fn, _on_current_device, _raw, _shape, _strides
 
 __all__ = [
     "sgemm_bf16_moe_route", "sgemm_bf16_moe_experts", "sgemm_moe_experts_workspace",
@@ -37,6 +41,56 @@ _LINEAR = struct.Struct("<10Q16q4ifI")   # sgemm_linear_attention_t
 
 _BF16 = torch.bfloat16
 _SCORING = {"softmax": SGEMM_ROUTE_SOFTMAX, "sigmoid": SGEMM_ROUTE_SIGMOID}
+
+
+class _None:
+    """In place of the native module where there is none for this Python and torch."""
+
+    def moe_route(self, *args):
+        return -1
+
+    moe_experts = latent_tree_attention = linear_step = linear_attention = moe_route
+
+
+class _Unbound:
+    """Stands in for it until the first call has loaded the library."""
+
+    def _first(self, name, args):
+        global _short
+        lib = load()
+        try:
+            loader = importlib.machinery.ExtensionFileLoader("_marshal", marshal_path())
+            module = importlib.util.module_from_spec(importlib.util.spec_from_loader("_marshal", loader))
+            loader.exec_module(module)
+            module.bind_layers(*(ctypes.cast(getattr(lib, f), ctypes.c_void_p).value for f in (
+                "sgemm_bf16_moe_route", "sgemm_bf16_moe_experts", "sgemm_bf16_latent_tree_attention",
+                "sgemm_bf16_linear_step", "sgemm_bf16_linear_attention")))
+        except (ImportError, AttributeError) as e:
+            warnings.warn(f"calls take longer than they need: {e}; build the module for this torch with "
+                          "python -c 'import __graft_entry__ as g; g.build()'", RuntimeWarning, stacklevel=4)
+            module = _None()
+        _short = module
+        return getattr(module, name)(*args)
+
+    def moe_route(self, *args):
+        return self._first("moe_route", args)
+
+    def moe_experts(self, *args):
+        return self._first("moe_experts", args)
+
+    def latent_tree_attention(self, *args):
+        return self._first("latent_tree_attention", args)
+
+    def linear_step(self, *args):
+        return self._first("linear_step", args)
+
+    def linear_attention(self, *args):
+        return self._first("linear_attention", args)
+
+
+# The short way of a well-formed call with all its buffers given (native/marshal.cpp), as in decode:
+# the call's status, or -1 for what the checks below have to look at.
+_short = _Unbound()
 
 
 def _call(name: str, args: bytes, t: torch.Tensor, stream, *more) -> None:
@@ -72,6 +126,11 @@ def sgemm_bf16_moe_route(x: torch.Tensor, w: torch.Tensor, k: int, bias: torch.T
     (plus ``bias``, FP32 [E], which counts for the choice only), the largest first, the lower index
     of equal ones.  ids: int32 [T, k]; weights: FP32 [T, k], the chosen scores (divided by their sum
     with ``renormalize``) times ``scale``.  Both may be columns of wider arrays."""
+    status = _short.moe_route(x, w, k, bias, _SCORING.get(scoring), renormalize, scale, ids, weights, flags, _raw(stream))
+    if status == 0:
+        return ids, weights
+    if status > 0:
+        raise SgemmError(status, "sgemm_bf16_moe_route")
     T, D = _shape(x, "x", _BF16, 2)
     E = _shape(w, "w", _BF16, 2)[0]
     if scoring not in _SCORING:
@@ -121,6 +180,11 @@ def sgemm_bf16_moe_experts(x: torch.Tensor, w_gate_up: torch.Tensor, w_down: tor
     x, y: BF16 [T, D], T <= ``MOE_MAX_TOKENS``; w_gate_up: BF16 [E, 2 F, D], a gate's rows before its
     up rows; w_down: BF16 [E, D, F]; ids: int32 [T, k]; weights: FP32 [T, k].  ``workspace``: scratch
     on the device (:func:`sgemm_moe_experts_workspace` bytes; allocated for the call where None)."""
+    status = _short.moe_experts(x, w_gate_up, w_down, ids, weights, y, workspace, flags, _raw(stream))
+    if status == 0:
+        return y
+    if status > 0:
+        raise SgemmError(status, "sgemm_bf16_moe_experts")
     T, D = _shape(x, "x", _BF16, 2)
     E, F2, _ = _shape(w_gate_up, "w_gate_up", _BF16, 3)
     k = _shape(ids, "ids", torch.int32, 2)[1]
@@ -177,6 +241,12 @@ def sgemm_bf16_latent_tree_attention(q: torch.Tensor, cache: torch.Tensor, block
     new ones sees the ``seq_lens - n`` rows before them, and new token j's row where bit ``j % 64`` of
     word ``j // 64`` is set (for a tree: its ancestors and itself).  At most 64 * words new tokens a
     sequence.  A token that sees nothing gets zeros (and -inf).  All else is as there."""
+    status = _short.latent_tree_attention(q, cache, block_table, seq_lens, rank, scale, cu_q, max_q, out, lse, workspace, flags,
+                                          _raw(stream), tree)
+    if status == 0:
+        return out, lse
+    if status > 0:
+        raise SgemmError(status, "sgemm_bf16_latent_tree_attention")
     total, H, W = shape = _shape(q, "q", _BF16, 3)
     pages, page_size, width = _shape(cache, "cache", _BF16, 3)
     B, table_width = _shape(block_table, "block_table", torch.int32, 2)
@@ -262,6 +332,11 @@ def sgemm_bf16_linear_step(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g:
     ``h // (Hv // Hk)``), Dk and Dv 64 or 128; g: FP32 [B, Hv], logarithms of the decays (strides of
     0 allowed); state: FP32 [slots, Hv, Dk, Dv]; slots: int64 [B], each sequence's state (negative:
     a padded sequence, whose out is 0).  In place, ``S = exp(g) S + k v^T``; ``out = scale * q^T S``."""
+    status = _short.linear_step(q, k, v, g, state, slots, scale, out, flags, _raw(stream))
+    if status == 0:
+        return out
+    if status > 0:
+        raise SgemmError(status, "sgemm_bf16_linear_step")
     (B, pool, Hk, Hv, Dk, Dv), s, out = _linear(q, k, v, g, state, out, stream)
     _strides(slots, "slots", torch.int64, (B,))
     _on_current_device(q=q, k=k, v=v, g=g, state=state, slots=slots, out=out)
@@ -296,6 +371,11 @@ def sgemm_bf16_linear_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tenso
     ``fresh[b]``, int32 [B], is not 0) and leaves its last state there (slots: int64 [B]; negative:
     from zeros, not kept).  ``workspace``: scratch on the device
     (:func:`sgemm_linear_attention_workspace` bytes; allocated for the call where None)."""
+    status = _short.linear_attention(q, k, v, g, state, slots, cu, scale, fresh, out, workspace, flags, _raw(stream))
+    if status == 0:
+        return out
+    if status > 0:
+        raise SgemmError(status, "sgemm_bf16_linear_attention")
     (N, pool, Hk, Hv, Dk, Dv), s, out = _linear(q, k, v, g, state, out, stream)
     B = _shape(slots, "slots", torch.int64, 1)[0]
     _strides(slots, "slots", torch.int64, (B,))
