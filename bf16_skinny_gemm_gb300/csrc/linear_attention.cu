@@ -430,9 +430,9 @@ constexpr int kOutStage = kC * 256;  // a chunk's outputs on their way
 __host__ __device__ constexpr int out_fixed(int dk) { return 2 * 3 * dk / 64 * kPart + kPart + kOutStage + kMiscOut; }
 constexpr int kStateFixed = 512 + 4 * kC * 4;
 // Columns of tensor memory: the state kernel's (U, two buffers of keys in three numbers), the output kernel's
-// (two buffers of values).
+// (two buffers of O1 and of values: O1 is what the next state waits for, not the outputs' warps).
 constexpr int kU = 0, kKeyT = 128;
-constexpr int kState = 0, kSb = 128, kA = 192, kO1 = 256, kO2 = 320, kValueT = 384;
+constexpr int kState = 0, kSb = 128, kA = 192, kO1 = 256, kO2 = 384, kValueT = 448;
 
 // ------------------------------------------------------------------------ 1. states of cut pieces
 template <int DK>
@@ -842,20 +842,20 @@ __global__ void __launch_bounds__(kOutThreads, 1) linear_outputs_kernel(const __
                 mma_commit(sdone + 8 * (n & 1));
             }
             __syncwarp();
-            if (!(ok = n == 0 || phase(ofree, (n - 1) & 1, &stop))) break;
-            tc_fence_after();
             if (elect()) {
+                // (the buffer of O1 two chunks ago was free before O2 of the last one)
 #pragma unroll
                 for (int i = 0; i < kKParts; ++i)
 #pragma unroll
                     for (int kk = 0; kk < 4; ++kk)
-                        mma_ts(d + kO1, d + kSb + 32 * i + 8 * kk, tc05::sw128_desc(st + i * kPart) + ((32 * kk) >> 4), kIdO, i != 0 || kk != 0);
+                        mma_ts(d + kO1 + 64 * (n & 1), d + kSb + 32 * i + 8 * kk, tc05::sw128_desc(st + i * kPart) + ((32 * kk) >> 4), kIdO,
+                               i != 0 || kk != 0);
                 mma_commit(o1done);
                 mma_commit(qempty + 8 * slot);
             }
             __syncwarp();
             if (++slot == S) slot = 0;
-            if (!(ok = phase(pready, n, &stop))) break;
+            if (!(ok = phase(pready, n, &stop) && (n == 0 || phase(ofree, n - 1, &stop)))) break;
             tc_fence_after();
             if (elect()) {
                 const uint64_t b = tc05::sw128_desc(saddr(ps));
@@ -1108,28 +1108,33 @@ __global__ void __launch_bounds__(kOutThreads, 1) linear_outputs_kernel(const __
             uint16_t *out = p.out + static_cast<long long>(c.t0) * p.o_token + c.h * p.o_head;
             if (32 * q < p.Dv)
 #pragma unroll 1
-                for (int part = 0; part < 8; ++part) {  // 16 rows x 16 tokens
-                    const int h = part & 1, t1 = 16 * (part >> 1);
+                for (int part = 0; part < 4; ++part) {  // 16 rows x 32 tokens
+                    const int h = part & 1, t1 = 32 * (part >> 1);
                     const uint32_t from = tmem + quarter + (static_cast<uint32_t>(16 * h) << 16) + t1;
-                    uint32_t a[8], b[8], o[4];
-                    tmem_ld_s(from + kO1, a);
+                    uint32_t a[16], b[16];
+                    tmem_ld_s(from + kO1 + 64 * (n & 1), a);
                     tmem_ld_s(from + kO2, b);
                     asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
                     if (bad)
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) {
+                        for (int i = 0; i < 16; ++i) {
                             const int first = first_bad[128 * (n & 3) + 32 * q + 16 * h + 8 * ((i >> 1) & 1) + (lane >> 2)];
                             if (t1 + 8 * (i >> 2) + c0 + (i & 1) >= first) b[i] = __float_as_uint(nan);
                         }
 #pragma unroll
-                    for (int m = 0; m < 4; ++m) {
-                        const unsigned long long ee = *reinterpret_cast<const unsigned long long *>(&e[t1 + 8 * (m >> 1) + c0]);
-                        uint32_t x, y;
-                        unpack2(ffma2(ee, pack2(a[2 * m], a[2 * m + 1]), mul2(scale, pack2(b[2 * m], b[2 * m + 1]))), x, y);
-                        o[m] = bf16x2(__uint_as_float(x), __uint_as_float(y));
+                    for (int i = 0; i < 2; ++i) {
+                        uint32_t o[4];
+#pragma unroll
+                        for (int m = 0; m < 4; ++m) {
+                            const int r = 8 * i + 2 * m;
+                            const unsigned long long ee = *reinterpret_cast<const unsigned long long *>(&e[t1 + 16 * i + 8 * (m >> 1) + c0]);
+                            uint32_t x, y;
+                            unpack2(ffma2(ee, pack2(a[r], a[r + 1]), mul2(scale, pack2(b[r], b[r + 1]))), x, y);
+                            o[m] = bf16x2(__uint_as_float(x), __uint_as_float(y));
+                        }
+                        stmatrix_turned(to_s + (t1 + 16 * i + 8 * (lane >> 4) + (lane & 7)) * 256 +
+                                            (((4 * q + 2 * h + ((lane >> 3) & 1)) ^ (lane & 7)) << 4), o);
                     }
-                    stmatrix_turned(to_s + (t1 + 8 * (lane >> 4) + (lane & 7)) * 256 +
-                                        (((4 * q + 2 * h + ((lane >> 3) & 1)) ^ (lane & 7)) << 4), o);
                 }
             tc_fence_before();
             __syncwarp();
