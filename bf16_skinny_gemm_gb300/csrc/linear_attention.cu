@@ -33,7 +33,7 @@
 // together in FP32.  Why K' in three numbers (cut off after 8 bits each: 24 bits): its rounding would be the
 // state's only error above FP32's, 2^-9 of every summand (in two numbers 2^-18), and it goes on to all later
 // tokens.  P and Sb are rounded once: what they make is rounded to BF16 right after.
-// Roles: a warp copies (TMA, a ring of chunks), a warp issues all products, a warp sums the decays, and
+// Roles: a warp copies (TMA, a ring of chunks), two issue the products, a warp sums the decays, and
 // eight turn the values and scale the keys, and four each carry the state, apply the decays to A, and write the outputs.
 // Exponents' sums are kept as pairs of FP32 numbers where states are made of them: differences of long sums
 // keep their digits.
@@ -60,8 +60,8 @@ constexpr int kC = 64;                 // tokens a chunk
 constexpr int kPart = kC * 128;        // 64 tokens x 64 elements, bytes
 constexpr int kStages = 6;             // of chunks in a ring, at most
 constexpr int kFew = 8;                // chunks a share has at least
-constexpr int kOutThreads = 24 * 32;   // copies, products, sums, (none), state, decays, outputs (4 each), values and keys (8)
-constexpr int kSums = 4;               // chunks whose sums of g are kept
+constexpr int kOutThreads = 24 * 32;   // copies, products, sums, products, state, decays, outputs (4 each), values and keys (8)
+constexpr int kSums = 8;               // chunks whose sums of g are kept
 constexpr int kStateThreads = 12 * 32;  // copies, products, keys (8), sums, (none)
 // A decay's exponent (base 2) is cut here: 2^-200 is 0.  The sum of a chunk's is then 12800 at most, one
 // FP32 number of it off by 2^-11, and a factor exp2 of a difference by 2^-10.5: below BF16's rounding.
@@ -310,12 +310,6 @@ __host__ __device__ constexpr uint32_t idesc_of(int m, int n, bool a_mn, bool b_
            (static_cast<uint32_t>(n >> 3) << 17) | (static_cast<uint32_t>(m >> 4) << 24);
 }
 
-// 16 columns of a 64-row accumulator in the 16 x 256-bit form: lane l has rows l / 4 and l / 4 + 8
-// of the warp's 16, of each 8 columns the pair 2 (l % 4).
-__device__ __forceinline__ void tmem_ld_a(uint32_t addr, uint32_t (&r)[8]) {
-    tmem_ld_s(addr, r);
-    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
-}
 // 16 lanes x 4 N columns (N = 2, 4 here): register 2 i of lane l goes to row l / 4, column 4 i + l % 4, register 2 i + 1
 // to row l / 4 + 8.  This is how turned 8 x 8 matrices of BF16 pairs come from shared memory.
 __device__ __forceinline__ void tmem_st_turned(uint32_t addr, const uint32_t (&r)[8]) {
@@ -697,8 +691,8 @@ __global__ void __launch_bounds__(kOutThreads, 1) linear_outputs_kernel(const __
     // values, keys and queries of a slot by themselves: each is free when it was read
     const uint32_t vfull = take(kStages), kfull = take(kStages), qfull = take(kStages), vempty = take(kStages),
                    kempty = take(kStages), qempty = take(kStages), gready = take(kSums), kready = take(2), vready = take(2),
-                   sdone = take(2), afull = take(1), afree = take(1), pready = take(1), odone = take(2), ofree = take(1),
-                   sready = take(1), o1done = take(1), fin = take(1);
+                   sdone = take(2), afull = take(1), afree = take(1), pready = take(1), odone = take(2), ofree = take(2),
+                   sready = take(1), o1done = take(2), fin = take(2);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = static_cast<int>(blockIdx.x);
     if (threadIdx.x == 0) {
         prefetch_tmap(&p.tq);
@@ -713,7 +707,7 @@ __global__ void __launch_bounds__(kOutThreads, 1) linear_outputs_kernel(const __
         init(qfull, kStages, 1);
         init(vempty, kStages, 8);
         init(kempty, kStages, 9);
-        init(qempty, kStages, 1);
+        init(qempty, kStages, 2);
         init(gready, kSums, 1);
         init(kready, 2, 8);
         init(vready, 2, 8);
@@ -722,10 +716,10 @@ __global__ void __launch_bounds__(kOutThreads, 1) linear_outputs_kernel(const __
         init(afree, 1, 4);
         init(pready, 1, 4);
         init(odone, 2, 1);
-        init(ofree, 1, 4);
+        init(ofree, 2, 4);
         init(sready, 1, 4);
-        init(o1done, 1, 1);
-        init(fin, 1, 1);
+        init(o1done, 2, 1);
+        init(fin, 2, 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     }
@@ -750,7 +744,8 @@ __global__ void __launch_bounds__(kOutThreads, 1) linear_outputs_kernel(const __
     const uint32_t quarter = static_cast<uint32_t>(32 * q) << 16;
     int issued = 0, vissued = 0, qissued = 0;
     Chunk c;
-    // (the sums of chunk n + 8 come after the state's product of n + 6, so after n's outputs)
+    // (the sums of chunk n + 8 come after the state's product of n + 6, so after O1 of n + 5, so after the outputs
+    // of n + 3: what is told and summed of n is not read any more)
     auto hear = [&](int n) {
         const int4 v = told[n & 7];
         c.b = v.x;
@@ -796,77 +791,84 @@ __global__ void __launch_bounds__(kOutThreads, 1) linear_outputs_kernel(const __
             }
         }
     } else if (warp == 1) {
-        // ------------------------------------------------------------------ the products
-        constexpr uint32_t kIdA = idesc_of(64, 64, false, false), kIdO = idesc_of(128, 64, false, false),
-                           kIdS = idesc_of(128, DK, false, true);
+        // ------------------------------------------------- the state's products, and O1 of it
+        constexpr uint32_t kIdO = idesc_of(128, 64, false, false), kIdS = idesc_of(128, DK, false, true);
         const uint32_t d = alike(static_cast<int>(tmem));
-        int slot = 0, aslot = 0;  // of the current chunk, of the next A
-        unsigned aph = 0;
-        bool ok = true;
-        auto scores = [&](int n) {
-            ok = phase(qfull + 8 * aslot, aph, &stop) && phase(kfull + 8 * aslot, aph, &stop) && (n == 0 || phase(afree, (n - 1) & 1, &stop));
-            if (!ok) return;
+        int slot = 0;
+        unsigned ph = 0;
+        for (int n = 0; n < total; ++n) {
+            if (!phase(vready + 8 * (n & 1), n >> 1, &stop) || !phase(kready + 8 * (n & 1), n >> 1, &stop) || !phase(sready, n, &stop)) break;
             tc_fence_after();
             if (elect()) {
-                const uint32_t st = saddr(base) + aslot * stage;
+                const uint64_t b = mn_desc(saddr(keys) + (n & 1) * 3 * kKeys);
+#pragma unroll 1
+                for (int part = 0; part < 3; ++part)
 #pragma unroll
+                    for (int kk = 0; kk < kC / 16; ++kk)
+                        mma_ts(d + kState, d + kValueT + 32 * (n & 1) + 8 * kk, b + ((part * kKeys) >> 4) + kk * (2048 >> 4), kIdS, true);
+                mma_commit(sdone + 8 * (n & 1));
+            }
+            __syncwarp();
+            if (!phase(qfull + 8 * slot, ph, &stop) || (n >= 2 && !phase(ofree + 8 * (n & 1), (n >> 1) - 1, &stop))) break;
+            tc_fence_after();
+            if (elect()) {
+                const uint32_t st = saddr(base) + slot * stage;
+#pragma unroll 1
+                for (int i = 0; i < kKParts; ++i)
+#pragma unroll
+                    for (int kk = 0; kk < 4; ++kk)
+                        mma_ts(d + kO1 + 64 * (n & 1), d + kSb + 32 * i + 8 * kk, tc05::sw128_desc(st + i * kPart) + ((32 * kk) >> 4), kIdO,
+                               i != 0 || kk != 0);
+                mma_commit(o1done + 8 * (n & 1));
+                mma_commit(qempty + 8 * slot);
+            }
+            __syncwarp();
+            if (++slot == S) {
+                slot = 0;
+                ph ^= 1;
+            }
+        }
+        finish(fin, &stop);
+    } else if (warp == 3) {
+        // ------------------------------------------- A, and O2 of it: a warp of their own, for neither
+        // is to wait for what the others' operands wait for
+        constexpr uint32_t kIdA = idesc_of(64, 64, false, false), kIdO = idesc_of(128, 64, false, false);
+        const uint32_t d = alike(static_cast<int>(tmem));
+        int slot = 0;
+        unsigned ph = 0;
+        for (int n = 0; n < total; ++n) {
+            if (!phase(qfull + 8 * slot, ph, &stop) || !phase(kfull + 8 * slot, ph, &stop) || (n > 0 && !phase(afree, n - 1, &stop))) break;
+            tc_fence_after();
+            if (elect()) {
+                const uint32_t st = saddr(base) + slot * stage;
+#pragma unroll 1
                 for (int i = 0; i < kKParts; ++i)
 #pragma unroll
                     for (int kk = 0; kk < 4; ++kk)
                         mma(d + kA, tc05::sw128_desc(st + i * kPart) + ((32 * kk) >> 4),
                             tc05::sw128_desc(st + kKeys + i * kPart) + ((32 * kk) >> 4), kIdA, i != 0 || kk != 0);
                 mma_commit(afull);
-                mma_commit(kempty + 8 * aslot);
-            }
-            __syncwarp();
-            if (++aslot == S) {
-                aslot = 0;
-                aph ^= 1;
-            }
-        };
-        scores(0);
-        for (int n = 0; ok && n < total; ++n) {
-            const uint32_t st = saddr(base) + slot * stage, vt = d + kValueT + 32 * (n & 1);
-            // the state first: its chain is the longest
-            if (!(ok = phase(vready + 8 * (n & 1), (n >> 1) & 1, &stop) && phase(kready + 8 * (n & 1), (n >> 1) & 1, &stop) &&
-                       phase(sready, n & 1, &stop)))
-                break;
-            tc_fence_after();
-            if (elect()) {
-                const uint64_t b = mn_desc(saddr(keys) + (n & 1) * 3 * kKeys);
-#pragma unroll
-                for (int part = 0; part < 3; ++part)
-#pragma unroll
-                    for (int kk = 0; kk < kC / 16; ++kk)
-                        mma_ts(d + kState, vt + 8 * kk, b + ((part * kKeys) >> 4) + kk * (2048 >> 4), kIdS, true);
-                mma_commit(sdone + 8 * (n & 1));
-            }
-            __syncwarp();
-            if (elect()) {
-                // (the buffer of O1 two chunks ago was free before O2 of the last one)
-#pragma unroll
-                for (int i = 0; i < kKParts; ++i)
-#pragma unroll
-                    for (int kk = 0; kk < 4; ++kk)
-                        mma_ts(d + kO1 + 64 * (n & 1), d + kSb + 32 * i + 8 * kk, tc05::sw128_desc(st + i * kPart) + ((32 * kk) >> 4), kIdO,
-                               i != 0 || kk != 0);
-                mma_commit(o1done);
+                mma_commit(kempty + 8 * slot);
                 mma_commit(qempty + 8 * slot);
             }
             __syncwarp();
-            if (++slot == S) slot = 0;
-            if (!(ok = phase(pready, n, &stop) && (n == 0 || phase(ofree, n - 1, &stop)))) break;
+            if (++slot == S) {
+                slot = 0;
+                ph ^= 1;
+            }
+            if (!phase(vready + 8 * (n & 1), n >> 1, &stop) || !phase(pready, n, &stop) ||
+                (n > 0 && !phase(ofree + 8 * ((n - 1) & 1), (n - 1) >> 1, &stop)))
+                break;
             tc_fence_after();
             if (elect()) {
                 const uint64_t b = tc05::sw128_desc(saddr(ps));
 #pragma unroll
-                for (int kk = 0; kk < kC / 16; ++kk) mma_ts(d + kO2, vt + 8 * kk, b + ((32 * kk) >> 4), kIdO, kk != 0);
+                for (int kk = 0; kk < kC / 16; ++kk) mma_ts(d + kO2, d + kValueT + 32 * (n & 1) + 8 * kk, b + ((32 * kk) >> 4), kIdO, kk != 0);
                 mma_commit(odone + 8 * (n & 1));
             }
             __syncwarp();
-            if (n + 1 < total) scores(n + 1);
         }
-        finish(fin, &stop);
+        finish(fin + 8, &stop);
     } else if (warp == 2) {
         // ---------------------------------------------------------------- the sums of decays
         Cursor ahead = cursor;
@@ -898,11 +900,17 @@ __global__ void __launch_bounds__(kOutThreads, 1) linear_outputs_kernel(const __
         for (int n = 0; n < total; ++n) {
             const int buf = n & (kSums - 1), b4 = n & 3;
             // (the sums come after the state's product that read this buffer of keys)
-            if (!phase(gready + 8 * buf, n / kSums, &stop) || !phase(vfull + 8 * slot, ph, &stop) ||
-                (n >= 2 && !phase(odone + 8 * (n & 1), (n >> 1) - 1, &stop)))
-                break;
-            tc_fence_after();
+            if (!phase(gready + 8 * buf, n / kSums, &stop) || !phase(kfull + 8 * slot, ph, &stop)) break;
             hear(n);
+            scale_keys<DK>(base + slot * stage + kKeys, keys + (n & 1) * 3 * kKeys, wk + buf * kC, warp - 16, c.valid);
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            __syncwarp();
+            if (lane == 0) {
+                bar_arrive(kready + 8 * (n & 1));
+                bar_arrive(kempty + 8 * slot);
+            }
+            if (!phase(vfull + 8 * slot, ph, &stop) || (n >= 2 && !phase(odone + 8 * (n & 1), (n >> 1) - 1, &stop))) break;
+            tc_fence_after();
             {
                 // 16 elements x 64 tokens a warp
                 const int h = (warp - 16) >> 2;
@@ -949,14 +957,6 @@ __global__ void __launch_bounds__(kOutThreads, 1) linear_outputs_kernel(const __
                 bar_arrive(vready + 8 * (n & 1));
                 bar_arrive(vempty + 8 * slot);
             }
-            if (!phase(kfull + 8 * slot, ph, &stop)) break;
-            scale_keys<DK>(base + slot * stage + kKeys, keys + (n & 1) * 3 * kKeys, wk + buf * kC, warp - 16, c.valid);
-            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-            __syncwarp();
-            if (lane == 0) {
-                bar_arrive(kready + 8 * (n & 1));
-                bar_arrive(kempty + 8 * slot);
-            }
             if (++slot == S) {
                 slot = 0;
                 ph ^= 1;
@@ -1001,7 +1001,7 @@ __global__ void __launch_bounds__(kOutThreads, 1) linear_outputs_kernel(const __
                 spoilt(n - 1);
             }
             // O1 of the chunk before has read Sb
-            if (n > 0 && !phase(o1done, n - 1, &stop)) break;
+            if (n > 0 && !phase(o1done + 8 * ((n - 1) & 1), (n - 1) >> 1, &stop)) break;
             tc_fence_after();
             const unsigned long long e = pack_f32x2(all_e[buf], all_e[buf]);
             const bool poisoned = __any_sync(0xffffffffu, poison != 0.0f);
@@ -1065,19 +1065,20 @@ __global__ void __launch_bounds__(kOutThreads, 1) linear_outputs_kernel(const __
             const int last0 = i0 < c.valid ? i0 : -1, last1 = i0 + 8 < c.valid ? i0 + 8 : -1;
             uint8_t *row = ps + i0 * 128;  // (O2 of the chunk before was issued before A)
 #pragma unroll 1
-            for (int t = 0; t < 4; ++t) {
-                uint32_t r[8];
-                tmem_ld_a(tmem + quarter + kA + 16 * t, r);
+            for (int t = 0; t < 2; ++t) {
+                uint32_t r[16];
+                tmem_ld_s(tmem + quarter + kA + 32 * t, r);
+                asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 #pragma unroll
-                for (int m = 0; m < 2; ++m) {
-                    const int j = 16 * t + 8 * m + j0;
+                for (int m = 0; m < 4; ++m) {
+                    const int j = 32 * t + 8 * m + j0;
                     const float2 g = *reinterpret_cast<const float2 *>(&gj[j]);
                     // (later tokens' exponents may overflow: they are not used)
                     const float a = j <= last0 ? ex2(g0 - g.x) * __uint_as_float(r[4 * m]) : 0.0f;
                     const float b = j + 1 <= last0 ? ex2(g0 - g.y) * __uint_as_float(r[4 * m + 1]) : 0.0f;
                     const float e = j <= last1 ? ex2(g1 - g.x) * __uint_as_float(r[4 * m + 2]) : 0.0f;
                     const float f = j + 1 <= last1 ? ex2(g1 - g.y) * __uint_as_float(r[4 * m + 3]) : 0.0f;
-                    const int to = (((2 * t + m) ^ (lane >> 2)) << 4) + 2 * j0;  // i0 % 8 = lane / 4
+                    const int to = (((4 * t + m) ^ (lane >> 2)) << 4) + 2 * j0;  // i0 % 8 = lane / 4
                     *reinterpret_cast<uint32_t *>(row + to) = bf16x2(a, b);
                     *reinterpret_cast<uint32_t *>(row + 8 * 128 + to) = bf16x2(e, f);
                 }
@@ -1100,7 +1101,7 @@ __global__ void __launch_bounds__(kOutThreads, 1) linear_outputs_kernel(const __
         int n = 0;
         for (; n < total; ++n) {
             // the four warps go on together, or none (they meet at barriers); what was staged is stored
-            if (!all_of(phase(odone + 8 * (n & 1), n >> 1, &stop))) break;
+            if (!all_of(phase(odone + 8 * (n & 1), n >> 1, &stop) && phase(o1done + 8 * (n & 1), n >> 1, &stop))) break;
             tc_fence_after();
             hear(n);
             const float *e = eg + (n & (kSums - 1)) * kC;
@@ -1138,7 +1139,7 @@ __global__ void __launch_bounds__(kOutThreads, 1) linear_outputs_kernel(const __
                 }
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) bar_arrive(ofree);
+            if (lane == 0) bar_arrive(ofree + 8 * (n & 1));
             asm volatile("bar.sync 1, 128;" ::: "memory");
             const int shift = p.Dv == 128 ? 4 : 3, end = c.valid << shift;
 #pragma unroll 1
