@@ -233,10 +233,11 @@ __device__ __forceinline__ bool all_of(bool v) {
     return r != 0;
 }
 
-// Scratch: the sum of g of each share's cut piece, then its state (what the next share begins
-// with, after the joining), then what a cut sequence begins with.
+// Scratch: exp of the sum of g of each share's cut piece; what the joining is to do from each share on;
+// the pieces' states (what the next share begins with, after the joining); what cut sequences begin with.
+__device__ __forceinline__ int4 *joins_of(const LinearParams &p) { return reinterpret_cast<int4 *>(p.ws + (p.groups + 3) / 4 * 4); }
 __device__ __forceinline__ float *state_of(const LinearParams &p, int g) {
-    return p.ws + (p.groups + 3) / 4 * 4 + static_cast<long long>(g) * p.Dk * p.Dv;
+    return p.ws + (p.groups + 3) / 4 * 4 + 4 * p.groups + static_cast<long long>(g) * p.Dk * p.Dv;
 }
 __device__ __forceinline__ float *begin_state(const LinearParams &p, int g) { return state_of(p, p.groups + g); }
 
@@ -463,10 +464,23 @@ __global__ void __launch_bounds__(kStateThreads, 1) linear_states_kernel(const _
     pdl_launch_dependents();  // the next kernels are this call's
     pdl_wait();
     const Share sh = share_of(p, g, false);
-    if (sh.u1 <= sh.u0) return;
-    const Place last = place_of(p, sh.u1 - 1);
-    if (last.k + 1 >= last.s.chunks) return;  // no cut sequence at this share's end
-    const int chunks = min(last.k + 1, sh.u1 - sh.u0);  // all of them whole: the sequence goes on behind
+    Place last;
+    last.k = 0;
+    last.s.chunks = 0;
+    if (sh.u1 > sh.u0) last = place_of(p, sh.u1 - 1);
+    const bool cut = last.k + 1 < last.s.chunks;  // a sequence goes on behind this share
+    if (threadIdx.x == 0) {
+        // Where it begins here: the shares behind which it goes on (up to, not with, the one that has its
+        // last chunk), its sequence and head.
+        int4 join = make_int4(0, 0, 0, 0);
+        if (cut && last.k < sh.u1 - sh.u0) {
+            const long long u = sh.u1 - 1LL + (last.s.chunks - last.k - 1);  // its last chunk
+            join = make_int4(g, static_cast<int>(((u + 1) * sh.groups - 1) / sh.units), last.b, last.h);
+        }
+        joins_of(p)[g] = join;
+    }
+    if (!cut) return;
+    const int chunks = min(last.k + 1, sh.u1 - sh.u0);  // all of them whole
     if (warp == 1) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(saddr(tmem_slot)), "r"(512)
                      : "memory");
@@ -618,45 +632,57 @@ __global__ void __launch_bounds__(kStateThreads, 1) linear_states_kernel(const _
 }
 
 // ------------------------------------------------------------------------------------ 2. joining
-// Along a cut sequence, from the share it begins in: S' = exp(G) S + U, in place of U, four elements
-// a thread; and a copy of what it begins with, for the third kernel, whose other CTAs may have
-// written its last state by the time it is read.
-constexpr int kJoinThreads = 256, kJoinBatch = 8;
+// Along a cut sequence, from the share it begins in: S' = exp(G) S + U, in place of U; and a copy of what it
+// begins with, for the third kernel, whose other CTAs may have written its last state by the time it is
+// read.  A thread has kJoinEach groups of four elements.
+constexpr int kJoinThreads = 256, kJoinEach = 4, kJoinBatch = 2;
 __global__ void __launch_bounds__(kJoinThreads) linear_join_kernel(const __grid_constant__ LinearParams p) {
     pdl_launch_dependents();
     pdl_wait();
-    const int g = static_cast<int>(blockIdx.x);
-    const Share sh = share_of(p, g, false);
-    if (sh.u1 <= sh.u0) return;
-    const Place last = place_of(p, sh.u1 - 1);
-    if (last.k + 1 >= last.s.chunks || last.k >= sh.u1 - sh.u0) return;  // not cut, or begun in an earlier share
-    const long long at = 4LL * (blockIdx.y * kJoinThreads + threadIdx.x);
-    if (at >= static_cast<long long>(p.Dk) * p.Dv) return;
-    float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    if (last.s.slot >= 0 && !(p.fresh && p.fresh[last.b]))
-        s = *reinterpret_cast<const float4 *>(p.state + last.s.slot * p.s_slot + last.h * p.s_head + at);
-    *reinterpret_cast<float4 *>(begin_state(p, g) + at) = s;
-    // the shares whose end the sequence goes on behind
-    const int rest = last.s.chunks - last.k - 1;  // chunks behind this share
-    int end = g + 1;                              // one past the last such share
-    while (end < sh.groups && begin_of(sh.units, end + 1, sh.groups) - sh.u1 < rest) ++end;
-    for (int i = g; i < end; i += kJoinBatch) {
-        float4 u[kJoinBatch];
-        float e[kJoinBatch];
+    const int4 join = joins_of(p)[blockIdx.x];
+    if (join.x >= join.y) return;
+    const int all = p.Dk * p.Dv / 4, step = static_cast<int>(gridDim.y) * kJoinThreads;
+    const int at = static_cast<int>(blockIdx.y) * kJoinThreads + static_cast<int>(threadIdx.x);
+    const long long slot = p.slots[join.z];
+    const float4 *from = nullptr;
+    if (slot >= 0 && slot < p.pool && !(p.fresh && p.fresh[join.z]))
+        from = reinterpret_cast<const float4 *>(p.state + slot * p.s_slot + join.w * p.s_head);
+    float4 s[kJoinEach];
+    float4 *begin = reinterpret_cast<float4 *>(begin_state(p, join.x));
 #pragma unroll
-        for (int j = 0; j < kJoinBatch; ++j)
-            if (i + j < end) {
-                u[j] = *reinterpret_cast<const float4 *>(state_of(p, i + j) + at);
-                e[j] = p.ws[i + j];
+    for (int j = 0; j < kJoinEach; ++j) {
+        const int e = at + j * step;
+        s[j] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        if (from && e < all) s[j] = from[e];
+    }
+#pragma unroll
+    for (int j = 0; j < kJoinEach; ++j)
+        if (at + j * step < all) begin[at + j * step] = s[j];
+    for (int i = join.x; i < join.y; i += kJoinBatch) {
+        float4 u[kJoinBatch][kJoinEach];
+        float f[kJoinBatch];
+#pragma unroll
+        for (int m = 0; m < kJoinBatch; ++m)
+            if (i + m < join.y) {
+                f[m] = p.ws[i + m];
+                const float4 *w = reinterpret_cast<const float4 *>(state_of(p, i + m));
+#pragma unroll
+                for (int j = 0; j < kJoinEach; ++j)
+                    if (at + j * step < all) u[m][j] = w[at + j * step];
             }
 #pragma unroll
-        for (int j = 0; j < kJoinBatch; ++j)
-            if (i + j < end) {
-                s.x = fmaf(e[j], s.x, u[j].x);
-                s.y = fmaf(e[j], s.y, u[j].y);
-                s.z = fmaf(e[j], s.z, u[j].z);
-                s.w = fmaf(e[j], s.w, u[j].w);
-                *reinterpret_cast<float4 *>(state_of(p, i + j) + at) = s;
+        for (int m = 0; m < kJoinBatch; ++m)
+            if (i + m < join.y) {
+                float4 *w = reinterpret_cast<float4 *>(state_of(p, i + m));
+#pragma unroll
+                for (int j = 0; j < kJoinEach; ++j)
+                    if (at + j * step < all) {
+                        s[j].x = fmaf(f[m], s[j].x, u[m][j].x);
+                        s[j].y = fmaf(f[m], s[j].y, u[m][j].y);
+                        s[j].z = fmaf(f[m], s[j].z, u[m][j].z);
+                        s[j].w = fmaf(f[m], s[j].w, u[m][j].w);
+                        w[at + j * step] = s[j];
+                    }
             }
     }
 }
@@ -1201,7 +1227,7 @@ sgemm_status_t check_sizes(const sgemm_linear_attention_t &a) {
 }
 
 long long scratch(const sgemm_linear_attention_t &a, int groups) {
-    return groups > 1 ? (groups + 3) / 4 * 16 + 2LL * groups * a.Dk * a.Dv * 4 : 0;
+    return groups > 1 ? (groups + 3) / 4 * 16 + 16LL * groups + 2LL * groups * a.Dk * a.Dv * 4 : 0;
 }
 
 bool allow(const void *fn, std::atomic<unsigned long long> &done) {
@@ -1311,7 +1337,7 @@ extern "C" sgemm_status_t sgemm_bf16_linear_attention(const sgemm_linear_attenti
         p.stages = stages_of(a->Dk, a->Dv, false);
         const size_t smem = 1024 + static_cast<size_t>(p.stages) * chunk_bytes(a->Dk, a->Dv, false) + kStateFixed;
         if (launch(fn, dim3(static_cast<unsigned>(p.groups)), dim3(kStateThreads), smem, cs, &p) != cudaSuccess) return SGEMM_ERR_CUDA;
-        const unsigned slices = static_cast<unsigned>((a->Dk * a->Dv / 4 + kJoinThreads - 1) / kJoinThreads);
+        const unsigned slices = static_cast<unsigned>(a->Dk * a->Dv / 4 / kJoinThreads / kJoinEach);  // 1 .. 4
         if (launch(reinterpret_cast<const void *>(&linear_join_kernel), dim3(static_cast<unsigned>(p.groups), slices), dim3(kJoinThreads),
                    0, cs, &p) != cudaSuccess)
             return SGEMM_ERR_CUDA;
