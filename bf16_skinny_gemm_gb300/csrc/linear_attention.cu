@@ -118,20 +118,28 @@ __device__ __forceinline__ int begin_of(int units, int g, int groups) {
     return static_cast<int>(static_cast<long long>(units) * g / groups);
 }
 
+// Chunks on the line of the kEachLane sequences from b on: a lane's (their loads are in flight together: batches of
+// many short sequences spend their time here).
+constexpr int kEachLane = 8;
+__device__ __forceinline__ int units_of(const LinearParams &p, int b, bool report) {
+    int n = 0;
+#pragma unroll
+    for (int i = 0; i < kEachLane; ++i)
+        if (b + i < p.B) {
+            const Seq q = seq_of(p, b + i);
+            n += q.chunks * p.Hv;
+            if (q.bad && report) atomicOr(p.err, kErrBadIndex);
+        }
+    return n;
+}
+
 // The line's length and share g of it (by a whole warp).
 __device__ __forceinline__ Share share_of(const LinearParams &p, int g, bool report) {
     const int lane = threadIdx.x & 31;
     Share s;
     s.units = 0;
-    for (int c = 0; c < p.B; c += 32) {
-        int mine = 0;
-        if (c + lane < p.B) {
-            const Seq q = seq_of(p, c + lane);
-            mine = q.chunks * p.Hv;
-            if (q.bad && report) atomicOr(p.err, kErrBadIndex);
-        }
-        s.units += static_cast<int>(__reduce_add_sync(0xffffffffu, static_cast<unsigned>(mine)));
-    }
+    for (int c = 0; c < p.B; c += 32 * kEachLane)
+        s.units += static_cast<int>(__reduce_add_sync(0xffffffffu, static_cast<unsigned>(units_of(p, c + kEachLane * lane, report))));
     s.groups = max(1, min(p.groups, (s.units + kFew - 1) / kFew));
     s.u0 = s.u1 = 0;
     if (g < s.groups) {
@@ -147,12 +155,12 @@ struct Place {
     Seq s;
 };
 
+// Where unit u is (there is such a unit).
 __device__ __forceinline__ Place place_of(const LinearParams &p, int u) {
     const int lane = threadIdx.x & 31;
     Place o;
-    for (int c = 0, at = 0;; c += 32) {
-        int mine = 0;
-        if (c + lane < p.B) mine = seq_of(p, c + lane).chunks * p.Hv;
+    for (int c = 0, at = 0;; c += 32 * kEachLane) {
+        const int mine = units_of(p, c + kEachLane * lane, false);
         int x = mine;
 #pragma unroll
         for (int off = 1; off < 32; off <<= 1) {
@@ -160,11 +168,15 @@ __device__ __forceinline__ Place place_of(const LinearParams &p, int u) {
             if (lane >= off) x += y;
         }
         const unsigned past = __ballot_sync(0xffffffffu, u < at + x);
-        if (past || c + 32 >= p.B) {
+        if (past || c + 32 * kEachLane >= p.B) {
             const int w = past ? __ffs(past) - 1 : 0;
-            o.b = c + w;
-            const int left = u - at - __shfl_sync(0xffffffffu, x - mine, w);
+            int left = u - at - __shfl_sync(0xffffffffu, x - mine, w);
+            o.b = c + kEachLane * w;
             o.s = seq_of(p, o.b);
+            while (left >= o.s.chunks * p.Hv && o.b + 1 < p.B) {
+                left -= o.s.chunks * p.Hv;
+                o.s = seq_of(p, ++o.b);
+            }
             o.h = left / max(1, o.s.chunks);
             o.k = left - o.h * o.s.chunks;
             return o;
@@ -1267,7 +1279,7 @@ extern "C" sgemm_status_t sgemm_bf16_linear_attention(const sgemm_linear_attenti
     if (!std::isfinite(a->scale)) return SGEMM_ERR_INVALID_ARG;
     if (a->B == 0) return SGEMM_OK;
     if (!a->slots || !a->cu || (a->pool > 0 && !a->state) || (a->N > 0 && (!a->q || !a->k || !a->v || !a->g || !a->out)) || a->pool < 0 ||
-        a->pool >= (1LL << 40) || a->workspace_bytes < 0)
+        a->pool >= (1LL << 31) || a->workspace_bytes < 0)
         return SGEMM_ERR_INVALID_ARG;
     const LinearView io{a->q, a->k, a->v, a->g, a->state, a->out, a->q_token, a->q_head, a->k_token, a->k_head, a->v_token,
                         a->v_head, a->g_token, a->g_head, a->s_slot, a->s_head, a->o_token, a->o_head, a->N, a->pool, a->Hk,

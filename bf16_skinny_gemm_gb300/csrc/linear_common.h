@@ -39,7 +39,7 @@ inline bool linear_touches(const LinearView &a, const void *b, long long bytes) 
 
 // Strides, alignment and overlap (the sizes are checked before).
 inline sgemm_status_t check_linear(const LinearView &a) {
-    const long long far = 1LL << 32;  // strides: their products with rows stay in 64 bits
+    const long long far = 1LL << 29;  // strides: their products with 2^31 rows, in bytes, stay in 64 bits
     const long long strides[] = {a.q_token, a.q_head, a.k_token, a.k_head, a.v_token, a.v_head, a.g_token, a.g_head,
                                  a.s_slot, a.s_head, a.o_token, a.o_head};
     for (long long s : strides)

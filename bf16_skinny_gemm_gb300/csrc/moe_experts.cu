@@ -490,7 +490,8 @@ extern "C" sgemm_status_t sgemm_bf16_moe_experts(const sgemm_moe_experts_t *a, s
     if (!a->x || !a->w_gate_up || !a->w_down || !a->ids || !a->weights || !a->y || a->workspace_bytes < 0) return SGEMM_ERR_INVALID_ARG;
     const long long far = kMapStride;
     if (a->ldx < a->D || a->gu_row < a->D || a->dn_row < a->F || a->ldi < a->k || a->ldwt < a->k || a->ldy < a->D ||
-        a->gu_expert < (2LL * a->F - 1) * a->gu_row + a->D || a->dn_expert < (a->D - 1LL) * a->dn_row + a->F)
+        (a->E > 1 && (a->gu_expert < (2LL * a->F - 1) * a->gu_row + a->D || a->dn_expert < (a->D - 1LL) * a->dn_row + a->F)) ||
+        a->gu_expert < 0 || a->dn_expert < 0)
         return SGEMM_ERR_INVALID_ARG;
     if (a->ldx >= far || a->gu_row >= far || a->dn_row >= far || a->ldi >= far || a->ldwt >= far || a->ldy >= far ||
         a->gu_expert >= far || a->dn_expert >= far)

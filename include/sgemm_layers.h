@@ -139,7 +139,8 @@ sgemm_status_t sgemm_latent_tree_attention_workspace(const sgemm_latent_attentio
  * - Two sequences of one call must not name the same slot.
  * - g is a logarithm: 0 keeps the state, -inf drops it (its finite part; an infinity
  *   or a NaN in a dropped state gives NaN).
- * - Dk and Dv: 64 or 128; Hv a multiple of Hk, Hv <= 1024; B < 2^31 / Hv.
+ * - Dk and Dv: 64 or 128; Hv a multiple of Hk, Hv <= 1024; B < 2^28 / Hv; less than 2^31
+ *   slots; strides below 2^29.
  * - q, k, v are 16-byte aligned with strides that are multiples of 8; out is 4-byte
  *   aligned with even strides; state is 16-byte aligned with strides that are
  *   multiples of 4 (each head's Dk x Dv is dense).  g's strides may be 0. */
@@ -181,7 +182,9 @@ sgemm_status_t sgemm_bf16_linear_step(const sgemm_linear_step_t *args, sgemm_str
  *   overflows; g = -inf drops what came before.  An infinity or a NaN in q reaches its
  *   token only, in k or g its sequence and head from its token on, in v the same for its
  *   element (as an infinity or NaN).
- * - Sizes, alignments and strides as for sgemm_bf16_linear_step; N < 2^31 / Hv.
+ * - Sizes, alignments and strides as for sgemm_bf16_linear_step; N < 2^31 / Hv; strides
+ *   of q, k and v along dimensions of more than one element are at least 8.
+ * - SGEMM_FLAG_TEST_STALL is accepted.
  * - workspace: device scratch of at least sgemm_linear_attention_workspace bytes
  *   (16-byte aligned; may be NULL where that is 0), as for the other operators.
  * - Waits inside the kernels are bounded, as in sgemm_bf16_moe_experts. */

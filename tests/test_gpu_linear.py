@@ -390,3 +390,10 @@ def test_rows_of_out_that_start_on_four_bytes():
     out, _ = prompt(*p, [n], out=wide[:, :, 2:130])
     dense, _ = prompt(*p, [n])
     assert torch.equal(out, dense) and torch.all(wide[:, :, :2] == 9) and torch.all(wide[:, :, 130:] == 9)
+
+
+@pytest.mark.parametrize("B", [255, 256, 257, 600])
+def test_batches_that_take_several_passes_over_their_offsets(B):
+    lens = [(b * b * 7) % 5 if b % 3 else 0 for b in range(B)]
+    lens[B - 1] = 130
+    compare(lens, 1, 1, 64, 64, seed=B, fresh=[b % 2 for b in range(B)])
