@@ -140,7 +140,8 @@ __device__ __forceinline__ Share share_of(const LinearParams &p, int g, bool rep
     s.units = 0;
     for (int c = 0; c < p.B; c += 32 * kEachLane)
         s.units += static_cast<int>(__reduce_add_sync(0xffffffffu, static_cast<unsigned>(units_of(p, c + kEachLane * lane, report))));
-    s.groups = max(1, min(p.groups, (s.units + kFew - 1) / kFew));
+    // as many as there are SMs, of kFew chunks at least; shorter ones where that makes one for each sequence and head
+    s.groups = max(1, min(p.groups, max((s.units + kFew - 1) / kFew, min(s.units, p.B * p.Hv))));
     s.u0 = s.u1 = 0;
     if (g < s.groups) {
         s.u0 = begin_of(s.units, g, s.groups);
@@ -1227,7 +1228,7 @@ int stages_of(int dk, int dv, bool with_q) {
 // Shares of a line, at most: one an SM, each of kFew chunks or more.
 int groups_of(const sgemm_linear_attention_t &a, int sms) {
     const long long units = (a.N / kC + 2 * a.B) * a.Hv;
-    return static_cast<int>(std::max(1LL, std::min<long long>(sms, (units + kFew - 1) / kFew)));
+    return static_cast<int>(std::max(1LL, std::min<long long>(sms, std::max((units + kFew - 1) / kFew, std::min(units, a.B * a.Hv)))));
 }
 
 sgemm_status_t check_sizes(const sgemm_linear_attention_t &a) {
