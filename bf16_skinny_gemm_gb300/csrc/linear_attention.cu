@@ -62,13 +62,13 @@ constexpr int kStages = 6;             // of chunks in a ring, at most
 constexpr int kFew = 8;                // chunks a share has at least
 constexpr int kOutThreads = 24 * 32;   // copies, products, sums, products, state, decays, outputs (4 each), values and keys (8)
 constexpr int kSums = 8;               // chunks whose sums of g are kept
-constexpr int kStateThreads = 12 * 32;  // copies, products, keys (8), sums, (none)
+constexpr int kStateThreads = 12 * 32;  // copies, products, keys (8), sums (2)
 // A decay's exponent (base 2) is cut here: 2^-200 is 0.  The sum of a chunk's is then 12800 at most, one
 // FP32 number of it off by 2^-11, and a factor exp2 of a difference by 2^-10.5: below BF16's rounding.
 constexpr float kLeast = -200.0f;
 
 struct LinearParams {
-    CUtensorMap tq, tk, tv;  // {D, N, heads}, boxes of 64 tokens x 64 elements
+    CUtensorMap tq, tk, tv;  // {64, N, D / 64, heads}, boxes of 64 tokens: a chunk's operand is one copy
     const float *g;
     float *state;
     const long long *slots;
@@ -436,7 +436,8 @@ __host__ __device__ constexpr int chunk_bytes(int dk, int dv, bool with_q) { ret
 constexpr int kMiscOut = 1024 + 3 * kSums * kC * 4 + 4 * 128 * 4;
 constexpr int kOutStage = kC * 256;  // a chunk's outputs on their way
 __host__ __device__ constexpr int out_fixed(int dk) { return 2 * 3 * dk / 64 * kPart + kPart + kOutStage + kMiscOut; }
-constexpr int kStateFixed = 512 + 4 * kC * 4;
+constexpr int kAhead = 8;  // chunks whose g the state kernel has on their way
+constexpr int kStateFixed = 512 + 4 * kC * 4 + kAhead * kC * 4 + 64;
 // Columns of tensor memory: the state kernel's (U, two buffers of keys in three numbers), the output kernel's
 // (two buffers of O1 and of values: O1 is what the next state waits for, not the outputs' warps).
 constexpr int kU = 0, kKeyT = 128;
@@ -453,8 +454,10 @@ __global__ void __launch_bounds__(kStateThreads, 1) linear_states_kernel(const _
     uint64_t *bars = reinterpret_cast<uint64_t *>(misc);
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(misc + 256);
     int &stop = *reinterpret_cast<int *>(misc + 260);
-    float *wk = reinterpret_cast<float *>(misc + 512);  // [4][64] the factors of a chunk's keys
-    const uint32_t full = saddr(bars), empty = full + 8 * kStages, kready = empty + 8 * kStages, kfree = kready + 16, fin = kfree + 16,
+    float *wk = reinterpret_cast<float *>(misc + 512);  // [4][64] exp of the sum of g behind a key in its chunk
+    float *gs = wk + 4 * kC;                            // [kAhead][64] g
+    float2 *sums = reinterpret_cast<float2 *>(gs + kAhead * kC);  // [4] a chunk's sum of g
+    const uint32_t full = saddr(bars), empty = full + 8 * kStages, kready = empty + 8 * kStages, kfree = kready + 16, fin = kfree + 32,
                    gready = fin + 8;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = static_cast<int>(blockIdx.x);
     if (threadIdx.x == 0) {
@@ -465,12 +468,12 @@ __global__ void __launch_bounds__(kStateThreads, 1) linear_states_kernel(const _
             bar_init(full + 8 * i, 1);
             bar_init(empty + 8 * i, 1);
         }
-        for (int i = 0; i < 2; ++i) {
-            bar_init(kready + 8 * i, kWarps);
+        for (int i = 0; i < 2; ++i) bar_init(kready + 8 * i, kWarps);
+        for (int i = 0; i < 4; ++i) {
             bar_init(kfree + 8 * i, 1);
+            bar_init(gready + 8 * i, 1);
         }
         bar_init(fin, 1);
-        for (int i = 0; i < 4; ++i) bar_init(gready + 8 * i, 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     }
@@ -506,6 +509,7 @@ __global__ void __launch_bounds__(kStateThreads, 1) linear_states_kernel(const _
     const bool stall = (p.flags & kFlagTestStall) != 0;
     int issued = 0;
     if (warp == 0) {
+        const uint64_t policy = policy_of(false);
         int slot = 0;
         unsigned ph = 1;
         for (int n = 0; n < chunks; ++n) {
@@ -516,8 +520,8 @@ __global__ void __launch_bounds__(kStateThreads, 1) linear_states_kernel(const _
                 bar_expect_tx(bar, static_cast<unsigned>(stage));
                 if (!stall) {
                     const int t = last.s.t0 + (last.k - n) * kC;
-                    for (int c = 0; c < kKParts; ++c) tma_3d(dst + c * kPart, &p.tk, 64 * c, t, last.h / p.share, bar);
-                    for (int c = 0; c < vparts; ++c) tma_3d(dst + kKeys + c * kPart, &p.tv, 64 * c, t, last.h, bar);
+                    tma_4d(dst, &p.tk, 0, t, 0, last.h / p.share, bar, policy);
+                    tma_4d(dst + kKeys, &p.tv, 0, t, 0, last.h, bar, policy);
                 }
             }
             __syncwarp();
@@ -542,7 +546,7 @@ __global__ void __launch_bounds__(kStateThreads, 1) linear_states_kernel(const _
                     for (int kk = 0; kk < kC / 16; ++kk)
                         mma_ts(d + kU, a + 32 * part + 8 * kk, b + kk * (2048 >> 4), idesc, n != 0 || part != 0 || kk != 0);
                 mma_commit(empty + 8 * slot);
-                mma_commit(kfree + 8 * (n & 1));
+                mma_commit(kfree + 8 * (n & 3));
             }
             __syncwarp();
             if (++slot == S) {
@@ -551,43 +555,54 @@ __global__ void __launch_bounds__(kStateThreads, 1) linear_states_kernel(const _
             }
         }
         finish(fin, &stop);
-    } else if (warp == 10) {
-        // the keys' factors: exp of the sum of g behind them, to the piece's end
-        Pair after{0.0f, 0.0f};
-        Chunk c;
-        c.h = last.h;
-        c.valid = kC;
-        c.t0 = last.s.t0 + last.k * kC;
-        Decays next = load_g(p, c);
-        bool ok = true;
-        for (int n = 0; n < chunks; ++n) {
-            const Decays now = next;
-            c.t0 -= kC;
-            if (n + 1 < chunks) next = load_g(p, c);
+    } else if (warp >= 10) {
+        // The sums of g, every other chunk a warp (its scan takes 1300 cycles, with one warp what a chunk
+        // took), up to four chunks ahead of the keys; the copies of g are further ahead.
+        auto fetch = [&](int n) {
+            if (n < chunks) {
+                const float *from = p.g + (last.s.t0 + static_cast<long long>(last.k - n) * kC + 2 * lane) * p.g_token + last.h * p.g_head;
+                const uint32_t to = saddr(gs + (n & (kAhead - 1)) * kC + 2 * lane);
+                copy4(to, from);
+                copy4(to + 4, from + p.g_token);
+            }
+            asm volatile("cp.async.commit_group;" ::: "memory");
+        };
+        for (int n = warp - 10; n < kAhead - 2; n += 2) fetch(n);
+        for (int n = warp - 10; n < chunks; n += 2) {
+            fetch(n + kAhead - 2);
+            asm volatile("cp.async.wait_group %0;" ::"n"(kAhead / 2 - 1) : "memory");  // (a lane reads what it copied)
+            const float2 v = *reinterpret_cast<const float2 *>(gs + (n & (kAhead - 1)) * kC + 2 * lane);
             Pair a, b, all;
-            sums_of(now, a, b, all);
-            after = add(all, after);
-            if (!(ok = n < 2 || phase(kfree + 8 * (n & 1), (n >> 1) - 1, &stop))) break;
-            *reinterpret_cast<float2 *>(&wk[(n & 3) * kC + 2 * lane]) = make_float2(exp2f(less(after, a)), exp2f(less(after, b)));
+            sums_of(Decays{v.x, v.y}, a, b, all);
+            if (n >= 4 && !phase(kfree + 8 * (n & 3), (n >> 2) - 1, &stop)) break;
+            *reinterpret_cast<float2 *>(&wk[(n & 3) * kC + 2 * lane]) = make_float2(exp2f(less(all, a)), exp2f(less(all, b)));
+            if (lane == 0) sums[n & 3] = make_float2(all.hi, all.lo);
             __syncwarp();
             if (lane == 0) bar_arrive(gready + 8 * (n & 3));
         }
-        if (lane == 0) p.ws[g] = ok ? exp2f(after.hi + after.lo) : __int_as_float(0x7fc00000);
-    } else if (warp < 10) {
+        asm volatile("cp.async.wait_all;" ::: "memory");
+    } else {
         // keys: a warp's 32 elements (a quarter of the lanes), half of the tokens
         const int q = warp & 3, half = (warp - 2) >> 2, d0 = 32 * q;
         const uint32_t quarter = static_cast<uint32_t>(32 * q) << 16;
         bool ok = true;
         int slot = 0;
         unsigned ph = 0;
+        Pair after{0.0f, 0.0f};  // the sum of g behind the chunk, to the piece's end
         for (int n = 0; n < chunks; ++n) {
-            // (the factors come after the product that read this buffer)
-            ok = phase(gready + 8 * (n & 3), n >> 2, &stop) && phase(full + 8 * slot, ph, &stop);
+            ok = phase(gready + 8 * (n & 3), n >> 2, &stop) && phase(full + 8 * slot, ph, &stop) &&
+                 (n < 2 || phase(kfree + 8 * ((n - 2) & 3), (n - 2) >> 2, &stop));
             if (!ok) break;
             tc_fence_after();
+            const float behind = exp2f(after.hi + after.lo);
+            const float2 sum = sums[n & 3];
+            after = add(Pair{sum.x, sum.y}, after);
             if (d0 < DK) {
                 // the factors of tokens 32 half + 8 i + 2 (lane % 4) and the next
-                const unsigned long long *w = reinterpret_cast<const unsigned long long *>(wk + (n & 3) * kC) + 16 * half + (lane & 3);
+                unsigned long long w[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    w[i] = mul2(reinterpret_cast<const unsigned long long *>(wk + (n & 3) * kC)[16 * half + 4 * i + (lane & 3)], pack_f32x2(behind, behind));
 #pragma unroll 1
                 for (int h = 0; h < 2; ++h) {  // 16 elements
                     uint32_t r[8], o[3][8];
@@ -596,7 +611,7 @@ __global__ void __launch_bounds__(kStateThreads, 1) linear_states_kernel(const _
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
                         uint32_t s[3];
-                        split(r[i], w[4 * (i >> 1)], s);
+                        split(r[i], w[i >> 1], s);
 #pragma unroll
                         for (int m = 0; m < 3; ++m) o[m][i] = s[m];
                     }
@@ -631,6 +646,7 @@ __global__ void __launch_bounds__(kStateThreads, 1) linear_states_kernel(const _
                                            : make_float4(nan, nan, nan, nan);
             }
         }
+        if (warp == 2 && lane == 0) p.ws[g] = ok ? exp2f(after.hi + after.lo) : nan;
     }
     __syncwarp();
     if (lane == 0 && *reinterpret_cast<volatile int *>(&stop) && warp == 0)
@@ -800,6 +816,7 @@ __global__ void __launch_bounds__(kOutThreads, 1) linear_outputs_kernel(const __
     // waits on it has seen it once.
     if (warp == 0) {
         // -------------------------------------------------------------------- the copies
+        const uint64_t policy = policy_of(false);
         int slot = 0;
         unsigned ph = 1;
         for (int n = 0; cursor.next(p, c); ++n) {
@@ -815,8 +832,7 @@ __global__ void __launch_bounds__(kOutThreads, 1) linear_outputs_kernel(const __
                         bar_expect_tx(bar, static_cast<unsigned>(parts * kPart));
                     else
                         bar_arrive(bar);
-                    if (!stall && any)
-                        for (int i = 0; i < parts; ++i) tma_3d(dst + i * kPart, &map, 64 * i, c.t0, head, bar);
+                    if (!stall && any) tma_4d(dst, &map, 0, c.t0, 0, head, bar, policy);
                 }
                 __syncwarp();
                 return true;
@@ -1314,9 +1330,9 @@ extern "C" sgemm_status_t sgemm_bf16_linear_attention(const sgemm_linear_attenti
     const long long rows = std::max(1LL, a->N);
     const void *none = reinterpret_cast<const void *>(4096);
     const CUtensorMapL2promotion promote = CU_TENSOR_MAP_L2_PROMOTION_L2_256B;
-    if (!map_3d(&p.tq, a->N ? a->q : none, a->Dk, rows, a->Hk, a->q_token, a->q_head, kC, promote) ||
-        !map_3d(&p.tk, a->N ? a->k : none, a->Dk, rows, a->Hk, a->k_token, a->k_head, kC, promote) ||
-        !map_3d(&p.tv, a->N ? a->v : none, a->Dv, rows, a->Hv, a->v_token, a->v_head, kC, promote))
+    if (!map_4d(&p.tq, a->N ? a->q : none, a->Dk, rows, a->Hk, a->q_token, a->q_head, kC, a->Dk / 64, true, promote) ||
+        !map_4d(&p.tk, a->N ? a->k : none, a->Dk, rows, a->Hk, a->k_token, a->k_head, kC, a->Dk / 64, true, promote) ||
+        !map_4d(&p.tv, a->N ? a->v : none, a->Dv, rows, a->Hv, a->v_token, a->v_head, kC, a->Dv / 64, true, promote))
         return SGEMM_ERR_CUDA;
     p.g = a->g;
     p.state = a->state;
