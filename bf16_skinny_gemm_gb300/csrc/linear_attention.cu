@@ -62,7 +62,7 @@ constexpr int kStages = 6;             // of chunks in a ring, at most
 constexpr int kFew = 8;                // chunks a share has at least
 constexpr int kOutThreads = 24 * 32;   // copies, products, sums, products, state, decays, outputs (4 each), values and keys (8)
 constexpr int kSums = 8;               // chunks whose sums of g are kept
-constexpr int kStateThreads = 12 * 32;  // copies, products, keys (8), sums (2)
+constexpr int kStateThreads = 12 * 32;  // copies, products, keys (4 + 4), sums (2)
 // A decay's exponent (base 2) is cut here: 2^-200 is 0.  The sum of a chunk's is then 12800 at most, one
 // FP32 number of it off by 2^-11, and a factor exp2 of a difference by 2^-10.5: below BF16's rounding.
 constexpr float kLeast = -200.0f;
@@ -446,10 +446,10 @@ constexpr int kState = 0, kSb = 128, kA = 192, kO1 = 256, kO2 = 384, kValueT = 4
 // ------------------------------------------------------------------------ 1. states of cut pieces
 template <int DK>
 __global__ void __launch_bounds__(kStateThreads, 1) linear_states_kernel(const __grid_constant__ LinearParams p) {
-    constexpr int kKParts = DK / 64, kKeys = kKParts * kPart, kWarps = 8;
+    constexpr int kKParts = DK / 64, kKeys = kKParts * kPart, kWarps = 4;
     extern __shared__ uint8_t raw[];
     uint8_t *base = raw + ((1024u - (saddr(raw) & 1023u)) & 1023u);
-    const int vparts = p.Dv / 64, stage = chunk_bytes(DK, p.Dv, false), S = p.stages;
+    const int stage = chunk_bytes(DK, p.Dv, false), S = p.stages;
     uint8_t *misc = base + S * stage;
     uint64_t *bars = reinterpret_cast<uint64_t *>(misc);
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(misc + 256);
@@ -574,7 +574,7 @@ __global__ void __launch_bounds__(kStateThreads, 1) linear_states_kernel(const _
             const float2 v = *reinterpret_cast<const float2 *>(gs + (n & (kAhead - 1)) * kC + 2 * lane);
             Pair a, b, all;
             sums_of(Decays{v.x, v.y}, a, b, all);
-            if (n >= 4 && !phase(kfree + 8 * (n & 3), (n >> 2) - 1, &stop)) break;
+            if (n >= 3 && !phase(kfree + 8 * ((n - 3) & 3), (n - 3) >> 2, &stop)) break;  // (the factors of n - 4 are read)
             *reinterpret_cast<float2 *>(&wk[(n & 3) * kC + 2 * lane]) = make_float2(exp2f(less(all, a)), exp2f(less(all, b)));
             if (lane == 0) sums[n & 3] = make_float2(all.hi, all.lo);
             __syncwarp();
@@ -582,52 +582,66 @@ __global__ void __launch_bounds__(kStateThreads, 1) linear_states_kernel(const _
         }
         asm volatile("cp.async.wait_all;" ::: "memory");
     } else {
-        // keys: a warp's 32 elements (a quarter of the lanes), half of the tokens
+        // keys: a warp's 32 elements (a quarter of the lanes); four warps take every other chunk
         const int q = warp & 3, half = (warp - 2) >> 2, d0 = 32 * q;
         const uint32_t quarter = static_cast<uint32_t>(32 * q) << 16;
         bool ok = true;
-        int slot = 0;
-        unsigned ph = 0;
         Pair after{0.0f, 0.0f};  // the sum of g behind the chunk, to the piece's end
-        for (int n = 0; n < chunks; ++n) {
+        auto more = [&](int n) {  // chunk n's is known, and counts from here on
+            const float2 sum = sums[n & 3];
+            after = add(Pair{sum.x, sum.y}, after);
+        };
+        int slot = half % S;
+        unsigned ph = static_cast<unsigned>(half / S) & 1u;
+        for (int n = half; n < chunks; n += 2) {
+            if (n > 0) {
+                if (!(ok = phase(gready + 8 * ((n - 1) & 3), (n - 1) >> 2, &stop))) break;
+                more(n - 1);
+            }
             ok = phase(gready + 8 * (n & 3), n >> 2, &stop) && phase(full + 8 * slot, ph, &stop) &&
                  (n < 2 || phase(kfree + 8 * ((n - 2) & 3), (n - 2) >> 2, &stop));
             if (!ok) break;
             tc_fence_after();
-            const float behind = exp2f(after.hi + after.lo);
-            const float2 sum = sums[n & 3];
-            after = add(Pair{sum.x, sum.y}, after);
             if (d0 < DK) {
-                // the factors of tokens 32 half + 8 i + 2 (lane % 4) and the next
-                unsigned long long w[4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    w[i] = mul2(reinterpret_cast<const unsigned long long *>(wk + (n & 3) * kC)[16 * half + 4 * i + (lane & 3)], pack_f32x2(behind, behind));
+                const float behind = exp2f(after.hi + after.lo);
 #pragma unroll 1
-                for (int h = 0; h < 2; ++h) {  // 16 elements
+                for (int part = 0; part < 4; ++part) {  // 16 elements x 32 tokens
+                    const int h = part & 1, t0 = 32 * (part >> 1);
                     uint32_t r[8], o[3][8];
-                    load_turned(saddr(base) + slot * stage, 32 * half, d0 + 16 * h, r[0], r[1], r[2], r[3]);
-                    load_turned(saddr(base) + slot * stage, 32 * half + 16, d0 + 16 * h, r[4], r[5], r[6], r[7]);
+                    load_turned(saddr(base) + slot * stage, t0, d0 + 16 * h, r[0], r[1], r[2], r[3]);
+                    load_turned(saddr(base) + slot * stage, t0 + 16, d0 + 16 * h, r[4], r[5], r[6], r[7]);
+                    // the factors of tokens t0 + 8 i + 2 (lane % 4) and the next
+                    const unsigned long long *w = reinterpret_cast<const unsigned long long *>(wk + (n & 3) * kC + t0) + (lane & 3);
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        uint32_t s[3];
-                        split(r[i], w[i >> 1], s);
+                    for (int i = 0; i < 4; ++i) {
+                        const unsigned long long f = mul2(w[4 * i], pack_f32x2(behind, behind));
 #pragma unroll
-                        for (int m = 0; m < 3; ++m) o[m][i] = s[m];
+                        for (int j = 0; j < 2; ++j) {
+                            uint32_t s[3];
+                            split(r[2 * i + j], f, s);
+#pragma unroll
+                            for (int m = 0; m < 3; ++m) o[m][2 * i + j] = s[m];
+                        }
                     }
 #pragma unroll
                     for (int m = 0; m < 3; ++m)
-                        tmem_st_turned(tmem + quarter + (static_cast<uint32_t>(16 * h) << 16) + kKeyT + 96 * (n & 1) + 32 * m + 16 * half, o[m]);
+                        tmem_st_turned(tmem + quarter + (static_cast<uint32_t>(16 * h) << 16) + kKeyT + 96 * (n & 1) + 32 * m + t0 / 2, o[m]);
                 }
                 asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
             }
+            more(n);
             tc_fence_before();
             __syncwarp();
             if (lane == 0) bar_arrive(kready + 8 * (n & 1));
-            if (++slot == S) {
-                slot = 0;
+            slot += 2;
+            if (slot >= S) {
+                slot -= S;
                 ph ^= 1;
             }
+        }
+        if (ok && chunks > 0 && ((chunks - 1) & 1) != half) {
+            // the last chunk was the others'
+            if ((ok = phase(gready + 8 * ((chunks - 1) & 3), (chunks - 1) >> 2, &stop))) more(chunks - 1);
         }
         // the piece's state, [Dk][Dv]: a row a lane, half of the columns a warp
         ok = ok && phase(fin, 0, &stop) && *reinterpret_cast<volatile int *>(&stop) == 0;
