@@ -39,6 +39,16 @@
 // keep their digits.
 // The roles' loops are short on purpose: unrolled, their code did not fit the instruction cache, and a chunk
 // took 9600 cycles (4500 without any other change).
+//
+// Measured on one GB300, calls one after the other:
+//   16384 tokens, 32 heads, 128 x 128 (541 MB)                         170 us
+//     states 50 us (235 MB, 4.7 TB/s), joining 4, outputs 114 (529 MB, 4.6 TB/s; alone, from a cold cache)
+//   8 ragged prompts of up to 2049, 8 key and 32 value heads, 64 x 128  99 us
+//   one prompt of 500, 16 heads                                         25 us
+// What bounds the output kernel: a chunk's chain, 3400 cycles (keys 1500, state's product 1300, the pass over the
+// state 800 to 1000, two barriers of 200 to 300), issue slots taken to 57%, the tensor pipe to 34%.  The states'
+// kernel is bound by memory, 41 GB/s an SM while it runs.  Around them: 2.4 us until the first copies are
+// issued, 3 us for a state's first load, 3 for the last store.
 #include <cuda.h>
 #include <cuda_runtime.h>
 

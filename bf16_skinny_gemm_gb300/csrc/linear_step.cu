@@ -11,6 +11,9 @@
 // A CTA takes W columns of one head's state: all of them, or 32 where the heads of a call are too few to
 // fill the SMs.  A thread has four columns of every (256 * 4 / W)-th row; the sums over the rows are joined
 // by shuffles within a warp and in shared memory between warps, in a fixed order.
+//
+// Measured on one GB300, calls one after the other: 128 sequences, 32 heads of 128 x 128 (477 MB without what is
+// padded) 70.4 us, the rate of a copy; one sequence of 32 heads 2.8 us (in slices of 32 columns; whole heads 3.6).
 #include <cuda_runtime.h>
 
 #include <cmath>

