@@ -69,7 +69,8 @@ using namespace roles;
 constexpr int kC = 64;                 // tokens a chunk
 constexpr int kPart = kC * 128;        // 64 tokens x 64 elements, bytes
 constexpr int kStages = 6;             // of chunks in a ring, at most
-constexpr int kFew = 8;                // chunks a share has at least
+constexpr int kFew = 8;                // chunks a share has at least, where sequences differ
+constexpr int kLeastCut = 4;           // and where they are alike
 constexpr int kOutThreads = 24 * 32;   // copies, products, sums, products, state, decays, outputs (4 each), values and keys (8)
 constexpr int kSums = 8;               // chunks whose sums of g are kept
 constexpr int kStateThreads = 12 * 32;  // copies, products, keys (4 + 4), sums (2)
@@ -129,29 +130,52 @@ __device__ __forceinline__ int begin_of(int units, int g, int groups) {
 }
 
 // Chunks on the line of the kEachLane sequences from b on: a lane's (their loads are in flight together: batches of
-// many short sequences spend their time here).
+// many short sequences spend their time here); the least and the most that one of them has.
 constexpr int kEachLane = 8;
-__device__ __forceinline__ int units_of(const LinearParams &p, int b, bool report) {
+__device__ __forceinline__ int units_of(const LinearParams &p, int b, bool report, int &least, int &most) {
     int n = 0;
 #pragma unroll
     for (int i = 0; i < kEachLane; ++i)
         if (b + i < p.B) {
             const Seq q = seq_of(p, b + i);
             n += q.chunks * p.Hv;
+            least = min(least, q.chunks);
+            most = max(most, q.chunks);
             if (q.bad && report) atomicOr(p.err, kErrBadIndex);
         }
     return n;
 }
 
 // The line's length and share g of it (by a whole warp).
+// How many shares.  A share's chunk takes 2.1 us (and 0.75 in the first kernel, if sequences are cut); cutting costs 13 us,
+// and a share that ends inside one sequence and begins inside another 8 more.  So sequences that are alike are
+// left whole or cut into equal parts, whichever is less; others into shares of kFew chunks or more, one for each
+// sequence and head where those are fewer.
+// Measured (us, 128 x 128; shares of 4, of 8, of 16 chunks or whole): 500 tokens, 16 heads 28.1, 25.1 (whole); 1000, 8:
+// 28.7, 37.1, 38.8 (whole); 2000, 4: 30.4, 37.8, 55.7; 4000, 2: 34.1, 39.6, 56.5; 2000, 32 heads, of 6.7, 8, 16: 46.9,
+// 42.8, 58.9.  The rule, and shares of kFew with no regard to where sequences end: 750 tokens, 16 heads 30.4, 40.8;
+// 640, 8: 28.8, 39.9; 3000, 16: 44.0, 50.0; 16384, 32: 170.6, 169.9.  Parts of 2 or 3 chunks gained nothing, and
+// 8000 tokens of one head took 54.4 for 43.7.
 __device__ __forceinline__ Share share_of(const LinearParams &p, int g, bool report) {
     const int lane = threadIdx.x & 31;
     Share s;
     s.units = 0;
+    int least = 1 << 30, most = 0;
     for (int c = 0; c < p.B; c += 32 * kEachLane)
-        s.units += static_cast<int>(__reduce_add_sync(0xffffffffu, static_cast<unsigned>(units_of(p, c + kEachLane * lane, report))));
-    // as many as there are SMs, of kFew chunks at least; shorter ones where that makes one for each sequence and head
-    s.groups = max(1, min(p.groups, max((s.units + kFew - 1) / kFew, min(s.units, p.B * p.Hv))));
+        s.units += static_cast<int>(__reduce_add_sync(0xffffffffu, static_cast<unsigned>(units_of(p, c + kEachLane * lane, report, least, most))));
+    least = __reduce_min_sync(0xffffffffu, least);
+    most = __reduce_max_sync(0xffffffffu, most);
+    const int pairs = p.B * p.Hv;
+    s.groups = max(1, min(p.groups, max((s.units + kFew - 1) / kFew, min(s.units, pairs))));
+    if (least == most && pairs <= p.groups) {
+        const int parts = max(1, min(p.groups / pairs, most / kLeastCut)), each = (most + parts - 1) / parts;
+        const int whole = 210 * most, cut = parts > 1 ? 1300 + 285 * each : whole;
+        const int line = 1300 + 800 + 285 * ((s.units + s.groups - 1) / s.groups);
+        if (whole <= cut && whole <= line)
+            s.groups = pairs;
+        else if (cut <= line)
+            s.groups = pairs * parts;
+    }
     s.u0 = s.u1 = 0;
     if (g < s.groups) {
         s.u0 = begin_of(s.units, g, s.groups);
@@ -171,7 +195,8 @@ __device__ __forceinline__ Place place_of(const LinearParams &p, int u) {
     const int lane = threadIdx.x & 31;
     Place o;
     for (int c = 0, at = 0;; c += 32 * kEachLane) {
-        const int mine = units_of(p, c + kEachLane * lane, false);
+        int least, most;  // (not asked for)
+        const int mine = units_of(p, c + kEachLane * lane, false, least, most);
         int x = mine;
 #pragma unroll
         for (int off = 1; off < 32; off <<= 1) {
@@ -1265,10 +1290,10 @@ int stages_of(int dk, int dv, bool with_q) {
     return std::min(kStages, room / chunk_bytes(dk, dv, with_q));
 }
 
-// Shares of a line, at most: one an SM, each of kFew chunks or more.
+// Shares of a line, at most: one an SM, of kLeastCut chunks, or one for each sequence and head.
 int groups_of(const sgemm_linear_attention_t &a, int sms) {
     const long long units = (a.N / kC + 2 * a.B) * a.Hv;
-    return static_cast<int>(std::max(1LL, std::min<long long>(sms, std::max((units + kFew - 1) / kFew, std::min(units, a.B * a.Hv)))));
+    return static_cast<int>(std::max(1LL, std::min<long long>(sms, std::max((units + kLeastCut - 1) / kLeastCut, std::min(units, a.B * a.Hv)))));
 }
 
 sgemm_status_t check_sizes(const sgemm_linear_attention_t &a) {
