@@ -5,15 +5,15 @@
 //
 // What bounds it.  A head's state (128 x 128 FP32: 64 KiB) is read and written once for 4 operations
 // an element: memory.  So a CTA's threads load all of their part of the state before anything
-// else happens, 16 bytes a load, whole rows of the state a warp (or 128 bytes of them, below), and
-// hold it in registers until it is written back.
+// else happens, 16 bytes a load, and hold it in registers until it is written back.
 //
-// A CTA takes W columns of one head's state: all of them, or 32 where the heads of a call are too few to
-// fill the SMs.  A thread has four columns of every (256 * 4 / W)-th row; the sums over the rows are joined
-// by shuffles within a warp and in shared memory between warps, in a fixed order.
+// A CTA takes 32 columns of one head's state (128 bytes of its rows; a whole head a CTA took 2.6 us in place of 1.8 for
+// one sequence of 32 heads, 17.2 for 16.2 for 24 of them, 78.9 for 77.6 for 128).  A thread has four columns of every
+// 32nd row; the sums over the rows are joined by shuffles within a warp and in shared memory between warps, in a
+// fixed order.
 //
-// Measured on one GB300, calls one after the other: 128 sequences, 32 heads of 128 x 128 (477 MB without what is
-// padded) 70.4 us, the rate of a copy; one sequence of 32 heads 2.8 us (in slices of 32 columns; whole heads 3.6).
+// Measured on one GB300: 128 sequences, 15 of them padded, 32 heads of 128 x 128 (477 MB) 70.2 us, the rate of a copy;
+// one sequence of 32 heads 1.8 us in a graph, 2.8 as calls one after the other.
 #include <cuda_runtime.h>
 
 #include <cmath>
@@ -36,19 +36,19 @@ struct StepParams {
     int *err;
     long long q_token, q_head, k_token, k_head, v_token, v_head, g_token, g_head, s_slot, s_head, o_token, o_head, pool;
     int Hv, share;  // heads, value heads a key head
-    int slices;     // CTAs a head
     int flags;
     float scale;
 };
 
-template <int DK, int DV, int W>
+template <int DK, int DV>
 __global__ void __launch_bounds__(kStepThreads) linear_step_kernel(const __grid_constant__ StepParams p) {
+    constexpr int W = 32, kSlices = DV / W;
     constexpr int kLanes = W / 4, kRows = kStepThreads / kLanes, kEach = DK / kRows;  // lanes a row, rows at a time, rows a thread
     constexpr int kWarps = kStepThreads / 32;
     __shared__ float qs[DK], ks[DK];
     __shared__ __align__(16) float part[kWarps][W];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int slice = static_cast<int>(blockIdx.x) % p.slices, item = static_cast<int>(blockIdx.x) / p.slices;
+    const int slice = static_cast<int>(blockIdx.x) % kSlices, item = static_cast<int>(blockIdx.x) / kSlices;
     const int b = item / p.Hv, h = item - b * p.Hv, hk = h / p.share;
     const int col = slice * W + 4 * (tid % kLanes), row0 = tid / kLanes;
     if (p.flags & kFlagPdl) pdl_launch_dependents();
@@ -105,14 +105,10 @@ __global__ void __launch_bounds__(kStepThreads) linear_step_kernel(const __grid_
     }
 }
 
-template <int W>
 const void *step_kernel(int dk, int dv) {
-    if (dk == 128) {
-        if (dv == 128) return reinterpret_cast<const void *>(&linear_step_kernel<128, 128, W>);
-        return reinterpret_cast<const void *>(&linear_step_kernel<128, 64, (W < 64 ? W : 64)>);
-    }
-    if (dv == 128) return reinterpret_cast<const void *>(&linear_step_kernel<64, 128, W>);
-    return reinterpret_cast<const void *>(&linear_step_kernel<64, 64, (W < 64 ? W : 64)>);
+    if (dk == 128)
+        return dv == 128 ? reinterpret_cast<const void *>(&linear_step_kernel<128, 128>) : reinterpret_cast<const void *>(&linear_step_kernel<128, 64>);
+    return dv == 128 ? reinterpret_cast<const void *>(&linear_step_kernel<64, 128>) : reinterpret_cast<const void *>(&linear_step_kernel<64, 64>);
 }
 
 }  // namespace linear
@@ -164,10 +160,7 @@ extern "C" sgemm_status_t sgemm_bf16_linear_step(const sgemm_linear_step_t *a, s
     p.share = a->Hv / a->Hk;
     p.scale = a->scale;
     p.flags = static_cast<int>(a->flags);
-    const bool few = a->B * a->Hv < 2LL * sms;
-    p.slices = few ? a->Dv / 32 : 1;
-    const void *fn = few ? step_kernel<32>(a->Dk, a->Dv) : step_kernel<128>(a->Dk, a->Dv);
-    if (launch(fn, dim3(static_cast<unsigned>(a->B * a->Hv * p.slices)), dim3(kStepThreads), 0,
+    if (launch(step_kernel(a->Dk, a->Dv), dim3(static_cast<unsigned>(a->B * a->Hv * (a->Dv / 32))), dim3(kStepThreads), 0,
                reinterpret_cast<cudaStream_t>(stream), &p) != cudaSuccess)
         return SGEMM_ERR_CUDA;
     return SGEMM_OK;
