@@ -57,7 +57,7 @@ __device__ __forceinline__ unsigned rank_of(float v) {
 }
 
 // EACH: experts a lane of the selecting warp holds (4 for up to 128 experts, 8, or 32; a token's k rounds over 32 of
-// them took 2 us more)
+// them: 1 token of 128 experts 6.6 us, 5.6 so)
 template <int EACH>
 __global__ void __launch_bounds__(kThreadsRoute) moe_route_kernel(const __grid_constant__ RouteParams p) {
     __shared__ float part[kWarps][kExperts][kTokens];
