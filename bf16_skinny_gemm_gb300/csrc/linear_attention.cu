@@ -31,7 +31,7 @@
 // The state stays in tensor memory, FP32, for the whole sequence; a lane holds a value element's row, so that
 // scaling it and rounding it for the next O1 needs no exchange.  out = scale (exp(G_i) O1 + O2) is put
 // together in FP32.  Why K' in three numbers (cut off after 8 bits each: 24 bits): its rounding would be the
-// state's only error above FP32's, 2^-9 of every summand (in two numbers 2^-18), and it goes on to all later
+// state's only error above FP32's, 2^-8 of every summand (in two numbers 2^-16), and it goes on to all later
 // tokens.  P and Sb are rounded once: what they make is rounded to BF16 right after.
 // Roles: a warp copies (TMA, a ring of chunks), two issue the products, a warp sums the decays, and
 // eight turn the values and scale the keys, and four each carry the state, apply the decays to A, and write the outputs.

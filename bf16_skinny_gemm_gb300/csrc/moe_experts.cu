@@ -13,7 +13,7 @@
 //    so that gate and up of an element are in one lane of tensor memory.  The epilogue writes
 //    w[t,e] silu(gate) up, BF16, as row t of expert e's block of scratch; zeros for tokens that did
 //    not choose e.  (The rounding of that product to BF16, the operand type of the second one,
-//    is the only one between x and y: 2^-9 of it at most, at random over F elements.)
+//    is the only one between x and y: 2^-8 of it at most, at random over F elements.)
 //  * Down: with those zeros, y = sum_e H_e Wd_e^T is ONE product over k = (expert, element of F),
 //    accumulated in tensor memory over all experts, in the order of their indices.  The 2, 4 or 8 CTAs
 //    of a cluster take a part of that k each for 8..128 rows of y, and swap FP32 partial sums
@@ -23,14 +23,14 @@
 // Both kernels stream with TMA into a ring: one warp copies the weights, one the other operand (x or H,
 // from the L2 cache), one issues the MMAs, four do the epilogue.  A slot holds one or more chunks of 64
 // elements of k: a copy, its wait and its products take about 600 cycles to issue whatever their size.  A ring
-// takes most of the shared memory (64 tokens, 128 experts of 4096 x 1024: 512 us; with half of it, so that
-// the second kernel's CTAs are there when the first one's end, 515 to 540).  The rows a tile has, the chunks a
+// takes most of the shared memory (64 tokens, 128 experts of 4096 x 1024: 493 us; with about half of it each, so that
+// the second kernel's CTAs are there while the first one's run, 548 to 580; 1 token 38.1, 39.5 to 40.5).  The rows a tile has, the chunks a
 // slot and the CTAs a cluster are chosen on the host, see shape_of.
 //
 // Measured on one GB300, both kernels, calls one after the other on changing weights:
-//   64 tokens, 8 of 128 experts of 4096 x 1024 (3.2 GB)   496 us   6.4 TB/s
-//   8 tokens, 6 of 64 experts of 2048 x 1408              93 us   as many bytes a second
-//   1 token, 8 of 128 experts (201 MB)                    40 us   5.0 TB/s
+//   64 tokens, 8 of 128 experts of 4096 x 1024 (3.2 GB)   493 us   6.4 TB/s
+//   8 tokens, 6 of 64 experts of 2048 x 1408              91 us   as many bytes a second
+//   1 token, 8 of 128 experts (201 MB)                    38 us   5.3 TB/s
 //   2 tokens, 2 of 16 experts of 1024 x 512               13 us
 // With few tokens the two starts are what is left: tables 0.7 us, the first slots 2 to 3 us (every SM asks for all
 // of its ring at once), between the kernels 2.9 us, the cluster's exchange 0.9 us.
@@ -57,7 +57,6 @@ constexpr int kMostTokens = 128;
 constexpr int kMostEntries = 32;  // a token
 constexpr int kThreadsExperts = 32 * 7;  // weights, MMA, 4 of epilogue, the other operand
 constexpr int kRing = 16;         // slots at most
-constexpr int kMostSplit = 8;     // CTAs of a cluster that share the second product's k, at most
 constexpr int kRingBytes = 180 * 1024;
 
 struct ExpertParams {
@@ -114,8 +113,7 @@ __global__ void __launch_bounds__(kThreadsExperts, 1) moe_experts_kernel(const _
                    fin = aempty + 16, redb = fin + 8;
     const uint32_t rank = UP ? 0u : cluster_rank();
 
-    // the second kernel may always come (it waits for this one), the caller's next one where asked
-    if (UP || (p.flags & kFlagPdl)) pdl_launch_dependents();
+    if (!UP && (p.flags & kFlagPdl)) pdl_launch_dependents();  // the caller's next kernel, where asked
     if (warp == 0) {
         if (lane == 0) {
             prefetch_tmap(&p.tw);
@@ -130,10 +128,16 @@ __global__ void __launch_bounds__(kThreadsExperts, 1) moe_experts_kernel(const _
     for (int i = threadIdx.x; i < kMostExperts / 32; i += kThreadsExperts) chosen[i] = 0u;
     __syncthreads();
     if (!UP) cluster_arrive_relaxed();  // this CTA has started (paired with the wait before the partial sums)
-    pdl_wait();
+    // The down kernel's CTAs may come once nothing runs that was before the up kernel.  They read the ids and begin
+    // to copy weights at once, while up's last CTAs run, and wait for those with everything else (64 tokens of 128
+    // experts 497 -> 493 us, 8 of 64 93.4 -> 90.7, 1 of 128 40.1 -> 38.9).
+    if (UP) {
+        pdl_wait();
+        pdl_launch_dependents();
+    }
     // the experts that some token chose, in the order of their indices
     for (int i = threadIdx.x; i < p.T * p.k; i += kThreadsExperts) {
-        const int t = i / p.k, id = p.ids[t * p.ldi + (i - t * p.k)];
+        const int t = i / p.k, id = __ldcg(p.ids + t * p.ldi + (i - t * p.k));
         if (id >= p.E) {
             if (blockIdx.x == 0) atomicOr(p.err, kErrBadIndex);
         } else if (id >= 0) {
@@ -176,6 +180,7 @@ __global__ void __launch_bounds__(kThreadsExperts, 1) moe_experts_kernel(const _
     const int c0 = UP ? 0 : static_cast<int>(all * rank / p.split);
     const int c1 = UP ? kc : static_cast<int>(all * (rank + 1) / p.split);
     const int d0 = UP ? 0 : static_cast<int>(blockIdx.x) / p.split * p.rows;
+    if (!UP && warp != 0) pdl_wait();  // (warp 0 copies weights only)
     int issued = 0;  // slots that this warp's copies were issued for
 
     if (warp == 0 || warp == 6) {
@@ -431,14 +436,14 @@ bool clusters_of(int (&most)[3]) {
 // cluster 498; up with 56 rows 517; down with 2 CTAs and 56 rows 533.  8 tokens, 64 experts of 2048 x 1408: 92
 // (112 rows, 4 CTAs); up with 64 rows 95, down with 2 CTAs and 64 rows 99 and more.  1 token, 8 of 128
 // experts: 38.0 (up 64 rows, down 128); with 56 and 120 rows 40.1.
-Shape shape_of(bool up, double blocks, long long of, long long chunks, int box, bool even, int sms, const int (&clusters)[3]) {
+Shape shape_of(bool up, double blocks, long long of, long long chunks, int box, int n, bool even, int sms, const int (&clusters)[3]) {
     Shape best{8, 1, 1};
     double least = -1.0;
     for (int i = 0; i < (up ? 1 : 3); ++i)
         for (int rows = 8; rows <= 128 && rows < of + 8; rows += 8) {
             const int split = up ? 1 : 2 << i;
             int deep = 1;
-            while (even && deep < 4 && 2 * deep * ((up ? 2 : 1) * rows + box) * 128 <= kRingBytes / 3 && deep < chunks) deep *= 2;
+            while (even && deep < 4 && slot_bytes(up, rows, n, 2 * deep) <= kRingBytes / 3 && deep < chunks) deep *= 2;
             const long long row_tiles = (of + rows - 1) / rows;
             // what the memory takes for all of it, and the busiest SM, which gets 1.15 of its share where others are done
             const double tiles = up ? blocks * static_cast<double>(row_tiles) / sms : static_cast<double>(row_tiles) / clusters[i];
@@ -563,13 +568,13 @@ extern "C" sgemm_status_t sgemm_bf16_moe_experts(const sgemm_moe_experts_t *a, s
         const int sums = up ? 0 : s.split * ((a->T + s.split - 1) / s.split) * 512;
         const int rest = tail_bytes(s.rows, n, s.deep) + 1024 + sums;
         const int room = std::min(kRingBytes, static_cast<int>(kMaxSmemOptin) - rest - 8 * 1024);
-        p.slots = std::min(kRing, room / bytes);  // (3 at least: 48 KiB a slot, 64 KiB of sums at most)
+        p.slots = std::min(kRing, room / bytes);  // (2 at least: 60 KiB a slot, 64 KiB of sums at most)
         return static_cast<size_t>(p.slots) * bytes + rest;
     };
     {
         const void *fn = kernel_of<true>(n);
         p.even = a->D % 64 == 0;
-        const size_t smem = ring(true, shape_of(true, likely, a->F, (a->D + 63) / 64, p.box, p.even, sms, clusters));
+        const size_t smem = ring(true, shape_of(true, likely, a->F, (a->D + 63) / 64, p.box, n, p.even, sms, clusters));
         p.tiles = (a->F + p.rows - 1) / p.rows;
         if (!map_4d(&p.tw, a->w_gate_up, a->D, 2LL * a->F, a->E, a->gu_row, a->gu_expert, p.rows, p.deep, p.even, CU_TENSOR_MAP_L2_PROMOTION_L2_256B) ||
             !map_4d(&p.tb, a->x, a->D, a->T, 1, a->ldx, a->ldx, p.box, p.deep, p.even, CU_TENSOR_MAP_L2_PROMOTION_L2_128B) ||
@@ -580,7 +585,7 @@ extern "C" sgemm_status_t sgemm_bf16_moe_experts(const sgemm_moe_experts_t *a, s
     }
     const void *fn = kernel_of<false>(n);
     p.even = a->F % 64 == 0;
-    const size_t smem = ring(false, shape_of(false, likely, a->D, (a->F + 63) / 64, p.box, p.even, sms, clusters));
+    const size_t smem = ring(false, shape_of(false, likely, a->D, (a->F + 63) / 64, p.box, n, p.even, sms, clusters));
     if (!map_4d(&p.tw, a->w_down, a->F, a->D, a->E, a->dn_row, a->dn_expert, p.rows, p.deep, p.even, CU_TENSOR_MAP_L2_PROMOTION_L2_256B) ||
         !map_4d(&p.tb, a->workspace, a->F, a->T, experts, a->F, static_cast<long long>(a->T) * a->F, p.box, p.deep, p.even,
                 CU_TENSOR_MAP_L2_PROMOTION_L2_128B) ||
