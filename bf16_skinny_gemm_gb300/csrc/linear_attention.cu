@@ -79,7 +79,7 @@ constexpr int kStateThreads = 12 * 32;  // copies, products, keys (4 + 4), sums 
 constexpr float kLeast = -200.0f;
 
 struct LinearParams {
-    CUtensorMap tq, tk, tv;  // {64, N, D / 64, heads}, boxes of 64 tokens: a chunk's operand is one copy
+    CUtensorMap tq, tk, tv, to;  // {64, N, D / 64, heads}, boxes of 64 tokens: a chunk's operand is one copy
     const float *g;
     float *state;
     const long long *slots;
@@ -92,7 +92,7 @@ struct LinearParams {
     int Dk, Dv;
     int groups;        // shares at most
     int stages;
-    int out16;         // out's rows start on 16 bytes
+    int out16;         // out's rows start on 16 bytes: whole chunks are stored as one copy
     int flags;
     float scale;
 };
@@ -280,6 +280,17 @@ __device__ __forceinline__ bool all_of(bool v) {
         : "memory");
     return r != 0;
 }
+
+// The copy of a chunk's outputs to memory; its thread's copies so far have read shared memory, or are done.
+__device__ __forceinline__ void tma_store_4d(uint32_t src, const CUtensorMap *map, int c0, int c1, int c2, int c3) {
+    asm volatile("cp.async.bulk.tensor.4d.global.shared::cta.tile.bulk_group [%0, {%1, %2, %3, %4}], [%5];" ::"l"(
+                     reinterpret_cast<uint64_t>(map)),
+                 "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(src)
+                 : "memory");
+    asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+}
+__device__ __forceinline__ void copies_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
+__device__ __forceinline__ void copies_done() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
 
 // Scratch: exp of the sum of g of each share's cut piece; what the joining is to do from each share on;
 // the pieces' states (what the next share begins with, after the joining); what cut sequences begin with.
@@ -1205,6 +1216,7 @@ __global__ void __launch_bounds__(kOutThreads, 1) linear_outputs_kernel(const __
         int n = 0;
         for (; n < total; ++n) {
             // the four warps go on together, or none (they meet at barriers); what was staged is stored
+            if (tid == 0) copies_read();
             if (!all_of(phase(odone + 8 * (n & 1), n >> 1, &stop) && phase(o1done + 8 * (n & 1), n >> 1, &stop))) break;
             tc_fence_after();
             hear(n);
@@ -1237,19 +1249,25 @@ __global__ void __launch_bounds__(kOutThreads, 1) linear_outputs_kernel(const __
                             unpack2(ffma2(ee, pack2(a[r], a[r + 1]), mul2(scale, pack2(b[r], b[r + 1]))), x, y);
                             o[m] = bf16x2(__uint_as_float(x), __uint_as_float(y));
                         }
-                        stmatrix_turned(to_s + (t1 + 16 * i + 8 * (lane >> 4) + (lane & 7)) * 256 +
-                                            (((4 * q + 2 * h + ((lane >> 3) & 1)) ^ (lane & 7)) << 4), o);
+                        stmatrix_turned(to_s + (q >> 1) * kPart + (t1 + 16 * i + 8 * (lane >> 4) + (lane & 7)) * 128 +
+                                            (((4 * (q & 1) + 2 * h + ((lane >> 3) & 1)) ^ (lane & 7)) << 4), o);
                     }
                 }
             tc_fence_before();
             __syncwarp();
             if (lane == 0) bar_arrive(ofree + 8 * (n & 1));
+            const bool copied = p.out16 && c.valid == kC;
+            if (copied) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             asm volatile("bar.sync 1, 128;" ::: "memory");
+            if (copied) {
+                if (tid == 0) tma_store_4d(to_s, &p.to, 0, c.t0, 0, c.h);
+                continue;
+            }
             const int shift = p.Dv == 128 ? 4 : 3, end = c.valid << shift;
 #pragma unroll 1
             for (int i = tid; i < end; i += 128) {
                 const int tok = i >> shift, u = i & ((1 << shift) - 1);
-                const uint4 v = *reinterpret_cast<const uint4 *>(os + tok * 256 + ((u ^ (tok & 7)) << 4));
+                const uint4 v = *reinterpret_cast<const uint4 *>(os + (u >> 3) * kPart + tok * 128 + (((u & 7) ^ (tok & 7)) << 4));
                 uint16_t *to = out + tok * p.o_token + 8 * u;
                 if (p.out16) {
                     *reinterpret_cast<uint4 *>(to) = v;
@@ -1262,6 +1280,7 @@ __global__ void __launch_bounds__(kOutThreads, 1) linear_outputs_kernel(const __
                 }
             }
         }
+        if (tid == 0) copies_done();
         // after a stop: NaN for the chunks that were not finished
         if (n < total)
             for (int i = 0; cursor.next(p, c); ++i)
@@ -1405,6 +1424,8 @@ extern "C" sgemm_status_t sgemm_bf16_linear_attention(const sgemm_linear_attenti
     p.Dv = a->Dv;
     p.scale = a->scale;
     p.out16 = aligned(a->out, 16) && a->o_token % 8 == 0 && a->o_head % 8 == 0 ? 1 : 0;
+    if (p.out16 && !map_4d(&p.to, a->N ? a->out : none, a->Dv, rows, a->Hv, a->o_token, a->o_head, kC, a->Dv / 64, true, promote))
+        return SGEMM_ERR_CUDA;
     p.flags = static_cast<int>(a->flags);
     const cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
     const bool wide = a->Dk == 128;
