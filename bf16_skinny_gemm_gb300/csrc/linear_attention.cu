@@ -9,8 +9,9 @@
 // if the chain of the chunks' states does not: that chain has to be short, and there have to be
 // enough of them.
 //
-// Work split.  The chunks of all (sequence, head) pairs form one line, cut into equal shares, one
-// for each SM; a share ends anywhere inside a sequence.  Three launches:
+// Work split.  Either an SM takes whole sequences of a head (the longest first, dealt out forwards and backwards in
+// turn), or the chunks of all (sequence, head) pairs form one line, cut into equal shares, one
+// for each SM; a share ends anywhere inside a sequence (see share_of).  Three launches:
 //   1. states: for every share that ends inside a sequence, what its part of that sequence adds to
 //      the state, U = sum_j exp(sum of g from j to the share's end) k_j v_j^T, and the sum of its g.  The
 //      chunks are taken from the last to the first, so that the factor of a key is known at once
@@ -41,10 +42,10 @@
 // took 9600 cycles (4500 without any other change).
 //
 // Measured on one GB300, calls one after the other:
-//   16384 tokens, 32 heads, 128 x 128 (541 MB)                         170 us
+//   16384 tokens, 32 heads, 128 x 128 (541 MB)                         169 us
 //     states 50 us (235 MB, 4.7 TB/s), joining 4, outputs 114 (529 MB, 4.6 TB/s; alone, from a cold cache)
-//   8 ragged prompts of up to 2049, 8 key and 32 value heads, 64 x 128  99 us
-//   one prompt of 500, 16 heads                                         25 us
+//   8 ragged prompts of up to 2049, 8 key and 32 value heads, 64 x 128  72 us (whole sequences)
+//   one prompt of 500, 16 heads                                         24 us
 // What bounds the output kernel: a chunk's chain, 3400 cycles (keys 1500, state's product 1300, the pass over the
 // state 800 to 1000, two barriers of 200 to 300), issue slots taken to 57%, the tensor pipe to 34%.  The states'
 // kernel is bound by memory, 41 GB/s an SM while it runs.  Around them: 2.4 us until the first copies are
@@ -123,6 +124,8 @@ __device__ __forceinline__ Seq seq_of(const LinearParams &p, int b) {
 
 struct Share {
     int units, groups, u0, u1;
+    bool whole;  // u1 chunks, of whole sequences, the first of which is
+    int b, h;
 };
 
 __device__ __forceinline__ int begin_of(int units, int g, int groups) {
@@ -132,7 +135,7 @@ __device__ __forceinline__ int begin_of(int units, int g, int groups) {
 // Chunks on the line of the kEachLane sequences from b on: a lane's (their loads are in flight together: batches of
 // many short sequences spend their time here); the least and the most that one of them has.
 constexpr int kEachLane = 8;
-__device__ __forceinline__ int units_of(const LinearParams &p, int b, bool report, int &least, int &most) {
+__device__ __forceinline__ int units_of(const LinearParams &p, int b, bool report, int &least, int &most, int *keep = nullptr) {
     int n = 0;
 #pragma unroll
     for (int i = 0; i < kEachLane; ++i)
@@ -141,43 +144,100 @@ __device__ __forceinline__ int units_of(const LinearParams &p, int b, bool repor
             n += q.chunks * p.Hv;
             least = min(least, q.chunks);
             most = max(most, q.chunks);
+            if (keep) keep[b + i] = q.chunks;
             if (q.bad && report) atomicOr(p.err, kErrBadIndex);
         }
     return n;
 }
 
-// The line's length and share g of it (by a whole warp).
-// How many shares.  A share's chunk takes 2.1 us (and 0.75 in the first kernel, if sequences are cut); cutting costs 13 us,
-// and a share that ends inside one sequence and begins inside another 8 more.  So sequences that are alike are
-// left whole or cut into equal parts, whichever is less; others into shares of kFew chunks or more, one for each
-// sequence and head where those are fewer.
-// Measured (us, 128 x 128; shares of 4, of 8, of 16 chunks or whole): 500 tokens, 16 heads 28.1, 25.1 (whole); 1000, 8:
+// Whole sequences, for the SMs: the pairs of a sequence and a head in the order of their chunks, the longest first, are
+// dealt out forwards and backwards in turn.
+constexpr int kMostSorted = 256, kMostRounds = 64;
+__device__ __forceinline__ int dealt(int round, int g, int groups) { return round & 1 ? (round + 1) * groups - 1 - g : round * groups + g; }
+
+// Sorts the sequences (room: their chunks): the chunks of the SM that has the most, if whole ones are dealt out.  A
+// function by itself, for shares that do not call it start 2 us later with it in their midst.
+__device__ __noinline__ int deal(const LinearParams &p, int bins, int *room, uint8_t *order) {
+    int *sorted = room + kMostSorted, *span = sorted + kMostSorted;
+    const int pairs = p.B * p.Hv;
+    if (threadIdx.x == 0) *span = 0;
+    __syncthreads();
+    for (int b = threadIdx.x; b < p.B; b += blockDim.x) {
+        const int mine = room[b];
+        int rank = 0;
+        for (int i = 0; i < p.B; ++i) rank += room[i] > mine || (room[i] == mine && i < b);
+        sorted[rank] = mine;
+        order[rank] = static_cast<uint8_t>(b);
+    }
+    __syncthreads();
+    for (int i = threadIdx.x; i < bins; i += blockDim.x) {
+        int n = 0;
+        for (int r = 0; r * bins < pairs; ++r) {
+            const int j = dealt(r, i, bins);
+            if (j < pairs) n += sorted[j / p.Hv];
+        }
+        atomicMax(span, n);
+    }
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // (copies come to where this was)
+    __syncthreads();
+    return *span;
+}
+
+// The chunks of an SM's whole sequences (by a whole warp).
+__device__ __noinline__ int dealt_chunks(const LinearParams &p, int g, int bins, const int *sorted) {
+    unsigned n = 0;
+    for (int r = threadIdx.x & 31; r * bins < p.B * p.Hv; r += 32) {
+        const int j = dealt(r, g, bins);
+        if (j < p.B * p.Hv) n += static_cast<unsigned>(sorted[j / p.Hv]);
+    }
+    return static_cast<int>(__reduce_add_sync(0xffffffffu, n));
+}
+
+// The line's length and share g of it (by all threads; `room` is shared memory).  order: the sequences, the longest first.
+// How many shares.  A share's chunk takes 1.85 us, and 0.95 more if its sequence is cut; cutting costs 7 us and half a
+// one a part, and 10 more where shares end inside one sequence and begin inside another.  So sequences are left whole, those
+// that are alike are cut into equal parts, or the line of all of them is cut into shares of kFew chunks or more (one for each
+// sequence and head where those are fewer), whichever takes the least.
+// Whole, and on the line (us, ragged prompts): 4 up to 2324, 32 heads 77.4, 84.0; 3 of 3000 93.6, 85.5; 8 of 2000, 16
+// heads 68.9, 78.4; 8 of 1500, 8 heads 52.7, 48.5; 16 of 900, 8 heads 38.7, 53.6; 32 of 500, 32 heads 116, 162; 200 of 200,
+// 16 heads (21 rounds) 234, 312; 3 of 1000, 32 heads of 64 x 128 33.4, 37.2; 3 of 4000 102.5, 84.8.
+// Alike (us, 128 x 128; shares of 4, of 8, of 16 chunks or whole): 500 tokens, 16 heads 28.1, 25.1 (whole); 1000, 8:
 // 28.7, 37.1, 38.8 (whole); 2000, 4: 30.4, 37.8, 55.7; 4000, 2: 34.1, 39.6, 56.5; 2000, 32 heads, of 6.7, 8, 16: 46.9,
-// 42.8, 58.9.  The rule, and shares of kFew with no regard to where sequences end: 750 tokens, 16 heads 30.4, 40.8;
+// 42.8, 58.9.  Equal parts, and shares of kFew with no regard to where sequences end: 750 tokens, 16 heads 30.4, 40.8;
 // 640, 8: 28.8, 39.9; 3000, 16: 44.0, 50.0; 16384, 32: 170.6, 169.9.  Parts of 2 or 3 chunks gained nothing, and
 // 8000 tokens of one head took 54.4 for 43.7.
-__device__ __forceinline__ Share share_of(const LinearParams &p, int g, bool report) {
-    const int lane = threadIdx.x & 31;
+__device__ __forceinline__ Share share_of(const LinearParams &p, int g, bool report, int *room, uint8_t *order) {
+    const int lane = threadIdx.x & 31, pairs = p.B * p.Hv, bins = min(pairs, p.groups);
+    const bool few = p.B <= kMostSorted && pairs <= kMostRounds * bins;
+    int *keep = few && pairs > bins && threadIdx.x < 32 ? room : nullptr;
     Share s;
     s.units = 0;
     int least = 1 << 30, most = 0;
     for (int c = 0; c < p.B; c += 32 * kEachLane)
-        s.units += static_cast<int>(__reduce_add_sync(0xffffffffu, static_cast<unsigned>(units_of(p, c + kEachLane * lane, report, least, most))));
+        s.units += static_cast<int>(__reduce_add_sync(0xffffffffu, static_cast<unsigned>(units_of(p, c + kEachLane * lane, report, least, most, keep))));
     least = __reduce_min_sync(0xffffffffu, least);
     most = __reduce_max_sync(0xffffffffu, most);
-    const int pairs = p.B * p.Hv;
+    const bool packs = few && most > 1, sorts = packs && pairs > bins;  // (a line of single chunks cuts nothing)
+    int busiest = most;
+    if (sorts) busiest = deal(p, bins, room, order);
     s.groups = max(1, min(p.groups, max((s.units + kFew - 1) / kFew, min(s.units, pairs))));
-    if (least == most && pairs <= p.groups) {
-        const int parts = max(1, min(p.groups / pairs, most / kLeastCut)), each = (most + parts - 1) / parts;
-        const int whole = 210 * most, cut = parts > 1 ? 1300 + 285 * each : whole;
-        const int line = 1300 + 800 + 285 * ((s.units + s.groups - 1) / s.groups);
-        if (whole <= cut && whole <= line)
-            s.groups = pairs;
-        else if (cut <= line)
-            s.groups = pairs * parts;
-    }
-    s.u0 = s.u1 = 0;
-    if (g < s.groups) {
+    const long long each = (s.units + s.groups - 1) / s.groups, whole = 185LL * busiest;
+    const long long line = 1700 + 185 * each + 95 * min(each, static_cast<long long>(most));
+    const bool alike = least == most && pairs <= p.groups;
+    const int parts = alike ? max(1, min(p.groups / pairs, most / kLeastCut)) : 1;
+    const long long cut = parts > 1 ? 700 + 50 * parts + 280LL * ((most + parts - 1) / parts) : line;
+    s.whole = packs && whole <= cut && whole <= line;
+    if (!s.whole && parts > 1 && cut <= line) s.groups = pairs * parts;
+    s.u0 = s.u1 = s.b = s.h = 0;
+    if (s.whole) {
+        s.groups = bins;
+        if (g < bins) {
+            const int at = g / p.Hv;
+            s.b = sorts ? order[at] : at;
+            s.h = g - at * p.Hv;
+            s.u1 = sorts ? dealt_chunks(p, g, bins, room + kMostSorted) : seq_of(p, s.b).chunks;
+        }
+    } else if (g < s.groups) {
         s.u0 = begin_of(s.units, g, s.groups);
         s.u1 = begin_of(s.units, g + 1, s.groups);
     }
@@ -228,12 +288,38 @@ struct Chunk {
     int b, h, t0, valid;  // first token, tokens
     bool head, tail;      // the first of its piece of a sequence, the sequence's last
     bool first;           // the sequence's first
+    long long slot;       // the sequence's
 };
+// The place after sequence b of head h: the next head's, or the next sequence's; or the next of the whole
+// sequences (one function for all roles: the instruction cache).
+__device__ __noinline__ Place after(const LinearParams &p, int b, int h, int round, const uint8_t *order) {
+    Place o;
+    o.k = 0;
+    if (order) {
+        const int j = dealt(round, static_cast<int>(blockIdx.x), min(p.B * p.Hv, p.groups)), i = j / p.Hv;
+        o.b = order[i];
+        o.h = j - i * p.Hv;
+        o.s = seq_of(p, o.b);
+        return o;
+    }
+    o.b = b;
+    o.h = h + 1;
+    if (o.h == p.Hv) {
+        o.h = 0;
+        do o.s = seq_of(p, ++o.b);
+        while (o.s.chunks == 0);
+    } else {
+        o.s = seq_of(p, b);
+    }
+    return o;
+}
 struct Cursor {
     Place at;
     int left;
     bool head;
-    __device__ __forceinline__ Cursor(const Place &o, int n) : at(o), left(n), head(true) {}
+    int round;             // of whole sequences
+    const uint8_t *order;  // of those, or none
+    __device__ __forceinline__ Cursor(const Place &o, int n, const uint8_t *f) : at(o), left(n), head(true), round(0), order(f) {}
     __device__ __forceinline__ bool next(const LinearParams &p, Chunk &c) {
         if (left <= 0) return false;
         --left;
@@ -242,18 +328,11 @@ struct Cursor {
         c.t0 = at.s.t0 + at.k * kC;
         c.valid = max(0, min(kC, at.s.len - at.k * kC));
         c.first = at.k == 0;
+        c.slot = at.s.slot;
         c.head = head || c.first;
         c.tail = at.k + 1 == at.s.chunks;
         head = false;
-        if (++at.k == at.s.chunks) {
-            at.k = 0;
-            if (++at.h == p.Hv) {
-                at.h = 0;
-                if (left > 0)
-                    do at.s = seq_of(p, ++at.b);
-                    while (at.s.chunks == 0);
-            }
-        }
+        if (++at.k == at.s.chunks && left > 0) at = after(p, at.b, at.h, ++round, order);
         return true;
     }
 };
@@ -479,7 +558,7 @@ __device__ __forceinline__ void scale_keys(const uint8_t *k, uint8_t *out, const
 
 __host__ __device__ constexpr int chunk_bytes(int dk, int dv, bool with_q) { return ((with_q ? 2 : 1) * dk + dv) / 64 * kPart; }
 // barriers, and arrays of each chunk's tokens or values
-constexpr int kMiscOut = 1024 + 3 * kSums * kC * 4 + 4 * 128 * 4;
+constexpr int kMiscOut = 1024 + 3 * kSums * kC * 4 + 4 * 128 * 4 + kMostSorted;
 constexpr int kOutStage = kC * 256;  // a chunk's outputs on their way
 __host__ __device__ constexpr int out_fixed(int dk) { return 2 * 3 * dk / 64 * kPart + kPart + kOutStage + kMiscOut; }
 constexpr int kAhead = 8;  // chunks whose g the state kernel has on their way
@@ -525,11 +604,11 @@ __global__ void __launch_bounds__(kStateThreads, 1) linear_states_kernel(const _
     }
     pdl_launch_dependents();  // the next kernels are this call's
     pdl_wait();
-    const Share sh = share_of(p, g, false);
+    const Share sh = share_of(p, g, false, reinterpret_cast<int *>(base), base + 4 * (2 * kMostSorted + 1));
     Place last;
     last.k = 0;
     last.s.chunks = 0;
-    if (sh.u1 > sh.u0) last = place_of(p, sh.u1 - 1);
+    if (sh.u1 > sh.u0 && !sh.whole) last = place_of(p, sh.u1 - 1);
     const bool cut = last.k + 1 < last.s.chunks;  // a sequence goes on behind this share
     if (threadIdx.x == 0) {
         // Where it begins here: the shares behind which it goes on (up to, not with, the one that has its
@@ -795,6 +874,7 @@ __global__ void __launch_bounds__(kOutThreads, 1) linear_outputs_kernel(const __
     // [kSums][64] of each token: G_i, scale exp(G_i), exp(G - G_i)
     float *gs = reinterpret_cast<float *>(misc + 1024), *eg = gs + kSums * kC, *wk = eg + kSums * kC;
     int *first_bad = reinterpret_cast<int *>(wk + kSums * kC);  // [4][128] the first token with such a value
+    uint8_t *order = reinterpret_cast<uint8_t *>(first_bad + 4 * 128);  // [kMostSorted] sequences, the longest first
     // [8] what chunk n is, by the warp of the sums: {b, h, first token, tokens and flags}
     int4 *told = reinterpret_cast<int4 *>(misc + 640);
     uint32_t at = saddr(bars);
@@ -840,14 +920,14 @@ __global__ void __launch_bounds__(kOutThreads, 1) linear_outputs_kernel(const __
     }
     if (p.flags & kFlagPdl) pdl_launch_dependents();
     pdl_wait();
-    const Share sh = share_of(p, g, g == 0 && warp == 0);
+    const Share sh = share_of(p, g, g == 0 && warp == 0, reinterpret_cast<int *>(os), order);
     if (sh.u1 <= sh.u0) return;
     if (warp == 1) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(saddr(tmem_slot)), "r"(512)
                      : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
-    Cursor cursor(place_of(p, sh.u0), sh.u1 - sh.u0);
+    Cursor cursor(sh.whole ? Place{sh.b, sh.h, 0, seq_of(p, sh.b)} : place_of(p, sh.u0), sh.u1 - sh.u0, sh.whole ? order : nullptr);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -993,7 +1073,16 @@ __global__ void __launch_bounds__(kOutThreads, 1) linear_outputs_kernel(const __
         for (int n = 0; n < total; ++n) {
             const Decays now = next;
             const int4 what = make_int4(nc.b, nc.h, nc.t0, nc.valid | (nc.head ? kHead : 0) | (nc.tail ? kTail : 0) | (nc.first ? kFirst : 0));
-            if (ahead.next(p, nc)) next = load_g(p, nc);
+            if (ahead.next(p, nc)) {
+                next = load_g(p, nc);
+                // the state that a sequence begins with, on its way while the one before ends (200 prompts of up to
+                // 200, 16 heads: 297 -> 261 us)
+                if (nc.first && nc.slot >= 0 && !(p.fresh && p.fresh[nc.b]) && elect())
+                    asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p.state + nc.slot * p.s_slot + nc.h * p.s_head),
+                                 "r"(p.Dk * p.Dv * 4)
+                                 : "memory");
+                __syncwarp();
+            }
             Pair a, b, all;
             sums_of(now, a, b, all);
             if (n >= 2 && !phase(sdone + 8 * (n & 1), ((n >> 1) - 1) & 1, &stop)) break;

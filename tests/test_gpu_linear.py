@@ -397,3 +397,48 @@ def test_batches_that_take_several_passes_over_their_offsets(B):
     lens = [(b * b * 7) % 5 if b % 3 else 0 for b in range(B)]
     lens[B - 1] = 130
     compare(lens, 1, 1, 64, 64, seed=B, fresh=[b % 2 for b in range(B)])
+
+
+@pytest.mark.parametrize("B,Hk,Hv,Dk,Dv,top", [(40, 2, 8, 128, 128, 200), (24, 16, 16, 128, 64, 350), (200, 1, 8, 64, 64, 130),
+                                                (256, 4, 4, 64, 128, 100), (9, 3, 18, 128, 128, 129)])
+def test_more_sequences_and_heads_than_sms(B, Hk, Hv, Dk, Dv, top):
+    """Whole sequences in several rounds, the longest first: lengths in no order, some of them 0."""
+    lens = [(b * b * 31 + 17 * b) % (top + 1) if b % 7 else 0 for b in range(B)]
+    lens[B // 2] = top
+    compare(lens, Hk, Hv, Dk, Dv, seed=B, fresh=[b % 2 for b in range(B)])
+
+
+def test_more_sequences_than_sms_with_bad_ones():
+    B, Hv = 60, 8
+    lens = [1 + (37 * b * b) % 150 for b in range(B)]
+    q, k, v, g, state, slots = problem(lens, 2, Hv, 64, 64, 21, pool=70)
+    want, last, ob, sb = expect(q, k, v, g, state, slots, lens, 1.0, True)
+    at = [sum(lens[:b]) for b in range(B + 1)]
+    # one sequence more, which runs backwards, a slot outside the pool, and one that is none
+    spare = [s for s in range(70) if s not in slots.tolist()]
+    cu = at[:31] + [at[30] - 5] + [at[30]] + at[31:]
+    cu[31] = at[30] - 5  # sequence 30 falls; 31 repeats rows of the one before
+    slots2 = torch.cat([slots[:30], torch.tensor([spare[0], -1]), slots[30:]])
+    out = torch.full((sum(lens), Hv, 64), 9.0, dtype=torch.bfloat16, device=DEV)
+    out, s = prompt(q, k, v, g, state, slots2, None, cu=cu, errors=2, out=out)
+    # sequence 31 writes rows that another one has too: those are left out
+    rows = torch.ones(sum(lens), dtype=torch.bool)
+    rows[at[30] - 5:at[30]] = False
+    D.check(out[rows], want[rows], ob[rows], "out")
+    assert torch.equal(s[spare[0]].cpu(), state[spare[0]])
+    used = torch.tensor(slots.tolist())
+    D.check(s[used], last[used], sb[used] + 1e-300, "state")
+    slots3 = slots.clone()
+    slots3[13] = 70
+    out, s = prompt(q, k, v, g, state, slots3, lens, errors=2)
+    others = torch.cat([slots[:13], slots[14:]])
+    D.check(s[others], last[others], sb[others] + 1e-300, "state")
+    assert torch.equal(s[slots[13]].cpu(), state[slots[13]])
+
+
+def test_stalled_copies_of_many_sequences():
+    lens = [1 + (37 * b * b) % 150 for b in range(40)]
+    p = problem(lens, 2, 8, 128, 128, 22)
+    out, s = prompt(*p, lens, errors=1, flags=sk.SGEMM_FLAG_TEST_STALL)
+    assert torch.isnan(out).all() and torch.isnan(s[p[5]]).all()
+    compare(lens, 2, 8, seed=22)
