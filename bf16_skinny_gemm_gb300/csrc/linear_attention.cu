@@ -12,6 +12,7 @@
 // Work split.  Either an SM takes whole sequences of a head (the longest first, dealt out forwards and backwards in
 // turn), or the chunks of all (sequence, head) pairs form one line, cut into equal shares, one
 // for each SM; a share ends anywhere inside a sequence (see share_of).  Three launches:
+//   (With few tokens there is nothing to cut, and the third is the only one.)
 //   1. states: for every share that ends inside a sequence, what its part of that sequence adds to
 //      the state, U = sum_j exp(sum of g from j to the share's end) k_j v_j^T, and the sum of its g.  The
 //      chunks are taken from the last to the first, so that the factor of a key is known at once
@@ -45,7 +46,7 @@
 //   16384 tokens, 32 heads, 128 x 128 (541 MB)                         168 us
 //     states 50 us (235 MB, 4.7 TB/s), joining 4, outputs 114 (529 MB, 4.6 TB/s; alone, from a cold cache)
 //   8 ragged prompts of up to 2049, 8 key and 32 value heads, 64 x 128  72 us (whole sequences)
-//   one prompt of 500, 16 heads                                         24 us
+//   one prompt of 500, 16 heads                                         20 us (the third kernel alone)
 // What bounds the output kernel: a chunk's chain, 3400 cycles (keys 1500, state's product 1300, the pass over the
 // state 800 to 1000, two barriers of 200 to 300), issue slots taken to 57%, the tensor pipe to 34%.  The states'
 // kernel is bound by memory, 41 GB/s an SM while it runs.  Around them: 2.4 us until the first copies are
@@ -92,6 +93,7 @@ struct LinearParams {
     int B, Hv, share;  // sequences, value heads, value heads a key head
     int Dk, Dv;
     int groups;        // shares at most
+    int whole;         // no sequence is cut, whatever the lengths, and the third kernel is the only one
     int stages;
     int out16;         // out's rows start on 16 bytes: whole chunks are stored as one copy
     int flags;
@@ -193,6 +195,7 @@ __device__ __noinline__ int dealt_chunks(const LinearParams &p, int g, int bins,
     return static_cast<int>(__reduce_add_sync(0xffffffffu, n));
 }
 
+constexpr int kChunkCost = 185, kLineCost = 1700, kStarts = 340;  // 10 ns
 // The line's length and share g of it (by all threads; `room` is shared memory).  order: the sequences, the longest first.
 // How many shares.  A share's chunk takes 1.85 us, and 0.95 more if its sequence is cut; cutting costs 7 us and half a
 // one a part, and 10 more where shares end inside one sequence and begin inside another.  So sequences are left whole, those
@@ -221,12 +224,12 @@ __device__ __forceinline__ Share share_of(const LinearParams &p, int g, bool rep
     int busiest = most;
     if (sorts) busiest = deal(p, bins, room, order);
     s.groups = max(1, min(p.groups, max((s.units + kFew - 1) / kFew, min(s.units, pairs))));
-    const long long each = (s.units + s.groups - 1) / s.groups, whole = 185LL * busiest;
-    const long long line = 1700 + 185 * each + 95 * min(each, static_cast<long long>(most));
+    const long long each = (s.units + s.groups - 1) / s.groups, whole = kChunkCost * static_cast<long long>(busiest);
+    const long long line = kLineCost + kChunkCost * each + 95 * min(each, static_cast<long long>(most));
     const bool alike = least == most && pairs <= p.groups;
     const int parts = alike ? max(1, min(p.groups / pairs, most / kLeastCut)) : 1;
     const long long cut = parts > 1 ? 700 + 50 * parts + 280LL * ((most + parts - 1) / parts) : line;
-    s.whole = packs && whole <= cut && whole <= line;
+    s.whole = p.whole || (packs && whole <= cut && whole <= line);
     if (!s.whole && parts > 1 && cut <= line) s.groups = pairs * parts;
     s.u0 = s.u1 = s.b = s.h = 0;
     if (s.whole) {
@@ -921,9 +924,10 @@ __global__ void __launch_bounds__(kOutThreads, 1) linear_outputs_kernel(const __
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     }
     if (p.flags & kFlagPdl) pdl_launch_dependents();
-    if (p.groups == 1) pdl_wait();  // (no kernel of this call before)
+    const bool alone = p.whole || p.groups == 1;  // no kernel of this call before
+    if (alone) pdl_wait();
     const Share sh = share_of(p, g, g == 0 && warp == 0, reinterpret_cast<int *>(os), order);
-    if (p.groups > 1) pdl_wait();
+    if (!alone) pdl_wait();
     if (sh.u1 <= sh.u0) return;
     if (warp == 1) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(saddr(tmem_slot)), "r"(512)
@@ -1519,10 +1523,17 @@ extern "C" sgemm_status_t sgemm_bf16_linear_attention(const sgemm_linear_attenti
     if (p.out16 && !map_4d(&p.to, a->N ? a->out : none, a->Dv, rows, a->Hv, a->o_token, a->o_head, kC, a->Dv / 64, true, promote))
         return SGEMM_ERR_CUDA;
     p.flags = static_cast<int>(a->flags);
+    // So few tokens that no sequence would be cut, if it had them all: neither a line nor two parts would pay against
+    // the first two kernels' time (500 tokens, 16 heads: 20.4 us, 23.8 with them; 704, 16: 25.8, 29.8).
+    const long long pairs = a->B * a->Hv, longest = (a->N + kC - 1) / kC;
+    if (pairs <= p.groups && kChunkCost * longest <= kLineCost + kStarts) {
+        p.whole = 1;
+        p.groups = static_cast<int>(pairs);
+    }
     const cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
     const bool wide = a->Dk == 128;
     static std::atomic<unsigned long long> done[4];
-    if (p.groups > 1) {
+    if (p.groups > 1 && !p.whole) {
         const void *fn = wide ? reinterpret_cast<const void *>(&linear_states_kernel<128>) : reinterpret_cast<const void *>(&linear_states_kernel<64>);
         if (!allow(fn, done[wide])) return SGEMM_ERR_CUDA;
         p.stages = stages_of(a->Dk, a->Dv, false);
