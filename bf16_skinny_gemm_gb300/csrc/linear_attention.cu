@@ -605,10 +605,7 @@ __global__ void __launch_bounds__(kStateThreads, 1) linear_states_kernel(const _
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     }
-    // The next kernels are this call's; they may come once nothing runs that was before it, and the third reads the
-    // call's inputs before it waits (4 ragged prompts of up to 3000, 16 heads: 62.7 -> 61.2 us).
     pdl_wait();
-    pdl_launch_dependents();
     const Share sh = share_of(p, g, false, reinterpret_cast<int *>(base), base + 4 * (2 * kMostSorted + 1));
     Place last;
     last.k = 0;
@@ -635,6 +632,10 @@ __global__ void __launch_bounds__(kStateThreads, 1) linear_states_kernel(const _
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
+    // The next kernels are this call's; they may come once nothing runs that was before it, and the third reads the
+    // call's inputs before it waits (4 ragged prompts of up to 3000, 16 heads: 62.7 -> 61.2 us).  Nor before this
+    // CTA has its tensor memory: a kernel behind them that takes some before it waits would hold what this one wants.
+    pdl_launch_dependents();
     const uint32_t tmem = *tmem_slot;
     const bool stall = (p.flags & kFlagTestStall) != 0;
     int issued = 0;
@@ -923,7 +924,6 @@ __global__ void __launch_bounds__(kOutThreads, 1) linear_outputs_kernel(const __
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     }
-    if (p.flags & kFlagPdl) pdl_launch_dependents();
     const bool alone = p.whole || p.groups == 1;  // no kernel of this call before
     if (alone) pdl_wait();
     const Share sh = share_of(p, g, g == 0 && warp == 0, reinterpret_cast<int *>(os), order);
@@ -938,6 +938,7 @@ __global__ void __launch_bounds__(kOutThreads, 1) linear_outputs_kernel(const __
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
+    if (p.flags & kFlagPdl) pdl_launch_dependents();  // (as above: not before the tensor memory is taken)
     const uint32_t tmem = *tmem_slot;
     const bool stall = (p.flags & kFlagTestStall) != 0;
     const float nan = __int_as_float(0x7fc00000);

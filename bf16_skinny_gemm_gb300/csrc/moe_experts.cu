@@ -113,7 +113,6 @@ __global__ void __launch_bounds__(kThreadsExperts, 1) moe_experts_kernel(const _
                    fin = aempty + 16, redb = fin + 8;
     const uint32_t rank = UP ? 0u : cluster_rank();
 
-    if (!UP && (p.flags & kFlagPdl)) pdl_launch_dependents();  // the caller's next kernel, where asked
     if (warp == 0) {
         if (lane == 0) {
             prefetch_tmap(&p.tw);
@@ -128,13 +127,7 @@ __global__ void __launch_bounds__(kThreadsExperts, 1) moe_experts_kernel(const _
     for (int i = threadIdx.x; i < kMostExperts / 32; i += kThreadsExperts) chosen[i] = 0u;
     __syncthreads();
     if (!UP) cluster_arrive_relaxed();  // this CTA has started (paired with the wait before the partial sums)
-    // The down kernel's CTAs may come once nothing runs that was before the up kernel.  They read the ids and begin
-    // to copy weights at once, while up's last CTAs run, and wait for those with everything else (64 tokens of 128
-    // experts 497 -> 493 us, 8 of 64 93.4 -> 90.7, 1 of 128 40.1 -> 38.9).
-    if (UP) {
-        pdl_wait();
-        pdl_launch_dependents();
-    }
+    if (UP) pdl_wait();
     // the experts that some token chose, in the order of their indices
     for (int i = threadIdx.x; i < p.T * p.k; i += kThreadsExperts) {
         const int t = i / p.k, id = __ldcg(p.ids + t * p.ldi + (i - t * p.k));
@@ -169,6 +162,12 @@ __global__ void __launch_bounds__(kThreadsExperts, 1) moe_experts_kernel(const _
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
+    // The down kernel's CTAs may come once nothing runs that was before the up kernel.  They read the ids and begin
+    // to copy weights at once, while up's last CTAs run, and wait for those with everything else (64 tokens of 128
+    // experts 497 -> 493 us, 8 of 64 93.4 -> 90.7, 1 of 128 40.1 -> 38.9).  The caller's next kernel comes where
+    // asked.  Neither comes before this CTA has its tensor memory: a kernel that takes some before it waits
+    // would hold what this one, which it waits for, wants.
+    if (UP || (p.flags & kFlagPdl)) pdl_launch_dependents();
     const uint32_t tmem = tmem_slot;
     const bool stall = (p.flags & kFlagTestStall) != 0;
 

@@ -442,3 +442,27 @@ def test_stalled_copies_of_many_sequences():
     out, s = prompt(*p, lens, errors=1, flags=sk.SGEMM_FLAG_TEST_STALL)
     assert torch.isnan(out).all() and torch.isnan(s[p[5]]).all()
     compare(lens, 2, 8, seed=22)
+
+
+def test_chained_launches():
+    """Calls and GEMMs one behind the other, each allowed to start while the one before runs: as without that."""
+    lens = [400, 30, 700]
+    q, k, v, g, state, slots = (t.to(DEV) for t in problem(lens, 2, 4, 128, 128, 31))
+    cu = torch.tensor([0, 400, 430, 1130], dtype=torch.int32, device=DEV)
+    w = torch.randn((1024, 512), generator=torch.Generator().manual_seed(5)).to(torch.bfloat16).to(DEV)
+    work = torch.empty(sk.sgemm_linear_attention_workspace(1130, 3, 4, 128, 128), dtype=torch.uint8, device=DEV)
+
+    def chain(flags):
+        s, out, y = state.clone(), torch.zeros_like(v), torch.zeros((8, 1024), dtype=torch.bfloat16, device=DEV)
+        token = torch.zeros((3, 4, 128), dtype=torch.bfloat16, device=DEV)
+        torch.cuda.synchronize()
+        for _ in range(20):
+            sk.sgemm_bf16_linear_attention(q, k, v, g, s, slots, cu, 0.1, out=out, workspace=work, flags=flags)
+            sk.sgemm_bf16_skinny_ex(out.view(-1, 512)[:8], w, y, flags=flags)
+            sk.sgemm_bf16_linear_step(q[:3], k[:3], v[:3], g[:3], s, slots, 0.1, out=token, flags=flags)
+        torch.cuda.synchronize()
+        assert sk.sgemm_device_errors() == 0
+        return s, out, y, token
+
+    for a, b in zip(chain(0), chain(sk.SGEMM_FLAG_PDL)):
+        assert torch.equal(a, b)

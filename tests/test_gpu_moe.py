@@ -253,3 +253,32 @@ def test_stalled_copies_end_in_nan_and_an_error():
     assert sk.sgemm_device_errors() == 1
     assert torch.isnan(y).all()
     compare(x, gu, dn, ids, weights)
+
+
+@pytest.mark.parametrize("T,E,k,width,F", [(1, 16, 2, 256, 64), (8, 32, 4, 512, 256), (70, 16, 4, 128, 128), (20, 8, 2, 64, 64)])
+def test_chained_launches(T, E, k, width, F):
+    """Router, experts and a GEMM one behind the other, each allowed to start while the one before runs, with one
+    buffer of ids: as without that."""
+    g = torch.Generator().manual_seed(T)
+    x0 = normal(g, T, width).to(DEV)
+    routers = [normal(g, E, width).to(DEV) for _ in range(4)]
+    gu, dn = normal(g, E, 2 * F, width, std=width ** -0.5).to(DEV), normal(g, E, width, F, std=F ** -0.5).to(DEV)
+    w = normal(g, width, width, std=width ** -0.5).to(DEV)
+    n = min(T, 8)
+
+    def chain(flags):
+        x, y, z = x0.clone(), torch.zeros_like(x0), torch.zeros((n, width), dtype=torch.bfloat16, device=DEV)
+        ids, weights = torch.zeros((T, k), dtype=torch.int32, device=DEV), torch.zeros((T, k), device=DEV)
+        work = torch.empty(sk.sgemm_moe_experts_workspace(T, E, k, width, F), dtype=torch.uint8, device=DEV)
+        torch.cuda.synchronize()
+        for i in range(24):
+            a, b = (x, y) if i % 2 == 0 else (y, x)
+            sk.sgemm_bf16_moe_route(a, routers[i % 4], k, ids=ids, weights=weights, flags=flags)
+            sk.sgemm_bf16_moe_experts(a, gu, dn, ids, weights, y=b, workspace=work, flags=flags)
+            sk.sgemm_bf16_skinny_ex(b[:n], w, z, flags=flags)
+        torch.cuda.synchronize()
+        assert sk.sgemm_device_errors() == 0
+        return x, y, z, ids, weights
+
+    for a, b in zip(chain(0), chain(sk.SGEMM_FLAG_PDL)):
+        assert torch.equal(a, b)
