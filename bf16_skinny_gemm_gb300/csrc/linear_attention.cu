@@ -43,12 +43,13 @@
 // took 9600 cycles (4500 without any other change).
 //
 // Measured on one GB300, calls one after the other:
-//   16384 tokens, 32 heads, 128 x 128 (541 MB)                         168 us
+//   16384 tokens, 32 heads, 128 x 128 (541 MB)                         167 us
 //     states 50 us (235 MB, 4.7 TB/s), joining 4, outputs 114 (529 MB, 4.6 TB/s; alone, from a cold cache)
 //   8 ragged prompts of up to 2049, 8 key and 32 value heads, 64 x 128  72 us (whole sequences)
 //   one prompt of 500, 16 heads                                         20 us (the third kernel alone)
-// What bounds the output kernel: a chunk's chain, 3400 cycles (keys 1500, state's product 1300, the pass over the
-// state 800 to 1000, two barriers of 200 to 300), issue slots taken to 57%, the tensor pipe to 34%.  The states'
+// What bounds the output kernel: a chunk takes 3200 to 3500 cycles, and three chains of about that length wait for one
+// another: the state's (product 1300, pass 1100, hand-overs 900), A's (decays 1600, two products and their hand-overs
+// 1700) and the outputs' (2000, and 1500 until the next).  Issue slots are taken to 54%, the tensor pipe to 36%.  The states'
 // kernel is bound by memory, 41 GB/s an SM while it runs.  Around them: 2.4 us until the first copies are
 // issued, 3 us for a state's first load, 3 for the last store.
 #include <cuda.h>
