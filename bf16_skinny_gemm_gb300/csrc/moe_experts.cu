@@ -33,7 +33,7 @@
 //   1 token, 8 of 128 experts (201 MB)                    38 us   5.3 TB/s
 //   2 tokens, 2 of 16 experts of 1024 x 512               13 us
 // With few tokens the two starts are what is left: tables 0.7 us, the first slots 2 to 3 us (every SM asks for all
-// of its ring at once), between the kernels 2.9 us, the cluster's exchange 0.9 us.
+// of its ring at once), between the kernels 1 to 2 us (2.9 before the second copied early), the cluster's exchange 0.9 us.
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -434,7 +434,7 @@ bool clusters_of(int (&most)[3]) {
 // Measured (us for both products): 64 tokens, 128 experts of 4096 x 1024: tiles of 128 rows, down with 4 CTAs a
 // cluster 498; up with 56 rows 517; down with 2 CTAs and 56 rows 533.  8 tokens, 64 experts of 2048 x 1408: 92
 // (112 rows, 4 CTAs); up with 64 rows 95, down with 2 CTAs and 64 rows 99 and more.  1 token, 8 of 128
-// experts: 38.0 (up 64 rows, down 128); with 56 and 120 rows 40.1.
+// experts: 38.1 (up 64 rows, down 120); up with 56 rows 38.9, and two slots.
 Shape shape_of(bool up, double blocks, long long of, long long chunks, int box, int n, bool even, int sms, const int (&clusters)[3]) {
     Shape best{8, 1, 1};
     double least = -1.0;
