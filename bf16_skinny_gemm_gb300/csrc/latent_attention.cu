@@ -212,6 +212,10 @@ struct Share {
     Seq s;              // that sequence
 };
 
+// Tiles that a line has at most.  Offsets that rise keep below it (checked on the host); those of drafted tokens that
+// fall and rise again over the same rows may not, and their sum may pass 32 bits: nothing is computed then.
+constexpr long long kMostUnits = 1LL << 30;
+
 // Found by each warp by itself (no block barrier before the first copies): a pass over the
 // sequences for the line's length, one for the place of the share's beginning.
 template <bool TREE>
@@ -219,7 +223,8 @@ __device__ __forceinline__ Share share_of(const LatentParams &p, int g, bool rep
     const int lane = threadIdx.x & 31;
     Share s;
     s.units = 0;
-    Seq mine;  // the lane's sequence of the last 32 read
+    long long sum = 0;  // (drafted tokens)
+    Seq mine;           // the lane's sequence of the last 32 read
     mine.n = 0;
     int c = 0;
     for (;;) {
@@ -229,9 +234,18 @@ __device__ __forceinline__ Share share_of(const LatentParams &p, int g, bool rep
         } else {
             mine.n = 0;
         }
-        s.units += static_cast<int>(__reduce_add_sync(0xffffffffu, static_cast<unsigned>(tiles_of(p, mine) * (TREE ? blocks_of(p, mine) : 1))));
+        if (TREE) {
+            const unsigned t = static_cast<unsigned>(tiles_of(p, mine) * blocks_of(p, mine));  // (below 2^30)
+            sum += __reduce_add_sync(0xffffffffu, t & 0xffffu) + (static_cast<long long>(__reduce_add_sync(0xffffffffu, t >> 16)) << 16);
+        } else {
+            s.units += static_cast<int>(__reduce_add_sync(0xffffffffu, static_cast<unsigned>(tiles_of(p, mine))));
+        }
         if (c + 32 >= p.B) break;
         c += 32;
+    }
+    if (TREE) {
+        if (sum >= kMostUnits && report && lane == 0) atomicOr(p.err, kErrBadIndex);
+        s.units = sum >= kMostUnits ? 0 : static_cast<int>(sum);
     }
     s.groups = min(p.groups, max(s.units, 1));
     s.u0 = s.u1 = s.b = s.k = s.r = 0;
@@ -687,6 +701,8 @@ __global__ void __launch_bounds__(threads_of(NT), 1) latent_attention_kernel(con
         int4 *desc = reinterpret_cast<int4 *>(p.ws);
         const bool tell = r == 0 && tid == 0 && p.groups > 1;
         if (tell && !p.by_seq) desc[g] = make_int4(0, 0, 0, -1);
+        if (TREE && tell && p.by_seq && g == 0 && sh.units == 0)  // (sequences with tokens, none of them computed)
+            for (int i = 0; i < p.B * p.most; ++i) desc[i] = make_int4(0, 0, 0, -1);
         while (walk.template next<TREE>(p, r, o)) {
             if (tell && o.first) {
                 const int u_last = sh.u0 + (sh.u1 - sh.u0 - o.left) + tiles_of(p, o.s) - 1;

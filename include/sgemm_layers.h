@@ -118,7 +118,9 @@ sgemm_status_t sgemm_bf16_moe_experts(const sgemm_moe_experts_t *args, sgemm_str
  * whatever numbers of new tokens the sequences have, and that the scratch is
  * sgemm_latent_tree_attention_workspace bytes.  (A row of a new token with an infinity or a NaN among its values adds nothing to the tokens
  * that do not see it, and may add nothing where it is infinite or NaN to those that do.)
- * - (table_width * page_size / 64 + 3) * (total_q * H / 16 + B) < 2^30.
+ * - (table_width * page_size / 64 + 3) * (total_q * H / 16 + B) < 2^30.  Where cu_q falls and rises again over the
+ *   same rows of q, so that its sequences come to 2^30 or more of what is bounded so (64 cached rows for
+ *   16, 32 or 64 rows of q), nothing is computed and bit 1 of the device error word is set.
  * - words >= 1: 64-bit words a token, max_q <= 64 * words; words <= ld_tree < 2^28;
  *   tree is 8-byte aligned and overlaps no output. */
 sgemm_status_t sgemm_bf16_latent_tree_attention(const sgemm_latent_attention_t *args,
