@@ -125,6 +125,10 @@ __device__ __forceinline__ Seq seq_of(const LinearParams &p, int b) {
     return s;
 }
 
+// Chunks that a line has at most.  Offsets that rise keep far below it (checked on the host); offsets that fall and rise
+// again over the same tokens may not, and their sum may pass 32 bits: nothing is computed then.
+constexpr long long kMostUnits = 1LL << 30;
+
 struct Share {
     int units, groups, u0, u1;
     bool whole;  // u1 chunks, of whole sequences, the first of which is
@@ -210,6 +214,9 @@ constexpr int kChunkCost = 185, kLineCost = 1700, kStarts = 340;  // 10 ns
 // 42.8, 58.9.  Equal parts, and shares of kFew with no regard to where sequences end: 750 tokens, 16 heads 30.4, 40.8;
 // 640, 8: 28.8, 39.9; 3000, 16: 44.0, 50.0; 16384, 32: 170.6, 169.9.  Parts of 2 or 3 chunks gained nothing, and
 // 8000 tokens of one head took 54.4 for 43.7.
+// COUNTS: the sequences may come to kMostUnits chunks, whatever their offsets, and are counted in 64 bits (a template
+// argument: with the test in the other kernels' midst ragged prompts took 72.1 us for 70.3, prompts of 500 20.5 for 20.3).
+template <bool COUNTS>
 __device__ __forceinline__ Share share_of(const LinearParams &p, int g, bool report, int *room, uint8_t *order) {
     const int lane = threadIdx.x & 31, pairs = p.B * p.Hv, bins = min(pairs, p.groups);
     const bool few = p.B <= kMostSorted && pairs <= kMostRounds * bins;
@@ -217,8 +224,24 @@ __device__ __forceinline__ Share share_of(const LinearParams &p, int g, bool rep
     Share s;
     s.units = 0;
     int least = 1 << 30, most = 0;
-    for (int c = 0; c < p.B; c += 32 * kEachLane)
-        s.units += static_cast<int>(__reduce_add_sync(0xffffffffu, static_cast<unsigned>(units_of(p, c + kEachLane * lane, report, least, most, keep))));
+    if (COUNTS) {
+        long long sum = 0;
+        for (int c = 0; c < p.B; c += 32 * kEachLane) {
+            const unsigned n = static_cast<unsigned>(units_of(p, c + kEachLane * lane, report, least, most, keep));  // (below 2^29)
+            sum += __reduce_add_sync(0xffffffffu, n & 0xffffu) + (static_cast<long long>(__reduce_add_sync(0xffffffffu, n >> 16)) << 16);
+        }
+        s.units = static_cast<int>(sum);
+        if (sum >= kMostUnits) {
+            if (report && lane == 0) atomicOr(p.err, kErrBadIndex);
+            s.units = s.u0 = s.u1 = s.b = s.h = 0;
+            s.groups = 1;
+            s.whole = false;
+            return s;
+        }
+    } else {
+        for (int c = 0; c < p.B; c += 32 * kEachLane)
+            s.units += static_cast<int>(__reduce_add_sync(0xffffffffu, static_cast<unsigned>(units_of(p, c + kEachLane * lane, report, least, most, keep))));
+    }
     least = __reduce_min_sync(0xffffffffu, least);
     most = __reduce_max_sync(0xffffffffu, most);
     const bool packs = few && most > 1, sorts = packs && pairs > bins;  // (a line of single chunks cuts nothing)
@@ -573,7 +596,7 @@ constexpr int kU = 0, kKeyT = 128;
 constexpr int kState = 0, kSb = 128, kA = 192, kO1 = 256, kO2 = 384, kValueT = 448;
 
 // ------------------------------------------------------------------------ 1. states of cut pieces
-template <int DK>
+template <int DK, bool COUNTS>
 __global__ void __launch_bounds__(kStateThreads, 1) linear_states_kernel(const __grid_constant__ LinearParams p) {
     constexpr int kKParts = DK / 64, kKeys = kKParts * kPart, kWarps = 4;
     extern __shared__ uint8_t raw[];
@@ -607,7 +630,7 @@ __global__ void __launch_bounds__(kStateThreads, 1) linear_states_kernel(const _
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     }
     pdl_wait();
-    const Share sh = share_of(p, g, false, reinterpret_cast<int *>(base), base + 4 * (2 * kMostSorted + 1));
+    const Share sh = share_of<COUNTS>(p, g, false, reinterpret_cast<int *>(base), base + 4 * (2 * kMostSorted + 1));
     Place last;
     last.k = 0;
     last.s.chunks = 0;
@@ -863,7 +886,7 @@ __global__ void __launch_bounds__(kJoinThreads) linear_join_kernel(const __grid_
 }
 
 // ------------------------------------------------------------------------------------ 3. outputs
-template <int DK>
+template <int DK, bool COUNTS>
 __global__ void __launch_bounds__(kOutThreads, 1) linear_outputs_kernel(const __grid_constant__ LinearParams p) {
     constexpr int kKParts = DK / 64, kKeys = kKParts * kPart;
     extern __shared__ uint8_t raw[];
@@ -927,7 +950,7 @@ __global__ void __launch_bounds__(kOutThreads, 1) linear_outputs_kernel(const __
     }
     const bool alone = p.whole || p.groups == 1;  // no kernel of this call before
     if (alone) pdl_wait();
-    const Share sh = share_of(p, g, g == 0 && warp == 0, reinterpret_cast<int *>(os), order);
+    const Share sh = share_of<COUNTS>(p, g, g == 0 && warp == 0, reinterpret_cast<int *>(os), order);
     if (!alone) pdl_wait();
     if (sh.u1 <= sh.u0) return;
     if (warp == 1) {
@@ -1402,6 +1425,15 @@ __global__ void __launch_bounds__(kOutThreads, 1) linear_outputs_kernel(const __
     }
 }
 
+template <bool COUNTS>
+const void *states_kernel(bool wide) {
+    return wide ? reinterpret_cast<const void *>(&linear_states_kernel<128, COUNTS>) : reinterpret_cast<const void *>(&linear_states_kernel<64, COUNTS>);
+}
+template <bool COUNTS>
+const void *outputs_kernel(bool wide) {
+    return wide ? reinterpret_cast<const void *>(&linear_outputs_kernel<128, COUNTS>) : reinterpret_cast<const void *>(&linear_outputs_kernel<64, COUNTS>);
+}
+
 int stages_of(int dk, int dv, bool with_q) {
     const int room = static_cast<int>(kMaxSmemOptin) - 1024 - (with_q ? out_fixed(dk) : kStateFixed);
     return std::min(kStages, room / chunk_bytes(dk, dv, with_q));
@@ -1534,10 +1566,11 @@ extern "C" sgemm_status_t sgemm_bf16_linear_attention(const sgemm_linear_attenti
     }
     const cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
     const bool wide = a->Dk == 128;
-    static std::atomic<unsigned long long> done[4];
+    const bool counts = pairs * longest >= kMostUnits;  // (chunks, if every sequence had all tokens)
+    static std::atomic<unsigned long long> done[8];
     if (p.groups > 1 && !p.whole) {
-        const void *fn = wide ? reinterpret_cast<const void *>(&linear_states_kernel<128>) : reinterpret_cast<const void *>(&linear_states_kernel<64>);
-        if (!allow(fn, done[wide])) return SGEMM_ERR_CUDA;
+        const void *fn = counts ? states_kernel<true>(wide) : states_kernel<false>(wide);
+        if (!allow(fn, done[2 * counts + wide])) return SGEMM_ERR_CUDA;
         p.stages = stages_of(a->Dk, a->Dv, false);
         const size_t smem = 1024 + static_cast<size_t>(p.stages) * chunk_bytes(a->Dk, a->Dv, false) + kStateFixed;
         if (launch(fn, dim3(static_cast<unsigned>(p.groups)), dim3(kStateThreads), smem, cs, &p) != cudaSuccess) return SGEMM_ERR_CUDA;
@@ -1546,8 +1579,8 @@ extern "C" sgemm_status_t sgemm_bf16_linear_attention(const sgemm_linear_attenti
                    0, cs, &p) != cudaSuccess)
             return SGEMM_ERR_CUDA;
     }
-    const void *fn = wide ? reinterpret_cast<const void *>(&linear_outputs_kernel<128>) : reinterpret_cast<const void *>(&linear_outputs_kernel<64>);
-    if (!allow(fn, done[2 + wide])) return SGEMM_ERR_CUDA;
+    const void *fn = counts ? outputs_kernel<true>(wide) : outputs_kernel<false>(wide);
+    if (!allow(fn, done[4 + 2 * counts + wide])) return SGEMM_ERR_CUDA;
     p.stages = stages_of(a->Dk, a->Dv, true);
     const size_t smem = 1024 + static_cast<size_t>(p.stages) * chunk_bytes(a->Dk, a->Dv, true) + out_fixed(a->Dk);
     if (launch(fn, dim3(static_cast<unsigned>(p.groups)), dim3(kOutThreads), smem, cs, &p) != cudaSuccess) return SGEMM_ERR_CUDA;

@@ -178,7 +178,10 @@ sgemm_status_t sgemm_bf16_linear_step(const sgemm_linear_step_t *args, sgemm_str
  * - A sequence without tokens leaves its slot as it is (zeros where fresh).
  * - cu rises from 0 or more to at most N; where it does not, the sequence is taken
  *   as one without tokens whose slot stays as it is, and bit 1 of the error word is
- *   set.  Rows of out before cu[0] and from cu[B] on are left as they are.
+ *   set.  Rows of out before cu[0] and from cu[B] on are left as they are.  Where cu
+ *   falls and rises again over the same tokens, the rows that two sequences share have
+ *   the values of either; where the sequences come to 2^30 or more chunks of all heads
+ *   so, nothing is computed and bit 1 of the error word is set.
  * - Two sequences of one call must not name the same slot.
  * - g <= 0 is what this is made for.  exp(g) may exceed 1 as long as no exp(G_i - G_j)
  *   overflows; g = -inf drops what came before.  An infinity or a NaN in q reaches its
