@@ -18,7 +18,9 @@
 //    accumulated in tensor memory over all experts, in the order of their indices.  The 2, 4 or 8 CTAs
 //    of a cluster take a part of that k each for 8..128 rows of y, and swap FP32 partial sums
 //    through distributed shared memory (st.async), a part of the tokens each, added in rank order.
-//    No atomics, no sorting: the result does not depend on timing.
+//    No atomics, no sorting: the result does not depend on timing.  (Zeros times an infinity or a NaN among the
+//    weights of an expert are NaN for the tokens that did not choose it: outputs that come as NaN are worked out
+//    again from the token's own experts, see chosen_only.)
 //
 // Both kernels stream with TMA into a ring: one warp copies the weights, one the other operand (x or H,
 // from the L2 cache), one issues the MMAs, four do the epilogue.  A slot holds one or more chunks of 64
@@ -67,6 +69,8 @@ struct ExpertParams {
     const int *ids;
     const float *weights;
     uint16_t *h;     // H, [expert of the list][T][F]
+    const uint16_t *down;  // the down matrices, as tw has them (for single outputs)
+    long long dn_expert, dn_row;
     uint16_t *y;
     int *err;
     long long ldi, ldwt, ldy;
@@ -85,6 +89,40 @@ __host__ __device__ constexpr int slot_bytes(bool up, int rows, int n, int deep)
 // behind the ring: an MMA reads 128 rows of weights though a tile may have fewer
 __host__ __device__ constexpr int tail_bytes(int rows, int n, int deep) {
     return 128 > rows + deep * n ? (128 - rows - deep * n) * 128 : 0;
+}
+
+// y[t][d] of `own` tokens from `first` on, where it is NaN: over the experts that t chose, and no others, an element of h
+// times its weight after the other, FP32.  For outputs that the shared product gives as NaN, which they are not where it
+// comes from 0 x an infinity or a NaN in the weights of an expert that t did not choose.  What is NaN indeed ends the
+// sum at once.  (A function by itself, after the sums: where it is not
+// called 2 tokens of 16 experts take 17.6 us for 17.4 without it, 1 token of 128 experts 43.8 for 43.7, 64 490 for 490.)
+__device__ __noinline__ void chosen_only(const ExpertParams &p, const unsigned *chosen, int first, int own, int d) {
+    for (int t = first; t < first + own; ++t) {
+        uint16_t *y = p.y + t * p.ldy + d;
+        if ((*y & 0x7fff) <= 0x7f80) continue;
+        const int *ids = p.ids + t * p.ldi;
+        float s = 0.0f;
+        for (int j = 0; j < p.k; ++j) {
+            const int id = ids[j];
+            bool take = id >= 0 && id < p.E;
+            for (int i = 0; i < j; ++i) take = take && ids[i] != id;  // (its block of h has all of its weights)
+            if (!take) continue;
+            int a = __popc(chosen[id >> 5] & ((1u << (id & 31)) - 1u));
+            for (int i = 0; i < id >> 5; ++i) a += __popc(chosen[i]);
+            const uint4 *h = reinterpret_cast<const uint4 *>(p.h + (static_cast<long long>(a) * p.T + t) * p.F);
+            const uint4 *w = reinterpret_cast<const uint4 *>(p.down + id * p.dn_expert + d * p.dn_row);
+            for (int f = 0; f < p.F / 8 && s == s; ++f) {
+                const uint4 x = __ldcg(h + f), v = __ldcg(w + f);
+                const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, vs[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                for (int m = 0; m < 4; ++m) {
+                    s = fmaf(bf16_lo(xs[m]), bf16_lo(vs[m]), s);
+                    s = fmaf(bf16_hi(xs[m]), bf16_hi(vs[m]), s);
+                }
+            }
+        }
+        *y = f32_to_bf16_rn(s);
+    }
 }
 
 template <int N, bool UP>
@@ -349,12 +387,15 @@ __global__ void __launch_bounds__(kThreadsExperts, 1) moe_experts_kernel(const _
             }
             const bool got = bar_wait_cluster(redb, 0);
             if (!got) atomicExch(&stop, 1);
+            bool odd = false;
             if (row < p.rows && d0 + row < p.D)
                 for (int t = 0; t < own; ++t) {
                     float s = red[t * 128 + row];
                     for (int r = 1; r < p.split; ++r) s += red[(r * each + t) * 128 + row];
+                    odd |= s != s;
                     p.y[(first + t) * p.ldy + d0 + row] = f32_to_bf16_rn(got ? s : nan);
                 }
+            if (odd && got) chosen_only(p, chosen, first, own, d0 + row);
         }
     }
     if (!UP && (warp < 2 || warp == 6)) cluster_wait_acquire();
@@ -538,6 +579,9 @@ extern "C" sgemm_status_t sgemm_bf16_moe_experts(const sgemm_moe_experts_t *a, s
     p.ids = a->ids;
     p.weights = a->weights;
     p.h = static_cast<uint16_t *>(a->workspace);
+    p.down = a->w_down;
+    p.dn_expert = a->dn_expert;
+    p.dn_row = a->dn_row;
     p.y = a->y;
     p.ldi = a->ldi;
     p.ldwt = a->ldwt;

@@ -76,8 +76,9 @@ sgemm_status_t sgemm_bf16_moe_route(const sgemm_moe_route_t *args, sgemm_stream_
  *   set bit 1 of the device error word.
  * - Experts that every token takes are entries like the others: ids[t][j] of them
  *   with weight 1.
- * - The tokens of a call share the products: an infinity or a NaN in the weights
- *   of an expert reaches every token of the call.  One in x[t] reaches y[t] only.
+ * - An infinity or a NaN in x[t] reaches y[t] only, one in the weights of an expert
+ *   the tokens that chose it.  (The tokens share the products: outputs that come as
+ *   NaN are summed again one by one, which takes longer.)
  * - 0 <= T <= 128; D and F multiples of 8, at most 2^20; 1 <= E <= 1024, 1 <= k <= 32;
  *   D and F at least 8.
  * - x, w_gate_up, w_down are 16-byte aligned, all their strides multiples of 8;
@@ -86,7 +87,8 @@ sgemm_status_t sgemm_bf16_moe_route(const sgemm_moe_route_t *args, sgemm_stream_
  *   (128-byte aligned).  Its contents need no preparation and do not survive the
  *   call.  Calls that may overlap on the GPU need scratch of their own.
  * - Waits inside the kernels are bounded: one that runs out sets bit 0 of the
- *   device error word and writes NaN outputs.  SGEMM_FLAG_TEST_STALL is accepted. */
+ *   device error word, and outputs that miss something are NaN.
+ *   SGEMM_FLAG_TEST_STALL is accepted. */
 typedef struct {
     const sgemm_bf16_t *x;          /* [T, D], row stride ldx */
     const sgemm_bf16_t *w_gate_up;  /* [E, 2F, D], strides gu_expert, gu_row */
