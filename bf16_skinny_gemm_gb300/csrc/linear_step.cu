@@ -121,7 +121,7 @@ extern "C" sgemm_status_t sgemm_bf16_linear_step(const sgemm_linear_step_t *a, s
     if (a->B < 0 || a->Hk < 1 || a->Hv < a->Hk || a->Hv % a->Hk || a->Hv > 1024 || !std::isfinite(a->scale)) return SGEMM_ERR_INVALID_ARG;
     if ((a->Dk != 64 && a->Dk != 128) || (a->Dv != 64 && a->Dv != 128)) return SGEMM_ERR_UNSUPPORTED_SHAPE;
     if (a->B == 0) return SGEMM_OK;
-    if (a->B * a->Hv >= (1LL << 28)) return SGEMM_ERR_UNSUPPORTED_SHAPE;
+    if (a->B > ((1LL << 28) - 1) / a->Hv) return SGEMM_ERR_UNSUPPORTED_SHAPE;
     if (!a->q || !a->k || !a->v || !a->g || (a->pool > 0 && !a->state) || !a->slots || !a->out || a->pool < 0 || a->pool >= (1LL << 31))
         return SGEMM_ERR_INVALID_ARG;
     const LinearView io{a->q, a->k, a->v, a->g, a->state, a->out, a->q_token, a->q_head, a->k_token, a->k_head, a->v_token,
