@@ -148,7 +148,7 @@ struct LatentParams {
     int out16;    // out's rows start on 16 bytes
     int by_seq;   // descriptors of split sequences: one a sequence (drafted tokens: and block of rows), else one a group
     int most;     // blocks of rows of a sequence with max_q drafted tokens
-    int words;    // of a drafted token's mask
+    int bits;     // of a drafted token's mask, 2^31 - 1 at most (a sequence has fewer new tokens)
     int tell;     // floats of the descriptors, before the pieces
     const unsigned long long *tree;  // the masks, or null
     long long ld_tree;
@@ -756,7 +756,7 @@ __global__ void __launch_bounds__(threads_of(NT), 1) latent_attention_kernel(con
                             if (TREE && hidden) {
                                 // a drafted token's row: its bit in the mask of the query's token
                                 const int col = col0 + 8 * i + c0 + (e & 1), draft = at - (o.s.len - o.s.n_all);
-                                if (col < o.nrows && at < o.s.len && draft < 64 * p.words) {
+                                if (col < o.nrows && at < o.s.len && draft < p.bits) {
                                     const int tok = o.s.q0 + p.heads.div(o.row0 + col);
                                     hidden = !((p.tree[tok * p.ld_tree + (draft >> 6)] >> (draft & 63)) & 1);
                                 }
@@ -1396,7 +1396,7 @@ sgemm_status_t attend(const sgemm_latent_attention_t *a, const Tree *tree, sgemm
     if (tree) {
         p.tree = reinterpret_cast<const unsigned long long *>(tree->masks);
         p.ld_tree = tree->ld;
-        p.words = tree->words;
+        p.bits = static_cast<int>(std::min(64LL * tree->words, 0x7fffffffLL));
     }
     p.heads = Divisor::of(a->H);
     p.ctas = Divisor::of(sp.rt);

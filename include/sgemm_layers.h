@@ -118,8 +118,9 @@ sgemm_status_t sgemm_bf16_moe_experts(const sgemm_moe_experts_t *args, sgemm_str
  * sequence does not have, and of rows before the cache's first, change nothing.
  * All else is as sgemm_bf16_latent_attention has it, but that the work is split evenly
  * whatever numbers of new tokens the sequences have, and that the scratch is
- * sgemm_latent_tree_attention_workspace bytes.  (A row of a new token with an infinity or a NaN among its values adds nothing to the tokens
- * that do not see it, and may add nothing where it is infinite or NaN to those that do.)
+ * sgemm_latent_tree_attention_workspace bytes.  (What a new token's row holds, infinities
+ * and NaN included, never reaches a token that does not see it.  A row that a token
+ * sees with an infinity and a score of -inf, so with weight 0, adds nothing.)
  * - (table_width * page_size / 64 + 3) * (total_q * H / 16 + B) < 2^30.  Where cu_q falls and rises again over the
  *   same rows of q, so that its sequences come to 2^30 or more of what is bounded so (64 cached rows for
  *   16, 32 or 64 rows of q), nothing is computed and bit 1 of the device error word is set.
