@@ -1572,7 +1572,7 @@ extern "C" sgemm_status_t sgemm_bf16_linear_attention(const sgemm_linear_attenti
         const void *fn = counts ? states_kernel<true>(wide) : states_kernel<false>(wide);
         if (!allow(fn, done[2 * counts + wide])) return SGEMM_ERR_CUDA;
         p.stages = stages_of(a->Dk, a->Dv, false);
-        const size_t smem = 1024 + static_cast<size_t>(p.stages) * chunk_bytes(a->Dk, a->Dv, false) + kStateFixed;
+        const size_t smem = std::max(kAloneSmem, 1024 + static_cast<size_t>(p.stages) * chunk_bytes(a->Dk, a->Dv, false) + kStateFixed);
         if (launch(fn, dim3(static_cast<unsigned>(p.groups)), dim3(kStateThreads), smem, cs, &p) != cudaSuccess) return SGEMM_ERR_CUDA;
         const unsigned slices = static_cast<unsigned>(a->Dk * a->Dv / 4 / kJoinThreads / kJoinEach);  // 1 .. 4
         if (launch(reinterpret_cast<const void *>(&linear_join_kernel), dim3(static_cast<unsigned>(p.groups), slices), dim3(kJoinThreads),

@@ -617,7 +617,8 @@ extern "C" sgemm_status_t sgemm_bf16_moe_experts(const sgemm_moe_experts_t *a, s
     {
         const void *fn = kernel_of<true>(n);
         p.even = a->D % 64 == 0;
-        const size_t smem = ring(true, shape_of(true, likely, a->F, (a->D + 63) / 64, p.box, n, p.even, sms, clusters));
+        size_t smem = ring(true, shape_of(true, likely, a->F, (a->D + 63) / 64, p.box, n, p.even, sms, clusters));
+        if (n >= 64) smem = std::max(smem, kAloneSmem);  // (half of the tensor memory, or all of it)
         p.tiles = (a->F + p.rows - 1) / p.rows;
         if (!map_4d(&p.tw, a->w_gate_up, a->D, 2LL * a->F, a->E, a->gu_row, a->gu_expert, p.rows, p.deep, p.even, CU_TENSOR_MAP_L2_PROMOTION_L2_256B) ||
             !map_4d(&p.tb, a->x, a->D, a->T, 1, a->ldx, a->ldx, p.box, p.deep, p.even, CU_TENSOR_MAP_L2_PROMOTION_L2_128B) ||

@@ -15,6 +15,13 @@ using tc05::tc_fence_after;
 using tc05::tc_fence_before;
 using tc05::tmem_ld16;
 
+// Shared memory that a CTA asks for at least where it takes half of the tensor memory or all of it.  It waits until it has
+// it.  Beside it on the SM there might be two CTAs of another stream's GEMMs (a ring of two stages of 16 KiB each at least),
+// of which one holds some until the other one is done, which waits behind this CTA for its own: there is no room for two.
+// (All the shared memory would leave the next kernel's small CTAs none: 3 prompts of 3000, 16 heads of 128 x 64: 55.3 ->
+// 56.8 us.)
+constexpr size_t kAloneSmem = kMaxSmemOptin - 48 * 1024;
+
 // Wait for a phase, at most kWaitLimitNs, and not past another role's giving up.
 __device__ __forceinline__ bool wait_or_stop(uint32_t b, unsigned parity, int *stop) {
     if (bar_try(b, parity)) return true;
