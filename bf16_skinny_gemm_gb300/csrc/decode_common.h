@@ -75,9 +75,12 @@ inline bool heads_overlap(const Heads &a, const Heads &b, long long T, long long
 inline bool valid_flags(unsigned flags) { return (flags & ~kDecodeFlags) == 0; }
 
 // Launch `fn` with one parameter structure, as a programmatic dependent of the
-// previous kernel on the stream.  Every kernel launched here waits for that one
-// (pdl_wait) before it reads or writes any memory, so the order is the stream's;
-// what overlaps is the launch itself, which costs as much as a small call does
+// previous kernel on the stream.  A call's first kernel waits for that one
+// (pdl_wait) before it reads or writes any memory, so the order is the stream's.
+// A later kernel of the call may read the call's inputs before it waits, and only
+// those, where the kernels before it in the call let it come (pdl_launch_dependents)
+// after their own wait, or are let come so themselves: nothing from before the call runs then.
+// What overlaps is the launch itself, which costs as much as a small call does
 // (norm of 1 x 4096: 2.5 us a call, 4.1 without; attention of one token over
 // 131072 rows: 36.7, 39.0; both as calls one after the other).
 // `cluster`: CTAs of a thread-block cluster.

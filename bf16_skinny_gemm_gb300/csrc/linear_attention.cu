@@ -656,8 +656,10 @@ __global__ void __launch_bounds__(kStateThreads, 1) linear_states_kernel(const _
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    // The next kernels are this call's; they may come once nothing runs that was before it, and the third reads the
-    // call's inputs before it waits (4 ragged prompts of up to 3000, 16 heads: 62.7 -> 61.2 us).  Nor before this
+    // The next kernels are this call's; they may come once nothing runs that was before it: this, and the return above,
+    // stand behind the wait, and have to.  For the third kernel reads the call's offsets and slots before it waits (4
+    // ragged prompts of up to 3000, 16 heads: 62.7 -> 61.2 us; the second lets it come at once, but comes itself
+    // when all of this kernel's CTAs have got here).  Nor before this
     // CTA has its tensor memory: a kernel behind them that takes some before it waits would hold what this one wants.
     pdl_launch_dependents();
     const uint32_t tmem = *tmem_slot;

@@ -200,8 +200,9 @@ __global__ void __launch_bounds__(kThreadsExperts, 1) moe_experts_kernel(const _
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    // The down kernel's CTAs may come once nothing runs that was before the up kernel.  They read the ids and begin
-    // to copy weights at once, while up's last CTAs run, and wait for those with everything else (64 tokens of 128
+    // The down kernel's CTAs may come once nothing runs that was before the up kernel: this stands behind the up
+    // kernel's wait, and has to.  For they read the ids and begin to copy weights at once,
+    // while up's last CTAs run, and wait for those with everything else (64 tokens of 128
     // experts 497 -> 493 us, 8 of 64 93.4 -> 90.7, 1 of 128 40.1 -> 38.9).  The caller's next kernel comes where
     // asked.  Neither comes before this CTA has its tensor memory: a kernel that takes some before it waits
     // would hold what this one, which it waits for, wants.
