@@ -3,6 +3,7 @@
 
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cstdint>
 #include <cstring>
 
@@ -73,6 +74,18 @@ inline bool heads_overlap(const Heads &a, const Heads &b, long long T, long long
 }
 
 inline bool valid_flags(unsigned flags) { return (flags & ~kDecodeFlags) == 0; }
+
+// Allow a kernel all the shared memory that there is, once per device.
+inline bool allow(const void *fn, std::atomic<unsigned long long> &done) {
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return false;
+    const unsigned long long bit = dev < 64 ? 1ULL << dev : 0ULL;
+    if (!(done.load(std::memory_order_acquire) & bit)) {
+        if (allow_max_dynamic_smem(fn) != cudaSuccess) return false;
+        done.fetch_or(bit, std::memory_order_release);
+    }
+    return true;
+}
 
 // Launch `fn` with one parameter structure, as a programmatic dependent of the
 // previous kernel on the stream.  A call's first kernel waits for that one

@@ -72,7 +72,6 @@
 // the first copies land, the pieces' results, the joining kernel.
 #include <cuda.h>
 #include <cuda_bf16.h>
-#include <cudaTypedefs.h>
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -83,6 +82,7 @@
 #include "decode_common.h"
 #include "sgemm_layers.h"
 #include "tc05_roles.cuh"
+#include "tensor_map.h"
 
 namespace sk {
 namespace latent {
@@ -1232,21 +1232,8 @@ sgemm_status_t check_sizes(const sgemm_latent_attention_t &a) {
     return SGEMM_OK;
 }
 
-PFN_cuTensorMapEncodeTiled_v12000 encoder() {
-    static PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
-        void *q = nullptr;
-        cudaDriverEntryPointQueryResult res;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &q, 12000, cudaEnableDefault, &res) !=
-                cudaSuccess ||
-            res != cudaDriverEntryPointSuccess)
-            q = nullptr;
-        return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(q);
-    }();
-    return fn;
-}
-
 bool encode_maps(LatentParams &p, const sgemm_latent_attention_t &a) {
-    auto enc = encoder();
+    auto enc = map_encoder();
     if (!enc) return false;
     if (p.q_even) {
         const cuuint64_t n = static_cast<cuuint64_t>(a.total_q) * static_cast<cuuint64_t>(a.H);
@@ -1413,18 +1400,8 @@ sgemm_status_t attend(const sgemm_latent_attention_t *a, const Tree *tree, sgemm
     p.slots = std::min(kMaxSlots, (static_cast<int>(kMaxSmemOptin) - fixed) / kSlot);
     const int smem = fixed + p.slots * kSlot;
     const void *fn = tree ? kernel_of<true>(sp.nt) : kernel_of<false>(sp.nt);
-    {
-        // once per kernel and device: allow the shared memory
-        static std::atomic<unsigned long long> done[6];
-        int dev = 0;
-        if (cudaGetDevice(&dev) != cudaSuccess) return SGEMM_ERR_CUDA;
-        std::atomic<unsigned long long> &d = done[(sp.nt == 64 ? 2 : sp.nt == 32 ? 1 : 0) + (tree ? 3 : 0)];
-        const unsigned long long bit = dev < 64 ? 1ULL << dev : 0ULL;
-        if (!(d.load(std::memory_order_acquire) & bit)) {
-            if (allow_max_dynamic_smem(fn) != cudaSuccess) return SGEMM_ERR_CUDA;
-            d.fetch_or(bit, std::memory_order_release);
-        }
-    }
+    static std::atomic<unsigned long long> done[6];
+    if (!allow(fn, done[(sp.nt == 64 ? 2 : sp.nt == 32 ? 1 : 0) + (tree ? 3 : 0)])) return SGEMM_ERR_CUDA;
     const cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
     if (launch(fn, dim3(static_cast<unsigned>(sp.groups * sp.rt)), dim3(static_cast<unsigned>(threads_of(sp.nt))), static_cast<size_t>(smem), cs, &p) != cudaSuccess)
         return SGEMM_ERR_CUDA;

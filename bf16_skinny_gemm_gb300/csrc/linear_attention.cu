@@ -1459,17 +1459,6 @@ long long scratch(const sgemm_linear_attention_t &a, int groups) {
     return groups > 1 ? (groups + 3) / 4 * 16 + 16LL * groups + 2LL * groups * a.Dk * a.Dv * 4 : 0;
 }
 
-bool allow(const void *fn, std::atomic<unsigned long long> &done) {
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess) return false;
-    const unsigned long long bit = dev < 64 ? 1ULL << dev : 0ULL;
-    if (!(done.load(std::memory_order_acquire) & bit)) {
-        if (allow_max_dynamic_smem(fn) != cudaSuccess) return false;
-        done.fetch_or(bit, std::memory_order_release);
-    }
-    return true;
-}
-
 }  // namespace linear
 }  // namespace sk
 

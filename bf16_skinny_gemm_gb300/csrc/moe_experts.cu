@@ -511,18 +511,6 @@ sgemm_status_t check_sizes(const sgemm_moe_experts_t &a) {
 long long listed(const sgemm_moe_experts_t &a) { return std::min<long long>(a.E, static_cast<long long>(a.T) * a.k); }
 long long scratch(const sgemm_moe_experts_t &a) { return listed(a) * a.T * a.F * 2; }
 
-// Allow a kernel all the shared memory that there is, once per device.
-bool allow(const void *fn, std::atomic<unsigned long long> &done) {
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess) return false;
-    const unsigned long long bit = dev < 64 ? 1ULL << dev : 0ULL;
-    if (!(done.load(std::memory_order_acquire) & bit)) {
-        if (allow_max_dynamic_smem(fn) != cudaSuccess) return false;
-        done.fetch_or(bit, std::memory_order_release);
-    }
-    return true;
-}
-
 }  // namespace moe
 }  // namespace sk
 

@@ -5,7 +5,6 @@
 // wait needs no allocated memory: every kernel that can give up a wait gets
 // its device address as a parameter.
 #include <cuda.h>
-#include <cudaTypedefs.h>
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -14,23 +13,11 @@
 
 #include "internal.h"
 #include "tc05_consts.h"
+#include "tensor_map.h"
 
 namespace {
 
 __device__ __align__(16) int g_device_error_word;
-
-PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
-    static PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
-        void *p = nullptr;
-        cudaDriverEntryPointQueryResult q;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault,
-                                             &q) != cudaSuccess ||
-            q != cudaDriverEntryPointSuccess)
-            p = nullptr;
-        return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
-    }();
-    return fn;
-}
 
 // A 2-D BF16 tensor map over rows x cols (row stride ld elements) with a box of
 // box_rows x 64 elements, 128-byte swizzled; elements outside the tensor read
@@ -38,7 +25,7 @@ PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
 // of 8) are those of the encoder.
 cudaError_t encode(CUtensorMap *map, const uint16_t *base, long long rows, long long cols,
                    long long ld, int box_rows, CUtensorMapL2promotion promo) {
-    PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
+    auto enc = sk::map_encoder();
     if (!enc) return cudaErrorNotSupported;
     const cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
     const cuuint64_t strides[1] = {static_cast<cuuint64_t>(ld) * 2};

@@ -1,4 +1,4 @@
-// Tensor maps of BF16 arrays for the operators of sgemm_layers.h.
+// The encoder of tensor maps, and maps of BF16 arrays for the operators of sgemm_layers.h.
 #pragma once
 
 #include <cuda.h>
