@@ -57,7 +57,8 @@
 // have many rows, and not all as many, so that their line has every NT rows of a sequence by themselves, one after the
 // other, and an SM each share of it: no CTA of a group idles where a sequence has fewer rows than the largest.  The CTAs
 // that read a sequence's keys do so at different times, from the L2 cache.  (8 sequences of up to 24 drafts and
-// 4099 rows, 20 heads: 48.7 us with the groups, 36.6 so; 2 of 64 drafts and 16384 rows, 64 heads: 412, 359.)
+// 4099 rows, 20 heads: 48.7 us with the groups, 36.6 so; 2 of 64 drafts and 16384 rows, 64 heads: 412, 359, today 349; 2 of 128
+// drafts 684.)
 //
 // Measured on one GB300, calls one after the other, 512 + 64 elements:
 //   32 heads, 64 sequences of up to 8192 (378 MB)    74.0 us  5.1 TB/s

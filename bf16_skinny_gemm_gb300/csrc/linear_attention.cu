@@ -159,6 +159,8 @@ __device__ __forceinline__ int units_of(const LinearParams &p, int b, bool repor
 
 // Whole sequences, for the SMs: the pairs of a sequence and a head in the order of their chunks, the longest first, are
 // dealt out forwards and backwards in turn.
+// Calls with more of either are cut, which takes longer (prompts of 200, 16 heads: 256 of them 338 us, 257 365, 400 545; 64
+// heads: 152 of them 759, 153 816).
 constexpr int kMostSorted = 256, kMostRounds = 64;
 __device__ __forceinline__ int dealt(int round, int g, int groups) { return round & 1 ? (round + 1) * groups - 1 - g : round * groups + g; }
 

@@ -31,7 +31,8 @@
 //
 // Measured on one GB300, both kernels, calls one after the other on changing weights:
 //   64 tokens, 8 of 128 experts of 4096 x 1024 (3.2 GB)   493 us   6.4 TB/s
-//   8 tokens, 6 of 64 experts of 2048 x 1408              91 us   as many bytes a second
+//   128 tokens, the same (3.2 GB)                         551 us  5.8 TB/s
+//   8 tokens, 6 of 64 experts of 2048 x 1408, 29 chosen   89 us   5.7 TB/s (35 chosen: 99 us, 6.1)
 //   1 token, 8 of 128 experts (201 MB)                    38 us   5.3 TB/s
 //   2 tokens, 2 of 16 experts of 1024 x 512               13 us
 // With few tokens the two starts are what is left: tables 0.7 us, the first slots 2 to 3 us (every SM asks for all

@@ -16,7 +16,9 @@
 //
 // Measured on one GB300, calls one after the other: 128 experts of 4096, 8 chosen: 1 token 5.6 us, 64 tokens
 // 5.9; 64 experts of 2048, 8 tokens 4.9; 16 of 1024, 2 tokens 3.9.  A launch and one chain: loads, the
-// sum over warps, the cluster's barrier, k rounds of the choice.
+// sum over warps, the cluster's barrier, k rounds of the choice.  More than 128 experts are further passes over blocks of
+// them, one after the other, and more than 256 take the choice over 32 a lane: 256 experts of 4096 8.5 us (64 tokens
+// 8.7), 288 10.5 (12.0), 1024 20.3 (23.6).
 #include <cuda_runtime.h>
 
 #include <cmath>

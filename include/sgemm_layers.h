@@ -186,6 +186,9 @@ sgemm_status_t sgemm_bf16_linear_step(const sgemm_linear_step_t *args, sgemm_str
  *   the values of either; where the sequences come to 2^30 or more chunks of all heads
  *   so, nothing is computed and bit 1 of the error word is set.
  * - Two sequences of one call must not name the same slot.
+ * - Sequences are left whole where that takes less time than cutting them, in calls of up
+ *   to 256 sequences and 64 pairs of a sequence and a head for each SM; larger
+ *   calls are always cut, which shows as a step in time of about a tenth.
  * - g <= 0 is what this is made for.  exp(g) may exceed 1 as long as no exp(G_i - G_j)
  *   overflows; g = -inf drops what came before.  An infinity or a NaN in q reaches its
  *   token only, in k or g its sequence and head from its token on, in v the same for its
